@@ -27,6 +27,10 @@ The route step of one MoE layer (see ``include/route.h``):
   ``gather_candidates`` is the exchange between them (torch.distributed), and
   ``gather_latent_logits`` the paired gather of the shards' latent and logit
   columns into the whole layer's.
+
+What a layer runs next to the route step (``layer.py``, ``include/route_layer.h``):
+``NormPlan``, ``LinearPlan``, ``GatedPlan`` and ``norm_``, ``linear_`` and
+``gated_`` ``forward`` / ``backward``.
 """
 
 from __future__ import annotations
@@ -144,6 +148,7 @@ def lib() -> ctypes.CDLL:
         for f in ("route_prepare", "route_destroy", "latent_router_forward", "topk16_select",
                   "route_step", "route_step_host", "route_step_sumsq", "route_device_status"):
             getattr(L, f).restype = i32
+        _layer.declare(L)
         _lib = L
     return _lib
 
@@ -573,3 +578,11 @@ def route_test_poison_scratch(plan: Plan, stream=None) -> None:
 def route_device_status(plan: Plan) -> None:
     """Synchronise and raise RouteError if a kernel of this plan gave up waiting."""
     _check(lib().route_device_status(plan.handle))
+
+
+# ---- the layer operators (layer.py) -------------------------------------------
+
+from . import layer as _layer  # noqa: E402  (it uses the names above)
+from .layer import (  # noqa: E402,F401
+    ACTIVATIONS, LAYER_MAX_ROWS, LAYER_MAX_WIDTH, NORM_MAX_WIDTH, GatedPlan, LinearPlan, NormPlan,
+    gated_backward, gated_forward, linear_backward, linear_forward, norm_backward, norm_forward)

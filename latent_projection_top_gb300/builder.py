@@ -27,8 +27,9 @@ DEBUG_LIB = os.path.join(DEBUG_BUILD, "libroute_debug.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["decode_kernel.cu", "prefill_kernel.cu", "topk_kernel.cu", "stage_kernel.cu",
-           "route_api.cu"]
-HEADERS = ["common.cuh", "sm103_ptx.cuh", "topk16.cuh", "twofloat.cuh"]
+           "route_api.cu", "layer_gemm.cu", "layer_elem.cu", "layer_norm.cu", "layer_api.cu"]
+HEADERS = ["common.cuh", "sm103_ptx.cuh", "topk16.cuh", "twofloat.cuh", "api_util.h", "layer.cuh",
+           "layer_math.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -38,7 +39,7 @@ FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
 
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
-    files.append(os.path.join(INCLUDE, "route.h"))
+    files += [os.path.join(INCLUDE, h) for h in ("route.h", "route_layer.h")]
     files.append(os.path.abspath(__file__))
     return files
 

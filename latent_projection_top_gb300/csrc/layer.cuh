@@ -1,0 +1,138 @@
+// Launch arguments and internal launch entry points of the layer operators
+// (layer norm, linear, gated block): the kernels' side is in layer_gemm.cu,
+// layer_elem.cu and layer_norm.cu, the C ABI's in layer_api.cu.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+
+namespace route {
+
+enum LayerType : int { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
+enum LayerAct : int {
+    kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4, kActSigmoid = 5,
+    kActCount = 6
+};
+__host__ __device__ constexpr int layer_esize(int type) { return type == kFp32 ? 4 : 2; }
+
+// What the epilogue makes of a tile's FP32 sums.
+enum LayerEpi : int {
+    kEpiLinear = 0,  // out = act(v + bias) + residual, z = v + bias kept when `saved` is set
+    kEpiGated = 1,   // v = (gate, up): out = act(gate) * up, both kept when `saved` is set
+    kEpiDGate = 2    // v = dh: out = dh * up * act'(gate), out2 = dh * act(gate), from `saved`
+};
+
+// One matrix product D[M, N] = A B with a contraction of `kblocks` blocks of
+// 64 (blocks from `kswitch` on come from the second pair of operands), and
+// what becomes of D.  Map indexes name entries of GemmMaps.
+struct GemmProblem {
+    int M, N;                   // rows and columns of the result (gated: N hidden columns)
+    int tiles_m, tiles_n, band; // 256-row tiles, column tiles, column tiles of a band
+    int item_base;              // first work item of this problem
+    int kblocks, kswitch;
+    uint8_t a[2], b[2][2];      // A map of each segment, B map of each segment and CTA of the pair
+    int out_type;               // type of out, out2 and residual
+    int bias_type;
+    const void *bias;           // [N]
+    const void *residual;       // [M, N], row stride ld_res
+    void *out;                  // [M, N], row stride ld_out
+    void *out2;                 // kEpiDGate: d up, same layout
+    float *saved;               // FP32 pre-activations, row stride ld_saved (see the epilogue)
+    long long ld_res, ld_out, ld_saved;
+    float *part;                // splits > 1: FP32 partials [split][M][ld_part]
+    long long ld_part;
+    int act;
+    int vec;                    // what may be read and written as vectors (kVec*)
+};
+
+constexpr int kGemmMaxProblems = 3;
+constexpr int kGemmMaxMaps = 6;
+
+struct GemmMaps {
+    CUtensorMap m[kGemmMaxMaps];
+};
+
+struct GemmArgs {
+    int nprob;
+    int items;                  // work items: tiles x splits over all problems
+    int splits;                 // K splits of every tile
+    int pairs;                  // CTA pairs launched
+    int fp16;                   // operands are FP16 (else BF16)
+    int trigger;                // a kernel of the same call follows: let it launch early
+    int test_stall;
+    unsigned long long timeout_ns;
+    unsigned *status;
+    GemmProblem p[kGemmMaxProblems];
+};
+
+// Partials of a split product summed in split order, then the epilogue.
+struct FinishArgs {
+    int splits;
+    int trigger;
+    GemmProblem p;
+};
+
+enum GemmForm : int {
+    kFormNT = 0,  // A rows K-contiguous, B [K, N] N-contiguous (forward)
+    kFormNN = 1,  // A rows K-contiguous, B [N, K] K-contiguous (input gradients)
+    kFormTT = 2   // A [K, M] M-contiguous, B [K, N] N-contiguous (weight gradients)
+};
+
+constexpr int kGemmBM = 256;
+cudaError_t gemm_configure();
+int gemm_smem_bytes();
+// bn: 256 or 128 accumulator columns a tile.
+cudaError_t gemm_launch(int form, int epi, int bn, const GemmMaps &maps, const GemmArgs &args,
+                        cudaStream_t stream);
+cudaError_t gemm_finish_launch(int epi, const FinishArgs &args, cudaStream_t stream);
+
+// dst[r, 0..cols) = src[r, 0..cols) of 16-bit values, for operands whose rows
+// TMA cannot read where they are.
+cudaError_t repack_launch(const void *src, long long ld_src, void *dst, long long ld_dst, int rows,
+                          int cols, cudaStream_t stream);
+
+// dz = dout * act'(z) (z: FP32, row stride ld_z; null: dz = dout), written
+// with row stride ld_dz unless dz is null, and FP32 column sums of the
+// unrounded dz when dbias is given (type `type`): `part` holds
+// elem_part_floats(N) floats.
+struct DzArgs {
+    int rows, n, type, act;
+    const void *dout;
+    long long ld_dout;
+    const float *z;
+    long long ld_z;
+    void *dz;
+    long long ld_dz;
+    void *dbias;
+    float *part;
+    int trigger;
+};
+size_t dz_part_floats(int n);
+cudaError_t dz_launch(const DzArgs &args, cudaStream_t stream);
+
+struct NormArgs {
+    int rows, dim, type;
+    float eps;
+    const void *x;
+    long long ld_x;
+    const void *gamma, *beta;
+    void *y;
+    long long ld_y;
+    float *stats;               // [rows][2]: mean, 1 / sqrt(var + eps); may be null (forward)
+    // backward
+    const void *dy;
+    long long ld_dy;
+    void *dx;
+    long long ld_dx;
+    void *dgamma, *dbeta;
+    float *part;                // norm_part_floats(dim) floats
+    int sms;
+};
+size_t norm_part_floats(int dim, int sms);
+cudaError_t norm_forward_launch(const NormArgs &args, cudaStream_t stream);
+cudaError_t norm_backward_launch(const NormArgs &args, cudaStream_t stream);
+
+}  // namespace route

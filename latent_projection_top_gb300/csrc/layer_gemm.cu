@@ -1,0 +1,430 @@
+// The layer operators' matrix products on the sm_103a tensor cores, two SMs
+// per tile.
+//
+//   D[m, n] = sum_k A[m, k] B[k, n]      16-bit operands, FP32 sums
+//
+// and, from the FP32 sums and without writing them to memory first, what the
+// operator makes of them (layer_math.cuh: epilogue): bias, activation and
+// residual; a gated block's act(gate) * up; its backward pass's d gate, d up.
+// The contraction runs over either dimension of either operand, so the
+// forward product, the input's and the weights' gradients read every tensor
+// where and as it is stored (GemmForm).
+//
+// A tile is 256 rows of D by BN columns (a gated product: BN / 2 columns of
+// gate and the same of up, the pair's first CTA loading the gate weights and
+// its second the up weights), computed by a cluster of two CTAs with
+// tcgen05.mma.cta_group::2: each CTA stages 128 rows of A and its half of
+// the tile's B columns per 64-deep k-block and holds its 128 rows x BN
+// columns of D in its TMEM.  Two accumulators alternate, so that one tile is
+// drained while the next is computed.
+//
+// Rows of D are the TMEM lanes: a thread owns one row and 16 consecutive
+// columns at a time, which it reads, transforms and stores as whole 32-byte
+// sectors; everything the epilogue reads (residual, saved pre-activations)
+// has the same shape.
+//
+// Split K: with few tiles, `splits` CTA pairs share a tile's contraction and
+// store FP32 partials; gemm_finish_kernel adds them in split order and runs
+// the same epilogue.  Results never depend on the order of arrival.
+//
+// Warp roles (320 threads, persistent, one CTA per SM, pairs = clusters):
+//   warp 0      TMA producer (both CTAs); completion counts on the leader's
+//               barrier, which the leader arms for both CTAs' bytes
+//   warp 1      TMEM owner (both CTAs); the leader's lane 0 issues the MMAs
+//   warps 2..9  epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 and half
+//               of the tile's columns
+//
+// Every wait is bounded: after timeout_ns a waiting thread sets the device
+// status word and the CTA's abort flag, in-flight copies and MMAs are
+// drained, TMEM is freed and both CTAs return.
+#include "layer.cuh"
+#include "layer_math.cuh"
+#include "sm103_ptx.cuh"
+
+namespace route {
+namespace {
+
+constexpr int kHalf = 128;                        // each CTA's rows of D
+constexpr uint32_t kABytes = kHalf * 64 * 2;      // 128 rows x 64 k
+constexpr int kEpiWarps = 8;
+constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
+constexpr uint32_t kSmemLimit = 227 * 1024;
+
+__host__ __device__ constexpr uint32_t b_bytes(int bn) { return (uint32_t)bn / 2 * 64 * 2; }
+__host__ __device__ constexpr uint32_t stage_bytes(int bn) { return kABytes + b_bytes(bn); }
+__host__ __device__ constexpr int stages_of(int bn) { return bn == 256 ? 6 : 8; }
+__host__ __device__ constexpr uint32_t smem_of(int bn) { return 1024 + stages_of(bn) * stage_bytes(bn) + 256; }
+static_assert(smem_of(256) <= kSmemLimit && smem_of(128) <= kSmemLimit, "shared memory");
+
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+    d |= 1ull << 46;  // descriptor version for tcgen05
+    d |= 2ull << 61;  // 128-byte swizzle
+    return d;
+}
+
+// Descriptor of 16 k of an operand tile.  K-contiguous: 128-byte swizzled
+// rows of 64 k, 8-row groups 1024 B apart; 16 k are 32 B.  M/N-contiguous:
+// boxes of 64 columns x 64 k, 8192 B apart, 8-k groups 1024 B apart; 16 k
+// are 2048 B.
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t base, int kk) {
+    return MN ? smem_desc(base + kk * 2048u, 8192u, 1024u) : smem_desc(base + kk * 32u, 16u, 1024u);
+}
+
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const GemmArgs &a,
+                                           volatile int *abort_flag) {
+    if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = ptx::global_timer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+        if ((it & 63u) == 0u) {
+            if (*abort_flag) return false;
+            if (ptx::global_timer_ns() - t0 > a.timeout_ns) {
+                *abort_flag = 1;
+                atomicOr(a.status, kStatusTimeout);
+                return false;
+            }
+        }
+    }
+}
+
+// Bounded wait used only while tearing down.
+__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, const GemmArgs &a) {
+    const uint64_t t0 = ptx::global_timer_ns();
+    while (!ptx::mbar_try_wait_cluster(bar, parity)) {
+        if (ptx::global_timer_ns() - t0 > a.timeout_ns) {
+            atomicOr(a.status, kStatusTimeout);
+            return;
+        }
+    }
+}
+
+// A work item: the tile's problem, its row and column tile, its split and
+// its k-blocks.  Tiles go in bands of `band` column tiles over every row
+// tile, so that the pairs at work at one time share rows of A and columns of
+// B; the splits of a tile are neighbours.
+struct Item {
+    int p, tm, tn, split, kb0, kb1;
+};
+__device__ __forceinline__ Item item_of(const GemmArgs &a, int i) {
+    Item w;
+    w.p = 0;
+    while (w.p + 1 < a.nprob && i >= a.p[w.p + 1].item_base) ++w.p;
+    const GemmProblem &p = a.p[w.p];
+    i -= p.item_base;
+    w.split = i % a.splits;
+    i /= a.splits;
+    const int per_band = p.band * p.tiles_m;
+    const int b = i / per_band, r = i - b * per_band;
+    const int c0 = b * p.band;
+    const int bw = p.tiles_n - c0 < p.band ? p.tiles_n - c0 : p.band;
+    w.tm = r / bw;
+    w.tn = c0 + r % bw;
+    w.kb0 = (int)((long long)p.kblocks * w.split / a.splits);
+    w.kb1 = (int)((long long)p.kblocks * (w.split + 1) / a.splits);
+    return w;
+}
+
+template <int FORM, int EPI, int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+    layer_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs args) {
+    constexpr bool A_MN = FORM == kFormTT, B_MN = FORM != kFormNN;
+    constexpr int S = stages_of(BN);
+    constexpr uint32_t kStage = stage_bytes(BN);
+    constexpr int kTileCols = EPI == kEpiGated ? BN / 2 : BN;  // columns of D a tile
+    constexpr int kBCols = BN / 2;                             // B columns each CTA loads
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t s_tmem_base;
+    __shared__ volatile int s_abort;
+
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    const uint32_t bars = sbase + S * kStage;
+    auto full_bar = [&](int s) { return bars + 8u * s; };             // leader's are used
+    auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
+    auto tfull_bar = [&](int t) { return bars + 8u * (2 * S + t); };
+    auto tempty_bar = [&](int t) { return bars + 8u * (2 * S + 2 + t); };  // leader's
+    const uint32_t drain_bar = bars + 8u * (2 * S + 4);
+
+    const uint32_t rank = ptx::cluster_ctarank();
+    const bool leader = rank == 0u;
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int pair = blockIdx.x >> 1;
+
+    if (threadIdx.x == 0) {
+        if (args.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        s_abort = 0;
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(full_bar(s), 1);
+            ptx::mbar_init(empty_bar(s), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(tfull_bar(t), 1);
+            ptx::mbar_init(tempty_bar(t), 2 * kEpiWarps);  // each epilogue warp of both CTAs
+        }
+        ptx::mbar_init(drain_bar, 1);
+        ptx::fence_barrier_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(ptx::smem_addr(&s_tmem_base), 2 * BN);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    ptx::cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = s_tmem_base;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA producer (both CTAs) ----------------
+            const uint64_t pol = ptx::policy_evict_normal();
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            int it = 0;
+            uint32_t armed = 0u, armed_par = 0u;
+            bool ok = true;
+            for (int i = pair; i < args.items && ok; i += args.pairs) {
+                const Item w = item_of(args, i);
+                const GemmProblem &p = args.p[w.p];
+                const int m0 = w.tm * kGemmBM + (int)rank * kHalf;
+                const int n0 = w.tn * kTileCols + (EPI == kEpiGated ? 0 : (int)rank * kBCols);
+                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                    const int s = it % S;
+                    const uint32_t ph = (uint32_t)(it / S) & 1u;
+                    if (!wait_phase(empty_bar(s), ph ^ 1u, args, &s_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = ptx::map_to_rank(full_bar(s), 0u);
+                    if (leader) {
+                        ptx::mbar_arrive_expect_tx(full_bar(s), 2u * kStage);
+                        armed |= 1u << s;
+                        armed_par = (armed_par & ~(1u << s)) | (ph << s);
+                    }
+                    if (args.test_stall && i + args.pairs >= args.items && kb == w.kb1 - 1 && leader)
+                        continue;  // test hook: the last k-block never arrives
+                    const int seg = kb >= p.kswitch;
+                    const int k0 = (seg ? kb - p.kswitch : kb) * 64;
+                    const CUtensorMap *ma = &maps.m[p.a[seg]];
+                    const CUtensorMap *mb = &maps.m[p.b[seg][rank]];
+                    const uint32_t sa = sbase + s * kStage, sb = sa + kABytes;
+                    if (A_MN) {
+                        ptx::tma_load_2d_pair(sa, ma, fb, m0, k0, pol);
+                        ptx::tma_load_2d_pair(sa + 8192u, ma, fb, m0 + 64, k0, pol);
+                    } else {
+                        ptx::tma_load_2d_pair(sa, ma, fb, k0, m0, pol);
+                    }
+                    if (B_MN) {
+#pragma unroll
+                        for (int j = 0; j < kBCols / 64; ++j)
+                            ptx::tma_load_2d_pair(sb + 8192u * j, mb, fb, n0 + 64 * j, k0, pol);
+                    } else {
+                        ptx::tma_load_2d_pair(sb, mb, fb, k0, n0, pol);
+                    }
+                }
+            }
+            // After an abort the leader lets every copy it armed land (the
+            // peer's copies complete on the same barriers).
+            if (leader && (!ok || s_abort)) {
+                for (int s = 0; s < S; ++s)
+                    if (armed & (1u << s)) wait_drain(full_bar(s), (armed_par >> s) & 1u, args);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            // ---------------- MMA issuer (leader CTA) ----------------
+            // kind::f16, FP32 accumulator, M = 256 over the pair, N = BN
+            const uint32_t fmt = args.fp16 ? 0u : 1u;
+            const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((A_MN ? 1u : 0u) << 15) |
+                                   ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(BN >> 3) << 17) |
+                                   ((uint32_t)(kGemmBM >> 4) << 24);
+            int it = 0, job = 0;
+            bool ok = true;
+            for (int i = pair; i < args.items && ok; i += args.pairs, ++job) {
+                const Item w = item_of(args, i);
+                const int t = job & 1;
+                if (!wait_phase(tempty_bar(t), (((uint32_t)job >> 1) & 1u) ^ 1u, args, &s_abort)) break;
+                ptx::tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (uint32_t)(t * BN);
+                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                    const int s = it % S;
+                    if (!wait_phase(full_bar(s), (uint32_t)(it / S) & 1u, args, &s_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t sa = sbase + s * kStage, sb = sa + kABytes;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        ptx::mma_bf16_pair(d_tmem, operand_desc<A_MN>(sa, kk),
+                                           operand_desc<B_MN>(sb, kk), idesc,
+                                           (kb > w.kb0 || kk > 0) ? 1u : 0u);
+                    ptx::mma_commit_pair(empty_bar(s), 0x3);  // frees stage s in both CTAs
+                }
+                if (ok) ptx::mma_commit_pair(tfull_bar(t), 0x3);
+            }
+            ptx::mma_commit_pair(drain_bar, 0x3);  // every MMA retired before TMEM is freed
+            wait_drain(drain_bar, 0u, args);
+        }
+    } else {
+        // ---------------- epilogue (warps 2..9, both CTAs) ----------------
+        const int lq = warp & 3;         // TMEM lanes 32 lq .. + 31 = rows of D
+        const int cs = (warp - 2) >> 2;  // which half of the tile's columns
+        const uint32_t lanes = tmem_base + ((uint32_t)(32 * lq) << 16);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        int job = 0;
+        for (int i = pair; i < args.items; i += args.pairs, ++job) {
+            const Item w = item_of(args, i);
+            const GemmProblem &p = args.p[w.p];
+            const int t = job & 1;
+            const bool ok = wait_phase(tfull_bar(t), ((uint32_t)job >> 1) & 1u, args, &s_abort);
+            __syncwarp();  // the TMEM loads that follow are warp-wide
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const int r = w.tm * kGemmBM + (int)rank * kHalf + 32 * lq + lane;
+            const int c0 = w.tn * kTileCols + cs * (kTileCols / 2);
+            const uint32_t acc = lanes + (uint32_t)(t * BN + cs * (kTileCols / 2));
+            constexpr int kChunks = kTileCols / 2 / 16;
+#pragma unroll 1
+            for (int ch = 0; ch < kChunks; ++ch) {
+                uint32_t v[16], u[16];
+                __syncwarp();  // lanes past the last row skipped the stores
+                ptx::tmem_ld_x16(acc + 16u * ch, v);
+                if (EPI == kEpiGated) ptx::tmem_ld_x16(acc + 16u * ch + kTileCols, u);
+                ptx::tmem_ld_wait();
+                if (ch == kChunks - 1) {  // every column is in registers
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (leader)
+                            ptx::mbar_arrive(tempty_bar(t));
+                        else
+                            ptx::mbar_arrive_remote(ptx::map_to_rank(tempty_bar(t), 0u));
+                    }
+                }
+                const int c = c0 + 16 * ch;
+                if (r >= p.M || c >= p.N) continue;
+                float vf[16], uf[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    vf[j] = __uint_as_float(v[j]);
+                    uf[j] = EPI == kEpiGated ? __uint_as_float(u[j]) : 0.f;
+                }
+                if (args.splits > 1) {  // partials: rows padded to whole chunks
+                    float *part = p.part + ((long long)w.split * p.M + r) * p.ld_part;
+                    if constexpr (EPI == kEpiGated) {
+                        store_vec<16>(part, kFp32, saved_gate(c), 16, 1, vf);
+                        store_vec<16>(part, kFp32, saved_gate(c) + 16, 16, 1, uf);
+                    } else {
+                        store_vec<16>(part, kFp32, c, 16, 1, vf);
+                    }
+                } else {
+                    epilogue<EPI, 16>(p, r, c, vf, uf);
+                }
+            }
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        // the leader's MMAs write this CTA's TMEM: the peer waits for them too
+        if (lane == 0 && !leader) wait_drain(drain_bar, 0u, args);
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem_base, 2 * BN);
+    }
+    ptx::cluster_sync();  // neither CTA leaves while the other may reach its shared memory
+}
+
+// Sums of the split partials in split order, four columns a thread, and the
+// epilogue.  The partials were just written and sit in L2.
+template <int EPI>
+__global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant__ FinishArgs a) {
+    if (threadIdx.x == 0 && a.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int groups = (a.p.N + 3) >> 2;
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= (long long)groups * a.p.M) return;
+    const int r = (int)(i / groups), c = (int)(i % groups) * 4;
+    const float *src = a.p.part + (long long)r * a.p.ld_part + (EPI == kEpiGated ? saved_gate(c) : c);
+    const long long step = (long long)a.p.M * a.p.ld_part;
+    float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s, src += step) {
+        const float4 x = *reinterpret_cast<const float4 *>(src);
+        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+        if (EPI == kEpiGated) {
+            const float4 y = *reinterpret_cast<const float4 *>(src + 16);
+            u[0] += y.x, u[1] += y.y, u[2] += y.z, u[3] += y.w;
+        }
+    }
+    epilogue<EPI, 4>(a.p, r, c, v, u);
+}
+
+cudaError_t launch_chained(const void *fn, dim3 grid, dim3 block, size_t smem, void **params,
+                           cudaStream_t stream) {
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute attr[1];
+    c.gridDim = grid;
+    c.blockDim = block;
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = attr;
+    c.numAttrs = 1;
+    return cudaLaunchKernelExC(&c, fn, params);
+}
+
+const void *kernel_of(int form, int epi, int bn) {
+#define ROUTE_GEMM(F, E)                                                            \
+    if (form == F && epi == E)                                                      \
+        return bn == 256 ? reinterpret_cast<const void *>(layer_gemm_kernel<F, E, 256>) \
+                         : reinterpret_cast<const void *>(layer_gemm_kernel<F, E, 128>);
+    ROUTE_GEMM(kFormNT, kEpiLinear)
+    ROUTE_GEMM(kFormNT, kEpiGated)
+    ROUTE_GEMM(kFormNN, kEpiLinear)
+    ROUTE_GEMM(kFormNN, kEpiDGate)
+    ROUTE_GEMM(kFormTT, kEpiLinear)
+#undef ROUTE_GEMM
+    return nullptr;
+}
+
+}  // namespace
+
+cudaError_t gemm_configure() {
+    for (int form = 0; form < 3; ++form)
+        for (int epi = 0; epi < 3; ++epi)
+            for (int bn : {256, 128})
+                if (const void *k = kernel_of(form, epi, bn)) {
+                    const cudaError_t e = cudaFuncSetAttribute(
+                        k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(bn));
+                    if (e != cudaSuccess) return e;
+                }
+    return cudaSuccess;
+}
+
+int gemm_smem_bytes() { return (int)(smem_of(256) > smem_of(128) ? smem_of(256) : smem_of(128)); }
+
+cudaError_t gemm_launch(int form, int epi, int bn, const GemmMaps &maps, const GemmArgs &args,
+                        cudaStream_t stream) {
+    const void *k = kernel_of(form, epi, bn);
+    if (k == nullptr || args.pairs <= 0 || args.items <= 0) return cudaErrorInvalidConfiguration;
+    void *params[] = {const_cast<GemmMaps *>(&maps), const_cast<GemmArgs *>(&args)};
+    return launch_chained(k, dim3(2 * args.pairs), dim3(kGemmThreads), smem_of(bn), params, stream);
+}
+
+cudaError_t gemm_finish_launch(int epi, const FinishArgs &args, cudaStream_t stream) {
+    const void *k = epi == kEpiLinear  ? reinterpret_cast<const void *>(gemm_finish_kernel<kEpiLinear>)
+                    : epi == kEpiGated ? reinterpret_cast<const void *>(gemm_finish_kernel<kEpiGated>)
+                                       : reinterpret_cast<const void *>(gemm_finish_kernel<kEpiDGate>);
+    const long long threads = (long long)((args.p.N + 3) / 4) * args.p.M;
+    void *params[] = {const_cast<FinishArgs *>(&args)};
+    return launch_chained(k, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, params, stream);
+}
+
+}  // namespace route

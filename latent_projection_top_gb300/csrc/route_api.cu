@@ -13,6 +13,7 @@
 #include <new>
 #include <vector>
 
+#include "api_util.h"
 #include "common.cuh"
 #include "route.h"
 
@@ -1273,3 +1274,36 @@ int route_plan_latent_cols(const route_plan *plan) { return plan ? plan->n_lat :
 int route_plan_experts(const route_plan *plan) { return plan ? plan->n_exp : -1; }
 
 }  // extern "C"
+
+// ---- shared with the layer operators' C ABI -------------------------------
+
+namespace route {
+
+route_status api_fail(route_status st, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return st;
+}
+
+route_status api_encode_operand(CUtensorMap *m, const void *ptr, bool fp16, uint64_t inner,
+                                uint64_t outer, uint64_t ld, uint32_t box_inner,
+                                uint32_t box_outer, const char *what) {
+    EncodeTiledFn enc = nullptr;
+    route_status st = get_encode(&enc);
+    if (st != ROUTE_OK) return st;
+    cuuint64_t dims[2] = {inner, outer};
+    cuuint64_t strides[1] = {ld * 2};
+    cuuint32_t box[2] = {box_inner, box_outer};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = enc(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                     const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return api_fail(ROUTE_ERR_CUDA, "tensor map for %s rejected (CUresult %d)", what, (int)r);
+    return ROUTE_OK;
+}
+
+}  // namespace route

@@ -1,0 +1,430 @@
+"""The layer operators on a GPU against their float64 forms (layer_ref.py):
+every output element within the bound that the kernels' arithmetic gives."""
+
+import pytest
+import torch
+
+import latent_projection_top_gb300 as route
+import layer_ref as ref
+from gpu_util import DEV, require_gpu
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def normal(seed, *shape, scale=1.0, dt=BF16, ld=None, offset=0):
+    """A seeded matrix or vector; with `ld` a view with that row stride that
+    starts `offset` elements into its buffer."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    v = (torch.randn(shape, generator=g, device=DEV) * scale).to(dt)
+    if ld is None:
+        return v
+    buf = torch.full((shape[0] * ld + offset,), float("nan"), dtype=dt, device=DEV)
+    view = buf[offset:].view(shape[0], ld)[:, :shape[1]]
+    view.copy_(v)
+    return view
+
+
+def blank(rows, cols, dt=BF16, ld=None, offset=0):
+    """An output full of NaN inside a buffer of sevens, and the check that
+    nothing but the output was written."""
+    ld = cols if ld is None else ld
+    buf = torch.full((rows * ld + offset + 16,), 7.0, dtype=dt, device=DEV)
+    view = buf[offset:offset + rows * ld].view(rows, ld)[:, :cols]
+    view.fill_(float("nan"))
+
+    def guarded():
+        mask = torch.ones_like(buf, dtype=torch.bool)
+        mask[offset:offset + rows * ld].view(rows, ld)[:, :cols] = False
+        assert bool((buf[mask] == 7).all()), "written outside the output"
+
+    return view, guarded
+
+
+def check(name, got, want, limit=1.0):
+    w = ref.worst(got, want)
+    assert w <= limit, f"{name}: {w:.3g} times the bound"
+
+
+# ---- linear -------------------------------------------------------------------
+
+LINEAR = [
+    # rows, k, n, dtype, act, bias, residual
+    (1, 64, 64, BF16, "none", False, False),
+    (1, 7168, 896, BF16, "none", False, True),
+    (7, 3584, 7168, BF16, "none", False, True),
+    (20, 896, 448, FP16, "gelu", True, True),
+    (33, 1001, 517, BF16, "gelu_tanh", True, True),
+    (64, 200, 1000, BF16, "relu", True, False),
+    (128, 512, 2048, BF16, "silu", False, False),
+    (129, 65, 129, FP16, "sigmoid", True, True),
+    (256, 256, 256, BF16, "none", True, False),
+    (257, 320, 264, BF16, "silu", True, True),
+    (300, 1, 1, BF16, "none", True, True),
+    (515, 8, 7, FP16, "relu", True, False),
+    (1024, 640, 1536, BF16, "gelu", True, True),
+    (2050, 896, 1792, FP16, "none", False, True),
+    (1, 13, 4096, BF16, "none", True, False),
+    (4099, 128, 72, BF16, "gelu", False, False),
+]
+
+
+@pytest.mark.parametrize("rows,k,n,dt,act,bias,residual", LINEAR)
+def test_linear_forward_and_backward(rows, k, n, dt, act, bias, residual):
+    x, W = normal(1, rows, k, dt=dt), normal(2, k, n, scale=k ** -0.5, dt=dt)
+    b = normal(3, n, dt=dt) if bias else None
+    res = normal(4, rows, n, dt=dt) if residual else None
+    dout = normal(5, rows, n, dt=dt)
+    with route.LinearPlan(rows, k, n, dt, act=act, train=True) as plan:
+        saved = plan.new_saved()
+        out, guard = blank(rows, n, dt)
+        route.linear_forward(plan, x, W, out, bias=b, residual=res, saved=saved)
+        dx, guard_dx = blank(rows, k, dt)
+        dW, guard_dW = blank(k, n, dt)
+        dbias = torch.full((n,), float("nan"), dtype=dt, device=DEV)
+        route.linear_backward(plan, dout, x, W, saved=saved, dx=dx, dW=dW, dbias=dbias)
+        plan.status()
+        again = torch.full_like(out, float("nan"))
+        route.linear_forward(plan, x, W, again, bias=b, residual=res)
+        plan.status()
+        assert torch.equal(again, out)  # the inference call is the same product
+    want, z = ref.linear(x, W, b, res, act, dt)
+    check("out", out, want)
+    grads = ref.linear_grads(x, W, z, dout, act, dt)
+    check("dx", dx, grads["dx"])
+    check("dW", dW, grads["dW"])
+    check("dbias", dbias, grads["dbias"])
+    for g in (guard, guard_dx, guard_dW):
+        g()
+
+
+@pytest.mark.parametrize("rows", [1, 5, 40, 300])
+def test_linear_strided_views_in_place_residual_and_fp32_out(rows):
+    k, n, dt = 136, 200, BF16
+    x = normal(1, rows, k, dt=dt, ld=k + 24, offset=8)
+    W = normal(2, k, n, scale=k ** -0.5, dt=dt, ld=n + 8, offset=16)
+    res = normal(3, rows, n, dt=FP32, ld=n + 3, offset=1)
+    want, _ = ref.linear(x, W, None, res, "none", dt, FP32)
+    out, guard = blank(rows, n, FP32, ld=n + 5, offset=3)
+    with route.LinearPlan(2 * rows, k, n, dt, out_dtype=FP32) as plan:
+        route.linear_forward(plan, x, W, out, residual=res)
+        check("out", out, want)
+        guard()
+        route.linear_forward(plan, x, W, res, residual=res)  # in place
+        plan.status()
+        assert torch.equal(res, out)
+
+
+@pytest.mark.parametrize("rows,k,n", [(9, 77, 131), (260, 131, 77)])
+def test_linear_odd_strides_and_offsets(rows, k, n):
+    """Widths that are no multiple of 8: any alignment of rows and bases."""
+    dt = BF16
+    x = normal(1, rows, k, dt=dt, ld=k + 2, offset=1)
+    W = normal(2, k, n, scale=k ** -0.5, dt=dt, ld=n + 4, offset=3)
+    b = normal(3, n, dt=dt)
+    dout = normal(4, rows, n, dt=dt, ld=n + 1, offset=5)
+    out, g0 = blank(rows, n, dt, ld=n + 1, offset=1)
+    dx, g1 = blank(rows, k, dt, ld=k + 3, offset=1)
+    dW, g2 = blank(k, n, dt, ld=n + 2, offset=7)
+    with route.LinearPlan(rows, k, n, dt, act="silu", train=True) as plan:
+        saved = plan.new_saved()
+        route.linear_forward(plan, x, W, out, bias=b, saved=saved)
+        route.linear_backward(plan, dout, x, W, saved=saved, dx=dx, dW=dW)
+        plan.status()
+    want, z = ref.linear(x, W, b, None, "silu", dt)
+    grads = ref.linear_grads(x, W, z, dout, "silu", dt)
+    for name, got, w in (("out", out, want), ("dx", dx, grads["dx"]), ("dW", dW, grads["dW"])):
+        check(name, got, w)
+    for g in (g0, g1, g2):
+        g()
+
+
+# ---- gated --------------------------------------------------------------------
+
+GATED = [
+    # rows, k, f, n, dtype, act, residual
+    (1, 7168, 512, 7168, BF16, "silu", True),
+    (8, 896, 1024, 896, BF16, "silu", False),
+    (20, 256, 130, 64, FP16, "gelu", True),
+    (33, 100, 51, 77, BF16, "gelu_tanh", True),
+    (130, 512, 640, 512, BF16, "silu", False),
+    (257, 264, 200, 328, FP16, "sigmoid", True),
+    (700, 1000, 702, 1000, BF16, "relu", False),
+    (1030, 448, 896, 448, BF16, "silu", True),
+    (2, 1, 1, 1, BF16, "silu", True),
+    (512, 64, 17, 9, FP16, "none", False),
+]
+
+
+@pytest.mark.parametrize("rows,k,f,n,dt,act,residual", GATED)
+def test_gated_forward_and_backward(rows, k, f, n, dt, act, residual):
+    x = normal(1, rows, k, dt=dt)
+    Wg, Wu = normal(2, k, f, scale=k ** -0.5, dt=dt), normal(3, k, f, scale=k ** -0.5, dt=dt)
+    Wd = normal(4, f, n, scale=f ** -0.5, dt=dt)
+    res = normal(5, rows, n, dt=dt) if residual else None
+    dout = normal(6, rows, n, dt=dt)
+    with route.GatedPlan(rows, k, f, n, dt, act=act, train=True) as plan:
+        saved = plan.new_saved()
+        out, g0 = blank(rows, n, dt)
+        route.gated_forward(plan, x, Wg, Wu, Wd, out, residual=res, saved=saved)
+        dx, g1 = blank(rows, k, dt)
+        dWg, g2 = blank(k, f, dt)
+        dWu, g3 = blank(k, f, dt)
+        dWd, g4 = blank(f, n, dt)
+        route.gated_backward(plan, dout, x, Wg, Wu, Wd, saved, dx=dx, dW_gate=dWg, dW_up=dWu,
+                             dW_down=dWd)
+        again = torch.full_like(out, float("nan"))
+        route.gated_forward(plan, x, Wg, Wu, Wd, again, residual=res)
+        only, g5 = blank(f, n, dt)
+        route.gated_backward(plan, dout, x, Wg, Wu, Wd, saved, dW_down=only)
+        plan.status()
+        assert torch.equal(again, out) and torch.equal(only, dWd)
+    want, kept = ref.gated(x, Wg, Wu, Wd, res, act, dt)
+    check("out", out, want)
+    grads = ref.gated_grads(x, Wg, Wu, Wd, kept, dout, act, dt)
+    for name, got in (("dx", dx), ("dW_gate", dWg), ("dW_up", dWu), ("dW_down", dWd)):
+        check(name, got, grads[name])
+    for g in (g0, g1, g2, g3, g4, g5):
+        g()
+
+
+# ---- norm ---------------------------------------------------------------------
+
+def norm_ref(x, gamma, beta, eps, dt):
+    v = x.double()
+    n = v.shape[1]
+    mean = v.mean(1, keepdim=True)
+    d = v - mean
+    var = (d * d).mean(1, keepdim=True)
+    r = (var + eps) ** -0.5
+    g = gamma.double() if gamma is not None else torch.ones(n, device=DEV, dtype=torch.float64)
+    b = beta.double() if beta is not None else torch.zeros(n, device=DEV, dtype=torch.float64)
+    y = d * r * g + b
+    # FP32 sums over blocks of at most 64 in sequence: the mean within
+    # 2^-18 of the mean magnitude, and through it each deviation; the
+    # variance within 2^-18 of itself and the squared error of the mean
+    em = 2.0 ** -18 * v.abs().mean(1, keepdim=True)
+    er = r * (2.0 ** -18 + 0.5 * r * r * em * em)
+    e = (em * r + d.abs() * er + ref.F32 * d.abs() * r) * g.abs() + ref.F32 * (y.abs() + b.abs())
+    return ref.rounded((y, e), dt), mean, r
+
+
+NORM = [(1, 7168, BF16), (3, 1, BF16), (5, 8, FP32), (9, 64, FP16), (33, 1000, BF16),
+        (64, 1001, FP32), (130, 1024, BF16), (17, 1032, FP16), (300, 3584, BF16),
+        (40, 4097, BF16), (70, 8192, FP32), (11, 9000, FP16), (6, 16384, BF16), (2, 16383, FP32),
+        (2000, 96, BF16)]
+
+
+@pytest.mark.parametrize("rows,dim,dt", NORM)
+def test_norm_forward_and_backward(rows, dim, dt):
+    x = normal(1, rows, dim, dt=dt) * 3 + normal(2, rows, 1, dt=dt)
+    x = x.to(dt)
+    gamma, beta = (1 + normal(3, dim, dt=dt) * 0.3).to(dt), normal(4, dim, dt=dt)
+    dy = normal(5, rows, dim, dt=dt)
+    y, g0 = blank(rows, dim, dt)
+    dx, g1 = blank(rows, dim, dt)
+    stats = torch.full((rows, 2), float("nan"), device=DEV)
+    dgamma, dbeta = (torch.full((dim,), float("nan"), dtype=dt, device=DEV) for _ in range(2))
+    with route.NormPlan(rows, dim, dt) as plan:
+        route.norm_forward(plan, x, gamma, beta, y, stats=stats)
+        route.norm_backward(plan, dy, x, gamma, stats, dx=dx, dgamma=dgamma, dbeta=dbeta)
+        plan.status()
+    want, mean, r = norm_ref(x, gamma, beta, 1e-5, dt)
+    check("y", y, want)
+    em = 2.0 ** -18 * x.double().abs().mean(1, keepdim=True)
+    check("mean", stats[:, :1], (mean, em + 1e-30))
+    # the backward pass with the statistics that it was given
+    m, s = stats[:, :1].double(), stats[:, 1:].double()
+    xh = (x.double() - m) * s
+    exh = ref.F32 * (x.double().abs() + m.abs()) * s
+    g = dy.double() * gamma.double()
+    a, b = g.mean(1, keepdim=True), (g * xh).mean(1, keepdim=True)
+    ea = 2.0 ** -18 * g.abs().mean(1, keepdim=True)
+    eb = 2.0 ** -18 * (g * xh).abs().mean(1, keepdim=True) + (g.abs() * exh).mean(1, keepdim=True)
+    v = s * (g - a - xh * b)
+    e = s * (ref.F32 * (g.abs() + a.abs() + (xh * b).abs()) + ea + xh.abs() * eb + exh * b.abs())
+    check("dx", dx, ref.rounded((v, e), dt))
+    terms = dy.double() * xh
+    eg = dy.double().abs() * exh + ref.F32 * terms.abs()
+    check("dgamma", dgamma, ref.rounded(ref.column_sum((terms, eg)), dt))
+    check("dbeta", dbeta, ref.rounded(ref.column_sum(ref.exact(dy)), dt))
+    g0()
+    g1()
+
+
+def test_norm_views_partial_gradients_and_in_place():
+    rows, dim, dt = 37, 333, BF16
+    x = normal(1, rows, dim, dt=dt, ld=dim + 2, offset=1)
+    dy = normal(2, rows, dim, dt=dt, ld=dim + 1, offset=3)
+    gamma = normal(3, dim, dt=dt)
+    y, g0 = blank(rows, dim, dt, ld=dim + 4, offset=1)
+    stats = torch.empty((rows, 2), device=DEV)
+    with route.NormPlan(64, dim, dt) as plan:
+        route.norm_forward(plan, x, gamma, None, y, stats=stats, eps=0.5)
+        check("y", y, norm_ref(x, gamma, None, 0.5, dt)[0])
+        full = [torch.empty((rows, dim), dtype=dt, device=DEV)] + \
+               [torch.empty((dim,), dtype=dt, device=DEV) for _ in range(2)]
+        route.norm_backward(plan, dy, x, gamma, stats, dx=full[0], dgamma=full[1], dbeta=full[2])
+        for i, name in enumerate(("dx", "dgamma", "dbeta")):
+            one = torch.empty_like(full[i])
+            route.norm_backward(plan, dy, x, gamma, stats, **{name: one})
+            assert torch.equal(one, full[i]), name
+        want = full[0].clone()
+        route.norm_backward(plan, dy, x, gamma, stats, dx=dy)  # over its own input
+        assert torch.equal(dy, want)
+        route.norm_forward(plan, x, None, None, x, eps=0.5)
+        plan.status()
+    g0()
+
+
+def test_norm_constant_rows_and_large_offsets():
+    """A constant row's variance is zero; a row far from zero keeps the
+    variance of its deviations."""
+    dim = 1024
+    x = torch.full((3, dim), 2.5, device=DEV)
+    x[1] = 4096.0 + torch.arange(dim, device=DEV) % 4
+    x[2] = 0
+    y = torch.empty_like(x)
+    with route.NormPlan(3, dim, FP32) as plan:
+        route.norm_forward(plan, x, None, None, y)
+        plan.status()
+    want = (x - x.mean(1, keepdim=True)).double()
+    want = want / (want.square().mean(1, keepdim=True) + 1e-5).sqrt()
+    assert torch.equal(y[0], torch.zeros_like(y[0])) and torch.equal(y[2], torch.zeros_like(y[2]))
+    assert (y - want).abs().max() < 1e-5
+
+
+# ---- common behaviour -----------------------------------------------------------
+
+def test_zero_rows():
+    k, f, n = 72, 48, 40
+    e = lambda *s: torch.empty(s, dtype=BF16, device=DEV)  # noqa: E731
+    nan = lambda *s: torch.full(s, float("nan"), dtype=BF16, device=DEV)  # noqa: E731
+    with route.LinearPlan(4, k, n, BF16, act="silu", train=True) as lin, \
+            route.GatedPlan(4, k, f, n, BF16, train=True) as gated, \
+            route.NormPlan(4, k, BF16) as norm:
+        dW, db = nan(k, n), nan(n)
+        route.linear_forward(lin, e(0, k), e(k, n), e(0, n))
+        route.linear_backward(lin, e(0, n), e(0, k), e(k, n), dx=e(0, k), dW=dW, dbias=db)
+        ws = nan(k, f), nan(k, f), nan(f, n)
+        route.gated_forward(gated, e(0, k), e(k, f), e(k, f), e(f, n), e(0, n))
+        route.gated_backward(gated, e(0, n), e(0, k), e(k, f), e(k, f), e(f, n), None, dx=e(0, k),
+                             dW_gate=ws[0], dW_up=ws[1], dW_down=ws[2])
+        dg = nan(k)
+        route.norm_forward(norm, e(0, k), None, None, e(0, k))
+        route.norm_backward(norm, e(0, k), e(0, k), None, torch.empty((0, 2), device=DEV),
+                            dx=e(0, k), dgamma=dg)
+        for p in (lin, gated, norm):
+            p.status()
+        for t in (dW, db, *ws, dg):
+            assert bool((t == 0).all())
+
+
+@pytest.mark.parametrize("rows", [6, 300])
+def test_special_values_stay_in_their_rows(rows):
+    """NaN and infinities of a row reach that row's results and no other's."""
+    k, f, n = 128, 96, 136
+    x = normal(1, rows, k)
+    Wg, Wu, Wd = normal(2, k, f), normal(3, k, f), normal(4, f, n)
+    clean, dirty = (torch.empty((rows, n), dtype=BF16, device=DEV) for _ in range(2))
+    bad = x.clone()
+    bad[2, 5] = float("nan")
+    bad[4, 0] = float("inf")
+    keep = [i for i in range(rows) if i not in (2, 4)]
+    with route.GatedPlan(rows, k, f, n, BF16) as plan:
+        route.gated_forward(plan, x, Wg, Wu, Wd, clean)
+        route.gated_forward(plan, bad, Wg, Wu, Wd, dirty)
+        plan.status()
+    assert torch.equal(clean[keep], dirty[keep])
+    assert bool(torch.isnan(dirty[2]).all()) and not bool(torch.isfinite(dirty[4]).any())
+    for act in route.ACTIVATIONS:
+        with route.LinearPlan(rows, k, n, BF16, act=act) as plan:
+            route.linear_forward(plan, bad, Wg[:, :1].repeat(1, n).contiguous(), dirty)
+            plan.status()
+        assert bool(torch.isnan(dirty[2]).all()) and bool(torch.isfinite(dirty[keep]).all()), act
+
+
+def test_other_stream_and_graph_replay():
+    rows, k, f, n = 70, 320, 192, 320
+    x = normal(1, rows, k)
+    w = normal(2, k, f, scale=0.05), normal(3, k, f, scale=0.05), normal(4, f, n, scale=0.05)
+    want, got = (torch.empty((rows, n), dtype=BF16, device=DEV) for _ in range(2))
+    y = torch.empty_like(x)
+    with route.GatedPlan(rows, k, f, n, BF16) as plan, route.NormPlan(rows, k, BF16) as norm:
+        def step(out):
+            route.norm_forward(norm, x, None, None, y)
+            route.gated_forward(plan, y, *w, out, residual=x)
+        step(want)
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            step(got)
+        s.synchronize()
+        assert torch.equal(want, got)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step(got)
+        for seed in (11, 12):
+            x.copy_(normal(seed, rows, k))
+            step(want)
+            got.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(want, got)
+        plan.status()
+
+
+def test_stalled_product_reports_a_timeout_and_recovers():
+    rows, k, n = 300, 512, 512
+    x, W = normal(1, rows, k), normal(2, k, n)
+    out, want = (torch.empty((rows, n), dtype=BF16, device=DEV) for _ in range(2))
+    with route.LinearPlan(rows, k, n, BF16) as plan:
+        route.linear_forward(plan, x, W, want)
+        plan.status()
+        assert route.lib().route_layer_test_stall(plan.handle, 1, 2_000_000) == 0
+        route.linear_forward(plan, x, W, out)
+        with pytest.raises(route.RouteError, match="TIMEOUT"):
+            plan.status()
+        assert route.lib().route_layer_test_stall(plan.handle, 0, 0) == 0
+        route.linear_forward(plan, x, W, out)
+        plan.status()
+        assert torch.equal(out, want)
+
+
+def test_refusals_of_tensors():
+    k, n = 64, 32
+    x, W = normal(1, 4, k), normal(2, k, n)
+    out = torch.empty((4, n), dtype=BF16, device=DEV)
+    with route.LinearPlan(4, k, n, BF16) as plan:
+        with pytest.raises(TypeError, match="dtype"):
+            route.linear_forward(plan, x.half(), W, out)
+        with pytest.raises(ValueError, match="shape"):
+            route.linear_forward(plan, x, W.t(), out)
+        with pytest.raises(ValueError, match="unit stride"):
+            route.linear_forward(plan, x, normal(2, n, k).t(), out)
+        with pytest.raises(ValueError, match="cuda:0"):
+            route.linear_forward(plan, x.cpu(), W, out)
+        with pytest.raises(route.RouteError, match="ROUTE_ERR_ROWS"):
+            route.linear_forward(plan, normal(1, 5, k), W, torch.empty((5, n), dtype=BF16, device=DEV))
+        with pytest.raises(route.RouteError, match="ROUTE_ERR_ALIGN"):
+            route.linear_forward(plan, normal(1, 4, k, ld=k + 1), W, out)
+        with pytest.raises(route.RouteError, match="ROUTE_ERR_ALIGN"):
+            route.linear_forward(plan, normal(1, 4, k, ld=k, offset=1), W, out)
+        with pytest.raises(route.RouteError, match="without train"):
+            route.linear_backward(plan, out, x, W, dx=torch.empty_like(x))
+        with pytest.raises(route.RouteError, match="ROUTE_ERR_PLAN"):
+            route.linear_forward(plan, x[:1].expand(4, k), W, out)
+    with route.LinearPlan(4, k, n, BF16, act="gelu", train=True) as plan:
+        with pytest.raises(ValueError, match="saved holds"):
+            route.linear_forward(plan, x, W, out, saved=torch.empty((8,), dtype=torch.uint8, device=DEV))
+        with pytest.raises(route.RouteError, match="ROUTE_ERR_NULL"):
+            route.linear_backward(plan, out, x, W, dx=torch.empty_like(x))
+    with pytest.raises(route.RouteError, match="closed"):
+        route.linear_forward(plan, x, W, out)
