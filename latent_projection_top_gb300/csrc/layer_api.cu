@@ -27,7 +27,7 @@ struct route_layer {
     int device, sms, pairs;
     int test_stall;
     unsigned long long timeout_ns;
-    unsigned *words;   // device status word
+    unsigned *words;   // device status word, then the streamed products' arrival counts
     uint8_t *scratch;
     size_t scratch_bytes;
     // offsets into scratch (0 size where the plan needs none)
@@ -37,10 +37,15 @@ struct route_layer {
 
 namespace {
 
+constexpr int kPlanWords = kWords + kStreamMaxTiles;
 constexpr unsigned long long kTimeoutNs = 2000000000ull;
 // Split products have at most one item a CTA pair: FP32 partials of a
 // 256 x 256 tile each.
 constexpr size_t kTilePartBytes = 256 * 256 * 4;
+// Rows up to which a product streams its weights (layer_stream.cu).
+constexpr int kStreamRows = kStreamMaxRows;
+
+bool streams(int rows) { return rows <= kStreamRows; }
 
 route_status cuda_fail(cudaError_t e, const char *what) {
     return api_fail(ROUTE_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
@@ -198,9 +203,21 @@ struct Product {
     Product(const route_layer *p) : fp16(p->type == kFp16) {
         memset(&args, 0, sizeof args);
         args.fp16 = fp16;
+        args.a_bytes = 128 * 64 * 2;
         args.timeout_ns = p->timeout_ns;
         args.status = p->words;
         args.test_stall = p->test_stall;
+    }
+    // Rows of a K-contiguous A's boxes: 128, or what there is of M.
+    uint32_t a_rows(int M) {
+        const uint32_t r = M >= 128 ? 128u : (uint32_t)up8(M);
+        static_assert(kStreamMaxRows <= 128, "a streamed product's rows are one box");
+        args.a_bytes = r * 64 * 2;
+        return r;
+    }
+    // Rows of a K-contiguous B's boxes: the weight columns a CTA loads.
+    uint32_t b_rows(int M, const Choice &ch) {
+        return streams(M) ? (uint32_t)kStreamTile : (uint32_t)ch.bn / 2;
     }
     // A map of `o` [outer, inner] in boxes of box_inner x box_outer.
     route_status map(const Operand &o, long long inner, long long outer, uint32_t box_outer,
@@ -211,10 +228,41 @@ struct Product {
     }
 };
 
+// A streamed product.  `chained`: the call's kernel before it is one too.
+route_status run_stream(const route_layer *p, const Product &pr, int form, int epi, bool chained,
+                        bool more, cudaStream_t stream) {
+    const GemmProblem &q = pr.args.p[0];
+    const int cols = epi == kEpiGated ? kStreamTile / 2 : kStreamTile;
+    StreamArgs a;
+    memset(&a, 0, sizeof a);
+    a.rows = q.M;
+    a.tiles = (q.N + cols - 1) / cols;
+    a.kblocks = q.kblocks, a.kswitch = q.kswitch;
+    const long long units = (long long)a.tiles * a.kblocks;
+    a.grid = units < p->sms ? (int)units : p->sms;
+    a.wait_first = !chained;
+    a.fp16 = pr.fp16;
+    a.trigger = more;
+    a.test_stall = p->test_stall;
+    a.x_bytes = (unsigned)up8(q.M) * 64 * 2;
+    a.timeout_ns = p->timeout_ns;
+    a.status = p->words;
+    a.arrived = p->words + kWords;
+    a.part = reinterpret_cast<float *>(p->scratch + p->o_part);
+    for (int seg = 0; seg < 2; ++seg) {
+        a.x[seg] = q.a[seg];
+        for (int h = 0; h < 2; ++h) a.w[seg][h] = q.b[seg][h];
+    }
+    a.p = q;
+    const cudaError_t e = stream_launch(form, epi, pr.maps, a, stream);
+    return e == cudaSuccess ? ROUTE_OK : cuda_fail(e, "streamed product kernel launch");
+}
+
 // Launch the product(s) and, when split, the kernel(s) that finish them.
 route_status run(const route_layer *p, Product &pr, int form, int epi, const Choice &ch,
-                 bool more, cudaStream_t stream) {
+                 bool chained, bool more, cudaStream_t stream) {
     GemmArgs &a = pr.args;
+    if (form != kFormTT && streams(a.p[0].M)) return run_stream(p, pr, form, epi, chained, more, stream);
     const int tile_cols = epi == kEpiGated ? ch.bn / 2 : ch.bn;
     a.splits = ch.splits;
     int items = 0;
@@ -267,7 +315,7 @@ void set_out(GemmProblem &q, void *out, long long ld_out, int out_type) {
 // out[M, N] = epilogue(A[M, K] W[K, N]): A K-contiguous, W N-contiguous.
 route_status forward_product(const route_layer *p, const Operand &A, const Operand &W, int M, int K,
                              int N, int act, const void *bias, const void *residual, int64_t ld_res,
-                             void *out, int64_t ld_out, int out_type, float *saved,
+                             void *out, int64_t ld_out, int out_type, float *saved, bool chained,
                              cudaStream_t stream) {
     Product pr(p);
     GemmProblem &q = pr.args.p[0];
@@ -283,16 +331,17 @@ route_status forward_product(const route_layer *p, const Operand &A, const Opera
     q.vec = vec_bits(out, q.ld_out, nullptr, residual, q.ld_res, out_type, bias);
     const Choice ch = choose_one(p, M, N, q.kblocks, false);
     route_status st;
-    if ((st = pr.map(A, K, M, 128, "x", &q.a[0])) != ROUTE_OK ||
+    if ((st = pr.map(A, K, M, pr.a_rows(M), "x", &q.a[0])) != ROUTE_OK ||
         (st = pr.map(W, N, K, 64, "W", &q.b[0][0])) != ROUTE_OK)
         return st;
     q.b[0][1] = q.b[0][0];
-    return run(p, pr, kFormNT, kEpiLinear, ch, false, stream);
+    return run(p, pr, kFormNT, kEpiLinear, ch, chained, false, stream);
 }
 
 // out[M, K] = sum over i of dz_i[M, N] W_i[K, N]^T, one or two terms.
 route_status input_grad(const route_layer *p, int terms, const Operand *dz, const Operand *W, int M,
-                        int N, int K, void *out, int64_t ld_out, bool more, cudaStream_t stream) {
+                        int N, int K, void *out, int64_t ld_out, bool chained, bool more,
+                        cudaStream_t stream) {
     Product pr(p);
     GemmProblem &q = pr.args.p[0];
     pr.args.nprob = 1;
@@ -303,12 +352,12 @@ route_status input_grad(const route_layer *p, int terms, const Operand *dz, cons
     const Choice ch = choose_one(p, M, K, q.kblocks, false);
     for (int i = 0; i < terms; ++i) {
         route_status st;
-        if ((st = pr.map(dz[i], N, M, 128, "dz", &q.a[i])) != ROUTE_OK ||
-            (st = pr.map(W[i], N, K, (uint32_t)ch.bn / 2, "W", &q.b[i][0])) != ROUTE_OK)
+        if ((st = pr.map(dz[i], N, M, pr.a_rows(M), "dz", &q.a[i])) != ROUTE_OK ||
+            (st = pr.map(W[i], N, K, pr.b_rows(M, ch), "W", &q.b[i][0])) != ROUTE_OK)
             return st;
         q.b[i][1] = q.b[i][0];
     }
-    return run(p, pr, kFormNN, kEpiLinear, ch, more, stream);
+    return run(p, pr, kFormNN, kEpiLinear, ch, chained, more, stream);
 }
 
 // dW_i[K_i, N_i] = x_i[rows, K_i]^T dz_i[rows, N_i] for up to three weights.
@@ -342,7 +391,7 @@ route_status weight_grads(const route_layer *p, const WeightGrad *w, int count, 
         return t;
     };
     const Choice ch = choose(p, tiles, kblocks_of(rows), elems);
-    return run(p, pr, kFormTT, kEpiLinear, ch, false, stream);
+    return run(p, pr, kFormTT, kEpiLinear, ch, false, false, stream);
 }
 
 route_status zero_matrix(void *p, int64_t ld, int rows, int cols, int esize, cudaStream_t stream) {
@@ -369,10 +418,12 @@ route_status finish_prepare(route_layer *p, int device, route_layer **out) {
         st = api_fail(ROUTE_ERR_DEVICE, "device %d is sm_%d%d; this library is built for sm_103a only",
                       device, prop.major, prop.minor);
     } else if (p->kind != kNorm && ((size_t)gemm_smem_bytes() > prop.sharedMemPerBlockOptin ||
+                                    (size_t)stream_smem_bytes() > prop.sharedMemPerBlockOptin ||
                                     prop.multiProcessorCount < 2)) {
         st = api_fail(ROUTE_ERR_DEVICE, "the product kernels need %d B of shared memory per block",
                       gemm_smem_bytes());
-    } else if (p->kind != kNorm && (e = gemm_configure()) != cudaSuccess) {
+    } else if (p->kind != kNorm && ((e = gemm_configure()) != cudaSuccess ||
+                                    (e = stream_configure()) != cudaSuccess)) {
         st = cuda_fail(e, "cudaFuncSetAttribute");
     }
     if (st != ROUTE_OK) {
@@ -396,6 +447,12 @@ route_status finish_prepare(route_layer *p, int device, route_layer **out) {
         p->o_part = area(norm_part_floats(p->k, p->sms) * 4);
     } else {
         size_t part = (size_t)p->pairs * kTilePartBytes;
+        const size_t widest = (size_t)(p->k > p->n ? p->k : p->n) > 2 * (size_t)p->f
+                                  ? (size_t)(p->k > p->n ? p->k : p->n)
+                                  : 2 * (size_t)p->f;
+        const size_t slots = p->sms + (widest + kStreamTile - 1) / kStreamTile;
+        const size_t few = R < kStreamRows ? R : kStreamRows;
+        if (part < slots * few * kStreamTile * 4) part = slots * few * kStreamTile * 4;
         if (p->kind == kLinear && p->train && part < dz_part_floats(p->n) * 4)
             part = dz_part_floats(p->n) * 4;
         p->o_part = area(part);
@@ -416,8 +473,8 @@ route_status finish_prepare(route_layer *p, int device, route_layer **out) {
         }
     }
     p->scratch_bytes = at;
-    if ((e = cudaMalloc(&p->words, kWords * sizeof(unsigned))) != cudaSuccess ||
-        (e = cudaMemset(p->words, 0, kWords * sizeof(unsigned))) != cudaSuccess ||
+    if ((e = cudaMalloc(&p->words, kPlanWords * sizeof(unsigned))) != cudaSuccess ||
+        (e = cudaMemset(p->words, 0, kPlanWords * sizeof(unsigned))) != cudaSuccess ||
         (e = cudaMalloc(&p->scratch, at ? at : 256)) != cudaSuccess) {
         if (p->words) cudaFree(p->words);
         delete p;
@@ -512,7 +569,8 @@ route_status route_layer_status(const route_layer *p) {
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
     unsigned w = 0;
     if ((e = cudaMemcpy(&w, p->words, sizeof w, cudaMemcpyDeviceToHost)) != cudaSuccess ||
-        (e = cudaMemset(p->words, 0, sizeof w)) != cudaSuccess)
+        // a call that gave up may have left arrival counts behind
+        (e = cudaMemset(p->words, 0, (w ? kPlanWords : 1) * sizeof w)) != cudaSuccess)
         return cuda_fail(e, "status word");
     if (w & kStatusBounds)
         return api_fail(ROUTE_ERR_DEVICE_BOUNDS, "a kernel skipped an index out of range");
@@ -627,7 +685,7 @@ route_status route_linear_forward(const route_layer *p, int rows, const void *x,
         (st = operand(p, W, ld_W, p->k, p->n, p->o_w[0], s, &ow)) != ROUTE_OK)
         return st;
     return forward_product(p, ox, ow, rows, p->k, p->n, p->act, bias, residual, ld_residual, out,
-                           ld_out, p->out_type, static_cast<float *>(saved), s);
+                           ld_out, p->out_type, static_cast<float *>(saved), false, s);
 }
 
 route_status route_linear_backward(const route_layer *p, int rows, const void *dout,
@@ -677,7 +735,7 @@ route_status route_linear_backward(const route_layer *p, int rows, const void *d
     if (dx) {
         Operand ow;
         if ((st = operand(p, W, ld_W, p->k, p->n, p->o_w[0], s, &ow)) != ROUTE_OK ||
-            (st = input_grad(p, 1, &dz, &ow, rows, p->n, p->k, dx, ld_dx, dW != nullptr, s)) != ROUTE_OK)
+            (st = input_grad(p, 1, &dz, &ow, rows, p->n, p->k, dx, ld_dx, false, dW != nullptr, s)) != ROUTE_OK)
             return st;
     }
     if (dW) {
@@ -727,14 +785,14 @@ route_status route_gated_forward(const route_layer *p, int rows, const void *x, 
         q.act = p->act;
         q.saved = static_cast<float *>(saved), q.ld_saved = 2 * ldf;
         const Choice ch = choose_one(p, rows, p->f, q.kblocks, true);
-        if ((st = pr.map(ox, p->k, rows, 128, "x", &q.a[0])) != ROUTE_OK ||
+        if ((st = pr.map(ox, p->k, rows, pr.a_rows(rows), "x", &q.a[0])) != ROUTE_OK ||
             (st = pr.map(og, p->f, p->k, 64, "W_gate", &q.b[0][0])) != ROUTE_OK ||
             (st = pr.map(ou, p->f, p->k, 64, "W_up", &q.b[0][1])) != ROUTE_OK ||
-            (st = run(p, pr, kFormNT, kEpiGated, ch, true, s)) != ROUTE_OK)
+            (st = run(p, pr, kFormNT, kEpiGated, ch, false, true, s)) != ROUTE_OK)
             return st;
     }
     return forward_product(p, {h, ldf}, od, rows, p->f, p->n, kActNone, nullptr, residual,
-                           ld_residual, out, ld_out, p->type, nullptr, s);
+                           ld_residual, out, ld_out, p->type, nullptr, true, s);
 }
 
 route_status route_gated_backward(const route_layer *p, int rows, const void *dout,
@@ -790,18 +848,19 @@ route_status route_gated_backward(const route_layer *p, int rows, const void *do
         q.act = p->act;
         q.saved = static_cast<float *>(const_cast<void *>(saved)), q.ld_saved = 2 * ldf;
         const Choice ch = choose_one(p, rows, p->f, q.kblocks, false);
-        if ((st = pr.map(dy, p->n, rows, 128, "dout", &q.a[0])) != ROUTE_OK ||
-            (st = pr.map(od, p->n, p->f, (uint32_t)ch.bn / 2, "W_down", &q.b[0][0])) != ROUTE_OK)
+        if ((st = pr.map(dy, p->n, rows, pr.a_rows(rows), "dout", &q.a[0])) != ROUTE_OK ||
+            (st = pr.map(od, p->n, p->f, pr.b_rows(rows, ch), "W_down", &q.b[0][0])) != ROUTE_OK)
             return st;
         q.b[0][1] = q.b[0][0];
-        if ((st = run(p, pr, kFormNN, kEpiDGate, ch, true, s)) != ROUTE_OK) return st;
+        if ((st = run(p, pr, kFormNN, kEpiDGate, ch, false, true, s)) != ROUTE_OK) return st;
     }
     const bool weights = dW_gate || dW_up || dW_down;
     if (dx) {
         Operand w[2];
+        const bool chained = p->f % 8 == 0;  // no copy of the weights between the two products
         if ((st = operand(p, W_gate, ld_gate, p->k, p->f, p->o_w[0], s, &w[0])) != ROUTE_OK ||
             (st = operand(p, W_up, ld_up, p->k, p->f, p->o_w[1], s, &w[1])) != ROUTE_OK ||
-            (st = input_grad(p, 2, dz, w, rows, p->f, p->k, dx, ld_dx, weights, s)) != ROUTE_OK)
+            (st = input_grad(p, 2, dz, w, rows, p->f, p->k, dx, ld_dx, chained, weights, s)) != ROUTE_OK)
             return st;
     }
     if (!weights) return ROUTE_OK;

@@ -200,7 +200,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                     }
                     const uint32_t fb = ptx::map_to_rank(full_bar(s), 0u);
                     if (leader) {
-                        ptx::mbar_arrive_expect_tx(full_bar(s), 2u * kStage);
+                        ptx::mbar_arrive_expect_tx(full_bar(s), 2u * (args.a_bytes + b_bytes(BN)));
                         armed |= 1u << s;
                         armed_par = (armed_par & ~(1u << s)) | (ph << s);
                     }
