@@ -67,13 +67,10 @@ __global__ void __launch_bounds__(256) dz_kernel(const __grid_constant__ DzArgs 
             if (a.z != nullptr) {
                 const float4 *q = reinterpret_cast<const float4 *>(a.z + (long long)r * a.ld_z + c);
                 const float4 z0 = q[0], z1 = q[1];
-                const float z[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+                float z[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w}, d[8];
+                act_slopes<8>(a.act, z, z, d);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float y, d;
-                    act_both(a.act, z[e], y, d);
-                    v[e] = e < n ? v[e] * d : 0.f;
-                }
+                for (int e = 0; e < 8; ++e) v[e] = e < n ? v[e] * d[e] : 0.f;
             }
             if (dz != nullptr)  // ld_dz is a multiple of 8
                 *reinterpret_cast<uint4 *>(dz + (long long)r * a.ld_dz + c) =

@@ -280,17 +280,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             const Item w = item_of(args, i);
             const GemmProblem &p = args.p[w.p];
             const int t = job & 1;
+            const int r = w.tm * kGemmBM + (int)rank * kHalf + 32 * lq + lane;
+            const int c0 = w.tn * kTileCols + cs * (kTileCols / 2);
+            EpiIn<EPI, 16> in, next;
+            if (args.splits == 1) epi_load<EPI, 16>(p, r, c0, in);
             const bool ok = wait_phase(tfull_bar(t), ((uint32_t)job >> 1) & 1u, args, &s_abort);
             __syncwarp();  // the TMEM loads that follow are warp-wide
             if (!ok) break;
             ptx::tc_fence_after();
-            const int r = w.tm * kGemmBM + (int)rank * kHalf + 32 * lq + lane;
-            const int c0 = w.tn * kTileCols + cs * (kTileCols / 2);
             const uint32_t acc = lanes + (uint32_t)(t * BN + cs * (kTileCols / 2));
             constexpr int kChunks = kTileCols / 2 / 16;
 #pragma unroll 1
             for (int ch = 0; ch < kChunks; ++ch) {
                 uint32_t v[16], u[16];
+                if (ch + 1 < kChunks && args.splits == 1)
+                    epi_load<EPI, 16>(p, r, c0 + 16 * ch + 16, next);
                 __syncwarp();  // lanes past the last row skipped the stores
                 ptx::tmem_ld_x16(acc + 16u * ch, v);
                 if (EPI == kEpiGated) ptx::tmem_ld_x16(acc + 16u * ch + kTileCols, u);
@@ -306,24 +310,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                     }
                 }
                 const int c = c0 + 16 * ch;
-                if (r >= p.M || c >= p.N) continue;
                 float vf[16], uf[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     vf[j] = __uint_as_float(v[j]);
                     uf[j] = EPI == kEpiGated ? __uint_as_float(u[j]) : 0.f;
                 }
-                if (args.splits > 1) {  // partials: rows padded to whole chunks
+                if (args.splits == 1) {
+                    epilogue<EPI, 16>(p, r, c, vf, uf, in);
+                } else if (r < p.M && c < p.N) {  // partials: rows padded to whole chunks
                     float *part = p.part + ((long long)w.split * p.M + r) * p.ld_part;
                     if constexpr (EPI == kEpiGated) {
-                        store_vec<16>(part, kFp32, saved_gate(c), 16, 1, vf);
-                        store_vec<16>(part, kFp32, saved_gate(c) + 16, 16, 1, uf);
+                        store_saved<16>(part + saved_gate(c), vf);
+                        store_saved<16>(part + saved_gate(c) + 16, uf);
                     } else {
-                        store_vec<16>(part, kFp32, c, 16, 1, vf);
+                        store_saved<16>(part + c, vf);
                     }
-                } else {
-                    epilogue<EPI, 16>(p, r, c, vf, uf);
                 }
+                in = next;
             }
         }
     }
@@ -353,6 +357,8 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
     const float *src = a.p.part + (long long)r * a.p.ld_part + (EPI == kEpiGated ? saved_gate(c) : c);
     const long long step = (long long)a.p.M * a.p.ld_part;
     float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+    EpiIn<EPI, 4> in;
+    epi_load<EPI, 4>(a.p, r, c, in);
 #pragma unroll 4
     for (int s = 0; s < a.splits; ++s, src += step) {
         const float4 x = *reinterpret_cast<const float4 *>(src);
@@ -362,7 +368,7 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
             u[0] += y.x, u[1] += y.y, u[2] += y.z, u[3] += y.w;
         }
     }
-    epilogue<EPI, 4>(a.p, r, c, v, u);
+    epilogue<EPI, 4>(a.p, r, c, v, u, in);
 }
 
 cudaError_t launch_chained(const void *fn, dim3 grid, dim3 block, size_t smem, void **params,

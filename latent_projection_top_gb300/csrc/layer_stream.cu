@@ -280,6 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int r = i / (kTileCols / 4), c = (i % (kTileCols / 4)) * 4;
                     const float *q = src + r * kStreamTile + c;
                     float v[4] = {0.f, 0.f, 0.f, 0.f}, up[4] = {0.f, 0.f, 0.f, 0.f};
+                    EpiIn<EPI, 4> in;
+                    epi_load<EPI, 4>(args.p, r, tile * kTileCols + c, in);
 #pragma unroll 4
                     for (int s = g0; s <= g1; ++s, q += step) {
                         const float4 x = __ldcg(reinterpret_cast<const float4 *>(q));
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             up[0] += y.x, up[1] += y.y, up[2] += y.z, up[3] += y.w;
                         }
                     }
-                    epilogue<EPI, 4>(args.p, r, tile * kTileCols + c, v, up);
+                    epilogue<EPI, 4>(args.p, r, tile * kTileCols + c, v, up, in);
                 }
             }
             u = min(u1, (tile + 1) * K);
