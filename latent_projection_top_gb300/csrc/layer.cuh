@@ -155,9 +155,10 @@ struct NormArgs {
     void *dx;
     long long ld_dx;
     void *dgamma, *dbeta;
-    float *part;                // norm_part_floats(dim) floats
+    float *part;                // norm_part_floats(dim, sms) floats
     int sms;
 };
+cudaError_t norm_configure();
 size_t norm_part_floats(int dim, int sms);
 cudaError_t norm_forward_launch(const NormArgs &args, cudaStream_t stream);
 cudaError_t norm_backward_launch(const NormArgs &args, cudaStream_t stream);

@@ -422,6 +422,8 @@ route_status finish_prepare(route_layer *p, int device, route_layer **out) {
                                     prop.multiProcessorCount < 2)) {
         st = api_fail(ROUTE_ERR_DEVICE, "the product kernels need %d B of shared memory per block",
                       gemm_smem_bytes());
+    } else if (p->kind == kNorm && (e = norm_configure()) != cudaSuccess) {
+        st = cuda_fail(e, "cudaFuncSetAttribute");
     } else if (p->kind != kNorm && ((e = gemm_configure()) != cudaSuccess ||
                                     (e = stream_configure()) != cudaSuccess)) {
         st = cuda_fail(e, "cudaFuncSetAttribute");

@@ -14,7 +14,7 @@ namespace route {
 namespace {
 
 constexpr int kV = 4;  // runs of eight values a thread
-constexpr int kMaxPart = 304;
+constexpr int kMaxBlocks = 3;  // backward blocks an SM, at most
 
 // Where value e of run v of thread t sits in the row: whole 16-byte vectors
 // when rows are aligned for it, else one element a thread at a time.
@@ -97,7 +97,330 @@ __device__ __forceinline__ float row_sum(float v, float *scratch) {
     return v;
 }
 
-template <int T, bool VEC>
+// ---- rows aligned for 16-byte access: a ring of rows in shared memory --------
+//
+// Memory-bound: 3 (forward: 2) times the row's bytes and little else, so what
+// counts is that enough bytes are always on their way (about 45 KB an SM at
+// this memory's rate and latency).  Blocks are persistent; a thread copies
+// the 16-byte vectors that it will itself use of the next rows into its own
+// places of a ring (cp.async: no registers held, no barrier to hand a row
+// over), and per row the block meets only to add the row's sums.
+
+// Eight values as they lie in memory.
+template <int ES>
+struct Run {
+    uint32_t w[2 * ES];
+};
+template <int ES>
+__device__ __forceinline__ void unpack_run(const Run<ES> &q, int type, float (&x)[8]) {
+    if constexpr (ES == 4) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(q.w[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack16(q.w[e], type);
+            x[2 * e] = f.x, x[2 * e + 1] = f.y;
+        }
+    }
+}
+
+template <int T, int V, int ES>
+struct Ring {
+    static constexpr int kHalves = ES / 2;                       // 16-byte vectors of a run
+    static constexpr uint32_t kRow = (uint32_t)V * kHalves * T * 16;  // bytes of a row's place
+    // The vector `h` of run v of thread t: neighbours in t are neighbours in
+    // shared memory.
+    static __device__ __forceinline__ uint32_t at(uint32_t base, int v, int h, int t) {
+        return base + (uint32_t)((v * kHalves + h) * T + t) * 16u;
+    }
+    static __device__ __forceinline__ void copy(uint32_t base, const void *p, long long row, int dim, int t) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = (v * T + t) * 8;
+            if (c < dim) {
+                const char *src = static_cast<const char *>(p) + (row + c) * ES;
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(base, v, h, t)),
+                                 "l"(src + 16 * h)
+                                 : "memory");
+            }
+        }
+    }
+    static __device__ __forceinline__ void load(uint32_t base, int v, int t, int dim, int type, float (&x)[8]) {
+        Run<ES> q;
+        if ((v * T + t) * 8 < dim) {
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(q.w[4 * h]), "=r"(q.w[4 * h + 1]), "=r"(q.w[4 * h + 2]),
+                               "=r"(q.w[4 * h + 3])
+                             : "r"(at(base, v, h, t))
+                             : "memory");
+        } else {
+#pragma unroll
+            for (int e = 0; e < 2 * ES; ++e) q.w[e] = 0u;
+        }
+        unpack_run<ES>(q, type, x);
+    }
+};
+
+// A parameter's values of this thread, kept packed in registers.
+template <int T, int V, int ES>
+__device__ __forceinline__ void load_param(const void *p, int type, int t, int dim, float none, Run<ES> (&q)[V]) {
+    uint32_t fill;
+    if (ES == 4)
+        fill = __float_as_uint(none);
+    else
+        fill = pack16(none, none, type);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = (v * T + t) * 8;
+        if (p != nullptr && c < dim) {
+            const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + (long long)c * ES);
+#pragma unroll
+            for (int h = 0; h < ES / 2; ++h) {
+                const uint4 x = s[h];
+                q[v].w[4 * h] = x.x, q[v].w[4 * h + 1] = x.y, q[v].w[4 * h + 2] = x.z, q[v].w[4 * h + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 2 * ES; ++e) q[v].w[e] = fill;
+        }
+    }
+}
+
+// Sums of a and b over a row's T threads, the same in every thread and every
+// run.  One barrier: consecutive sums use alternate scratch.
+template <int T>
+__device__ __forceinline__ void row_sums(float &a, float &b, float2 (*scratch)[T / 32], int &turn) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    }
+    if constexpr (T > 32) {
+        if ((threadIdx.x & 31) == 0) scratch[turn][threadIdx.x >> 5] = make_float2(a, b);
+        __syncthreads();
+        a = b = 0.f;
+#pragma unroll
+        for (int i = 0; i < T / 32; ++i) {
+            const float2 s = scratch[turn][i];
+            a += s.x, b += s.y;
+        }
+        turn ^= 1;
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+__host__ __device__ constexpr int block_of(int t) { return t > 32 ? t : 128; }
+__host__ __device__ constexpr int rows_of(int t) { return block_of(t) / t; }
+
+// Blocks an SM and rows of a ring: up to ~190 KB of rows an SM.
+__host__ __device__ constexpr int fwd_blocks(int t, int es) {
+    return t <= 128 ? (es == 2 ? 5 : 4) : t == 256 ? (es == 2 ? 3 : 2) : 1;
+}
+template <int T, int V, int ES>
+__host__ __device__ constexpr int fwd_depth() {
+    constexpr uint32_t per = 190u * 1024u / fwd_blocks(T, ES) / (Ring<T, V, ES>::kRow * rows_of(T));
+    return per > 6 ? 6 : per < 2 ? 2 : (int)per;
+}
+__host__ __device__ constexpr int bwd_blocks(int t, int es) {
+    return t == 32 ? 3 : t == 128 ? 3 : t == 256 ? (es == 2 ? 2 : 1) : 1;
+}
+template <int T, int V, int ES>
+__host__ __device__ constexpr int bwd_depth() {
+    constexpr uint32_t per = 190u * 1024u / bwd_blocks(T, ES) / (2 * Ring<T, V, ES>::kRow * rows_of(T));
+    return per > 6 ? 6 : per < 2 ? 2 : (int)per;
+}
+
+template <int T, int V, int ES>
+__global__ void __launch_bounds__(block_of(T), fwd_blocks(T, ES))
+    norm_forward_ring_kernel(const __grid_constant__ NormArgs a) {
+    using R = Ring<T, V, ES>;
+    constexpr int P = fwd_depth<T, V, ES>(), kRows = rows_of(T);
+    extern __shared__ uint4 ring[];
+    __shared__ float2 scratch[2][T / 32];
+    const int t = threadIdx.x % T;
+    const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + (threadIdx.x / T) * P * R::kRow;
+    const int stride = gridDim.x * kRows;
+    const int r0 = blockIdx.x * kRows + threadIdx.x / T;
+    int turn = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < P - 1; ++i) {
+        if (r0 + (long long)i * stride < a.rows)
+            R::copy(mine + i * R::kRow, a.x, (long long)(r0 + i * stride) * a.ld_x, a.dim, t);
+        copy_commit();
+    }
+    Run<ES> gamma[V], beta[V];
+    load_param<T, V, ES>(a.gamma, a.type, t, a.dim, 1.f, gamma);
+    load_param<T, V, ES>(a.beta, a.type, t, a.dim, 0.f, beta);
+    const float inv = 1.f / (float)a.dim;
+    int slot = 0;
+    for (int r = r0; r < a.rows; r += stride) {
+        const int slot_in = slot == 0 ? P - 1 : slot - 1;
+        if (r + (long long)(P - 1) * stride < a.rows)
+            R::copy(mine + slot_in * R::kRow, a.x, (long long)(r + (P - 1) * stride) * a.ld_x, a.dim, t);
+        copy_commit();
+        copy_wait<P - 1>();
+        const uint32_t base = mine + slot * R::kRow;
+        slot = slot + 1 == P ? 0 : slot + 1;
+        float x[V][8], s = 0.f, none = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            R::load(base, v, t, a.dim, a.type, x[v]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += x[v][e];
+        }
+        row_sums<T>(s, none, scratch, turn);
+        const float mean = s * inv;
+        s = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const bool in = (v * T + t) * 8 < a.dim;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[v][e] -= mean;
+                if (in) s += x[v][e] * x[v][e];
+            }
+        }
+        row_sums<T>(s, none, scratch, turn);
+        const float rstd = 1.f / sqrtf(s * inv + a.eps);
+        if (t == 0 && a.stats != nullptr)
+            *reinterpret_cast<float2 *>(a.stats + 2 * (long long)r) = make_float2(mean, rstd);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float g[8], b[8];
+            unpack_run<ES>(gamma[v], a.type, g);
+            unpack_run<ES>(beta[v], a.type, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[v][e] = x[v][e] * rstd * g[e] + b[e];
+            store_run<T, true>(a.y, a.type, (long long)r * a.ld_y, v, t, a.dim, x[v]);
+        }
+    }
+}
+
+// A thread keeps the gain's and offset's gradient sums of its own columns
+// over its rows in registers and writes them once, as a row of partials a
+// block; x and dy are read from the ring twice rather than kept.
+template <int T, int V, int ES>
+__global__ void __launch_bounds__(block_of(T), bwd_blocks(T, ES))
+    norm_backward_ring_kernel(const __grid_constant__ NormArgs a) {
+    using R = Ring<T, V, ES>;
+    constexpr int P = bwd_depth<T, V, ES>(), kRows = rows_of(T);
+    extern __shared__ uint4 ring[];
+    __shared__ float2 scratch[2][T / 32];
+    const int t = threadIdx.x % T, sub = threadIdx.x / T;
+    const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + sub * P * 2 * R::kRow;
+    const int stride = gridDim.x * kRows;
+    const int r0 = blockIdx.x * kRows + sub;
+    int turn = 0;
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    auto copy_row = [&](int r, int slot) {
+        R::copy(mine + slot * 2 * R::kRow, a.x, (long long)r * a.ld_x, a.dim, t);
+        R::copy(mine + slot * 2 * R::kRow + R::kRow, a.dy, (long long)r * a.ld_dy, a.dim, t);
+    };
+    const float2 *stats = reinterpret_cast<const float2 *>(a.stats);
+#pragma unroll
+    for (int i = 0; i < P - 1; ++i) {
+        if (r0 + (long long)i * stride < a.rows) copy_row(r0 + i * stride, i);
+        copy_commit();
+    }
+    Run<ES> gamma[V];
+    load_param<T, V, ES>(a.gamma, a.type, t, a.dim, 1.f, gamma);
+    const float inv = 1.f / (float)a.dim;
+    float dg[V][8] = {}, db[V][8] = {};
+    float2 ms = r0 < a.rows ? stats[r0] : make_float2(0.f, 0.f);
+    int slot = 0;
+    for (int r = r0; r < a.rows; r += stride) {
+        const int slot_in = slot == 0 ? P - 1 : slot - 1;
+        if (r + (long long)(P - 1) * stride < a.rows) copy_row(r + (P - 1) * stride, slot_in);
+        copy_commit();
+        const float mean = ms.x, rstd = ms.y;
+        if (r + (long long)stride < a.rows) ms = stats[r + stride];
+        copy_wait<P - 1>();
+        const uint32_t base = mine + slot * 2 * R::kRow;
+        slot = slot + 1 == P ? 0 : slot + 1;
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float x[8], dy[8], g[8];
+            R::load(base, v, t, a.dim, a.type, x);
+            R::load(base + R::kRow, v, t, a.dim, a.type, dy);
+            unpack_run<ES>(gamma[v], a.type, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float xh = (x[e] - mean) * rstd, p = dy[e] * xh;
+                dg[v][e] += p;
+                db[v][e] += dy[e];
+                s1 += dy[e] * g[e];  // zero past the row's end: dy is
+                s2 += p * g[e];
+            }
+        }
+        if (a.dx == nullptr) continue;
+        row_sums<T>(s1, s2, scratch, turn);
+        s1 *= inv, s2 *= inv;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float x[8], dy[8], g[8];
+            R::load(base, v, t, a.dim, a.type, x);
+            R::load(base + R::kRow, v, t, a.dim, a.type, dy);
+            unpack_run<ES>(gamma[v], a.type, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                dy[e] = rstd * (dy[e] * g[e] - s1 - (x[e] - mean) * rstd * s2);
+            store_run<T, true>(a.dx, a.type, (long long)r * a.ld_dx, v, t, a.dim, dy);
+        }
+    }
+    if (a.part == nullptr) return;
+    float *part = a.part + (long long)blockIdx.x * 2 * a.dim;
+    if constexpr (T > 32) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = (v * T + t) * 8;
+            if (c < a.dim) {
+                float4 *q = reinterpret_cast<float4 *>(part + c);
+                q[0] = make_float4(dg[v][0], dg[v][1], dg[v][2], dg[v][3]);
+                q[1] = make_float4(dg[v][4], dg[v][5], dg[v][6], dg[v][7]);
+                q = reinterpret_cast<float4 *>(part + a.dim + c);
+                q[0] = make_float4(db[v][0], db[v][1], db[v][2], db[v][3]);
+                q[1] = make_float4(db[v][4], db[v][5], db[v][6], db[v][7]);
+            }
+        }
+    } else {
+        // the block's rows meet in the ring's memory, gradient by gradient
+        copy_wait<0>();
+        float *acc = reinterpret_cast<float *>(ring);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            __syncthreads();
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    acc[sub * V * 256 + (v * T + t) * 8 + e] = k ? db[v][e] : dg[v][e];
+            __syncthreads();
+            for (int c = threadIdx.x; c < a.dim; c += block_of(T)) {
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) sum += acc[i * V * 256 + c];
+                part[k * a.dim + c] = sum;
+            }
+        }
+    }
+}
+
+// ---- any alignment: one element at a time -------------------------------------
+
+template <int T>
 __global__ void __launch_bounds__(T > 32 ? T : 128)
     norm_forward_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float scratch[T / 32];
@@ -111,7 +434,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 128)
     float s = 0.f;
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
-        load_run<T, VEC>(a.x, a.type, row, v, t, a.dim, x[v]);
+        load_run<T, false>(a.x, a.type, row, v, t, a.dim, x[v]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) s += x[v][e];
     }
@@ -123,7 +446,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 128)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             x[v][e] -= mean;
-            if (col_of<T, VEC>(v, e, t) < a.dim) s += x[v][e] * x[v][e];
+            if (col_of<T, false>(v, e, t) < a.dim) s += x[v][e] * x[v][e];
         }
     const float rstd = 1.f / sqrtf(row_sum<T>(s, scratch) * inv + a.eps);
     if (t == 0 && a.stats != nullptr) {
@@ -134,27 +457,27 @@ __global__ void __launch_bounds__(T > 32 ? T : 128)
     for (int v = 0; v < kV; ++v) {
         float g[8], b[8];
         if (a.gamma != nullptr) {
-            load_run<T, VEC>(a.gamma, a.type, 0, v, t, a.dim, g);
+            load_run<T, false>(a.gamma, a.type, 0, v, t, a.dim, g);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[e] = 1.f;
         }
         if (a.beta != nullptr) {
-            load_run<T, VEC>(a.beta, a.type, 0, v, t, a.dim, b);
+            load_run<T, false>(a.beta, a.type, 0, v, t, a.dim, b);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) b[e] = 0.f;
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[v][e] = x[v][e] * rstd * g[e] + b[e];
-        store_run<T, VEC>(a.y, a.type, (long long)r * a.ld_y, v, t, a.dim, x[v]);
+        store_run<T, false>(a.y, a.type, (long long)r * a.ld_y, v, t, a.dim, x[v]);
     }
 }
 
 // Rows are dealt to `gridDim.x` blocks; a thread keeps the gain's and
 // offset's gradient sums of its own columns over its rows in registers and
 // writes them once, as one row of partials a block.
-template <int T, bool VEC>
+template <int T>
 __global__ void __launch_bounds__(T > 32 ? T : 128)
     norm_backward_kernel(const __grid_constant__ NormArgs a) {
     constexpr int kRows = T > 32 ? 1 : 4;
@@ -172,10 +495,10 @@ __global__ void __launch_bounds__(T > 32 ? T : 128)
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
             float gm[8];
-            load_run<T, VEC>(a.x, a.type, (long long)r * a.ld_x, v, t, a.dim, xh[v]);
-            load_run<T, VEC>(a.dy, a.type, (long long)r * a.ld_dy, v, t, a.dim, g[v]);
+            load_run<T, false>(a.x, a.type, (long long)r * a.ld_x, v, t, a.dim, xh[v]);
+            load_run<T, false>(a.dy, a.type, (long long)r * a.ld_dy, v, t, a.dim, g[v]);
             if (a.gamma != nullptr) {
-                load_run<T, VEC>(a.gamma, a.type, 0, v, t, a.dim, gm);
+                load_run<T, false>(a.gamma, a.type, 0, v, t, a.dim, gm);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) gm[e] = 1.f;
@@ -197,7 +520,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 128)
         for (int v = 0; v < kV; ++v) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[v][e] = rstd * (g[v][e] - s1 - xh[v][e] * s2);
-            store_run<T, VEC>(a.dx, a.type, (long long)r * a.ld_dx, v, t, a.dim, g[v]);
+            store_run<T, false>(a.dx, a.type, (long long)r * a.ld_dx, v, t, a.dim, g[v]);
         }
     }
     if (a.part == nullptr) return;
@@ -207,7 +530,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 128)
         for (int v = 0; v < kV; ++v)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int c = col_of<T, VEC>(v, e, t);
+                const int c = col_of<T, false>(v, e, t);
                 if (c < a.dim) part[c] = dg[v][e], part[a.dim + c] = db[v][e];
             }
     } else {
@@ -219,7 +542,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 128)
             for (int v = 0; v < kV; ++v)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    s_acc[sub * 1024 + col_of<T, VEC>(v, e, t)] = k ? db[v][e] : dg[v][e];
+                    s_acc[sub * 1024 + col_of<T, false>(v, e, t)] = k ? db[v][e] : dg[v][e];
             __syncthreads();
             for (int c = threadIdx.x; c < a.dim; c += 32 * kRows) {
                 float sum = 0.f;
@@ -231,22 +554,27 @@ __global__ void __launch_bounds__(T > 32 ? T : 128)
     }
 }
 
-// Column sums of the blocks' partials: dgamma in the first dim columns,
-// dbeta in the rest.
-__global__ void __launch_bounds__(256) norm_sum_kernel(const float *part, int blocks, int dim,
-                                                       void *dgamma, void *dbeta, int type) {
-    __shared__ float s_sum[8][33];
+// Column sums of the blocks' partials (read from L2, where they were just
+// written): dgamma in the first dim columns, dbeta in the rest.  A block
+// takes 32 columns; each of its 16 warps adds every sixteenth row, and the
+// sums meet in order.
+constexpr int kSumWarps = 16;
+__global__ void __launch_bounds__(32 * kSumWarps)
+    norm_sum_kernel(const float *part, int blocks, int dim, void *dgamma, void *dbeta, int type) {
+    __shared__ float s_sum[kSumWarps][32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float t = 0.f;
-    if (c < 2 * dim)
-        for (int b = warp; b < blocks; b += 8) t += part[(long long)b * 2 * dim + c];
+    if (c < 2 * dim) {
+#pragma unroll 8
+        for (int b = warp; b < blocks; b += kSumWarps) t += __ldcg(part + (long long)b * 2 * dim + c);
+    }
     s_sum[warp][lane] = t;
     __syncthreads();
     if (warp == 0 && c < 2 * dim) {
 #pragma unroll
-        for (int w = 1; w < 8; ++w) t += s_sum[w][lane];
+        for (int w = 1; w < kSumWarps; ++w) t += s_sum[w][lane];
         if (c < dim) {
             if (dgamma != nullptr) store_elem(dgamma, type, c, t);
         } else if (dbeta != nullptr) {
@@ -256,11 +584,12 @@ __global__ void __launch_bounds__(256) norm_sum_kernel(const float *part, int bl
 }
 
 template <class... P, class... A>
-cudaError_t launch_pdl(void (*fn)(P...), dim3 grid, dim3 block, cudaStream_t stream, A... args) {
+cudaError_t launch_pdl(void (*fn)(P...), int grid, int block, size_t smem, cudaStream_t stream, A... args) {
     cudaLaunchConfig_t c = {};
     cudaLaunchAttribute attr[1];
-    c.gridDim = grid;
-    c.blockDim = block;
+    c.gridDim = dim3(grid);
+    c.blockDim = dim3(block);
+    c.dynamicSmemBytes = smem;
     c.stream = stream;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -276,38 +605,115 @@ bool rows_aligned(const void *p, long long ld, int esize) {
 // Threads of a row: 32 values a thread at most.
 int threads_of(int dim) { return dim <= 1024 ? 32 : dim <= 4096 ? 128 : dim <= 8192 ? 256 : 512; }
 
-template <bool VEC>
-cudaError_t forward(const NormArgs &a, cudaStream_t stream) {
+int blocks_for(int rows, int t, int most) {
+    const int need = (rows + rows_of(t) - 1) / rows_of(t);
+    return need < most ? need : most;
+}
+
+template <int T, int V, int ES>
+constexpr size_t fwd_smem() {
+    return (size_t)fwd_depth<T, V, ES>() * rows_of(T) * Ring<T, V, ES>::kRow;
+}
+template <int T, int V, int ES>
+constexpr size_t bwd_smem() {
+    return (size_t)bwd_depth<T, V, ES>() * rows_of(T) * 2 * Ring<T, V, ES>::kRow;
+}
+
+// FP32 rows past 8192: two places of x and dy would not fit.
+template <int T, int ES>
+constexpr bool kHasBackwardRing = !(T == 512 && ES == 4);
+
+template <int T, int V, int ES>
+cudaError_t configure_one() {
+    static_assert(fwd_smem<T, V, ES>() <= 224 * 1024, "shared memory");
+    static_assert(!kHasBackwardRing<T, ES> || bwd_smem<T, V, ES>() <= 224 * 1024, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(norm_forward_ring_kernel<T, V, ES>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)fwd_smem<T, V, ES>());
+    if constexpr (kHasBackwardRing<T, ES>)
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(norm_backward_ring_kernel<T, V, ES>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)bwd_smem<T, V, ES>());
+    return e;
+}
+template <int ES>
+cudaError_t configure_type() {
+    cudaError_t e = configure_one<32, 1, ES>();
+    if (e == cudaSuccess) e = configure_one<32, 4, ES>();
+    if (e == cudaSuccess) e = configure_one<128, 4, ES>();
+    if (e == cudaSuccess) e = configure_one<256, 4, ES>();
+    if (e == cudaSuccess) e = configure_one<512, 4, ES>();
+    return e;
+}
+
+template <int T, int V, int ES>
+cudaError_t forward_ring(const NormArgs &a, cudaStream_t stream) {
+    return launch_pdl(norm_forward_ring_kernel<T, V, ES>,
+                      blocks_for(a.rows, T, a.sms * fwd_blocks(T, ES)), block_of(T),
+                      fwd_smem<T, V, ES>(), stream, a);
+}
+template <int ES>
+cudaError_t forward_aligned(const NormArgs &a, cudaStream_t stream) {
+    if (a.dim <= 256) return forward_ring<32, 1, ES>(a, stream);
     switch (threads_of(a.dim)) {
-        case 32: return launch_pdl(norm_forward_kernel<32, VEC>, dim3((a.rows + 3) / 4), dim3(128), stream, a);
-        case 128: return launch_pdl(norm_forward_kernel<128, VEC>, dim3(a.rows), dim3(128), stream, a);
-        case 256: return launch_pdl(norm_forward_kernel<256, VEC>, dim3(a.rows), dim3(256), stream, a);
-        default: return launch_pdl(norm_forward_kernel<512, VEC>, dim3(a.rows), dim3(512), stream, a);
+        case 32: return forward_ring<32, 4, ES>(a, stream);
+        case 128: return forward_ring<128, 4, ES>(a, stream);
+        case 256: return forward_ring<256, 4, ES>(a, stream);
+        default: return forward_ring<512, 4, ES>(a, stream);
     }
 }
 
-template <bool VEC>
-cudaError_t backward(const NormArgs &a, int grid, cudaStream_t stream) {
+cudaError_t backward_any(const NormArgs &a, int *grid, cudaStream_t stream) {
+    const int t = threads_of(a.dim);
+    *grid = blocks_for(a.rows, t, 2 * a.sms);
+    return launch_pdl(t == 32    ? norm_backward_kernel<32>
+                      : t == 128 ? norm_backward_kernel<128>
+                      : t == 256 ? norm_backward_kernel<256>
+                                 : norm_backward_kernel<512>,
+                      *grid, block_of(t), 0, stream, a);
+}
+
+template <int T, int V, int ES>
+cudaError_t backward_ring(const NormArgs &a, int *grid, cudaStream_t stream) {
+    *grid = blocks_for(a.rows, T, a.sms * bwd_blocks(T, ES));
+    return launch_pdl(norm_backward_ring_kernel<T, V, ES>, *grid, block_of(T),
+                      bwd_smem<T, V, ES>(), stream, a);
+}
+template <int ES>
+cudaError_t backward_aligned(const NormArgs &a, int *grid, cudaStream_t stream) {
+    if (a.dim <= 256) return backward_ring<32, 1, ES>(a, grid, stream);
     switch (threads_of(a.dim)) {
-        case 32: return launch_pdl(norm_backward_kernel<32, VEC>, dim3(grid), dim3(128), stream, a);
-        case 128: return launch_pdl(norm_backward_kernel<128, VEC>, dim3(grid), dim3(128), stream, a);
-        case 256: return launch_pdl(norm_backward_kernel<256, VEC>, dim3(grid), dim3(256), stream, a);
-        default: return launch_pdl(norm_backward_kernel<512, VEC>, dim3(grid), dim3(512), stream, a);
+        case 32: return backward_ring<32, 4, ES>(a, grid, stream);
+        case 128: return backward_ring<128, 4, ES>(a, grid, stream);
+        case 256: return backward_ring<256, 4, ES>(a, grid, stream);
+        default:
+            if constexpr (kHasBackwardRing<512, ES>) return backward_ring<512, 4, ES>(a, grid, stream);
+            return backward_any(a, grid, stream);
     }
 }
 
+cudaError_t forward_any(const NormArgs &a, cudaStream_t stream) {
+    const int t = threads_of(a.dim), grid = (a.rows + rows_of(t) - 1) / rows_of(t);
+    return launch_pdl(t == 32    ? norm_forward_kernel<32>
+                      : t == 128 ? norm_forward_kernel<128>
+                      : t == 256 ? norm_forward_kernel<256>
+                                 : norm_forward_kernel<512>,
+                      grid, block_of(t), 0, stream, a);
+}
 }  // namespace
 
-size_t norm_part_floats(int dim, int sms) {
-    (void)sms;
-    return (size_t)kMaxPart * 2 * dim;
+cudaError_t norm_configure() {
+    const cudaError_t e = configure_type<2>();
+    return e == cudaSuccess ? configure_type<4>() : e;
 }
+
+size_t norm_part_floats(int dim, int sms) { return (size_t)kMaxBlocks * sms * 2 * dim; }
 
 cudaError_t norm_forward_launch(const NormArgs &a, cudaStream_t stream) {
     const int es = layer_esize(a.type);
     const bool vec = a.dim % 8 == 0 && rows_aligned(a.x, a.ld_x, es) && rows_aligned(a.y, a.ld_y, es) &&
                      rows_aligned(a.gamma, 0, es) && rows_aligned(a.beta, 0, es);
-    return vec ? forward<true>(a, stream) : forward<false>(a, stream);
+    return !vec ? forward_any(a, stream) : es == 2 ? forward_aligned<2>(a, stream) : forward_aligned<4>(a, stream);
 }
 
 cudaError_t norm_backward_launch(const NormArgs &args, cudaStream_t stream) {
@@ -317,12 +723,12 @@ cudaError_t norm_backward_launch(const NormArgs &args, cudaStream_t stream) {
     if (!sums) a.part = nullptr;
     const bool vec = a.dim % 8 == 0 && rows_aligned(a.x, a.ld_x, es) && rows_aligned(a.dy, a.ld_dy, es) &&
                      rows_aligned(a.dx, a.ld_dx, es) && rows_aligned(a.gamma, 0, es);
-    const int per = threads_of(a.dim) == 32 ? 4 : 1;
-    int grid = (a.rows + per - 1) / per;
-    grid = grid < kMaxPart ? grid : kMaxPart;
-    const cudaError_t e = vec ? backward<true>(a, grid, stream) : backward<false>(a, grid, stream);
+    int grid = 0;
+    const cudaError_t e = !vec      ? backward_any(a, &grid, stream)
+                          : es == 2 ? backward_aligned<2>(a, &grid, stream)
+                                    : backward_aligned<4>(a, &grid, stream);
     if (e != cudaSuccess || !sums) return e;
-    return launch_pdl(norm_sum_kernel, dim3((2 * a.dim + 31) / 32), dim3(256), stream,
+    return launch_pdl(norm_sum_kernel, (2 * a.dim + 31) / 32, 32 * kSumWarps, 0, stream,
                       static_cast<const float *>(a.part), grid, a.dim, a.dgamma, a.dbeta, a.type);
 }
 
