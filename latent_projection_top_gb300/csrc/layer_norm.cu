@@ -9,6 +9,7 @@
 // from the mean, not a difference of large sums.  Sums are FP32.
 #include "layer.cuh"
 #include "layer_math.cuh"
+#include "sm103_ptx.cuh"
 
 namespace route {
 namespace {
@@ -106,74 +107,108 @@ __device__ __forceinline__ float row_sum(float v, float *scratch) {
 // places of a ring (cp.async: no registers held, no barrier to hand a row
 // over), and per row the block meets only to add the row's sums.
 
-// Eight values as they lie in memory.
-template <int ES>
+// Eight values as they lie in memory, and as four pairs: the arithmetic runs
+// on FP32 pairs (fma.rn.f32x2), half the instructions, which at two or three
+// blocks an SM bound the backward pass before memory does.
+template <int TY>
 struct Run {
-    uint32_t w[2 * ES];
+    uint32_t w[2 * layer_esize(TY)];
 };
-template <int ES>
-__device__ __forceinline__ void unpack_run(const Run<ES> &q, int type, float (&x)[8]) {
-    if constexpr (ES == 4) {
+template <int TY>
+__device__ __forceinline__ void unpack_run(const Run<TY> &q, uint64_t (&x)[4]) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(q.w[e]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack16(q.w[e], type);
-            x[2 * e] = f.x, x[2 * e + 1] = f.y;
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (TY == kFp32) {
+            x[e] = ptx::f32x2_pack(__uint_as_float(q.w[2 * e]), __uint_as_float(q.w[2 * e + 1]));
+        } else {
+            const float2 f = unpack16(q.w[e], TY);
+            x[e] = ptx::f32x2_pack(f.x, f.y);
         }
     }
 }
+// The same of a parameter's run inside the loop over rows.  Unpacking does
+// not change from row to row, and hoisted out of the loop it would hold twice
+// the registers and spill (forward 16384x7168: 171 us); the empty statement
+// keeps it in.
+template <int TY>
+__device__ __forceinline__ void unpack_param(Run<TY> &q, uint64_t (&x)[4]) {
+    if constexpr (TY != kFp32)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) asm volatile("" : "+r"(q.w[e]));
+    unpack_run<TY>(q, x);
+}
+__device__ __forceinline__ uint64_t pair(float v) { return ptx::f32x2_pack(v, v); }
+__device__ __forceinline__ float pair_sum(uint64_t v) {
+    float a, b;
+    ptx::f32x2_unpack(v, a, b);
+    return a + b;
+}
+__device__ __forceinline__ void unpair(const uint64_t (&x)[4], float (&f)[8]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ptx::f32x2_unpack(x[e], f[2 * e], f[2 * e + 1]);
+}
 
-template <int T, int V, int ES>
+// A row's T threads (a block, or a warp) hold V runs of eight values each.
+template <int V, int TY>
 struct Ring {
-    static constexpr int kHalves = ES / 2;                       // 16-byte vectors of a run
-    static constexpr uint32_t kRow = (uint32_t)V * kHalves * T * 16;  // bytes of a row's place
+    static constexpr int ES = layer_esize(TY);
+    static constexpr int kHalves = ES / 2;  // 16-byte vectors of a run
+    // bytes of a row's place
+    static __host__ __device__ constexpr uint32_t row_bytes(int T) { return (uint32_t)V * kHalves * T * 16; }
     // The vector `h` of run v of thread t: neighbours in t are neighbours in
     // shared memory.
-    static __device__ __forceinline__ uint32_t at(uint32_t base, int v, int h, int t) {
+    static __device__ __forceinline__ uint32_t at(uint32_t base, int v, int h, int T, int t) {
         return base + (uint32_t)((v * kHalves + h) * T + t) * 16u;
     }
-    static __device__ __forceinline__ void copy(uint32_t base, const void *p, long long row, int dim, int t) {
+    static __device__ __forceinline__ void copy(uint32_t base, const void *p, long long row, int dim,
+                                                int T, int t) {
+        const char *src = static_cast<const char *>(p) + (row + t * 8) * ES;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = (v * T + t) * 8;
-            if (c < dim) {
-                const char *src = static_cast<const char *>(p) + (row + c) * ES;
+        for (int v = 0; v < V; ++v)
+            if ((v * T + t) * 8 < dim)
 #pragma unroll
                 for (int h = 0; h < kHalves; ++h)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(base, v, h, t)),
-                                 "l"(src + 16 * h)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(base, v, h, T, t)),
+                                 "l"(src + (v * T * 8 * ES + 16 * h))
                                  : "memory");
-            }
-        }
     }
-    static __device__ __forceinline__ void load(uint32_t base, int v, int t, int dim, int type, float (&x)[8]) {
-        Run<ES> q;
-        if ((v * T + t) * 8 < dim) {
+    static __device__ __forceinline__ void load(uint32_t base, int v, int T, int t, Run<TY> &q) {
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h)
-                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(q.w[4 * h]), "=r"(q.w[4 * h + 1]), "=r"(q.w[4 * h + 2]),
-                               "=r"(q.w[4 * h + 3])
-                             : "r"(at(base, v, h, t))
-                             : "memory");
-        } else {
-#pragma unroll
-            for (int e = 0; e < 2 * ES; ++e) q.w[e] = 0u;
-        }
-        unpack_run<ES>(q, type, x);
+        for (int h = 0; h < kHalves; ++h)
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(q.w[4 * h]), "=r"(q.w[4 * h + 1]), "=r"(q.w[4 * h + 2]),
+                           "=r"(q.w[4 * h + 3])
+                         : "r"(at(base, v, h, T, t))
+                         : "memory");
+    }
+    static __device__ __forceinline__ void load(uint32_t base, int v, int T, int t, uint64_t (&x)[4]) {
+        Run<TY> q;
+        load(base, v, T, t, q);
+        unpack_run<TY>(q, x);
     }
 };
 
+// Store a run; 16-byte aligned rows.
+template <int TY>
+__device__ __forceinline__ void store_pairs(void *p, long long i, const uint64_t (&x)[4]) {
+    float f[8];
+    unpair(x, f);
+    if constexpr (TY == kFp32) {
+        float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
+        q[0] = make_float4(f[0], f[1], f[2], f[3]);
+        q[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) =
+            make_uint4(pack16(f[0], f[1], TY), pack16(f[2], f[3], TY), pack16(f[4], f[5], TY),
+                       pack16(f[6], f[7], TY));
+    }
+}
+
 // A parameter's values of this thread, kept packed in registers.
-template <int T, int V, int ES>
-__device__ __forceinline__ void load_param(const void *p, int type, int t, int dim, float none, Run<ES> (&q)[V]) {
-    uint32_t fill;
-    if (ES == 4)
-        fill = __float_as_uint(none);
-    else
-        fill = pack16(none, none, type);
+template <int V, int TY>
+__device__ __forceinline__ void load_param(const void *p, int T, int t, int dim, float none, Run<TY> (&q)[V]) {
+    constexpr int ES = layer_esize(TY);
+    const uint32_t fill = TY == kFp32 ? __float_as_uint(none) : pack16(none, none, TY);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int c = (v * T + t) * 8;
@@ -191,24 +226,25 @@ __device__ __forceinline__ void load_param(const void *p, int type, int t, int d
     }
 }
 
-// Sums of a and b over a row's T threads, the same in every thread and every
+// Sums of a and b over a row's threads, the same in every thread and every
 // run.  One barrier: consecutive sums use alternate scratch.
-template <int T>
-__device__ __forceinline__ void row_sums(float &a, float &b, float2 (*scratch)[T / 32], int &turn) {
+template <int MAXT>
+__device__ __forceinline__ void row_sums(float &a, float &b, float2 (*scratch)[MAXT / 32], int &turn, int T) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
         b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
     }
-    if constexpr (T > 32) {
+    if constexpr (MAXT > 32) {
         if ((threadIdx.x & 31) == 0) scratch[turn][threadIdx.x >> 5] = make_float2(a, b);
         __syncthreads();
         a = b = 0.f;
 #pragma unroll
-        for (int i = 0; i < T / 32; ++i) {
-            const float2 s = scratch[turn][i];
-            a += s.x, b += s.y;
-        }
+        for (int i = 0; i < MAXT / 32; ++i)
+            if (32 * i < T) {
+                const float2 s = scratch[turn][i];
+                a += s.x, b += s.y;
+            }
         turn ^= 1;
     }
 }
@@ -222,87 +258,110 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 __host__ __device__ constexpr int block_of(int t) { return t > 32 ? t : 128; }
 __host__ __device__ constexpr int rows_of(int t) { return block_of(t) / t; }
 
-// Blocks an SM and rows of a ring: up to ~190 KB of rows an SM.
-__host__ __device__ constexpr int fwd_blocks(int t, int es) {
-    return t <= 128 ? (es == 2 ? 5 : 4) : t == 256 ? (es == 2 ? 3 : 2) : 1;
+// Blocks an SM and rows of a ring: up to ~190 KB of rows an SM.  `t`: the
+// most threads of a row that a kernel is made for.
+__host__ __device__ constexpr int fwd_blocks(int t, int ty) {
+    return t <= 128 ? (ty != kFp32 ? 5 : 4) : t == 256 ? (ty != kFp32 ? 3 : 2) : 1;
 }
-template <int T, int V, int ES>
+__host__ __device__ constexpr int bwd_blocks(int t, int ty) {
+    return t == 32 ? 3 : t == 128 ? 3 : t == 256 ? (ty != kFp32 ? 2 : 1) : 1;
+}
+__host__ __device__ constexpr int depth_of(uint32_t block_bytes, uint32_t row_bytes) {
+    const uint32_t d = block_bytes / row_bytes;
+    return d > 6 ? 6 : d < 2 ? 2 : (int)d;
+}
+template <int T, int V, int TY>
 __host__ __device__ constexpr int fwd_depth() {
-    constexpr uint32_t per = 190u * 1024u / fwd_blocks(T, ES) / (Ring<T, V, ES>::kRow * rows_of(T));
-    return per > 6 ? 6 : per < 2 ? 2 : (int)per;
+    return depth_of(190u * 1024u / fwd_blocks(T, TY), Ring<V, TY>::row_bytes(T) * rows_of(T));
 }
-__host__ __device__ constexpr int bwd_blocks(int t, int es) {
-    return t == 32 ? 3 : t == 128 ? 3 : t == 256 ? (es == 2 ? 2 : 1) : 1;
-}
-template <int T, int V, int ES>
+template <int T, int V, int TY>
 __host__ __device__ constexpr int bwd_depth() {
-    constexpr uint32_t per = 190u * 1024u / bwd_blocks(T, ES) / (2 * Ring<T, V, ES>::kRow * rows_of(T));
-    return per > 6 ? 6 : per < 2 ? 2 : (int)per;
+    return depth_of(190u * 1024u / bwd_blocks(T, TY), 2 * Ring<V, TY>::row_bytes(T) * rows_of(T));
 }
 
-template <int T, int V, int ES>
-__global__ void __launch_bounds__(block_of(T), fwd_blocks(T, ES))
+// MAXT: 32 (a warp a row, four rows a block), else the most threads of a
+// block, which holds one row.
+template <int MAXT, int V, int TY>
+__global__ void __launch_bounds__(block_of(MAXT), fwd_blocks(MAXT, TY))
     norm_forward_ring_kernel(const __grid_constant__ NormArgs a) {
-    using R = Ring<T, V, ES>;
-    constexpr int P = fwd_depth<T, V, ES>(), kRows = rows_of(T);
+    using R = Ring<V, TY>;
+    constexpr int P = fwd_depth<MAXT, V, TY>(), kRows = rows_of(MAXT);
     extern __shared__ uint4 ring[];
-    __shared__ float2 scratch[2][T / 32];
+    __shared__ float2 scratch[2][MAXT / 32];
+    const int T = MAXT == 32 ? 32 : blockDim.x;
     const int t = threadIdx.x % T;
-    const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + (threadIdx.x / T) * P * R::kRow;
+    const uint32_t place = R::row_bytes(T);
+    const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + (threadIdx.x / T) * P * place;
     const int stride = gridDim.x * kRows;
     const int r0 = blockIdx.x * kRows + threadIdx.x / T;
     int turn = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < P - 1; ++i) {
-        if (r0 + (long long)i * stride < a.rows)
-            R::copy(mine + i * R::kRow, a.x, (long long)(r0 + i * stride) * a.ld_x, a.dim, t);
+        if (r0 + i * stride < a.rows)
+            R::copy(mine + i * place, a.x, (long long)(r0 + i * stride) * a.ld_x, a.dim, T, t);
         copy_commit();
     }
-    Run<ES> gamma[V], beta[V];
-    load_param<T, V, ES>(a.gamma, a.type, t, a.dim, 1.f, gamma);
-    load_param<T, V, ES>(a.beta, a.type, t, a.dim, 0.f, beta);
+    Run<TY> gamma[V], beta[V];
+    load_param<V, TY>(a.gamma, T, t, a.dim, 1.f, gamma);
+    load_param<V, TY>(a.beta, T, t, a.dim, 0.f, beta);
     const float inv = 1.f / (float)a.dim;
     int slot = 0;
     for (int r = r0; r < a.rows; r += stride) {
         const int slot_in = slot == 0 ? P - 1 : slot - 1;
-        if (r + (long long)(P - 1) * stride < a.rows)
-            R::copy(mine + slot_in * R::kRow, a.x, (long long)(r + (P - 1) * stride) * a.ld_x, a.dim, t);
+        if (r + (P - 1) * stride < a.rows)
+            R::copy(mine + slot_in * place, a.x, (long long)(r + (P - 1) * stride) * a.ld_x, a.dim, T, t);
         copy_commit();
         copy_wait<P - 1>();
-        const uint32_t base = mine + slot * R::kRow;
+        const uint32_t base = mine + slot * place;
         slot = slot + 1 == P ? 0 : slot + 1;
-        float x[V][8], s = 0.f, none = 0.f;
+        // the row stays packed: unpacking it again costs less than the registers
+        Run<TY> q[V];
+        uint64_t acc = 0u;
+        float none = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            R::load(base, v, t, a.dim, a.type, x[v]);
+            if ((v * T + t) * 8 >= a.dim) break;
+            uint64_t x[4];
+            R::load(base, v, T, t, q[v]);
+            unpack_run<TY>(q[v], x);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s += x[v][e];
+            for (int e = 0; e < 4; ++e) acc = ptx::f32x2_add(acc, x[e]);
         }
-        row_sums<T>(s, none, scratch, turn);
+        float s = pair_sum(acc);
+        row_sums<MAXT>(s, none, scratch, turn, T);
         const float mean = s * inv;
-        s = 0.f;
+        const uint64_t mean2 = pair(mean);
+        acc = 0u;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const bool in = (v * T + t) * 8 < a.dim;
+            if ((v * T + t) * 8 >= a.dim) break;
+            uint64_t x[4];
+            unpack_run<TY>(q[v], x);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[v][e] -= mean;
-                if (in) s += x[v][e] * x[v][e];
+            for (int e = 0; e < 4; ++e) {
+                x[e] = ptx::f32x2_sub(x[e], mean2);
+                acc = ptx::f32x2_fma(x[e], x[e], acc);
             }
         }
-        row_sums<T>(s, none, scratch, turn);
+        s = pair_sum(acc);
+        row_sums<MAXT>(s, none, scratch, turn, T);
         const float rstd = 1.f / sqrtf(s * inv + a.eps);
+        const uint64_t rstd2 = pair(rstd);
         if (t == 0 && a.stats != nullptr)
             *reinterpret_cast<float2 *>(a.stats + 2 * (long long)r) = make_float2(mean, rstd);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float g[8], b[8];
-            unpack_run<ES>(gamma[v], a.type, g);
-            unpack_run<ES>(beta[v], a.type, b);
+            const int c = (v * T + t) * 8;
+            if (c >= a.dim) break;
+            uint64_t x[4], g[4], b[4];
+            unpack_run<TY>(q[v], x);
+            unpack_param<TY>(gamma[v], g);
+            unpack_param<TY>(beta[v], b);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[v][e] = x[v][e] * rstd * g[e] + b[e];
-            store_run<T, true>(a.y, a.type, (long long)r * a.ld_y, v, t, a.dim, x[v]);
+            for (int e = 0; e < 4; ++e)
+                g[e] = ptx::f32x2_fma(ptx::f32x2_mul(ptx::f32x2_sub(x[e], mean2), rstd2), g[e], b[e]);
+            store_pairs<TY>(a.y, (long long)r * a.ld_y + c, g);
         }
     }
 }
@@ -310,89 +369,97 @@ __global__ void __launch_bounds__(block_of(T), fwd_blocks(T, ES))
 // A thread keeps the gain's and offset's gradient sums of its own columns
 // over its rows in registers and writes them once, as a row of partials a
 // block; x and dy are read from the ring twice rather than kept.
-template <int T, int V, int ES>
-__global__ void __launch_bounds__(block_of(T), bwd_blocks(T, ES))
+template <int MAXT, int V, int TY>
+__global__ void __launch_bounds__(block_of(MAXT), bwd_blocks(MAXT, TY))
     norm_backward_ring_kernel(const __grid_constant__ NormArgs a) {
-    using R = Ring<T, V, ES>;
-    constexpr int P = bwd_depth<T, V, ES>(), kRows = rows_of(T);
+    using R = Ring<V, TY>;
+    constexpr int P = bwd_depth<MAXT, V, TY>(), kRows = rows_of(MAXT);
     extern __shared__ uint4 ring[];
-    __shared__ float2 scratch[2][T / 32];
+    __shared__ float2 scratch[2][MAXT / 32];
+    const int T = MAXT == 32 ? 32 : blockDim.x;
     const int t = threadIdx.x % T, sub = threadIdx.x / T;
-    const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + sub * P * 2 * R::kRow;
+    const uint32_t place = R::row_bytes(T);
+    const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + sub * P * 2 * place;
     const int stride = gridDim.x * kRows;
     const int r0 = blockIdx.x * kRows + sub;
     int turn = 0;
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     auto copy_row = [&](int r, int slot) {
-        R::copy(mine + slot * 2 * R::kRow, a.x, (long long)r * a.ld_x, a.dim, t);
-        R::copy(mine + slot * 2 * R::kRow + R::kRow, a.dy, (long long)r * a.ld_dy, a.dim, t);
+        R::copy(mine + slot * 2 * place, a.x, (long long)r * a.ld_x, a.dim, T, t);
+        R::copy(mine + slot * 2 * place + place, a.dy, (long long)r * a.ld_dy, a.dim, T, t);
     };
     const float2 *stats = reinterpret_cast<const float2 *>(a.stats);
 #pragma unroll
     for (int i = 0; i < P - 1; ++i) {
-        if (r0 + (long long)i * stride < a.rows) copy_row(r0 + i * stride, i);
+        if (r0 + i * stride < a.rows) copy_row(r0 + i * stride, i);
         copy_commit();
     }
-    Run<ES> gamma[V];
-    load_param<T, V, ES>(a.gamma, a.type, t, a.dim, 1.f, gamma);
+    Run<TY> gamma[V];
+    load_param<V, TY>(a.gamma, T, t, a.dim, 1.f, gamma);
     const float inv = 1.f / (float)a.dim;
-    float dg[V][8] = {}, db[V][8] = {};
+    uint64_t dg[V][4] = {}, db[V][4] = {};
     float2 ms = r0 < a.rows ? stats[r0] : make_float2(0.f, 0.f);
     int slot = 0;
     for (int r = r0; r < a.rows; r += stride) {
         const int slot_in = slot == 0 ? P - 1 : slot - 1;
-        if (r + (long long)(P - 1) * stride < a.rows) copy_row(r + (P - 1) * stride, slot_in);
+        if (r + (P - 1) * stride < a.rows) copy_row(r + (P - 1) * stride, slot_in);
         copy_commit();
-        const float mean = ms.x, rstd = ms.y;
-        if (r + (long long)stride < a.rows) ms = stats[r + stride];
+        const float rstd = ms.y;
+        const uint64_t rstd2 = pair(rstd), shift2 = pair(-ms.x * rstd);  // xh = x rstd - mean rstd
+        if (r + stride < a.rows) ms = stats[r + stride];
         copy_wait<P - 1>();
-        const uint32_t base = mine + slot * 2 * R::kRow;
+        const uint32_t base = mine + slot * 2 * place;
         slot = slot + 1 == P ? 0 : slot + 1;
-        float s1 = 0.f, s2 = 0.f;
+        uint64_t a1 = 0u, a2 = 0u;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float x[8], dy[8], g[8];
-            R::load(base, v, t, a.dim, a.type, x);
-            R::load(base + R::kRow, v, t, a.dim, a.type, dy);
-            unpack_run<ES>(gamma[v], a.type, g);
+            if ((v * T + t) * 8 >= a.dim) break;
+            uint64_t x[4], dy[4], g[4];
+            R::load(base, v, T, t, x);
+            R::load(base + place, v, T, t, dy);
+            unpack_param<TY>(gamma[v], g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float xh = (x[e] - mean) * rstd, p = dy[e] * xh;
-                dg[v][e] += p;
-                db[v][e] += dy[e];
-                s1 += dy[e] * g[e];  // zero past the row's end: dy is
-                s2 += p * g[e];
+            for (int e = 0; e < 4; ++e) {
+                const uint64_t xh = ptx::f32x2_fma(x[e], rstd2, shift2);
+                const uint64_t gy = ptx::f32x2_mul(dy[e], g[e]);
+                dg[v][e] = ptx::f32x2_fma(dy[e], xh, dg[v][e]);
+                db[v][e] = ptx::f32x2_add(dy[e], db[v][e]);
+                a1 = ptx::f32x2_add(a1, gy);
+                a2 = ptx::f32x2_fma(gy, xh, a2);
             }
         }
         if (a.dx == nullptr) continue;
-        row_sums<T>(s1, s2, scratch, turn);
-        s1 *= inv, s2 *= inv;
+        float s1 = pair_sum(a1), s2 = pair_sum(a2);
+        row_sums<MAXT>(s1, s2, scratch, turn, T);
+        // dx = rstd g dy - (rstd s1 + rstd s2 xh)
+        const uint64_t k1 = pair(-rstd * s1 * inv), k2 = pair(-rstd * s2 * inv);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float x[8], dy[8], g[8];
-            R::load(base, v, t, a.dim, a.type, x);
-            R::load(base + R::kRow, v, t, a.dim, a.type, dy);
-            unpack_run<ES>(gamma[v], a.type, g);
+            const int c = (v * T + t) * 8;
+            if (c >= a.dim) break;
+            uint64_t x[4], dy[4], g[4];
+            R::load(base, v, T, t, x);
+            R::load(base + place, v, T, t, dy);
+            unpack_param<TY>(gamma[v], g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                dy[e] = rstd * (dy[e] * g[e] - s1 - (x[e] - mean) * rstd * s2);
-            store_run<T, true>(a.dx, a.type, (long long)r * a.ld_dx, v, t, a.dim, dy);
+            for (int e = 0; e < 4; ++e) {
+                const uint64_t xh = ptx::f32x2_fma(x[e], rstd2, shift2);
+                const uint64_t gy = ptx::f32x2_mul(ptx::f32x2_mul(dy[e], g[e]), rstd2);
+                dy[e] = ptx::f32x2_add(gy, ptx::f32x2_fma(xh, k2, k1));
+            }
+            store_pairs<TY>(a.dx, (long long)r * a.ld_dx + c, dy);
         }
     }
     if (a.part == nullptr) return;
     float *part = a.part + (long long)blockIdx.x * 2 * a.dim;
-    if constexpr (T > 32) {
+    if constexpr (MAXT > 32) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = (v * T + t) * 8;
             if (c < a.dim) {
-                float4 *q = reinterpret_cast<float4 *>(part + c);
-                q[0] = make_float4(dg[v][0], dg[v][1], dg[v][2], dg[v][3]);
-                q[1] = make_float4(dg[v][4], dg[v][5], dg[v][6], dg[v][7]);
-                q = reinterpret_cast<float4 *>(part + a.dim + c);
-                q[0] = make_float4(db[v][0], db[v][1], db[v][2], db[v][3]);
-                q[1] = make_float4(db[v][4], db[v][5], db[v][6], db[v][7]);
+                store_pairs<kFp32>(part, c, dg[v]);
+                store_pairs<kFp32>(part, a.dim + c, db[v]);
             }
         }
     } else {
@@ -404,11 +471,9 @@ __global__ void __launch_bounds__(block_of(T), bwd_blocks(T, ES))
             __syncthreads();
 #pragma unroll
             for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    acc[sub * V * 256 + (v * T + t) * 8 + e] = k ? db[v][e] : dg[v][e];
+                store_pairs<kFp32>(acc, sub * V * 256 + (v * T + t) * 8, k ? db[v] : dg[v]);
             __syncthreads();
-            for (int c = threadIdx.x; c < a.dim; c += block_of(T)) {
+            for (int c = threadIdx.x; c < a.dim; c += block_of(MAXT)) {
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < kRows; ++i) sum += acc[i * V * 256 + c];
@@ -605,61 +670,65 @@ bool rows_aligned(const void *p, long long ld, int esize) {
 // Threads of a row: 32 values a thread at most.
 int threads_of(int dim) { return dim <= 1024 ? 32 : dim <= 4096 ? 128 : dim <= 8192 ? 256 : 512; }
 
+// Threads of a ring kernel's block: as few whole warps as hold the row in
+// four runs a thread.
+int threads_for(int t, int dim) { return t == 32 ? block_of(t) : ((dim + 31) / 32 + 31) / 32 * 32; }
+
 int blocks_for(int rows, int t, int most) {
     const int need = (rows + rows_of(t) - 1) / rows_of(t);
     return need < most ? need : most;
 }
 
-template <int T, int V, int ES>
+template <int T, int V, int TY>
 constexpr size_t fwd_smem() {
-    return (size_t)fwd_depth<T, V, ES>() * rows_of(T) * Ring<T, V, ES>::kRow;
+    return (size_t)fwd_depth<T, V, TY>() * rows_of(T) * Ring<V, TY>::row_bytes(T);
 }
-template <int T, int V, int ES>
+template <int T, int V, int TY>
 constexpr size_t bwd_smem() {
-    return (size_t)bwd_depth<T, V, ES>() * rows_of(T) * 2 * Ring<T, V, ES>::kRow;
+    return (size_t)bwd_depth<T, V, TY>() * rows_of(T) * 2 * Ring<V, TY>::row_bytes(T);
 }
 
 // FP32 rows past 8192: two places of x and dy would not fit.
-template <int T, int ES>
-constexpr bool kHasBackwardRing = !(T == 512 && ES == 4);
+template <int T, int TY>
+constexpr bool kHasBackwardRing = !(T == 512 && TY == kFp32);
 
-template <int T, int V, int ES>
+template <int T, int V, int TY>
 cudaError_t configure_one() {
-    static_assert(fwd_smem<T, V, ES>() <= 224 * 1024, "shared memory");
-    static_assert(!kHasBackwardRing<T, ES> || bwd_smem<T, V, ES>() <= 224 * 1024, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(norm_forward_ring_kernel<T, V, ES>,
+    static_assert(fwd_smem<T, V, TY>() <= 224 * 1024, "shared memory");
+    static_assert(!kHasBackwardRing<T, TY> || bwd_smem<T, V, TY>() <= 224 * 1024, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(norm_forward_ring_kernel<T, V, TY>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)fwd_smem<T, V, ES>());
-    if constexpr (kHasBackwardRing<T, ES>)
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(norm_backward_ring_kernel<T, V, ES>,
+                                         (int)fwd_smem<T, V, TY>());
+    if constexpr (kHasBackwardRing<T, TY>)
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(norm_backward_ring_kernel<T, V, TY>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)bwd_smem<T, V, ES>());
+                                 (int)bwd_smem<T, V, TY>());
     return e;
 }
-template <int ES>
+template <int TY>
 cudaError_t configure_type() {
-    cudaError_t e = configure_one<32, 1, ES>();
-    if (e == cudaSuccess) e = configure_one<32, 4, ES>();
-    if (e == cudaSuccess) e = configure_one<128, 4, ES>();
-    if (e == cudaSuccess) e = configure_one<256, 4, ES>();
-    if (e == cudaSuccess) e = configure_one<512, 4, ES>();
+    cudaError_t e = configure_one<32, 1, TY>();
+    if (e == cudaSuccess) e = configure_one<32, 4, TY>();
+    if (e == cudaSuccess) e = configure_one<128, 4, TY>();
+    if (e == cudaSuccess) e = configure_one<256, 4, TY>();
+    if (e == cudaSuccess) e = configure_one<512, 4, TY>();
     return e;
 }
 
-template <int T, int V, int ES>
+template <int T, int V, int TY>
 cudaError_t forward_ring(const NormArgs &a, cudaStream_t stream) {
-    return launch_pdl(norm_forward_ring_kernel<T, V, ES>,
-                      blocks_for(a.rows, T, a.sms * fwd_blocks(T, ES)), block_of(T),
-                      fwd_smem<T, V, ES>(), stream, a);
+    return launch_pdl(norm_forward_ring_kernel<T, V, TY>,
+                      blocks_for(a.rows, T, a.sms * fwd_blocks(T, TY)), threads_for(T, a.dim),
+                      fwd_smem<T, V, TY>(), stream, a);
 }
-template <int ES>
+template <int TY>
 cudaError_t forward_aligned(const NormArgs &a, cudaStream_t stream) {
-    if (a.dim <= 256) return forward_ring<32, 1, ES>(a, stream);
+    if (a.dim <= 256) return forward_ring<32, 1, TY>(a, stream);
     switch (threads_of(a.dim)) {
-        case 32: return forward_ring<32, 4, ES>(a, stream);
-        case 128: return forward_ring<128, 4, ES>(a, stream);
-        case 256: return forward_ring<256, 4, ES>(a, stream);
-        default: return forward_ring<512, 4, ES>(a, stream);
+        case 32: return forward_ring<32, 4, TY>(a, stream);
+        case 128: return forward_ring<128, 4, TY>(a, stream);
+        case 256: return forward_ring<256, 4, TY>(a, stream);
+        default: return forward_ring<512, 4, TY>(a, stream);
     }
 }
 
@@ -673,21 +742,21 @@ cudaError_t backward_any(const NormArgs &a, int *grid, cudaStream_t stream) {
                       *grid, block_of(t), 0, stream, a);
 }
 
-template <int T, int V, int ES>
+template <int T, int V, int TY>
 cudaError_t backward_ring(const NormArgs &a, int *grid, cudaStream_t stream) {
-    *grid = blocks_for(a.rows, T, a.sms * bwd_blocks(T, ES));
-    return launch_pdl(norm_backward_ring_kernel<T, V, ES>, *grid, block_of(T),
-                      bwd_smem<T, V, ES>(), stream, a);
+    *grid = blocks_for(a.rows, T, a.sms * bwd_blocks(T, TY));
+    return launch_pdl(norm_backward_ring_kernel<T, V, TY>, *grid, threads_for(T, a.dim),
+                      bwd_smem<T, V, TY>(), stream, a);
 }
-template <int ES>
+template <int TY>
 cudaError_t backward_aligned(const NormArgs &a, int *grid, cudaStream_t stream) {
-    if (a.dim <= 256) return backward_ring<32, 1, ES>(a, grid, stream);
+    if (a.dim <= 256) return backward_ring<32, 1, TY>(a, grid, stream);
     switch (threads_of(a.dim)) {
-        case 32: return backward_ring<32, 4, ES>(a, grid, stream);
-        case 128: return backward_ring<128, 4, ES>(a, grid, stream);
-        case 256: return backward_ring<256, 4, ES>(a, grid, stream);
+        case 32: return backward_ring<32, 4, TY>(a, grid, stream);
+        case 128: return backward_ring<128, 4, TY>(a, grid, stream);
+        case 256: return backward_ring<256, 4, TY>(a, grid, stream);
         default:
-            if constexpr (kHasBackwardRing<512, ES>) return backward_ring<512, 4, ES>(a, grid, stream);
+            if constexpr (kHasBackwardRing<512, TY>) return backward_ring<512, 4, TY>(a, grid, stream);
             return backward_any(a, grid, stream);
     }
 }
@@ -703,8 +772,9 @@ cudaError_t forward_any(const NormArgs &a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t norm_configure() {
-    const cudaError_t e = configure_type<2>();
-    return e == cudaSuccess ? configure_type<4>() : e;
+    cudaError_t e = configure_type<kBf16>();
+    if (e == cudaSuccess) e = configure_type<kFp16>();
+    return e == cudaSuccess ? configure_type<kFp32>() : e;
 }
 
 size_t norm_part_floats(int dim, int sms) { return (size_t)kMaxBlocks * sms * 2 * dim; }
@@ -713,7 +783,10 @@ cudaError_t norm_forward_launch(const NormArgs &a, cudaStream_t stream) {
     const int es = layer_esize(a.type);
     const bool vec = a.dim % 8 == 0 && rows_aligned(a.x, a.ld_x, es) && rows_aligned(a.y, a.ld_y, es) &&
                      rows_aligned(a.gamma, 0, es) && rows_aligned(a.beta, 0, es);
-    return !vec ? forward_any(a, stream) : es == 2 ? forward_aligned<2>(a, stream) : forward_aligned<4>(a, stream);
+    return !vec                ? forward_any(a, stream)
+           : a.type == kBf16 ? forward_aligned<kBf16>(a, stream)
+           : a.type == kFp16 ? forward_aligned<kFp16>(a, stream)
+                             : forward_aligned<kFp32>(a, stream);
 }
 
 cudaError_t norm_backward_launch(const NormArgs &args, cudaStream_t stream) {
@@ -724,9 +797,10 @@ cudaError_t norm_backward_launch(const NormArgs &args, cudaStream_t stream) {
     const bool vec = a.dim % 8 == 0 && rows_aligned(a.x, a.ld_x, es) && rows_aligned(a.dy, a.ld_dy, es) &&
                      rows_aligned(a.dx, a.ld_dx, es) && rows_aligned(a.gamma, 0, es);
     int grid = 0;
-    const cudaError_t e = !vec      ? backward_any(a, &grid, stream)
-                          : es == 2 ? backward_aligned<2>(a, &grid, stream)
-                                    : backward_aligned<4>(a, &grid, stream);
+    const cudaError_t e = !vec              ? backward_any(a, &grid, stream)
+                          : a.type == kBf16 ? backward_aligned<kBf16>(a, &grid, stream)
+                          : a.type == kFp16 ? backward_aligned<kFp16>(a, &grid, stream)
+                                            : backward_aligned<kFp32>(a, &grid, stream);
     if (e != cudaSuccess || !sums) return e;
     return launch_pdl(norm_sum_kernel, (2 * a.dim + 31) / 32, 32 * kSumWarps, 0, stream,
                       static_cast<const float *>(a.part), grid, a.dim, a.dgamma, a.dbeta, a.type);
