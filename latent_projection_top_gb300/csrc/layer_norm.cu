@@ -107,17 +107,20 @@ __device__ __forceinline__ float row_sum(float v, float *scratch) {
 // places of a ring (cp.async: no registers held, no barrier to hand a row
 // over), and per row the block meets only to add the row's sums.
 
-// Eight values as they lie in memory, and as four pairs: the arithmetic runs
-// on FP32 pairs (fma.rn.f32x2), half the instructions, which at two or three
+// A 16-byte vector as it lies in memory, and as FP32 pairs: the arithmetic
+// runs on pairs (fma.rn.f32x2), half the instructions, which at two or three
 // blocks an SM bound the backward pass before memory does.
 template <int TY>
+constexpr int kVec = 16 / layer_esize(TY);  // values of a vector
+template <int TY>
+constexpr int kPairs = kVec<TY> / 2;
 struct Run {
-    uint32_t w[2 * layer_esize(TY)];
+    uint32_t w[4];
 };
 template <int TY>
-__device__ __forceinline__ void unpack_run(const Run<TY> &q, uint64_t (&x)[4]) {
+__device__ __forceinline__ void unpack_run(const Run &q, uint64_t (&x)[kPairs<TY>]) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < kPairs<TY>; ++e) {
         if constexpr (TY == kFp32) {
             x[e] = ptx::f32x2_pack(__uint_as_float(q.w[2 * e]), __uint_as_float(q.w[2 * e + 1]));
         } else {
@@ -126,12 +129,12 @@ __device__ __forceinline__ void unpack_run(const Run<TY> &q, uint64_t (&x)[4]) {
         }
     }
 }
-// The same of a parameter's run inside the loop over rows.  Unpacking does
+// The same of a parameter's vector inside the loop over rows.  Unpacking does
 // not change from row to row, and hoisted out of the loop it would hold twice
 // the registers and spill (forward 16384x7168: 171 us); the empty statement
 // keeps it in.
 template <int TY>
-__device__ __forceinline__ void unpack_param(Run<TY> &q, uint64_t (&x)[4]) {
+__device__ __forceinline__ void unpack_param(Run &q, uint64_t (&x)[kPairs<TY>]) {
     if constexpr (TY != kFp32)
 #pragma unroll
         for (int e = 0; e < 4; ++e) asm volatile("" : "+r"(q.w[e]));
@@ -143,85 +146,78 @@ __device__ __forceinline__ float pair_sum(uint64_t v) {
     ptx::f32x2_unpack(v, a, b);
     return a + b;
 }
-__device__ __forceinline__ void unpair(const uint64_t (&x)[4], float (&f)[8]) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) ptx::f32x2_unpack(x[e], f[2 * e], f[2 * e + 1]);
-}
 
-// A row's T threads (a block, or a warp) hold V runs of eight values each.
+// A row's T threads (a block, or a warp) hold V vectors each: vector v of
+// thread t starts at column (v T + t) kVec.
 template <int V, int TY>
 struct Ring {
-    static constexpr int ES = layer_esize(TY);
-    static constexpr int kHalves = ES / 2;  // 16-byte vectors of a run
     // bytes of a row's place
-    static __host__ __device__ constexpr uint32_t row_bytes(int T) { return (uint32_t)V * kHalves * T * 16; }
-    // The vector `h` of run v of thread t: neighbours in t are neighbours in
-    // shared memory.
-    static __device__ __forceinline__ uint32_t at(uint32_t base, int v, int h, int T, int t) {
-        return base + (uint32_t)((v * kHalves + h) * T + t) * 16u;
+    static __host__ __device__ constexpr uint32_t row_bytes(int T) { return (uint32_t)V * T * 16; }
+    // Neighbours in t are neighbours in shared memory.
+    static __device__ __forceinline__ uint32_t at(uint32_t base, int v, int T, int t) {
+        return base + (uint32_t)(v * T + t) * 16u;
     }
     static __device__ __forceinline__ void copy(uint32_t base, const void *p, long long row, int dim,
                                                 int T, int t) {
-        const char *src = static_cast<const char *>(p) + (row + t * 8) * ES;
+        const char *src = static_cast<const char *>(p) + row * layer_esize(TY) + t * 16;
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if ((v * T + t) * 8 < dim)
-#pragma unroll
-                for (int h = 0; h < kHalves; ++h)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(base, v, h, T, t)),
-                                 "l"(src + (v * T * 8 * ES + 16 * h))
-                                 : "memory");
+            if ((v * T + t) * kVec<TY> < dim)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(base, v, T, t)),
+                             "l"(src + v * T * 16)
+                             : "memory");
     }
-    static __device__ __forceinline__ void load(uint32_t base, int v, int T, int t, Run<TY> &q) {
-#pragma unroll
-        for (int h = 0; h < kHalves; ++h)
-            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(q.w[4 * h]), "=r"(q.w[4 * h + 1]), "=r"(q.w[4 * h + 2]),
-                           "=r"(q.w[4 * h + 3])
-                         : "r"(at(base, v, h, T, t))
-                         : "memory");
+    static __device__ __forceinline__ void load(uint32_t base, int v, int T, int t, Run &q) {
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(q.w[0]), "=r"(q.w[1]), "=r"(q.w[2]), "=r"(q.w[3])
+                     : "r"(at(base, v, T, t))
+                     : "memory");
     }
-    static __device__ __forceinline__ void load(uint32_t base, int v, int T, int t, uint64_t (&x)[4]) {
-        Run<TY> q;
+    static __device__ __forceinline__ void load(uint32_t base, int v, int T, int t,
+                                                uint64_t (&x)[kPairs<TY>]) {
+        Run q;
         load(base, v, T, t, q);
         unpack_run<TY>(q, x);
     }
 };
 
-// Store a run; 16-byte aligned rows.
+// Store a vector at column i.
 template <int TY>
-__device__ __forceinline__ void store_pairs(void *p, long long i, const uint64_t (&x)[4]) {
-    float f[8];
-    unpair(x, f);
-    if constexpr (TY == kFp32) {
-        float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
-        q[0] = make_float4(f[0], f[1], f[2], f[3]);
-        q[1] = make_float4(f[4], f[5], f[6], f[7]);
-    } else {
+__device__ __forceinline__ void store_pairs(void *p, long long i, const uint64_t (&x)[kPairs<TY>]) {
+    float f[kVec<TY>];
+#pragma unroll
+    for (int e = 0; e < kPairs<TY>; ++e) ptx::f32x2_unpack(x[e], f[2 * e], f[2 * e + 1]);
+    if constexpr (TY == kFp32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = make_float4(f[0], f[1], f[2], f[3]);
+    else
         *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) =
             make_uint4(pack16(f[0], f[1], TY), pack16(f[2], f[3], TY), pack16(f[4], f[5], TY),
                        pack16(f[6], f[7], TY));
+}
+// FP32 values of a vector's columns.
+template <int TY>
+__device__ __forceinline__ void store_sums(float *p, const uint64_t (&x)[kPairs<TY>]) {
+#pragma unroll
+    for (int e = 0; e < kPairs<TY>; e += 2) {
+        float4 f;
+        ptx::f32x2_unpack(x[e], f.x, f.y);
+        ptx::f32x2_unpack(x[e + 1], f.z, f.w);
+        *reinterpret_cast<float4 *>(p + 2 * e) = f;
     }
 }
 
 // A parameter's values of this thread, kept packed in registers.
 template <int V, int TY>
-__device__ __forceinline__ void load_param(const void *p, int T, int t, int dim, float none, Run<TY> (&q)[V]) {
-    constexpr int ES = layer_esize(TY);
+__device__ __forceinline__ void load_param(const void *p, int T, int t, int dim, float none, Run (&q)[V]) {
     const uint32_t fill = TY == kFp32 ? __float_as_uint(none) : pack16(none, none, TY);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int c = (v * T + t) * 8;
-        if (p != nullptr && c < dim) {
-            const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + (long long)c * ES);
-#pragma unroll
-            for (int h = 0; h < ES / 2; ++h) {
-                const uint4 x = s[h];
-                q[v].w[4 * h] = x.x, q[v].w[4 * h + 1] = x.y, q[v].w[4 * h + 2] = x.z, q[v].w[4 * h + 3] = x.w;
-            }
+        if (p != nullptr && (v * T + t) * kVec<TY> < dim) {
+            const uint4 x = static_cast<const uint4 *>(p)[v * T + t];
+            q[v].w[0] = x.x, q[v].w[1] = x.y, q[v].w[2] = x.z, q[v].w[3] = x.w;
         } else {
 #pragma unroll
-            for (int e = 0; e < 2 * ES; ++e) q[v].w[e] = fill;
+            for (int e = 0; e < 4; ++e) q[v].w[e] = fill;
         }
     }
 }
@@ -285,6 +281,7 @@ template <int MAXT, int V, int TY>
 __global__ void __launch_bounds__(block_of(MAXT), fwd_blocks(MAXT, TY))
     norm_forward_ring_kernel(const __grid_constant__ NormArgs a) {
     using R = Ring<V, TY>;
+    constexpr int kP = kPairs<TY>;
     constexpr int P = fwd_depth<MAXT, V, TY>(), kRows = rows_of(MAXT);
     extern __shared__ uint4 ring[];
     __shared__ float2 scratch[2][MAXT / 32];
@@ -302,7 +299,7 @@ __global__ void __launch_bounds__(block_of(MAXT), fwd_blocks(MAXT, TY))
             R::copy(mine + i * place, a.x, (long long)(r0 + i * stride) * a.ld_x, a.dim, T, t);
         copy_commit();
     }
-    Run<TY> gamma[V], beta[V];
+    Run gamma[V], beta[V];
     load_param<V, TY>(a.gamma, T, t, a.dim, 1.f, gamma);
     load_param<V, TY>(a.beta, T, t, a.dim, 0.f, beta);
     const float inv = 1.f / (float)a.dim;
@@ -316,17 +313,17 @@ __global__ void __launch_bounds__(block_of(MAXT), fwd_blocks(MAXT, TY))
         const uint32_t base = mine + slot * place;
         slot = slot + 1 == P ? 0 : slot + 1;
         // the row stays packed: unpacking it again costs less than the registers
-        Run<TY> q[V];
+        Run q[V];
         uint64_t acc = 0u;
         float none = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            if ((v * T + t) * 8 >= a.dim) break;
-            uint64_t x[4];
+            if ((v * T + t) * kVec<TY> >= a.dim) break;
+            uint64_t x[kP];
             R::load(base, v, T, t, q[v]);
             unpack_run<TY>(q[v], x);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc = ptx::f32x2_add(acc, x[e]);
+            for (int e = 0; e < kP; ++e) acc = ptx::f32x2_add(acc, x[e]);
         }
         float s = pair_sum(acc);
         row_sums<MAXT>(s, none, scratch, turn, T);
@@ -335,11 +332,11 @@ __global__ void __launch_bounds__(block_of(MAXT), fwd_blocks(MAXT, TY))
         acc = 0u;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            if ((v * T + t) * 8 >= a.dim) break;
-            uint64_t x[4];
+            if ((v * T + t) * kVec<TY> >= a.dim) break;
+            uint64_t x[kP];
             unpack_run<TY>(q[v], x);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < kP; ++e) {
                 x[e] = ptx::f32x2_sub(x[e], mean2);
                 acc = ptx::f32x2_fma(x[e], x[e], acc);
             }
@@ -352,14 +349,14 @@ __global__ void __launch_bounds__(block_of(MAXT), fwd_blocks(MAXT, TY))
             *reinterpret_cast<float2 *>(a.stats + 2 * (long long)r) = make_float2(mean, rstd);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = (v * T + t) * 8;
+            const int c = (v * T + t) * kVec<TY>;
             if (c >= a.dim) break;
-            uint64_t x[4], g[4], b[4];
+            uint64_t x[kP], g[kP], b[kP];
             unpack_run<TY>(q[v], x);
             unpack_param<TY>(gamma[v], g);
             unpack_param<TY>(beta[v], b);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < kP; ++e)
                 g[e] = ptx::f32x2_fma(ptx::f32x2_mul(ptx::f32x2_sub(x[e], mean2), rstd2), g[e], b[e]);
             store_pairs<TY>(a.y, (long long)r * a.ld_y + c, g);
         }
@@ -373,6 +370,7 @@ template <int MAXT, int V, int TY>
 __global__ void __launch_bounds__(block_of(MAXT), bwd_blocks(MAXT, TY))
     norm_backward_ring_kernel(const __grid_constant__ NormArgs a) {
     using R = Ring<V, TY>;
+    constexpr int kP = kPairs<TY>;
     constexpr int P = bwd_depth<MAXT, V, TY>(), kRows = rows_of(MAXT);
     extern __shared__ uint4 ring[];
     __shared__ float2 scratch[2][MAXT / 32];
@@ -395,10 +393,10 @@ __global__ void __launch_bounds__(block_of(MAXT), bwd_blocks(MAXT, TY))
         if (r0 + i * stride < a.rows) copy_row(r0 + i * stride, i);
         copy_commit();
     }
-    Run<TY> gamma[V];
+    Run gamma[V];
     load_param<V, TY>(a.gamma, T, t, a.dim, 1.f, gamma);
     const float inv = 1.f / (float)a.dim;
-    uint64_t dg[V][4] = {}, db[V][4] = {};
+    uint64_t dg[V][kP] = {}, db[V][kP] = {};
     float2 ms = r0 < a.rows ? stats[r0] : make_float2(0.f, 0.f);
     int slot = 0;
     for (int r = r0; r < a.rows; r += stride) {
@@ -414,13 +412,13 @@ __global__ void __launch_bounds__(block_of(MAXT), bwd_blocks(MAXT, TY))
         uint64_t a1 = 0u, a2 = 0u;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            if ((v * T + t) * 8 >= a.dim) break;
-            uint64_t x[4], dy[4], g[4];
+            if ((v * T + t) * kVec<TY> >= a.dim) break;
+            uint64_t x[kP], dy[kP], g[kP];
             R::load(base, v, T, t, x);
             R::load(base + place, v, T, t, dy);
             unpack_param<TY>(gamma[v], g);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < kP; ++e) {
                 const uint64_t xh = ptx::f32x2_fma(x[e], rstd2, shift2);
                 const uint64_t gy = ptx::f32x2_mul(dy[e], g[e]);
                 dg[v][e] = ptx::f32x2_fma(dy[e], xh, dg[v][e]);
@@ -436,14 +434,14 @@ __global__ void __launch_bounds__(block_of(MAXT), bwd_blocks(MAXT, TY))
         const uint64_t k1 = pair(-rstd * s1 * inv), k2 = pair(-rstd * s2 * inv);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = (v * T + t) * 8;
+            const int c = (v * T + t) * kVec<TY>;
             if (c >= a.dim) break;
-            uint64_t x[4], dy[4], g[4];
+            uint64_t x[kP], dy[kP], g[kP];
             R::load(base, v, T, t, x);
             R::load(base + place, v, T, t, dy);
             unpack_param<TY>(gamma[v], g);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < kP; ++e) {
                 const uint64_t xh = ptx::f32x2_fma(x[e], rstd2, shift2);
                 const uint64_t gy = ptx::f32x2_mul(ptx::f32x2_mul(dy[e], g[e]), rstd2);
                 dy[e] = ptx::f32x2_add(gy, ptx::f32x2_fma(xh, k2, k1));
@@ -456,10 +454,10 @@ __global__ void __launch_bounds__(block_of(MAXT), bwd_blocks(MAXT, TY))
     if constexpr (MAXT > 32) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = (v * T + t) * 8;
+            const int c = (v * T + t) * kVec<TY>;
             if (c < a.dim) {
-                store_pairs<kFp32>(part, c, dg[v]);
-                store_pairs<kFp32>(part, a.dim + c, db[v]);
+                store_sums<TY>(part + c, dg[v]);
+                store_sums<TY>(part + a.dim + c, db[v]);
             }
         }
     } else {
@@ -471,12 +469,12 @@ __global__ void __launch_bounds__(block_of(MAXT), bwd_blocks(MAXT, TY))
             __syncthreads();
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                store_pairs<kFp32>(acc, sub * V * 256 + (v * T + t) * 8, k ? db[v] : dg[v]);
+                store_sums<TY>(acc + (sub * V * 32 + v * 32 + t) * kVec<TY>, k ? db[v] : dg[v]);
             __syncthreads();
             for (int c = threadIdx.x; c < a.dim; c += block_of(MAXT)) {
                 float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < kRows; ++i) sum += acc[i * V * 256 + c];
+                for (int i = 0; i < kRows; ++i) sum += acc[i * V * 32 * kVec<TY> + c];
                 part[k * a.dim + c] = sum;
             }
         }
@@ -705,13 +703,18 @@ cudaError_t configure_one() {
                                  (int)bwd_smem<T, V, TY>());
     return e;
 }
+// Vectors a thread that hold n times eight values.
+template <int TY>
+constexpr int runs(int n) {
+    return n * 8 / kVec<TY>;
+}
 template <int TY>
 cudaError_t configure_type() {
-    cudaError_t e = configure_one<32, 1, TY>();
-    if (e == cudaSuccess) e = configure_one<32, 4, TY>();
-    if (e == cudaSuccess) e = configure_one<128, 4, TY>();
-    if (e == cudaSuccess) e = configure_one<256, 4, TY>();
-    if (e == cudaSuccess) e = configure_one<512, 4, TY>();
+    cudaError_t e = configure_one<32, runs<TY>(1), TY>();
+    if (e == cudaSuccess) e = configure_one<32, runs<TY>(4), TY>();
+    if (e == cudaSuccess) e = configure_one<128, runs<TY>(4), TY>();
+    if (e == cudaSuccess) e = configure_one<256, runs<TY>(4), TY>();
+    if (e == cudaSuccess) e = configure_one<512, runs<TY>(4), TY>();
     return e;
 }
 
@@ -723,12 +726,12 @@ cudaError_t forward_ring(const NormArgs &a, cudaStream_t stream) {
 }
 template <int TY>
 cudaError_t forward_aligned(const NormArgs &a, cudaStream_t stream) {
-    if (a.dim <= 256) return forward_ring<32, 1, TY>(a, stream);
+    if (a.dim <= 256) return forward_ring<32, runs<TY>(1), TY>(a, stream);
     switch (threads_of(a.dim)) {
-        case 32: return forward_ring<32, 4, TY>(a, stream);
-        case 128: return forward_ring<128, 4, TY>(a, stream);
-        case 256: return forward_ring<256, 4, TY>(a, stream);
-        default: return forward_ring<512, 4, TY>(a, stream);
+        case 32: return forward_ring<32, runs<TY>(4), TY>(a, stream);
+        case 128: return forward_ring<128, runs<TY>(4), TY>(a, stream);
+        case 256: return forward_ring<256, runs<TY>(4), TY>(a, stream);
+        default: return forward_ring<512, runs<TY>(4), TY>(a, stream);
     }
 }
 
@@ -750,13 +753,13 @@ cudaError_t backward_ring(const NormArgs &a, int *grid, cudaStream_t stream) {
 }
 template <int TY>
 cudaError_t backward_aligned(const NormArgs &a, int *grid, cudaStream_t stream) {
-    if (a.dim <= 256) return backward_ring<32, 1, TY>(a, grid, stream);
+    if (a.dim <= 256) return backward_ring<32, runs<TY>(1), TY>(a, grid, stream);
     switch (threads_of(a.dim)) {
-        case 32: return backward_ring<32, 4, TY>(a, grid, stream);
-        case 128: return backward_ring<128, 4, TY>(a, grid, stream);
-        case 256: return backward_ring<256, 4, TY>(a, grid, stream);
+        case 32: return backward_ring<32, runs<TY>(4), TY>(a, grid, stream);
+        case 128: return backward_ring<128, runs<TY>(4), TY>(a, grid, stream);
+        case 256: return backward_ring<256, runs<TY>(4), TY>(a, grid, stream);
         default:
-            if constexpr (kHasBackwardRing<512, TY>) return backward_ring<512, 4, TY>(a, grid, stream);
+            if constexpr (kHasBackwardRing<512, TY>) return backward_ring<512, runs<TY>(4), TY>(a, grid, stream);
             return backward_any(a, grid, stream);
     }
 }
