@@ -222,8 +222,23 @@ __device__ __forceinline__ void load_param(const void *p, int T, int t, int dim,
     }
 }
 
-// Sums of a and b over a row's threads, the same in every thread and every
-// run.  One barrier: consecutive sums use alternate scratch.
+// Sums over a row's threads, the same in every thread and every run.  One
+// barrier: consecutive sums use alternate scratch.
+template <int MAXT>
+__device__ __forceinline__ float row_sum(float a, float2 (*scratch)[MAXT / 32], int &turn, int T) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+    if constexpr (MAXT > 32) {
+        if ((threadIdx.x & 31) == 0) scratch[turn][threadIdx.x >> 5].x = a;
+        __syncthreads();
+        a = 0.f;
+#pragma unroll
+        for (int i = 0; i < MAXT / 32; ++i)
+            if (32 * i < T) a += scratch[turn][i].x;
+        turn ^= 1;
+    }
+    return a;
+}
 template <int MAXT>
 __device__ __forceinline__ void row_sums(float &a, float &b, float2 (*scratch)[MAXT / 32], int &turn, int T) {
 #pragma unroll
@@ -257,7 +272,7 @@ __host__ __device__ constexpr int rows_of(int t) { return block_of(t) / t; }
 // Blocks an SM and rows of a ring: up to ~190 KB of rows an SM.  `t`: the
 // most threads of a row that a kernel is made for.
 __host__ __device__ constexpr int fwd_blocks(int t, int ty) {
-    return t <= 128 ? (ty != kFp32 ? 5 : 4) : t == 256 ? (ty != kFp32 ? 3 : 2) : 1;
+    return t <= 128 ? 4 : t == 256 ? 2 : 1;
 }
 __host__ __device__ constexpr int bwd_blocks(int t, int ty) {
     return t == 32 ? 3 : t == 128 ? 3 : t == 256 ? (ty != kFp32 ? 2 : 1) : 1;
@@ -312,38 +327,27 @@ __global__ void __launch_bounds__(block_of(MAXT), fwd_blocks(MAXT, TY))
         copy_wait<P - 1>();
         const uint32_t base = mine + slot * place;
         slot = slot + 1 == P ? 0 : slot + 1;
-        // the row stays packed: unpacking it again costs less than the registers
-        Run q[V];
-        uint64_t acc = 0u;
-        float none = 0.f;
+        uint64_t x[V][kP], acc = 0u;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             if ((v * T + t) * kVec<TY> >= a.dim) break;
-            uint64_t x[kP];
-            R::load(base, v, T, t, q[v]);
-            unpack_run<TY>(q[v], x);
+            R::load(base, v, T, t, x[v]);
 #pragma unroll
-            for (int e = 0; e < kP; ++e) acc = ptx::f32x2_add(acc, x[e]);
+            for (int e = 0; e < kP; ++e) acc = ptx::f32x2_add(acc, x[v][e]);
         }
-        float s = pair_sum(acc);
-        row_sums<MAXT>(s, none, scratch, turn, T);
-        const float mean = s * inv;
-        const uint64_t mean2 = pair(mean);
+        const float mean = row_sum<MAXT>(pair_sum(acc), scratch, turn, T) * inv;
+        const uint64_t mean2 = pair(-mean);
         acc = 0u;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             if ((v * T + t) * kVec<TY> >= a.dim) break;
-            uint64_t x[kP];
-            unpack_run<TY>(q[v], x);
 #pragma unroll
             for (int e = 0; e < kP; ++e) {
-                x[e] = ptx::f32x2_sub(x[e], mean2);
-                acc = ptx::f32x2_fma(x[e], x[e], acc);
+                x[v][e] = ptx::f32x2_add(x[v][e], mean2);
+                acc = ptx::f32x2_fma(x[v][e], x[v][e], acc);
             }
         }
-        s = pair_sum(acc);
-        row_sums<MAXT>(s, none, scratch, turn, T);
-        const float rstd = 1.f / sqrtf(s * inv + a.eps);
+        const float rstd = 1.f / sqrtf(row_sum<MAXT>(pair_sum(acc), scratch, turn, T) * inv + a.eps);
         const uint64_t rstd2 = pair(rstd);
         if (t == 0 && a.stats != nullptr)
             *reinterpret_cast<float2 *>(a.stats + 2 * (long long)r) = make_float2(mean, rstd);
@@ -351,14 +355,13 @@ __global__ void __launch_bounds__(block_of(MAXT), fwd_blocks(MAXT, TY))
         for (int v = 0; v < V; ++v) {
             const int c = (v * T + t) * kVec<TY>;
             if (c >= a.dim) break;
-            uint64_t x[kP], g[kP], b[kP];
-            unpack_run<TY>(q[v], x);
-            unpack_param<TY>(gamma[v], g);
-            unpack_param<TY>(beta[v], b);
+            uint64_t g[kP], b[kP];
+            unpack_run<TY>(gamma[v], g);
+            unpack_run<TY>(beta[v], b);
 #pragma unroll
             for (int e = 0; e < kP; ++e)
-                g[e] = ptx::f32x2_fma(ptx::f32x2_mul(ptx::f32x2_sub(x[e], mean2), rstd2), g[e], b[e]);
-            store_pairs<TY>(a.y, (long long)r * a.ld_y + c, g);
+                x[v][e] = ptx::f32x2_fma(ptx::f32x2_mul(x[v][e], rstd2), g[e], b[e]);
+            store_pairs<TY>(a.y, (long long)r * a.ld_y + c, x[v]);
         }
     }
 }
