@@ -27,7 +27,7 @@ DEBUG_LIB = os.path.join(DEBUG_BUILD, "libroute_debug.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["decode_kernel.cu", "prefill_kernel.cu", "topk_kernel.cu", "stage_kernel.cu",
-           "route_api.cu", "layer_gemm.cu", "layer_stream.cu", "layer_elem.cu",
+           "route_api.cu", "layer_gemm.cu", "layer_small.cu", "layer_elem.cu",
            "layer_norm.cu", "layer_api.cu"]
 HEADERS = ["common.cuh", "sm103_ptx.cuh", "topk16.cuh", "twofloat.cuh", "api_util.h", "layer.cuh",
            "layer_math.cuh"]

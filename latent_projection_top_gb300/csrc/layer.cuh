@@ -90,31 +90,18 @@ cudaError_t gemm_launch(int form, int epi, int bn, const GemmMaps &maps, const G
                         cudaStream_t stream);
 cudaError_t gemm_finish_launch(int epi, const FinishArgs &args, cudaStream_t stream);
 
-// Few rows (at most 128): the weights stream through the SMs once, split over
-// them whatever the tile count, weight columns on the tensor cores' M side.
-struct StreamArgs {
-    int rows;
-    int tiles, kblocks, kswitch;  // 128-column tiles (gated: 64 + 64), k-blocks, second operands from kswitch
-    int grid;                     // CTAs: CTA g owns units [units g / grid, units (g + 1) / grid)
-    int wait_first;               // 0: the call's kernel before this one waited for its own
-                                  // predecessors before it let this one launch, so the weights
-                                  // may be read at once
-    int fp16, trigger, test_stall;
-    unsigned x_bytes;             // bytes of a box of token rows
-    unsigned long long timeout_ns;
-    unsigned *status;
-    unsigned *arrived;            // [tiles] CTAs that have stored a tile's partials (zero between calls)
-    float *part;                  // [grid + tiles slots][rows][128]
-    uint8_t w[2][2], x[2];        // weight map of each segment and (gated) half, token map of each segment
-    GemmProblem p;
-};
-constexpr int kStreamMaxRows = 128;
-constexpr int kStreamMaxTiles = 1024;
-constexpr int kStreamTile = 128;
-cudaError_t stream_configure();
-int stream_smem_bytes();
-cudaError_t stream_launch(int form, int epi, const GemmMaps &maps, const StreamArgs &args,
-                          cudaStream_t stream);
+// Products of few rows or few tiles: 128 columns x up to 128 rows a tile, the
+// contraction split over the CTAs of a cluster (args.splits: 1, 2, 4 or 8).
+// Takes the same arguments as gemm_launch; `rows`: MMA rows a tile (16, 32,
+// 64 or 128).  With `chained` the call's kernel before this one waited for
+// its own predecessors before it let this one launch, and does not write the
+// columns' operand, which is then read at once.
+constexpr int kSmallTile = 128;
+constexpr int kSmallMaxSplits = 8;
+cudaError_t small_configure();
+int small_smem_bytes();
+cudaError_t small_launch(int form, int epi, int rows, const GemmMaps &maps, const GemmArgs &args,
+                         bool chained, cudaStream_t stream);
 
 // dst[r, 0..cols) = src[r, 0..cols) of 16-bit values, for operands whose rows
 // TMA cannot read where they are.

@@ -27,7 +27,7 @@ struct route_layer {
     int device, sms, pairs;
     int test_stall;
     unsigned long long timeout_ns;
-    unsigned *words;   // device status word, then the streamed products' arrival counts
+    unsigned *words;   // device status word
     uint8_t *scratch;
     size_t scratch_bytes;
     // offsets into scratch (0 size where the plan needs none)
@@ -37,15 +37,10 @@ struct route_layer {
 
 namespace {
 
-constexpr int kPlanWords = kWords + kStreamMaxTiles;
 constexpr unsigned long long kTimeoutNs = 2000000000ull;
 // Split products have at most one item a CTA pair: FP32 partials of a
 // 256 x 256 tile each.
 constexpr size_t kTilePartBytes = 256 * 256 * 4;
-// Rows up to which a product streams its weights (layer_stream.cu).
-constexpr int kStreamRows = kStreamMaxRows;
-
-bool streams(int rows) { return rows <= kStreamRows; }
 
 route_status cuda_fail(cudaError_t e, const char *what) {
     return api_fail(ROUTE_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
@@ -160,35 +155,64 @@ route_status operand(const route_layer *p, const void *src, long long ld, int ro
     return ROUTE_OK;
 }
 
+// How a launch covers its products: CTA-pair tiles of 256 x bn
+// (layer_gemm.cu), or 128-column tiles of bn rows (layer_small.cu), and the
+// splits of the contraction.
 struct Choice {
+    bool small;
     int bn, splits;
 };
 
-// Tile width and K splits of products of `ntiles(bn)` tiles and `kblocks`
-// k-blocks: the smallest estimate of waves x (k-blocks x time of one + the
-// tile's fixed part), plus, when split, the partials' second kernel.
-template <class Tiles>
-Choice choose(const route_layer *p, Tiles ntiles, int kblocks, double out_elems) {
-    Choice best = {256, 1};
-    double t_best = 1e30;
+struct Shape {
+    int M, N;  // N: columns of D (gated: hidden columns)
+};
+
+int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+
+// The choice with the smallest estimated time, from what the kernels measure:
+// a k-block of a pair's 256 x 256 tile takes 0.34 us and of a 256 x 128 tile
+// 0.30 us; the small tiles are bound by what an SM reads, about 70 bytes a
+// nanosecond, or by memory.
+Choice choose(const route_layer *p, int form, int epi, const Shape *shape, int count, int kblocks) {
+    Choice best = {false, 256, 1};
+    double t_best = 1e30, elems = 0;
+    int rows = 0;
+    for (int i = 0; i < count; ++i) {
+        elems += (double)shape[i].M * shape[i].N * (epi == kEpiGated ? 2 : 1);
+        rows = rows < shape[i].M ? shape[i].M : rows;
+    }
     for (int bn : {256, 128}) {
-        const double kb_us = bn == 256 ? 0.33 : 0.19, fixed_us = bn == 256 ? 3.0 : 2.0;
-        const long long tiles = ntiles(bn);
-        const int smax = tiles >= p->pairs ? 1 : (int)(p->pairs / tiles);
-        for (int s = 1; s <= smax && s <= 64 && (s == 1 || kblocks / s >= 2); ++s) {
-            const long long waves = (tiles * s + p->pairs - 1) / p->pairs;
-            const int kb = (kblocks + s - 1) / s;
-            double t = (double)waves * (kb * kb_us) + fixed_us + (waves - 1) * 0.3;
-            if (s > 1) t += 2.5 + out_elems * 4.0 * (s + 1) / 4e6;
-            if (t < t_best) t_best = t, best = {bn, s};
+        long long tiles = 0;
+        const int cols = epi == kEpiGated ? bn / 2 : bn;
+        for (int i = 0; i < count; ++i)
+            tiles += (long long)ceil_div(shape[i].M, kGemmBM) * ceil_div(shape[i].N, cols);
+        const int most = tiles >= p->pairs ? 1 : (int)(p->pairs / tiles);
+        for (int s = 1; s <= most && (s == 1 || kblocks / s >= 2); ++s) {
+            const int waves = ceil_div(tiles * s, p->pairs);
+            double t = 7.0 + waves * (ceil_div(kblocks, s) * (bn == 256 ? 0.34 : 0.30));
+            if (s > 1) t += 2.5 + elems * 4.0 * (s + 1) / 4e6;
+            if (t < t_best) t_best = t, best = {false, bn, s};
         }
+    }
+    {
+        int bn = form == kFormTT ? 64 : 16;
+        while (bn < 128 && bn < rows) bn *= 2;
+        long long tiles = 0;
+        const int cols = epi == kEpiGated ? kSmallTile / 2 : kSmallTile;
+        for (int i = 0; i < count; ++i)
+            tiles += (long long)ceil_div(shape[i].M, bn) * ceil_div(shape[i].N, cols);
+        int s = 1;
+        while (s < kSmallMaxSplits && tiles * s * 2 <= 2 * p->sms && s * 2 <= kblocks) s *= 2;
+        const double kb_us = (16384 + bn * 128) / 70e3;
+        const double t = 5.0 + ceil_div(tiles * s, p->sms) * (ceil_div(kblocks, s) * kb_us + 0.5);
+        if (t < t_best) best = {true, bn, s};
     }
     return best;
 }
 
-void set_tiles(GemmProblem &q, int tile_cols, int pairs) {
-    q.tiles_m = (q.M + kGemmBM - 1) / kGemmBM;
-    q.tiles_n = (q.N + tile_cols - 1) / tile_cols;
+void set_tiles(GemmProblem &q, int tile_rows, int tile_cols, int pairs) {
+    q.tiles_m = ceil_div(q.M, tile_rows);
+    q.tiles_n = ceil_div(q.N, tile_cols);
     // column tiles of a band: about as many as the row tiles at work at once
     int band = (pairs + q.tiles_m - 1) / q.tiles_m;
     band = band < 8 ? 8 : band;
@@ -208,16 +232,17 @@ struct Product {
         args.status = p->words;
         args.test_stall = p->test_stall;
     }
-    // Rows of a K-contiguous A's boxes: 128, or what there is of M.
-    uint32_t a_rows(int M) {
-        const uint32_t r = M >= 128 ? 128u : (uint32_t)up8(M);
-        static_assert(kStreamMaxRows <= 128, "a streamed product's rows are one box");
+    // Rows of the boxes of a K-contiguous A (a tile's rows for one CTA, or
+    // what there is of M: a box higher than its tensor loads slowly, 98
+    // against 25 us at 8x3584x7168) and of a K-contiguous B.
+    uint32_t a_rows(int M, const Choice &ch) {
+        const uint32_t most = ch.small ? (uint32_t)ch.bn : 128u;
+        const uint32_t r = (uint32_t)M >= most ? most : (uint32_t)up8(M);
         args.a_bytes = r * 64 * 2;
         return r;
     }
-    // Rows of a K-contiguous B's boxes: the weight columns a CTA loads.
-    uint32_t b_rows(int M, const Choice &ch) {
-        return streams(M) ? (uint32_t)kStreamTile : (uint32_t)ch.bn / 2;
+    static uint32_t b_rows(const Choice &ch) {
+        return ch.small ? (uint32_t)kSmallTile : (uint32_t)ch.bn / 2;
     }
     // A map of `o` [outer, inner] in boxes of box_inner x box_outer.
     route_status map(const Operand &o, long long inner, long long outer, uint32_t box_outer,
@@ -228,57 +253,34 @@ struct Product {
     }
 };
 
-// A streamed product.  `chained`: the call's kernel before it is one too.
-route_status run_stream(const route_layer *p, const Product &pr, int form, int epi, bool chained,
-                        bool more, cudaStream_t stream) {
-    const GemmProblem &q = pr.args.p[0];
-    const int cols = epi == kEpiGated ? kStreamTile / 2 : kStreamTile;
-    StreamArgs a;
-    memset(&a, 0, sizeof a);
-    a.rows = q.M;
-    a.tiles = (q.N + cols - 1) / cols;
-    a.kblocks = q.kblocks, a.kswitch = q.kswitch;
-    const long long units = (long long)a.tiles * a.kblocks;
-    a.grid = units < p->sms ? (int)units : p->sms;
-    a.wait_first = !chained;
-    a.fp16 = pr.fp16;
-    a.trigger = more;
-    a.test_stall = p->test_stall;
-    a.x_bytes = (unsigned)up8(q.M) * 64 * 2;
-    a.timeout_ns = p->timeout_ns;
-    a.status = p->words;
-    a.arrived = p->words + kWords;
-    a.part = reinterpret_cast<float *>(p->scratch + p->o_part);
-    for (int seg = 0; seg < 2; ++seg) {
-        a.x[seg] = q.a[seg];
-        for (int h = 0; h < 2; ++h) a.w[seg][h] = q.b[seg][h];
-    }
-    a.p = q;
-    const cudaError_t e = stream_launch(form, epi, pr.maps, a, stream);
-    return e == cudaSuccess ? ROUTE_OK : cuda_fail(e, "streamed product kernel launch");
-}
-
-// Launch the product(s) and, when split, the kernel(s) that finish them.
+// Launch the product(s) and, when pair tiles are split, the kernel(s) that
+// finish them.  `more`: another kernel of the call follows; `chained`: the
+// one before is a product that does not write this one's B.
 route_status run(const route_layer *p, Product &pr, int form, int epi, const Choice &ch,
                  bool chained, bool more, cudaStream_t stream) {
     GemmArgs &a = pr.args;
-    if (form != kFormTT && streams(a.p[0].M)) return run_stream(p, pr, form, epi, chained, more, stream);
-    const int tile_cols = epi == kEpiGated ? ch.bn / 2 : ch.bn;
+    const int width = ch.small ? kSmallTile : ch.bn;
     a.splits = ch.splits;
     int items = 0;
     float *part = reinterpret_cast<float *>(p->scratch + p->o_part);
     for (int i = 0; i < a.nprob; ++i) {
         GemmProblem &q = a.p[i];
-        set_tiles(q, tile_cols, p->pairs);
+        set_tiles(q, ch.small ? ch.bn : kGemmBM, epi == kEpiGated ? width / 2 : width, p->pairs);
         q.item_base = items;
-        items += q.tiles_m * q.tiles_n * ch.splits;
-        if (ch.splits > 1) {
+        items += q.tiles_m * q.tiles_n * (ch.small ? 1 : ch.splits);
+        if (!ch.small && ch.splits > 1) {
             q.part = part;
             q.ld_part = up16(q.N) * (epi == kEpiGated ? 2 : 1);
             part += (size_t)ch.splits * q.M * q.ld_part;
         }
     }
     a.items = items;
+    if (ch.small) {
+        if (form == kFormTT) a.a_bytes = (unsigned)ch.bn * 64 * 2;
+        a.trigger = more;
+        const cudaError_t e = small_launch(form, epi, ch.bn, pr.maps, a, chained, stream);
+        return e == cudaSuccess ? ROUTE_OK : cuda_fail(e, "product kernel launch");
+    }
     a.pairs = items < p->pairs ? items : p->pairs;
     a.trigger = more || ch.splits > 1;
     cudaError_t e = gemm_launch(form, epi, ch.bn, pr.maps, a, stream);
@@ -295,12 +297,9 @@ route_status run(const route_layer *p, Product &pr, int form, int epi, const Cho
     return ROUTE_OK;
 }
 
-Choice choose_one(const route_layer *p, int M, int N, int kblocks, bool gated) {
-    auto tiles = [&](int bn) {
-        const int cols = gated ? bn / 2 : bn;
-        return (long long)((M + kGemmBM - 1) / kGemmBM) * ((N + cols - 1) / cols);
-    };
-    return choose(p, tiles, kblocks, (double)M * N * (gated ? 2 : 1));
+Choice choose_one(const route_layer *p, int form, int epi, int M, int N, int kblocks) {
+    const Shape s = {M, N};
+    return choose(p, form, epi, &s, 1, kblocks);
 }
 
 int kblocks_of(int k) { return (k + 63) / 64; }
@@ -329,9 +328,9 @@ route_status forward_product(const route_layer *p, const Operand &A, const Opera
     q.act = act;
     q.saved = saved, q.ld_saved = up16(N);
     q.vec = vec_bits(out, q.ld_out, nullptr, residual, q.ld_res, out_type, bias);
-    const Choice ch = choose_one(p, M, N, q.kblocks, false);
+    const Choice ch = choose_one(p, kFormNT, kEpiLinear, M, N, q.kblocks);
     route_status st;
-    if ((st = pr.map(A, K, M, pr.a_rows(M), "x", &q.a[0])) != ROUTE_OK ||
+    if ((st = pr.map(A, K, M, pr.a_rows(M, ch), "x", &q.a[0])) != ROUTE_OK ||
         (st = pr.map(W, N, K, 64, "W", &q.b[0][0])) != ROUTE_OK)
         return st;
     q.b[0][1] = q.b[0][0];
@@ -349,11 +348,11 @@ route_status input_grad(const route_layer *p, int terms, const Operand *dz, cons
     q.kswitch = kblocks_of(N);
     q.kblocks = terms * q.kswitch;
     set_out(q, out, ld_out, p->type);
-    const Choice ch = choose_one(p, M, K, q.kblocks, false);
+    const Choice ch = choose_one(p, kFormNN, kEpiLinear, M, K, q.kblocks);
     for (int i = 0; i < terms; ++i) {
         route_status st;
-        if ((st = pr.map(dz[i], N, M, pr.a_rows(M), "dz", &q.a[i])) != ROUTE_OK ||
-            (st = pr.map(W[i], N, K, pr.b_rows(M, ch), "W", &q.b[i][0])) != ROUTE_OK)
+        if ((st = pr.map(dz[i], N, M, pr.a_rows(M, ch), "dz", &q.a[i])) != ROUTE_OK ||
+            (st = pr.map(W[i], N, K, pr.b_rows(ch), "W", &q.b[i][0])) != ROUTE_OK)
             return st;
         q.b[i][1] = q.b[i][0];
     }
@@ -367,30 +366,24 @@ struct WeightGrad {
     void *dW;
     int64_t ld;
 };
+// `shapes`: of all the weights the operator has, so that a gradient's bits do
+// not depend on which others are asked for.
 route_status weight_grads(const route_layer *p, const WeightGrad *w, int count, int rows,
-                          cudaStream_t stream) {
+                          const Shape *shapes, int all, cudaStream_t stream) {
     Product pr(p);
     pr.args.nprob = count;
-    double elems = 0;
     for (int i = 0; i < count; ++i) {
         GemmProblem &q = pr.args.p[i];
         q.M = w[i].K, q.N = w[i].N;
         q.kblocks = q.kswitch = kblocks_of(rows);
         set_out(q, w[i].dW, w[i].ld, p->type);
-        elems += (double)q.M * q.N;
         route_status st;
         if ((st = pr.map(w[i].x, q.M, rows, 64, "x", &q.a[0])) != ROUTE_OK ||
             (st = pr.map(w[i].dz, q.N, rows, 64, "dz", &q.b[0][0])) != ROUTE_OK)
             return st;
         q.b[0][1] = q.b[0][0];
     }
-    auto tiles = [&](int bn) {
-        long long t = 0;
-        for (int i = 0; i < count; ++i)
-            t += (long long)((w[i].K + kGemmBM - 1) / kGemmBM) * ((w[i].N + bn - 1) / bn);
-        return t;
-    };
-    const Choice ch = choose(p, tiles, kblocks_of(rows), elems);
+    const Choice ch = choose(p, kFormTT, kEpiLinear, shapes, all, kblocks_of(rows));
     return run(p, pr, kFormTT, kEpiLinear, ch, false, false, stream);
 }
 
@@ -418,14 +411,14 @@ route_status finish_prepare(route_layer *p, int device, route_layer **out) {
         st = api_fail(ROUTE_ERR_DEVICE, "device %d is sm_%d%d; this library is built for sm_103a only",
                       device, prop.major, prop.minor);
     } else if (p->kind != kNorm && ((size_t)gemm_smem_bytes() > prop.sharedMemPerBlockOptin ||
-                                    (size_t)stream_smem_bytes() > prop.sharedMemPerBlockOptin ||
+                                    (size_t)small_smem_bytes() > prop.sharedMemPerBlockOptin ||
                                     prop.multiProcessorCount < 2)) {
         st = api_fail(ROUTE_ERR_DEVICE, "the product kernels need %d B of shared memory per block",
                       gemm_smem_bytes());
     } else if (p->kind == kNorm && (e = norm_configure()) != cudaSuccess) {
         st = cuda_fail(e, "cudaFuncSetAttribute");
     } else if (p->kind != kNorm && ((e = gemm_configure()) != cudaSuccess ||
-                                    (e = stream_configure()) != cudaSuccess)) {
+                                    (e = small_configure()) != cudaSuccess)) {
         st = cuda_fail(e, "cudaFuncSetAttribute");
     }
     if (st != ROUTE_OK) {
@@ -449,12 +442,6 @@ route_status finish_prepare(route_layer *p, int device, route_layer **out) {
         p->o_part = area(norm_part_floats(p->k, p->sms) * 4);
     } else {
         size_t part = (size_t)p->pairs * kTilePartBytes;
-        const size_t widest = (size_t)(p->k > p->n ? p->k : p->n) > 2 * (size_t)p->f
-                                  ? (size_t)(p->k > p->n ? p->k : p->n)
-                                  : 2 * (size_t)p->f;
-        const size_t slots = p->sms + (widest + kStreamTile - 1) / kStreamTile;
-        const size_t few = R < kStreamRows ? R : kStreamRows;
-        if (part < slots * few * kStreamTile * 4) part = slots * few * kStreamTile * 4;
         if (p->kind == kLinear && p->train && part < dz_part_floats(p->n) * 4)
             part = dz_part_floats(p->n) * 4;
         p->o_part = area(part);
@@ -475,8 +462,8 @@ route_status finish_prepare(route_layer *p, int device, route_layer **out) {
         }
     }
     p->scratch_bytes = at;
-    if ((e = cudaMalloc(&p->words, kPlanWords * sizeof(unsigned))) != cudaSuccess ||
-        (e = cudaMemset(p->words, 0, kPlanWords * sizeof(unsigned))) != cudaSuccess ||
+    if ((e = cudaMalloc(&p->words, kWords * sizeof(unsigned))) != cudaSuccess ||
+        (e = cudaMemset(p->words, 0, kWords * sizeof(unsigned))) != cudaSuccess ||
         (e = cudaMalloc(&p->scratch, at ? at : 256)) != cudaSuccess) {
         if (p->words) cudaFree(p->words);
         delete p;
@@ -571,8 +558,7 @@ route_status route_layer_status(const route_layer *p) {
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
     unsigned w = 0;
     if ((e = cudaMemcpy(&w, p->words, sizeof w, cudaMemcpyDeviceToHost)) != cudaSuccess ||
-        // a call that gave up may have left arrival counts behind
-        (e = cudaMemset(p->words, 0, (w ? kPlanWords : 1) * sizeof w)) != cudaSuccess)
+        (e = cudaMemset(p->words, 0, sizeof w)) != cudaSuccess)
         return cuda_fail(e, "status word");
     if (w & kStatusBounds)
         return api_fail(ROUTE_ERR_DEVICE_BOUNDS, "a kernel skipped an index out of range");
@@ -743,7 +729,8 @@ route_status route_linear_backward(const route_layer *p, int rows, const void *d
     if (dW) {
         WeightGrad g = {{}, dz, p->k, p->n, dW, ld_dW};
         if ((st = operand(p, x, ld_x, rows, p->k, p->o_x, s, &g.x)) != ROUTE_OK) return st;
-        return weight_grads(p, &g, 1, rows, s);
+        const Shape shape = {p->k, p->n};
+        return weight_grads(p, &g, 1, rows, &shape, 1, s);
     }
     return ROUTE_OK;
 }
@@ -786,8 +773,8 @@ route_status route_gated_forward(const route_layer *p, int rows, const void *x, 
         set_out(q, h, ldf, p->type);
         q.act = p->act;
         q.saved = static_cast<float *>(saved), q.ld_saved = 2 * ldf;
-        const Choice ch = choose_one(p, rows, p->f, q.kblocks, true);
-        if ((st = pr.map(ox, p->k, rows, pr.a_rows(rows), "x", &q.a[0])) != ROUTE_OK ||
+        const Choice ch = choose_one(p, kFormNT, kEpiGated, rows, p->f, q.kblocks);
+        if ((st = pr.map(ox, p->k, rows, pr.a_rows(rows, ch), "x", &q.a[0])) != ROUTE_OK ||
             (st = pr.map(og, p->f, p->k, 64, "W_gate", &q.b[0][0])) != ROUTE_OK ||
             (st = pr.map(ou, p->f, p->k, 64, "W_up", &q.b[0][1])) != ROUTE_OK ||
             (st = run(p, pr, kFormNT, kEpiGated, ch, false, true, s)) != ROUTE_OK)
@@ -849,9 +836,9 @@ route_status route_gated_backward(const route_layer *p, int rows, const void *do
         q.out2 = const_cast<void *>(dz[1].p);
         q.act = p->act;
         q.saved = static_cast<float *>(const_cast<void *>(saved)), q.ld_saved = 2 * ldf;
-        const Choice ch = choose_one(p, rows, p->f, q.kblocks, false);
-        if ((st = pr.map(dy, p->n, rows, pr.a_rows(rows), "dout", &q.a[0])) != ROUTE_OK ||
-            (st = pr.map(od, p->n, p->f, pr.b_rows(rows, ch), "W_down", &q.b[0][0])) != ROUTE_OK)
+        const Choice ch = choose_one(p, kFormNN, kEpiDGate, rows, p->f, q.kblocks);
+        if ((st = pr.map(dy, p->n, rows, pr.a_rows(rows, ch), "dout", &q.a[0])) != ROUTE_OK ||
+            (st = pr.map(od, p->n, p->f, pr.b_rows(ch), "W_down", &q.b[0][0])) != ROUTE_OK)
             return st;
         q.b[0][1] = q.b[0][0];
         if ((st = run(p, pr, kFormNN, kEpiDGate, ch, false, true, s)) != ROUTE_OK) return st;
@@ -878,7 +865,8 @@ route_status route_gated_backward(const route_layer *p, int rows, const void *do
         const Operand h = {static_cast<const uint8_t *>(saved) + saved_h(p, rows), ldf};
         g[count++] = {h, dy, p->f, p->n, dW_down, ld_ddown};
     }
-    return weight_grads(p, g, count, rows, s);
+    const Shape shapes[3] = {{p->k, p->f}, {p->k, p->f}, {p->f, p->n}};
+    return weight_grads(p, g, count, rows, shapes, 3, s);
 }
 
 }  // extern "C"

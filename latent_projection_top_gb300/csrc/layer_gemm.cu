@@ -156,7 +156,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     const int pair = blockIdx.x >> 1;
 
     if (threadIdx.x == 0) {
-        if (args.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         s_abort = 0;
         for (int s = 0; s < S; ++s) {
             ptx::mbar_init(full_bar(s), 1);
@@ -183,6 +182,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             // ---------------- TMA producer (both CTAs) ----------------
             const uint64_t pol = ptx::policy_evict_normal();
             asm volatile("griddepcontrol.wait;" ::: "memory");
+            // after the wait: what follows may read this call's weights at once
+            if (args.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
             int it = 0;
             uint32_t armed = 0u, armed_par = 0u;
             bool ok = true;
@@ -348,8 +349,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 // epilogue.  The partials were just written and sit in L2.
 template <int EPI>
 __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant__ FinishArgs a) {
-    if (threadIdx.x == 0 && a.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x == 0 && a.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int groups = (a.p.N + 3) >> 2;
     const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= (long long)groups * a.p.M) return;

@@ -1,0 +1,347 @@
+// The layer operators' products with few rows (decode batches: each weight is
+// read once from memory, and reading it is the whole cost) or few tiles.
+//
+//   D[r, n] = sum_k A[r, k] B[k, n]
+//
+// Columns of D are the tensor cores' M side (128 a tile; a gated block: 64 of
+// gate and the same 64 of up), its rows their N side (16 to 128 a tile), so
+// that no MMA work is spent on rows that do not exist and one weight column
+// never meets more than one SM per 128 rows.  A tile's contraction is split
+// over a cluster of up to eight CTAs, enough of them to have the whole chip
+// read: their FP32 sums meet in distributed shared memory, each CTA adds its
+// share of the tile's elements over the cluster, in rank order, and runs the
+// operator's epilogue (layer_math.cuh) on the sums.  No partial goes through
+// global memory and no second kernel or counter is needed: at 128 rows of
+// 896x896 the sums' last step took 25 of 31 us when one CTA did it for a
+// tile, from partials in L2.
+//
+// Two CTAs fit an SM, so that a call's second product fetches its first
+// weights under the first one's last sums.
+//
+// Warp roles (320 threads): warp 0 TMA producer, warp 1 TMEM owner and MMA
+// issuer, warps 2..9 epilogue.  Every wait on a copy or an MMA is bounded, as
+// in layer_gemm.cu; all threads of a cluster reach its barriers whatever
+// happened before.
+#include "layer.cuh"
+#include "layer_math.cuh"
+#include "sm103_ptx.cuh"
+
+namespace route {
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kEpiThreads = 256;
+constexpr uint32_t kColBytes = kSmallTile * 64 * 2;  // 128 columns x 64 k
+
+__host__ __device__ constexpr uint32_t stage_bytes(int bn) { return kColBytes + (uint32_t)bn * 128; }
+__host__ __device__ constexpr int stages_of(int bn) { return bn == 16 ? 6 : bn == 32 ? 5 : bn == 64 ? 4 : 3; }
+__host__ __device__ constexpr uint32_t smem_of(int bn) { return 1024 + stages_of(bn) * stage_bytes(bn) + 256; }
+static_assert(2 * (smem_of(16) + 1024) <= 228 * 1024 && 2 * (smem_of(32) + 1024) <= 228 * 1024 &&
+                  2 * (smem_of(64) + 1024) <= 228 * 1024 && 2 * (smem_of(128) + 1024) <= 228 * 1024,
+              "two CTAs an SM");
+static_assert(128 * kSmallTile * 4 <= stages_of(128) * stage_bytes(128), "the sums fit the stages");
+
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+    d |= 1ull << 46;  // descriptor version for tcgen05
+    d |= 2ull << 61;  // 128-byte swizzle
+    return d;
+}
+// 16 k of an operand tile, as in layer_gemm.cu.
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t base, int kk) {
+    return MN ? smem_desc(base + kk * 2048u, 8192u, 1024u) : smem_desc(base + kk * 32u, 16u, 1024u);
+}
+
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const GemmArgs &a,
+                                           volatile int *abort_flag) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::global_timer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0u) {
+            if (*abort_flag) return false;
+            if (ptx::global_timer_ns() - t0 > a.timeout_ns) {
+                *abort_flag = 1;
+                atomicOr(a.status, kStatusTimeout);
+                return false;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, const GemmArgs &a) {
+    const uint64_t t0 = ptx::global_timer_ns();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if (ptx::global_timer_ns() - t0 > a.timeout_ns) {
+            atomicOr(a.status, kStatusTimeout);
+            return;
+        }
+    }
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+template <int FORM, int EPI, int BN>
+__global__ void __launch_bounds__(kThreads, 2)
+    layer_small_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs args,
+                       int chained) {
+    constexpr bool R_MN = FORM == kFormTT;   // rows' operand: M-contiguous, else K-contiguous
+    constexpr bool C_MN = FORM != kFormNN;   // columns' operand: N-contiguous, else K-contiguous
+    static_assert(!R_MN || BN >= 64, "an M-contiguous operand comes in boxes of 64");
+    constexpr int S = stages_of(BN);
+    constexpr uint32_t kStage = stage_bytes(BN);
+    constexpr int kTileCols = EPI == kEpiGated ? kSmallTile / 2 : kSmallTile;
+    constexpr uint32_t kTmemCols = BN < 32 ? 32 : BN;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t s_tmem_base;
+    __shared__ volatile int s_abort;
+
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    const uint32_t bars = sbase + S * kStage;
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
+    const uint32_t done_bar = bars + 8u * (2 * S);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int C = args.splits;
+    const int rank = blockIdx.x % C;  // clusters are C consecutive CTAs
+    int i = blockIdx.x / C;
+    int pi = 0;
+    while (pi + 1 < args.nprob && i >= args.p[pi + 1].item_base) ++pi;
+    const GemmProblem &p = args.p[pi];
+    i -= p.item_base;
+    const int tm = i % p.tiles_m, tn = i / p.tiles_m;
+    const int kb0 = (int)((long long)p.kblocks * rank / C);
+    const int total = (int)((long long)p.kblocks * (rank + 1) / C) - kb0;
+    const int row0 = tm * BN, col0 = tn * kTileCols;
+
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(full_bar(s), 1);
+            ptx::mbar_init(empty_bar(s), 1);
+        }
+        ptx::mbar_init(done_bar, 1);
+        ptx::fence_barrier_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_addr(&s_tmem_base), kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = s_tmem_base;
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA producer ----------------
+            // columns of one row tile are read once: they leave L2 first
+            const uint64_t pol_c = p.tiles_m == 1 ? ptx::policy_evict_first() : ptx::policy_evict_normal();
+            const uint64_t pol_r = ptx::policy_evict_last();
+            const uint32_t tx = kColBytes + args.a_bytes;
+            auto columns_of = [&](int it) {
+                const int kb = kb0 + it, s = it % S, seg = kb >= p.kswitch;
+                const int k0 = (seg ? kb - p.kswitch : kb) * 64;
+                const uint32_t sc = sbase + s * kStage, fb = full_bar(s);
+                const CUtensorMap *m = &maps.m[p.b[seg][0]];
+                ptx::mbar_arrive_expect_tx(fb, tx);
+                if (EPI == kEpiGated) {
+                    ptx::tma_load_2d(sc, m, fb, col0, k0, pol_c);
+                    ptx::tma_load_2d(sc + 8192u, &maps.m[p.b[seg][1]], fb, col0, k0, pol_c);
+                } else if (C_MN) {
+                    ptx::tma_load_2d(sc, m, fb, col0, k0, pol_c);
+                    ptx::tma_load_2d(sc + 8192u, m, fb, col0 + 64, k0, pol_c);
+                } else {
+                    ptx::tma_load_2d(sc, m, fb, k0, col0, pol_c);
+                }
+            };
+            auto rows_of = [&](int it) {
+                const int kb = kb0 + it, s = it % S, seg = kb >= p.kswitch;
+                const int k0 = (seg ? kb - p.kswitch : kb) * 64;
+                const uint32_t sr = sbase + s * kStage + kColBytes, fb = full_bar(s);
+                const CUtensorMap *m = &maps.m[p.a[seg]];
+                if (R_MN) {
+#pragma unroll
+                    for (int j = 0; j < BN / 64; ++j)
+                        ptx::tma_load_2d(sr + 8192u * j, m, fb, row0 + 64 * j, k0, pol_r);
+                } else {
+                    ptx::tma_load_2d(sr, m, fb, k0, row0, pol_r);
+                }
+            };
+            const int n_pre = chained ? min(total, S) : 0;
+            for (int it = 0; it < n_pre; ++it) columns_of(it);
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            if (args.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+            int issued = 0;
+            for (int it = 0; it < total; ++it, ++issued) {
+                if (!wait_phase(empty_bar(it % S), ((uint32_t)(it / S) & 1u) ^ 1u, args, &s_abort)) break;
+                if (args.test_stall && it == total - 1) break;  // test hook: it never arrives
+                if (it >= n_pre) columns_of(it);
+                rows_of(it);
+            }
+            if (s_abort)  // let every copy that was issued whole land
+                for (int it = issued > S ? issued - S : 0; it < issued; ++it)
+                    wait_drain(full_bar(it % S), (uint32_t)(it / S) & 1u, args);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---------------- MMA issuer ----------------
+            // kind::f16, FP32 accumulator, M = 128 columns, N = BN rows
+            const uint32_t fmt = args.fp16 ? 0u : 1u;
+            const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((C_MN ? 1u : 0u) << 15) |
+                                   ((R_MN ? 1u : 0u) << 16) | ((uint32_t)(BN >> 3) << 17) |
+                                   ((uint32_t)(kSmallTile >> 4) << 24);
+            for (int it = 0; it < total; ++it) {
+                const int s = it % S;
+                if (!wait_phase(full_bar(s), (uint32_t)(it / S) & 1u, args, &s_abort)) break;
+                ptx::tc_fence_after();
+                const uint32_t sc = sbase + s * kStage, sr = sc + kColBytes;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    ptx::mma_bf16(tmem_base, operand_desc<C_MN>(sc, kk), operand_desc<R_MN>(sr, kk), idesc,
+                                  (it > 0 || kk > 0) ? 1u : 0u);
+                ptx::mma_commit(empty_bar(s));
+            }
+            ptx::mma_commit(done_bar);  // every MMA retired (after an abort too)
+        }
+    }
+
+    // ---------------- sums over the cluster, and the epilogue ----------------
+    const int e = (int)threadIdx.x - 64;  // epilogue thread
+    const int rows = min(BN, p.M - row0);
+    constexpr int kGroups = kTileCols / 4;  // a thread's item: 4 columns of a row
+    const int items = rows * kGroups;
+    const int i0 = items * rank / C, i1 = items * (rank + 1) / C;
+    auto row_of = [&](int x) { return row0 + x / kGroups; };
+    auto col_of = [&](int x) { return col0 + x % kGroups * 4; };
+    EpiIn<EPI, 4> in;
+    if (warp >= 2) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (i0 + e < i1) epi_load<EPI, 4>(p, row_of(i0 + e), col_of(i0 + e), in);
+        ok = wait_phase(done_bar, 0u, args, &s_abort) && !s_abort;
+        __syncwarp();
+        ptx::tc_fence_after();
+        // the stages are free: this CTA's sums go there, [row][128 columns]
+        const int lq = warp & 3, cs = (warp - 2) >> 2;
+        float *sums = reinterpret_cast<float *>(smem_raw + (sbase - raw));
+#pragma unroll 1
+        for (int r = cs * 16; r < rows; r += 32) {
+            uint32_t v[16];
+            ptx::tmem_ld_x16(tmem_base + ((uint32_t)(32 * lq) << 16) + (uint32_t)r, v);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (r + j < rows) sums[(r + j) * kSmallTile + 32 * lq + lane] = total > 0 ? __uint_as_float(v[j]) : 0.f;
+        }
+        ptx::tc_fence_before();
+    }
+    __syncwarp();
+    if (C > 1)
+        ptx::cluster_sync();
+    else
+        __syncthreads();
+    if (warp >= 2 && ok) {
+        for (int x = i0 + e; x < i1; x += kEpiThreads) {
+            const uint32_t at = sbase + (uint32_t)((x / kGroups) * kSmallTile + x % kGroups * 4) * 4u;
+            float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+            if (x > i0 + e) epi_load<EPI, 4>(p, row_of(x), col_of(x), in);
+#pragma unroll 2
+            for (int j = 0; j < C; ++j) {
+                const uint32_t q = ptx::map_to_rank(at, (uint32_t)j);
+                const float4 f = ld_cluster_f4(q);
+                v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+                if (EPI == kEpiGated) {
+                    const float4 h = ld_cluster_f4(q + kTileCols * 4u);
+                    u[0] += h.x, u[1] += h.y, u[2] += h.z, u[3] += h.w;
+                }
+            }
+            epilogue<EPI, 4>(p, row_of(x), col_of(x), v, u, in);
+        }
+    }
+    if (warp == 1) {
+        if (lane == 0) wait_drain(done_bar, 0u, args);
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem_base, kTmemCols);
+    }
+    __syncwarp();
+    if (C > 1) ptx::cluster_sync();  // no CTA leaves while another may read its sums
+}
+
+const void *kernel_of(int form, int epi, int bn) {
+#define ROUTE_SMALL(F, E)                                                                       \
+    if (form == F && epi == E)                                                                  \
+        return bn == 16   ? reinterpret_cast<const void *>(layer_small_kernel<F, E, 16>)        \
+               : bn == 32 ? reinterpret_cast<const void *>(layer_small_kernel<F, E, 32>)        \
+               : bn == 64 ? reinterpret_cast<const void *>(layer_small_kernel<F, E, 64>)        \
+                          : reinterpret_cast<const void *>(layer_small_kernel<F, E, 128>);
+    ROUTE_SMALL(kFormNT, kEpiLinear)
+    ROUTE_SMALL(kFormNT, kEpiGated)
+    ROUTE_SMALL(kFormNN, kEpiLinear)
+    ROUTE_SMALL(kFormNN, kEpiDGate)
+#undef ROUTE_SMALL
+    if (form == kFormTT && epi == kEpiLinear)
+        return bn <= 64 ? reinterpret_cast<const void *>(layer_small_kernel<kFormTT, kEpiLinear, 64>)
+                        : reinterpret_cast<const void *>(layer_small_kernel<kFormTT, kEpiLinear, 128>);
+    return nullptr;
+}
+
+}  // namespace
+
+cudaError_t small_configure() {
+    for (int form = 0; form < 3; ++form)
+        for (int epi = 0; epi < 3; ++epi)
+            for (int bn : {16, 32, 64, 128})
+                if (const void *k = kernel_of(form, epi, bn)) {
+                    const int smem = (int)smem_of(form == kFormTT && bn < 64 ? 64 : bn);
+                    const cudaError_t e =
+                        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                    if (e != cudaSuccess) return e;
+                }
+    return cudaSuccess;
+}
+
+int small_smem_bytes() {
+    uint32_t most = 0;
+    for (int bn : {16, 32, 64, 128}) most = most < smem_of(bn) ? smem_of(bn) : most;
+    return (int)most;
+}
+
+cudaError_t small_launch(int form, int epi, int rows, const GemmMaps &maps, const GemmArgs &args,
+                         bool chained, cudaStream_t stream) {
+    const void *k = kernel_of(form, epi, rows);
+    if (k == nullptr || args.items < 1 || args.splits < 1 || args.splits > kSmallMaxSplits)
+        return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute attr[2];
+    c.gridDim = dim3((unsigned)(args.items * args.splits));
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = smem_of(rows);
+    c.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)args.splits;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    c.attrs = attr;
+    c.numAttrs = 2;
+    int ch = chained;
+    void *params[] = {const_cast<GemmMaps *>(&maps), const_cast<GemmArgs *>(&args), &ch};
+    return cudaLaunchKernelExC(&c, k, params);
+}
+
+}  // namespace route
