@@ -27,12 +27,12 @@
 // store FP32 partials; gemm_finish_kernel adds them in split order and runs
 // the same epilogue.  Results never depend on the order of arrival.
 //
-// Warp roles (320 threads, persistent, one CTA per SM, pairs = clusters):
+// Warp roles (576 or 320 threads, persistent, one CTA per SM, pairs = clusters):
 //   warp 0      TMA producer (both CTAs); completion counts on the leader's
 //               barrier, which the leader arms for both CTAs' bytes
 //   warp 1      TMEM owner (both CTAs); the leader's lane 0 issues the MMAs
-//   warps 2..9  epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 and half
-//               of the tile's columns
+//   the others  epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 and its
+//               share of the tile's columns
 //
 // Every wait is bounded: after timeout_ns a waiting thread sets the device
 // status word and the CTA's abort flag, in-flight copies and MMAs are
@@ -46,8 +46,11 @@ namespace {
 
 constexpr int kHalf = 128;                        // each CTA's rows of D
 constexpr uint32_t kABytes = kHalf * 64 * 2;      // 128 rows x 64 k
-constexpr int kEpiWarps = 8;
-constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
+// Epilogue warps: as many as the registers allow (the gradients of a gated
+// block need more than 113 a thread).  With 8 instead of 16 a tile of a short
+// contraction waited for the epilogue of the one before it.
+__host__ __device__ constexpr int epi_warps(int epi) { return epi == kEpiDGate ? 8 : 16; }
+__host__ __device__ constexpr int gemm_threads(int epi) { return 64 + 32 * epi_warps(epi); }
 constexpr uint32_t kSmemLimit = 227 * 1024;
 
 __host__ __device__ constexpr uint32_t b_bytes(int bn) { return (uint32_t)bn / 2 * 64 * 2; }
@@ -129,13 +132,16 @@ __device__ __forceinline__ Item item_of(const GemmArgs &a, int i) {
 }
 
 template <int FORM, int EPI, int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1)
     layer_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs args) {
     constexpr bool A_MN = FORM == kFormTT, B_MN = FORM != kFormNN;
     constexpr int S = stages_of(BN);
     constexpr uint32_t kStage = stage_bytes(BN);
     constexpr int kTileCols = EPI == kEpiGated ? BN / 2 : BN;  // columns of D a tile
     constexpr int kBCols = BN / 2;                             // B columns each CTA loads
+    constexpr int kEpiWarps = epi_warps(EPI);
+    constexpr int kWarpCols = kTileCols / (kEpiWarps / 4);     // columns of D an epilogue warp drains
+    static_assert(kWarpCols % 16 == 0, "whole chunks");
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t s_tmem_base;
     __shared__ volatile int s_abort;
@@ -271,9 +277,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             wait_drain(drain_bar, 0u, args);
         }
     } else {
-        // ---------------- epilogue (warps 2..9, both CTAs) ----------------
+        // ---------------- epilogue (both CTAs) ----------------
         const int lq = warp & 3;         // TMEM lanes 32 lq .. + 31 = rows of D
-        const int cs = (warp - 2) >> 2;  // which half of the tile's columns
+        const int cs = (warp - 2) >> 2;  // which share of the tile's columns
         const uint32_t lanes = tmem_base + ((uint32_t)(32 * lq) << 16);
         asm volatile("griddepcontrol.wait;" ::: "memory");
         int job = 0;
@@ -282,15 +288,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             const GemmProblem &p = args.p[w.p];
             const int t = job & 1;
             const int r = w.tm * kGemmBM + (int)rank * kHalf + 32 * lq + lane;
-            const int c0 = w.tn * kTileCols + cs * (kTileCols / 2);
+            const int c0 = w.tn * kTileCols + cs * kWarpCols;
             EpiIn<EPI, 16> in, next;
             if (args.splits == 1) epi_load<EPI, 16>(p, r, c0, in);
             const bool ok = wait_phase(tfull_bar(t), ((uint32_t)job >> 1) & 1u, args, &s_abort);
             __syncwarp();  // the TMEM loads that follow are warp-wide
             if (!ok) break;
             ptx::tc_fence_after();
-            const uint32_t acc = lanes + (uint32_t)(t * BN + cs * (kTileCols / 2));
-            constexpr int kChunks = kTileCols / 2 / 16;
+            const uint32_t acc = lanes + (uint32_t)(t * BN + cs * kWarpCols);
+            constexpr int kChunks = kWarpCols / 16;
 #pragma unroll 1
             for (int ch = 0; ch < kChunks; ++ch) {
                 uint32_t v[16], u[16];
@@ -422,7 +428,7 @@ cudaError_t gemm_launch(int form, int epi, int bn, const GemmMaps &maps, const G
     const void *k = kernel_of(form, epi, bn);
     if (k == nullptr || args.pairs <= 0 || args.items <= 0) return cudaErrorInvalidConfiguration;
     void *params[] = {const_cast<GemmMaps *>(&maps), const_cast<GemmArgs *>(&args)};
-    return launch_chained(k, dim3(2 * args.pairs), dim3(kGemmThreads), smem_of(bn), params, stream);
+    return launch_chained(k, dim3(2 * args.pairs), dim3(gemm_threads(epi)), smem_of(bn), params, stream);
 }
 
 cudaError_t gemm_finish_launch(int epi, const FinishArgs &args, cudaStream_t stream) {
