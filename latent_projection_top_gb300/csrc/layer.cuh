@@ -25,27 +25,34 @@ enum LayerEpi : int {
     kEpiDGate = 2    // v = dh: out = dh * up * act'(gate), out2 = dh * act(gate), from `saved`
 };
 
-// One matrix product D[M, N] = A B with a contraction of `kblocks` blocks of
-// 64 (blocks from `kswitch` on come from the second pair of operands), and
-// what becomes of D.  Map indexes name entries of GemmMaps.
-struct GemmProblem {
+// What becomes of a product's sums D[M, N].  A kernel copies this into
+// registers: read from the launch's arguments with an index that is known
+// only at run time, a step of the epilogue waited for each field (a tile's
+// epilogue took 20 us).
+struct Epilogue {
     int M, N;                   // rows and columns of the result (gated: N hidden columns)
-    int tiles_m, tiles_n, band; // 256-row tiles, column tiles, column tiles of a band
-    int item_base;              // first work item of this problem
-    int kblocks, kswitch;
-    uint8_t a[2], b[2][2];      // A map of each segment, B map of each segment and CTA of the pair
     int out_type;               // type of out, out2 and residual
     int bias_type;
+    int act;
+    int vec;                    // what may be read and written as vectors (kVec*)
     const void *bias;           // [N]
     const void *residual;       // [M, N], row stride ld_res
     void *out;                  // [M, N], row stride ld_out
     void *out2;                 // kEpiDGate: d up, same layout
-    float *saved;               // FP32 pre-activations, row stride ld_saved (see the epilogue)
-    long long ld_res, ld_out, ld_saved;
+    float *saved, *saved2;      // FP32 pre-activations (gated: of gate and of up), row stride ld_saved
     float *part;                // splits > 1: FP32 partials [split][M][ld_part]
-    long long ld_part;
-    int act;
-    int vec;                    // what may be read and written as vectors (kVec*)
+    long long ld_res, ld_out, ld_saved, ld_part;
+};
+
+// One matrix product D[M, N] = A B with a contraction of `kblocks` blocks of
+// 64 (blocks from `kswitch` on come from the second pair of operands).  Map
+// indexes name entries of GemmMaps.
+struct GemmProblem {
+    Epilogue e;
+    int tiles_m, tiles_n, band; // row tiles, column tiles, column tiles of a band
+    int item_base;              // first work item of this problem
+    int kblocks, kswitch;
+    uint8_t a[2], b[2][2];      // A map of each segment, B map of each segment and CTA of the pair
 };
 
 constexpr int kGemmMaxProblems = 3;
@@ -73,7 +80,7 @@ struct GemmArgs {
 struct FinishArgs {
     int splits;
     int trigger;
-    GemmProblem p;
+    Epilogue e;
 };
 
 enum GemmForm : int {

@@ -115,17 +115,15 @@ route_status check_plan(const route_layer *p, LayerKind kind, int rows) {
 
 int vec_bits(const void *out, long long ld_out, const void *out2, const void *res, long long ld_res,
              int out_type, const void *bias) {
-    const int es = layer_esize(out_type);
-    int v = 0;
-    auto rows_on = [&](const void *p, long long ld, unsigned a) {
-        return p == nullptr || (aligned(p, a) && ld * es % a == 0);
+    // four values at a time
+    const int bytes = 4 * layer_esize(out_type);
+    auto rows_on = [&](const void *p, long long ld) {
+        return p == nullptr || (aligned(p, (unsigned)bytes) && ld % 4 == 0);
     };
-    if (rows_on(out, ld_out, 32) && rows_on(out2, ld_out, 32))
-        v |= 2;
-    else if (rows_on(out, ld_out, 16) && rows_on(out2, ld_out, 16))
-        v |= 1;
-    if (rows_on(res, ld_res, 16)) v |= kVecRes;
-    if (aligned(bias, 16)) v |= kVecBias;
+    int v = 0;
+    if (rows_on(out, ld_out) && rows_on(out2, ld_out)) v |= kVecOut;
+    if (rows_on(res, ld_res)) v |= kVecRes;
+    if (aligned(bias, 8)) v |= kVecBias;
     return v;
 }
 
@@ -211,8 +209,8 @@ Choice choose(const route_layer *p, int form, int epi, const Shape *shape, int c
 }
 
 void set_tiles(GemmProblem &q, int tile_rows, int tile_cols, int pairs) {
-    q.tiles_m = ceil_div(q.M, tile_rows);
-    q.tiles_n = ceil_div(q.N, tile_cols);
+    q.tiles_m = ceil_div(q.e.M, tile_rows);
+    q.tiles_n = ceil_div(q.e.N, tile_cols);
     // column tiles of a band: about as many as the row tiles at work at once
     int band = (pairs + q.tiles_m - 1) / q.tiles_m;
     band = band < 8 ? 8 : band;
@@ -269,9 +267,9 @@ route_status run(const route_layer *p, Product &pr, int form, int epi, const Cho
         q.item_base = items;
         items += q.tiles_m * q.tiles_n * (ch.small ? 1 : ch.splits);
         if (!ch.small && ch.splits > 1) {
-            q.part = part;
-            q.ld_part = up16(q.N) * (epi == kEpiGated ? 2 : 1);
-            part += (size_t)ch.splits * q.M * q.ld_part;
+            q.e.part = part;
+            q.e.ld_part = up16(q.e.N) * (epi == kEpiGated ? 2 : 1);
+            part += (size_t)ch.splits * q.e.M * q.e.ld_part;
         }
     }
     a.items = items;
@@ -290,7 +288,7 @@ route_status run(const route_layer *p, Product &pr, int form, int epi, const Cho
             FinishArgs f;
             f.splits = ch.splits;
             f.trigger = more || i + 1 < a.nprob;
-            f.p = a.p[i];
+            f.e = a.p[i].e;
             e = gemm_finish_launch(epi, f, stream);
             if (e != cudaSuccess) return cuda_fail(e, "product finish kernel launch");
         }
@@ -305,10 +303,10 @@ Choice choose_one(const route_layer *p, int form, int epi, int M, int N, int kbl
 int kblocks_of(int k) { return (k + 63) / 64; }
 
 void set_out(GemmProblem &q, void *out, long long ld_out, int out_type) {
-    q.out = out;
-    q.ld_out = q.M > 1 ? ld_out : up16(q.N);
-    q.out_type = out_type;
-    q.vec = vec_bits(q.out, q.ld_out, nullptr, nullptr, 0, out_type, nullptr);
+    q.e.out = out;
+    q.e.ld_out = q.e.M > 1 ? ld_out : up16(q.e.N);
+    q.e.out_type = out_type;
+    q.e.vec = vec_bits(q.e.out, q.e.ld_out, nullptr, nullptr, 0, out_type, nullptr);
 }
 
 // out[M, N] = epilogue(A[M, K] W[K, N]): A K-contiguous, W N-contiguous.
@@ -319,15 +317,15 @@ route_status forward_product(const route_layer *p, const Operand &A, const Opera
     Product pr(p);
     GemmProblem &q = pr.args.p[0];
     pr.args.nprob = 1;
-    q.M = M, q.N = N;
+    q.e.M = M, q.e.N = N;
     q.kblocks = q.kswitch = kblocks_of(K);
     set_out(q, out, ld_out, out_type);
-    q.bias = bias, q.bias_type = p->type;
-    q.residual = residual;
-    q.ld_res = M > 1 ? ld_res : up16(N);
-    q.act = act;
-    q.saved = saved, q.ld_saved = up16(N);
-    q.vec = vec_bits(out, q.ld_out, nullptr, residual, q.ld_res, out_type, bias);
+    q.e.bias = bias, q.e.bias_type = p->type;
+    q.e.residual = residual;
+    q.e.ld_res = M > 1 ? ld_res : up16(N);
+    q.e.act = act;
+    q.e.saved = saved, q.e.ld_saved = up16(N);
+    q.e.vec = vec_bits(out, q.e.ld_out, nullptr, residual, q.e.ld_res, out_type, bias);
     const Choice ch = choose_one(p, kFormNT, kEpiLinear, M, N, q.kblocks);
     route_status st;
     if ((st = pr.map(A, K, M, pr.a_rows(M, ch), "x", &q.a[0])) != ROUTE_OK ||
@@ -344,7 +342,7 @@ route_status input_grad(const route_layer *p, int terms, const Operand *dz, cons
     Product pr(p);
     GemmProblem &q = pr.args.p[0];
     pr.args.nprob = 1;
-    q.M = M, q.N = K;
+    q.e.M = M, q.e.N = K;
     q.kswitch = kblocks_of(N);
     q.kblocks = terms * q.kswitch;
     set_out(q, out, ld_out, p->type);
@@ -374,12 +372,12 @@ route_status weight_grads(const route_layer *p, const WeightGrad *w, int count, 
     pr.args.nprob = count;
     for (int i = 0; i < count; ++i) {
         GemmProblem &q = pr.args.p[i];
-        q.M = w[i].K, q.N = w[i].N;
+        q.e.M = w[i].K, q.e.N = w[i].N;
         q.kblocks = q.kswitch = kblocks_of(rows);
         set_out(q, w[i].dW, w[i].ld, p->type);
         route_status st;
-        if ((st = pr.map(w[i].x, q.M, rows, 64, "x", &q.a[0])) != ROUTE_OK ||
-            (st = pr.map(w[i].dz, q.N, rows, 64, "dz", &q.b[0][0])) != ROUTE_OK)
+        if ((st = pr.map(w[i].x, q.e.M, rows, 64, "x", &q.a[0])) != ROUTE_OK ||
+            (st = pr.map(w[i].dz, q.e.N, rows, 64, "dz", &q.b[0][0])) != ROUTE_OK)
             return st;
         q.b[0][1] = q.b[0][0];
     }
@@ -768,11 +766,12 @@ route_status route_gated_forward(const route_layer *p, int rows, const void *x, 
         Product pr(p);
         GemmProblem &q = pr.args.p[0];
         pr.args.nprob = 1;
-        q.M = rows, q.N = p->f;
+        q.e.M = rows, q.e.N = p->f;
         q.kblocks = q.kswitch = kblocks_of(p->k);
         set_out(q, h, ldf, p->type);
-        q.act = p->act;
-        q.saved = static_cast<float *>(saved), q.ld_saved = 2 * ldf;
+        q.e.act = p->act;
+        q.e.saved = static_cast<float *>(saved), q.e.ld_saved = ldf;
+        q.e.saved2 = saved ? q.e.saved + (size_t)rows * ldf : nullptr;
         const Choice ch = choose_one(p, kFormNT, kEpiGated, rows, p->f, q.kblocks);
         if ((st = pr.map(ox, p->k, rows, pr.a_rows(rows, ch), "x", &q.a[0])) != ROUTE_OK ||
             (st = pr.map(og, p->f, p->k, 64, "W_gate", &q.b[0][0])) != ROUTE_OK ||
@@ -829,13 +828,14 @@ route_status route_gated_backward(const route_layer *p, int rows, const void *do
         Product pr(p);
         GemmProblem &q = pr.args.p[0];
         pr.args.nprob = 1;
-        q.M = rows, q.N = p->f;
+        q.e.M = rows, q.e.N = p->f;
         q.kblocks = q.kswitch = kblocks_of(p->n);
         set_out(q, const_cast<void *>(dz[0].p), ldf, p->type);
-        q.ld_out = ldf;
-        q.out2 = const_cast<void *>(dz[1].p);
-        q.act = p->act;
-        q.saved = static_cast<float *>(const_cast<void *>(saved)), q.ld_saved = 2 * ldf;
+        q.e.ld_out = ldf;
+        q.e.out2 = const_cast<void *>(dz[1].p);
+        q.e.act = p->act;
+        q.e.saved = static_cast<float *>(const_cast<void *>(saved)), q.e.ld_saved = ldf;
+        q.e.saved2 = q.e.saved + (size_t)rows * ldf;
         const Choice ch = choose_one(p, kFormNN, kEpiDGate, rows, p->f, q.kblocks);
         if ((st = pr.map(dy, p->n, rows, pr.a_rows(rows, ch), "dout", &q.a[0])) != ROUTE_OK ||
             (st = pr.map(od, p->n, p->f, pr.b_rows(ch), "W_down", &q.b[0][0])) != ROUTE_OK)

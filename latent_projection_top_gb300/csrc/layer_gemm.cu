@@ -18,16 +18,15 @@
 // columns of D in its TMEM.  Two accumulators alternate, so that one tile is
 // drained while the next is computed.
 //
-// Rows of D are the TMEM lanes: a thread owns one row and 16 consecutive
-// columns at a time, which it reads, transforms and stores as whole 32-byte
-// sectors; everything the epilogue reads (residual, saved pre-activations)
-// has the same shape.
+// Rows of D are the TMEM lanes.  An epilogue warp takes 64 (or 32) columns of its 32
+// rows out of TMEM into shared memory and back with neighbouring threads on
+// neighbouring columns, four to a thread, for the operator's epilogue.
 //
 // Split K: with few tiles, `splits` CTA pairs share a tile's contraction and
 // store FP32 partials; gemm_finish_kernel adds them in split order and runs
 // the same epilogue.  Results never depend on the order of arrival.
 //
-// Warp roles (576 or 320 threads, persistent, one CTA per SM, pairs = clusters):
+// Warp roles (320 threads, persistent, one CTA per SM, pairs = clusters):
 //   warp 0      TMA producer (both CTAs); completion counts on the leader's
 //               barrier, which the leader arms for both CTAs' bytes
 //   warp 1      TMEM owner (both CTAs); the leader's lane 0 issues the MMAs
@@ -46,18 +45,22 @@ namespace {
 
 constexpr int kHalf = 128;                        // each CTA's rows of D
 constexpr uint32_t kABytes = kHalf * 64 * 2;      // 128 rows x 64 k
-// Epilogue warps: as many as the registers allow (the gradients of a gated
-// block need more than 113 a thread).  With 8 instead of 16 a tile of a short
-// contraction waited for the epilogue of the one before it.
-__host__ __device__ constexpr int epi_warps(int epi) { return epi == kEpiDGate ? 8 : 16; }
-__host__ __device__ constexpr int gemm_threads(int epi) { return 64 + 32 * epi_warps(epi); }
+constexpr int kEpiWarps = 8;
+constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
+// Columns of D an epilogue warp turns around at once, limited by the registers
+// that its values and inputs take, and a warp's buffer for it.
+__host__ __device__ constexpr int group_cols(int epi) { return epi == kEpiLinear ? 64 : 32; }
+constexpr uint32_t kTurnBytes = 32 * 64 * 4;
 constexpr uint32_t kSmemLimit = 227 * 1024;
 
 __host__ __device__ constexpr uint32_t b_bytes(int bn) { return (uint32_t)bn / 2 * 64 * 2; }
 __host__ __device__ constexpr uint32_t stage_bytes(int bn) { return kABytes + b_bytes(bn); }
-__host__ __device__ constexpr int stages_of(int bn) { return bn == 256 ? 6 : 8; }
-__host__ __device__ constexpr uint32_t smem_of(int bn) { return 1024 + stages_of(bn) * stage_bytes(bn) + 256; }
+__host__ __device__ constexpr int stages_of(int bn) { return bn == 256 ? 5 : 6; }
+__host__ __device__ constexpr uint32_t smem_of(int bn) { return 1024 + stages_of(bn) * stage_bytes(bn) + kEpiWarps * kTurnBytes + 256; }
 static_assert(smem_of(256) <= kSmemLimit && smem_of(128) <= kSmemLimit, "shared memory");
+
+// How long a poll of a barrier may be held in hardware.
+constexpr uint32_t kWaitHintNs = 20000;
 
 __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
     uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
@@ -79,17 +82,15 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t base, int kk) {
 
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const GemmArgs &a,
                                            volatile int *abort_flag) {
-    if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+    if (ptx::mbar_try_wait_hint(bar, parity, kWaitHintNs)) return true;
     const uint64_t t0 = ptx::global_timer_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
-        if ((it & 63u) == 0u) {
-            if (*abort_flag) return false;
-            if (ptx::global_timer_ns() - t0 > a.timeout_ns) {
-                *abort_flag = 1;
-                atomicOr(a.status, kStatusTimeout);
-                return false;
-            }
+    for (;;) {
+        if (ptx::mbar_try_wait_hint(bar, parity, kWaitHintNs)) return true;
+        if (*abort_flag) return false;
+        if (ptx::global_timer_ns() - t0 > a.timeout_ns) {
+            *abort_flag = 1;
+            atomicOr(a.status, kStatusTimeout);
+            return false;
         }
     }
 }
@@ -97,7 +98,7 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const 
 // Bounded wait used only while tearing down.
 __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, const GemmArgs &a) {
     const uint64_t t0 = ptx::global_timer_ns();
-    while (!ptx::mbar_try_wait_cluster(bar, parity)) {
+    while (!ptx::mbar_try_wait_hint(bar, parity, kWaitHintNs)) {
         if (ptx::global_timer_ns() - t0 > a.timeout_ns) {
             atomicOr(a.status, kStatusTimeout);
             return;
@@ -132,23 +133,24 @@ __device__ __forceinline__ Item item_of(const GemmArgs &a, int i) {
 }
 
 template <int FORM, int EPI, int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     layer_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs args) {
     constexpr bool A_MN = FORM == kFormTT, B_MN = FORM != kFormNN;
     constexpr int S = stages_of(BN);
     constexpr uint32_t kStage = stage_bytes(BN);
     constexpr int kTileCols = EPI == kEpiGated ? BN / 2 : BN;  // columns of D a tile
     constexpr int kBCols = BN / 2;                             // B columns each CTA loads
-    constexpr int kEpiWarps = epi_warps(EPI);
-    constexpr int kWarpCols = kTileCols / (kEpiWarps / 4);     // columns of D an epilogue warp drains
-    static_assert(kWarpCols % 16 == 0, "whole chunks");
+    constexpr int kWarpCols = kTileCols / 2;                   // columns of D an epilogue warp drains
+    constexpr int kG = group_cols(EPI);
+    static_assert(kWarpCols % kG == 0 && kG % 16 == 0, "whole groups");
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t s_tmem_base;
     __shared__ volatile int s_abort;
 
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
-    const uint32_t bars = sbase + S * kStage;
+    const uint32_t turn = sbase + S * kStage;
+    const uint32_t bars = turn + kEpiWarps * kTurnBytes;
     auto full_bar = [&](int s) { return bars + 8u * s; };             // leader's are used
     auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
     auto tfull_bar = [&](int t) { return bars + 8u * (2 * S + t); };
@@ -281,32 +283,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
         const int lq = warp & 3;         // TMEM lanes 32 lq .. + 31 = rows of D
         const int cs = (warp - 2) >> 2;  // which share of the tile's columns
         const uint32_t lanes = tmem_base + ((uint32_t)(32 * lq) << 16);
+        const uint32_t mine = turn + (uint32_t)(warp - 2) * kTurnBytes;
         asm volatile("griddepcontrol.wait;" ::: "memory");
         int job = 0;
         for (int i = pair; i < args.items; i += args.pairs, ++job) {
             const Item w = item_of(args, i);
-            const GemmProblem &p = args.p[w.p];
+            const Epilogue p = args.p[w.p].e;
             const int t = job & 1;
-            const int r = w.tm * kGemmBM + (int)rank * kHalf + 32 * lq + lane;
+            const int r0 = w.tm * kGemmBM + (int)rank * kHalf + 32 * lq;
             const int c0 = w.tn * kTileCols + cs * kWarpCols;
-            EpiIn<EPI, 16> in, next;
-            if (args.splits == 1) epi_load<EPI, 16>(p, r, c0, in);
-            const bool ok = wait_phase(tfull_bar(t), ((uint32_t)job >> 1) & 1u, args, &s_abort);
-            __syncwarp();  // the TMEM loads that follow are warp-wide
-            if (!ok) break;
+            // A thread's share of a group: four columns of kSteps rows, kStep apart.
+            constexpr int kLanesRow = kG / 4, kStep = 32 / kLanesRow, kSteps = 32 / kStep;
+            constexpr int kGroups = kWarpCols / kG;
+            const int tr = r0 + lane / kLanesRow, tc = c0 + lane % kLanesRow * 4;
+            const bool rows_full = args.splits == 1 && r0 + 32 <= p.M &&
+                                   (p.vec & (kVecOut | kVecRes | kVecBias)) == (kVecOut | kVecRes | kVecBias);
+            auto full = [&](int g) { return rows_full && c0 + (g + 1) * kG <= p.N; };
+            GroupIn<EPI, kSteps> in;
+            // inputs go out before the tile's sums are complete
+            if (full(0)) group_load<EPI, kSteps>(p, tr, tc, kStep, in);
+            // one warp polls, the others sleep at the barrier
+            const bool ok = warp != 2 || wait_phase(tfull_bar(t), ((uint32_t)job >> 1) & 1u, args, &s_abort);
+            if (!ptx::named_bar_and(1, 32 * kEpiWarps, ok)) break;
             ptx::tc_fence_after();
             const uint32_t acc = lanes + (uint32_t)(t * BN + cs * kWarpCols);
-            constexpr int kChunks = kWarpCols / 16;
+            // Four columns (16 bytes, unit x) of a row sit at unit x ^ (row & 7):
+            // rows a line apart, and columns of a row, are both free of conflicts.
+            auto unit = [&](int row, int x) {
+                return mine + (uint32_t)(row * kG * 4 + ((x ^ (row & 7)) << 4));
+            };
+            auto put = [&](uint32_t tmem) {  // this thread's row of kG columns
+#pragma unroll
+                for (int h = 0; h < kG / 16; ++h) {
+                    uint32_t v[16];
+                    ptx::tmem_ld_x16(tmem + 16u * h, v);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(unit(lane, 4 * h + x)),
+                                     "r"(v[4 * x]), "r"(v[4 * x + 1]), "r"(v[4 * x + 2]), "r"(v[4 * x + 3])
+                                     : "memory");
+                }
+                __syncwarp();
+            };
+            auto get = [&](float (&v)[4 * kSteps]) {  // this thread's columns of kSteps rows
+#pragma unroll
+                for (int j = 0; j < kSteps; ++j)
+                    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                 : "=f"(v[4 * j]), "=f"(v[4 * j + 1]), "=f"(v[4 * j + 2]), "=f"(v[4 * j + 3])
+                                 : "r"(unit(j * kStep + lane / kLanesRow, lane % kLanesRow))
+                                 : "memory");
+                __syncwarp();
+            };
 #pragma unroll 1
-            for (int ch = 0; ch < kChunks; ++ch) {
-                uint32_t v[16], u[16];
-                if (ch + 1 < kChunks && args.splits == 1)
-                    epi_load<EPI, 16>(p, r, c0 + 16 * ch + 16, next);
-                __syncwarp();  // lanes past the last row skipped the stores
-                ptx::tmem_ld_x16(acc + 16u * ch, v);
-                if (EPI == kEpiGated) ptx::tmem_ld_x16(acc + 16u * ch + kTileCols, u);
-                ptx::tmem_ld_wait();
-                if (ch == kChunks - 1) {  // every column is in registers
+            for (int g = 0; g < kGroups; ++g) {
+                float v[4 * kSteps], u[EPI == kEpiGated ? 4 * kSteps : 1];
+                const uint32_t from = acc + (uint32_t)(g * kG);
+                if constexpr (EPI == kEpiGated) {
+                    put(from + kTileCols);
+                    get(u);
+                }
+                put(from);
+                if (g == kGroups - 1) {  // everything has left TMEM
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -316,25 +354,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
                             ptx::mbar_arrive_remote(ptx::map_to_rank(tempty_bar(t), 0u));
                     }
                 }
-                const int c = c0 + 16 * ch;
-                float vf[16], uf[16];
+                get(v);
+                const int c = tc + g * kG;
+                if (full(g)) {
+                    group_epilogue<EPI, kSteps>(p, tr, c, kStep, v, u, in);
+                    if (g + 1 < kGroups && full(g + 1)) group_load<EPI, kSteps>(p, tr, c + kG, kStep, in);
+                } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    vf[j] = __uint_as_float(v[j]);
-                    uf[j] = EPI == kEpiGated ? __uint_as_float(u[j]) : 0.f;
-                }
-                if (args.splits == 1) {
-                    epilogue<EPI, 16>(p, r, c, vf, uf, in);
-                } else if (r < p.M && c < p.N) {  // partials: rows padded to whole chunks
-                    float *part = p.part + ((long long)w.split * p.M + r) * p.ld_part;
-                    if constexpr (EPI == kEpiGated) {
-                        store_saved<16>(part + saved_gate(c), vf);
-                        store_saved<16>(part + saved_gate(c) + 16, uf);
-                    } else {
-                        store_saved<16>(part + c, vf);
+                    for (int j = 0; j < kSteps; ++j) {
+                        const int r = tr + j * kStep;
+                        float x[4], y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[e] = v[4 * j + e];
+                            if constexpr (EPI == kEpiGated) y[e] = u[4 * j + e];
+                        }
+                        if (args.splits == 1) {
+                            EpiIn<EPI> one;
+                            epi_load<EPI>(p, r, c, one);
+                            epilogue<EPI>(p, r, c, x, y, one);
+                        } else if (r < p.M && c < p.N) {  // partials: rows padded to whole groups
+                            float *part = p.part + ((long long)w.split * p.M + r) * p.ld_part + c;
+                            *reinterpret_cast<float4 *>(part) = make_float4(x[0], x[1], x[2], x[3]);
+                            if (EPI == kEpiGated)
+                                *reinterpret_cast<float4 *>(part + p.ld_part / 2) = make_float4(y[0], y[1], y[2], y[3]);
+                        }
                     }
                 }
-                in = next;
             }
         }
     }
@@ -357,25 +403,25 @@ template <int EPI>
 __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant__ FinishArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x == 0 && a.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int groups = (a.p.N + 3) >> 2;
+    const int groups = (a.e.N + 3) >> 2;
     const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= (long long)groups * a.p.M) return;
+    if (i >= (long long)groups * a.e.M) return;
     const int r = (int)(i / groups), c = (int)(i % groups) * 4;
-    const float *src = a.p.part + (long long)r * a.p.ld_part + (EPI == kEpiGated ? saved_gate(c) : c);
-    const long long step = (long long)a.p.M * a.p.ld_part;
+    const float *src = a.e.part + (long long)r * a.e.ld_part + c;
+    const long long step = (long long)a.e.M * a.e.ld_part;
     float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
-    EpiIn<EPI, 4> in;
-    epi_load<EPI, 4>(a.p, r, c, in);
+    EpiIn<EPI> in;
+    epi_load<EPI>(a.e, r, c, in);
 #pragma unroll 4
     for (int s = 0; s < a.splits; ++s, src += step) {
         const float4 x = *reinterpret_cast<const float4 *>(src);
         v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
         if (EPI == kEpiGated) {
-            const float4 y = *reinterpret_cast<const float4 *>(src + 16);
+            const float4 y = *reinterpret_cast<const float4 *>(src + a.e.ld_part / 2);
             u[0] += y.x, u[1] += y.y, u[2] += y.z, u[3] += y.w;
         }
     }
-    epilogue<EPI, 4>(a.p, r, c, v, u, in);
+    epilogue<EPI>(a.e, r, c, v, u, in);
 }
 
 cudaError_t launch_chained(const void *fn, dim3 grid, dim3 block, size_t smem, void **params,
@@ -428,14 +474,14 @@ cudaError_t gemm_launch(int form, int epi, int bn, const GemmMaps &maps, const G
     const void *k = kernel_of(form, epi, bn);
     if (k == nullptr || args.pairs <= 0 || args.items <= 0) return cudaErrorInvalidConfiguration;
     void *params[] = {const_cast<GemmMaps *>(&maps), const_cast<GemmArgs *>(&args)};
-    return launch_chained(k, dim3(2 * args.pairs), dim3(gemm_threads(epi)), smem_of(bn), params, stream);
+    return launch_chained(k, dim3(2 * args.pairs), dim3(kGemmThreads), smem_of(bn), params, stream);
 }
 
 cudaError_t gemm_finish_launch(int epi, const FinishArgs &args, cudaStream_t stream) {
     const void *k = epi == kEpiLinear  ? reinterpret_cast<const void *>(gemm_finish_kernel<kEpiLinear>)
                     : epi == kEpiGated ? reinterpret_cast<const void *>(gemm_finish_kernel<kEpiGated>)
                                        : reinterpret_cast<const void *>(gemm_finish_kernel<kEpiDGate>);
-    const long long threads = (long long)((args.p.N + 3) / 4) * args.p.M;
+    const long long threads = (long long)((args.e.N + 3) / 4) * args.e.M;
     void *params[] = {const_cast<FinishArgs *>(&args)};
     return launch_chained(k, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, params, stream);
 }

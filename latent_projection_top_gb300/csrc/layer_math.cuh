@@ -147,231 +147,254 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, int type) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ void st_global_v8(void *p, const uint32_t (&w)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
-                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
-__device__ __forceinline__ void ld_global_v8(const void *p, uint32_t (&w)[8]) {
-    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
-                   "=r"(w[6]), "=r"(w[7])
-                 : "l"(p)
-                 : "memory");
-}
-
-// W consecutive values at element i; `n` of them exist; `vec`: the address is
-// aligned for whole-vector access (32 bytes for W = 16, 8 for W = 4).
-template <int W>
-__device__ __forceinline__ void load_vec(const void *p, int type, long long i, int n, bool vec,
-                                         float (&v)[W]) {
-    if (vec && n >= W) {
-        if (type == kFp32) {
-            const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-#pragma unroll
-            for (int j = 0; j < W / 4; ++j) {
-                const float4 t = q[j];
-                v[4 * j] = t.x, v[4 * j + 1] = t.y, v[4 * j + 2] = t.z, v[4 * j + 3] = t.w;
-            }
-        } else if constexpr (W == 16) {
-            const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint4 t = q[j];
-                const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = unpack16(w[e], type);
-                    v[8 * j + 2 * e] = f.x, v[8 * j + 2 * e + 1] = f.y;
-                }
-            }
+// Four values of a type as they lie in memory (16-bit types: packed in the
+// first two words), at element i; `n` of them exist; `vec`: the address is
+// aligned for them all.
+__device__ __forceinline__ void load4_raw(const void *p, int type, long long i, int n, bool vec,
+                                          uint32_t (&w)[4]) {
+    if (type == kFp32) {
+        const uint32_t *q = static_cast<const uint32_t *>(p) + i;
+        if (vec && n >= 4) {
+            const uint4 t = *reinterpret_cast<const uint4 *>(q);
+            w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
         } else {
-            static_assert(W == 4, "vector width");
-            const uint2 t = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
-            const float2 f0 = unpack16(t.x, type), f1 = unpack16(t.y, type);
-            v[0] = f0.x, v[1] = f0.y, v[2] = f1.x, v[3] = f1.y;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = j < n ? q[j] : 0u;
         }
     } else {
+        const uint16_t *q = static_cast<const uint16_t *>(p) + i;
+        if (vec && n >= 4) {
+            const uint2 t = *reinterpret_cast<const uint2 *>(q);
+            w[0] = t.x, w[1] = t.y;
+        } else {
+            uint32_t e[4];
 #pragma unroll
-        for (int j = 0; j < W; ++j) v[j] = j < n ? load_elem(p, type, i + j) : 0.f;
+            for (int j = 0; j < 4; ++j) e[j] = j < n ? q[j] : 0u;
+            w[0] = e[0] | (e[1] << 16), w[1] = e[2] | (e[3] << 16);
+        }
     }
 }
-
-// `vec`: 0 element by element, 1 the address is 16-byte aligned (8 for
-// W = 4), 2 it is 32-byte aligned.
-template <int W>
-__device__ __forceinline__ void store_vec(void *p, int type, long long i, int n, int vec,
-                                          const float (&v)[W]) {
-    if (vec != 0 && n >= W) {
-        if (type == kFp32) {
-            float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
+__device__ __forceinline__ float4 values4(const uint32_t (&w)[4], int type) {
+    if (type == kFp32)
+        return make_float4(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]),
+                           __uint_as_float(w[3]));
+    const float2 a = unpack16(w[0], type), b = unpack16(w[1], type);
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store4(void *p, int type, long long i, int n, bool vec, const float (&v)[4]) {
+    if (!vec || n < 4) {
 #pragma unroll
-            for (int j = 0; j < W / 4; ++j)
-                q[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        } else if constexpr (W == 16) {
-            uint32_t w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = pack16(v[2 * e], v[2 * e + 1], type);
-            if (vec == 2) {
-                st_global_v8(static_cast<uint16_t *>(p) + i, w);
-            } else {
-                uint4 *q = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i);
-                q[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                q[1] = make_uint4(w[4], w[5], w[6], w[7]);
-            }
-        } else {
-            static_assert(W == 4, "vector width");
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i) =
-                make_uint2(pack16(v[0], v[1], type), pack16(v[2], v[3], type));
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < W; ++j)
+        for (int j = 0; j < 4; ++j)
             if (j < n) store_elem(p, type, i + j, v[j]);
+    } else if (type == kFp32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i) =
+            make_uint2(pack16(v[0], v[1], type), pack16(v[2], v[3], type));
     }
 }
 
-// GemmProblem::vec
-constexpr int kVecOut = 3, kVecRes = 4, kVecBias = 8;  // kVecOut: store_vec's `vec`
+// Epilogue::vec: rows that may be read and written four values at a time.
+constexpr int kVecOut = 1, kVecRes = 2, kVecBias = 4;
 
-// Offsets of column c's pair in a gated block's saved row: 16 gate values,
-// then the 16 up values of the same columns, so that one thread's 16-column
-// chunk is one 128-byte line.
-__host__ __device__ constexpr int saved_gate(int c) { return (c >> 4) * 32 + (c & 15); }
+// The epilogues work on four columns of a row a thread, neighbouring threads
+// on neighbouring columns, so that what they read and write of a row is whole
+// lines.  (A row a thread, as the sums leave TMEM, wrote 32 bytes of 32 lines
+// an instruction: 34 us for the 59 MB result of 4096x64x7168.)
 
-// What the epilogue of W columns of a row reads from memory besides bias,
-// as it lies there: loaded ahead of its use (before the tile's sums are
-// complete, and a chunk ahead of the one in work), because a load's latency
-// in each of a tile's chunks costs more than the tile's products.
-template <int EPI, int W>
+// What they read from memory besides the bias, as it lies there: loaded
+// ahead of its use, because a load's latency in each of a tile's steps costs
+// more than the tile's products.
+template <int EPI>
 struct EpiIn {
-    static constexpr int kWords = EPI == kEpiDGate ? 2 * W : EPI == kEpiLinear ? W : 1;
+    static constexpr int kWords = EPI == kEpiDGate ? 8 : EPI == kEpiLinear ? 4 : 1;
     uint32_t w[kWords];
 };
 
-template <int EPI, int W>
-__device__ __forceinline__ void epi_load(const GemmProblem &p, int r, int c, EpiIn<EPI, W> &in) {
+template <int EPI>
+__device__ __forceinline__ void epi_load(const Epilogue &p, int r, int c, EpiIn<EPI> &in) {
     if (r >= p.M || c >= p.N) return;
     if constexpr (EPI == kEpiLinear) {
-        if (p.residual == nullptr) return;
-        const long long i = (long long)r * p.ld_res + c;
-        const int n = p.N - c;
-        if ((p.vec & kVecRes) && n >= W) {
-            if (p.out_type == kFp32) {
-                const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const float *>(p.residual) + i);
-#pragma unroll
-                for (int j = 0; j < W / 4; ++j) {
-                    const uint4 t = q[j];
-                    in.w[4 * j] = t.x, in.w[4 * j + 1] = t.y, in.w[4 * j + 2] = t.z, in.w[4 * j + 3] = t.w;
-                }
-            } else if constexpr (W >= 8) {
-                const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.residual) + i);
-#pragma unroll
-                for (int j = 0; j < W / 8; ++j) {
-                    const uint4 t = q[j];
-                    in.w[4 * j] = t.x, in.w[4 * j + 1] = t.y, in.w[4 * j + 2] = t.z, in.w[4 * j + 3] = t.w;
-                }
-            } else {
-                const uint2 t = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.residual) + i);
-                in.w[0] = t.x, in.w[1] = t.y;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < W; ++j)
-                in.w[j] = j >= n ? 0u
-                          : p.out_type == kFp32 ? static_cast<const uint32_t *>(p.residual)[i + j]
-                                                : static_cast<const uint16_t *>(p.residual)[i + j];
-        }
+        if (p.residual != nullptr)
+            load4_raw(p.residual, p.out_type, (long long)r * p.ld_res + c, p.N - c,
+                      (p.vec & kVecRes) != 0, in.w);
     } else if constexpr (EPI == kEpiDGate) {
-        const float *s = p.saved + (long long)r * p.ld_saved + saved_gate(c);
-        if constexpr (W == 16) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t t[8];
-                ld_global_v8(s + 8 * k, t);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) in.w[8 * k + e] = t[e];
-            }
-        } else {
-            const uint4 g = *reinterpret_cast<const uint4 *>(s);
-            const uint4 u = *reinterpret_cast<const uint4 *>(s + 16);
-            in.w[0] = g.x, in.w[1] = g.y, in.w[2] = g.z, in.w[3] = g.w;
-            in.w[4] = u.x, in.w[5] = u.y, in.w[6] = u.z, in.w[7] = u.w;
-        }
+        const long long i = (long long)r * p.ld_saved + c;
+        const uint4 g = *reinterpret_cast<const uint4 *>(p.saved + i);
+        const uint4 u = *reinterpret_cast<const uint4 *>(p.saved2 + i);
+        in.w[0] = g.x, in.w[1] = g.y, in.w[2] = g.z, in.w[3] = g.w;
+        in.w[4] = u.x, in.w[5] = u.y, in.w[6] = u.z, in.w[7] = u.w;
     }
 }
 
-// FP32 values to the plan's own memory, rows padded to whole chunks.
-template <int W>
-__device__ __forceinline__ void store_saved(float *p, const float (&v)[W]) {
-    if constexpr (W == 16) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint32_t t[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] = __float_as_uint(v[8 * k + e]);
-            st_global_v8(p + 8 * k, t);
-        }
-    } else {
-        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    }
-}
-
-// The epilogue of W columns from column c of row r: v holds the FP32 sums
-// (gated: u the up sums), `in` what epi_load read for them.
-template <int EPI, int W>
-__device__ __forceinline__ void epilogue(const GemmProblem &p, int r, int c, float (&v)[W],
-                                         const float (&u)[W], const EpiIn<EPI, W> &in) {
+// The epilogue of four columns from column c (a multiple of 4) of row r: v
+// holds the FP32 sums (gated: u the up sums), `in` what epi_load read.
+template <int EPI>
+__device__ __forceinline__ void epilogue(const Epilogue &p, int r, int c, float (&v)[4],
+                                         const float (&u)[4], const EpiIn<EPI> &in) {
     const int n = p.N - c;  // columns that exist
     if (r >= p.M || n <= 0) return;
     const long long o = (long long)r * p.ld_out + c;
+    const bool vec = (p.vec & kVecOut) != 0;
+    // rows of what is kept are padded to whole groups: no guard
+    auto keep = [&](float *q, const float (&x)[4]) {
+        *reinterpret_cast<float4 *>(q + (long long)r * p.ld_saved + c) = make_float4(x[0], x[1], x[2], x[3]);
+    };
     if constexpr (EPI == kEpiLinear) {
         if (p.bias != nullptr) {
-            float b[W];
-            load_vec<W>(p.bias, p.bias_type, c, n, (p.vec & kVecBias) != 0, b);
-#pragma unroll
-            for (int j = 0; j < W; ++j) v[j] += b[j];
+            uint32_t w[4];
+            load4_raw(p.bias, p.bias_type, c, n, (p.vec & kVecBias) != 0, w);
+            const float4 b = values4(w, p.bias_type);
+            v[0] += b.x, v[1] += b.y, v[2] += b.z, v[3] += b.w;
         }
-        if (p.saved != nullptr) store_saved<W>(p.saved + (long long)r * p.ld_saved + c, v);
-        act_values<W>(p.act, v);
+        if (p.saved != nullptr) keep(p.saved, v);
+        act_values<4>(p.act, v);
+        if (p.residual != nullptr) {
+            const float4 b = values4(in.w, p.out_type);
+            v[0] += b.x, v[1] += b.y, v[2] += b.z, v[3] += b.w;
+        }
+        store4(p.out, p.out_type, o, n, vec, v);
+    } else if constexpr (EPI == kEpiGated) {
+        if (p.saved != nullptr) {
+            keep(p.saved, v);
+            keep(p.saved2, u);
+        }
+        act_values<4>(p.act, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] *= u[j];
+        store4(p.out, p.out_type, o, n, vec, v);
+    } else {
+        float a[4], d[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] = __uint_as_float(in.w[j]);
+        act_slopes<4>(p.act, a, a, d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            a[j] *= v[j];
+            d[j] *= v[j] * __uint_as_float(in.w[4 + j]);
+        }
+        store4(p.out, p.out_type, o, n, vec, d);
+        store4(p.out2, p.out_type, o, n, vec, a);
+    }
+}
+
+// The same for R steps at once: a thread's four columns c of the rows r,
+// r + step, .. (all of them exist, and everything may be accessed as
+// vectors).  Each question that is the same for the whole tile (which type,
+// is there a bias, ..) is asked once for 4 R values: asked for every four,
+// the questions and not the memory set the time (plain 4096x64x7168: 77 us).
+template <int EPI, int R>
+struct GroupIn {
+    static constexpr int kWords = EPI == kEpiDGate ? 8 : EPI == kEpiLinear ? 2 : 1;
+    uint32_t w[R][kWords];
+};
+
+template <int EPI, int R>
+__device__ __forceinline__ void group_load(const Epilogue &p, int r, int c, int step, GroupIn<EPI, R> &in) {
+    if constexpr (EPI == kEpiLinear) {
+        if (p.residual == nullptr || p.out_type == kFp32) return;
+        const uint16_t *q = static_cast<const uint16_t *>(p.residual) + (long long)r * p.ld_res + c;
+#pragma unroll
+        for (int j = 0; j < R; ++j, q += step * p.ld_res) {
+            const uint2 t = *reinterpret_cast<const uint2 *>(q);
+            in.w[j][0] = t.x, in.w[j][1] = t.y;
+        }
+    } else if constexpr (EPI == kEpiDGate) {
+        const float *g = p.saved + (long long)r * p.ld_saved + c, *u = p.saved2 + (long long)r * p.ld_saved + c;
+#pragma unroll
+        for (int j = 0; j < R; ++j, g += step * p.ld_saved, u += step * p.ld_saved) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(g), y = *reinterpret_cast<const uint4 *>(u);
+            in.w[j][0] = x.x, in.w[j][1] = x.y, in.w[j][2] = x.z, in.w[j][3] = x.w;
+            in.w[j][4] = y.x, in.w[j][5] = y.y, in.w[j][6] = y.z, in.w[j][7] = y.w;
+        }
+    }
+}
+
+template <int TY, int R>
+__device__ __forceinline__ void group_store(void *out, long long ld, int r, int c, int step,
+                                            const float (&v)[4 * R]) {
+    if constexpr (TY == kFp32) {
+        float *q = static_cast<float *>(out) + (long long)r * ld + c;
+#pragma unroll
+        for (int j = 0; j < R; ++j, q += step * ld)
+            *reinterpret_cast<float4 *>(q) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    } else {
+        uint16_t *q = static_cast<uint16_t *>(out) + (long long)r * ld + c;
+#pragma unroll
+        for (int j = 0; j < R; ++j, q += step * ld)
+            *reinterpret_cast<uint2 *>(q) =
+                make_uint2(pack16(v[4 * j], v[4 * j + 1], TY), pack16(v[4 * j + 2], v[4 * j + 3], TY));
+    }
+}
+template <int R>
+__device__ __forceinline__ void group_store(void *out, int type, long long ld, int r, int c, int step,
+                                            const float (&v)[4 * R]) {
+    if (type == kBf16)
+        group_store<kBf16, R>(out, ld, r, c, step, v);
+    else if (type == kFp16)
+        group_store<kFp16, R>(out, ld, r, c, step, v);
+    else
+        group_store<kFp32, R>(out, ld, r, c, step, v);
+}
+
+template <int EPI, int R>
+__device__ __forceinline__ void group_epilogue(const Epilogue &p, int r, int c, int step, float (&v)[4 * R],
+                                               float (&u)[EPI == kEpiGated ? 4 * R : 1],
+                                               const GroupIn<EPI, R> &in) {
+    if constexpr (EPI == kEpiLinear) {
+        if (p.bias != nullptr) {
+            uint32_t w[4];
+            load4_raw(p.bias, p.bias_type, c, 4, true, w);
+            const float4 b = values4(w, p.bias_type);
+#pragma unroll
+            for (int j = 0; j < R; ++j) v[4 * j] += b.x, v[4 * j + 1] += b.y, v[4 * j + 2] += b.z, v[4 * j + 3] += b.w;
+        }
+        if (p.saved != nullptr) group_store<kFp32, R>(p.saved, p.ld_saved, r, c, step, v);
+        act_values<4 * R>(p.act, v);
         if (p.residual != nullptr) {
             if (p.out_type == kFp32) {
+                const float *q = static_cast<const float *>(p.residual) + (long long)r * p.ld_res + c;
 #pragma unroll
-                for (int j = 0; j < W; ++j) v[j] += __uint_as_float(in.w[j]);
-            } else if ((p.vec & kVecRes) && n >= W) {
+                for (int j = 0; j < R; ++j, q += step * p.ld_res) {
+                    const float4 b = *reinterpret_cast<const float4 *>(q);
+                    v[4 * j] += b.x, v[4 * j + 1] += b.y, v[4 * j + 2] += b.z, v[4 * j + 3] += b.w;
+                }
+            } else if (p.out_type == kBf16) {
 #pragma unroll
-                for (int j = 0; j < W / 2; ++j) {
-                    const float2 f = unpack16(in.w[j], p.out_type);
-                    v[2 * j] += f.x, v[2 * j + 1] += f.y;
+                for (int e = 0; e < 2 * R; ++e) {
+                    const float2 f = unpack16(in.w[e / 2][e % 2], kBf16);
+                    v[2 * e] += f.x, v[2 * e + 1] += f.y;
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < W; ++j) v[j] += unpack16(in.w[j], p.out_type).x;
+                for (int e = 0; e < 2 * R; ++e) {
+                    const float2 f = unpack16(in.w[e / 2][e % 2], kFp16);
+                    v[2 * e] += f.x, v[2 * e + 1] += f.y;
+                }
             }
         }
-        store_vec<W>(p.out, p.out_type, o, n, p.vec & kVecOut, v);
+        group_store<R>(p.out, p.out_type, p.ld_out, r, c, step, v);
     } else if constexpr (EPI == kEpiGated) {
         if (p.saved != nullptr) {
-            float *s = p.saved + (long long)r * p.ld_saved + saved_gate(c);
-            store_saved<W>(s, v);
-            store_saved<W>(s + 16, u);
+            group_store<kFp32, R>(p.saved, p.ld_saved, r, c, step, v);
+            group_store<kFp32, R>(p.saved2, p.ld_saved, r, c, step, u);
         }
-        act_values<W>(p.act, v);
+        act_values<4 * R>(p.act, v);
 #pragma unroll
-        for (int j = 0; j < W; ++j) v[j] *= u[j];
-        store_vec<W>(p.out, p.out_type, o, n, p.vec & kVecOut, v);
+        for (int j = 0; j < 4 * R; ++j) v[j] *= u[j];
+        group_store<R>(p.out, p.out_type, p.ld_out, r, c, step, v);
     } else {
-        float a[W], d[W];
+        float a[4 * R], d[4 * R];
 #pragma unroll
-        for (int j = 0; j < W; ++j) a[j] = __uint_as_float(in.w[j]);
-        act_slopes<W>(p.act, a, a, d);
+        for (int j = 0; j < 4 * R; ++j) a[j] = __uint_as_float(in.w[j / 4][j % 4]);
+        act_slopes<4 * R>(p.act, a, a, d);
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
+        for (int j = 0; j < 4 * R; ++j) {
             a[j] *= v[j];
-            d[j] *= v[j] * __uint_as_float(in.w[W + j]);
+            d[j] *= v[j] * __uint_as_float(in.w[j / 4][4 + j % 4]);
         }
-        store_vec<W>(p.out, p.out_type, o, n, p.vec & kVecOut, d);
-        store_vec<W>(p.out2, p.out_type, o, n, p.vec & kVecOut, a);
+        group_store<R>(p.out, p.out_type, p.ld_out, r, c, step, d);
+        group_store<R>(p.out2, p.out_type, p.ld_out, r, c, step, a);
     }
 }
 

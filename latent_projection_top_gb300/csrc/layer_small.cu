@@ -222,16 +222,17 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     // ---------------- sums over the cluster, and the epilogue ----------------
     const int e = (int)threadIdx.x - 64;  // epilogue thread
-    const int rows = min(BN, p.M - row0);
+    const Epilogue ep = p.e;
+    const int rows = min(BN, ep.M - row0);
     constexpr int kGroups = kTileCols / 4;  // a thread's item: 4 columns of a row
     const int items = rows * kGroups;
     const int i0 = items * rank / C, i1 = items * (rank + 1) / C;
     auto row_of = [&](int x) { return row0 + x / kGroups; };
     auto col_of = [&](int x) { return col0 + x % kGroups * 4; };
-    EpiIn<EPI, 4> in;
+    EpiIn<EPI> in;
     if (warp >= 2) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (i0 + e < i1) epi_load<EPI, 4>(p, row_of(i0 + e), col_of(i0 + e), in);
+        if (i0 + e < i1) epi_load<EPI>(ep, row_of(i0 + e), col_of(i0 + e), in);
         ok = wait_phase(done_bar, 0u, args, &s_abort) && !s_abort;
         __syncwarp();
         ptx::tc_fence_after();
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int x = i0 + e; x < i1; x += kEpiThreads) {
             const uint32_t at = sbase + (uint32_t)((x / kGroups) * kSmallTile + x % kGroups * 4) * 4u;
             float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
-            if (x > i0 + e) epi_load<EPI, 4>(p, row_of(x), col_of(x), in);
+            if (x > i0 + e) epi_load<EPI>(ep, row_of(x), col_of(x), in);
 #pragma unroll 2
             for (int j = 0; j < C; ++j) {
                 const uint32_t q = ptx::map_to_rank(at, (uint32_t)j);
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     u[0] += h.x, u[1] += h.y, u[2] += h.z, u[3] += h.w;
                 }
             }
-            epilogue<EPI, 4>(p, row_of(x), col_of(x), v, u, in);
+            epilogue<EPI>(ep, row_of(x), col_of(x), v, u, in);
         }
     }
     if (warp == 1) {
