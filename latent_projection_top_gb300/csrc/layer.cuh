@@ -20,10 +20,13 @@ __host__ __device__ constexpr int layer_esize(int type) { return type == kFp32 ?
 
 // What the epilogue makes of a tile's FP32 sums.
 enum LayerEpi : int {
-    kEpiLinear = 0,  // out = act(v + bias) + residual, z = v + bias kept when `saved` is set
+    kEpiLinear = 0,  // out = v + bias + residual
     kEpiGated = 1,   // v = (gate, up): out = act(gate) * up, both kept when `saved` is set
-    kEpiDGate = 2    // v = dh: out = dh * up * act'(gate), out2 = dh * act(gate), from `saved`
+    kEpiDGate = 2,   // v = dh: out = dh * up * act'(gate), out2 = dh * act(gate), from `saved`
+    kEpiAct = 3,     // out = act(v + bias) + residual, z = v + bias kept when `saved` is set
+    kEpiCount = 4
 };
+__host__ __device__ constexpr bool epi_linear(int epi) { return epi == kEpiLinear || epi == kEpiAct; }
 
 // What becomes of a product's sums D[M, N].  A kernel copies this into
 // registers: read from the launch's arguments with an index that is known

@@ -326,13 +326,14 @@ route_status forward_product(const route_layer *p, const Operand &A, const Opera
     q.e.act = act;
     q.e.saved = saved, q.e.ld_saved = up16(N);
     q.e.vec = vec_bits(out, q.e.ld_out, nullptr, residual, q.e.ld_res, out_type, bias);
-    const Choice ch = choose_one(p, kFormNT, kEpiLinear, M, N, q.kblocks);
+    const int epi = act == kActNone ? kEpiLinear : kEpiAct;
+    const Choice ch = choose_one(p, kFormNT, epi, M, N, q.kblocks);
     route_status st;
     if ((st = pr.map(A, K, M, pr.a_rows(M, ch), "x", &q.a[0])) != ROUTE_OK ||
         (st = pr.map(W, N, K, 64, "W", &q.b[0][0])) != ROUTE_OK)
         return st;
     q.b[0][1] = q.b[0][0];
-    return run(p, pr, kFormNT, kEpiLinear, ch, chained, false, stream);
+    return run(p, pr, kFormNT, epi, ch, chained, false, stream);
 }
 
 // out[M, K] = sum over i of dz_i[M, N] W_i[K, N]^T, one or two terms.

@@ -47,9 +47,9 @@ constexpr int kHalf = 128;                        // each CTA's rows of D
 constexpr uint32_t kABytes = kHalf * 64 * 2;      // 128 rows x 64 k
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
-// Columns of D an epilogue warp turns around at once, limited by the registers
-// that its values and inputs take, and a warp's buffer for it.
-__host__ __device__ constexpr int group_cols(int epi) { return epi == kEpiLinear ? 64 : 32; }
+// Columns of D an epilogue warp turns around at once (gated: of gate and of
+// up), and a warp's buffer for them.
+__host__ __device__ constexpr int group_cols(int epi) { return epi == kEpiGated ? 32 : 64; }
 constexpr uint32_t kTurnBytes = 32 * 64 * 4;
 constexpr uint32_t kSmemLimit = 227 * 1024;
 
@@ -292,16 +292,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             const int t = job & 1;
             const int r0 = w.tm * kGemmBM + (int)rank * kHalf + 32 * lq;
             const int c0 = w.tn * kTileCols + cs * kWarpCols;
-            // A thread's share of a group: four columns of kSteps rows, kStep apart.
+            // A thread's share of a group is four columns of kSteps rows, kStep
+            // apart, worked on kBatch rows at a time: all of them without an
+            // activation, else 4, because code for 64 activations in a row does
+            // not stay in the instruction cache (gelu 2048x64x3584 28 us).
             constexpr int kLanesRow = kG / 4, kStep = 32 / kLanesRow, kSteps = 32 / kStep;
-            constexpr int kGroups = kWarpCols / kG;
-            const int tr = r0 + lane / kLanesRow, tc = c0 + lane % kLanesRow * 4;
-            const bool rows_full = args.splits == 1 && r0 + 32 <= p.M &&
-                                   (p.vec & (kVecOut | kVecRes | kVecBias)) == (kVecOut | kVecRes | kVecBias);
-            auto full = [&](int g) { return rows_full && c0 + (g + 1) * kG <= p.N; };
-            GroupIn<EPI, kSteps> in;
-            // inputs go out before the tile's sums are complete
-            if (full(0)) group_load<EPI, kSteps>(p, tr, tc, kStep, in);
+            constexpr int kBatch = EPI == kEpiLinear ? 8 : 4, kGroupBatches = kSteps / kBatch;
+            constexpr bool kAhead = EPI != kEpiGated;  // inputs a batch ahead
+            constexpr int kBatches = kWarpCols / kG * kGroupBatches;
+            static_assert(kSteps % kBatch == 0, "whole batches");
+            const bool whole = args.splits == 1;
+            auto row_of = [&](int b) { return b % kGroupBatches * (kBatch * kStep) + lane / kLanesRow; };
+            auto col_of = [&](int b) { return c0 + b / kGroupBatches * kG + lane % kLanesRow * 4; };
+            GroupIn<EPI, kBatch> in, next;
+            // the first inputs go out before the tile's sums are complete
+            if (whole) group_load<EPI, kBatch>(p, r0 + row_of(0), col_of(0), kStep, in);
             // one warp polls, the others sleep at the barrier
             const bool ok = warp != 2 || wait_phase(tfull_bar(t), ((uint32_t)job >> 1) & 1u, args, &s_abort);
             if (!ptx::named_bar_and(1, 32 * kEpiWarps, ok)) break;
@@ -312,7 +317,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             auto unit = [&](int row, int x) {
                 return mine + (uint32_t)(row * kG * 4 + ((x ^ (row & 7)) << 4));
             };
-            auto put = [&](uint32_t tmem) {  // this thread's row of kG columns
+            auto put = [&](uint32_t tmem, uint32_t half) {  // this thread's row of kG columns
 #pragma unroll
                 for (int h = 0; h < kG / 16; ++h) {
                     uint32_t v[16];
@@ -320,67 +325,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                     ptx::tmem_ld_wait();
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(unit(lane, 4 * h + x)),
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(unit(lane, 4 * h + x) + half),
                                      "r"(v[4 * x]), "r"(v[4 * x + 1]), "r"(v[4 * x + 2]), "r"(v[4 * x + 3])
                                      : "memory");
                 }
-                __syncwarp();
             };
-            auto get = [&](float (&v)[4 * kSteps]) {  // this thread's columns of kSteps rows
+            auto get = [&](int row, uint32_t half, float (&v)[4 * kBatch]) {
 #pragma unroll
-                for (int j = 0; j < kSteps; ++j)
+                for (int j = 0; j < kBatch; ++j)
                     asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
                                  : "=f"(v[4 * j]), "=f"(v[4 * j + 1]), "=f"(v[4 * j + 2]), "=f"(v[4 * j + 3])
-                                 : "r"(unit(j * kStep + lane / kLanesRow, lane % kLanesRow))
+                                 : "r"(unit(row + j * kStep, lane % kLanesRow) + half)
                                  : "memory");
-                __syncwarp();
             };
 #pragma unroll 1
-            for (int g = 0; g < kGroups; ++g) {
-                float v[4 * kSteps], u[EPI == kEpiGated ? 4 * kSteps : 1];
-                const uint32_t from = acc + (uint32_t)(g * kG);
-                if constexpr (EPI == kEpiGated) {
-                    put(from + kTileCols);
-                    get(u);
-                }
-                put(from);
-                if (g == kGroups - 1) {  // everything has left TMEM
+            for (int b = 0; b < kBatches; ++b) {
+                if (b % kGroupBatches == 0) {
+                    const uint32_t from = acc + (uint32_t)(b / kGroupBatches * kG);
+                    __syncwarp();  // the last group has been read
+                    put(from, 0u);
+                    if (EPI == kEpiGated) put(from + kTileCols, kTurnBytes / 2);
                     ptx::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) {
+                    if (b + kGroupBatches == kBatches && lane == 0) {  // everything has left TMEM
                         if (leader)
                             ptx::mbar_arrive(tempty_bar(t));
                         else
                             ptx::mbar_arrive_remote(ptx::map_to_rank(tempty_bar(t), 0u));
                     }
                 }
-                get(v);
-                const int c = tc + g * kG;
-                if (full(g)) {
-                    group_epilogue<EPI, kSteps>(p, tr, c, kStep, v, u, in);
-                    if (g + 1 < kGroups && full(g + 1)) group_load<EPI, kSteps>(p, tr, c + kG, kStep, in);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kSteps; ++j) {
-                        const int r = tr + j * kStep;
-                        float x[4], y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[e] = v[4 * j + e];
-                            if constexpr (EPI == kEpiGated) y[e] = u[4 * j + e];
-                        }
-                        if (args.splits == 1) {
-                            EpiIn<EPI> one;
-                            epi_load<EPI>(p, r, c, one);
-                            epilogue<EPI>(p, r, c, x, y, one);
-                        } else if (r < p.M && c < p.N) {  // partials: rows padded to whole groups
-                            float *part = p.part + ((long long)w.split * p.M + r) * p.ld_part + c;
-                            *reinterpret_cast<float4 *>(part) = make_float4(x[0], x[1], x[2], x[3]);
-                            if (EPI == kEpiGated)
-                                *reinterpret_cast<float4 *>(part + p.ld_part / 2) = make_float4(y[0], y[1], y[2], y[3]);
-                        }
-                    }
+                if (kAhead && whole && b + 1 < kBatches)
+                    group_load<EPI, kBatch>(p, r0 + row_of(b + 1), col_of(b + 1), kStep, next);
+                float v[4 * kBatch], u[EPI == kEpiGated ? 4 * kBatch : 1];
+                get(row_of(b), 0u, v);
+                if constexpr (EPI == kEpiGated) get(row_of(b), kTurnBytes / 2, u);
+                const int r = r0 + row_of(b), c = col_of(b);
+                if (whole) {
+                    group_epilogue<EPI, kBatch>(p, r, c, kStep, v, u, in);
+                } else if (c < p.N) {  // partials: rows padded to whole groups
+                    float *part = p.part + (long long)w.split * p.M * p.ld_part;
+                    group_keep<kBatch>(part, p.ld_part, r, p.M, c, kStep, v);
+                    if constexpr (EPI == kEpiGated)
+                        group_keep<kBatch>(part + p.ld_part / 2, p.ld_part, r, p.M, c, kStep, u);
                 }
+                if constexpr (kAhead) in = next;
             }
         }
     }
@@ -445,6 +433,7 @@ const void *kernel_of(int form, int epi, int bn) {
         return bn == 256 ? reinterpret_cast<const void *>(layer_gemm_kernel<F, E, 256>) \
                          : reinterpret_cast<const void *>(layer_gemm_kernel<F, E, 128>);
     ROUTE_GEMM(kFormNT, kEpiLinear)
+    ROUTE_GEMM(kFormNT, kEpiAct)
     ROUTE_GEMM(kFormNT, kEpiGated)
     ROUTE_GEMM(kFormNN, kEpiLinear)
     ROUTE_GEMM(kFormNN, kEpiDGate)
@@ -457,7 +446,7 @@ const void *kernel_of(int form, int epi, int bn) {
 
 cudaError_t gemm_configure() {
     for (int form = 0; form < 3; ++form)
-        for (int epi = 0; epi < 3; ++epi)
+        for (int epi = 0; epi < kEpiCount; ++epi)
             for (int bn : {256, 128})
                 if (const void *k = kernel_of(form, epi, bn)) {
                     const cudaError_t e = cudaFuncSetAttribute(
@@ -480,6 +469,7 @@ cudaError_t gemm_launch(int form, int epi, int bn, const GemmMaps &maps, const G
 cudaError_t gemm_finish_launch(int epi, const FinishArgs &args, cudaStream_t stream) {
     const void *k = epi == kEpiLinear  ? reinterpret_cast<const void *>(gemm_finish_kernel<kEpiLinear>)
                     : epi == kEpiGated ? reinterpret_cast<const void *>(gemm_finish_kernel<kEpiGated>)
+                    : epi == kEpiAct   ? reinterpret_cast<const void *>(gemm_finish_kernel<kEpiAct>)
                                        : reinterpret_cast<const void *>(gemm_finish_kernel<kEpiDGate>);
     const long long threads = (long long)((args.e.N + 3) / 4) * args.e.M;
     void *params[] = {const_cast<FinishArgs *>(&args)};

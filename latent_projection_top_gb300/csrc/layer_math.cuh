@@ -207,14 +207,14 @@ constexpr int kVecOut = 1, kVecRes = 2, kVecBias = 4;
 // more than the tile's products.
 template <int EPI>
 struct EpiIn {
-    static constexpr int kWords = EPI == kEpiDGate ? 8 : EPI == kEpiLinear ? 4 : 1;
+    static constexpr int kWords = EPI == kEpiDGate ? 8 : epi_linear(EPI) ? 4 : 1;
     uint32_t w[kWords];
 };
 
 template <int EPI>
 __device__ __forceinline__ void epi_load(const Epilogue &p, int r, int c, EpiIn<EPI> &in) {
     if (r >= p.M || c >= p.N) return;
-    if constexpr (EPI == kEpiLinear) {
+    if constexpr (epi_linear(EPI)) {
         if (p.residual != nullptr)
             load4_raw(p.residual, p.out_type, (long long)r * p.ld_res + c, p.N - c,
                       (p.vec & kVecRes) != 0, in.w);
@@ -240,15 +240,17 @@ __device__ __forceinline__ void epilogue(const Epilogue &p, int r, int c, float 
     auto keep = [&](float *q, const float (&x)[4]) {
         *reinterpret_cast<float4 *>(q + (long long)r * p.ld_saved + c) = make_float4(x[0], x[1], x[2], x[3]);
     };
-    if constexpr (EPI == kEpiLinear) {
+    if constexpr (epi_linear(EPI)) {
         if (p.bias != nullptr) {
             uint32_t w[4];
             load4_raw(p.bias, p.bias_type, c, n, (p.vec & kVecBias) != 0, w);
             const float4 b = values4(w, p.bias_type);
             v[0] += b.x, v[1] += b.y, v[2] += b.z, v[3] += b.w;
         }
-        if (p.saved != nullptr) keep(p.saved, v);
-        act_values<4>(p.act, v);
+        if constexpr (EPI == kEpiAct) {
+            if (p.saved != nullptr) keep(p.saved, v);
+            act_values<4>(p.act, v);
+        }
         if (p.residual != nullptr) {
             const float4 b = values4(in.w, p.out_type);
             v[0] += b.x, v[1] += b.y, v[2] += b.z, v[3] += b.w;
@@ -279,86 +281,137 @@ __device__ __forceinline__ void epilogue(const Epilogue &p, int r, int c, float 
 }
 
 // The same for R steps at once: a thread's four columns c of the rows r,
-// r + step, .. (all of them exist, and everything may be accessed as
-// vectors).  Each question that is the same for the whole tile (which type,
-// is there a bias, ..) is asked once for 4 R values: asked for every four,
-// the questions and not the memory set the time (plain 4096x64x7168: 77 us).
+// r + step, ..  Each question that is the same for the whole tile (which
+// type, is there a bias, ..) is asked once for 4 R values: asked for every
+// four, the questions and not the memory set the time (plain 4096x64x7168:
+// 77 us).  What is asked for a step is whether its row exists.
 template <int EPI, int R>
 struct GroupIn {
-    static constexpr int kWords = EPI == kEpiDGate ? 8 : EPI == kEpiLinear ? 2 : 1;
+    static constexpr int kWords = EPI == kEpiDGate ? 8 : epi_linear(EPI) ? 2 : 1;
     uint32_t w[R][kWords];
 };
 
 template <int EPI, int R>
 __device__ __forceinline__ void group_load(const Epilogue &p, int r, int c, int step, GroupIn<EPI, R> &in) {
-    if constexpr (EPI == kEpiLinear) {
+    if (c >= p.N) return;
+    if constexpr (epi_linear(EPI)) {
         if (p.residual == nullptr || p.out_type == kFp32) return;
         const uint16_t *q = static_cast<const uint16_t *>(p.residual) + (long long)r * p.ld_res + c;
+        const long long move = step * p.ld_res;
+        if ((p.vec & kVecRes) && c + 4 <= p.N) {
 #pragma unroll
-        for (int j = 0; j < R; ++j, q += step * p.ld_res) {
-            const uint2 t = *reinterpret_cast<const uint2 *>(q);
-            in.w[j][0] = t.x, in.w[j][1] = t.y;
+            for (int j = 0; j < R; ++j, q += move)
+                if (r + j * step < p.M) {
+                    const uint2 t = *reinterpret_cast<const uint2 *>(q);
+                    in.w[j][0] = t.x, in.w[j][1] = t.y;
+                }
+        } else {
+#pragma unroll
+            for (int j = 0; j < R; ++j, q += move)
+                if (r + j * step < p.M) {
+                    const uint32_t e1 = c + 1 < p.N ? q[1] : 0, e2 = c + 2 < p.N ? q[2] : 0,
+                                   e3 = c + 3 < p.N ? q[3] : 0;
+                    in.w[j][0] = q[0] | (e1 << 16), in.w[j][1] = e2 | (e3 << 16);
+                }
         }
     } else if constexpr (EPI == kEpiDGate) {
         const float *g = p.saved + (long long)r * p.ld_saved + c, *u = p.saved2 + (long long)r * p.ld_saved + c;
+        const long long move = step * p.ld_saved;
 #pragma unroll
-        for (int j = 0; j < R; ++j, g += step * p.ld_saved, u += step * p.ld_saved) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(g), y = *reinterpret_cast<const uint4 *>(u);
-            in.w[j][0] = x.x, in.w[j][1] = x.y, in.w[j][2] = x.z, in.w[j][3] = x.w;
-            in.w[j][4] = y.x, in.w[j][5] = y.y, in.w[j][6] = y.z, in.w[j][7] = y.w;
-        }
+        for (int j = 0; j < R; ++j, g += move, u += move)
+            if (r + j * step < p.M) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(g), y = *reinterpret_cast<const uint4 *>(u);
+                in.w[j][0] = x.x, in.w[j][1] = x.y, in.w[j][2] = x.z, in.w[j][3] = x.w;
+                in.w[j][4] = y.x, in.w[j][5] = y.y, in.w[j][6] = y.z, in.w[j][7] = y.w;
+            }
     }
 }
 
+// `vec`: rows take four values at a time; `n`: columns that exist.
 template <int TY, int R>
-__device__ __forceinline__ void group_store(void *out, long long ld, int r, int c, int step,
-                                            const float (&v)[4 * R]) {
+__device__ __forceinline__ void group_store(void *out, long long ld, int r, int M, int c, int n, int step,
+                                            bool vec, const float (&v)[4 * R]) {
+    const long long move = step * ld;
     if constexpr (TY == kFp32) {
         float *q = static_cast<float *>(out) + (long long)r * ld + c;
 #pragma unroll
-        for (int j = 0; j < R; ++j, q += step * ld)
-            *reinterpret_cast<float4 *>(q) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        for (int j = 0; j < R; ++j, q += move)
+            if (r + j * step < M) {
+                if (vec && n >= 4) {
+                    *reinterpret_cast<float4 *>(q) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (e < n) q[e] = v[4 * j + e];
+                }
+            }
     } else {
         uint16_t *q = static_cast<uint16_t *>(out) + (long long)r * ld + c;
+        if (vec && n >= 4) {
 #pragma unroll
-        for (int j = 0; j < R; ++j, q += step * ld)
-            *reinterpret_cast<uint2 *>(q) =
-                make_uint2(pack16(v[4 * j], v[4 * j + 1], TY), pack16(v[4 * j + 2], v[4 * j + 3], TY));
+            for (int j = 0; j < R; ++j, q += move)
+                if (r + j * step < M)
+                    *reinterpret_cast<uint2 *>(q) =
+                        make_uint2(pack16(v[4 * j], v[4 * j + 1], TY), pack16(v[4 * j + 2], v[4 * j + 3], TY));
+        } else {
+#pragma unroll
+            for (int j = 0; j < R; ++j, q += move)
+                if (r + j * step < M) {
+                    const uint32_t a = pack16(v[4 * j], v[4 * j + 1], TY), b = pack16(v[4 * j + 2], v[4 * j + 3], TY);
+                    if (n > 0) q[0] = (uint16_t)a;
+                    if (n > 1) q[1] = (uint16_t)(a >> 16);
+                    if (n > 2) q[2] = (uint16_t)b;
+                    if (n > 3) q[3] = (uint16_t)(b >> 16);
+                }
+        }
     }
 }
 template <int R>
-__device__ __forceinline__ void group_store(void *out, int type, long long ld, int r, int c, int step,
+__device__ __forceinline__ void group_store(void *out, const Epilogue &p, int r, int c, int step,
                                             const float (&v)[4 * R]) {
-    if (type == kBf16)
-        group_store<kBf16, R>(out, ld, r, c, step, v);
-    else if (type == kFp16)
-        group_store<kFp16, R>(out, ld, r, c, step, v);
+    const bool vec = (p.vec & kVecOut) != 0;
+    if (p.out_type == kBf16)
+        group_store<kBf16, R>(out, p.ld_out, r, p.M, c, p.N - c, step, vec, v);
+    else if (p.out_type == kFp16)
+        group_store<kFp16, R>(out, p.ld_out, r, p.M, c, p.N - c, step, vec, v);
     else
-        group_store<kFp32, R>(out, ld, r, c, step, v);
+        group_store<kFp32, R>(out, p.ld_out, r, p.M, c, p.N - c, step, vec, v);
+}
+// FP32 values to memory of the plan's own, whose rows are padded.
+template <int R>
+__device__ __forceinline__ void group_keep(float *out, long long ld, int r, int M, int c, int step,
+                                           const float (&v)[4 * R]) {
+    group_store<kFp32, R>(out, ld, r, M, c, 4, step, true, v);
 }
 
 template <int EPI, int R>
 __device__ __forceinline__ void group_epilogue(const Epilogue &p, int r, int c, int step, float (&v)[4 * R],
                                                float (&u)[EPI == kEpiGated ? 4 * R : 1],
                                                const GroupIn<EPI, R> &in) {
-    if constexpr (EPI == kEpiLinear) {
+    if (c >= p.N) return;
+    if constexpr (epi_linear(EPI)) {
         if (p.bias != nullptr) {
             uint32_t w[4];
-            load4_raw(p.bias, p.bias_type, c, 4, true, w);
+            load4_raw(p.bias, p.bias_type, c, p.N - c, (p.vec & kVecBias) != 0, w);
             const float4 b = values4(w, p.bias_type);
 #pragma unroll
             for (int j = 0; j < R; ++j) v[4 * j] += b.x, v[4 * j + 1] += b.y, v[4 * j + 2] += b.z, v[4 * j + 3] += b.w;
         }
-        if (p.saved != nullptr) group_store<kFp32, R>(p.saved, p.ld_saved, r, c, step, v);
-        act_values<4 * R>(p.act, v);
+        if constexpr (EPI == kEpiAct) {
+            if (p.saved != nullptr) group_keep<R>(p.saved, p.ld_saved, r, p.M, c, step, v);
+            act_values<4 * R>(p.act, v);
+        }
         if (p.residual != nullptr) {
             if (p.out_type == kFp32) {
-                const float *q = static_cast<const float *>(p.residual) + (long long)r * p.ld_res + c;
 #pragma unroll
-                for (int j = 0; j < R; ++j, q += step * p.ld_res) {
-                    const float4 b = *reinterpret_cast<const float4 *>(q);
-                    v[4 * j] += b.x, v[4 * j + 1] += b.y, v[4 * j + 2] += b.z, v[4 * j + 3] += b.w;
-                }
+                for (int j = 0; j < R; ++j)
+                    if (r + j * step < p.M) {
+                        uint32_t w[4];
+                        load4_raw(p.residual, kFp32, (long long)(r + j * step) * p.ld_res + c, p.N - c,
+                                  (p.vec & kVecRes) != 0, w);
+                        const float4 b = values4(w, kFp32);
+                        v[4 * j] += b.x, v[4 * j + 1] += b.y, v[4 * j + 2] += b.z, v[4 * j + 3] += b.w;
+                    }
             } else if (p.out_type == kBf16) {
 #pragma unroll
                 for (int e = 0; e < 2 * R; ++e) {
@@ -373,16 +426,16 @@ __device__ __forceinline__ void group_epilogue(const Epilogue &p, int r, int c, 
                 }
             }
         }
-        group_store<R>(p.out, p.out_type, p.ld_out, r, c, step, v);
+        group_store<R>(p.out, p, r, c, step, v);
     } else if constexpr (EPI == kEpiGated) {
         if (p.saved != nullptr) {
-            group_store<kFp32, R>(p.saved, p.ld_saved, r, c, step, v);
-            group_store<kFp32, R>(p.saved2, p.ld_saved, r, c, step, u);
+            group_keep<R>(p.saved, p.ld_saved, r, p.M, c, step, v);
+            group_keep<R>(p.saved2, p.ld_saved, r, p.M, c, step, u);
         }
         act_values<4 * R>(p.act, v);
 #pragma unroll
         for (int j = 0; j < 4 * R; ++j) v[j] *= u[j];
-        group_store<R>(p.out, p.out_type, p.ld_out, r, c, step, v);
+        group_store<R>(p.out, p, r, c, step, v);
     } else {
         float a[4 * R], d[4 * R];
 #pragma unroll
@@ -393,8 +446,8 @@ __device__ __forceinline__ void group_epilogue(const Epilogue &p, int r, int c, 
             a[j] *= v[j];
             d[j] *= v[j] * __uint_as_float(in.w[j / 4][4 + j % 4]);
         }
-        group_store<R>(p.out, p.out_type, p.ld_out, r, c, step, d);
-        group_store<R>(p.out2, p.out_type, p.ld_out, r, c, step, a);
+        group_store<R>(p.out, p, r, c, step, d);
+        group_store<R>(p.out2, p, r, c, step, a);
     }
 }
 

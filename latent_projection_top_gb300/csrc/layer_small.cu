@@ -291,6 +291,7 @@ const void *kernel_of(int form, int epi, int bn) {
                : bn == 64 ? reinterpret_cast<const void *>(layer_small_kernel<F, E, 64>)        \
                           : reinterpret_cast<const void *>(layer_small_kernel<F, E, 128>);
     ROUTE_SMALL(kFormNT, kEpiLinear)
+    ROUTE_SMALL(kFormNT, kEpiAct)
     ROUTE_SMALL(kFormNT, kEpiGated)
     ROUTE_SMALL(kFormNN, kEpiLinear)
     ROUTE_SMALL(kFormNN, kEpiDGate)
@@ -305,7 +306,7 @@ const void *kernel_of(int form, int epi, int bn) {
 
 cudaError_t small_configure() {
     for (int form = 0; form < 3; ++form)
-        for (int epi = 0; epi < 3; ++epi)
+        for (int epi = 0; epi < kEpiCount; ++epi)
             for (int bn : {16, 32, 64, 128})
                 if (const void *k = kernel_of(form, epi, bn)) {
                     const int smem = (int)smem_of(form == kFormTT && bn < 64 ? 64 : bn);
