@@ -211,9 +211,14 @@ Choice choose(const route_layer *p, int form, int epi, const Shape *shape, int c
 void set_tiles(GemmProblem &q, int tile_rows, int tile_cols, int pairs) {
     q.tiles_m = ceil_div(q.e.M, tile_rows);
     q.tiles_n = ceil_div(q.e.N, tile_cols);
-    // column tiles of a band: about as many as the row tiles at work at once
-    int band = (pairs + q.tiles_m - 1) / q.tiles_m;
-    band = band < 8 ? 8 : band;
+    // Column tiles of a band: with up to 16 tiles either way the whole of that
+    // way stays in L2 while the other streams past it (all 14 columns of
+    // 8192x3584x3584: 130.8 us, 8 of them 133.6; 2 columns with all 16 rows of
+    // 4096x3584x7168: 129.0, 8 columns 131.9), else about a square of tiles at
+    // work (8192x3584x7168: 8 columns 264.7, 28 270.8, 2 269.3).
+    int band = q.tiles_n <= 16 ? q.tiles_n : q.tiles_m <= 16 ? 2 : 8;
+    const int least = ceil_div(pairs, q.tiles_m);  // as many tiles as pairs in a band
+    band = q.tiles_m < 8 && band < least ? least : band;
     q.band = band < q.tiles_n ? band : q.tiles_n;
 }
 

@@ -188,7 +188,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     if (warp == 0) {
         if (lane == 0) {
             // ---------------- TMA producer (both CTAs) ----------------
-            const uint64_t pol = ptx::policy_evict_normal();
+            // operands stay in L2 before results: 2-3% less under the power cap
+            // (4096x3584x7168 128.0 against 131.7 us, 8192x3584x3584 128.1
+            // against 131.3) than the default; operands first out: 4-5% more
+            const uint64_t pol = ptx::policy_evict_last();
             asm volatile("griddepcontrol.wait;" ::: "memory");
             // after the wait: what follows may read this call's weights at once
             if (args.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
