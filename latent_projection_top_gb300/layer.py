@@ -90,6 +90,7 @@ class _LayerPlan:
         _route._check(getattr(_route.lib(), prepare)(int(rows), *args, int(device),
                                                      ctypes.byref(h)))
         self._h = h
+        self._p = h.value  # what the calls pass; None once closed
         self.rows = int(rows)
         self.dtype = dtype
         self.device = int(device)
@@ -118,7 +119,7 @@ class _LayerPlan:
     def close(self) -> None:
         if self._h is not None and self._h.value:
             _route.lib().route_layer_destroy(self._h)
-        self._h = None
+        self._h = self._p = None
 
     def __enter__(self):
         return self
@@ -182,7 +183,8 @@ def _refuse(t, name, shape, dtype, device):
 def _mat(t, name, rows, cols, dtype, device):
     """(pointer, row stride) of a matrix with unit stride between columns."""
     try:
-        if t.is_cuda and t.dtype == dtype and t.get_device() == device and t.shape == (rows, cols):
+        # get_device() is -1 off the GPU
+        if t.dtype is dtype and t.get_device() == device and t.shape == (rows, cols):
             ld, unit = t.stride()
             if unit == 1 or cols == 1:
                 return t.data_ptr(), ld
@@ -200,7 +202,7 @@ def _vec(t, name, n, dtype, device):
     if t is None:
         return None
     try:
-        if (t.is_cuda and t.dtype == dtype and t.get_device() == device and t.shape == (n,)
+        if (t.dtype is dtype and t.get_device() == device and t.shape == (n,)
                 and t.is_contiguous()):
             return t.data_ptr()
     except AttributeError:
@@ -241,9 +243,29 @@ def _rows(t, name):
 
 def _stream(stream, device):
     if stream is None:
-        import torch
-        stream = torch.cuda.current_stream(device)
+        return _current_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _current_stream(device):
+    """torch's current stream as a handle (the first call finds the cheapest
+    way to ask: building a Stream object costs as much as a kernel launch)."""
+    global _current_stream
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _current_stream = raw if raw is not None else (
+        lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _call(name, plan, *args):
+    """One C entry point; the message of a refusal is its exception's."""
+    handle = plan._p
+    if handle is None:
+        plan.handle  # raises: closed
+    status = getattr(_route._lib, name)(handle, *args)
+    if status:
+        _route._check(status)
 
 
 # ---- the C entry points -------------------------------------------------------
@@ -253,31 +275,28 @@ def norm_forward(plan: NormPlan, x, gamma, beta, out, stats=None, eps: float = 1
     """``out = (x - mean) rstd gamma + beta``; `stats` [rows, 2] FP32 receives
     (mean, rstd).  gamma and beta may be None."""
     R, d, dev, dt = _rows(x, "x"), plan.dim, plan.device, plan.dtype
-    _route._check(_route.lib().route_norm_forward(
-        plan.handle, R, *_mat(x, "x", R, d, dt, dev), _vec(gamma, "gamma", d, dt, dev),
+    _call("route_norm_forward", plan, R, *_mat(x, "x", R, d, dt, dev), _vec(gamma, "gamma", d, dt, dev),
         _vec(beta, "beta", d, dt, dev), eps, *_mat(out, "out", R, d, dt, dev),
-        _stats(stats, R, dev, False), _stream(stream, dev)))
+        _stats(stats, R, dev, False), _stream(stream, dev))
 
 
 def norm_backward(plan: NormPlan, dout, x, gamma, stats, dx=None, dgamma=None, dbeta=None,
                   stream=None) -> None:
     R, d, dev, dt = _rows(dout, "dout"), plan.dim, plan.device, plan.dtype
-    _route._check(_route.lib().route_norm_backward(
-        plan.handle, R, *_mat(dout, "dout", R, d, dt, dev), *_mat(x, "x", R, d, dt, dev),
+    _call("route_norm_backward", plan, R, *_mat(dout, "dout", R, d, dt, dev), *_mat(x, "x", R, d, dt, dev),
         _vec(gamma, "gamma", d, dt, dev), _stats(stats, R, dev, True),
         *_opt_mat(dx, "dx", R, d, dt, dev), _vec(dgamma, "dgamma", d, dt, dev),
-        _vec(dbeta, "dbeta", d, dt, dev), _stream(stream, dev)))
+        _vec(dbeta, "dbeta", d, dt, dev), _stream(stream, dev))
 
 
 def linear_forward(plan: LinearPlan, x, W, out, bias=None, residual=None, saved=None,
                    stream=None) -> None:
     R, k, n, dev, dt = _rows(x, "x"), plan.k, plan.n, plan.device, plan.dtype
-    _route._check(_route.lib().route_linear_forward(
-        plan.handle, R, *_mat(x, "x", R, k, dt, dev), *_mat(W, "W", k, n, dt, dev),
+    _call("route_linear_forward", plan, R, *_mat(x, "x", R, k, dt, dev), *_mat(W, "W", k, n, dt, dev),
         _vec(bias, "bias", n, dt, dev),
         *_opt_mat(residual, "residual", R, n, plan.out_dtype, dev),
         *_mat(out, "out", R, n, plan.out_dtype, dev), _saved(plan, saved, R),
-        _stream(stream, dev)))
+        _stream(stream, dev))
 
 
 def linear_backward(plan: LinearPlan, dout, x, W, saved=None, dx=None, dW=None, dbias=None,
@@ -285,30 +304,27 @@ def linear_backward(plan: LinearPlan, dout, x, W, saved=None, dx=None, dW=None, 
     """`saved`: what the forward call kept (plans with an activation).  x may
     be None without dW, W without dx."""
     R, k, n, dev, dt = _rows(dout, "dout"), plan.k, plan.n, plan.device, plan.dtype
-    _route._check(_route.lib().route_linear_backward(
-        plan.handle, R, *_mat(dout, "dout", R, n, dt, dev), *_opt_mat(x, "x", R, k, dt, dev),
+    _call("route_linear_backward", plan, R, *_mat(dout, "dout", R, n, dt, dev), *_opt_mat(x, "x", R, k, dt, dev),
         *_opt_mat(W, "W", k, n, dt, dev), _saved(plan, saved, R),
         *_opt_mat(dx, "dx", R, k, dt, dev), *_opt_mat(dW, "dW", k, n, dt, dev),
-        _vec(dbias, "dbias", n, dt, dev), _stream(stream, dev)))
+        _vec(dbias, "dbias", n, dt, dev), _stream(stream, dev))
 
 
 def gated_forward(plan: GatedPlan, x, W_gate, W_up, W_down, out, residual=None, saved=None,
                   stream=None) -> None:
     R, k, f, n, dev, dt = _rows(x, "x"), plan.k, plan.f, plan.n, plan.device, plan.dtype
-    _route._check(_route.lib().route_gated_forward(
-        plan.handle, R, *_mat(x, "x", R, k, dt, dev), *_mat(W_gate, "W_gate", k, f, dt, dev),
+    _call("route_gated_forward", plan, R, *_mat(x, "x", R, k, dt, dev), *_mat(W_gate, "W_gate", k, f, dt, dev),
         *_mat(W_up, "W_up", k, f, dt, dev), *_mat(W_down, "W_down", f, n, dt, dev),
         *_opt_mat(residual, "residual", R, n, dt, dev), *_mat(out, "out", R, n, dt, dev),
-        _saved(plan, saved, R), _stream(stream, dev)))
+        _saved(plan, saved, R), _stream(stream, dev))
 
 
 def gated_backward(plan: GatedPlan, dout, x, W_gate, W_up, W_down, saved, dx=None, dW_gate=None,
                    dW_up=None, dW_down=None, stream=None) -> None:
     R, k, f, n, dev, dt = _rows(dout, "dout"), plan.k, plan.f, plan.n, plan.device, plan.dtype
-    _route._check(_route.lib().route_gated_backward(
-        plan.handle, R, *_mat(dout, "dout", R, n, dt, dev), *_mat(x, "x", R, k, dt, dev),
+    _call("route_gated_backward", plan, R, *_mat(dout, "dout", R, n, dt, dev), *_mat(x, "x", R, k, dt, dev),
         *_mat(W_gate, "W_gate", k, f, dt, dev), *_mat(W_up, "W_up", k, f, dt, dev),
         *_mat(W_down, "W_down", f, n, dt, dev), _saved(plan, saved, R),
         *_opt_mat(dx, "dx", R, k, dt, dev), *_opt_mat(dW_gate, "dW_gate", k, f, dt, dev),
         *_opt_mat(dW_up, "dW_up", k, f, dt, dev), *_opt_mat(dW_down, "dW_down", f, n, dt, dev),
-        _stream(stream, dev)))
+        _stream(stream, dev))
