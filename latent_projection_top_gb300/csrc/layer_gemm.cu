@@ -18,15 +18,15 @@
 // columns of D in its TMEM.  Two accumulators alternate, so that one tile is
 // drained while the next is computed.
 //
-// Rows of D are the TMEM lanes.  An epilogue warp takes 64 (or 32) columns of its 32
-// rows out of TMEM into shared memory and back with neighbouring threads on
+// Rows of D are the TMEM lanes.  An epilogue warp takes 32 columns of its 32 rows
+// out of TMEM into shared memory and back with neighbouring threads on
 // neighbouring columns, four to a thread, for the operator's epilogue.
 //
 // Split K: with few tiles, `splits` CTA pairs share a tile's contraction and
 // store FP32 partials; gemm_finish_kernel adds them in split order and runs
 // the same epilogue.  Results never depend on the order of arrival.
 //
-// Warp roles (320 threads, persistent, one CTA per SM, pairs = clusters):
+// Warp roles (576 or 320 threads, persistent, one CTA per SM, pairs = clusters):
 //   warp 0      TMA producer (both CTAs); completion counts on the leader's
 //               barrier, which the leader arms for both CTAs' bytes
 //   warp 1      TMEM owner (both CTAs); the leader's lane 0 issues the MMAs
@@ -45,18 +45,20 @@ namespace {
 
 constexpr int kHalf = 128;                        // each CTA's rows of D
 constexpr uint32_t kABytes = kHalf * 64 * 2;      // 128 rows x 64 k
-constexpr int kEpiWarps = 8;
-constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
-// Columns of D an epilogue warp turns around at once (gated: of gate and of
-// up), and a warp's buffer for them.
-__host__ __device__ constexpr int group_cols(int epi) { return epi == kEpiGated ? 32 : 64; }
-constexpr uint32_t kTurnBytes = 32 * 64 * 4;
+// Epilogue warps, the columns of D that one turns around at once, and its
+// buffer for them (a gated block: of gate and of up, with half the warps).
+__host__ __device__ constexpr int epi_warps(int epi) { return epi == kEpiGated ? 8 : 16; }
+__host__ __device__ constexpr int gemm_threads(int epi) { return 64 + 32 * epi_warps(epi); }
+constexpr int kG = 32;
+constexpr uint32_t kHalfTurn = 32 * kG * 4;
+__host__ __device__ constexpr uint32_t turn_bytes(int epi) { return epi == kEpiGated ? 2 * kHalfTurn : kHalfTurn; }
+constexpr uint32_t kTurns = 16 * kHalfTurn;  // all warps' buffers
 constexpr uint32_t kSmemLimit = 227 * 1024;
 
 __host__ __device__ constexpr uint32_t b_bytes(int bn) { return (uint32_t)bn / 2 * 64 * 2; }
 __host__ __device__ constexpr uint32_t stage_bytes(int bn) { return kABytes + b_bytes(bn); }
 __host__ __device__ constexpr int stages_of(int bn) { return bn == 256 ? 5 : 6; }
-__host__ __device__ constexpr uint32_t smem_of(int bn) { return 1024 + stages_of(bn) * stage_bytes(bn) + kEpiWarps * kTurnBytes + 256; }
+__host__ __device__ constexpr uint32_t smem_of(int bn) { return 1024 + stages_of(bn) * stage_bytes(bn) + kTurns + 256; }
 static_assert(smem_of(256) <= kSmemLimit && smem_of(128) <= kSmemLimit, "shared memory");
 
 // How long a poll of a barrier may be held in hardware.
@@ -133,15 +135,15 @@ __device__ __forceinline__ Item item_of(const GemmArgs &a, int i) {
 }
 
 template <int FORM, int EPI, int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1)
     layer_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs args) {
     constexpr bool A_MN = FORM == kFormTT, B_MN = FORM != kFormNN;
     constexpr int S = stages_of(BN);
     constexpr uint32_t kStage = stage_bytes(BN);
     constexpr int kTileCols = EPI == kEpiGated ? BN / 2 : BN;  // columns of D a tile
     constexpr int kBCols = BN / 2;                             // B columns each CTA loads
-    constexpr int kWarpCols = kTileCols / 2;                   // columns of D an epilogue warp drains
-    constexpr int kG = group_cols(EPI);
+    constexpr int kEpiWarps = epi_warps(EPI);
+    constexpr int kWarpCols = kTileCols / (kEpiWarps / 4);     // columns of D an epilogue warp drains
     static_assert(kWarpCols % kG == 0 && kG % 16 == 0, "whole groups");
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t s_tmem_base;
@@ -150,7 +152,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
     const uint32_t turn = sbase + S * kStage;
-    const uint32_t bars = turn + kEpiWarps * kTurnBytes;
+    const uint32_t bars = turn + kTurns;
     auto full_bar = [&](int s) { return bars + 8u * s; };             // leader's are used
     auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
     auto tfull_bar = [&](int t) { return bars + 8u * (2 * S + t); };
@@ -286,7 +288,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const int lq = warp & 3;         // TMEM lanes 32 lq .. + 31 = rows of D
         const int cs = (warp - 2) >> 2;  // which share of the tile's columns
         const uint32_t lanes = tmem_base + ((uint32_t)(32 * lq) << 16);
-        const uint32_t mine = turn + (uint32_t)(warp - 2) * kTurnBytes;
+        const uint32_t mine = turn + (uint32_t)(warp - 2) * turn_bytes(EPI);
         asm volatile("griddepcontrol.wait;" ::: "memory");
         int job = 0;
         for (int i = pair; i < args.items; i += args.pairs, ++job) {
@@ -300,7 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             // activation, else 4, because code for 64 activations in a row does
             // not stay in the instruction cache (gelu 2048x64x3584 28 us).
             constexpr int kLanesRow = kG / 4, kStep = 32 / kLanesRow, kSteps = 32 / kStep;
-            constexpr int kBatch = EPI == kEpiLinear ? 8 : 4, kGroupBatches = kSteps / kBatch;
+            constexpr int kBatch = EPI == kEpiDGate ? 2 : 4, kGroupBatches = kSteps / kBatch;
             constexpr bool kAhead = EPI != kEpiGated;  // inputs a batch ahead
             constexpr int kBatches = kWarpCols / kG * kGroupBatches;
             static_assert(kSteps % kBatch == 0, "whole batches");
@@ -347,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                     const uint32_t from = acc + (uint32_t)(b / kGroupBatches * kG);
                     __syncwarp();  // the last group has been read
                     put(from, 0u);
-                    if (EPI == kEpiGated) put(from + kTileCols, kTurnBytes / 2);
+                    if (EPI == kEpiGated) put(from + kTileCols, kHalfTurn);
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (b + kGroupBatches == kBatches && lane == 0) {  // everything has left TMEM
@@ -361,7 +363,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                     group_load<EPI, kBatch>(p, r0 + row_of(b + 1), col_of(b + 1), kStep, next);
                 float v[4 * kBatch], u[EPI == kEpiGated ? 4 * kBatch : 1];
                 get(row_of(b), 0u, v);
-                if constexpr (EPI == kEpiGated) get(row_of(b), kTurnBytes / 2, u);
+                if constexpr (EPI == kEpiGated) get(row_of(b), kHalfTurn, u);
                 const int r = r0 + row_of(b), c = col_of(b);
                 if (whole) {
                     group_epilogue<EPI, kBatch>(p, r, c, kStep, v, u, in);
@@ -466,7 +468,7 @@ cudaError_t gemm_launch(int form, int epi, int bn, const GemmMaps &maps, const G
     const void *k = kernel_of(form, epi, bn);
     if (k == nullptr || args.pairs <= 0 || args.items <= 0) return cudaErrorInvalidConfiguration;
     void *params[] = {const_cast<GemmMaps *>(&maps), const_cast<GemmArgs *>(&args)};
-    return launch_chained(k, dim3(2 * args.pairs), dim3(kGemmThreads), smem_of(bn), params, stream);
+    return launch_chained(k, dim3(2 * args.pairs), dim3(gemm_threads(epi)), smem_of(bn), params, stream);
 }
 
 cudaError_t gemm_finish_launch(int epi, const FinishArgs &args, cudaStream_t stream) {
