@@ -47,36 +47,48 @@ struct Epilogue {
     long long ld_res, ld_out, ld_saved, ld_part;
 };
 
+enum GemmForm : int {
+    kFormNT = 0,  // A rows K-contiguous, B [K, N] N-contiguous (forward)
+    kFormNN = 1,  // A rows K-contiguous, B [N, K] K-contiguous (input gradients)
+    kFormTT = 2,  // A [K, M] M-contiguous, B [K, N] N-contiguous (weight gradients)
+    kFormMixed = 3  // (a kernel's) NN and TT, as each problem says
+};
+
 // One matrix product D[M, N] = A B with a contraction of `kblocks` blocks of
 // 64 (blocks from `kswitch` on come from the second pair of operands).  Map
 // indexes name entries of GemmMaps.
 struct GemmProblem {
     Epilogue e;
+    int form;
     int tiles_m, tiles_n, band; // row tiles, column tiles, column tiles of a band
     int item_base;              // first work item of this problem
     int kblocks, kswitch;
+    unsigned a_bytes;           // bytes of an A box: fewer rows than a tile's when M is less
     uint8_t a[2], b[2][2];      // A map of each segment, B map of each segment and CTA of the pair
 };
 
-constexpr int kGemmMaxProblems = 3;
-constexpr int kGemmMaxMaps = 6;
+constexpr int kGemmMaxProblems = 4;
+constexpr int kGemmMaxMaps = 12;
+constexpr int kGemmMaxPairs = 80;  // pairs that `count` can describe
 
 struct GemmMaps {
     CUtensorMap m[kGemmMaxMaps];
 };
 
 struct GemmArgs {
-    int nprob;
+    int nprob;                  // problems, the longest contraction first
     int items;                  // work items: tiles x splits over all problems
     int splits;                 // K splits of every tile
     int pairs;                  // CTA pairs launched
-    unsigned a_bytes;           // bytes of an A box: fewer than 128 rows when M is
+    int listed;                 // pair j takes items first[c][j] .. of problem c, count[c][j] of them
+                                // (else items j, j + pairs, .. of all)
     int fp16;                   // operands are FP16 (else BF16)
     int trigger;                // a kernel of the same call follows: let it launch early
     int test_stall;
     unsigned long long timeout_ns;
     unsigned *status;
     GemmProblem p[kGemmMaxProblems];
+    uint16_t first[kGemmMaxProblems][kGemmMaxPairs], count[kGemmMaxProblems][kGemmMaxPairs];
 };
 
 // Partials of a split product summed in split order, then the epilogue.
@@ -84,12 +96,6 @@ struct FinishArgs {
     int splits;
     int trigger;
     Epilogue e;
-};
-
-enum GemmForm : int {
-    kFormNT = 0,  // A rows K-contiguous, B [K, N] N-contiguous (forward)
-    kFormNN = 1,  // A rows K-contiguous, B [N, K] K-contiguous (input gradients)
-    kFormTT = 2   // A [K, M] M-contiguous, B [K, N] N-contiguous (weight gradients)
 };
 
 constexpr int kGemmBM = 256;
@@ -105,18 +111,27 @@ cudaError_t gemm_finish_launch(int epi, const FinishArgs &args, cudaStream_t str
 // Takes the same arguments as gemm_launch; `rows`: MMA rows a tile (16, 32,
 // 64 or 128).  With `chained` the call's kernel before this one waited for
 // its own predecessors before it let this one launch, and does not write the
-// columns' operand, which is then read at once.
+// columns' operand of the NT and NN products, which is then read at once.
 constexpr int kSmallTile = 128;
 constexpr int kSmallMaxSplits = 8;
 cudaError_t small_configure();
 int small_smem_bytes();
-cudaError_t small_launch(int form, int epi, int rows, const GemmMaps &maps, const GemmArgs &args,
+cudaError_t small_launch(int epi, int rows, const GemmMaps &maps, const GemmArgs &args,
                          bool chained, cudaStream_t stream);
 
 // dst[r, 0..cols) = src[r, 0..cols) of 16-bit values, for operands whose rows
-// TMA cannot read where they are.
-cudaError_t repack_launch(const void *src, long long ld_src, void *dst, long long ld_dst, int rows,
-                          int cols, cudaStream_t stream);
+// TMA cannot read where they are; all of a call's in one launch.
+constexpr int kMaxRepacks = 5;
+struct RepackArgs {
+    int count;
+    struct {
+        const void *src;
+        void *dst;
+        long long ld_src, ld_dst;
+        int rows, cols;
+    } c[kMaxRepacks];
+};
+cudaError_t repack_launch(const RepackArgs &args, cudaStream_t stream);
 
 // dz = dout * act'(z) (z: FP32, row stride ld_z; null: dz = dout), written
 // with row stride ld_dz unless dz is null, and FP32 column sums of the

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <cstddef>
 #include <cstring>
 #include <initializer_list>
 #include <new>
@@ -134,24 +135,27 @@ struct Operand {
     long long ld;
 };
 
-// An operand as TMA can read it: in place, or copied into scratch.
-route_status operand(const route_layer *p, const void *src, long long ld, int rows, int cols,
-                     size_t scratch, cudaStream_t stream, Operand *out) {
-    if (cols % 8 == 0) {
-        *out = {src, rows > 1 ? ld : cols};
-        return ROUTE_OK;
+// Operands as TMA can read them: in place, or copied into scratch by one
+// launch for all of a call's.
+struct Copies {
+    const route_layer *p;
+    RepackArgs args;
+    explicit Copies(const route_layer *plan) : p(plan) { args.count = 0; }
+    Operand operand(const void *src, long long ld, int rows, int cols, size_t scratch) {
+        if (cols % 8 == 0) return {src, rows > 1 ? ld : cols};
+        if (aligned(src, 16) && ld % 8 == 0 && rows > 1) return {src, ld};
+        auto &c = args.c[args.count++];
+        c.src = src, c.ld_src = rows > 1 ? ld : cols;
+        c.dst = p->scratch + scratch, c.ld_dst = up8(cols);
+        c.rows = rows, c.cols = cols;
+        return {c.dst, c.ld_dst};
     }
-    const long long ldp = up8(cols);
-    if (aligned(src, 16) && ld % 8 == 0 && rows > 1) {
-        *out = {src, ld};
-        return ROUTE_OK;
+    route_status launch(cudaStream_t stream) {
+        if (args.count == 0) return ROUTE_OK;
+        const cudaError_t e = repack_launch(args, stream);
+        return e == cudaSuccess ? ROUTE_OK : cuda_fail(e, "operand copy");
     }
-    void *dst = p->scratch + scratch;
-    const cudaError_t e = repack_launch(src, rows > 1 ? ld : cols, dst, ldp, rows, cols, stream);
-    if (e != cudaSuccess) return cuda_fail(e, "operand copy");
-    *out = {dst, ldp};
-    return ROUTE_OK;
-}
+};
 
 // How a launch covers its products: CTA-pair tiles of 256 x bn
 // (layer_gemm.cu), or 128-column tiles of bn rows (layer_small.cu), and the
@@ -161,8 +165,13 @@ struct Choice {
     int bn, splits;
 };
 
-struct Shape {
-    int M, N;  // N: columns of D (gated: hidden columns)
+// A product of a launch: its form, the rows and columns of its result (gated:
+// hidden columns), its contraction's terms and each one's length.
+struct Prod {
+    int form, M, N, terms, K;
+    Operand a[2], b[2];  // of each term (gated: b of gate and of up)
+    Epilogue e;
+    int kblocks() const { return terms * ((K + 63) / 64); }
 };
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
@@ -170,40 +179,61 @@ int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 // The choice with the smallest estimated time, from what the kernels measure:
 // a k-block of a pair's 256 x 256 tile takes 0.34 us and of a 256 x 128 tile
 // 0.30 us; the small tiles are bound by what an SM reads, about 70 bytes a
-// nanosecond, or by memory.
-Choice choose(const route_layer *p, int form, int epi, const Shape *shape, int count, int kblocks) {
+// nanosecond.
+Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
     Choice best = {false, 256, 1};
     double t_best = 1e30, elems = 0;
-    int rows = 0;
+    int rows = 0, kmost = 0, kleast = 1 << 30;
+    bool tt = false;
     for (int i = 0; i < count; ++i) {
-        elems += (double)shape[i].M * shape[i].N * (epi == kEpiGated ? 2 : 1);
-        rows = rows < shape[i].M ? shape[i].M : rows;
+        elems += (double)w[i].M * w[i].N * (epi == kEpiGated ? 2 : 1);
+        rows = rows < w[i].M ? w[i].M : rows;
+        kmost = kmost < w[i].kblocks() ? w[i].kblocks() : kmost;
+        kleast = kleast > w[i].kblocks() ? w[i].kblocks() : kleast;
+        tt = tt || w[i].form == kFormTT;
     }
     for (int bn : {256, 128}) {
         long long tiles = 0;
+        double work = 0;
         const int cols = epi == kEpiGated ? bn / 2 : bn;
-        for (int i = 0; i < count; ++i)
-            tiles += (long long)ceil_div(shape[i].M, kGemmBM) * ceil_div(shape[i].N, cols);
+        for (int i = 0; i < count; ++i) {
+            const long long n = (long long)ceil_div(w[i].M, kGemmBM) * ceil_div(w[i].N, cols);
+            tiles += n, work += (double)n * w[i].kblocks();
+        }
         const int most = tiles >= p->pairs ? 1 : (int)(p->pairs / tiles);
-        for (int s = 1; s <= most && (s == 1 || kblocks / s >= 2); ++s) {
-            const int waves = ceil_div(tiles * s, p->pairs);
-            double t = 7.0 + waves * (ceil_div(kblocks, s) * (bn == 256 ? 0.34 : 0.30));
-            if (s > 1) t += 2.5 + elems * 4.0 * (s + 1) / 4e6;
+        const double kb_us = bn == 256 ? 0.34 : 0.30;
+        for (int s = 1; s <= most && (s == 1 || kleast / s >= 2); ++s) {
+            const double longest = ceil_div(kmost, s) * kb_us;
+            double t = ceil_div(tiles * s, p->pairs) * longest;  // equal items
+            if (count > 1) {
+                const double level = work * kb_us / p->pairs + 0.35 * longest;
+                t = level > longest ? level : longest;
+            }
+            t += 7.0;
+            if (s > 1) t += 2.5 * count + elems * 4.0 * (s + 1) / 4e6;
             if (t < t_best) t_best = t, best = {false, bn, s};
         }
     }
     {
-        int bn = form == kFormTT ? 64 : 16;
+        int bn = tt ? 64 : 16;
         while (bn < 128 && bn < rows) bn *= 2;
-        long long tiles = 0;
         const int cols = epi == kEpiGated ? kSmallTile / 2 : kSmallTile;
-        for (int i = 0; i < count; ++i)
-            tiles += (long long)ceil_div(shape[i].M, bn) * ceil_div(shape[i].N, cols);
+        long long tiles = 0;
+        for (int i = 0; i < count; ++i) tiles += (long long)ceil_div(w[i].M, bn) * ceil_div(w[i].N, cols);
         int s = 1;
-        while (s < kSmallMaxSplits && tiles * s * 2 <= 2 * p->sms && s * 2 <= kblocks) s *= 2;
+        while (s < kSmallMaxSplits && tiles * s * 2 <= 2 * p->sms && s * 2 <= kmost) s *= 2;
         const double kb_us = (16384 + bn * 128) / 70e3;
-        const double t = 5.0 + ceil_div(tiles * s, p->sms) * (ceil_div(kblocks, s) * kb_us + 0.5);
-        if (t < t_best) best = {true, bn, s};
+        const double longest = ceil_div(kmost, s) * kb_us + 0.5;
+        double t = ceil_div(tiles * s, p->sms) * longest;
+        if (count > 1) {
+            double level = 0;
+            for (int i = 0; i < count; ++i)
+                level += (double)ceil_div(w[i].M, bn) * ceil_div(w[i].N, cols) * s *
+                         (ceil_div(w[i].kblocks(), s) * kb_us + 0.5);
+            level = level / p->sms + 0.35 * longest;
+            t = level > longest ? level : longest;
+        }
+        if (t + 5.0 < t_best) best = {true, bn, s};
     }
     return best;
 }
@@ -222,77 +252,139 @@ void set_tiles(GemmProblem &q, int tile_rows, int tile_cols, int pairs) {
     q.band = band < q.tiles_n ? band : q.tiles_n;
 }
 
-struct Product {
-    GemmMaps maps;
-    GemmArgs args;
-    int nmaps = 0;
-    bool fp16;
-    Product(const route_layer *p) : fp16(p->type == kFp16) {
-        memset(&args, 0, sizeof args);
-        args.fp16 = fp16;
-        args.a_bytes = 128 * 64 * 2;
-        args.timeout_ns = p->timeout_ns;
-        args.status = p->words;
-        args.test_stall = p->test_stall;
+// Who takes which items when there are few of them and their products'
+// contractions differ: the longest first, each to the pair with the least so
+// far.  (Items in turn leave some pairs with two long ones: dx and dW of
+// 2050x896x3584 then take 89 k-blocks where this takes 66.)
+void deal_items(GemmArgs &a, int pairs) {
+    // a heap of the pairs, the least loaded (then the lowest) on top
+    int heap[kGemmMaxPairs];
+    for (int j = 0; j < pairs; ++j) heap[j] = j;
+    auto add_to_top = [&](int cost) {
+        const int key = heap[0] + cost * kGemmMaxPairs;
+        int i = 0;
+        for (;;) {
+            int c = 2 * i + 1;
+            if (c >= pairs) break;
+            if (c + 1 < pairs && heap[c + 1] < heap[c]) ++c;
+            if (heap[c] >= key) break;
+            heap[i] = heap[c];
+            i = c;
+        }
+        heap[i] = key;
+    };
+    a.listed = 1;
+    for (int c = 0; c < a.nprob; ++c) {
+        const int items = (c + 1 < a.nprob ? a.p[c + 1].item_base : a.items) - a.p[c].item_base;
+        const int cost = ceil_div(a.p[c].kblocks, a.splits);
+        for (int j = 0; j < pairs; ++j) a.count[c][j] = 0;
+        for (int i = 0; i < items; ++i) {
+            ++a.count[c][heap[0] % kGemmMaxPairs];
+            add_to_top(cost);
+        }
+        int at = 0;
+        for (int j = 0; j < pairs; ++j) a.first[c][j] = (uint16_t)at, at += a.count[c][j];
     }
-    // Rows of the boxes of a K-contiguous A (a tile's rows for one CTA, or
-    // what there is of M: a box higher than its tensor loads slowly, 98
-    // against 25 us at 8x3584x7168) and of a K-contiguous B.
-    uint32_t a_rows(int M, const Choice &ch) {
-        const uint32_t most = ch.small ? (uint32_t)ch.bn : 128u;
-        const uint32_t r = (uint32_t)M >= most ? most : (uint32_t)up8(M);
-        args.a_bytes = r * 64 * 2;
-        return r;
-    }
-    static uint32_t b_rows(const Choice &ch) {
-        return ch.small ? (uint32_t)kSmallTile : (uint32_t)ch.bn / 2;
-    }
-    // A map of `o` [outer, inner] in boxes of box_inner x box_outer.
-    route_status map(const Operand &o, long long inner, long long outer, uint32_t box_outer,
-                     const char *what, uint8_t *index) {
-        *index = (uint8_t)nmaps;
-        return api_encode_operand(&maps.m[nmaps++], o.p, fp16, (uint64_t)inner, (uint64_t)outer,
-                                  (uint64_t)(outer > 1 ? o.ld : up8(inner)), 64, box_outer, what);
-    }
-};
+}
 
-// Launch the product(s) and, when pair tiles are split, the kernel(s) that
-// finish them.  `more`: another kernel of the call follows; `chained`: the
-// one before is a product that does not write this one's B.
-route_status run(const route_layer *p, Product &pr, int form, int epi, const Choice &ch,
+// Launch `count` products with one epilogue and, when pair tiles are split,
+// the kernels that finish them.  `all`, `count_all`: the products that the
+// choice of tiles goes by.  `more`: another kernel of the call follows;
+// `chained`: the one before is a product that does not write the B of this
+// launch's NT and NN products.
+route_status run(const route_layer *p, int epi, Prod *w, int count, const Prod *all, int count_all,
                  bool chained, bool more, cudaStream_t stream) {
-    GemmArgs &a = pr.args;
-    const int width = ch.small ? kSmallTile : ch.bn;
+    const Choice ch = choose(p, epi, all, count_all);
+    GemmMaps maps;
+    GemmArgs a;
+    memset(&a, 0, offsetof(GemmArgs, first));
+    a.nprob = count;
     a.splits = ch.splits;
-    int items = 0;
+    a.fp16 = p->type == kFp16;
+    a.timeout_ns = p->timeout_ns;
+    a.status = p->words;
+    a.test_stall = p->test_stall;
+
+    struct {
+        const void *ptr;
+        long long ld, inner, outer;
+        uint32_t box;
+    } made[kGemmMaxMaps];
+    int nmaps = 0;
+    route_status st = ROUTE_OK;
+    // The map of `o` [outer, inner] in boxes of 64 x box_outer; operands that
+    // two products share have one.
+    auto map = [&](const Operand &o, long long inner, long long outer, uint32_t box, const char *what) {
+        for (int i = 0; i < nmaps; ++i)
+            if (made[i].ptr == o.p && made[i].ld == o.ld && made[i].inner == inner &&
+                made[i].outer == outer && made[i].box == box)
+                return (uint8_t)i;
+        if (st == ROUTE_OK)
+            st = api_encode_operand(&maps.m[nmaps], o.p, a.fp16, (uint64_t)inner, (uint64_t)outer,
+                                    (uint64_t)(outer > 1 ? o.ld : up8(inner)), 64, box, what);
+        made[nmaps] = {o.p, o.ld, inner, outer, box};
+        return (uint8_t)nmaps++;
+    };
+
+    const int width = ch.small ? kSmallTile : ch.bn;
+    const int tile_rows = ch.small ? ch.bn : kGemmBM, tile_cols = epi == kEpiGated ? width / 2 : width;
+    const uint32_t cta_rows = ch.small ? (uint32_t)ch.bn : 128u;  // A rows a CTA loads
+    const uint32_t cta_cols = ch.small ? (uint32_t)kSmallTile : (uint32_t)ch.bn / 2;
+    // the longest contraction first
+    for (int i = 1; i < count; ++i)
+        for (int j = i; j > 0 && w[j].kblocks() > w[j - 1].kblocks(); --j) {
+            const Prod t = w[j];
+            w[j] = w[j - 1], w[j - 1] = t;
+        }
     float *part = reinterpret_cast<float *>(p->scratch + p->o_part);
-    for (int i = 0; i < a.nprob; ++i) {
+    for (int i = 0; i < count; ++i) {
         GemmProblem &q = a.p[i];
-        set_tiles(q, ch.small ? ch.bn : kGemmBM, epi == kEpiGated ? width / 2 : width, p->pairs);
-        q.item_base = items;
-        items += q.tiles_m * q.tiles_n * (ch.small ? 1 : ch.splits);
+        const Prod &x = w[i];
+        q.e = x.e;
+        q.e.M = x.M, q.e.N = x.N;
+        q.form = x.form;
+        q.kblocks = x.kblocks(), q.kswitch = x.kblocks() / x.terms;
+        // A box is no higher than its tensor (one that is loads slowly, 98
+        // against 25 us at 8x3584x7168).
+        const uint32_t box = (uint32_t)x.M >= cta_rows ? cta_rows : (uint32_t)up8(x.M);
+        q.a_bytes = (x.form == kFormTT ? cta_rows : box) * 64 * 2;
+        for (int t = 0; t < x.terms; ++t) {
+            if (x.form == kFormTT)
+                q.a[t] = map(x.a[t], x.M, x.K, 64, "x");
+            else
+                q.a[t] = map(x.a[t], x.K, x.M, box, "rows' operand");
+            if (x.form == kFormNN)
+                q.b[t][0] = map(x.b[t], x.K, x.N, cta_cols, "W");
+            else
+                q.b[t][0] = map(x.b[t], x.N, x.K, 64, "columns' operand");
+            q.b[t][1] = epi == kEpiGated ? map(x.b[1], x.N, x.K, 64, "W_up") : q.b[t][0];
+        }
+        set_tiles(q, tile_rows, tile_cols, p->pairs);
+        q.item_base = a.items;
+        a.items += q.tiles_m * q.tiles_n * (ch.small ? 1 : ch.splits);
         if (!ch.small && ch.splits > 1) {
             q.e.part = part;
-            q.e.ld_part = up16(q.e.N) * (epi == kEpiGated ? 2 : 1);
-            part += (size_t)ch.splits * q.e.M * q.e.ld_part;
+            q.e.ld_part = up16(x.N) * (epi == kEpiGated ? 2 : 1);
+            part += (size_t)ch.splits * x.M * q.e.ld_part;
         }
     }
-    a.items = items;
+    if (st != ROUTE_OK) return st;
     if (ch.small) {
-        if (form == kFormTT) a.a_bytes = (unsigned)ch.bn * 64 * 2;
         a.trigger = more;
-        const cudaError_t e = small_launch(form, epi, ch.bn, pr.maps, a, chained, stream);
+        const cudaError_t e = small_launch(epi, ch.bn, maps, a, chained, stream);
         return e == cudaSuccess ? ROUTE_OK : cuda_fail(e, "product kernel launch");
     }
-    a.pairs = items < p->pairs ? items : p->pairs;
+    a.pairs = a.items < p->pairs ? a.items : p->pairs;
+    if (count > 1 && a.items <= 4 * p->pairs && p->pairs <= kGemmMaxPairs) deal_items(a, a.pairs);
     a.trigger = more || ch.splits > 1;
-    cudaError_t e = gemm_launch(form, epi, ch.bn, pr.maps, a, stream);
+    const int form = w[0].form == kFormNT ? kFormNT : epi == kEpiDGate ? kFormNN : kFormMixed;
+    cudaError_t e = gemm_launch(form, epi, ch.bn, maps, a, stream);
     if (e != cudaSuccess) return cuda_fail(e, "product kernel launch");
     if (ch.splits > 1)
-        for (int i = 0; i < a.nprob; ++i) {
+        for (int i = 0; i < count; ++i) {
             FinishArgs f;
             f.splits = ch.splits;
-            f.trigger = more || i + 1 < a.nprob;
+            f.trigger = more || i + 1 < count;
             f.e = a.p[i].e;
             e = gemm_finish_launch(epi, f, stream);
             if (e != cudaSuccess) return cuda_fail(e, "product finish kernel launch");
@@ -300,95 +392,34 @@ route_status run(const route_layer *p, Product &pr, int form, int epi, const Cho
     return ROUTE_OK;
 }
 
-Choice choose_one(const route_layer *p, int form, int epi, int M, int N, int kblocks) {
-    const Shape s = {M, N};
-    return choose(p, form, epi, &s, 1, kblocks);
+// A product whose result goes to out[M, N].
+Prod product(const route_layer *p, int form, int M, int N, int K, const Operand &a, const Operand &b,
+             void *out, long long ld_out, int out_type) {
+    Prod w;
+    memset(static_cast<void *>(&w), 0, sizeof w);
+    w.form = form, w.M = M, w.N = N, w.terms = 1, w.K = K;
+    w.a[0] = a, w.b[0] = b;
+    w.e.out = out;
+    w.e.ld_out = M > 1 ? ld_out : up16(N);
+    w.e.out_type = out_type;
+    w.e.bias_type = p->type;
+    w.e.vec = vec_bits(out, w.e.ld_out, nullptr, nullptr, 0, out_type, nullptr);
+    return w;
 }
 
-int kblocks_of(int k) { return (k + 63) / 64; }
-
-void set_out(GemmProblem &q, void *out, long long ld_out, int out_type) {
-    q.e.out = out;
-    q.e.ld_out = q.e.M > 1 ? ld_out : up16(q.e.N);
-    q.e.out_type = out_type;
-    q.e.vec = vec_bits(q.e.out, q.e.ld_out, nullptr, nullptr, 0, out_type, nullptr);
-}
-
-// out[M, N] = epilogue(A[M, K] W[K, N]): A K-contiguous, W N-contiguous.
+// out[M, N] = act(A[M, K] W[K, N] + bias) + residual.
 route_status forward_product(const route_layer *p, const Operand &A, const Operand &W, int M, int K,
                              int N, int act, const void *bias, const void *residual, int64_t ld_res,
                              void *out, int64_t ld_out, int out_type, float *saved, bool chained,
                              cudaStream_t stream) {
-    Product pr(p);
-    GemmProblem &q = pr.args.p[0];
-    pr.args.nprob = 1;
-    q.e.M = M, q.e.N = N;
-    q.kblocks = q.kswitch = kblocks_of(K);
-    set_out(q, out, ld_out, out_type);
-    q.e.bias = bias, q.e.bias_type = p->type;
-    q.e.residual = residual;
-    q.e.ld_res = M > 1 ? ld_res : up16(N);
-    q.e.act = act;
-    q.e.saved = saved, q.e.ld_saved = up16(N);
-    q.e.vec = vec_bits(out, q.e.ld_out, nullptr, residual, q.e.ld_res, out_type, bias);
-    const int epi = act == kActNone ? kEpiLinear : kEpiAct;
-    const Choice ch = choose_one(p, kFormNT, epi, M, N, q.kblocks);
-    route_status st;
-    if ((st = pr.map(A, K, M, pr.a_rows(M, ch), "x", &q.a[0])) != ROUTE_OK ||
-        (st = pr.map(W, N, K, 64, "W", &q.b[0][0])) != ROUTE_OK)
-        return st;
-    q.b[0][1] = q.b[0][0];
-    return run(p, pr, kFormNT, epi, ch, chained, false, stream);
-}
-
-// out[M, K] = sum over i of dz_i[M, N] W_i[K, N]^T, one or two terms.
-route_status input_grad(const route_layer *p, int terms, const Operand *dz, const Operand *W, int M,
-                        int N, int K, void *out, int64_t ld_out, bool chained, bool more,
-                        cudaStream_t stream) {
-    Product pr(p);
-    GemmProblem &q = pr.args.p[0];
-    pr.args.nprob = 1;
-    q.e.M = M, q.e.N = K;
-    q.kswitch = kblocks_of(N);
-    q.kblocks = terms * q.kswitch;
-    set_out(q, out, ld_out, p->type);
-    const Choice ch = choose_one(p, kFormNN, kEpiLinear, M, K, q.kblocks);
-    for (int i = 0; i < terms; ++i) {
-        route_status st;
-        if ((st = pr.map(dz[i], N, M, pr.a_rows(M, ch), "dz", &q.a[i])) != ROUTE_OK ||
-            (st = pr.map(W[i], N, K, pr.b_rows(ch), "W", &q.b[i][0])) != ROUTE_OK)
-            return st;
-        q.b[i][1] = q.b[i][0];
-    }
-    return run(p, pr, kFormNN, kEpiLinear, ch, chained, more, stream);
-}
-
-// dW_i[K_i, N_i] = x_i[rows, K_i]^T dz_i[rows, N_i] for up to three weights.
-struct WeightGrad {
-    Operand x, dz;
-    int K, N;
-    void *dW;
-    int64_t ld;
-};
-// `shapes`: of all the weights the operator has, so that a gradient's bits do
-// not depend on which others are asked for.
-route_status weight_grads(const route_layer *p, const WeightGrad *w, int count, int rows,
-                          const Shape *shapes, int all, cudaStream_t stream) {
-    Product pr(p);
-    pr.args.nprob = count;
-    for (int i = 0; i < count; ++i) {
-        GemmProblem &q = pr.args.p[i];
-        q.e.M = w[i].K, q.e.N = w[i].N;
-        q.kblocks = q.kswitch = kblocks_of(rows);
-        set_out(q, w[i].dW, w[i].ld, p->type);
-        route_status st;
-        if ((st = pr.map(w[i].x, q.e.M, rows, 64, "x", &q.a[0])) != ROUTE_OK ||
-            (st = pr.map(w[i].dz, q.e.N, rows, 64, "dz", &q.b[0][0])) != ROUTE_OK)
-            return st;
-        q.b[0][1] = q.b[0][0];
-    }
-    const Choice ch = choose(p, kFormTT, kEpiLinear, shapes, all, kblocks_of(rows));
-    return run(p, pr, kFormTT, kEpiLinear, ch, false, false, stream);
+    Prod w = product(p, kFormNT, M, N, K, A, W, out, ld_out, out_type);
+    w.e.bias = bias;
+    w.e.residual = residual;
+    w.e.ld_res = M > 1 ? ld_res : up16(N);
+    w.e.act = act;
+    w.e.saved = saved, w.e.ld_saved = up16(N);
+    w.e.vec = vec_bits(out, w.e.ld_out, nullptr, residual, w.e.ld_res, out_type, bias);
+    return run(p, act == kActNone ? kEpiLinear : kEpiAct, &w, 1, &w, 1, chained, false, stream);
 }
 
 route_status zero_matrix(void *p, int64_t ld, int rows, int cols, int esize, cudaStream_t stream) {
@@ -672,10 +703,10 @@ route_status route_linear_forward(const route_layer *p, int rows, const void *x,
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     DeviceGuard guard(p->device);
-    Operand ox, ow;
-    if ((st = operand(p, x, ld_x, rows, p->k, p->o_x, s, &ox)) != ROUTE_OK ||
-        (st = operand(p, W, ld_W, p->k, p->n, p->o_w[0], s, &ow)) != ROUTE_OK)
-        return st;
+    Copies copies(p);
+    const Operand ox = copies.operand(x, ld_x, rows, p->k, p->o_x);
+    const Operand ow = copies.operand(W, ld_W, p->k, p->n, p->o_w[0]);
+    if ((st = copies.launch(s)) != ROUTE_OK) return st;
     return forward_product(p, ox, ow, rows, p->k, p->n, p->act, bias, residual, ld_residual, out,
                            ld_out, p->out_type, static_cast<float *>(saved), false, s);
 }
@@ -724,19 +755,21 @@ route_status route_linear_backward(const route_layer *p, int rows, const void *d
         const cudaError_t e = dz_launch(a, s);
         if (e != cudaSuccess) return cuda_fail(e, "pre-activation gradient kernel launch");
     }
-    if (dx) {
-        Operand ow;
-        if ((st = operand(p, W, ld_W, p->k, p->n, p->o_w[0], s, &ow)) != ROUTE_OK ||
-            (st = input_grad(p, 1, &dz, &ow, rows, p->n, p->k, dx, ld_dx, false, dW != nullptr, s)) != ROUTE_OK)
-            return st;
-    }
-    if (dW) {
-        WeightGrad g = {{}, dz, p->k, p->n, dW, ld_dW};
-        if ((st = operand(p, x, ld_x, rows, p->k, p->o_x, s, &g.x)) != ROUTE_OK) return st;
-        const Shape shape = {p->k, p->n};
-        return weight_grads(p, &g, 1, rows, &shape, 1, s);
-    }
-    return ROUTE_OK;
+    if (!dx && !dW) return ROUTE_OK;
+    // dx = dz W^T and dW = x^T dz, in one launch
+    Copies copies(p);
+    const Operand ox = dW ? copies.operand(x, ld_x, rows, p->k, p->o_x) : Operand{nullptr, 0};
+    const Operand ow = dx ? copies.operand(W, ld_W, p->k, p->n, p->o_w[0]) : Operand{nullptr, 0};
+    if ((st = copies.launch(s)) != ROUTE_OK) return st;
+    // both, for the choice of tiles: a gradient's bits do not depend on
+    // whether the other is asked for
+    const Prod all[2] = {product(p, kFormNN, rows, p->k, p->n, dz, ow, dx, ld_dx, p->type),
+                         product(p, kFormTT, p->k, p->n, rows, ox, dz, dW, ld_dW, p->type)};
+    Prod w[2];
+    int count = 0;
+    if (dx) w[count++] = all[0];
+    if (dW) w[count++] = all[1];
+    return run(p, kEpiLinear, w, count, all, 2, false, false, s);
 }
 
 route_status route_gated_forward(const route_layer *p, int rows, const void *x, int64_t ld_x,
@@ -759,32 +792,21 @@ route_status route_gated_forward(const route_layer *p, int rows, const void *x, 
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     DeviceGuard guard(p->device);
-    Operand ox, og, ou, od;
-    if ((st = operand(p, x, ld_x, rows, p->k, p->o_x, s, &ox)) != ROUTE_OK ||
-        (st = operand(p, W_gate, ld_gate, p->k, p->f, p->o_w[0], s, &og)) != ROUTE_OK ||
-        (st = operand(p, W_up, ld_up, p->k, p->f, p->o_w[1], s, &ou)) != ROUTE_OK ||
-        (st = operand(p, W_down, ld_down, p->f, p->n, p->o_w[2], s, &od)) != ROUTE_OK)
-        return st;
+    Copies copies(p);
+    const Operand ox = copies.operand(x, ld_x, rows, p->k, p->o_x);
+    const Operand og = copies.operand(W_gate, ld_gate, p->k, p->f, p->o_w[0]);
+    const Operand ou = copies.operand(W_up, ld_up, p->k, p->f, p->o_w[1]);
+    const Operand od = copies.operand(W_down, ld_down, p->f, p->n, p->o_w[2]);
+    if ((st = copies.launch(s)) != ROUTE_OK) return st;
     // h = act(x W_gate) * (x W_up): one kernel for both projections
     const long long ldf = up16(p->f);
     uint8_t *h = saved ? static_cast<uint8_t *>(saved) + saved_h(p, rows) : p->scratch + p->o_h;
-    {
-        Product pr(p);
-        GemmProblem &q = pr.args.p[0];
-        pr.args.nprob = 1;
-        q.e.M = rows, q.e.N = p->f;
-        q.kblocks = q.kswitch = kblocks_of(p->k);
-        set_out(q, h, ldf, p->type);
-        q.e.act = p->act;
-        q.e.saved = static_cast<float *>(saved), q.e.ld_saved = ldf;
-        q.e.saved2 = saved ? q.e.saved + (size_t)rows * ldf : nullptr;
-        const Choice ch = choose_one(p, kFormNT, kEpiGated, rows, p->f, q.kblocks);
-        if ((st = pr.map(ox, p->k, rows, pr.a_rows(rows, ch), "x", &q.a[0])) != ROUTE_OK ||
-            (st = pr.map(og, p->f, p->k, 64, "W_gate", &q.b[0][0])) != ROUTE_OK ||
-            (st = pr.map(ou, p->f, p->k, 64, "W_up", &q.b[0][1])) != ROUTE_OK ||
-            (st = run(p, pr, kFormNT, kEpiGated, ch, false, true, s)) != ROUTE_OK)
-            return st;
-    }
+    Prod w = product(p, kFormNT, rows, p->f, p->k, ox, og, h, ldf, p->type);
+    w.b[1] = ou;
+    w.e.act = p->act;
+    w.e.saved = static_cast<float *>(saved), w.e.ld_saved = ldf;
+    w.e.saved2 = saved ? w.e.saved + (size_t)rows * ldf : nullptr;
+    if ((st = run(p, kEpiGated, &w, 1, &w, 1, false, true, s)) != ROUTE_OK) return st;
     return forward_product(p, {h, ldf}, od, rows, p->f, p->n, kActNone, nullptr, residual,
                            ld_residual, out, ld_out, p->type, nullptr, true, s);
 }
@@ -824,55 +846,42 @@ route_status route_gated_backward(const route_layer *p, int rows, const void *do
     if ((st = check_vec("saved", saved, 32)) != ROUTE_OK) return st;
 
     const long long ldf = up16(p->f);
-    Operand dy;
-    if ((st = operand(p, dout, ld_dout, rows, p->n, p->o_dout, s, &dy)) != ROUTE_OK) return st;
-    Operand dz[2] = {{p->scratch + p->o_dg, ldf}, {p->scratch + p->o_du, ldf}};
+    const bool weights = dW_gate || dW_up || dW_down;
+    const Operand none = {nullptr, 0};
+    Copies copies(p);
+    const Operand dy = copies.operand(dout, ld_dout, rows, p->n, p->o_dout);
+    const Operand od = pre ? copies.operand(W_down, ld_down, p->f, p->n, p->o_w[2]) : none;
+    const Operand og = dx ? copies.operand(W_gate, ld_gate, p->k, p->f, p->o_w[0]) : none;
+    const Operand ou = dx ? copies.operand(W_up, ld_up, p->k, p->f, p->o_w[1]) : none;
+    const Operand ox = dW_gate || dW_up ? copies.operand(x, ld_x, rows, p->k, p->o_x) : none;
+    if ((st = copies.launch(s)) != ROUTE_OK) return st;
+    const Operand dg = {p->scratch + p->o_dg, ldf}, du = {p->scratch + p->o_du, ldf};
     if (pre) {
         // dh = dout W_down^T, turned into dgate and dup in its epilogue
-        Operand od;
-        if ((st = operand(p, W_down, ld_down, p->f, p->n, p->o_w[2], s, &od)) != ROUTE_OK) return st;
-        Product pr(p);
-        GemmProblem &q = pr.args.p[0];
-        pr.args.nprob = 1;
-        q.e.M = rows, q.e.N = p->f;
-        q.kblocks = q.kswitch = kblocks_of(p->n);
-        set_out(q, const_cast<void *>(dz[0].p), ldf, p->type);
-        q.e.ld_out = ldf;
-        q.e.out2 = const_cast<void *>(dz[1].p);
-        q.e.act = p->act;
-        q.e.saved = static_cast<float *>(const_cast<void *>(saved)), q.e.ld_saved = ldf;
-        q.e.saved2 = q.e.saved + (size_t)rows * ldf;
-        const Choice ch = choose_one(p, kFormNN, kEpiDGate, rows, p->f, q.kblocks);
-        if ((st = pr.map(dy, p->n, rows, pr.a_rows(rows, ch), "dout", &q.a[0])) != ROUTE_OK ||
-            (st = pr.map(od, p->n, p->f, pr.b_rows(ch), "W_down", &q.b[0][0])) != ROUTE_OK)
-            return st;
-        q.b[0][1] = q.b[0][0];
-        if ((st = run(p, pr, kFormNN, kEpiDGate, ch, false, true, s)) != ROUTE_OK) return st;
+        Prod w = product(p, kFormNN, rows, p->f, p->n, dy, od, const_cast<void *>(dg.p), ldf, p->type);
+        w.e.ld_out = ldf;
+        w.e.out2 = const_cast<void *>(du.p);
+        w.e.act = p->act;
+        w.e.saved = static_cast<float *>(const_cast<void *>(saved)), w.e.ld_saved = ldf;
+        w.e.saved2 = w.e.saved + (size_t)rows * ldf;
+        if ((st = run(p, kEpiDGate, &w, 1, &w, 1, false, dx || weights, s)) != ROUTE_OK) return st;
     }
-    const bool weights = dW_gate || dW_up || dW_down;
-    if (dx) {
-        Operand w[2];
-        const bool chained = p->f % 8 == 0;  // no copy of the weights between the two products
-        if ((st = operand(p, W_gate, ld_gate, p->k, p->f, p->o_w[0], s, &w[0])) != ROUTE_OK ||
-            (st = operand(p, W_up, ld_up, p->k, p->f, p->o_w[1], s, &w[1])) != ROUTE_OK ||
-            (st = input_grad(p, 2, dz, w, rows, p->f, p->k, dx, ld_dx, chained, weights, s)) != ROUTE_OK)
-            return st;
-    }
-    if (!weights) return ROUTE_OK;
-    WeightGrad g[3];
+    // dx = dgate W_gate^T + dup W_up^T and the weights' gradients, in one
+    // launch; the choice of tiles goes by all four, so that a gradient's bits
+    // do not depend on which others are asked for
+    const Operand h = {static_cast<const uint8_t *>(saved) + saved_h(p, rows), ldf};
+    Prod all[4] = {product(p, kFormNN, rows, p->k, p->f, dg, og, dx, ld_dx, p->type),
+                   product(p, kFormTT, p->k, p->f, rows, ox, dg, dW_gate, ld_dgate, p->type),
+                   product(p, kFormTT, p->k, p->f, rows, ox, du, dW_up, ld_dup, p->type),
+                   product(p, kFormTT, p->f, p->n, rows, h, dy, dW_down, ld_ddown, p->type)};
+    all[0].terms = 2, all[0].a[1] = du, all[0].b[1] = ou;
+    Prod w[4];
     int count = 0;
-    if (dW_gate || dW_up) {
-        Operand ox;
-        if ((st = operand(p, x, ld_x, rows, p->k, p->o_x, s, &ox)) != ROUTE_OK) return st;
-        if (dW_gate) g[count++] = {ox, dz[0], p->k, p->f, dW_gate, ld_dgate};
-        if (dW_up) g[count++] = {ox, dz[1], p->k, p->f, dW_up, ld_dup};
-    }
-    if (dW_down) {
-        const Operand h = {static_cast<const uint8_t *>(saved) + saved_h(p, rows), ldf};
-        g[count++] = {h, dy, p->f, p->n, dW_down, ld_ddown};
-    }
-    const Shape shapes[3] = {{p->k, p->f}, {p->k, p->f}, {p->f, p->n}};
-    return weight_grads(p, g, count, rows, shapes, 3, s);
+    if (dx) w[count++] = all[0];
+    if (dW_gate) w[count++] = all[1];
+    if (dW_up) w[count++] = all[2];
+    if (dW_down) w[count++] = all[3];
+    return run(p, kEpiLinear, w, count, all, 4, pre, false, s);
 }
 
 }  // extern "C"

@@ -8,26 +8,34 @@ namespace route {
 namespace {
 
 constexpr int kDzCols = 256;       // columns of a block: 32 threads of 8
+constexpr int kDzRows = 4;
 constexpr int kDzMaxBlocks = 128;  // row blocks: partial sums a column
 
 // Eight values a thread; columns past `cols` become zeros up to the next
 // multiple of 8 (ld_dst is one).
-__global__ void __launch_bounds__(256)
-    repack_kernel(const uint16_t *src, long long ld_src, uint16_t *dst, long long ld_dst, int rows,
-                  int cols) {
+__global__ void __launch_bounds__(256) repack_kernel(const __grid_constant__ RepackArgs args) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int groups = (cols + 7) >> 3;
-    const long long total = (long long)rows * groups;
+    const auto &a = args.c[blockIdx.y];
+    const uint16_t *src = static_cast<const uint16_t *>(a.src);
+    uint16_t *dst = static_cast<uint16_t *>(a.dst);
+    const long long ld_src = a.ld_src, ld_dst = a.ld_dst;
+    const int cols = a.cols, groups = (cols + 7) >> 3;
+    const long long total = (long long)a.rows * groups;
     for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total;
          i += (long long)gridDim.x * blockDim.x) {
         const int r = (int)(i / groups), c = (int)(i % groups) * 8;
         const uint16_t *s = src + (long long)r * ld_src + c;
         uint32_t w[4];
+        if (c + 8 <= cols) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t lo = c + 2 * e < cols ? s[2 * e] : 0u;
-            const uint32_t hi = c + 2 * e + 1 < cols ? s[2 * e + 1] : 0u;
-            w[e] = lo | (hi << 16);
+            for (int e = 0; e < 4; ++e) w[e] = s[2 * e] | ((uint32_t)s[2 * e + 1] << 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t lo = c + 2 * e < cols ? s[2 * e] : 0u;
+                const uint32_t hi = c + 2 * e + 1 < cols ? s[2 * e + 1] : 0u;
+                w[e] = lo | (hi << 16);
+            }
         }
         *reinterpret_cast<uint4 *>(dst + (long long)r * ld_dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
@@ -49,35 +57,55 @@ __global__ void __launch_bounds__(256) dz_kernel(const __grid_constant__ DzArgs 
         const int n = a.n - c;
         const uint16_t *dout = static_cast<const uint16_t *>(a.dout);
         uint16_t *dz = static_cast<uint16_t *>(a.dz);
-        for (int r = blockIdx.y * rows_per_block + warp; r < r1; r += 8) {
-            float v[8];
-            const uint16_t *s = dout + (long long)r * a.ld_dout + c;
-            if (vec && n >= 8) {
-                const uint4 t = *reinterpret_cast<const uint4 *>(s);
-                const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+        // four rows at a time, so that their loads are on the way together
+        for (int r = blockIdx.y * rows_per_block + warp; r < r1; r += 8 * kDzRows) {
+            uint4 t[kDzRows];
+            float4 z0[kDzRows], z1[kDzRows];
+#pragma unroll
+            for (int k = 0; k < kDzRows; ++k) {
+                const int row = r + 8 * k;
+                if (row >= r1) break;
+                const uint16_t *s = dout + (long long)row * a.ld_dout + c;
+                if (vec && n >= 8) {
+                    t[k] = *reinterpret_cast<const uint4 *>(s);
+                } else {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t lo = 2 * e < n ? s[2 * e] : 0u, hi = 2 * e + 1 < n ? s[2 * e + 1] : 0u;
+                        w[e] = lo | (hi << 16);
+                    }
+                    t[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                if (a.z != nullptr) {
+                    const float4 *q = reinterpret_cast<const float4 *>(a.z + (long long)row * a.ld_z + c);
+                    z0[k] = q[0], z1[k] = q[1];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kDzRows; ++k) {
+                const int row = r + 8 * k;
+                if (row >= r1) break;
+                float v[8];
+                const uint32_t w[4] = {t[k].x, t[k].y, t[k].z, t[k].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 f = unpack16(w[e], a.type);
                     v[2 * e] = f.x, v[2 * e + 1] = f.y;
                 }
-            } else {
+                if (a.z != nullptr) {
+                    float z[8] = {z0[k].x, z0[k].y, z0[k].z, z0[k].w, z1[k].x, z1[k].y, z1[k].z, z1[k].w}, d[8];
+                    act_slopes<8>(a.act, z, z, d);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = e < n ? load_elem(s, a.type, e) : 0.f;
+                    for (int e = 0; e < 8; ++e) v[e] = e < n ? v[e] * d[e] : 0.f;
+                }
+                if (dz != nullptr)  // ld_dz is a multiple of 8
+                    *reinterpret_cast<uint4 *>(dz + (long long)row * a.ld_dz + c) =
+                        make_uint4(pack16(v[0], v[1], a.type), pack16(v[2], v[3], a.type),
+                                   pack16(v[4], v[5], a.type), pack16(v[6], v[7], a.type));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[e] += v[e];
             }
-            if (a.z != nullptr) {
-                const float4 *q = reinterpret_cast<const float4 *>(a.z + (long long)r * a.ld_z + c);
-                const float4 z0 = q[0], z1 = q[1];
-                float z[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w}, d[8];
-                act_slopes<8>(a.act, z, z, d);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = e < n ? v[e] * d[e] : 0.f;
-            }
-            if (dz != nullptr)  // ld_dz is a multiple of 8
-                *reinterpret_cast<uint4 *>(dz + (long long)r * a.ld_dz + c) =
-                    make_uint4(pack16(v[0], v[1], a.type), pack16(v[2], v[3], a.type),
-                               pack16(v[4], v[5], a.type), pack16(v[6], v[7], a.type));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] += v[e];
         }
     }
     if (a.dbias == nullptr) return;
@@ -91,23 +119,26 @@ __global__ void __launch_bounds__(256) dz_kernel(const __grid_constant__ DzArgs 
     if (col < a.n) a.part[(long long)blockIdx.y * a.n + col] = t;
 }
 
-// Column sums of `blocks` rows of partials, in order within each of eight
-// runs and then run by run.
-__global__ void __launch_bounds__(256) colsum_kernel(const float *part, int blocks, int n, void *out,
-                                                     int type, int trigger) {
-    __shared__ float s_sum[8][33];
+// Column sums of `blocks` rows of partials: each of 16 warps adds every
+// sixteenth, and the sums meet in order.
+constexpr int kSumWarps = 16;
+__global__ void __launch_bounds__(32 * kSumWarps)
+    colsum_kernel(const float *part, int blocks, int n, void *out, int type, int trigger) {
+    __shared__ float s_sum[kSumWarps][32];
     if (threadIdx.x == 0 && trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float t = 0.f;
-    if (c < n)
-        for (int b = warp; b < blocks; b += 8) t += part[(long long)b * n + c];
+    if (c < n) {
+#pragma unroll 8
+        for (int b = warp; b < blocks; b += kSumWarps) t += __ldcg(part + (long long)b * n + c);
+    }
     s_sum[warp][lane] = t;
     __syncthreads();
     if (warp == 0 && c < n) {
 #pragma unroll
-        for (int w = 1; w < 8; ++w) t += s_sum[w][lane];
+        for (int w = 1; w < kSumWarps; ++w) t += s_sum[w][lane];
         store_elem(out, type, c, t);
     }
 }
@@ -128,13 +159,14 @@ cudaError_t launch_pdl(void (*fn)(P...), dim3 grid, dim3 block, cudaStream_t str
 
 }  // namespace
 
-cudaError_t repack_launch(const void *src, long long ld_src, void *dst, long long ld_dst, int rows,
-                          int cols, cudaStream_t stream) {
-    const long long total = (long long)rows * ((cols + 7) / 8);
-    const unsigned blocks = (unsigned)(total / 256 < 2432 ? (total + 255) / 256 : 2432);
-    return launch_pdl(repack_kernel, dim3(blocks), dim3(256), stream,
-                      static_cast<const uint16_t *>(src), ld_src, static_cast<uint16_t *>(dst),
-                      ld_dst, rows, cols);
+cudaError_t repack_launch(const RepackArgs &args, cudaStream_t stream) {
+    long long most = 0;
+    for (int i = 0; i < args.count; ++i) {
+        const long long n = (long long)args.c[i].rows * ((args.c[i].cols + 7) / 8);
+        most = most < n ? n : most;
+    }
+    const unsigned blocks = (unsigned)(most / 256 < 1216 ? (most + 255) / 256 : 1216);
+    return launch_pdl(repack_kernel, dim3(blocks, args.count), dim3(256), stream, args);
 }
 
 size_t dz_part_floats(int n) { return (size_t)kDzMaxBlocks * n; }
@@ -152,7 +184,7 @@ cudaError_t dz_launch(const DzArgs &args, cudaStream_t stream) {
     first.trigger = args.trigger || args.dbias != nullptr;
     cudaError_t e = launch_pdl(dz_kernel, dim3(cb, rb), dim3(256), stream, first, per, vec);
     if (e != cudaSuccess || args.dbias == nullptr) return e;
-    return launch_pdl(colsum_kernel, dim3((args.n + 31) / 32), dim3(256), stream,
+    return launch_pdl(colsum_kernel, dim3((args.n + 31) / 32), dim3(32 * kSumWarps), stream,
                       static_cast<const float *>(args.part), rb, args.n, args.dbias, args.type,
                       args.trigger);
 }

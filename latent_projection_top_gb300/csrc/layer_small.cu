@@ -22,6 +22,8 @@
 // issuer, warps 2..9 epilogue.  Every wait on a copy or an MMA is bounded, as
 // in layer_gemm.cu; all threads of a cluster reach its barriers whatever
 // happened before.
+#include <type_traits>
+
 #include "layer.cuh"
 #include "layer_math.cuh"
 #include "sm103_ptx.cuh"
@@ -49,6 +51,7 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
     d |= 2ull << 61;  // 128-byte swizzle
     return d;
 }
+
 // 16 k of an operand tile, as in layer_gemm.cu.
 template <bool MN>
 __device__ __forceinline__ uint64_t operand_desc(uint32_t base, int kk) {
@@ -91,13 +94,10 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     return v;
 }
 
-template <int FORM, int EPI, int BN>
+template <int EPI, int BN>
 __global__ void __launch_bounds__(kThreads, 2)
     layer_small_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs args,
                        int chained) {
-    constexpr bool R_MN = FORM == kFormTT;   // rows' operand: M-contiguous, else K-contiguous
-    constexpr bool C_MN = FORM != kFormNN;   // columns' operand: N-contiguous, else K-contiguous
-    static_assert(!R_MN || BN >= 64, "an M-contiguous operand comes in boxes of 64");
     constexpr int S = stages_of(BN);
     constexpr uint32_t kStage = stage_bytes(BN);
     constexpr int kTileCols = EPI == kEpiGated ? kSmallTile / 2 : kSmallTile;
@@ -121,6 +121,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     int pi = 0;
     while (pi + 1 < args.nprob && i >= args.p[pi + 1].item_base) ++pi;
     const GemmProblem &p = args.p[pi];
+    const int form = EPI == kEpiLinear ? p.form : EPI == kEpiDGate ? kFormNN : kFormNT;
+    const bool r_mn = form == kFormTT;  // rows' operand: M-contiguous (BN >= 64), else K-contiguous
+    const bool c_mn = form != kFormNN;  // columns' operand: N-contiguous, else K-contiguous
     i -= p.item_base;
     const int tm = i % p.tiles_m, tn = i / p.tiles_m;
     const int kb0 = (int)((long long)p.kblocks * rank / C);
@@ -152,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             // columns of one row tile are read once: they leave L2 first
             const uint64_t pol_c = p.tiles_m == 1 ? ptx::policy_evict_first() : ptx::policy_evict_normal();
             const uint64_t pol_r = ptx::policy_evict_last();
-            const uint32_t tx = kColBytes + args.a_bytes;
+            const uint32_t tx = kColBytes + p.a_bytes;
             auto columns_of = [&](int it) {
                 const int kb = kb0 + it, s = it % S, seg = kb >= p.kswitch;
                 const int k0 = (seg ? kb - p.kswitch : kb) * 64;
@@ -162,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (EPI == kEpiGated) {
                     ptx::tma_load_2d(sc, m, fb, col0, k0, pol_c);
                     ptx::tma_load_2d(sc + 8192u, &maps.m[p.b[seg][1]], fb, col0, k0, pol_c);
-                } else if (C_MN) {
+                } else if (c_mn) {
                     ptx::tma_load_2d(sc, m, fb, col0, k0, pol_c);
                     ptx::tma_load_2d(sc + 8192u, m, fb, col0 + 64, k0, pol_c);
                 } else {
@@ -174,15 +177,15 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const int k0 = (seg ? kb - p.kswitch : kb) * 64;
                 const uint32_t sr = sbase + s * kStage + kColBytes, fb = full_bar(s);
                 const CUtensorMap *m = &maps.m[p.a[seg]];
-                if (R_MN) {
+                if (r_mn) {
 #pragma unroll
-                    for (int j = 0; j < BN / 64; ++j)
+                    for (int j = 0; j < (BN < 64 ? 1 : BN / 64); ++j)
                         ptx::tma_load_2d(sr + 8192u * j, m, fb, row0 + 64 * j, k0, pol_r);
                 } else {
                     ptx::tma_load_2d(sr, m, fb, k0, row0, pol_r);
                 }
             };
-            const int n_pre = chained ? min(total, S) : 0;
+            const int n_pre = chained && !r_mn ? min(total, S) : 0;
             for (int it = 0; it < n_pre; ++it) columns_of(it);
             asm volatile("griddepcontrol.wait;" ::: "memory");
             if (args.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -202,20 +205,29 @@ __global__ void __launch_bounds__(kThreads, 2)
             // ---------------- MMA issuer ----------------
             // kind::f16, FP32 accumulator, M = 128 columns, N = BN rows
             const uint32_t fmt = args.fp16 ? 0u : 1u;
-            const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((C_MN ? 1u : 0u) << 15) |
-                                   ((R_MN ? 1u : 0u) << 16) | ((uint32_t)(BN >> 3) << 17) |
-                                   ((uint32_t)(kSmallTile >> 4) << 24);
-            for (int it = 0; it < total; ++it) {
-                const int s = it % S;
-                if (!wait_phase(full_bar(s), (uint32_t)(it / S) & 1u, args, &s_abort)) break;
-                ptx::tc_fence_after();
-                const uint32_t sc = sbase + s * kStage, sr = sc + kColBytes;
+            const uint32_t idesc0 = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(BN >> 3) << 17) |
+                                    ((uint32_t)(kSmallTile >> 4) << 24);
+            auto k_loop = [&](auto cols_mn, auto rows_mn) {
+                constexpr bool C_MN = decltype(cols_mn)::value, R_MN = decltype(rows_mn)::value;
+                const uint32_t idesc = idesc0 | ((C_MN ? 1u : 0u) << 15) | ((R_MN ? 1u : 0u) << 16);
+                for (int it = 0; it < total; ++it) {
+                    const int s = it % S;
+                    if (!wait_phase(full_bar(s), (uint32_t)(it / S) & 1u, args, &s_abort)) break;
+                    ptx::tc_fence_after();
+                    const uint32_t sc = sbase + s * kStage, sr = sc + kColBytes;
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    ptx::mma_bf16(tmem_base, operand_desc<C_MN>(sc, kk), operand_desc<R_MN>(sr, kk), idesc,
-                                  (it > 0 || kk > 0) ? 1u : 0u);
-                ptx::mma_commit(empty_bar(s));
-            }
+                    for (int kk = 0; kk < 4; ++kk)
+                        ptx::mma_bf16(tmem_base, operand_desc<C_MN>(sc, kk), operand_desc<R_MN>(sr, kk), idesc,
+                                      (it > 0 || kk > 0) ? 1u : 0u);
+                    ptx::mma_commit(empty_bar(s));
+                }
+            };
+            if (!c_mn)
+                k_loop(std::false_type{}, std::false_type{});
+            else if (!r_mn)
+                k_loop(std::true_type{}, std::false_type{});
+            else
+                k_loop(std::true_type{}, std::true_type{});
             ptx::mma_commit(done_bar);  // every MMA retired (after an abort too)
         }
     }
@@ -283,37 +295,30 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (C > 1) ptx::cluster_sync();  // no CTA leaves while another may read its sums
 }
 
-const void *kernel_of(int form, int epi, int bn) {
-#define ROUTE_SMALL(F, E)                                                                       \
-    if (form == F && epi == E)                                                                  \
-        return bn == 16   ? reinterpret_cast<const void *>(layer_small_kernel<F, E, 16>)        \
-               : bn == 32 ? reinterpret_cast<const void *>(layer_small_kernel<F, E, 32>)        \
-               : bn == 64 ? reinterpret_cast<const void *>(layer_small_kernel<F, E, 64>)        \
-                          : reinterpret_cast<const void *>(layer_small_kernel<F, E, 128>);
-    ROUTE_SMALL(kFormNT, kEpiLinear)
-    ROUTE_SMALL(kFormNT, kEpiAct)
-    ROUTE_SMALL(kFormNT, kEpiGated)
-    ROUTE_SMALL(kFormNN, kEpiLinear)
-    ROUTE_SMALL(kFormNN, kEpiDGate)
+const void *kernel_of(int epi, int bn) {
+#define ROUTE_SMALL(E)                                                                       \
+    if (epi == E)                                                                            \
+        return bn == 16   ? reinterpret_cast<const void *>(layer_small_kernel<E, 16>)        \
+               : bn == 32 ? reinterpret_cast<const void *>(layer_small_kernel<E, 32>)        \
+               : bn == 64 ? reinterpret_cast<const void *>(layer_small_kernel<E, 64>)        \
+                          : reinterpret_cast<const void *>(layer_small_kernel<E, 128>);
+    ROUTE_SMALL(kEpiLinear)
+    ROUTE_SMALL(kEpiAct)
+    ROUTE_SMALL(kEpiGated)
+    ROUTE_SMALL(kEpiDGate)
 #undef ROUTE_SMALL
-    if (form == kFormTT && epi == kEpiLinear)
-        return bn <= 64 ? reinterpret_cast<const void *>(layer_small_kernel<kFormTT, kEpiLinear, 64>)
-                        : reinterpret_cast<const void *>(layer_small_kernel<kFormTT, kEpiLinear, 128>);
     return nullptr;
 }
 
 }  // namespace
 
 cudaError_t small_configure() {
-    for (int form = 0; form < 3; ++form)
-        for (int epi = 0; epi < kEpiCount; ++epi)
-            for (int bn : {16, 32, 64, 128})
-                if (const void *k = kernel_of(form, epi, bn)) {
-                    const int smem = (int)smem_of(form == kFormTT && bn < 64 ? 64 : bn);
-                    const cudaError_t e =
-                        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-                    if (e != cudaSuccess) return e;
-                }
+    for (int epi = 0; epi < kEpiCount; ++epi)
+        for (int bn : {16, 32, 64, 128}) {
+            const cudaError_t e = cudaFuncSetAttribute(
+                kernel_of(epi, bn), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(bn));
+            if (e != cudaSuccess) return e;
+        }
     return cudaSuccess;
 }
 
@@ -323,9 +328,9 @@ int small_smem_bytes() {
     return (int)most;
 }
 
-cudaError_t small_launch(int form, int epi, int rows, const GemmMaps &maps, const GemmArgs &args,
+cudaError_t small_launch(int epi, int rows, const GemmMaps &maps, const GemmArgs &args,
                          bool chained, cudaStream_t stream) {
-    const void *k = kernel_of(form, epi, rows);
+    const void *k = kernel_of(epi, rows);
     if (k == nullptr || args.items < 1 || args.splits < 1 || args.splits > kSmallMaxSplits)
         return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t c = {};
