@@ -62,6 +62,7 @@ struct GemmProblem {
     int form;
     int tiles_m, tiles_n, band; // row tiles, column tiles, column tiles of a band
     int item_base;              // first work item of this problem
+    int splits;                 // K splits of a tile
     int kblocks, kswitch;
     unsigned a_bytes;           // bytes of an A box: fewer rows than a tile's when M is less
     uint8_t a[2], b[2][2];      // A map of each segment, B map of each segment and CTA of the pair
@@ -70,6 +71,7 @@ struct GemmProblem {
 constexpr int kGemmMaxProblems = 4;
 constexpr int kGemmMaxMaps = 12;
 constexpr int kGemmMaxPairs = 80;  // pairs that `count` can describe
+constexpr int kGemmMaxSplits = 32;
 
 struct GemmMaps {
     CUtensorMap m[kGemmMaxMaps];
@@ -78,7 +80,7 @@ struct GemmMaps {
 struct GemmArgs {
     int nprob;                  // problems, the longest contraction first
     int items;                  // work items: tiles x splits over all problems
-    int splits;                 // K splits of every tile
+    int splits;                 // (small tiles) K splits of every tile: the CTAs of a cluster
     int pairs;                  // CTA pairs launched
     int listed;                 // pair j takes items first[c][j] .. of problem c, count[c][j] of them
                                 // (else items j, j + pairs, .. of all)

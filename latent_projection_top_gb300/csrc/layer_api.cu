@@ -39,8 +39,8 @@ struct route_layer {
 namespace {
 
 constexpr unsigned long long kTimeoutNs = 2000000000ull;
-// Split products have at most one item a CTA pair: FP32 partials of a
-// 256 x 256 tile each.
+// A launch's split products have at most two items a CTA pair: FP32 partials
+// of a 256 x 256 tile each.
 constexpr size_t kTilePartBytes = 256 * 256 * 4;
 
 route_status cuda_fail(cudaError_t e, const char *what) {
@@ -162,12 +162,14 @@ struct Copies {
 // splits of the contraction.
 struct Choice {
     bool small;
-    int bn, splits;
+    int bn;
+    int splits[kGemmMaxProblems];  // of each product (small tiles: the same for all)
 };
 
 // A product of a launch: its form, the rows and columns of its result (gated:
 // hidden columns), its contraction's terms and each one's length.
 struct Prod {
+    int id;  // its place among the products that the choice of tiles goes by
     int form, M, N, terms, K;
     Operand a[2], b[2];  // of each term (gated: b of gate and of up)
     Epilogue e;
@@ -181,37 +183,52 @@ int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 // 0.30 us; the small tiles are bound by what an SM reads, about 70 bytes a
 // nanosecond.
 Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
-    Choice best = {false, 256, 1};
-    double t_best = 1e30, elems = 0;
-    int rows = 0, kmost = 0, kleast = 1 << 30;
+    Choice best = {false, 256, {1, 1, 1, 1}};
+    double t_best = 1e30;
+    int rows = 0, kmost = 0;
     bool tt = false;
     for (int i = 0; i < count; ++i) {
-        elems += (double)w[i].M * w[i].N * (epi == kEpiGated ? 2 : 1);
         rows = rows < w[i].M ? w[i].M : rows;
         kmost = kmost < w[i].kblocks() ? w[i].kblocks() : kmost;
-        kleast = kleast > w[i].kblocks() ? w[i].kblocks() : kleast;
         tt = tt || w[i].form == kFormTT;
     }
     for (int bn : {256, 128}) {
-        long long tiles = 0;
-        double work = 0;
         const int cols = epi == kEpiGated ? bn / 2 : bn;
-        for (int i = 0; i < count; ++i) {
-            const long long n = (long long)ceil_div(w[i].M, kGemmBM) * ceil_div(w[i].N, cols);
-            tiles += n, work += (double)n * w[i].kblocks();
-        }
-        const int most = tiles >= p->pairs ? 1 : (int)(p->pairs / tiles);
         const double kb_us = bn == 256 ? 0.34 : 0.30;
-        for (int s = 1; s <= most && (s == 1 || kleast / s >= 2); ++s) {
-            const double longest = ceil_div(kmost, s) * kb_us;
-            double t = ceil_div(tiles * s, p->pairs) * longest;  // equal items
-            if (count > 1) {
-                const double level = work * kb_us / p->pairs + 0.35 * longest;
-                t = level > longest ? level : longest;
+        long long tiles[kGemmMaxProblems];
+        double work = 0;
+        for (int i = 0; i < count; ++i) {
+            tiles[i] = (long long)ceil_div(w[i].M, kGemmBM) * ceil_div(w[i].N, cols);
+            work += (double)tiles[i] * w[i].kblocks();
+        }
+        // No contraction is left longer than `part` of an equal share: without
+        // splits, and with several sizes of them.
+        for (double part : {0.0, 2.0, 1.0, 0.7, 0.5, 0.34, 0.25}) {
+            Choice c = {false, bn, {1, 1, 1, 1}};
+            long long items = 0, split_items = 0;
+            double longest = 0, t = 7.0;
+            for (int i = 0; i < count; ++i) {
+                int s = part > 0 ? (int)(w[i].kblocks() * p->pairs / (work * part) + 0.99) : 1;
+                s = s > kGemmMaxSplits ? kGemmMaxSplits : s;
+                s = s > w[i].kblocks() / 2 ? w[i].kblocks() / 2 : s;
+                s = s < 1 ? 1 : s;
+                c.splits[i] = s;
+                items += tiles[i] * s;
+                const double one = ceil_div(w[i].kblocks(), s) * kb_us;
+                longest = longest < one ? one : longest;
+                if (s > 1) {
+                    split_items += tiles[i] * s;
+                    t += 2.5 + (double)w[i].M * w[i].N * (epi == kEpiGated ? 2 : 1) * 4.0 * (s + 1) / 4e6;
+                }
             }
-            t += 7.0;
-            if (s > 1) t += 2.5 * count + elems * 4.0 * (s + 1) / 4e6;
-            if (t < t_best) t_best = t, best = {false, bn, s};
+            if (split_items > 2 * p->pairs) continue;
+            if (count == 1) {
+                t += ceil_div(items, p->pairs) * longest;  // equal items
+            } else {
+                const double level = work * kb_us / p->pairs + 0.35 * longest;
+                t += level > longest ? level : longest;
+            }
+            if (t < t_best) t_best = t, best = c;
         }
     }
     {
@@ -233,7 +250,7 @@ Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
             level = level / p->sms + 0.35 * longest;
             t = level > longest ? level : longest;
         }
-        if (t + 5.0 < t_best) best = {true, bn, s};
+        if (t + 5.0 < t_best) best = {true, bn, {s, s, s, s}};
     }
     return best;
 }
@@ -276,7 +293,7 @@ void deal_items(GemmArgs &a, int pairs) {
     a.listed = 1;
     for (int c = 0; c < a.nprob; ++c) {
         const int items = (c + 1 < a.nprob ? a.p[c + 1].item_base : a.items) - a.p[c].item_base;
-        const int cost = ceil_div(a.p[c].kblocks, a.splits);
+        const int cost = ceil_div(a.p[c].kblocks, a.p[c].splits);
         for (int j = 0; j < pairs; ++j) a.count[c][j] = 0;
         for (int i = 0; i < items; ++i) {
             ++a.count[c][heap[0] % kGemmMaxPairs];
@@ -299,7 +316,7 @@ route_status run(const route_layer *p, int epi, Prod *w, int count, const Prod *
     GemmArgs a;
     memset(&a, 0, offsetof(GemmArgs, first));
     a.nprob = count;
-    a.splits = ch.splits;
+    a.splits = ch.splits[0];
     a.fp16 = p->type == kFp16;
     a.timeout_ns = p->timeout_ns;
     a.status = p->words;
@@ -330,13 +347,15 @@ route_status run(const route_layer *p, int epi, Prod *w, int count, const Prod *
     const int tile_rows = ch.small ? ch.bn : kGemmBM, tile_cols = epi == kEpiGated ? width / 2 : width;
     const uint32_t cta_rows = ch.small ? (uint32_t)ch.bn : 128u;  // A rows a CTA loads
     const uint32_t cta_cols = ch.small ? (uint32_t)kSmallTile : (uint32_t)ch.bn / 2;
-    // the longest contraction first
+    // the longest items first
+    auto item_blocks = [&](const Prod &x) { return ceil_div(x.kblocks(), ch.splits[x.id]); };
     for (int i = 1; i < count; ++i)
-        for (int j = i; j > 0 && w[j].kblocks() > w[j - 1].kblocks(); --j) {
+        for (int j = i; j > 0 && item_blocks(w[j]) > item_blocks(w[j - 1]); --j) {
             const Prod t = w[j];
             w[j] = w[j - 1], w[j - 1] = t;
         }
     float *part = reinterpret_cast<float *>(p->scratch + p->o_part);
+    int unfinished = 0;
     for (int i = 0; i < count; ++i) {
         GemmProblem &q = a.p[i];
         const Prod &x = w[i];
@@ -361,11 +380,13 @@ route_status run(const route_layer *p, int epi, Prod *w, int count, const Prod *
         }
         set_tiles(q, tile_rows, tile_cols, p->pairs);
         q.item_base = a.items;
-        a.items += q.tiles_m * q.tiles_n * (ch.small ? 1 : ch.splits);
-        if (!ch.small && ch.splits > 1) {
+        q.splits = ch.splits[x.id];
+        a.items += q.tiles_m * q.tiles_n * (ch.small ? 1 : q.splits);
+        if (!ch.small && q.splits > 1) {
             q.e.part = part;
             q.e.ld_part = up16(x.N) * (epi == kEpiGated ? 2 : 1);
-            part += (size_t)ch.splits * x.M * q.e.ld_part;
+            part += (size_t)q.splits * x.M * q.e.ld_part;
+            ++unfinished;
         }
     }
     if (st != ROUTE_OK) return st;
@@ -376,15 +397,15 @@ route_status run(const route_layer *p, int epi, Prod *w, int count, const Prod *
     }
     a.pairs = a.items < p->pairs ? a.items : p->pairs;
     if (count > 1 && a.items <= 4 * p->pairs && p->pairs <= kGemmMaxPairs) deal_items(a, a.pairs);
-    a.trigger = more || ch.splits > 1;
+    a.trigger = more || unfinished > 0;
     const int form = w[0].form == kFormNT ? kFormNT : epi == kEpiDGate ? kFormNN : kFormMixed;
     cudaError_t e = gemm_launch(form, epi, ch.bn, maps, a, stream);
     if (e != cudaSuccess) return cuda_fail(e, "product kernel launch");
-    if (ch.splits > 1)
-        for (int i = 0; i < count; ++i) {
+    for (int i = 0; i < count; ++i)
+        if (a.p[i].splits > 1) {
             FinishArgs f;
-            f.splits = ch.splits;
-            f.trigger = more || i + 1 < count;
+            f.splits = a.p[i].splits;
+            f.trigger = more || --unfinished > 0;
             f.e = a.p[i].e;
             e = gemm_finish_launch(epi, f, stream);
             if (e != cudaSuccess) return cuda_fail(e, "product finish kernel launch");
@@ -476,7 +497,7 @@ route_status finish_prepare(route_layer *p, int device, route_layer **out) {
     if (p->kind == kNorm) {
         p->o_part = area(norm_part_floats(p->k, p->sms) * 4);
     } else {
-        size_t part = (size_t)p->pairs * kTilePartBytes;
+        size_t part = 2 * (size_t)p->pairs * kTilePartBytes;
         if (p->kind == kLinear && p->train && part < dz_part_floats(p->n) * 4)
             part = dz_part_floats(p->n) * 4;
         p->o_part = area(part);
@@ -763,8 +784,9 @@ route_status route_linear_backward(const route_layer *p, int rows, const void *d
     if ((st = copies.launch(s)) != ROUTE_OK) return st;
     // both, for the choice of tiles: a gradient's bits do not depend on
     // whether the other is asked for
-    const Prod all[2] = {product(p, kFormNN, rows, p->k, p->n, dz, ow, dx, ld_dx, p->type),
+    Prod all[2] = {product(p, kFormNN, rows, p->k, p->n, dz, ow, dx, ld_dx, p->type),
                          product(p, kFormTT, p->k, p->n, rows, ox, dz, dW, ld_dW, p->type)};
+    all[1].id = 1;
     Prod w[2];
     int count = 0;
     if (dx) w[count++] = all[0];
@@ -875,6 +897,7 @@ route_status route_gated_backward(const route_layer *p, int rows, const void *do
                    product(p, kFormTT, p->k, p->f, rows, ox, du, dW_up, ld_dup, p->type),
                    product(p, kFormTT, p->f, p->n, rows, h, dy, dW_down, ld_ddown, p->type)};
     all[0].terms = 2, all[0].a[1] = du, all[0].b[1] = ou;
+    for (int i = 0; i < 4; ++i) all[i].id = i;
     Prod w[4];
     int count = 0;
     if (dx) w[count++] = all[0];

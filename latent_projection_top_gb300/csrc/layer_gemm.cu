@@ -122,16 +122,16 @@ __device__ __forceinline__ Item item_of(const GemmArgs &a, int i) {
     while (w.p + 1 < a.nprob && i >= a.p[w.p + 1].item_base) ++w.p;
     const GemmProblem &p = a.p[w.p];
     i -= p.item_base;
-    w.split = i % a.splits;
-    i /= a.splits;
+    w.split = i % p.splits;
+    i /= p.splits;
     const int per_band = p.band * p.tiles_m;
     const int b = i / per_band, r = i - b * per_band;
     const int c0 = b * p.band;
     const int bw = p.tiles_n - c0 < p.band ? p.tiles_n - c0 : p.band;
     w.tm = r / bw;
     w.tn = c0 + r % bw;
-    w.kb0 = (int)((long long)p.kblocks * w.split / a.splits);
-    w.kb1 = (int)((long long)p.kblocks * (w.split + 1) / a.splits);
+    w.kb0 = (int)((long long)p.kblocks * w.split / p.splits);
+    w.kb1 = (int)((long long)p.kblocks * (w.split + 1) / p.splits);
     return w;
 }
 
@@ -373,7 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
             constexpr bool kAhead = EPI != kEpiGated;  // inputs a batch ahead
             constexpr int kBatches = kWarpCols / kG * kGroupBatches;
             static_assert(kSteps % kBatch == 0, "whole batches");
-            const bool whole = args.splits == 1;
+            const bool whole = args.p[w.p].splits == 1;
             auto row_of = [&](int b) { return b % kGroupBatches * (kBatch * kStep) + lane / kLanesRow; };
             auto col_of = [&](int b) { return c0 + b / kGroupBatches * kG + lane % kLanesRow * 4; };
             GroupIn<EPI, kBatch> in, next;
