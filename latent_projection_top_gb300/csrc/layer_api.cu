@@ -237,20 +237,19 @@ Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
         const int cols = epi == kEpiGated ? kSmallTile / 2 : kSmallTile;
         long long tiles = 0;
         for (int i = 0; i < count; ++i) tiles += (long long)ceil_div(w[i].M, bn) * ceil_div(w[i].N, cols);
-        int s = 1;
-        while (s < kSmallMaxSplits && tiles * s * 2 <= 2 * p->sms && s * 2 <= kmost) s *= 2;
-        const double kb_us = (16384 + bn * 128) / 70e3;
-        const double longest = ceil_div(kmost, s) * kb_us + 0.5;
-        double t = ceil_div(tiles * s, p->sms) * longest;
-        if (count > 1) {
+        const double kb_us = (16384 + bn * 128) / 70e3, cta_us = 0.8;
+        for (int s = 1; s <= kSmallMaxSplits && s <= kmost; s *= 2) {
+            if (tiles * s > 8192) break;
+            const double longest = ceil_div(kmost, s) * kb_us + cta_us;
             double level = 0;
             for (int i = 0; i < count; ++i)
                 level += (double)ceil_div(w[i].M, bn) * ceil_div(w[i].N, cols) * s *
-                         (ceil_div(w[i].kblocks(), s) * kb_us + 0.5);
-            level = level / p->sms + 0.35 * longest;
-            t = level > longest ? level : longest;
+                         (ceil_div(w[i].kblocks(), s) * kb_us + cta_us) / p->sms;
+            const double t = 5.0 + (count > 1        ? level + 0.3 * longest
+                                    : longest > level ? longest
+                                                      : level);
+            if (t < t_best) t_best = t, best = {true, bn, {s, s, s, s}};
         }
-        if (t + 5.0 < t_best) best = {true, bn, {s, s, s, s}};
     }
     return best;
 }

@@ -121,17 +121,22 @@ __device__ __forceinline__ Item item_of(const GemmArgs &a, int i) {
     w.p = 0;
     while (w.p + 1 < a.nprob && i >= a.p[w.p + 1].item_base) ++w.p;
     const GemmProblem &p = a.p[w.p];
-    i -= p.item_base;
-    w.split = i % p.splits;
-    i /= p.splits;
-    const int per_band = p.band * p.tiles_m;
-    const int b = i / per_band, r = i - b * per_band;
-    const int c0 = b * p.band;
-    const int bw = p.tiles_n - c0 < p.band ? p.tiles_n - c0 : p.band;
-    w.tm = r / bw;
-    w.tn = c0 + r % bw;
-    w.kb0 = (int)((long long)p.kblocks * w.split / p.splits);
-    w.kb1 = (int)((long long)p.kblocks * (w.split + 1) / p.splits);
+    unsigned u = (unsigned)(i - p.item_base);
+    const unsigned splits = (unsigned)p.splits, kblocks = (unsigned)p.kblocks;
+    w.split = 0, w.kb0 = 0, w.kb1 = (int)kblocks;
+    if (splits > 1) {
+        const unsigned t = u / splits;
+        w.split = (int)(u - t * splits);
+        u = t;
+        w.kb0 = (int)(kblocks * (unsigned)w.split / splits);
+        w.kb1 = (int)(kblocks * (unsigned)(w.split + 1) / splits);
+    }
+    const unsigned per_band = (unsigned)(p.band * p.tiles_m);
+    const unsigned b = u / per_band, r = u - b * per_band, c0 = b * (unsigned)p.band;
+    const unsigned left = (unsigned)p.tiles_n - c0, bw = left < (unsigned)p.band ? left : (unsigned)p.band;
+    const unsigned tm = r / bw;
+    w.tm = (int)tm;
+    w.tn = (int)(c0 + r - tm * bw);
     return w;
 }
 
@@ -357,10 +362,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
         const uint32_t mine = turn + (uint32_t)(warp - 2) * turn_bytes(EPI);
         asm volatile("griddepcontrol.wait;" ::: "memory");
         int job = 0;
+        Epilogue p = args.p[0].e;
+        int of = 0;  // whose
         Walk walk(pair);
         for (int i; walk.next(args, pair, i); ++job) {
             const Item w = item_of(args, i);
-            const Epilogue p = args.p[w.p].e;
+            if (w.p != of) p = args.p[w.p].e, of = w.p;
             const int t = job & 1;
             const int r0 = w.tm * kGemmBM + (int)rank * kHalf + 32 * lq;
             const int c0 = w.tn * kTileCols + cs * kWarpCols;
