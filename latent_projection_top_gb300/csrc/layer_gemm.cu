@@ -277,6 +277,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
         }
         ptx::mbar_init(drain_bar, 1);
         ptx::fence_barrier_init();
+        ptx::prefetch_tensormap(&maps.m[args.p[0].a[0]]);
+        ptx::prefetch_tensormap(&maps.m[args.p[0].b[0][rank]]);
     }
     if (warp == 1) {
         ptx::tmem_alloc_pair(ptx::smem_addr(&s_tmem_base), 2 * BN);

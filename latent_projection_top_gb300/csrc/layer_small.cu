@@ -130,7 +130,47 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int total = (int)((long long)p.kblocks * (rank + 1) / C) - kb0;
     const int row0 = tm * BN, col0 = tn * kTileCols;
 
-    if (threadIdx.x == 0) {
+    // TMA producer: lane 0 of warp 0
+    // columns of one row tile are read once: they leave L2 first
+    const uint64_t pol_c = p.tiles_m == 1 ? ptx::policy_evict_first() : ptx::policy_evict_normal();
+    const uint64_t pol_r = ptx::policy_evict_last();
+    auto columns_of = [&](int it) {
+        const int kb = kb0 + it, s = it % S, seg = kb >= p.kswitch;
+        const int k0 = (seg ? kb - p.kswitch : kb) * 64;
+        const uint32_t sc = sbase + s * kStage, fb = full_bar(s);
+        const CUtensorMap *m = &maps.m[p.b[seg][0]];
+        ptx::mbar_arrive_expect_tx(fb, kColBytes + p.a_bytes);
+        if (EPI == kEpiGated) {
+            ptx::tma_load_2d(sc, m, fb, col0, k0, pol_c);
+            ptx::tma_load_2d(sc + 8192u, &maps.m[p.b[seg][1]], fb, col0, k0, pol_c);
+        } else if (c_mn) {
+            ptx::tma_load_2d(sc, m, fb, col0, k0, pol_c);
+            ptx::tma_load_2d(sc + 8192u, m, fb, col0 + 64, k0, pol_c);
+        } else {
+            ptx::tma_load_2d(sc, m, fb, k0, col0, pol_c);
+        }
+    };
+    auto rows_of = [&](int it) {
+        const int kb = kb0 + it, s = it % S, seg = kb >= p.kswitch;
+        const int k0 = (seg ? kb - p.kswitch : kb) * 64;
+        const uint32_t sr = sbase + s * kStage + kColBytes, fb = full_bar(s);
+        const CUtensorMap *m = &maps.m[p.a[seg]];
+        if (r_mn) {
+#pragma unroll
+            for (int j = 0; j < (BN < 64 ? 1 : BN / 64); ++j)
+                ptx::tma_load_2d(sr + 8192u * j, m, fb, row0 + 64 * j, k0, pol_r);
+        } else {
+            ptx::tma_load_2d(sr, m, fb, k0, row0, pol_r);
+        }
+    };
+    // test hook: the last copies never arrive
+    const int copies = total - (args.test_stall && total > 0 ? 1 : 0);
+    const int first = min(copies, S);
+
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_addr(&s_tmem_base), kTmemCols);
+        ptx::tmem_relinquish();
+    } else if (threadIdx.x == 0) {
         s_abort = 0;
         for (int s = 0; s < S; ++s) {
             ptx::mbar_init(full_bar(s), 1);
@@ -138,10 +178,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         ptx::mbar_init(done_bar, 1);
         ptx::fence_barrier_init();
-    }
-    if (warp == 1) {
-        ptx::tmem_alloc(ptx::smem_addr(&s_tmem_base), kTmemCols);
-        ptx::tmem_relinquish();
+        // the first copies go out while TMEM is being allocated
+        const int n_pre = chained && !r_mn ? first : 0;
+        for (int it = 0; it < n_pre; ++it) columns_of(it);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (args.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        for (int it = 0; it < first; ++it) {
+            if (it >= n_pre) columns_of(it);
+            rows_of(it);
+        }
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -151,52 +196,14 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     if (warp == 0) {
         if (lane == 0) {
-            // ---------------- TMA producer ----------------
-            // columns of one row tile are read once: they leave L2 first
-            const uint64_t pol_c = p.tiles_m == 1 ? ptx::policy_evict_first() : ptx::policy_evict_normal();
-            const uint64_t pol_r = ptx::policy_evict_last();
-            const uint32_t tx = kColBytes + p.a_bytes;
-            auto columns_of = [&](int it) {
-                const int kb = kb0 + it, s = it % S, seg = kb >= p.kswitch;
-                const int k0 = (seg ? kb - p.kswitch : kb) * 64;
-                const uint32_t sc = sbase + s * kStage, fb = full_bar(s);
-                const CUtensorMap *m = &maps.m[p.b[seg][0]];
-                ptx::mbar_arrive_expect_tx(fb, tx);
-                if (EPI == kEpiGated) {
-                    ptx::tma_load_2d(sc, m, fb, col0, k0, pol_c);
-                    ptx::tma_load_2d(sc + 8192u, &maps.m[p.b[seg][1]], fb, col0, k0, pol_c);
-                } else if (c_mn) {
-                    ptx::tma_load_2d(sc, m, fb, col0, k0, pol_c);
-                    ptx::tma_load_2d(sc + 8192u, m, fb, col0 + 64, k0, pol_c);
-                } else {
-                    ptx::tma_load_2d(sc, m, fb, k0, col0, pol_c);
-                }
-            };
-            auto rows_of = [&](int it) {
-                const int kb = kb0 + it, s = it % S, seg = kb >= p.kswitch;
-                const int k0 = (seg ? kb - p.kswitch : kb) * 64;
-                const uint32_t sr = sbase + s * kStage + kColBytes, fb = full_bar(s);
-                const CUtensorMap *m = &maps.m[p.a[seg]];
-                if (r_mn) {
-#pragma unroll
-                    for (int j = 0; j < (BN < 64 ? 1 : BN / 64); ++j)
-                        ptx::tma_load_2d(sr + 8192u * j, m, fb, row0 + 64 * j, k0, pol_r);
-                } else {
-                    ptx::tma_load_2d(sr, m, fb, k0, row0, pol_r);
-                }
-            };
-            const int n_pre = chained && !r_mn ? min(total, S) : 0;
-            for (int it = 0; it < n_pre; ++it) columns_of(it);
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-            if (args.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-            int issued = 0;
-            for (int it = 0; it < total; ++it, ++issued) {
+            int issued = first;
+            for (; issued < copies; ++issued) {
+                const int it = issued;
                 if (!wait_phase(empty_bar(it % S), ((uint32_t)(it / S) & 1u) ^ 1u, args, &s_abort)) break;
-                if (args.test_stall && it == total - 1) break;  // test hook: it never arrives
-                if (it >= n_pre) columns_of(it);
+                columns_of(it);
                 rows_of(it);
             }
-            if (s_abort)  // let every copy that was issued whole land
+            if (s_abort)  // let every copy that was issued land
                 for (int it = issued > S ? issued - S : 0; it < issued; ++it)
                     wait_drain(full_bar(it % S), (uint32_t)(it / S) & 1u, args);
         }
@@ -272,16 +279,23 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint32_t at = sbase + (uint32_t)((x / kGroups) * kSmallTile + x % kGroups * 4) * 4u;
             float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
             if (x > i0 + e) epi_load<EPI>(ep, row_of(x), col_of(x), in);
-#pragma unroll 2
-            for (int j = 0; j < C; ++j) {
-                const uint32_t q = ptx::map_to_rank(at, (uint32_t)j);
-                const float4 f = ld_cluster_f4(q);
-                v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
-                if (EPI == kEpiGated) {
-                    const float4 h = ld_cluster_f4(q + kTileCols * 4u);
-                    u[0] += h.x, u[1] += h.y, u[2] += h.z, u[3] += h.w;
+            // every CTA's part is on its way before the first is added
+            float4 f[kSmallMaxSplits], h[EPI == kEpiGated ? kSmallMaxSplits : 1];
+#pragma unroll
+            for (int j = 0; j < kSmallMaxSplits; ++j)
+                if (j < C) {
+                    const uint32_t q = ptx::map_to_rank(at, (uint32_t)j);
+                    f[j] = ld_cluster_f4(q);
+                    if (EPI == kEpiGated) h[EPI == kEpiGated ? j : 0] = ld_cluster_f4(q + kTileCols * 4u);
                 }
-            }
+#pragma unroll
+            for (int j = 0; j < kSmallMaxSplits; ++j)
+                if (j < C) {
+                    v[0] += f[j].x, v[1] += f[j].y, v[2] += f[j].z, v[3] += f[j].w;
+                    if constexpr (EPI == kEpiGated) {
+                        u[0] += h[j].x, u[1] += h[j].y, u[2] += h[j].z, u[3] += h[j].w;
+                    }
+                }
             epilogue<EPI>(ep, row_of(x), col_of(x), v, u, in);
         }
     }
