@@ -15,6 +15,8 @@ constexpr int kDzMaxBlocks = 128;  // row blocks: partial sums a column
 // multiple of 8 (ld_dst is one).
 __global__ void __launch_bounds__(256) repack_kernel(const __grid_constant__ RepackArgs args) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // a product of the same call follows
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const auto &a = args.c[blockIdx.y];
     const uint16_t *src = static_cast<const uint16_t *>(a.src);
     uint16_t *dst = static_cast<uint16_t *>(a.dst);
@@ -47,8 +49,8 @@ __global__ void __launch_bounds__(256) repack_kernel(const __grid_constant__ Rep
 __global__ void __launch_bounds__(256) dz_kernel(const __grid_constant__ DzArgs a, int rows_per_block,
                                                  int vec) {
     __shared__ float s_sum[8][kDzCols];
-    if (threadIdx.x == 0 && a.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x == 0 && a.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * kDzCols + lane * 8;
     const int r1 = min(a.rows, (int)(blockIdx.y + 1) * rows_per_block);
@@ -125,8 +127,8 @@ constexpr int kSumWarps = 16;
 __global__ void __launch_bounds__(32 * kSumWarps)
     colsum_kernel(const float *part, int blocks, int n, void *out, int type, int trigger) {
     __shared__ float s_sum[kSumWarps][32];
-    if (threadIdx.x == 0 && trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x == 0 && trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float t = 0.f;

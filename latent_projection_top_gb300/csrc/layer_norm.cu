@@ -4,8 +4,7 @@
 //   dx = r (g - mean(g) - xh mean(g xh)),  g = dy gamma,  xh = (x - mean) r
 //   dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy
 //
-// A row is held in the registers of T threads (up to 32 values each), so x
-// and dy are read once and the variance is the sum of squared deviations
+// x and dy are read once, and the variance is the sum of squared deviations
 // from the mean, not a difference of large sums.  Sums are FP32.
 #include "layer.cuh"
 #include "layer_math.cuh"
@@ -14,89 +13,11 @@
 namespace route {
 namespace {
 
-constexpr int kV = 4;  // runs of eight values a thread
 constexpr int kMaxBlocks = 3;  // backward blocks an SM, at most
 
-// Where value e of run v of thread t sits in the row: whole 16-byte vectors
-// when rows are aligned for it, else one element a thread at a time.
-template <int T, bool VEC>
-__device__ __forceinline__ int col_of(int v, int e, int t) {
-    return VEC ? (v * T + t) * 8 + e : (v * 8 + e) * T + t;
-}
-
-template <int T, bool VEC>
-__device__ __forceinline__ void load_run(const void *p, int type, long long row, int v, int t,
-                                         int dim, float (&x)[8]) {
-    if constexpr (VEC) {
-        const int c = (v * T + t) * 8;
-        if (c < dim) {  // dim is a multiple of 8
-            if (type == kFp32) {
-                const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + row + c);
-                const float4 a = q[0], b = q[1];
-                x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-                x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-            } else {
-                const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + row + c);
-                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = unpack16(w[e], type);
-                    x[2 * e] = f.x, x[2 * e + 1] = f.y;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = 0.f;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int c = col_of<T, false>(v, e, t);
-            x[e] = c < dim ? load_elem(p, type, row + c) : 0.f;
-        }
-    }
-}
-
-template <int T, bool VEC>
-__device__ __forceinline__ void store_run(void *p, int type, long long row, int v, int t, int dim,
-                                          const float (&x)[8]) {
-    if constexpr (VEC) {
-        const int c = (v * T + t) * 8;
-        if (c >= dim) return;
-        if (type == kFp32) {
-            float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + row + c);
-            q[0] = make_float4(x[0], x[1], x[2], x[3]);
-            q[1] = make_float4(x[4], x[5], x[6], x[7]);
-        } else {
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + row + c) =
-                make_uint4(pack16(x[0], x[1], type), pack16(x[2], x[3], type),
-                           pack16(x[4], x[5], type), pack16(x[6], x[7], type));
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int c = col_of<T, false>(v, e, t);
-            if (c < dim) store_elem(p, type, row + c, x[e]);
-        }
-    }
-}
-
-// Sum over the T threads of a row, the same in every thread and every run.
-template <int T>
-__device__ __forceinline__ float row_sum(float v, float *scratch) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if constexpr (T > 32) {
-        const int w = threadIdx.x >> 5;
-        __syncthreads();  // the last sum has been read
-        if ((threadIdx.x & 31) == 0) scratch[w] = v;
-        __syncthreads();
-        v = 0.f;
-#pragma unroll
-        for (int i = 0; i < T / 32; ++i) v += scratch[i];
-    }
-    return v;
-}
+// Threads of a block and rows it holds, with up to t threads a row.
+__host__ __device__ constexpr int block_of(int t) { return t > 32 ? t : 128; }
+__host__ __device__ constexpr int rows_of(int t) { return block_of(t) / t; }
 
 // ---- rows aligned for 16-byte access: a ring of rows in shared memory --------
 //
@@ -266,8 +187,6 @@ __device__ __forceinline__ void copy_wait() {
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-__host__ __device__ constexpr int block_of(int t) { return t > 32 ? t : 128; }
-__host__ __device__ constexpr int rows_of(int t) { return block_of(t) / t; }
 
 // Blocks an SM and rows of a ring: up to ~190 KB of rows an SM.  `t`: the
 // most threads of a row that a kernel is made for.
@@ -484,133 +403,125 @@ __global__ void __launch_bounds__(block_of(MAXT), bwd_blocks(MAXT, TY))
     }
 }
 
-// ---- any alignment: one element at a time -------------------------------------
+// ---- any alignment: one element a thread at a time ------------------------------
+//
+// A row is held in the registers of T threads (up to 32 values each), thread
+// t's value i at column i T + t.
 
+template <int T, int TY>
+__device__ __forceinline__ void load_values(const void *p, long long row, int t, int dim, float (&x)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = i * T + t < dim ? load_elem(p, TY, row + i * T + t) : 0.f;
+}
+
+// Sum over the T threads of a row, the same in every thread and every run.
 template <int T>
-__global__ void __launch_bounds__(T > 32 ? T : 128)
-    norm_forward_kernel(const __grid_constant__ NormArgs a) {
+__device__ __forceinline__ float sum_of_row(float v, float *scratch) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if constexpr (T > 32) {
+        const int w = threadIdx.x >> 5;
+        __syncthreads();  // the last sum has been read
+        if ((threadIdx.x & 31) == 0) scratch[w] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < T / 32; ++i) v += scratch[i];
+    }
+    return v;
+}
+
+template <int T, int TY>
+__global__ void __launch_bounds__(block_of(T)) norm_forward_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float scratch[T / 32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int kRows = T > 32 ? 1 : 4;
     const int t = threadIdx.x % T;
-    const int r = blockIdx.x * kRows + threadIdx.x / T;
+    const int r = blockIdx.x * rows_of(T) + threadIdx.x / T;
     if (r >= a.rows) return;  // whole rows: every thread of a row
-    const long long row = (long long)r * a.ld_x;
-    float x[kV][8];
-    float s = 0.f;
+    float x[32], s = 0.f;
+    load_values<T, TY>(a.x, (long long)r * a.ld_x, t, a.dim, x);
 #pragma unroll
-    for (int v = 0; v < kV; ++v) {
-        load_run<T, false>(a.x, a.type, row, v, t, a.dim, x[v]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s += x[v][e];
-    }
+    for (int i = 0; i < 32; ++i) s += x[i];
     const float inv = 1.f / (float)a.dim;
-    const float mean = row_sum<T>(s, scratch) * inv;
+    const float mean = sum_of_row<T>(s, scratch) * inv;
     s = 0.f;
 #pragma unroll
-    for (int v = 0; v < kV; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[v][e] -= mean;
-            if (col_of<T, false>(v, e, t) < a.dim) s += x[v][e] * x[v][e];
-        }
-    const float rstd = 1.f / sqrtf(row_sum<T>(s, scratch) * inv + a.eps);
-    if (t == 0 && a.stats != nullptr) {
-        a.stats[2 * (long long)r] = mean;
-        a.stats[2 * (long long)r + 1] = rstd;
+    for (int i = 0; i < 32; ++i) {
+        x[i] -= mean;
+        if (i * T + t < a.dim) s += x[i] * x[i];
     }
+    const float rstd = 1.f / sqrtf(sum_of_row<T>(s, scratch) * inv + a.eps);
+    if (t == 0 && a.stats != nullptr)
+        *reinterpret_cast<float2 *>(a.stats + 2 * (long long)r) = make_float2(mean, rstd);
+    // eight columns' parameters before the first of their stores: a load does
+    // not move ahead of a store that might change it
 #pragma unroll
-    for (int v = 0; v < kV; ++v) {
+    for (int k = 0; k < 32; k += 8) {
         float g[8], b[8];
-        if (a.gamma != nullptr) {
-            load_run<T, false>(a.gamma, a.type, 0, v, t, a.dim, g);
-        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = 1.f;
-        }
-        if (a.beta != nullptr) {
-            load_run<T, false>(a.beta, a.type, 0, v, t, a.dim, b);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) b[e] = 0.f;
+        for (int i = 0; i < 8; ++i) {
+            const int c = (k + i) * T + t;
+            g[i] = a.gamma != nullptr && c < a.dim ? load_elem(a.gamma, TY, c) : 1.f;
+            b[i] = a.beta != nullptr && c < a.dim ? load_elem(a.beta, TY, c) : 0.f;
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[v][e] = x[v][e] * rstd * g[e] + b[e];
-        store_run<T, false>(a.y, a.type, (long long)r * a.ld_y, v, t, a.dim, x[v]);
+        for (int i = 0; i < 8; ++i) {
+            const int c = (k + i) * T + t;
+            if (c < a.dim) store_elem(a.y, TY, (long long)r * a.ld_y + c, x[k + i] * rstd * g[i] + b[i]);
+        }
     }
 }
 
-// Rows are dealt to `gridDim.x` blocks; a thread keeps the gain's and
-// offset's gradient sums of its own columns over its rows in registers and
-// writes them once, as one row of partials a block.
-template <int T>
-__global__ void __launch_bounds__(T > 32 ? T : 128)
-    norm_backward_kernel(const __grid_constant__ NormArgs a) {
-    constexpr int kRows = T > 32 ? 1 : 4;
+template <int T, int TY>
+__global__ void __launch_bounds__(block_of(T)) norm_backward_kernel(const __grid_constant__ NormArgs a) {
+    constexpr int kRows = rows_of(T);
     __shared__ float scratch[T / 32];
     __shared__ float s_acc[T > 32 ? 1 : kRows * 1024];
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int t = threadIdx.x % T, sub = threadIdx.x / T;
     const float inv = 1.f / (float)a.dim;
-    float dg[kV][8] = {}, db[kV][8] = {};
+    float dg[32] = {}, db[32] = {};
     for (int r = blockIdx.x * kRows + sub; r < a.rows; r += gridDim.x * kRows) {
         const float mean = a.stats[2 * (long long)r], rstd = a.stats[2 * (long long)r + 1];
-        float xh[kV][8], g[kV][8];
-        float s1 = 0.f, s2 = 0.f;
+        float xh[32], g[32], s1 = 0.f, s2 = 0.f;
+        load_values<T, TY>(a.x, (long long)r * a.ld_x, t, a.dim, xh);
+        load_values<T, TY>(a.dy, (long long)r * a.ld_dy, t, a.dim, g);
 #pragma unroll
-        for (int v = 0; v < kV; ++v) {
-            float gm[8];
-            load_run<T, false>(a.x, a.type, (long long)r * a.ld_x, v, t, a.dim, xh[v]);
-            load_run<T, false>(a.dy, a.type, (long long)r * a.ld_dy, v, t, a.dim, g[v]);
-            if (a.gamma != nullptr) {
-                load_run<T, false>(a.gamma, a.type, 0, v, t, a.dim, gm);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) gm[e] = 1.f;
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                xh[v][e] = (xh[v][e] - mean) * rstd;
-                dg[v][e] += g[v][e] * xh[v][e];
-                db[v][e] += g[v][e];
-                g[v][e] *= gm[e];  // zero past the row's end: dy is
-                s1 += g[v][e];
-                s2 += g[v][e] * xh[v][e];
-            }
+        for (int i = 0; i < 32; ++i) {
+            const float gm = a.gamma != nullptr && i * T + t < a.dim ? load_elem(a.gamma, TY, i * T + t) : 1.f;
+            xh[i] = (xh[i] - mean) * rstd;
+            dg[i] += g[i] * xh[i];
+            db[i] += g[i];
+            g[i] *= gm;  // zero past the row's end: dy is
+            s1 += g[i];
+            s2 += g[i] * xh[i];
         }
         if (a.dx == nullptr) continue;
-        s1 = row_sum<T>(s1, scratch) * inv;
-        s2 = row_sum<T>(s2, scratch) * inv;
+        s1 = sum_of_row<T>(s1, scratch) * inv;
+        s2 = sum_of_row<T>(s2, scratch) * inv;
 #pragma unroll
-        for (int v = 0; v < kV; ++v) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) g[v][e] = rstd * (g[v][e] - s1 - xh[v][e] * s2);
-            store_run<T, false>(a.dx, a.type, (long long)r * a.ld_dx, v, t, a.dim, g[v]);
-        }
+        for (int i = 0; i < 32; ++i)
+            if (i * T + t < a.dim)
+                store_elem(a.dx, TY, (long long)r * a.ld_dx + i * T + t, rstd * (g[i] - s1 - xh[i] * s2));
     }
     if (a.part == nullptr) return;
     float *part = a.part + (long long)blockIdx.x * 2 * a.dim;
     if constexpr (T > 32) {
 #pragma unroll
-        for (int v = 0; v < kV; ++v)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = col_of<T, false>(v, e, t);
-                if (c < a.dim) part[c] = dg[v][e], part[a.dim + c] = db[v][e];
-            }
+        for (int i = 0; i < 32; ++i) {
+            const int c = i * T + t;
+            if (c < a.dim) part[c] = dg[i], part[a.dim + c] = db[i];
+        }
     } else {
         // the block's rows meet in shared memory, gradient by gradient
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             __syncthreads();
 #pragma unroll
-            for (int v = 0; v < kV; ++v)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    s_acc[sub * 1024 + col_of<T, false>(v, e, t)] = k ? db[v][e] : dg[v][e];
+            for (int i = 0; i < 32; ++i) s_acc[sub * 1024 + i * T + t] = k ? db[i] : dg[i];
             __syncthreads();
-            for (int c = threadIdx.x; c < a.dim; c += 32 * kRows) {
+            for (int c = threadIdx.x; c < a.dim; c += block_of(T)) {
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < kRows; ++i) sum += s_acc[i * 1024 + c];
@@ -738,13 +649,24 @@ cudaError_t forward_aligned(const NormArgs &a, cudaStream_t stream) {
     }
 }
 
+
+template <int TY>
+cudaError_t forward_any(const NormArgs &a, cudaStream_t stream) {
+    const int t = threads_of(a.dim), grid = (a.rows + rows_of(t) - 1) / rows_of(t);
+    return launch_pdl(t == 32    ? norm_forward_kernel<32, TY>
+                      : t == 128 ? norm_forward_kernel<128, TY>
+                      : t == 256 ? norm_forward_kernel<256, TY>
+                                 : norm_forward_kernel<512, TY>,
+                      grid, block_of(t), 0, stream, a);
+}
+template <int TY>
 cudaError_t backward_any(const NormArgs &a, int *grid, cudaStream_t stream) {
     const int t = threads_of(a.dim);
-    *grid = blocks_for(a.rows, t, 2 * a.sms);
-    return launch_pdl(t == 32    ? norm_backward_kernel<32>
-                      : t == 128 ? norm_backward_kernel<128>
-                      : t == 256 ? norm_backward_kernel<256>
-                                 : norm_backward_kernel<512>,
+    *grid = blocks_for(a.rows, t, (t == 512 ? 1 : kMaxBlocks) * a.sms);
+    return launch_pdl(t == 32    ? norm_backward_kernel<32, TY>
+                      : t == 128 ? norm_backward_kernel<128, TY>
+                      : t == 256 ? norm_backward_kernel<256, TY>
+                                 : norm_backward_kernel<512, TY>,
                       *grid, block_of(t), 0, stream, a);
 }
 
@@ -763,18 +685,10 @@ cudaError_t backward_aligned(const NormArgs &a, int *grid, cudaStream_t stream) 
         case 256: return backward_ring<256, runs<TY>(4), TY>(a, grid, stream);
         default:
             if constexpr (kHasBackwardRing<512, TY>) return backward_ring<512, runs<TY>(4), TY>(a, grid, stream);
-            return backward_any(a, grid, stream);
+            return backward_any<TY>(a, grid, stream);
     }
 }
 
-cudaError_t forward_any(const NormArgs &a, cudaStream_t stream) {
-    const int t = threads_of(a.dim), grid = (a.rows + rows_of(t) - 1) / rows_of(t);
-    return launch_pdl(t == 32    ? norm_forward_kernel<32>
-                      : t == 128 ? norm_forward_kernel<128>
-                      : t == 256 ? norm_forward_kernel<256>
-                                 : norm_forward_kernel<512>,
-                      grid, block_of(t), 0, stream, a);
-}
 }  // namespace
 
 cudaError_t norm_configure() {
@@ -785,28 +699,36 @@ cudaError_t norm_configure() {
 
 size_t norm_part_floats(int dim, int sms) { return (size_t)kMaxBlocks * sms * 2 * dim; }
 
-cudaError_t norm_forward_launch(const NormArgs &a, cudaStream_t stream) {
-    const int es = layer_esize(a.type);
+template <int TY>
+static cudaError_t forward_typed(const NormArgs &a, cudaStream_t stream) {
+    const int es = layer_esize(TY);
     const bool vec = a.dim % 8 == 0 && rows_aligned(a.x, a.ld_x, es) && rows_aligned(a.y, a.ld_y, es) &&
                      rows_aligned(a.gamma, 0, es) && rows_aligned(a.beta, 0, es);
-    return !vec                ? forward_any(a, stream)
-           : a.type == kBf16 ? forward_aligned<kBf16>(a, stream)
-           : a.type == kFp16 ? forward_aligned<kFp16>(a, stream)
-                             : forward_aligned<kFp32>(a, stream);
+    return vec ? forward_aligned<TY>(a, stream) : forward_any<TY>(a, stream);
+}
+
+template <int TY>
+static cudaError_t backward_typed(const NormArgs &a, int *grid, cudaStream_t stream) {
+    const int es = layer_esize(TY);
+    const bool vec = a.dim % 8 == 0 && rows_aligned(a.x, a.ld_x, es) && rows_aligned(a.dy, a.ld_dy, es) &&
+                     rows_aligned(a.dx, a.ld_dx, es) && rows_aligned(a.gamma, 0, es);
+    return vec ? backward_aligned<TY>(a, grid, stream) : backward_any<TY>(a, grid, stream);
+}
+
+cudaError_t norm_forward_launch(const NormArgs &a, cudaStream_t stream) {
+    return a.type == kBf16   ? forward_typed<kBf16>(a, stream)
+           : a.type == kFp16 ? forward_typed<kFp16>(a, stream)
+                             : forward_typed<kFp32>(a, stream);
 }
 
 cudaError_t norm_backward_launch(const NormArgs &args, cudaStream_t stream) {
     NormArgs a = args;
-    const int es = layer_esize(a.type);
     const bool sums = a.dgamma != nullptr || a.dbeta != nullptr;
     if (!sums) a.part = nullptr;
-    const bool vec = a.dim % 8 == 0 && rows_aligned(a.x, a.ld_x, es) && rows_aligned(a.dy, a.ld_dy, es) &&
-                     rows_aligned(a.dx, a.ld_dx, es) && rows_aligned(a.gamma, 0, es);
     int grid = 0;
-    const cudaError_t e = !vec              ? backward_any(a, &grid, stream)
-                          : a.type == kBf16 ? backward_aligned<kBf16>(a, &grid, stream)
-                          : a.type == kFp16 ? backward_aligned<kFp16>(a, &grid, stream)
-                                            : backward_aligned<kFp32>(a, &grid, stream);
+    const cudaError_t e = a.type == kBf16   ? backward_typed<kBf16>(a, &grid, stream)
+                          : a.type == kFp16 ? backward_typed<kFp16>(a, &grid, stream)
+                                            : backward_typed<kFp32>(a, &grid, stream);
     if (e != cudaSuccess || !sums) return e;
     return launch_pdl(norm_sum_kernel, (2 * a.dim + 31) / 32, 32 * kSumWarps, 0, stream,
                       static_cast<const float *>(a.part), grid, a.dim, a.dgamma, a.dbeta, a.type);
