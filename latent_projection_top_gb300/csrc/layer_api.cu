@@ -237,17 +237,19 @@ Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
         const int cols = epi == kEpiGated ? kSmallTile / 2 : kSmallTile;
         long long tiles = 0;
         for (int i = 0; i < count; ++i) tiles += (long long)ceil_div(w[i].M, bn) * ceil_div(w[i].N, cols);
-        const double kb_us = (16384 + bn * 128) / 70e3, cta_us = 0.8;
+        const double cta_us = 0.8;
         for (int s = 1; s <= kSmallMaxSplits && s <= kmost; s *= 2) {
             if (tiles * s > 8192) break;
-            const double longest = ceil_div(kmost, s) * kb_us + cta_us;
-            double level = 0;
-            for (int i = 0; i < count; ++i)
-                level += (double)ceil_div(w[i].M, bn) * ceil_div(w[i].N, cols) * s *
-                         (ceil_div(w[i].kblocks(), s) * kb_us + cta_us) / p->sms;
-            const double t = 5.0 + (count > 1        ? level + 0.3 * longest
-                                    : longest > level ? longest
-                                                      : level);
+            double longest = 0, level = 0;
+            for (int i = 0; i < count; ++i) {
+                const int box = w[i].form != kFormTT && w[i].M < bn ? w[i].M : bn;
+                const double one = ceil_div(w[i].kblocks(), s) * (16384 + box * 128) / 70e3 + cta_us;
+                longest = longest < one ? one : longest;
+                level += (double)ceil_div(w[i].M, bn) * ceil_div(w[i].N, cols) * s * one / p->sms;
+            }
+            double t = count > 1 ? level + 0.3 * longest : longest > level ? longest : level;
+            // CTAs past two an SM start when others have left
+            t += 5.0 + 3.0 * (ceil_div(tiles * s, 2 * p->sms) - 1);
             if (t < t_best) t_best = t, best = {true, bn, {s, s, s, s}};
         }
     }
