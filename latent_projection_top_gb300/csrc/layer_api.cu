@@ -18,8 +18,27 @@
 using namespace route;
 
 namespace {
+
 enum LayerKind { kNorm, kLinear, kGated };
-}
+
+// How a launch covers its products: CTA-pair tiles of 256 x bn
+// (layer_gemm.cu), or 128-column tiles of bn rows (layer_small.cu), and the
+// splits of the contraction.
+struct Choice {
+    bool small;
+    int bn;
+    int splits[kGemmMaxProblems];  // of each product (small tiles: the same for all)
+    double us;                     // the estimate that it was chosen by
+};
+
+// What the last call of a kind chose, for its number of rows.
+enum ChoiceSlot { kSlotForward, kSlotDown, kSlotDGate, kSlotBackward, kSlotInput, kSlotWeights, kSlots };
+struct ChoiceMemo {
+    int rows;
+    Choice c;
+};
+
+}  // namespace
 
 struct route_layer {
     LayerKind kind;
@@ -34,6 +53,7 @@ struct route_layer {
     // offsets into scratch (0 size where the plan needs none)
     size_t o_part;     // split partials, or column-sum partials
     size_t o_x, o_w[3], o_dout, o_h, o_dg, o_du;
+    mutable ChoiceMemo memo[kSlots];
 };
 
 namespace {
@@ -157,15 +177,6 @@ struct Copies {
     }
 };
 
-// How a launch covers its products: CTA-pair tiles of 256 x bn
-// (layer_gemm.cu), or 128-column tiles of bn rows (layer_small.cu), and the
-// splits of the contraction.
-struct Choice {
-    bool small;
-    int bn;
-    int splits[kGemmMaxProblems];  // of each product (small tiles: the same for all)
-};
-
 // A product of a launch: its form, the rows and columns of its result (gated:
 // hidden columns), its contraction's terms and each one's length.
 struct Prod {
@@ -183,8 +194,8 @@ int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 // 0.30 us; the small tiles are bound by what an SM reads, about 70 bytes a
 // nanosecond.
 Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
-    Choice best = {false, 256, {1, 1, 1, 1}};
-    double t_best = 1e30;
+    Choice best = {false, 256, {1, 1, 1, 1}, 1e30};
+    double &t_best = best.us;
     int rows = 0, kmost = 0;
     bool tt = false;
     for (int i = 0; i < count; ++i) {
@@ -204,7 +215,7 @@ Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
         // No contraction is left longer than `part` of an equal share: without
         // splits, and with several sizes of them.
         for (double part : {0.0, 2.0, 1.0, 0.7, 0.5, 0.34, 0.25}) {
-            Choice c = {false, bn, {1, 1, 1, 1}};
+            Choice c = {false, bn, {1, 1, 1, 1}, 0};
             long long items = 0, split_items = 0;
             double longest = 0, t = 7.0;
             for (int i = 0; i < count; ++i) {
@@ -228,32 +239,43 @@ Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
                 const double level = work * kb_us / p->pairs + 0.35 * longest;
                 t += level > longest ? level : longest;
             }
-            if (t < t_best) t_best = t, best = c;
+            c.us = t;
+            if (t < t_best) best = c;
         }
     }
     {
-        int bn = tt ? 64 : 16;
-        while (bn < 128 && bn < rows) bn *= 2;
+        int need = tt ? 64 : 16;
+        while (need < 128 && need < rows) need *= 2;
         const int cols = epi == kEpiGated ? kSmallTile / 2 : kSmallTile;
-        long long tiles = 0;
-        for (int i = 0; i < count; ++i) tiles += (long long)ceil_div(w[i].M, bn) * ceil_div(w[i].N, cols);
-        const double cta_us = 0.8;
-        for (int s = 1; s <= kSmallMaxSplits && s <= kmost; s *= 2) {
-            if (tiles * s > 8192) break;
-            double longest = 0, level = 0;
-            for (int i = 0; i < count; ++i) {
-                const int box = w[i].form != kFormTT && w[i].M < bn ? w[i].M : bn;
-                const double one = ceil_div(w[i].kblocks(), s) * (16384 + box * 128) / 70e3 + cta_us;
-                longest = longest < one ? one : longest;
-                level += (double)ceil_div(w[i].M, bn) * ceil_div(w[i].N, cols) * s * one / p->sms;
+        // fewer rows a tile than there are: more CTAs for short contractions
+        for (int bn = tt ? 64 : 16; bn <= need; bn *= 2) {
+            long long tiles = 0;
+            for (int i = 0; i < count; ++i)
+                tiles += (long long)ceil_div(w[i].M, bn) * ceil_div(w[i].N, cols);
+            for (int s = 1; s <= kSmallMaxSplits && s <= kmost; s *= 2) {
+                if (tiles * s > 8192) break;
+                double longest = 0, level = 0;
+                for (int i = 0; i < count; ++i) {
+                    const int box = w[i].form != kFormTT && w[i].M < bn ? w[i].M : bn;
+                    const double one = ceil_div(w[i].kblocks(), s) * (16384 + box * 128) / 70e3 + 0.8 +
+                                       (epi == kEpiDGate ? 0.04 : 0.015) * box / s;
+                    longest = longest < one ? one : longest;
+                    level += (double)ceil_div(w[i].M, bn) * ceil_div(w[i].N, cols) * s * one / p->sms;
+                }
+                double t = count > 1 ? level + 0.3 * longest : longest > level ? longest : level;
+                // CTAs past two an SM start when others have left
+                t += 5.0 + 3.0 * (ceil_div(tiles * s, 2 * p->sms) - 1);
+                if (t < t_best) best = {true, bn, {s, s, s, s}, t};
             }
-            double t = count > 1 ? level + 0.3 * longest : longest > level ? longest : level;
-            // CTAs past two an SM start when others have left
-            t += 5.0 + 3.0 * (ceil_div(tiles * s, 2 * p->sms) - 1);
-            if (t < t_best) t_best = t, best = {true, bn, {s, s, s, s}};
         }
     }
     return best;
+}
+
+const Choice &choice_of(const route_layer *p, ChoiceSlot slot, int rows, int epi, const Prod *w, int count) {
+    ChoiceMemo &m = p->memo[slot];
+    if (m.rows != rows) m.c = choose(p, epi, w, count), m.rows = rows;
+    return m.c;
 }
 
 void set_tiles(GemmProblem &q, int tile_rows, int tile_cols, int pairs) {
@@ -306,13 +328,11 @@ void deal_items(GemmArgs &a, int pairs) {
 }
 
 // Launch `count` products with one epilogue and, when pair tiles are split,
-// the kernels that finish them.  `all`, `count_all`: the products that the
-// choice of tiles goes by.  `more`: another kernel of the call follows;
+// the kernels that finish them.  `more`: another kernel of the call follows;
 // `chained`: the one before is a product that does not write the B of this
 // launch's NT and NN products.
-route_status run(const route_layer *p, int epi, Prod *w, int count, const Prod *all, int count_all,
-                 bool chained, bool more, cudaStream_t stream) {
-    const Choice ch = choose(p, epi, all, count_all);
+route_status run(const route_layer *p, int epi, Prod *w, int count, const Choice &ch, bool chained,
+                 bool more, cudaStream_t stream) {
     GemmMaps maps;
     GemmArgs a;
     memset(&a, 0, offsetof(GemmArgs, first));
@@ -430,7 +450,7 @@ Prod product(const route_layer *p, int form, int M, int N, int K, const Operand 
 }
 
 // out[M, N] = act(A[M, K] W[K, N] + bias) + residual.
-route_status forward_product(const route_layer *p, const Operand &A, const Operand &W, int M, int K,
+route_status forward_product(const route_layer *p, ChoiceSlot slot, const Operand &A, const Operand &W, int M, int K,
                              int N, int act, const void *bias, const void *residual, int64_t ld_res,
                              void *out, int64_t ld_out, int out_type, float *saved, bool chained,
                              cudaStream_t stream) {
@@ -441,7 +461,35 @@ route_status forward_product(const route_layer *p, const Operand &A, const Opera
     w.e.act = act;
     w.e.saved = saved, w.e.ld_saved = up16(N);
     w.e.vec = vec_bits(out, w.e.ld_out, nullptr, residual, w.e.ld_res, out_type, bias);
-    return run(p, act == kActNone ? kEpiLinear : kEpiAct, &w, 1, &w, 1, chained, false, stream);
+    const int epi = act == kActNone ? kEpiLinear : kEpiAct;
+    return run(p, epi, &w, 1, choice_of(p, slot, M, epi, &w, 1), chained, false, stream);
+}
+
+// A backward pass's products: dx (all[0]) and the weights' gradients, those
+// whose result is wanted.  One launch, unless the contractions (over the
+// widths for dx, over the rows for the others) differ so much that no one
+// way to cut them suits both.  What is chosen goes by all of them, so that a
+// gradient's bits do not depend on which others are asked for.
+route_status backward_products(const route_layer *p, int rows, Prod *all, int count, bool chained,
+                               cudaStream_t stream) {
+    for (int i = 0; i < count; ++i) all[i].id = i;
+    const Choice &one = choice_of(p, kSlotBackward, rows, kEpiLinear, all, count);
+    const Choice &input = choice_of(p, kSlotInput, rows, kEpiLinear, all, 1);
+    const Choice &weights = choice_of(p, kSlotWeights, rows, kEpiLinear, all + 1, count - 1);
+    Prod w[kGemmMaxProblems];
+    int n = 0;
+    // a launch more costs about 2 us where the one before it hides its start
+    if (input.us + weights.us - 3.0 < one.us) {
+        Prod *dx = all[0].e.out ? all : nullptr;
+        for (int i = 1; i < count; ++i)
+            if (all[i].e.out) w[n] = all[i], w[n++].id = i - 1;
+        route_status st;
+        if (dx && (st = run(p, kEpiLinear, dx, 1, input, chained, n > 0, stream)) != ROUTE_OK) return st;
+        return n ? run(p, kEpiLinear, w, n, weights, false, false, stream) : ROUTE_OK;
+    }
+    for (int i = 0; i < count; ++i)
+        if (all[i].e.out) w[n++] = all[i];
+    return n ? run(p, kEpiLinear, w, n, one, chained, false, stream) : ROUTE_OK;
 }
 
 route_status zero_matrix(void *p, int64_t ld, int rows, int cols, int esize, cudaStream_t stream) {
@@ -729,7 +777,7 @@ route_status route_linear_forward(const route_layer *p, int rows, const void *x,
     const Operand ox = copies.operand(x, ld_x, rows, p->k, p->o_x);
     const Operand ow = copies.operand(W, ld_W, p->k, p->n, p->o_w[0]);
     if ((st = copies.launch(s)) != ROUTE_OK) return st;
-    return forward_product(p, ox, ow, rows, p->k, p->n, p->act, bias, residual, ld_residual, out,
+    return forward_product(p, kSlotForward, ox, ow, rows, p->k, p->n, p->act, bias, residual, ld_residual, out,
                            ld_out, p->out_type, static_cast<float *>(saved), false, s);
 }
 
@@ -778,21 +826,14 @@ route_status route_linear_backward(const route_layer *p, int rows, const void *d
         if (e != cudaSuccess) return cuda_fail(e, "pre-activation gradient kernel launch");
     }
     if (!dx && !dW) return ROUTE_OK;
-    // dx = dz W^T and dW = x^T dz, in one launch
+    // dx = dz W^T and dW = x^T dz
     Copies copies(p);
     const Operand ox = dW ? copies.operand(x, ld_x, rows, p->k, p->o_x) : Operand{nullptr, 0};
     const Operand ow = dx ? copies.operand(W, ld_W, p->k, p->n, p->o_w[0]) : Operand{nullptr, 0};
     if ((st = copies.launch(s)) != ROUTE_OK) return st;
-    // both, for the choice of tiles: a gradient's bits do not depend on
-    // whether the other is asked for
     Prod all[2] = {product(p, kFormNN, rows, p->k, p->n, dz, ow, dx, ld_dx, p->type),
-                         product(p, kFormTT, p->k, p->n, rows, ox, dz, dW, ld_dW, p->type)};
-    all[1].id = 1;
-    Prod w[2];
-    int count = 0;
-    if (dx) w[count++] = all[0];
-    if (dW) w[count++] = all[1];
-    return run(p, kEpiLinear, w, count, all, 2, false, false, s);
+                   product(p, kFormTT, p->k, p->n, rows, ox, dz, dW, ld_dW, p->type)};
+    return backward_products(p, rows, all, 2, false, s);
 }
 
 route_status route_gated_forward(const route_layer *p, int rows, const void *x, int64_t ld_x,
@@ -829,8 +870,8 @@ route_status route_gated_forward(const route_layer *p, int rows, const void *x, 
     w.e.act = p->act;
     w.e.saved = static_cast<float *>(saved), w.e.ld_saved = ldf;
     w.e.saved2 = saved ? w.e.saved + (size_t)rows * ldf : nullptr;
-    if ((st = run(p, kEpiGated, &w, 1, &w, 1, false, true, s)) != ROUTE_OK) return st;
-    return forward_product(p, {h, ldf}, od, rows, p->f, p->n, kActNone, nullptr, residual,
+    if ((st = run(p, kEpiGated, &w, 1, choice_of(p, kSlotForward, rows, kEpiGated, &w, 1), false, true, s)) != ROUTE_OK) return st;
+    return forward_product(p, kSlotDown, {h, ldf}, od, rows, p->f, p->n, kActNone, nullptr, residual,
                            ld_residual, out, ld_out, p->type, nullptr, true, s);
 }
 
@@ -887,25 +928,16 @@ route_status route_gated_backward(const route_layer *p, int rows, const void *do
         w.e.act = p->act;
         w.e.saved = static_cast<float *>(const_cast<void *>(saved)), w.e.ld_saved = ldf;
         w.e.saved2 = w.e.saved + (size_t)rows * ldf;
-        if ((st = run(p, kEpiDGate, &w, 1, &w, 1, false, dx || weights, s)) != ROUTE_OK) return st;
+        if ((st = run(p, kEpiDGate, &w, 1, choice_of(p, kSlotDGate, rows, kEpiDGate, &w, 1), false, dx || weights, s)) != ROUTE_OK) return st;
     }
-    // dx = dgate W_gate^T + dup W_up^T and the weights' gradients, in one
-    // launch; the choice of tiles goes by all four, so that a gradient's bits
-    // do not depend on which others are asked for
+    // dx = dgate W_gate^T + dup W_up^T and the weights' gradients
     const Operand h = {static_cast<const uint8_t *>(saved) + saved_h(p, rows), ldf};
     Prod all[4] = {product(p, kFormNN, rows, p->k, p->f, dg, og, dx, ld_dx, p->type),
                    product(p, kFormTT, p->k, p->f, rows, ox, dg, dW_gate, ld_dgate, p->type),
                    product(p, kFormTT, p->k, p->f, rows, ox, du, dW_up, ld_dup, p->type),
                    product(p, kFormTT, p->f, p->n, rows, h, dy, dW_down, ld_ddown, p->type)};
     all[0].terms = 2, all[0].a[1] = du, all[0].b[1] = ou;
-    for (int i = 0; i < 4; ++i) all[i].id = i;
-    Prod w[4];
-    int count = 0;
-    if (dx) w[count++] = all[0];
-    if (dW_gate) w[count++] = all[1];
-    if (dW_up) w[count++] = all[2];
-    if (dW_down) w[count++] = all[3];
-    return run(p, kEpiLinear, w, count, all, 4, pre, false, s);
+    return backward_products(p, rows, all, 4, pre, s);
 }
 
 }  // extern "C"

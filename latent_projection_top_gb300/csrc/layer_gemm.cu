@@ -236,7 +236,9 @@ __device__ __forceinline__ bool mma_tile(Stages<BN> &st, int kblocks, uint32_t d
     return true;
 }
 
-template <int FORM, int EPI, int BN>
+// WIDE: rows of the result are accessed four columns at a time (else one; a
+// kernel of its own, for the registers).
+template <int FORM, int EPI, int BN, bool WIDE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1)
     layer_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs args) {
     constexpr int S = stages_of(BN);
@@ -387,7 +389,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
             auto col_of = [&](int b) { return c0 + b / kGroupBatches * kG + lane % kLanesRow * 4; };
             GroupIn<EPI, kBatch> in, next;
             // the first inputs go out before the tile's sums are complete
-            if (whole) group_load<EPI, kBatch>(p, r0 + row_of(0), col_of(0), kStep, in);
+            if (WIDE && whole) group_load<EPI, kBatch>(p, r0 + row_of(0), col_of(0), kStep, in);
             // one warp polls, the others sleep at the barrier
             const bool ok = warp != 2 || wait_phase(tfull_bar(t), ((uint32_t)job >> 1) & 1u, args, &s_abort);
             if (!ptx::named_bar_and(1, 32 * kEpiWarps, ok)) break;
@@ -419,6 +421,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
                                  : "r"(unit(row + j * kStep, lane % kLanesRow) + half)
                                  : "memory");
             };
+            if (!WIDE && whole) {  // rows of odd widths: a column a thread
+                constexpr int kRows = EPI == kEpiDGate ? 4 : 8;
+#pragma unroll 1
+                for (int g = 0; g < kWarpCols / kG; ++g) {
+                    __syncwarp();  // the last group has been read
+                    put(acc + (uint32_t)(g * kG), 0u);
+                    if (EPI == kEpiGated) put(acc + (uint32_t)(g * kG) + kTileCols, kHalfTurn);
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (g + 1 == kWarpCols / kG && lane == 0) {  // everything has left TMEM
+                        if (leader)
+                            ptx::mbar_arrive(tempty_bar(t));
+                        else
+                            ptx::mbar_arrive_remote(ptx::map_to_rank(tempty_bar(t), 0u));
+                    }
+                    const int c = c0 + g * kG + lane;
+#pragma unroll 1
+                    for (int r = 0; r < 32; r += kRows) {
+                        ColumnIn<EPI, kRows> in;
+                        column_load<EPI, kRows>(p, r0 + r, c, 1, in);
+                        float v[kRows], u[EPI == kEpiGated ? kRows : 1];
+#pragma unroll
+                        for (int j = 0; j < kRows; ++j) {
+                            const uint32_t at = unit(r + j, lane >> 2) + (lane & 3) * 4u;
+                            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[j]) : "r"(at) : "memory");
+                            if constexpr (EPI == kEpiGated)
+                                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(u[j]) : "r"(at + kHalfTurn) : "memory");
+                        }
+                        column_epilogue<EPI, kRows>(p, r0 + r, c, 1, v, u, in);
+                    }
+                }
+                continue;
+            }
 #pragma unroll 1
             for (int b = 0; b < kBatches; ++b) {
                 if (b % kGroupBatches == 0) {
@@ -435,13 +470,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
                             ptx::mbar_arrive_remote(ptx::map_to_rank(tempty_bar(t), 0u));
                     }
                 }
-                if (kAhead && whole && b + 1 < kBatches)
+                if (WIDE && kAhead && whole && b + 1 < kBatches)
                     group_load<EPI, kBatch>(p, r0 + row_of(b + 1), col_of(b + 1), kStep, next);
                 float v[4 * kBatch], u[EPI == kEpiGated ? 4 * kBatch : 1];
                 get(row_of(b), 0u, v);
                 if constexpr (EPI == kEpiGated) get(row_of(b), kHalfTurn, u);
                 const int r = r0 + row_of(b), c = col_of(b);
-                if (whole) {
+                if (WIDE && whole) {
                     group_epilogue<EPI, kBatch>(p, r, c, kStep, v, u, in);
                 } else if (c < p.N) {  // partials: rows padded to whole groups
                     float *part = p.part + (long long)w.split * p.M * p.ld_part;
@@ -508,11 +543,13 @@ cudaError_t launch_chained(const void *fn, dim3 grid, dim3 block, size_t smem, v
     return cudaLaunchKernelExC(&c, fn, params);
 }
 
-const void *kernel_of(int form, int epi, int bn) {
-#define ROUTE_GEMM(F, E)                                                            \
-    if (form == F && epi == E)                                                      \
-        return bn == 256 ? reinterpret_cast<const void *>(layer_gemm_kernel<F, E, 256>) \
-                         : reinterpret_cast<const void *>(layer_gemm_kernel<F, E, 128>);
+const void *kernel_of(int form, int epi, int bn, bool wide) {
+#define ROUTE_GEMM(F, E)                                                                       \
+    if (form == F && epi == E)                                                                 \
+        return bn == 256 ? (wide ? reinterpret_cast<const void *>(layer_gemm_kernel<F, E, 256, true>)   \
+                                 : reinterpret_cast<const void *>(layer_gemm_kernel<F, E, 256, false>)) \
+                         : (wide ? reinterpret_cast<const void *>(layer_gemm_kernel<F, E, 128, true>)   \
+                                 : reinterpret_cast<const void *>(layer_gemm_kernel<F, E, 128, false>));
     ROUTE_GEMM(kFormNT, kEpiLinear)
     ROUTE_GEMM(kFormNT, kEpiAct)
     ROUTE_GEMM(kFormNT, kEpiGated)
@@ -528,11 +565,12 @@ cudaError_t gemm_configure() {
     for (int form : {kFormNT, kFormNN, kFormMixed})
         for (int epi = 0; epi < kEpiCount; ++epi)
             for (int bn : {256, 128})
-                if (const void *k = kernel_of(form, epi, bn)) {
-                    const cudaError_t e = cudaFuncSetAttribute(
-                        k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(bn));
-                    if (e != cudaSuccess) return e;
-                }
+                for (bool wide : {false, true})
+                    if (const void *k = kernel_of(form, epi, bn, wide)) {
+                        const cudaError_t e = cudaFuncSetAttribute(
+                            k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(bn));
+                        if (e != cudaSuccess) return e;
+                    }
     return cudaSuccess;
 }
 
@@ -540,7 +578,9 @@ int gemm_smem_bytes() { return (int)(smem_of(256) > smem_of(128) ? smem_of(256) 
 
 cudaError_t gemm_launch(int form, int epi, int bn, const GemmMaps &maps, const GemmArgs &args,
                         cudaStream_t stream) {
-    const void *k = kernel_of(form, epi, bn);
+    bool wide = true;
+    for (int i = 0; i < args.nprob; ++i) wide = wide && (args.p[i].e.vec & kVecOut);
+    const void *k = kernel_of(form, epi, bn, wide);
     if (k == nullptr || args.pairs <= 0 || args.items <= 0) return cudaErrorInvalidConfiguration;
     void *params[] = {const_cast<GemmMaps *>(&maps), const_cast<GemmArgs *>(&args)};
     return launch_chained(k, dim3(2 * args.pairs), dim3(gemm_threads(epi)), smem_of(bn), params, stream);

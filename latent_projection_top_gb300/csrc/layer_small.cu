@@ -94,6 +94,12 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ float ld_cluster_f(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 template <int EPI, int BN>
 __global__ void __launch_bounds__(kThreads, 2)
     layer_small_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs args,
@@ -243,21 +249,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int e = (int)threadIdx.x - 64;  // epilogue thread
     const Epilogue ep = p.e;
     const int rows = min(BN, ep.M - row0);
-    constexpr int kGroups = kTileCols / 4;  // a thread's item: 4 columns of a row
-    const int items = rows * kGroups;
-    const int i0 = items * rank / C, i1 = items * (rank + 1) / C;
-    auto row_of = [&](int x) { return row0 + x / kGroups; };
-    auto col_of = [&](int x) { return col0 + x % kGroups * 4; };
-    EpiIn<EPI> in;
+    // A thread's item is G columns of a row, neighbouring threads on
+    // neighbouring columns: four, or one where rows cannot be accessed four
+    // values at a time.  The cluster's CTAs share a tile's items.
+    const bool wide = (ep.vec & kVecOut) != 0;
+    float *sums = reinterpret_cast<float *>(smem_raw + (sbase - raw));
     if (warp >= 2) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (i0 + e < i1) epi_load<EPI>(ep, row_of(i0 + e), col_of(i0 + e), in);
         ok = wait_phase(done_bar, 0u, args, &s_abort) && !s_abort;
         __syncwarp();
         ptx::tc_fence_after();
         // the stages are free: this CTA's sums go there, [row][128 columns]
         const int lq = warp & 3, cs = (warp - 2) >> 2;
-        float *sums = reinterpret_cast<float *>(smem_raw + (sbase - raw));
 #pragma unroll 1
         for (int r = cs * 16; r < rows; r += 32) {
             uint32_t v[16];
@@ -274,11 +277,18 @@ __global__ void __launch_bounds__(kThreads, 2)
         ptx::cluster_sync();
     else
         __syncthreads();
-    if (warp >= 2 && ok) {
+    if (warp >= 2 && ok && wide) {
+        constexpr int kGroups = kTileCols / 4;
+        const int items = rows * kGroups;
+        const int i0 = items * rank / C, i1 = items * (rank + 1) / C;
+        auto row_of = [&](int x) { return row0 + x / kGroups; };
+        auto col_of = [&](int x) { return col0 + x % kGroups * 4; };
+        EpiIn<EPI> in, next;
+        if (i0 + e < i1) epi_load<EPI>(ep, row_of(i0 + e), col_of(i0 + e), in);
         for (int x = i0 + e; x < i1; x += kEpiThreads) {
             const uint32_t at = sbase + (uint32_t)((x / kGroups) * kSmallTile + x % kGroups * 4) * 4u;
             float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
-            if (x > i0 + e) epi_load<EPI>(ep, row_of(x), col_of(x), in);
+            if (x + kEpiThreads < i1) epi_load<EPI>(ep, row_of(x + kEpiThreads), col_of(x + kEpiThreads), next);
             // every CTA's part is on its way before the first is added
             float4 f[kSmallMaxSplits], h[EPI == kEpiGated ? kSmallMaxSplits : 1];
 #pragma unroll
@@ -297,6 +307,32 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                 }
             epilogue<EPI>(ep, row_of(x), col_of(x), v, u, in);
+            in = next;
+        }
+    } else if (warp >= 2 && ok) {
+        // a thread's rows of one column, kRows of them at a time
+        constexpr int kRows = EPI == kEpiGated || EPI == kEpiDGate ? 2 : 4;
+        constexpr int kStep = kEpiThreads / kTileCols;  // rows that the threads cover at once
+        const int rows0 = rows * rank / C, rows1 = rows * (rank + 1) / C;
+        const int c = e % kTileCols;
+        for (int r = rows0 + e / kTileCols; r < rows1; r += kStep * kRows) {
+            ColumnIn<EPI, kRows> in;
+            column_load<EPI, kRows>(ep, row0 + r, col0 + c, kStep, in);
+            float v[kRows] = {}, u[EPI == kEpiGated ? kRows : 1] = {};
+            for (int j = 0; j < C; ++j) {
+                const uint32_t q = ptx::map_to_rank(sbase + (uint32_t)(r * kSmallTile + c) * 4u, (uint32_t)j);
+#pragma unroll
+                for (int k = 0; k < kRows; ++k)
+                    if (r + k * kStep < rows1) {
+                        v[k] += ld_cluster_f(q + (uint32_t)(k * kStep * kSmallTile) * 4u);
+                        if constexpr (EPI == kEpiGated)
+                            u[k] += ld_cluster_f(q + (uint32_t)(k * kStep * kSmallTile + kTileCols) * 4u);
+                    }
+            }
+            // rows of other CTAs' shares are not this one's to write
+            Epilogue own = ep;
+            own.M = row0 + rows1;
+            column_epilogue<EPI, kRows>(own, row0 + r, col0 + c, kStep, v, u, in);
         }
     }
     if (warp == 1) {
