@@ -205,7 +205,7 @@ Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
     }
     for (int bn : {256, 128}) {
         const int cols = epi == kEpiGated ? bn / 2 : bn;
-        const double kb_us = bn == 256 ? 0.34 : 0.30;
+        const double kb_us = bn == 256 ? 0.34 : 0.30, drain_us = bn == 256 ? 4.0 : 2.2;
         long long tiles[kGemmMaxProblems];
         double work = 0;
         for (int i = 0; i < count; ++i) {
@@ -217,7 +217,7 @@ Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
         for (double part : {0.0, 2.0, 1.0, 0.7, 0.5, 0.34, 0.25}) {
             Choice c = {false, bn, {1, 1, 1, 1}, 0};
             long long items = 0, split_items = 0;
-            double longest = 0, t = 7.0;
+            double longest = 0, level = 0, t = 7.0;
             for (int i = 0; i < count; ++i) {
                 int s = part > 0 ? (int)(w[i].kblocks() * p->pairs / (work * part) + 0.99) : 1;
                 s = s > kGemmMaxSplits ? kGemmMaxSplits : s;
@@ -225,18 +225,21 @@ Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
                 s = s < 1 ? 1 : s;
                 c.splits[i] = s;
                 items += tiles[i] * s;
-                const double one = ceil_div(w[i].kblocks(), s) * kb_us;
+                double one = ceil_div(w[i].kblocks(), s) * kb_us;
                 longest = longest < one ? one : longest;
+                // a tile's epilogue hides behind the next one's k-blocks
+                one = one < drain_us ? drain_us : one;
+                level += (double)tiles[i] * s * one / p->pairs;
                 if (s > 1) {
                     split_items += tiles[i] * s;
                     t += 2.5 + (double)w[i].M * w[i].N * (epi == kEpiGated ? 2 : 1) * 4.0 * (s + 1) / 4e6;
                 }
             }
             if (split_items > 2 * p->pairs) continue;
-            if (count == 1) {
-                t += ceil_div(items, p->pairs) * longest;  // equal items
+            if (count == 1) {  // equal items
+                t += longest + (ceil_div(items, p->pairs) - 1) * (longest < drain_us ? drain_us : longest);
             } else {
-                const double level = work * kb_us / p->pairs + 0.35 * longest;
+                level += 0.35 * longest;
                 t += level > longest ? level : longest;
             }
             c.us = t;
@@ -257,12 +260,20 @@ Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
                 double longest = 0, level = 0;
                 for (int i = 0; i < count; ++i) {
                     const int box = w[i].form != kFormTT && w[i].M < bn ? w[i].M : bn;
-                    const double one = ceil_div(w[i].kblocks(), s) * (16384 + box * 128) / 70e3 + 0.8 +
-                                       (epi == kEpiDGate ? 0.04 : 0.015) * box / s;
+                    const double kb = ceil_div(w[i].kblocks(), s) * (16384 + box * 128) / 70e3;
+                    const double drain = (epi == kEpiDGate ? 0.04 : 0.015) * box / s;
+                    double one = kb + 0.8 + drain;
                     longest = longest < one ? one : longest;
-                    level += (double)ceil_div(w[i].M, bn) * ceil_div(w[i].N, cols) * s * one / p->sms;
+                    // two CTAs of an SM hide each other's start and end, not more
+                    const double half = 0.5 * (6.5 + kb + drain);
+                    one = one < half ? half : one;
+                    const long long ctas = (long long)ceil_div(w[i].M, bn) * ceil_div(w[i].N, cols) * s;
+                    level += (double)ctas * one / p->sms;
                 }
-                double t = count > 1 ? level + 0.3 * longest : longest > level ? longest : level;
+                // one round of CTAs is as long as the longest of them
+                if (tiles * s <= p->sms) level = 0;
+                double t = count > 1 && level > 0 ? level + 0.3 * longest : longest;
+                t = t < longest ? longest : t < level ? level : t;
                 // CTAs past two an SM start when others have left
                 t += 5.0 + 3.0 * (ceil_div(tiles * s, 2 * p->sms) - 1);
                 if (t < t_best) best = {true, bn, {s, s, s, s}, t};
@@ -478,8 +489,8 @@ route_status backward_products(const route_layer *p, int rows, Prod *all, int co
     const Choice &weights = choice_of(p, kSlotWeights, rows, kEpiLinear, all + 1, count - 1);
     Prod w[kGemmMaxProblems];
     int n = 0;
-    // a launch more costs about 2 us where the one before it hides its start
-    if (input.us + weights.us - 3.0 < one.us) {
+    // (the second launch's start hides behind the first)
+    if (input.us + weights.us - 1.0 < one.us) {
         Prod *dx = all[0].e.out ? all : nullptr;
         for (int i = 1; i < count; ++i)
             if (all[i].e.out) w[n] = all[i], w[n++].id = i - 1;

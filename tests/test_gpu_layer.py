@@ -428,3 +428,178 @@ def test_refusals_of_tensors():
             route.linear_backward(plan, out, x, W, dx=torch.empty_like(x))
     with pytest.raises(route.RouteError, match="closed"):
         route.linear_forward(plan, x, W, out)
+
+
+# ---- the ways products are cut ----------------------------------------------------
+
+def _random_shapes(seed, count, odd):
+    import random
+    r = random.Random(seed)
+
+    def width():
+        w = int(2 ** r.uniform(2, 10.4))
+        return (w | 1) if odd else max(8, w // 8 * 8)
+    return [(int(2 ** r.uniform(0, 11)), width(), width(), width()) for _ in range(count)]
+
+
+@pytest.mark.parametrize("odd", [False, True])
+@pytest.mark.parametrize("dt", [BF16, FP16])
+def test_linear_over_many_shapes(dt, odd):
+    """Shapes over the ranges where tile, split and launch choices change."""
+    for i, (rows, k, n, _) in enumerate(_random_shapes(3 + odd, 24, odd)):
+        act = route.ACTIVATIONS[i % len(route.ACTIVATIONS)]
+        x, W = normal(i, rows, k, dt=dt), normal(i + 1, k, n, scale=k ** -0.5, dt=dt)
+        b, res, dout = normal(i + 2, n, dt=dt), normal(i + 3, rows, n, dt=dt), normal(i + 4, rows, n, dt=dt)
+        with route.LinearPlan(rows, k, n, dt, act=act, train=True) as plan:
+            saved = plan.new_saved()
+            out, g0 = blank(rows, n, dt)
+            dx, g1 = blank(rows, k, dt)
+            dW, g2 = blank(k, n, dt)
+            db = torch.full((n,), float("nan"), dtype=dt, device=DEV)
+            route.linear_forward(plan, x, W, out, bias=b, residual=res, saved=saved)
+            route.linear_backward(plan, dout, x, W, saved=saved, dx=dx, dW=dW, dbias=db)
+            plan.status()
+        want, z = ref.linear(x, W, b, res, act, dt)
+        grads = ref.linear_grads(x, W, z, dout, act, dt)
+        for name, got, w in (("out", out, want), ("dx", dx, grads["dx"]), ("dW", dW, grads["dW"]),
+                             ("dbias", db, grads["dbias"])):
+            check(f"{name} of {rows}x{k}x{n} {act}", got, w)
+        for g in (g0, g1, g2):
+            g()
+
+
+@pytest.mark.parametrize("odd", [False, True])
+def test_gated_over_many_shapes(odd):
+    dt = BF16
+    for i, (rows, k, f, n) in enumerate(_random_shapes(7 + odd, 16, odd)):
+        act = route.ACTIVATIONS[i % len(route.ACTIVATIONS)]
+        x = normal(i, rows, k, dt=dt)
+        Wg, Wu = (normal(i + j, k, f, scale=k ** -0.5, dt=dt) for j in (1, 2))
+        Wd, dout = normal(i + 3, f, n, scale=f ** -0.5, dt=dt), normal(i + 4, rows, n, dt=dt)
+        with route.GatedPlan(rows, k, f, n, dt, act=act, train=True) as plan:
+            saved = plan.new_saved()
+            out, g0 = blank(rows, n, dt)
+            outs = {"dx": blank(rows, k, dt), "dW_gate": blank(k, f, dt), "dW_up": blank(k, f, dt),
+                    "dW_down": blank(f, n, dt)}
+            route.gated_forward(plan, x, Wg, Wu, Wd, out, saved=saved)
+            route.gated_backward(plan, dout, x, Wg, Wu, Wd, saved, **{m: v[0] for m, v in outs.items()})
+            plan.status()
+        want, kept = ref.gated(x, Wg, Wu, Wd, None, act, dt)
+        check(f"out of {rows}x{k}x{f}x{n} {act}", out, want)
+        grads = ref.gated_grads(x, Wg, Wu, Wd, kept, dout, act, dt)
+        for m, (got, guard) in outs.items():
+            check(f"{m} of {rows}x{k}x{f}x{n} {act}", got, grads[m])
+            guard()
+        g0()
+
+
+def test_fewer_rows_than_the_plan_and_choices_by_row_count():
+    """One plan, calls of many row counts in turn: each as on its own plan."""
+    k, n, dt = 264, 520, BF16
+    W = normal(1, k, n, scale=k ** -0.5)
+    with route.LinearPlan(3000, k, n, dt, act="silu", train=True) as plan:
+        for rows in (3000, 1, 700, 17, 3000, 129, 1):
+            x, dout = normal(rows, rows, k), normal(rows + 1, rows, n)
+            outs = []
+            for p in (plan, route.LinearPlan(rows, k, n, dt, act="silu", train=True)):
+                saved = p.new_saved(rows)
+                o = [torch.full(s, float("nan"), dtype=dt, device=DEV) for s in ((rows, n), (rows, k), (k, n))]
+                route.linear_forward(p, x, W, o[0], saved=saved)
+                route.linear_backward(p, dout, x, W, saved=saved, dx=o[1], dW=o[2])
+                p.status()
+                outs.append(o)
+            assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+def test_results_do_not_depend_on_what_else_is_asked_for_or_ran():
+    """Bits of each gradient alone and with the others, and of repeated calls."""
+    for rows, k, n in ((6, 896, 448), (300, 200, 1032), (2050, 128, 904), (5000, 72, 40)):
+        x, W = normal(1, rows, k), normal(2, k, n, scale=k ** -0.5)
+        dout = normal(3, rows, n)
+        with route.LinearPlan(rows, k, n, BF16, train=True) as plan:
+            dx, dW = torch.empty_like(x), torch.empty_like(W)
+            route.linear_backward(plan, dout, x, W, dx=dx, dW=dW)
+            for _ in range(2):
+                a, b = torch.empty_like(x), torch.empty_like(W)
+                route.linear_backward(plan, dout, None, W, dx=a)
+                route.linear_backward(plan, dout, x, None, dW=b)
+                plan.status()
+                assert torch.equal(a, dx) and torch.equal(b, dW)
+
+
+def test_offsets_past_32_bits():
+    """A result of more than 2^31 elements (5.2 GB): its last rows."""
+    rows, k, n = 65536, 64, 40000
+    x, W = normal(1, rows, k), normal(2, k, n, scale=k ** -0.5)
+    out = torch.full((rows, n), float("nan"), dtype=BF16, device=DEV)
+    with route.LinearPlan(rows, k, n, BF16) as plan:
+        route.linear_forward(plan, x, W, out)
+        plan.status()
+    for at in (0, 53686, rows - 40):
+        want, _ = ref.linear(x[at:at + 40], W, None, None, "none", BF16)
+        check(f"rows {at}", out[at:at + 40], want)
+    assert not bool(torch.isnan(out[:, ::4999]).any())
+
+
+def test_operands_that_share_memory():
+    """The same tensor as two weights, and weights that start at one address
+    with other shapes."""
+    rows, k = 40, 128
+    x, W = normal(1, rows, k), normal(2, k, k, scale=k ** -0.5)
+    out = torch.empty((rows, k), dtype=BF16, device=DEV)
+    with route.GatedPlan(rows, k, k, k, BF16, train=True) as plan:
+        saved = plan.new_saved()
+        route.gated_forward(plan, x, W, W, W, out, saved=saved)
+        dx = torch.empty_like(x)
+        dW = [torch.empty_like(W) for _ in range(3)]
+        route.gated_backward(plan, x, x, W, W, W, saved, dx=dx, dW_gate=dW[0], dW_up=dW[1], dW_down=dW[2])
+        plan.status()
+    want, kept = ref.gated(x, W, W, W, None, "silu", BF16)
+    check("out", out, want)
+    grads = ref.gated_grads(x, W, W, W, kept, x, "silu", BF16)
+    for got, name in zip((dx, *dW), ("dx", "dW_gate", "dW_up", "dW_down")):
+        check(name, got, grads[name])
+    # W_gate [128, 64] and W_down [64, 128] are views of one buffer's start
+    f = 64
+    buf = normal(5, k * k, 1, scale=k ** -0.5).view(-1)
+    Wg, Wd = buf[:k * f].view(k, f), buf[:f * k].view(f, k)
+    Wu = normal(6, k, f, scale=k ** -0.5)
+    with route.GatedPlan(rows, k, f, k, BF16, train=True) as plan:
+        saved = plan.new_saved()
+        route.gated_forward(plan, x, Wg, Wu, Wd, out, saved=saved)
+        route.gated_backward(plan, x, x, Wg, Wu, Wd, saved, dx=dx)
+        plan.status()
+    want, kept = ref.gated(x, Wg, Wu, Wd, None, "silu", BF16)
+    check("out", out, want)
+    check("dx", dx, ref.gated_grads(x, Wg, Wu, Wd, kept, x, "silu", BF16)["dx"])
+
+
+@pytest.mark.parametrize("rows,dim,dt", [(70, 200, BF16), (70, 201, FP32)])
+def test_norm_gradients_against_differences(rows, dim, dt):
+    """The kernels' gradients in a direction against central differences of
+    the FP64 loss: the differences' own error is h^2 of third derivatives
+    (h = 1e-4: under 1e-6 of the sum of magnitudes), the gradients' that of
+    their elements' rounding, 2^-8 or 2^-20 of each."""
+    x, dy = normal(1, rows, dim, dt=dt), normal(2, rows, dim, dt=dt)
+    gamma, beta = normal(3, dim, dt=dt), normal(4, dim, dt=dt)
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    stats = torch.empty((rows, 2), device=DEV)
+    dg, db = torch.empty_like(gamma), torch.empty_like(beta)
+    with route.NormPlan(rows, dim, dt) as plan:
+        route.norm_forward(plan, x, gamma, beta, y, stats=stats)
+        route.norm_backward(plan, dy, x, gamma, stats, dx=dx, dgamma=dg, dbeta=db)
+        plan.status()
+
+    def loss(x, g, b):
+        d = x - x.mean(1, keepdim=True)
+        return float((dy.double() * (d * (d.square().mean(1, keepdim=True) + 1e-5) ** -0.5 * g + b)).sum())
+
+    p = [x.double(), gamma.double(), beta.double()]
+    rel = {BF16: 2.0 ** -8, FP32: 2.0 ** -20}[dt]
+    for i, grad in enumerate((dx, dg, db)):
+        v = normal(9 + i, *p[i].shape, dt=FP32).double()
+        hi, lo = list(p), list(p)
+        hi[i], lo[i] = p[i] + 1e-4 * v, p[i] - 1e-4 * v
+        diff = (loss(*hi) - loss(*lo)) / 2e-4
+        got = grad.double() * v
+        assert abs(diff - float(got.sum())) <= (rel + 1e-6) * float(got.abs().sum()) + 1e-6
