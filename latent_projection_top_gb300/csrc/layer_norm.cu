@@ -6,6 +6,8 @@
 //
 // x and dy are read once, and the variance is the sum of squared deviations
 // from the mean, not a difference of large sums.  Sums are FP32.
+#include <initializer_list>
+
 #include "layer.cuh"
 #include "layer_math.cuh"
 #include "sm103_ptx.cuh"
@@ -406,12 +408,66 @@ __global__ void __launch_bounds__(block_of(MAXT), bwd_blocks(MAXT, TY))
 // ---- any alignment: one element a thread at a time ------------------------------
 //
 // A row is held in the registers of T threads (up to 32 values each), thread
-// t's value i at column i T + t.
+// t's value i at column i T + t.  The backward pass's rows come through a
+// ring as above, but as the 4-byte words that they lie in (rows of 16-bit
+// values may start in the middle of one), each copied by any thread of the
+// row (8192x1001 BF16: 27 us, loaded directly 45).  The forward pass has
+// registers for enough blocks to load directly (20 us, through a ring 49).
 
+template <int TY>
+__host__ __device__ constexpr uint32_t loose_bytes(int t) {  // a row's place
+    return (uint32_t)(32 * t * layer_esize(TY) + 16);
+}
+// Two places of FP32 rows past 8192 do not fit: those are loaded directly.
+template <int T, int TY>
+constexpr bool kLooseRing = !(T == 512 && TY == kFp32);
+__host__ __device__ constexpr int loose_blocks(int t) { return t == 512 ? 1 : t == 256 ? 2 : 3; }
+template <int T, int TY>
+__host__ __device__ constexpr int loose_depth() {
+    return depth_of(186u * 1024u / loose_blocks(T), 2 * loose_bytes<TY>(T) * rows_of(T));
+}
+
+template <int T, int TY>
+__device__ __forceinline__ void copy_words(uint32_t base, const void *p, long long row, int dim, int t) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p) + (uintptr_t)(row * layer_esize(TY));
+    const uintptr_t from = at & ~(uintptr_t)3;
+    const int words = (int)((at - from + (uintptr_t)dim * layer_esize(TY) + 3) / 4);
+    for (int i = t; i < words; i += T)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(base + 4u * i), "l"(from + 4u * i) : "memory");
+}
+// Values of the row that copy_words brought.
+template <int T, int TY>
+__device__ __forceinline__ void take_values(uint32_t base, const void *p, long long row, int t, int dim,
+                                            float (&x)[32]) {
+    if constexpr (TY == kFp32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            x[i] = 0.f;
+            if (i * T + t < dim)
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x[i]) : "r"(base + 4u * (i * T + t)) : "memory");
+        }
+    } else {
+        base += (uint32_t)(reinterpret_cast<uintptr_t>(p) + (uintptr_t)(row * 2)) & 2u;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            uint16_t w = 0;
+            if (i * T + t < dim)
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(base + 2u * (i * T + t)) : "memory");
+            x[i] = unpack16(w, TY).x;
+        }
+    }
+}
 template <int T, int TY>
 __device__ __forceinline__ void load_values(const void *p, long long row, int t, int dim, float (&x)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) x[i] = i * T + t < dim ? load_elem(p, TY, row + i * T + t) : 0.f;
+}
+template <int T>
+__device__ __forceinline__ void row_sync() {
+    if (T > 32)
+        __syncthreads();
+    else
+        __syncwarp();
 }
 
 // Sum over the T threads of a row, the same in every thread and every run.
@@ -453,19 +509,21 @@ __global__ void __launch_bounds__(block_of(T)) norm_forward_kernel(const __grid_
     const float rstd = 1.f / sqrtf(sum_of_row<T>(s, scratch) * inv + a.eps);
     if (t == 0 && a.stats != nullptr)
         *reinterpret_cast<float2 *>(a.stats + 2 * (long long)r) = make_float2(mean, rstd);
-    // eight columns' parameters before the first of their stores: a load does
-    // not move ahead of a store that might change it
+    // FP32: eight columns' parameters before the first of their stores, ahead
+    // of which a load does not move (8192x1001: 13.0 us, one by one 22.6; two-
+    // byte loads, whose unpacking fills the time, 24.3 and 20.2)
+    constexpr int kTogether = TY == kFp32 ? 8 : 1;
 #pragma unroll
-    for (int k = 0; k < 32; k += 8) {
-        float g[8], b[8];
+    for (int k = 0; k < 32; k += kTogether) {
+        float g[kTogether], b[kTogether];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kTogether; ++i) {
             const int c = (k + i) * T + t;
             g[i] = a.gamma != nullptr && c < a.dim ? load_elem(a.gamma, TY, c) : 1.f;
             b[i] = a.beta != nullptr && c < a.dim ? load_elem(a.beta, TY, c) : 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kTogether; ++i) {
             const int c = (k + i) * T + t;
             if (c < a.dim) store_elem(a.y, TY, (long long)r * a.ld_y + c, x[k + i] * rstd * g[i] + b[i]);
         }
@@ -473,20 +531,48 @@ __global__ void __launch_bounds__(block_of(T)) norm_forward_kernel(const __grid_
 }
 
 template <int T, int TY>
-__global__ void __launch_bounds__(block_of(T)) norm_backward_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(block_of(T), loose_blocks(T)) norm_backward_kernel(const __grid_constant__ NormArgs a) {
     constexpr int kRows = rows_of(T);
+    constexpr bool RING = kLooseRing<T, TY>;
+    constexpr int P = RING ? loose_depth<T, TY>() : 1;
+    constexpr uint32_t kPlace = loose_bytes<TY>(T);
+    extern __shared__ uint4 ring[];
     __shared__ float scratch[T / 32];
-    __shared__ float s_acc[T > 32 ? 1 : kRows * 1024];
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int t = threadIdx.x % T, sub = threadIdx.x / T;
+    const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + sub * P * 2 * kPlace;
+    const int stride = gridDim.x * kRows, r0 = blockIdx.x * kRows + sub;
+    auto copy_row = [&](int r, int place) {
+        copy_words<T, TY>(mine + place * 2 * kPlace, a.x, (long long)r * a.ld_x, a.dim, t);
+        copy_words<T, TY>(mine + place * 2 * kPlace + kPlace, a.dy, (long long)r * a.ld_dy, a.dim, t);
+    };
+    if constexpr (RING)
+        for (int i = 0; i < P - 1; ++i) {
+            if (r0 + i * stride < a.rows) copy_row(r0 + i * stride, i);
+            copy_commit();
+        }
     const float inv = 1.f / (float)a.dim;
     float dg[32] = {}, db[32] = {};
-    for (int r = blockIdx.x * kRows + sub; r < a.rows; r += gridDim.x * kRows) {
-        const float mean = a.stats[2 * (long long)r], rstd = a.stats[2 * (long long)r + 1];
+    int slot = 0;
+    for (int r = r0; r < a.rows; r += stride) {
+        const float2 ms = *reinterpret_cast<const float2 *>(a.stats + 2 * (long long)r);
+        const float mean = ms.x, rstd = ms.y;
         float xh[32], g[32], s1 = 0.f, s2 = 0.f;
-        load_values<T, TY>(a.x, (long long)r * a.ld_x, t, a.dim, xh);
-        load_values<T, TY>(a.dy, (long long)r * a.ld_dy, t, a.dim, g);
+        if constexpr (RING) {
+            row_sync<T>();  // every thread has taken the last row's values
+            if (r + (P - 1) * stride < a.rows) copy_row(r + (P - 1) * stride, slot == 0 ? P - 1 : slot - 1);
+            copy_commit();
+            copy_wait<P - 1>();
+            row_sync<T>();
+            const uint32_t base = mine + slot * 2 * kPlace;
+            take_values<T, TY>(base, a.x, (long long)r * a.ld_x, t, a.dim, xh);
+            take_values<T, TY>(base + kPlace, a.dy, (long long)r * a.ld_dy, t, a.dim, g);
+            slot = slot + 1 == P ? 0 : slot + 1;
+        } else {
+            load_values<T, TY>(a.x, (long long)r * a.ld_x, t, a.dim, xh);
+            load_values<T, TY>(a.dy, (long long)r * a.ld_dy, t, a.dim, g);
+        }
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
             const float gm = a.gamma != nullptr && i * T + t < a.dim ? load_elem(a.gamma, TY, i * T + t) : 1.f;
@@ -514,7 +600,9 @@ __global__ void __launch_bounds__(block_of(T)) norm_backward_kernel(const __grid
             if (c < a.dim) part[c] = dg[i], part[a.dim + c] = db[i];
         }
     } else {
-        // the block's rows meet in shared memory, gradient by gradient
+        // the block's rows meet in the ring's memory, gradient by gradient
+        copy_wait<0>();
+        float *s_acc = reinterpret_cast<float *>(ring);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             __syncthreads();
@@ -650,6 +738,22 @@ cudaError_t forward_aligned(const NormArgs &a, cudaStream_t stream) {
 }
 
 
+template <int T, int TY>
+constexpr size_t loose_smem() {
+    return kLooseRing<T, TY> ? (size_t)loose_depth<T, TY>() * 2 * loose_bytes<TY>(T) * rows_of(T) : 0;
+}
+template <int T, int TY>
+cudaError_t configure_loose() {
+    static_assert(loose_smem<T, TY>() <= 224 * 1024, "shared memory");
+    static_assert(T > 32 || loose_smem<T, TY>() >= 4 * 1024 * 4, "the gradients' sums");
+    return cudaFuncSetAttribute(norm_backward_kernel<T, TY>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)loose_smem<T, TY>());
+}
+template <int T, int TY>
+cudaError_t backward_loose(const NormArgs &a, int *grid, cudaStream_t stream) {
+    *grid = blocks_for(a.rows, T, loose_blocks(T) * a.sms);
+    return launch_pdl(norm_backward_kernel<T, TY>, *grid, block_of(T), loose_smem<T, TY>(), stream, a);
+}
 template <int TY>
 cudaError_t forward_any(const NormArgs &a, cudaStream_t stream) {
     const int t = threads_of(a.dim), grid = (a.rows + rows_of(t) - 1) / rows_of(t);
@@ -662,12 +766,10 @@ cudaError_t forward_any(const NormArgs &a, cudaStream_t stream) {
 template <int TY>
 cudaError_t backward_any(const NormArgs &a, int *grid, cudaStream_t stream) {
     const int t = threads_of(a.dim);
-    *grid = blocks_for(a.rows, t, (t == 512 ? 1 : kMaxBlocks) * a.sms);
-    return launch_pdl(t == 32    ? norm_backward_kernel<32, TY>
-                      : t == 128 ? norm_backward_kernel<128, TY>
-                      : t == 256 ? norm_backward_kernel<256, TY>
-                                 : norm_backward_kernel<512, TY>,
-                      *grid, block_of(t), 0, stream, a);
+    return t == 32    ? backward_loose<32, TY>(a, grid, stream)
+           : t == 128 ? backward_loose<128, TY>(a, grid, stream)
+           : t == 256 ? backward_loose<256, TY>(a, grid, stream)
+                      : backward_loose<512, TY>(a, grid, stream);
 }
 
 template <int T, int V, int TY>
@@ -691,10 +793,22 @@ cudaError_t backward_aligned(const NormArgs &a, int *grid, cudaStream_t stream) 
 
 }  // namespace
 
+namespace {
+template <int TY>
+cudaError_t configure_loose_type() {
+    cudaError_t e = configure_loose<32, TY>();
+    if (e == cudaSuccess) e = configure_loose<128, TY>();
+    if (e == cudaSuccess) e = configure_loose<256, TY>();
+    return e == cudaSuccess ? configure_loose<512, TY>() : e;
+}
+}  // namespace
+
 cudaError_t norm_configure() {
-    cudaError_t e = configure_type<kBf16>();
-    if (e == cudaSuccess) e = configure_type<kFp16>();
-    return e == cudaSuccess ? configure_type<kFp32>() : e;
+    for (cudaError_t e : {configure_type<kBf16>(), configure_type<kFp16>(), configure_type<kFp32>(),
+                          configure_loose_type<kBf16>(), configure_loose_type<kFp16>(),
+                          configure_loose_type<kFp32>()})
+        if (e != cudaSuccess) return e;
+    return cudaSuccess;
 }
 
 size_t norm_part_floats(int dim, int sms) { return (size_t)kMaxBlocks * sms * 2 * dim; }
