@@ -305,8 +305,9 @@ __global__ void __launch_bounds__(block_of(MAXT), bwd_blocks(MAXT, TY))
     const int stride = gridDim.x * kRows;
     const int r0 = blockIdx.x * kRows + sub;
     int turn = 0;
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the sums follow; the last kernel of a call lets nothing launch early
+    if (threadIdx.x == 0 && a.part != nullptr) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     auto copy_row = [&](int r, int slot) {
         R::copy(mine + slot * 2 * place, a.x, (long long)r * a.ld_x, a.dim, T, t);
         R::copy(mine + slot * 2 * place + place, a.dy, (long long)r * a.ld_dy, a.dim, T, t);
@@ -538,8 +539,9 @@ __global__ void __launch_bounds__(block_of(T), loose_blocks(T)) norm_backward_ke
     constexpr uint32_t kPlace = loose_bytes<TY>(T);
     extern __shared__ uint4 ring[];
     __shared__ float scratch[T / 32];
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the sums follow; the last kernel of a call lets nothing launch early
+    if (threadIdx.x == 0 && a.part != nullptr) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int t = threadIdx.x % T, sub = threadIdx.x / T;
     const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + sub * P * 2 * kPlace;
     const int stride = gridDim.x * kRows, r0 = blockIdx.x * kRows + sub;
