@@ -21,7 +21,11 @@
 //
 // Rows of D are the TMEM lanes.  An epilogue warp takes 32 columns of its 32 rows
 // out of TMEM into shared memory and back with neighbouring threads on
-// neighbouring columns, four to a thread, for the operator's epilogue.
+// neighbouring columns, four to a thread, for the operator's epilogue.  Its "TMEM is read"
+// to the other CTA is a relaxed arrival: ordered after the warp's stores of
+// results, as an arrival is by default, it waited for them to reach the L2
+// (2050x64x3584 11.5 us, so 10.4; gelu with z kept 20.5, so 19.3).  For the
+// same reason the last meeting of the pair is relaxed (0.4 us a launch).
 //
 // Split K: with few tiles, `splits` CTA pairs share a tile's contraction and
 // store FP32 partials; gemm_finish_kernel adds them in split order and runs
@@ -434,7 +438,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
                         if (leader)
                             ptx::mbar_arrive(tempty_bar(t));
                         else
-                            ptx::mbar_arrive_remote(ptx::map_to_rank(tempty_bar(t), 0u));
+                            ptx::mbar_arrive_remote_relaxed(ptx::map_to_rank(tempty_bar(t), 0u));
                     }
                     const int c = c0 + g * kG + lane;
 #pragma unroll 1
@@ -467,7 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
                         if (leader)
                             ptx::mbar_arrive(tempty_bar(t));
                         else
-                            ptx::mbar_arrive_remote(ptx::map_to_rank(tempty_bar(t), 0u));
+                            ptx::mbar_arrive_remote_relaxed(ptx::map_to_rank(tempty_bar(t), 0u));
                     }
                 }
                 if (WIDE && kAhead && whole && b + 1 < kBatches)
@@ -498,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
         ptx::tc_fence_after();
         ptx::tmem_dealloc_pair(tmem_base, 2 * BN);
     }
-    ptx::cluster_sync();  // neither CTA leaves while the other may reach its shared memory
+    ptx::cluster_sync_relaxed();  // neither CTA leaves while the other may reach its shared memory
 }
 
 // Sums of the split partials in split order, four columns a thread, and the

@@ -342,7 +342,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         ptx::tmem_dealloc(tmem_base, kTmemCols);
     }
     __syncwarp();
-    if (C > 1) ptx::cluster_sync();  // no CTA leaves while another may read its sums
+    // no CTA leaves while another may read its sums (relaxed: ordered after the
+    // stores of results it takes 0.5 us longer, 64x896x896 5.1 against 4.6)
+    if (C > 1) ptx::cluster_sync_relaxed();
 }
 
 const void *kernel_of(int epi, int bn) {
