@@ -136,9 +136,11 @@ struct RepackArgs {
 cudaError_t repack_launch(const RepackArgs &args, cudaStream_t stream);
 
 // dz = dout * act'(z) (z: FP32, row stride ld_z; null: dz = dout), written
-// with row stride ld_dz unless dz is null, and FP32 column sums of the
-// unrounded dz when dbias is given (type `type`): `part` holds
-// elem_part_floats(N) floats.
+// with row stride ld_dz unless dz is null.  dbias (type `type`): column sums
+// of the unrounded dz, in two steps with FP32 partials in `part`
+// (dz_part_floats(n) floats): dz_launch makes them with dz, or bias_launch
+// from dout (`sums_only`: no activation, and the products read dout itself);
+// bias_launch adds them.
 struct DzArgs {
     int rows, n, type, act;
     const void *dout;
@@ -147,12 +149,17 @@ struct DzArgs {
     long long ld_z;
     void *dz;
     long long ld_dz;
+    int sums_only;
     void *dbias;
     float *part;
-    int trigger;
 };
 size_t dz_part_floats(int n);
+// The kernel of a call that always has one after it.
 cudaError_t dz_launch(const DzArgs &args, cudaStream_t stream);
+// `after`: the call's kernel before this one has waited for all that came
+// before it, dz_launch's kernel among it, and writes nothing that is read
+// here: the sums then run beside it.
+cudaError_t bias_launch(const DzArgs &args, bool after, cudaStream_t stream);
 
 struct NormArgs {
     int rows, dim, type;

@@ -51,7 +51,8 @@ struct route_layer {
     uint8_t *scratch;
     size_t scratch_bytes;
     // offsets into scratch (0 size where the plan needs none)
-    size_t o_part;     // split partials, or column-sum partials
+    size_t o_part;     // split partials (norm: column-sum partials)
+    size_t o_sum;      // the bias gradient's partials
     size_t o_x, o_w[3], o_dout, o_h, o_dg, o_du;
     mutable ChoiceMemo memo[kSlots];
 };
@@ -113,10 +114,7 @@ route_status check_mat(const Mat &m) {
 
 route_status check_mats(std::initializer_list<Mat> ms) {
     for (const Mat &m : ms)
-        if (m.p || m.cols > 0) {
-            const route_status st = check_mat(m);
-            if (st != ROUTE_OK) return st;
-        }
+        if (const route_status st = check_mat(m)) return st;
     return ROUTE_OK;
 }
 
@@ -480,9 +478,10 @@ route_status forward_product(const route_layer *p, ChoiceSlot slot, const Operan
 // whose result is wanted.  One launch, unless the contractions (over the
 // widths for dx, over the rows for the others) differ so much that no one
 // way to cut them suits both.  What is chosen goes by all of them, so that a
-// gradient's bits do not depend on which others are asked for.
+// gradient's bits do not depend on which others are asked for.  `more`:
+// another kernel of the call follows.
 route_status backward_products(const route_layer *p, int rows, Prod *all, int count, bool chained,
-                               cudaStream_t stream) {
+                               bool more, cudaStream_t stream) {
     for (int i = 0; i < count; ++i) all[i].id = i;
     const Choice &one = choice_of(p, kSlotBackward, rows, kEpiLinear, all, count);
     const Choice &input = choice_of(p, kSlotInput, rows, kEpiLinear, all, 1);
@@ -495,12 +494,12 @@ route_status backward_products(const route_layer *p, int rows, Prod *all, int co
         for (int i = 1; i < count; ++i)
             if (all[i].e.out) w[n] = all[i], w[n++].id = i - 1;
         route_status st;
-        if (dx && (st = run(p, kEpiLinear, dx, 1, input, chained, n > 0, stream)) != ROUTE_OK) return st;
-        return n ? run(p, kEpiLinear, w, n, weights, false, false, stream) : ROUTE_OK;
+        if (dx && (st = run(p, kEpiLinear, dx, 1, input, chained, more || n > 0, stream)) != ROUTE_OK) return st;
+        return n ? run(p, kEpiLinear, w, n, weights, false, more, stream) : ROUTE_OK;
     }
     for (int i = 0; i < count; ++i)
         if (all[i].e.out) w[n++] = all[i];
-    return n ? run(p, kEpiLinear, w, n, one, chained, false, stream) : ROUTE_OK;
+    return n ? run(p, kEpiLinear, w, n, one, chained, more, stream) : ROUTE_OK;
 }
 
 route_status zero_matrix(void *p, int64_t ld, int rows, int cols, int esize, cudaStream_t stream) {
@@ -557,14 +556,12 @@ route_status finish_prepare(route_layer *p, int device, route_layer **out) {
     if (p->kind == kNorm) {
         p->o_part = area(norm_part_floats(p->k, p->sms) * 4);
     } else {
-        size_t part = 2 * (size_t)p->pairs * kTilePartBytes;
-        if (p->kind == kLinear && p->train && part < dz_part_floats(p->n) * 4)
-            part = dz_part_floats(p->n) * 4;
-        p->o_part = area(part);
+        p->o_part = area(2 * (size_t)p->pairs * kTilePartBytes);
         p->o_x = copy(R, p->k);
         if (p->kind == kLinear) {
             p->o_w[0] = copy(p->k, p->n);
             p->o_dg = area(p->train && (p->act != kActNone || p->n % 8) ? R * up16(p->n) * 2 : 0);
+            p->o_sum = area(p->train ? dz_part_floats(p->n) * 4 : 0);
         } else {
             p->o_w[0] = copy(p->k, p->f);
             p->o_w[1] = copy(p->k, p->f);
@@ -821,8 +818,8 @@ route_status route_linear_backward(const route_layer *p, int rows, const void *d
     const bool in_place = p->act == kActNone && aligned(dout, 16) &&
                           (rows > 1 ? ld_dout % 8 == 0 : p->n % 8 == 0);
     const bool make_dz = !in_place && (dx || dW);
+    DzArgs a = {};
     if (make_dz || dbias) {
-        DzArgs a = {};
         a.rows = rows, a.n = p->n, a.type = p->type, a.act = p->act;
         a.dout = dout, a.ld_dout = dz.ld;
         if (p->act != kActNone) a.z = static_cast<const float *>(saved), a.ld_z = up16(p->n);
@@ -830,13 +827,17 @@ route_status route_linear_backward(const route_layer *p, int rows, const void *d
             a.dz = p->scratch + p->o_dg, a.ld_dz = up16(p->n);
             dz = {a.dz, a.ld_dz};
         }
+        a.sums_only = in_place;
         a.dbias = dbias;
-        a.part = reinterpret_cast<float *>(p->scratch + p->o_part);
-        a.trigger = dx || dW;
+        a.part = reinterpret_cast<float *>(p->scratch + p->o_sum);
         const cudaError_t e = dz_launch(a, s);
         if (e != cudaSuccess) return cuda_fail(e, "pre-activation gradient kernel launch");
     }
-    if (!dx && !dW) return ROUTE_OK;
+    auto sums = [&](bool after) {
+        const cudaError_t e = dbias ? bias_launch(a, after, s) : cudaSuccess;
+        return e == cudaSuccess ? ROUTE_OK : cuda_fail(e, "bias gradient kernel launch");
+    };
+    if (!dx && !dW) return sums(false);
     // dx = dz W^T and dW = x^T dz
     Copies copies(p);
     const Operand ox = dW ? copies.operand(x, ld_x, rows, p->k, p->o_x) : Operand{nullptr, 0};
@@ -844,7 +845,9 @@ route_status route_linear_backward(const route_layer *p, int rows, const void *d
     if ((st = copies.launch(s)) != ROUTE_OK) return st;
     Prod all[2] = {product(p, kFormNN, rows, p->k, p->n, dz, ow, dx, ld_dx, p->type),
                    product(p, kFormTT, p->k, p->n, rows, ox, dz, dW, ld_dW, p->type)};
-    return backward_products(p, rows, all, 2, false, s);
+    // dz's kernel, if it was the last one, waited and does not write W
+    st = backward_products(p, rows, all, 2, make_dz && copies.args.count == 0, dbias != nullptr, s);
+    return st != ROUTE_OK ? st : sums(true);
 }
 
 route_status route_gated_forward(const route_layer *p, int rows, const void *x, int64_t ld_x,
@@ -948,7 +951,7 @@ route_status route_gated_backward(const route_layer *p, int rows, const void *do
                    product(p, kFormTT, p->k, p->f, rows, ox, du, dW_up, ld_dup, p->type),
                    product(p, kFormTT, p->f, p->n, rows, h, dy, dW_down, ld_ddown, p->type)};
     all[0].terms = 2, all[0].a[1] = du, all[0].b[1] = ou;
-    return backward_products(p, rows, all, 4, pre, s);
+    return backward_products(p, rows, all, 4, pre, false, s);
 }
 
 }  // extern "C"
