@@ -19,9 +19,10 @@
 // columns of D in its TMEM.  Two accumulators alternate, so that one tile is
 // drained while the next is computed.
 //
-// Rows of D are the TMEM lanes.  An epilogue warp takes 32 columns of its 32 rows
+// Rows of D are the TMEM lanes.  An epilogue warp takes columns of its 32 rows
 // out of TMEM into shared memory and back with neighbouring threads on
-// neighbouring columns, four to a thread, for the operator's epilogue.  Its "TMEM is read"
+// neighbouring columns (Access: how many, and on which side of shared memory
+// the operator's epilogue is).  Its "TMEM is read"
 // to the other CTA is a relaxed arrival: ordered after the warp's stores of
 // results, as an arrival is by default, it waited for them to reach the L2
 // (2050x64x3584 11.5 us, so 10.4; gelu with z kept 20.5, so 19.3).  For the
@@ -240,9 +241,15 @@ __device__ __forceinline__ bool mma_tile(Stages<BN> &st, int kblocks, uint32_t d
     return true;
 }
 
-// WIDE: rows of the result are accessed four columns at a time (else one; a
-// kernel of its own, for the registers).
-template <int FORM, int EPI, int BN, bool WIDE>
+// How rows of the result are accessed, a kernel each for the registers: one
+// column a thread (rows of odd widths); four FP32 sums a thread, for what has
+// to be read or kept beside the result; or, where the result is 16-bit values
+// of the sums alone, finished and packed by the thread that took a row's
+// columns out of TMEM, so that half the bytes go through shared memory, in one
+// pass, and a row leaves in whole 128-byte lines (4096x64x7168 15.6 us, by
+// fours 23.3; 64x3584x7168's backward pass 32.8, by fours 39.4).
+enum Access { kColumns = 0, kFours = 1, kPacked = 2 };
+template <int FORM, int EPI, int BN, int ACCESS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1)
     layer_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs args) {
     constexpr int S = stages_of(BN);
@@ -393,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
             auto col_of = [&](int b) { return c0 + b / kGroupBatches * kG + lane % kLanesRow * 4; };
             GroupIn<EPI, kBatch> in, next;
             // the first inputs go out before the tile's sums are complete
-            if (WIDE && whole) group_load<EPI, kBatch>(p, r0 + row_of(0), col_of(0), kStep, in);
+            if (ACCESS == kFours && whole) group_load<EPI, kBatch>(p, r0 + row_of(0), col_of(0), kStep, in);
             // one warp polls, the others sleep at the barrier
             const bool ok = warp != 2 || wait_phase(tfull_bar(t), ((uint32_t)job >> 1) & 1u, args, &s_abort);
             if (!ptx::named_bar_and(1, 32 * kEpiWarps, ok)) break;
@@ -425,21 +432,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
                                  : "r"(unit(row + j * kStep, lane % kLanesRow) + half)
                                  : "memory");
             };
-            if (!WIDE && whole) {  // rows of odd widths: a column a thread
+            auto read_out = [&] {  // everything has left TMEM
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane != 0) return;
+                if (leader)
+                    ptx::mbar_arrive(tempty_bar(t));
+                else
+                    ptx::mbar_arrive_remote_relaxed(ptx::map_to_rank(tempty_bar(t), 0u));
+            };
+            if (ACCESS == kPacked && whole) {
+                if constexpr (ACCESS == kPacked) {
+                    // A row of the warp's columns, packed to 16 bits, is kUnits units of
+                    // 16 bytes; those of the rows of a 128-byte line are interleaved.
+                    constexpr int kUnits = kWarpCols / 8, kLineRows = 8 / kUnits;
+                    auto slot = [&](int row, int x) {
+                        return mine + (uint32_t)(row * kUnits * 16 + ((x ^ ((row / kLineRows) & (kUnits - 1))) << 4));
+                    };
+                    __syncwarp();  // the last tile's rows have been read
+                    constexpr int kTake = EPI == kEpiLinear ? 32 : 16;  // columns at a time
+                    const bool half = p.out_type == kFp16;
+#pragma unroll(EPI == kEpiLinear ? kWarpCols / kTake : 1)
+                    for (int g = 0; g < kWarpCols; g += kTake) {
+                        uint32_t raw[kTake], raw2[EPI == kEpiGated ? kTake : 1];
+#pragma unroll
+                        for (int h = 0; h < kTake; h += 16)
+                            ptx::tmem_ld_x16(acc + (uint32_t)(g + h), reinterpret_cast<uint32_t(&)[16]>(raw[h]));
+                        if constexpr (EPI == kEpiGated) ptx::tmem_ld_x16(acc + (uint32_t)(kTileCols + g), raw2);
+                        ptx::tmem_ld_wait();
+                        float v[kTake];
+#pragma unroll
+                        for (int e = 0; e < kTake; ++e) v[e] = __uint_as_float(raw[e]);
+                        if constexpr (epi_linear(EPI))
+                            if (p.bias != nullptr) packed_bias<kTake>(p, c0 + g, half, v);
+                        if constexpr (EPI != kEpiLinear) act_values<kTake>(p.act, v);
+                        if constexpr (EPI == kEpiGated)
+#pragma unroll
+                            for (int e = 0; e < kTake; ++e) v[e] *= __uint_as_float(raw2[e]);
+                        uint32_t w[kTake / 2];
+                        pack_values<kTake>(half, v, w);
+#pragma unroll
+                        for (int h = 0; h < kTake / 8; ++h)
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(slot(lane, g / 8 + h)),
+                                         "r"(w[4 * h]), "r"(w[4 * h + 1]), "r"(w[4 * h + 2]), "r"(w[4 * h + 3])
+                                         : "memory");
+                    }
+                    read_out();
+                    constexpr int kStepRows = 32 / kUnits;
+                    const int x = lane % kUnits, c = c0 + 8 * x;
+                    int r = lane / kUnits;
+                    uint16_t *q = static_cast<uint16_t *>(p.out) + (long long)(r0 + r) * p.ld_out + c;
+                    if (c < p.N)
+#pragma unroll
+                        for (int j = 0; j < 32; j += kStepRows, r += kStepRows, q += kStepRows * p.ld_out) {
+                            uint4 w;
+                            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                         : "r"(slot(r, x))
+                                         : "memory");
+                            if (r0 + r < p.M) *reinterpret_cast<uint4 *>(q) = w;
+                        }
+                }
+                continue;
+            }
+            if (ACCESS == kColumns && whole) {  // rows of odd widths: a column a thread
                 constexpr int kRows = EPI == kEpiDGate ? 4 : 8;
 #pragma unroll 1
                 for (int g = 0; g < kWarpCols / kG; ++g) {
                     __syncwarp();  // the last group has been read
                     put(acc + (uint32_t)(g * kG), 0u);
                     if (EPI == kEpiGated) put(acc + (uint32_t)(g * kG) + kTileCols, kHalfTurn);
-                    ptx::tc_fence_before();
                     __syncwarp();
-                    if (g + 1 == kWarpCols / kG && lane == 0) {  // everything has left TMEM
-                        if (leader)
-                            ptx::mbar_arrive(tempty_bar(t));
-                        else
-                            ptx::mbar_arrive_remote_relaxed(ptx::map_to_rank(tempty_bar(t), 0u));
-                    }
+                    if (g + 1 == kWarpCols / kG) read_out();
                     const int c = c0 + g * kG + lane;
 #pragma unroll 1
                     for (int r = 0; r < 32; r += kRows) {
@@ -465,22 +529,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
                     __syncwarp();  // the last group has been read
                     put(from, 0u);
                     if (EPI == kEpiGated) put(from + kTileCols, kHalfTurn);
-                    ptx::tc_fence_before();
                     __syncwarp();
-                    if (b + kGroupBatches == kBatches && lane == 0) {  // everything has left TMEM
-                        if (leader)
-                            ptx::mbar_arrive(tempty_bar(t));
-                        else
-                            ptx::mbar_arrive_remote_relaxed(ptx::map_to_rank(tempty_bar(t), 0u));
-                    }
+                    if (b + kGroupBatches == kBatches) read_out();
                 }
-                if (WIDE && kAhead && whole && b + 1 < kBatches)
+                if (ACCESS == kFours && kAhead && whole && b + 1 < kBatches)
                     group_load<EPI, kBatch>(p, r0 + row_of(b + 1), col_of(b + 1), kStep, next);
                 float v[4 * kBatch], u[EPI == kEpiGated ? 4 * kBatch : 1];
                 get(row_of(b), 0u, v);
                 if constexpr (EPI == kEpiGated) get(row_of(b), kHalfTurn, u);
                 const int r = r0 + row_of(b), c = col_of(b);
-                if (WIDE && whole) {
+                if (ACCESS == kFours && whole) {
                     group_epilogue<EPI, kBatch>(p, r, c, kStep, v, u, in);
                 } else if (c < p.N) {  // partials: rows padded to whole groups
                     float *part = p.part + (long long)w.split * p.M * p.ld_part;
@@ -547,18 +605,19 @@ cudaError_t launch_chained(const void *fn, dim3 grid, dim3 block, size_t smem, v
     return cudaLaunchKernelExC(&c, fn, params);
 }
 
-const void *kernel_of(int form, int epi, int bn, bool wide) {
-#define ROUTE_GEMM(F, E)                                                                       \
-    if (form == F && epi == E)                                                                 \
-        return bn == 256 ? (wide ? reinterpret_cast<const void *>(layer_gemm_kernel<F, E, 256, true>)   \
-                                 : reinterpret_cast<const void *>(layer_gemm_kernel<F, E, 256, false>)) \
-                         : (wide ? reinterpret_cast<const void *>(layer_gemm_kernel<F, E, 128, true>)   \
-                                 : reinterpret_cast<const void *>(layer_gemm_kernel<F, E, 128, false>));
-    ROUTE_GEMM(kFormNT, kEpiLinear)
-    ROUTE_GEMM(kFormNT, kEpiAct)
-    ROUTE_GEMM(kFormNT, kEpiGated)
-    ROUTE_GEMM(kFormNN, kEpiDGate)
-    ROUTE_GEMM(kFormMixed, kEpiLinear)
+const void *kernel_of(int form, int epi, int bn, Access access) {
+#define ROUTE_GEMM(F, E, A)                                                                    \
+    if (form == F && epi == E && access == A)                                                  \
+        return bn == 256 ? reinterpret_cast<const void *>(layer_gemm_kernel<F, E, 256, A>)     \
+                         : reinterpret_cast<const void *>(layer_gemm_kernel<F, E, 128, A>);
+#define ROUTE_GEMM3(F, E) ROUTE_GEMM(F, E, kColumns) ROUTE_GEMM(F, E, kFours) ROUTE_GEMM(F, E, kPacked)
+    ROUTE_GEMM3(kFormNT, kEpiLinear)
+    ROUTE_GEMM3(kFormNT, kEpiAct)
+    ROUTE_GEMM3(kFormNT, kEpiGated)
+    ROUTE_GEMM(kFormNN, kEpiDGate, kColumns)
+    ROUTE_GEMM(kFormNN, kEpiDGate, kFours)
+    ROUTE_GEMM3(kFormMixed, kEpiLinear)
+#undef ROUTE_GEMM3
 #undef ROUTE_GEMM
     return nullptr;
 }
@@ -569,8 +628,8 @@ cudaError_t gemm_configure() {
     for (int form : {kFormNT, kFormNN, kFormMixed})
         for (int epi = 0; epi < kEpiCount; ++epi)
             for (int bn : {256, 128})
-                for (bool wide : {false, true})
-                    if (const void *k = kernel_of(form, epi, bn, wide)) {
+                for (Access access : {kColumns, kFours, kPacked})
+                    if (const void *k = kernel_of(form, epi, bn, access)) {
                         const cudaError_t e = cudaFuncSetAttribute(
                             k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(bn));
                         if (e != cudaSuccess) return e;
@@ -582,9 +641,13 @@ int gemm_smem_bytes() { return (int)(smem_of(256) > smem_of(128) ? smem_of(256) 
 
 cudaError_t gemm_launch(int form, int epi, int bn, const GemmMaps &maps, const GemmArgs &args,
                         cudaStream_t stream) {
-    bool wide = true;
-    for (int i = 0; i < args.nprob; ++i) wide = wide && (args.p[i].e.vec & kVecOut);
-    const void *k = kernel_of(form, epi, bn, wide);
+    bool fours = true, packed = epi != kEpiDGate;
+    for (int i = 0; i < args.nprob; ++i) {
+        const Epilogue &e = args.p[i].e;
+        fours = fours && (e.vec & kVecOut);
+        packed = packed && (e.vec & kVecPacked) && e.N % 8 == 0 && e.saved == nullptr && e.residual == nullptr;
+    }
+    const void *k = kernel_of(form, epi, bn, packed ? kPacked : fours ? kFours : kColumns);
     if (k == nullptr || args.pairs <= 0 || args.items <= 0) return cudaErrorInvalidConfiguration;
     void *params[] = {const_cast<GemmMaps *>(&maps), const_cast<GemmArgs *>(&args)};
     return launch_chained(k, dim3(2 * args.pairs), dim3(gemm_threads(epi)), smem_of(bn), params, stream);
