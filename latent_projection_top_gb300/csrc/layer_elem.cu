@@ -123,13 +123,12 @@ __global__ void __launch_bounds__(256) dz_kernel(const __grid_constant__ DzArgs 
 }
 
 // The column sums of dout itself, a row of partials a warp: as dz_kernel, of
-// 16-bit values and with nothing to write.  This kernel and the next are small
-// enough (128 threads, under 768 bytes of shared memory, 10,240 registers) to
-// run on an SM beside a block of the products, and read what was there before
-// these were launched: with `after` they wait only before they leave, so that
-// the sums run beside the products (backward 2050x896x3584 without activation
-// 36.4 us ahead of them, so 32.2, without dbias 27.2; with gelu 44.3, 42.5 and
-// 40.7).  Few rows make one block of rows, which adds its own partials.
+// 16-bit values and with nothing to write.  This kernel and the next read what
+// was there before these were launched: with `after` they wait only before
+// they leave, so that they start as blocks of the products leave (backward
+// 2050x896x3584 without activation 32.2 us, with the sums ahead of the
+// products 36.4, without dbias 27.2; with gelu 42.5, 44.3 and 40.7).  Few rows
+// make one block of rows, which adds its own partials.
 constexpr int kBiasWarps = 4;
 constexpr int kBiasMaxBlocks = kDzMaxBlocks / kBiasWarps;
 constexpr int kBiasOneBlock = 128;  // rows
