@@ -8,7 +8,7 @@ namespace route {
 namespace {
 
 constexpr int kDzCols = 256;       // columns of a block: 32 threads of 8
-constexpr int kDzRows = 4;
+constexpr int kDzRows = 2;
 constexpr int kDzMaxBlocks = 128;  // row blocks: partial sums a column
 
 // Eight values a thread; columns past `cols` become zeros up to the next
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(256) repack_kernel(const __grid_constant__ Rep
 // dz = dout * act'(z) for a block of rows and 256 columns: a warp walks rows,
 // a thread holds 8 columns and the FP32 sums of the dz it made, before they
 // are rounded to 16 bits for the products.
-__global__ void __launch_bounds__(256) dz_kernel(const __grid_constant__ DzArgs a, int rows_per_block,
+__global__ void __launch_bounds__(256, 4) dz_kernel(const __grid_constant__ DzArgs a, int rows_per_block,
                                                  int vec) {
     __shared__ float s_sum[8][kDzCols];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -60,7 +60,8 @@ __global__ void __launch_bounds__(256) dz_kernel(const __grid_constant__ DzArgs 
         const int n = a.n - c;
         const uint16_t *dout = static_cast<const uint16_t *>(a.dout);
         uint16_t *dz = static_cast<uint16_t *>(a.dz);
-        // four rows at a time, so that their loads are on the way together
+        // two rows at a time, so that their loads are on the way together (four, with
+        // half as many blocks an SM, took 2 us longer: backward 2050x896x3584, gelu)
         for (int r = blockIdx.y * rows_per_block + warp; r < r1; r += 8 * kDzRows) {
             uint4 t[kDzRows];
             float4 z0[kDzRows], z1[kDzRows];
@@ -129,6 +130,7 @@ __global__ void __launch_bounds__(256) dz_kernel(const __grid_constant__ DzArgs 
 // 2050x896x3584 without activation 32.2 us, with the sums ahead of the
 // products 36.4, without dbias 27.2; with gelu 42.5, 44.3 and 40.7).  Few rows
 // make one block of rows, which adds its own partials.
+constexpr int kBiasRows = 4;  // rows whose loads are on the way together
 constexpr int kBiasWarps = 4;
 constexpr int kBiasMaxBlocks = kDzMaxBlocks / kBiasWarps;
 constexpr int kBiasOneBlock = 128;  // rows
@@ -143,10 +145,10 @@ __global__ void __launch_bounds__(32 * kBiasWarps)
     if (n > 0) {
         float sum[8] = {};
         const uint16_t *s = static_cast<const uint16_t *>(a.dout) + c;
-        for (int r = part * rows_per_warp; r < r1; r += kDzRows) {
-            uint32_t w[kDzRows][4] = {};
+        for (int r = part * rows_per_warp; r < r1; r += kBiasRows) {
+            uint32_t w[kBiasRows][4] = {};
 #pragma unroll
-            for (int k = 0; k < kDzRows; ++k) {
+            for (int k = 0; k < kBiasRows; ++k) {
                 if (r + k >= r1) break;
                 const uint16_t *q = s + (long long)(r + k) * a.ld_dout;
                 if (vec && n >= 8) {
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(32 * kBiasWarps)
                 }
             }
 #pragma unroll
-            for (int k = 0; k < kDzRows; ++k)
+            for (int k = 0; k < kBiasRows; ++k)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 f = unpack16(w[k][e], a.type);
@@ -242,7 +244,7 @@ namespace {
 // Row blocks of dz_kernel and the rows of each: about eight blocks an SM,
 // eight rows at least to a block.
 int dz_blocks(int rows, int n, int &per) {
-    int rb = 1216 / ((n + kDzCols - 1) / kDzCols);
+    int rb = 608 / ((n + kDzCols - 1) / kDzCols);
     rb = rb < 1 ? 1 : rb > kDzMaxBlocks ? kDzMaxBlocks : rb;
     rb = rb > (rows + 7) / 8 ? (rows + 7) / 8 : rb;
     per = (rows + rb - 1) / rb;
@@ -267,7 +269,7 @@ cudaError_t bias_launch(const DzArgs &args, bool after, cudaStream_t stream) {
     int per, parts = 0;
     if (args.sums_only) {
         // four rows at least to a warp
-        int blocks = (args.rows + kDzRows * kBiasWarps - 1) / (kDzRows * kBiasWarps);
+        int blocks = (args.rows + kBiasRows * kBiasWarps - 1) / (kBiasRows * kBiasWarps);
         blocks = args.rows <= kBiasOneBlock ? 1 : blocks;
         blocks = blocks > kBiasMaxBlocks ? kBiasMaxBlocks : blocks;
         parts = blocks * kBiasWarps;
