@@ -242,13 +242,13 @@ __device__ __forceinline__ bool mma_tile(Stages<BN> &st, int kblocks, uint32_t d
 }
 
 // How rows of the result are accessed, a kernel each for the registers: one
-// column a thread (rows of odd widths); four FP32 sums a thread, for what has
-// to be read or kept beside the result; or, where the result is 16-bit values
-// of the sums alone, finished and packed by the thread that took a row's
+// column a thread (rows of odd widths); four FP32 sums a thread, where FP32
+// values are read or kept beside the result; or, where there is 16-bit data
+// only besides the sums, finished and packed by the thread that took a row's
 // columns out of TMEM, so that half the bytes go through shared memory, in one
 // pass, and a row leaves in whole 128-byte lines (4096x64x7168 15.6 us, by
 // fours 23.3; 64x3584x7168's backward pass 32.8, by fours 39.4).
-enum Access { kColumns = 0, kFours = 1, kPacked = 2 };
+enum Access { kColumns = 0, kFours = 1, kPacked = 2, kPackedResidual = 3 };
 template <int FORM, int EPI, int BN, int ACCESS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1)
     layer_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs args) {
@@ -257,6 +257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
     constexpr int kTileCols = EPI == kEpiGated ? BN / 2 : BN;  // columns of D a tile
     constexpr int kBCols = BN / 2;                             // B columns each CTA loads
     constexpr int kEpiWarps = epi_warps(EPI);
+    constexpr bool kPack = ACCESS == kPacked || ACCESS == kPackedResidual;
     constexpr int kWarpCols = kTileCols / (kEpiWarps / 4);     // columns of D an epilogue warp drains
     static_assert(kWarpCols % kG == 0 && kG % 16 == 0, "whole groups");
     extern __shared__ uint8_t smem_raw[];
@@ -399,7 +400,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
             auto row_of = [&](int b) { return b % kGroupBatches * (kBatch * kStep) + lane / kLanesRow; };
             auto col_of = [&](int b) { return c0 + b / kGroupBatches * kG + lane % kLanesRow * 4; };
             GroupIn<EPI, kBatch> in, next;
-            // the first inputs go out before the tile's sums are complete
+            // Packed: a row of the warp's columns is kUnits units of 16 bytes; those of
+            // the rows of a 128-byte line are interleaved.  A thread's share of them
+            // on the way from and to memory: unit px of every kStepRows-th row.
+            constexpr int kUnits = kWarpCols / 8, kLineRows = 8 / kUnits, kStepRows = 32 / kUnits;
+            auto slot = [&](int row, int x) {
+                return mine + (uint32_t)(row * kUnits * 16 + ((x ^ ((row / kLineRows) & (kUnits - 1))) << 4));
+            };
+            const int px = lane % kUnits, pr = lane / kUnits, pc = c0 + 8 * px;
+            // what is read besides goes out before the tile's sums are complete
+            if constexpr (kPack) {
+                __syncwarp();  // the last tile's rows have left shared memory
+                if (ACCESS == kPackedResidual && whole && pc < p.N) {
+                    const uint16_t *q = static_cast<const uint16_t *>(p.residual) + (long long)(r0 + pr) * p.ld_res + pc;
+#pragma unroll
+                    for (int j = 0; j < 32; j += kStepRows, q += kStepRows * p.ld_res) {
+                        if (r0 + pr + j >= p.M) break;
+                        const uint4 w = *reinterpret_cast<const uint4 *>(q);
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(slot(pr + j, px)), "r"(w.x),
+                                     "r"(w.y), "r"(w.z), "r"(w.w)
+                                     : "memory");
+                    }
+                }
+                if (ACCESS == kPackedResidual) __syncwarp();
+            }
             if (ACCESS == kFours && whole) group_load<EPI, kBatch>(p, r0 + row_of(0), col_of(0), kStep, in);
             // one warp polls, the others sleep at the barrier
             const bool ok = warp != 2 || wait_phase(tfull_bar(t), ((uint32_t)job >> 1) & 1u, args, &s_abort);
@@ -441,15 +465,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
                 else
                     ptx::mbar_arrive_remote_relaxed(ptx::map_to_rank(tempty_bar(t), 0u));
             };
-            if (ACCESS == kPacked && whole) {
-                if constexpr (ACCESS == kPacked) {
-                    // A row of the warp's columns, packed to 16 bits, is kUnits units of
-                    // 16 bytes; those of the rows of a 128-byte line are interleaved.
-                    constexpr int kUnits = kWarpCols / 8, kLineRows = 8 / kUnits;
-                    auto slot = [&](int row, int x) {
-                        return mine + (uint32_t)(row * kUnits * 16 + ((x ^ ((row / kLineRows) & (kUnits - 1))) << 4));
-                    };
-                    __syncwarp();  // the last tile's rows have been read
+            if (kPack && whole) {
+                if constexpr (kPack) {
                     constexpr int kTake = EPI == kEpiLinear ? 32 : 16;  // columns at a time
                     const bool half = p.out_type == kFp16;
 #pragma unroll(EPI == kEpiLinear ? kWarpCols / kTake : 1)
@@ -466,6 +483,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
                         if constexpr (epi_linear(EPI))
                             if (p.bias != nullptr) packed_bias<kTake>(p, c0 + g, half, v);
                         if constexpr (EPI != kEpiLinear) act_values<kTake>(p.act, v);
+                        if constexpr (ACCESS == kPackedResidual)
+#pragma unroll
+                            for (int h = 0; h < kTake / 8; ++h) {
+                                uint32_t w[4];
+                                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                             : "r"(slot(lane, g / 8 + h))
+                                             : "memory");
+                                add_values(half, w, v + 8 * h);
+                            }
                         if constexpr (EPI == kEpiGated)
 #pragma unroll
                             for (int e = 0; e < kTake; ++e) v[e] *= __uint_as_float(raw2[e]);
@@ -478,20 +505,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
                                          : "memory");
                     }
                     read_out();
-                    constexpr int kStepRows = 32 / kUnits;
-                    const int x = lane % kUnits, c = c0 + 8 * x;
-                    int r = lane / kUnits;
-                    uint16_t *q = static_cast<uint16_t *>(p.out) + (long long)(r0 + r) * p.ld_out + c;
-                    if (c < p.N)
+                    if (pc < p.N) {
+                        uint16_t *q = static_cast<uint16_t *>(p.out) + (long long)(r0 + pr) * p.ld_out + pc;
 #pragma unroll
-                        for (int j = 0; j < 32; j += kStepRows, r += kStepRows, q += kStepRows * p.ld_out) {
+                        for (int j = 0; j < 32; j += kStepRows, q += kStepRows * p.ld_out) {
                             uint4 w;
                             asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                                          : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                                         : "r"(slot(r, x))
+                                         : "r"(slot(pr + j, px))
                                          : "memory");
-                            if (r0 + r < p.M) *reinterpret_cast<uint4 *>(q) = w;
+                            if (r0 + pr + j < p.M) *reinterpret_cast<uint4 *>(q) = w;
                         }
+                    }
                 }
                 continue;
             }
@@ -614,6 +639,8 @@ const void *kernel_of(int form, int epi, int bn, Access access) {
     ROUTE_GEMM3(kFormNT, kEpiLinear)
     ROUTE_GEMM3(kFormNT, kEpiAct)
     ROUTE_GEMM3(kFormNT, kEpiGated)
+    ROUTE_GEMM(kFormNT, kEpiLinear, kPackedResidual)
+    ROUTE_GEMM(kFormNT, kEpiAct, kPackedResidual)
     ROUTE_GEMM(kFormNN, kEpiDGate, kColumns)
     ROUTE_GEMM(kFormNN, kEpiDGate, kFours)
     ROUTE_GEMM3(kFormMixed, kEpiLinear)
@@ -628,7 +655,7 @@ cudaError_t gemm_configure() {
     for (int form : {kFormNT, kFormNN, kFormMixed})
         for (int epi = 0; epi < kEpiCount; ++epi)
             for (int bn : {256, 128})
-                for (Access access : {kColumns, kFours, kPacked})
+                for (Access access : {kColumns, kFours, kPacked, kPackedResidual})
                     if (const void *k = kernel_of(form, epi, bn, access)) {
                         const cudaError_t e = cudaFuncSetAttribute(
                             k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(bn));
@@ -641,13 +668,20 @@ int gemm_smem_bytes() { return (int)(smem_of(256) > smem_of(128) ? smem_of(256) 
 
 cudaError_t gemm_launch(int form, int epi, int bn, const GemmMaps &maps, const GemmArgs &args,
                         cudaStream_t stream) {
-    bool fours = true, packed = epi != kEpiDGate;
+    // A residual is read packed only where a tile's products take longer than
+    // that, since no buffer is left to read it a tile ahead (4096x3584x7168 132.7
+    // us, by fours 135.5; 4096x1024x3584 28.0, by fours 27.3).
+    constexpr int kResidualBlocks = 24;
+    bool fours = true, packed = epi != kEpiDGate, residual = false;
     for (int i = 0; i < args.nprob; ++i) {
         const Epilogue &e = args.p[i].e;
         fours = fours && (e.vec & kVecOut);
-        packed = packed && (e.vec & kVecPacked) && e.N % 8 == 0 && e.saved == nullptr && e.residual == nullptr;
+        packed = packed && (e.vec & kVecPacked) && e.N % 8 == 0 && e.saved == nullptr;
+        residual = residual || e.residual != nullptr;
+        if (e.residual != nullptr && args.p[i].kblocks < kResidualBlocks) packed = false;
     }
-    const void *k = kernel_of(form, epi, bn, packed ? kPacked : fours ? kFours : kColumns);
+    const Access access = packed ? (residual ? kPackedResidual : kPacked) : fours ? kFours : kColumns;
+    const void *k = kernel_of(form, epi, bn, access);
     if (k == nullptr || args.pairs <= 0 || args.items <= 0) return cudaErrorInvalidConfiguration;
     void *params[] = {const_cast<GemmMaps *>(&maps), const_cast<GemmArgs *>(&args)};
     return launch_chained(k, dim3(2 * args.pairs), dim3(gemm_threads(epi)), smem_of(bn), params, stream);

@@ -234,8 +234,8 @@ __device__ __forceinline__ void store4(void *p, int type, long long i, int n, bo
 
 // Epilogue::vec: rows that may be read and written four values at a time.
 constexpr int kVecOut = 1, kVecRes = 2, kVecBias = 4;
-// 16-bit rows of the result, and the bias, that may be accessed eight values
-// at a time.
+// 16-bit rows of the result and the residual, and the bias, that may be
+// accessed eight values at a time.
 constexpr int kVecPacked = 8;
 
 // The epilogues work on four columns of a row a thread, neighbouring threads
@@ -494,6 +494,21 @@ __device__ __forceinline__ void group_epilogue(const Epilogue &p, int r, int c, 
 
 // ---- a row's columns a thread, to be stored as 16-bit values ------------------
 
+__device__ __forceinline__ void add_values(bool half, const uint32_t (&w)[4], float *v) {
+    if (half) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack16(w[e], kFp16);
+            v[2 * e] += f.x, v[2 * e + 1] += f.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack16(w[e], kBf16);
+            v[2 * e] += f.x, v[2 * e + 1] += f.y;
+        }
+    }
+}
 template <int W>
 __device__ __forceinline__ void packed_bias(const Epilogue &p, int c, bool half, float (&v)[W]) {
     const uint16_t *b = static_cast<const uint16_t *>(p.bias) + c;
@@ -502,11 +517,7 @@ __device__ __forceinline__ void packed_bias(const Epilogue &p, int c, bool half,
         if (c + h >= p.N) break;
         const uint4 t = *reinterpret_cast<const uint4 *>(b + h);
         const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack16(w[e], half ? kFp16 : kBf16);
-            v[h + 2 * e] += f.x, v[h + 2 * e + 1] += f.y;
-        }
+        add_values(half, w, v + h);
     }
 }
 template <int W>
