@@ -603,3 +603,56 @@ def test_norm_gradients_against_differences(rows, dim, dt):
         diff = (loss(*hi) - loss(*lo)) / 2e-4
         got = grad.double() * v
         assert abs(diff - float(got.sum())) <= (rel + 1e-6) * float(got.abs().sum()) + 1e-6
+
+
+# ---- rows of the result at every alignment, in the products' large tiles ---------
+
+@pytest.mark.parametrize("dt,act", [(BF16, "none"), (FP16, "silu")])
+@pytest.mark.parametrize("k", [72, 1608])  # a short contraction, and one past every rule on lengths
+@pytest.mark.parametrize("pad,offset", [(0, 0), (8, 8), (4, 4), (1, 3)])
+def test_large_tiles_with_rows_of_any_alignment(dt, act, k, pad, offset):
+    rows, n = 1097, 3528  # no tile's multiples
+    x, W = normal(61, rows, k, dt=dt), normal(62, k, n, scale=k ** -0.5, dt=dt)
+    b = normal(63, 1, n, dt=dt, ld=n, offset=offset)[0]
+    res = normal(64, rows, n, dt=dt, ld=n + pad, offset=offset)
+    with route.LinearPlan(rows, k, n, dt, act=act) as plan:
+        for residual in (None, res):
+            out, guard = blank(rows, n, dt, ld=n + pad, offset=offset)
+            route.linear_forward(plan, x, W, out, bias=b, residual=residual)
+            plan.status()
+            want, _ = ref.linear(x, W, b, residual, act, dt)
+            check("out", out, want)
+            guard()
+        # in place of the residual
+        inplace, guard = blank(rows, n, dt, ld=n + pad, offset=offset)
+        inplace.copy_(res)
+        route.linear_forward(plan, x, W, inplace, bias=b, residual=inplace)
+        plan.status()
+        assert torch.equal(inplace, out)
+        guard()
+
+
+@pytest.mark.parametrize("rows", [1, 15, 128, 129, 700, 2300])
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("offset", [0, 3])
+def test_bias_gradient_alone_and_beside_the_products(rows, act, offset):
+    # with an offset the rows start at any alignment, and the products copy them
+    k, n, dt = 200, 521 if offset else 520, BF16
+    x = normal(71, rows, k, dt=dt)
+    W = normal(72, k, n, scale=k ** -0.5, dt=dt)
+    dout = normal(73, rows, n, dt=dt, ld=n + 2, offset=offset) if offset else normal(73, rows, n, dt=dt)
+    with route.LinearPlan(rows, k, n, dt, act=act, train=True) as plan:
+        saved = plan.new_saved()
+        out = torch.empty(rows, n, dtype=dt, device=DEV)
+        route.linear_forward(plan, x, W, out, saved=saved)
+        got = []
+        for what in ((), ("dx",), ("dx", "dW"), ("dW",), ()):
+            dbias = torch.full((n,), float("nan"), dtype=dt, device=DEV)
+            bufs = {"dx": torch.empty_like(x), "dW": torch.empty_like(W)}
+            route.linear_backward(plan, dout, x, W, saved=saved, dbias=dbias, **{w: bufs[w] for w in what})
+            got.append(dbias)
+        plan.status()
+    z = ref.linear(x, W, None, None, act, dt)[1]
+    check("dbias", got[0], ref.linear_grads(x, W, z, dout, act, dt)["dbias"])
+    for g in got[1:]:
+        assert torch.equal(g, got[0])
