@@ -61,13 +61,15 @@ def declare(L) -> None:
 
 
 _TYPES = None
+_FP32 = _UINT8 = None  # torch's, once a plan exists
 
 
 def _type_code(dtype) -> int:
-    global _TYPES
+    global _TYPES, _FP32, _UINT8
     if _TYPES is None:
         import torch
         _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+        _FP32, _UINT8 = torch.float32, torch.uint8
     try:
         return _TYPES[dtype]
     except (KeyError, TypeError):
@@ -94,6 +96,8 @@ class _LayerPlan:
         self.rows = int(rows)
         self.dtype = dtype
         self.device = int(device)
+        # what a training forward call keeps of each row
+        self.saved_row = _route._lib.route_layer_saved_bytes(h, 1)
 
     @property
     def handle(self) -> ctypes.c_void_p:
@@ -213,8 +217,7 @@ def _vec(t, name, n, dtype, device):
 def _stats(t, rows, device, need):
     if t is None and not need:
         return None
-    import torch
-    p, ld = _mat(t, "stats", rows, 2, torch.float32, device)
+    p, ld = _mat(t, "stats", rows, 2, _FP32, device)
     if ld != 2 and rows > 1:
         raise ValueError("stats must be contiguous")
     return p
@@ -223,15 +226,18 @@ def _stats(t, rows, device, need):
 def _saved(plan, t, rows):
     if t is None:
         return None
+    try:
+        if (t.dtype is _UINT8 and t.get_device() == plan.device and t.is_contiguous()
+                and t.numel() >= rows * plan.saved_row):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     import torch
-    need = plan.saved_bytes(rows)
     if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
         raise TypeError("saved must be a uint8 tensor (plan.new_saved())")
     if not t.is_cuda or t.get_device() != plan.device or not t.is_contiguous():
         raise ValueError(f"saved must be contiguous and on cuda:{plan.device}")
-    if t.numel() < need:
-        raise ValueError(f"saved holds {t.numel()} bytes; {rows} rows need {need}")
-    return t.data_ptr()
+    raise ValueError(f"saved holds {t.numel()} bytes; {rows} rows need {rows * plan.saved_row}")
 
 
 def _rows(t, name):
@@ -275,28 +281,29 @@ def norm_forward(plan: NormPlan, x, gamma, beta, out, stats=None, eps: float = 1
     """``out = (x - mean) rstd gamma + beta``; `stats` [rows, 2] FP32 receives
     (mean, rstd).  gamma and beta may be None."""
     R, d, dev, dt = _rows(x, "x"), plan.dim, plan.device, plan.dtype
-    _call("route_norm_forward", plan, R, *_mat(x, "x", R, d, dt, dev), _vec(gamma, "gamma", d, dt, dev),
-        _vec(beta, "beta", d, dt, dev), eps, *_mat(out, "out", R, d, dt, dev),
-        _stats(stats, R, dev, False), _stream(stream, dev))
+    _call("route_norm_forward", plan, R, *_mat(x, "x", R, d, dt, dev),
+          _vec(gamma, "gamma", d, dt, dev), _vec(beta, "beta", d, dt, dev), eps,
+          *_mat(out, "out", R, d, dt, dev), _stats(stats, R, dev, False), _stream(stream, dev))
 
 
 def norm_backward(plan: NormPlan, dout, x, gamma, stats, dx=None, dgamma=None, dbeta=None,
                   stream=None) -> None:
     R, d, dev, dt = _rows(dout, "dout"), plan.dim, plan.device, plan.dtype
-    _call("route_norm_backward", plan, R, *_mat(dout, "dout", R, d, dt, dev), *_mat(x, "x", R, d, dt, dev),
-        _vec(gamma, "gamma", d, dt, dev), _stats(stats, R, dev, True),
-        *_opt_mat(dx, "dx", R, d, dt, dev), _vec(dgamma, "dgamma", d, dt, dev),
-        _vec(dbeta, "dbeta", d, dt, dev), _stream(stream, dev))
+    _call("route_norm_backward", plan, R, *_mat(dout, "dout", R, d, dt, dev),
+          *_mat(x, "x", R, d, dt, dev), _vec(gamma, "gamma", d, dt, dev),
+          _stats(stats, R, dev, True), *_opt_mat(dx, "dx", R, d, dt, dev),
+          _vec(dgamma, "dgamma", d, dt, dev), _vec(dbeta, "dbeta", d, dt, dev),
+          _stream(stream, dev))
 
 
 def linear_forward(plan: LinearPlan, x, W, out, bias=None, residual=None, saved=None,
                    stream=None) -> None:
     R, k, n, dev, dt = _rows(x, "x"), plan.k, plan.n, plan.device, plan.dtype
-    _call("route_linear_forward", plan, R, *_mat(x, "x", R, k, dt, dev), *_mat(W, "W", k, n, dt, dev),
-        _vec(bias, "bias", n, dt, dev),
-        *_opt_mat(residual, "residual", R, n, plan.out_dtype, dev),
-        *_mat(out, "out", R, n, plan.out_dtype, dev), _saved(plan, saved, R),
-        _stream(stream, dev))
+    _call("route_linear_forward", plan, R, *_mat(x, "x", R, k, dt, dev),
+          *_mat(W, "W", k, n, dt, dev), _vec(bias, "bias", n, dt, dev),
+          *_opt_mat(residual, "residual", R, n, plan.out_dtype, dev),
+          *_mat(out, "out", R, n, plan.out_dtype, dev), _saved(plan, saved, R),
+          _stream(stream, dev))
 
 
 def linear_backward(plan: LinearPlan, dout, x, W, saved=None, dx=None, dW=None, dbias=None,
@@ -304,27 +311,28 @@ def linear_backward(plan: LinearPlan, dout, x, W, saved=None, dx=None, dW=None, 
     """`saved`: what the forward call kept (plans with an activation).  x may
     be None without dW, W without dx."""
     R, k, n, dev, dt = _rows(dout, "dout"), plan.k, plan.n, plan.device, plan.dtype
-    _call("route_linear_backward", plan, R, *_mat(dout, "dout", R, n, dt, dev), *_opt_mat(x, "x", R, k, dt, dev),
-        *_opt_mat(W, "W", k, n, dt, dev), _saved(plan, saved, R),
-        *_opt_mat(dx, "dx", R, k, dt, dev), *_opt_mat(dW, "dW", k, n, dt, dev),
-        _vec(dbias, "dbias", n, dt, dev), _stream(stream, dev))
+    _call("route_linear_backward", plan, R, *_mat(dout, "dout", R, n, dt, dev),
+          *_opt_mat(x, "x", R, k, dt, dev), *_opt_mat(W, "W", k, n, dt, dev),
+          _saved(plan, saved, R), *_opt_mat(dx, "dx", R, k, dt, dev),
+          *_opt_mat(dW, "dW", k, n, dt, dev), _vec(dbias, "dbias", n, dt, dev),
+          _stream(stream, dev))
 
 
 def gated_forward(plan: GatedPlan, x, W_gate, W_up, W_down, out, residual=None, saved=None,
                   stream=None) -> None:
     R, k, f, n, dev, dt = _rows(x, "x"), plan.k, plan.f, plan.n, plan.device, plan.dtype
-    _call("route_gated_forward", plan, R, *_mat(x, "x", R, k, dt, dev), *_mat(W_gate, "W_gate", k, f, dt, dev),
-        *_mat(W_up, "W_up", k, f, dt, dev), *_mat(W_down, "W_down", f, n, dt, dev),
-        *_opt_mat(residual, "residual", R, n, dt, dev), *_mat(out, "out", R, n, dt, dev),
-        _saved(plan, saved, R), _stream(stream, dev))
+    _call("route_gated_forward", plan, R, *_mat(x, "x", R, k, dt, dev),
+          *_mat(W_gate, "W_gate", k, f, dt, dev), *_mat(W_up, "W_up", k, f, dt, dev),
+          *_mat(W_down, "W_down", f, n, dt, dev), *_opt_mat(residual, "residual", R, n, dt, dev),
+          *_mat(out, "out", R, n, dt, dev), _saved(plan, saved, R), _stream(stream, dev))
 
 
 def gated_backward(plan: GatedPlan, dout, x, W_gate, W_up, W_down, saved, dx=None, dW_gate=None,
                    dW_up=None, dW_down=None, stream=None) -> None:
     R, k, f, n, dev, dt = _rows(dout, "dout"), plan.k, plan.f, plan.n, plan.device, plan.dtype
-    _call("route_gated_backward", plan, R, *_mat(dout, "dout", R, n, dt, dev), *_mat(x, "x", R, k, dt, dev),
-        *_mat(W_gate, "W_gate", k, f, dt, dev), *_mat(W_up, "W_up", k, f, dt, dev),
-        *_mat(W_down, "W_down", f, n, dt, dev), _saved(plan, saved, R),
-        *_opt_mat(dx, "dx", R, k, dt, dev), *_opt_mat(dW_gate, "dW_gate", k, f, dt, dev),
-        *_opt_mat(dW_up, "dW_up", k, f, dt, dev), *_opt_mat(dW_down, "dW_down", f, n, dt, dev),
-        _stream(stream, dev))
+    _call("route_gated_backward", plan, R, *_mat(dout, "dout", R, n, dt, dev),
+          *_mat(x, "x", R, k, dt, dev), *_mat(W_gate, "W_gate", k, f, dt, dev),
+          *_mat(W_up, "W_up", k, f, dt, dev), *_mat(W_down, "W_down", f, n, dt, dev),
+          _saved(plan, saved, R), *_opt_mat(dx, "dx", R, k, dt, dev),
+          *_opt_mat(dW_gate, "dW_gate", k, f, dt, dev), *_opt_mat(dW_up, "dW_up", k, f, dt, dev),
+          *_opt_mat(dW_down, "dW_down", f, n, dt, dev), _stream(stream, dev))
