@@ -8,13 +8,18 @@ spills, shared memory) is written to ``_build/ptxas.log``.
 in the kernels, and a failed check is reported through the device status
 word (``route_device_status`` returns ROUTE_ERR_DEVICE_BOUNDS) instead of
 faulting.  The binding loads it when the environment sets ROUTE_DEBUG_LIB=1.
+
+With either goes ``_build/_layer_call.so``, the Python module of the layer
+operators' calls (``csrc/layer_call.cpp``, host code only).
 """
 
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -25,6 +30,8 @@ LIB = os.path.join(BUILD, "libroute.so")
 DEBUG_BUILD = os.path.join(BUILD, "debug")
 DEBUG_LIB = os.path.join(DEBUG_BUILD, "libroute_debug.so")
 INCLUDE = os.path.join(ROOT, "include")
+CALL_MODULE = os.path.join(BUILD, "_layer_call.so")
+CALL_SOURCE = os.path.join(CSRC, "layer_call.cpp")
 
 SOURCES = ["decode_kernel.cu", "prefill_kernel.cu", "topk_kernel.cu", "stage_kernel.cu",
            "route_api.cu", "layer_gemm.cu", "layer_small.cu", "layer_elem.cu",
@@ -45,11 +52,11 @@ def _inputs():
     return files
 
 
-def _stale(lib: str) -> bool:
+def _stale(lib: str, inputs: list | None = None) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    return any(os.path.getmtime(f) > t for f in _inputs())
+    return any(os.path.getmtime(f) > t for f in inputs or _inputs())
 
 
 def _compile(src: str, build_dir: str, extra: list) -> tuple[str, str]:
@@ -70,6 +77,19 @@ def _link(objs: list, lib: str) -> None:
     os.replace(tmp, lib)
 
 
+def _compile_call_module() -> None:
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    tmp = CALL_MODULE + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", CALL_SOURCE,
+           "-o", tmp, "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(torch, "include"), "-L", os.path.join(torch, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for layer_call.cpp:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, CALL_MODULE)
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False,
           both: bool = False) -> str:
     """Build the release library (or, with debug=True, the checked one; with
@@ -79,12 +99,21 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False,
     if debug or both:
         targets.append((DEBUG_LIB, DEBUG_BUILD, ["-DROUTE_DEBUG"]))
     todo = [(lib, d, x) for lib, d, x in targets if force or _stale(lib)]
+    call_inputs = [CALL_SOURCE, os.path.join(INCLUDE, "route.h"),
+                   os.path.join(INCLUDE, "route_layer.h"), os.path.abspath(__file__)]
+    call = force or _stale(CALL_MODULE, call_inputs)
+    os.makedirs(BUILD, exist_ok=True)
+    if not todo and call:
+        _compile_call_module()
     if todo:
         for _, d, _ in todo:
             os.makedirs(d, exist_ok=True)
         jobs = [(src, d, x) for _, d, x in todo for src in SOURCES]
-        with ThreadPoolExecutor(max_workers=len(jobs)) as pool:
+        with ThreadPoolExecutor(max_workers=len(jobs) + 1) as pool:
+            module = pool.submit(_compile_call_module) if call else None
             results = list(pool.map(lambda j: _compile(*j), jobs))
+            if module:
+                module.result()
         for k, (lib, d, _) in enumerate(todo):
             part = results[k * len(SOURCES):(k + 1) * len(SOURCES)]
             with open(os.path.join(d, "ptxas.log"), "w") as f:

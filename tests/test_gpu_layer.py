@@ -656,3 +656,45 @@ def test_bias_gradient_alone_and_beside_the_products(rows, act, offset):
     check("dbias", got[0], ref.linear_grads(x, W, z, dout, act, dt)["dbias"])
     for g in got[1:]:
         assert torch.equal(g, got[0])
+
+
+def test_calls_by_either_way_are_the_same():
+    """The compiled way of a call (taken here) and the checks in Python (taken
+    with a stream given) reach the same entry points with the same arguments."""
+    rows, k, f, n, dt = 70, 200, 136, 264, BF16
+    s = torch.cuda.current_stream()
+    x = normal(81, rows, k, dt=dt, ld=k + 8)
+    Wg, Wu, Wd = (normal(82 + i, a, b, scale=a ** -0.5, dt=dt) for i, (a, b) in
+                  enumerate(((k, f), (k, f), (f, n))))
+    W, b, res = normal(85, k, n, scale=k ** -0.5, dt=dt), normal(86, n, dt=dt), normal(87, rows, n, dt=dt)
+    dout, dk = normal(88, rows, n, dt=dt), normal(89, rows, k, dt=dt)
+    gamma = torch.nn.Parameter(normal(90, k, dt=dt))  # a subclass, and one that autograd watches
+    got = []
+    with route.NormPlan(rows, k, dt) as np, route.LinearPlan(rows, k, n, dt, act="gelu", train=True) as lp, \
+            route.GatedPlan(rows, k, f, n, dt, train=True) as gp:
+        for stream in (None, s, s.cuda_stream):
+            e = lambda *shape, d=dt: torch.full(shape, float("nan"), dtype=d, device=DEV)  # noqa: E731
+            o = [e(rows, k), e(rows, 2, d=FP32), e(rows, k), e(k), e(k), e(rows, n), e(rows, k), e(k, n), e(n),
+                 e(rows, n), e(rows, k), e(k, f), e(k, f), e(f, n)]
+            ls, gs = lp.new_saved(), gp.new_saved()
+            route.norm_forward(np, x, gamma, None, o[0], stats=o[1], eps=0.5, stream=stream)
+            route.norm_backward(np, dk, x, gamma, o[1], dx=o[2], dgamma=o[3], dbeta=o[4], stream=stream)
+            route.linear_forward(lp, x, W, o[5], bias=b, residual=res, saved=ls, stream=stream)
+            route.linear_backward(lp, dout, x, W, saved=ls, dx=o[6], dW=o[7], dbias=o[8], stream=stream)
+            route.gated_forward(gp, x, Wg, Wu, Wd, o[9], residual=res, saved=gs, stream=stream)
+            route.gated_backward(gp, dout, x, Wg, Wu, Wd, gs, dx=o[10], dW_gate=o[11], dW_up=o[12],
+                                 dW_down=o[13], stream=stream)
+            for p in (np, lp, gp):
+                p.status()
+            got.append(o)
+        # an integer eps goes through the checks
+        y = torch.empty_like(got[0][0])
+        route.norm_forward(np, x, gamma, None, y, eps=0)
+        z = torch.empty_like(y)
+        route.norm_forward(np, x, gamma, None, z, eps=0.0)
+        assert torch.equal(y, z)
+    for others in got[1:]:
+        for a, c in zip(got[0], others):
+            assert not bool(torch.isnan(a).any()) and torch.equal(a, c)
+    with pytest.raises(route.RouteError):
+        route.norm_forward(np, x, gamma, None, y)  # closed

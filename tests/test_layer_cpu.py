@@ -162,3 +162,34 @@ def test_reference_bound_sees_a_dropped_term():
     assert ref.worst((want[0] - x[:, 9:10].double() @ W[9:10].double()).bfloat16(), want) > 1
     assert ref.worst((want[0] - b.double()).bfloat16(), want) > 1
     assert ref.worst(torch.full_like(good, float("nan")), want) == float("inf")
+
+
+def test_short_way_leaves_what_is_not_plain_to_the_checks(lib):
+    """The compiled module of the calls refuses with -1 and raises nothing."""
+    from latent_projection_top_gb300 import layer
+    short = layer._short_way()
+    bf16 = torch.bfloat16
+    plan = (1, 0, 0, 0, 8, 16, 8, 64)  # never passed on: no tensor here is on a GPU
+    x, W = torch.zeros(4, 8, dtype=bf16), torch.zeros(8, 8, dtype=bf16)
+    v, stats = torch.zeros(8, dtype=bf16), torch.zeros(4, 2)
+    for call in (
+        lambda: short.norm_forward(),
+        lambda: short.norm_forward(plan),
+        lambda: short.norm_forward(plan, x, v, v, x, stats, 1e-5, 0),
+        lambda: short.norm_forward(None, x, v, v, x, stats, 1e-5, 0),
+        lambda: short.norm_forward(("a",) * 8, x, v, v, x, stats, 1e-5, 0),
+        lambda: short.norm_forward((0,) * 8, x, v, v, x, stats, 1e-5, 0),
+        lambda: short.norm_forward(plan, None, v, v, x, stats, 1e-5, 0),
+        lambda: short.norm_forward(plan, [1], v, v, "x", stats, "eps", None),
+        lambda: short.norm_forward(plan, x.to_sparse(), v, v, x, stats, 1e-5, 0),
+        lambda: short.norm_forward(plan, torch.empty(4, 8, dtype=bf16, device="meta"), v, v, x,
+                                   stats, 1e-5, 0),
+        lambda: short.norm_backward(plan, x, x, v, stats, None, None, None, 0),
+        lambda: short.linear_forward(plan, x, W, x, None, None, None, 0),
+        lambda: short.linear_backward(plan, x, x, W, None, None, None, None, 0),
+        lambda: short.gated_forward(plan, x, W, W, W, x, None, None, 0),
+        lambda: short.gated_backward(plan, x, x, W, W, W, None, None, None, None, None, 0),
+    ):
+        assert call() == -1
+    with pytest.raises(TypeError):
+        short.bind(1)
