@@ -143,6 +143,7 @@ int vec_bits(const void *out, long long ld_out, const void *out2, const void *re
     if (rows_on(out, ld_out) && rows_on(out2, ld_out)) v |= kVecOut;
     if (rows_on(res, ld_res)) v |= kVecRes;
     if (aligned(bias, 8)) v |= kVecBias;
+    if (out_type != kFp32 && aligned(bias, 16)) v |= kVecAny;
     if (out_type != kFp32 && aligned(out, 16) && ld_out % 8 == 0 && aligned(bias, 16) && aligned(res, 16) &&
         (res == nullptr || ld_res % 8 == 0))
         v |= kVecPacked;

@@ -247,8 +247,10 @@ __device__ __forceinline__ bool mma_tile(Stages<BN> &st, int kblocks, uint32_t d
 // only besides the sums, finished and packed by the thread that took a row's
 // columns out of TMEM, so that half the bytes go through shared memory, in one
 // pass, and a row leaves in whole 128-byte lines (4096x64x7168 15.6 us, by
-// fours 23.3; 64x3584x7168's backward pass 32.8, by fours 39.4).
-enum Access { kColumns = 0, kFours = 1, kPacked = 2, kPackedResidual = 3 };
+// fours 23.3; 64x3584x7168's backward pass 32.8, by fours 39.4).  Packed rows
+// of odd widths leave by 4-byte words (4096x64x7167 32.0, by columns 55.1;
+// rows that take fours are better off with them, 4096x64x7164 26.0 and 29.7).
+enum Access { kColumns = 0, kFours = 1, kPacked = 2, kPackedResidual = 3, kPackedAny = 4 };
 template <int FORM, int EPI, int BN, int ACCESS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1)
     layer_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs args) {
@@ -257,7 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
     constexpr int kTileCols = EPI == kEpiGated ? BN / 2 : BN;  // columns of D a tile
     constexpr int kBCols = BN / 2;                             // B columns each CTA loads
     constexpr int kEpiWarps = epi_warps(EPI);
-    constexpr bool kPack = ACCESS == kPacked || ACCESS == kPackedResidual;
+    constexpr bool kPack = ACCESS == kPacked || ACCESS == kPackedResidual || ACCESS == kPackedAny;
     constexpr int kWarpCols = kTileCols / (kEpiWarps / 4);     // columns of D an epilogue warp drains
     static_assert(kWarpCols % kG == 0 && kG % 16 == 0, "whole groups");
     extern __shared__ uint8_t smem_raw[];
@@ -505,7 +507,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
                                          : "memory");
                     }
                     read_out();
-                    if (pc < p.N) {
+                    if constexpr (ACCESS == kPackedAny) {
+                        // Rows that start at any element: a thread has a word (two columns)
+                        // of the row, and where the row starts at an odd element stores the
+                        // second with the next thread's first.
+                        constexpr int kWords = kWarpCols / 2;
+                        const int x = lane % kWords, n = p.N - c0;
+                        int r = lane / kWords;
+                        uint16_t *q = static_cast<uint16_t *>(p.out) + (long long)(r0 + r) * p.ld_out + c0;
+#pragma unroll 8
+                        for (int j = 0; j < 32; j += 32 / kWords, r += 32 / kWords, q += 32 / kWords * p.ld_out) {
+                            uint32_t w;
+                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(slot(r, x / 4) + x % 4 * 4) : "memory");
+                            const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w, 1, kWords);
+                            if (r0 + r >= p.M) continue;
+                            const int odd = (int)(reinterpret_cast<uintptr_t>(q) >> 1) & 1, c = 2 * x + odd;
+                            const uint32_t v = odd ? __byte_perm(w, next, 0x5432) : w;
+                            if (c + 1 < n && !(odd && x == kWords - 1))
+                                *reinterpret_cast<uint32_t *>(q + c) = v;
+                            else if (c < n)
+                                q[c] = (uint16_t)v;
+                            if (odd && x == 0 && n > 0) q[0] = (uint16_t)w;
+                        }
+                    } else if (pc < p.N) {
                         uint16_t *q = static_cast<uint16_t *>(p.out) + (long long)(r0 + pr) * p.ld_out + pc;
 #pragma unroll
                         for (int j = 0; j < 32; j += kStepRows, q += kStepRows * p.ld_out) {
@@ -603,7 +627,7 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
     float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
     EpiIn<EPI> in;
     epi_load<EPI>(a.e, r, c, in);
-#pragma unroll 4
+#pragma unroll 8
     for (int s = 0; s < a.splits; ++s, src += step) {
         const float4 x = *reinterpret_cast<const float4 *>(src);
         v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
@@ -635,16 +659,17 @@ const void *kernel_of(int form, int epi, int bn, Access access) {
     if (form == F && epi == E && access == A)                                                  \
         return bn == 256 ? reinterpret_cast<const void *>(layer_gemm_kernel<F, E, 256, A>)     \
                          : reinterpret_cast<const void *>(layer_gemm_kernel<F, E, 128, A>);
-#define ROUTE_GEMM3(F, E) ROUTE_GEMM(F, E, kColumns) ROUTE_GEMM(F, E, kFours) ROUTE_GEMM(F, E, kPacked)
-    ROUTE_GEMM3(kFormNT, kEpiLinear)
-    ROUTE_GEMM3(kFormNT, kEpiAct)
-    ROUTE_GEMM3(kFormNT, kEpiGated)
+#define ROUTE_GEMM4(F, E) \
+    ROUTE_GEMM(F, E, kColumns) ROUTE_GEMM(F, E, kFours) ROUTE_GEMM(F, E, kPacked) ROUTE_GEMM(F, E, kPackedAny)
+    ROUTE_GEMM4(kFormNT, kEpiLinear)
+    ROUTE_GEMM4(kFormNT, kEpiAct)
+    ROUTE_GEMM4(kFormNT, kEpiGated)
     ROUTE_GEMM(kFormNT, kEpiLinear, kPackedResidual)
     ROUTE_GEMM(kFormNT, kEpiAct, kPackedResidual)
     ROUTE_GEMM(kFormNN, kEpiDGate, kColumns)
     ROUTE_GEMM(kFormNN, kEpiDGate, kFours)
-    ROUTE_GEMM3(kFormMixed, kEpiLinear)
-#undef ROUTE_GEMM3
+    ROUTE_GEMM4(kFormMixed, kEpiLinear)
+#undef ROUTE_GEMM4
 #undef ROUTE_GEMM
     return nullptr;
 }
@@ -655,7 +680,7 @@ cudaError_t gemm_configure() {
     for (int form : {kFormNT, kFormNN, kFormMixed})
         for (int epi = 0; epi < kEpiCount; ++epi)
             for (int bn : {256, 128})
-                for (Access access : {kColumns, kFours, kPacked, kPackedResidual})
+                for (Access access : {kColumns, kFours, kPacked, kPackedResidual, kPackedAny})
                     if (const void *k = kernel_of(form, epi, bn, access)) {
                         const cudaError_t e = cudaFuncSetAttribute(
                             k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(bn));
@@ -672,15 +697,19 @@ cudaError_t gemm_launch(int form, int epi, int bn, const GemmMaps &maps, const G
     // that, since no buffer is left to read it a tile ahead (4096x3584x7168 132.7
     // us, by fours 135.5; 4096x1024x3584 28.0, by fours 27.3).
     constexpr int kResidualBlocks = 24;
-    bool fours = true, packed = epi != kEpiDGate, residual = false;
+    bool fours = true, any = epi != kEpiDGate, packed = any, residual = false;
     for (int i = 0; i < args.nprob; ++i) {
         const Epilogue &e = args.p[i].e;
         fours = fours && (e.vec & kVecOut);
+        any = any && (e.vec & kVecAny) && e.saved == nullptr && e.residual == nullptr;
         packed = packed && (e.vec & kVecPacked) && e.N % 8 == 0 && e.saved == nullptr;
         residual = residual || e.residual != nullptr;
         if (e.residual != nullptr && args.p[i].kblocks < kResidualBlocks) packed = false;
     }
-    const Access access = packed ? (residual ? kPackedResidual : kPacked) : fours ? kFours : kColumns;
+    const Access access = packed  ? (residual ? kPackedResidual : kPacked)
+                          : fours ? kFours
+                          : any   ? kPackedAny
+                                  : kColumns;
     const void *k = kernel_of(form, epi, bn, access);
     if (k == nullptr || args.pairs <= 0 || args.items <= 0) return cudaErrorInvalidConfiguration;
     void *params[] = {const_cast<GemmMaps *>(&maps), const_cast<GemmArgs *>(&args)};

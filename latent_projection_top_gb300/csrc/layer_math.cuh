@@ -235,8 +235,8 @@ __device__ __forceinline__ void store4(void *p, int type, long long i, int n, bo
 // Epilogue::vec: rows that may be read and written four values at a time.
 constexpr int kVecOut = 1, kVecRes = 2, kVecBias = 4;
 // 16-bit rows of the result and the residual, and the bias, that may be
-// accessed eight values at a time.
-constexpr int kVecPacked = 8;
+// accessed eight values at a time; of these the bias only.
+constexpr int kVecPacked = 8, kVecAny = 16;
 
 // The epilogues work on four columns of a row a thread, neighbouring threads
 // on neighbouring columns, so that what they read and write of a row is whole
@@ -515,9 +515,15 @@ __device__ __forceinline__ void packed_bias(const Epilogue &p, int c, bool half,
 #pragma unroll
     for (int h = 0; h < W; h += 8) {
         if (c + h >= p.N) break;
-        const uint4 t = *reinterpret_cast<const uint4 *>(b + h);
-        const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-        add_values(half, w, v + h);
+        if (c + h + 8 <= p.N) {
+            const uint4 t = *reinterpret_cast<const uint4 *>(b + h);
+            const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+            add_values(half, w, v + h);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (c + h + e < p.N) v[h + e] += load_elem(b, half ? kFp16 : kBf16, h + e);
+        }
     }
 }
 template <int W>

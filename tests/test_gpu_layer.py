@@ -698,3 +698,32 @@ def test_calls_by_either_way_are_the_same():
             assert not bool(torch.isnan(a).any()) and torch.equal(a, c)
     with pytest.raises(route.RouteError):
         route.norm_forward(np, x, gamma, None, y)  # closed
+
+
+@pytest.mark.parametrize("dt,act", [(BF16, "none"), (FP16, "gelu")])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (0, 1), (1, 1), (2, 3), (4, 2)])
+@pytest.mark.parametrize("rows,n", [(1097, 3527), (1281, 3529), (2050, 449)])
+def test_large_tiles_of_odd_rows(rows, n, dt, act, pad, offset):
+    """No residual, an aligned bias: rows of the result at every alignment, and
+    the gradients dx and dW of odd widths."""
+    k = 73
+    x, W = normal(91, rows, k, dt=dt), normal(92, k, n, scale=k ** -0.5, dt=dt)
+    b, dout = normal(93, n, dt=dt), normal(94, rows, n, dt=dt)
+    with route.LinearPlan(rows, k, n, dt, act=act, train=True) as plan:
+        out, guard = blank(rows, n, dt, ld=n + pad, offset=offset)
+        route.linear_forward(plan, x, W, out, bias=b)
+        saved = plan.new_saved()
+        kept = torch.empty(rows, n, dtype=dt, device=DEV)
+        route.linear_forward(plan, x, W, kept, bias=b, saved=saved)
+        dx, guard_dx = blank(rows, k, dt, ld=k + pad, offset=offset)
+        dW, guard_dW = blank(k, n, dt, ld=n + pad, offset=offset)
+        route.linear_backward(plan, dout, x, W, saved=saved, dx=dx, dW=dW)
+        plan.status()
+    want, z = ref.linear(x, W, b, None, act, dt)
+    check("out", out, want)
+    assert torch.equal(kept, out)
+    grads = ref.linear_grads(x, W, z, dout, act, dt)
+    check("dx", dx, grads["dx"])
+    check("dW", dW, grads["dW"])
+    for g in (guard, guard_dx, guard_dW):
+        g()
