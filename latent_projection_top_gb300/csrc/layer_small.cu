@@ -140,18 +140,20 @@ __global__ void __launch_bounds__(kThreads, 2)
     // columns of one row tile are read once: they leave L2 first
     const uint64_t pol_c = p.tiles_m == 1 ? ptx::policy_evict_first() : ptx::policy_evict_normal();
     const uint64_t pol_r = ptx::policy_evict_last();
+    // (copies of columns that do not exist take as long as others, or longer)
+    const bool second = EPI == kEpiGated || !c_mn || col0 + 64 < p.e.N;
     auto columns_of = [&](int it) {
         const int kb = kb0 + it, s = it % S, seg = kb >= p.kswitch;
         const int k0 = (seg ? kb - p.kswitch : kb) * 64;
         const uint32_t sc = sbase + s * kStage, fb = full_bar(s);
         const CUtensorMap *m = &maps.m[p.b[seg][0]];
-        ptx::mbar_arrive_expect_tx(fb, kColBytes + p.a_bytes);
+        ptx::mbar_arrive_expect_tx(fb, p.a_bytes + (second ? kColBytes : kColBytes / 2));
         if (EPI == kEpiGated) {
             ptx::tma_load_2d(sc, m, fb, col0, k0, pol_c);
             ptx::tma_load_2d(sc + 8192u, &maps.m[p.b[seg][1]], fb, col0, k0, pol_c);
         } else if (c_mn) {
             ptx::tma_load_2d(sc, m, fb, col0, k0, pol_c);
-            ptx::tma_load_2d(sc + 8192u, m, fb, col0 + 64, k0, pol_c);
+            if (second) ptx::tma_load_2d(sc + 8192u, m, fb, col0 + 64, k0, pol_c);
         } else {
             ptx::tma_load_2d(sc, m, fb, k0, col0, pol_c);
         }
