@@ -192,9 +192,10 @@ struct Prod {
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // The choice with the smallest estimated time, from what the kernels measure:
-// a k-block of a pair's 256 x 256 tile takes 0.34 us and of a 256 x 128 tile
-// 0.30 us; the small tiles are bound by what an SM reads, about 70 bytes a
-// nanosecond.
+// a launch of pair tiles has 5.0 us (4.5 with 128 columns) besides its
+// k-blocks, of 0.34 us in a 256 x 256 tile and 0.29 us in a 256 x 128 tile,
+// and 1.8 us more where the epilogue does more than store; the small tiles
+// have 2.6 us and are bound by what an SM reads, about 70 bytes a nanosecond.
 Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
     Choice best = {false, 256, {1, 1, 1, 1}, 1e30};
     double &t_best = best.us;
@@ -207,7 +208,9 @@ Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
     }
     for (int bn : {256, 128}) {
         const int cols = epi == kEpiGated ? bn / 2 : bn;
-        const double kb_us = bn == 256 ? 0.34 : 0.30, drain_us = bn == 256 ? 4.0 : 2.2;
+        const double kb_us = bn == 256 ? 0.34 : 0.29;
+        const double drain_us = (bn == 256 ? 1.0 : 0.55) * (epi == kEpiLinear ? 2.5 : 4.0);
+        const double start_us = (bn == 256 ? 5.0 : 4.5) + (epi == kEpiLinear ? 0.0 : 1.8);
         long long tiles[kGemmMaxProblems];
         double work = 0;
         for (int i = 0; i < count; ++i) {
@@ -219,7 +222,7 @@ Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
         for (double part : {0.0, 2.0, 1.0, 0.7, 0.5, 0.34, 0.25}) {
             Choice c = {false, bn, {1, 1, 1, 1}, 0};
             long long items = 0, split_items = 0;
-            double longest = 0, level = 0, t = 7.0;
+            double longest = 0, level = 0, t = start_us;
             for (int i = 0; i < count; ++i) {
                 int s = part > 0 ? (int)(w[i].kblocks() * p->pairs / (work * part) + 0.99) : 1;
                 s = s > kGemmMaxSplits ? kGemmMaxSplits : s;
@@ -234,7 +237,7 @@ Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
                 level += (double)tiles[i] * s * one / p->pairs;
                 if (s > 1) {
                     split_items += tiles[i] * s;
-                    t += 2.5 + (double)w[i].M * w[i].N * (epi == kEpiGated ? 2 : 1) * 4.0 * (s + 1) / 4e6;
+                    t += 3.5 + (double)w[i].M * w[i].N * (epi == kEpiGated ? 2 : 1) * 4.0 * (s + 1) / 4e6;
                 }
             }
             if (split_items > 2 * p->pairs) continue;
@@ -263,11 +266,11 @@ Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
                 for (int i = 0; i < count; ++i) {
                     const int box = w[i].form != kFormTT && w[i].M < bn ? w[i].M : bn;
                     const double kb = ceil_div(w[i].kblocks(), s) * (16384 + box * 128) / 70e3;
-                    const double drain = (epi == kEpiDGate ? 0.04 : 0.015) * box / s;
+                    const double drain = (epi == kEpiLinear ? 0.025 : 0.045) * box / s;
                     double one = kb + 0.8 + drain;
                     longest = longest < one ? one : longest;
                     // two CTAs of an SM hide each other's start and end, not more
-                    const double half = 0.5 * (6.5 + kb + drain);
+                    const double half = 0.5 * (4.0 + kb + drain);
                     one = one < half ? half : one;
                     const long long ctas = (long long)ceil_div(w[i].M, bn) * ceil_div(w[i].N, cols) * s;
                     level += (double)ctas * one / p->sms;
@@ -277,7 +280,7 @@ Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
                 double t = count > 1 && level > 0 ? level + 0.3 * longest : longest;
                 t = t < longest ? longest : t < level ? level : t;
                 // CTAs past two an SM start when others have left
-                t += 5.0 + 3.0 * (ceil_div(tiles * s, 2 * p->sms) - 1);
+                t += 2.6 + (s > 1 ? 0.3 : 0.0) + 3.0 * (ceil_div(tiles * s, 2 * p->sms) - 1);
                 if (t < t_best) best = {true, bn, {s, s, s, s}, t};
             }
         }
@@ -308,8 +311,9 @@ void set_tiles(GemmProblem &q, int tile_rows, int tile_cols, int pairs) {
 // Who takes which items when there are few of them and their products'
 // contractions differ: the longest first, each to the pair with the least so
 // far.  (Items in turn leave some pairs with two long ones: dx and dW of
-// 2050x896x3584 then take 89 k-blocks where this takes 66.)
-void deal_items(GemmArgs &a, int pairs) {
+// 2050x896x3584 then take 89 k-blocks where this takes 66.)  No item is shorter
+// than a tile's epilogue, `drain` k-blocks.
+void deal_items(GemmArgs &a, int pairs, int drain) {
     // a heap of the pairs, the least loaded (then the lowest) on top
     int heap[kGemmMaxPairs];
     for (int j = 0; j < pairs; ++j) heap[j] = j;
@@ -329,7 +333,7 @@ void deal_items(GemmArgs &a, int pairs) {
     a.listed = 1;
     for (int c = 0; c < a.nprob; ++c) {
         const int items = (c + 1 < a.nprob ? a.p[c + 1].item_base : a.items) - a.p[c].item_base;
-        const int cost = ceil_div(a.p[c].kblocks, a.p[c].splits);
+        const int blocks = ceil_div(a.p[c].kblocks, a.p[c].splits), cost = blocks < drain ? drain : blocks;
         for (int j = 0; j < pairs; ++j) a.count[c][j] = 0;
         for (int i = 0; i < items; ++i) {
             ++a.count[c][heap[0] % kGemmMaxPairs];
@@ -430,7 +434,7 @@ route_status run(const route_layer *p, int epi, Prod *w, int count, const Choice
         return e == cudaSuccess ? ROUTE_OK : cuda_fail(e, "product kernel launch");
     }
     a.pairs = a.items < p->pairs ? a.items : p->pairs;
-    if (count > 1 && a.items <= 4 * p->pairs && p->pairs <= kGemmMaxPairs) deal_items(a, a.pairs);
+    if (count > 1 && a.items <= 4 * p->pairs && p->pairs <= kGemmMaxPairs) deal_items(a, a.pairs, ch.bn == 256 ? 7 : 5);
     a.trigger = more || unfinished > 0;
     const int form = w[0].form == kFormNT ? kFormNT : epi == kEpiDGate ? kFormNN : kFormMixed;
     cudaError_t e = gemm_launch(form, epi, ch.bn, maps, a, stream);
@@ -493,7 +497,7 @@ route_status backward_products(const route_layer *p, int rows, Prod *all, int co
     Prod w[kGemmMaxProblems];
     int n = 0;
     // (the second launch's start hides behind the first)
-    if (input.us + weights.us - 1.0 < one.us) {
+    if (input.us + weights.us + 1.4 < one.us) {
         Prod *dx = all[0].e.out ? all : nullptr;
         for (int i = 1; i < count; ++i)
             if (all[i].e.out) w[n] = all[i], w[n++].id = i - 1;
