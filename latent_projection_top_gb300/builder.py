@@ -37,7 +37,7 @@ SOURCES = ["decode_kernel.cu", "prefill_kernel.cu", "topk_kernel.cu", "stage_ker
            "route_api.cu", "layer_gemm.cu", "layer_small.cu", "layer_elem.cu",
            "layer_norm.cu", "layer_api.cu"]
 HEADERS = ["common.cuh", "sm103_ptx.cuh", "topk16.cuh", "twofloat.cuh", "api_util.h", "layer.cuh",
-           "layer_math.cuh"]
+           "layer_math.cuh", "layer_ptx.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -11,6 +11,8 @@ constexpr int kDzCols = 256;       // columns of a block: 32 threads of 8
 constexpr int kDzRows = 2;
 constexpr int kDzMaxBlocks = 128;  // row blocks: partial sums a column
 
+// Bound by HBM: 2405x4151 BF16 6.5 us (40 MB in and out, 6.1 TB/s).
+//
 // Eight values a thread; columns past `cols` become zeros up to the next
 // multiple of 8 (ld_dst is one).
 __global__ void __launch_bounds__(256) repack_kernel(const __grid_constant__ RepackArgs args) {
@@ -43,6 +45,9 @@ __global__ void __launch_bounds__(256) repack_kernel(const __grid_constant__ Rep
     }
 }
 
+// Bound by what it reads and writes, 8 bytes a value: 2050x3584 gelu 10 us (59
+// MB, 5.9 TB/s, some of it from L2).
+//
 // dz = dout * act'(z) for a block of rows and 256 columns: a warp walks rows,
 // a thread holds 8 columns and the FP32 sums of the dz it made, before they
 // are rounded to 16 bits for the products.

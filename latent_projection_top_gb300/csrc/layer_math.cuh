@@ -6,7 +6,7 @@
 #include <cuda_fp16.h>
 
 #include "layer.cuh"
-#include "sm103_ptx.cuh"
+#include "layer_ptx.cuh"
 
 namespace route {
 

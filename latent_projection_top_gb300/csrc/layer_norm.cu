@@ -4,13 +4,16 @@
 //   dx = r (g - mean(g) - xh mean(g xh)),  g = dy gamma,  xh = (x - mean) r
 //   dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy
 //
+// Bound by HBM: forward 16384x7168 BF16 85 us (5.5 TB/s), backward 8192x7168
+// 64 us (5.5 TB/s; 58 without the parameters' sums).
+//
 // x and dy are read once, and the variance is the sum of squared deviations
 // from the mean, not a difference of large sums.  Sums are FP32.
 #include <initializer_list>
 
 #include "layer.cuh"
 #include "layer_math.cuh"
-#include "sm103_ptx.cuh"
+#include "layer_ptx.cuh"
 
 namespace route {
 namespace {
@@ -624,7 +627,7 @@ __global__ void __launch_bounds__(block_of(T), loose_blocks(T)) norm_backward_ke
 // Column sums of the blocks' partials (read from L2, where they were just
 // written): dgamma in the first dim columns, dbeta in the rest.  A block
 // takes 32 columns; each of its 16 warps adds every sixteenth row, and the
-// sums meet in order.
+// sums meet in order (8192x7168: 304 rows, 17 MB, about 3 us).
 constexpr int kSumWarps = 16;
 __global__ void __launch_bounds__(32 * kSumWarps)
     norm_sum_kernel(const float *part, int blocks, int dim, void *dgamma, void *dbeta, int type) {
