@@ -9,8 +9,8 @@
 // never meets more than one SM per 128 rows.  A tile's contraction is split
 // over a cluster of up to eight CTAs, enough of them to have the whole chip
 // read: their FP32 sums meet in distributed shared memory, each CTA adds its
-// share of the tile's elements over the cluster, in rank order, and runs the
-// operator's epilogue (layer_math.cuh) on the sums.  No partial goes through
+// share of the tile's elements over the cluster, in rank order, lets its peers
+// leave and runs the operator's epilogue (layer_math.cuh) on the sums.  No partial goes through
 // global memory and no second kernel or counter is needed: at 128 rows of
 // 896x896 the sums' last step took 25 of 31 us when one CTA did it for a
 // tile, from partials in L2.
@@ -103,6 +103,50 @@ __device__ __forceinline__ float ld_cluster_f(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
+}
+
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_shared_f(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared_f4(uint32_t addr, float4 v) {
+    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ void st_shared_f(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// Four columns' sums of the cluster's C CTAs, added in rank order into this
+// one's; N of them, `next` bytes apart.  Every CTA's part is on its way before
+// the first is added.
+template <int N>
+__device__ __forceinline__ void add_parts(uint32_t at, uint32_t next, int C) {
+    float4 f[N][kSmallMaxSplits];
+#pragma unroll
+    for (int j = 0; j < kSmallMaxSplits; ++j)
+        if (j < C) {
+            const uint32_t q = ptx::map_to_rank(at, (uint32_t)j);
+#pragma unroll
+            for (int k = 0; k < N; ++k) f[k][j] = ld_cluster_f4(q + k * next);
+        }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < kSmallMaxSplits; ++j)
+            if (j < C) v.x += f[k][j].x, v.y += f[k][j].y, v.z += f[k][j].z, v.w += f[k][j].w;
+        st_shared_f4(at + k * next, v);
+    }
 }
 
 template <int EPI, int BN>
@@ -284,58 +328,71 @@ __global__ void __launch_bounds__(kThreads, 2)
         ptx::cluster_sync();
     else
         __syncthreads();
+    // A CTA's share of the cluster's sums, added into its own copy of them: of
+    // each copy only its CTA's share is written, and only others are read by
+    // its peers.  Columns that do not exist are not read.
+    constexpr int kGroups = kTileCols / 4;
+    const int cols = min(kTileCols, ep.N - col0);
+    const int items = rows * kGroups, i0 = items * rank / C, i1 = items * (rank + 1) / C;
+    constexpr int kStep = kEpiThreads / kTileCols;  // rows that the threads cover at once
+    const int rows0 = rows * rank / C, rows1 = rows * (rank + 1) / C;
+    auto item_at = [&](int x) { return sbase + (uint32_t)((x / kGroups) * kSmallTile + x % kGroups * 4) * 4u; };
+    auto value_at = [&](int r) { return sbase + (uint32_t)(r * kSmallTile + e % kTileCols) * 4u; };
+    if (C > 1) {
+        if (warp >= 2 && ok && wide) {
+            for (int x = i0 + e; x < i1; x += kEpiThreads) {
+                if (x % kGroups * 4 >= cols) continue;
+                add_parts<EPI == kEpiGated ? 2 : 1>(item_at(x), kTileCols * 4u, C);
+            }
+        } else if (warp >= 2 && ok && e % kTileCols < cols) {
+            // a thread's rows of one column
+#pragma unroll 2
+            for (int r = rows0 + e / kTileCols; r < rows1; r += kStep) {
+                float v = 0.f, u = 0.f;
+                for (int j = 0; j < C; ++j) {
+                    const uint32_t q = ptx::map_to_rank(value_at(r), (uint32_t)j);
+                    v += ld_cluster_f(q);
+                    if (EPI == kEpiGated) u += ld_cluster_f(q + kTileCols * 4u);
+                }
+                st_shared_f(value_at(r), v);
+                if (EPI == kEpiGated) st_shared_f(value_at(r) + kTileCols * 4u, u);
+            }
+        }
+        __syncwarp();
+        // After the last remote read (ordered: peers may leave) and before the
+        // stores of results, which the order would wait for (0.5 us at 64x896x896).
+        ptx::cluster_arrive();
+    }
     if (warp >= 2 && ok && wide) {
-        constexpr int kGroups = kTileCols / 4;
-        const int items = rows * kGroups;
-        const int i0 = items * rank / C, i1 = items * (rank + 1) / C;
         auto row_of = [&](int x) { return row0 + x / kGroups; };
         auto col_of = [&](int x) { return col0 + x % kGroups * 4; };
         EpiIn<EPI> in, next;
         if (i0 + e < i1) epi_load<EPI>(ep, row_of(i0 + e), col_of(i0 + e), in);
         for (int x = i0 + e; x < i1; x += kEpiThreads) {
-            const uint32_t at = sbase + (uint32_t)((x / kGroups) * kSmallTile + x % kGroups * 4) * 4u;
-            float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
             if (x + kEpiThreads < i1) epi_load<EPI>(ep, row_of(x + kEpiThreads), col_of(x + kEpiThreads), next);
-            // every CTA's part is on its way before the first is added
-            float4 f[kSmallMaxSplits], h[EPI == kEpiGated ? kSmallMaxSplits : 1];
-#pragma unroll
-            for (int j = 0; j < kSmallMaxSplits; ++j)
-                if (j < C) {
-                    const uint32_t q = ptx::map_to_rank(at, (uint32_t)j);
-                    f[j] = ld_cluster_f4(q);
-                    if (EPI == kEpiGated) h[EPI == kEpiGated ? j : 0] = ld_cluster_f4(q + kTileCols * 4u);
-                }
-#pragma unroll
-            for (int j = 0; j < kSmallMaxSplits; ++j)
-                if (j < C) {
-                    v[0] += f[j].x, v[1] += f[j].y, v[2] += f[j].z, v[3] += f[j].w;
-                    if constexpr (EPI == kEpiGated) {
-                        u[0] += h[j].x, u[1] += h[j].y, u[2] += h[j].z, u[3] += h[j].w;
-                    }
-                }
+            const float4 f = ld_shared_f4(item_at(x));
+            float v[4] = {0.f + f.x, 0.f + f.y, 0.f + f.z, 0.f + f.w}, u[4] = {0.f, 0.f, 0.f, 0.f};  // no -0
+            if constexpr (EPI == kEpiGated) {
+                const float4 h = ld_shared_f4(item_at(x) + kTileCols * 4u);
+                u[0] += h.x, u[1] += h.y, u[2] += h.z, u[3] += h.w;
+            }
             epilogue<EPI>(ep, row_of(x), col_of(x), v, u, in);
             in = next;
         }
     } else if (warp >= 2 && ok) {
         // a thread's rows of one column, kRows of them at a time
         constexpr int kRows = EPI == kEpiGated || EPI == kEpiDGate ? 2 : 4;
-        constexpr int kStep = kEpiThreads / kTileCols;  // rows that the threads cover at once
-        const int rows0 = rows * rank / C, rows1 = rows * (rank + 1) / C;
         const int c = e % kTileCols;
         for (int r = rows0 + e / kTileCols; r < rows1; r += kStep * kRows) {
             ColumnIn<EPI, kRows> in;
             column_load<EPI, kRows>(ep, row0 + r, col0 + c, kStep, in);
             float v[kRows] = {}, u[EPI == kEpiGated ? kRows : 1] = {};
-            for (int j = 0; j < C; ++j) {
-                const uint32_t q = ptx::map_to_rank(sbase + (uint32_t)(r * kSmallTile + c) * 4u, (uint32_t)j);
 #pragma unroll
-                for (int k = 0; k < kRows; ++k)
-                    if (r + k * kStep < rows1) {
-                        v[k] += ld_cluster_f(q + (uint32_t)(k * kStep * kSmallTile) * 4u);
-                        if constexpr (EPI == kEpiGated)
-                            u[k] += ld_cluster_f(q + (uint32_t)(k * kStep * kSmallTile + kTileCols) * 4u);
-                    }
-            }
+            for (int k = 0; k < kRows; ++k)
+                if (r + k * kStep < rows1) {
+                    v[k] += ld_shared_f(value_at(r + k * kStep));
+                    if constexpr (EPI == kEpiGated) u[k] += ld_shared_f(value_at(r + k * kStep) + kTileCols * 4u);
+                }
             // rows of other CTAs' shares are not this one's to write
             Epilogue own = ep;
             own.M = row0 + rows1;
@@ -349,9 +406,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         ptx::tmem_dealloc(tmem_base, kTmemCols);
     }
     __syncwarp();
-    // no CTA leaves while another may read its sums (relaxed: ordered after the
-    // stores of results it takes 0.5 us longer, 64x896x896 5.1 against 4.6)
-    if (C > 1) ptx::cluster_sync_relaxed();
+    if (C > 1) ptx::cluster_wait();  // no CTA leaves while another may read its sums
 }
 
 const void *kernel_of(int epi, int bn) {
