@@ -26,7 +26,9 @@
 // to the other CTA is a relaxed arrival: ordered after the warp's stores of
 // results, as an arrival is by default, it waited for them to reach the L2
 // (2050x64x3584 11.5 us, so 10.4; gelu with z kept 20.5, so 19.3).  For the
-// same reason the last meeting of the pair is relaxed (0.4 us a launch).
+// same reason the last meeting of the pair is relaxed (0.4 us a launch): it
+// orders no access, so each CTA first waits for every arrival on its barriers
+// from the other.
 //
 // Split K: with few tiles, `splits` CTA pairs share a tile's contraction and
 // store FP32 partials; gemm_finish_kernel adds them in split order and runs
@@ -346,9 +348,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
                 else
                     ok = load_tile<true, true>(st, l, leader, pol, armed, armed_par);
             }
+            // The leader's MMAs release the last stages in both CTAs, and nobody
+            // waits for that to load another: it has arrived before they leave.
+            for (int it = st.it > S ? st.it - S : 0; ok && it < st.it; ++it)
+                ok = wait_phase(empty_bar(it % S), (uint32_t)(it / S) & 1u, args, &s_abort);
             // After an abort the leader lets every copy it armed land (the
             // peer's copies complete on the same barriers).
-            if (leader && (!ok || s_abort)) {
+            if (leader && !ok) {
                 for (int s = 0; s < S; ++s)
                     if (armed & (1u << s)) wait_drain(full_bar(s), (armed_par >> s) & 1u, args);
             }
@@ -358,7 +364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
             // ---------------- MMA issuer (leader CTA) ----------------
             const uint32_t fmt = args.fp16 ? 0u : 1u;
             Stages<BN> st{args, &s_abort, sbase, bars};
-            int job = 0;
+            int job = 0, done = 0;  // tiles begun, and handed to the epilogue
             bool ok = true;
             Walk walk(pair);
             for (int i; ok && walk.next(args, pair, i); ++job) {
@@ -374,10 +380,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
                     ok = mma_tile<false, false>(st, n, d_tmem, fmt);
                 else
                     ok = mma_tile<true, true>(st, n, d_tmem, fmt);
-                if (ok) ptx::mma_commit_pair(tfull_bar(t), 0x3);
+                if (ok) ptx::mma_commit_pair(tfull_bar(t), 0x3), ++done;
             }
             ptx::mma_commit_pair(drain_bar, 0x3);  // every MMA retired before TMEM is freed
             wait_drain(drain_bar, 0u, args);
+            // The peer's arrivals for the last tiles have landed before this CTA's
+            // shared memory is another's: no later tile waits for them.
+            for (int t = 0; t < 2; ++t) {
+                const int tiles = (done + 1 - t) / 2;  // with accumulator t
+                if (tiles > 0) wait_drain(tempty_bar(t), (uint32_t)(tiles - 1) & 1u, args);
+            }
         }
     } else {
         // ---------------- epilogue (both CTAs) ----------------

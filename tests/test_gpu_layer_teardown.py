@@ -82,3 +82,64 @@ def test_gated_columns_that_do_not_exist(rows, k, f, n):
     grads = ref.gated_grads(x, Wg, Wu, Wd, kept, dout, "silu", BF16)
     for got, w in zip(outs[0], (want, grads["dx"], grads["dW_gate"], grads["dW_up"], grads["dW_down"])):
         assert ref.worst(got, w) <= 1
+
+
+# ---- tiles of a pair of SMs: the last tiles of each pair, and what starts behind them
+
+@pytest.mark.parametrize("rows,k,n", [
+    (2050, 64, 3584),    # tiles whose epilogue is their whole time
+    (4096, 896, 2432),   # more tiles than pairs, an odd number of them a pair
+    (700, 2048, 1032),   # fewer tiles than pairs
+])
+@pytest.mark.parametrize("act", ["none", "gelu"])
+def test_pair_tiles_with_calls_right_behind(rows, k, n, act):
+    x, W = normal(1, rows, k), normal(2, k, n, scale=k ** -0.5)
+    dout = normal(3, rows, n)
+    outs = outputs((rows, n), (rows, k), (k, n))
+    with route.LinearPlan(rows, k, n, BF16, act=act, train=True) as plan, \
+            route.NormPlan(rows, k, BF16) as norm:
+        saved, y = plan.new_saved(), torch.empty_like(x)
+        for out, dx, dW in outs:
+            route.linear_forward(plan, x, W, out, saved=saved)
+            route.norm_forward(norm, x, None, None, y)
+            route.linear_backward(plan, dout, x, W, saved=saved, dx=dx, dW=dW)
+        plan.status()
+    same(outs)
+    want, z = ref.linear(x, W, None, None, act, BF16)
+    grads = ref.linear_grads(x, W, z, dout, act, BF16)
+    for got, w in zip(outs[0], (want, grads["dx"], grads["dW"])):
+        assert ref.worst(got, w) <= 1
+
+
+@pytest.mark.parametrize("rows,k,n", [
+    (300, 512, 512),      # small tiles, one block of the contraction a CTA
+    (16, 16384, 256),     # small tiles, more blocks than stages a CTA
+    (4096, 512, 2048),    # pair tiles, one or two a pair
+    (16384, 192, 2048),   # pair tiles, many a pair
+])
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_expired_waits_leave_the_next_call_right(rows, k, n, act):
+    """Copies that never come (the hook of test_stalled_product..): every wait
+    gives up, the kernels return, and the call after that is right."""
+    x, W = normal(1, rows, k), normal(2, k, n, scale=k ** -0.5)
+    dout = normal(3, rows, n)
+    e = lambda *s: torch.full(s, float("nan"), dtype=BF16, device=DEV)  # noqa: E731
+    with route.LinearPlan(rows, k, n, BF16, act=act, train=True) as plan:
+        saved = plan.new_saved()
+
+        def step():
+            o = e(rows, n), e(rows, k), e(k, n)
+            route.linear_forward(plan, x, W, o[0], saved=saved)
+            route.linear_backward(plan, dout, x, W, saved=saved, dx=o[1], dW=o[2])
+            return o
+
+        want = step()
+        plan.status()
+        assert route.lib().route_layer_test_stall(plan.handle, 1, 2_000_000) == 0
+        step()
+        with pytest.raises(route.RouteError, match="TIMEOUT"):
+            plan.status()
+        assert route.lib().route_layer_test_stall(plan.handle, 0, 0) == 0
+        got = step()
+        plan.status()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
