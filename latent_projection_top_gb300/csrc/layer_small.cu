@@ -260,9 +260,14 @@ __global__ void __launch_bounds__(kThreads, 2)
                 columns_of(it);
                 rows_of(it);
             }
-            if (s_abort)  // let every copy that was issued land
-                for (int it = issued > S ? issued - S : 0; it < issued; ++it)
-                    wait_drain(full_bar(it % S), (uint32_t)(it / S) & 1u, args);
+            // Not to leave before every copy has landed: the MMAs have released its
+            // stage, or, after a wait that expired (maybe only now), it is waited for.
+            bool released = true;
+            for (int it = issued > S ? issued - S : 0; it < issued; ++it) {
+                const uint32_t parity = (uint32_t)(it / S) & 1u;
+                released = released && wait_phase(empty_bar(it % S), parity, args, &s_abort);
+                if (!released) wait_drain(full_bar(it % S), parity, args);
+            }
         }
     } else if (warp == 1) {
         if (lane == 0) {
