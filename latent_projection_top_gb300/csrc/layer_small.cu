@@ -343,6 +343,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int rows0 = rows * rank / C, rows1 = rows * (rank + 1) / C;
     auto item_at = [&](int x) { return sbase + (uint32_t)((x / kGroups) * kSmallTile + x % kGroups * 4) * 4u; };
     auto value_at = [&](int r) { return sbase + (uint32_t)(r * kSmallTile + e % kTileCols) * 4u; };
+    // the first item's inputs besides the sums are on their way meanwhile
+    auto row_of = [&](int x) { return row0 + x / kGroups; };
+    auto col_of = [&](int x) { return col0 + x % kGroups * 4; };
+    EpiIn<EPI> in, next;
+    if (warp >= 2 && wide && i0 + e < i1) epi_load<EPI>(ep, row_of(i0 + e), col_of(i0 + e), in);
     if (C > 1) {
         if (warp >= 2 && ok && wide) {
             for (int x = i0 + e; x < i1; x += kEpiThreads) {
@@ -364,15 +369,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
         __syncwarp();
-        // After the last remote read (ordered: peers may leave) and before the
-        // stores of results, which the order would wait for (0.5 us at 64x896x896).
+        // After the last remote read (ordered: peers may leave; the order takes 0.17
+        // us, 64x896x896 4.84, so 4.66) and before the stores of results, which the
+        // order would wait for too (0.5 us).
         ptx::cluster_arrive();
     }
     if (warp >= 2 && ok && wide) {
-        auto row_of = [&](int x) { return row0 + x / kGroups; };
-        auto col_of = [&](int x) { return col0 + x % kGroups * 4; };
-        EpiIn<EPI> in, next;
-        if (i0 + e < i1) epi_load<EPI>(ep, row_of(i0 + e), col_of(i0 + e), in);
         for (int x = i0 + e; x < i1; x += kEpiThreads) {
             if (x + kEpiThreads < i1) epi_load<EPI>(ep, row_of(x + kEpiThreads), col_of(x + kEpiThreads), next);
             const float4 f = ld_shared_f4(item_at(x));
