@@ -57,3 +57,45 @@ def test_norm_gradients_of_rows_far_from_zero(dim, offset, dt):
     e = (d.abs() * exh + U * terms.abs()).sum(0) + rows * U * terms.abs().sum(0)
     assert ref.worst(dgamma, ref.rounded((terms.sum(0), e), dt)) <= 1
     assert ref.worst(dbeta, ref.rounded((d.sum(0), rows * U * d.abs().sum(0)), dt)) <= 1
+
+
+def every_bf16(least, most):
+    """All BF16 values of both signs whose magnitude is in [least, most]."""
+    v = torch.arange(0, 1 << 15, device=DEV, dtype=torch.int32).to(torch.int16).view(BF16)
+    v = v[(v.float() >= least) & (v.float() <= most)]
+    return torch.cat([v, -v])
+
+
+def activated(act, z, bias=None):
+    """act(z) in FP32 of each value: a product with the 64 x 64 identity."""
+    n = 64
+    rows = (z.numel() + n - 1) // n
+    x = torch.zeros(rows * n, device=DEV, dtype=BF16)
+    x[:z.numel()] = z
+    W, out = torch.eye(n, device=DEV, dtype=BF16), torch.empty((rows, n), device=DEV)
+    with route.LinearPlan(rows, n, n, BF16, act=act, out_dtype=FP32) as plan:
+        route.linear_forward(plan, x.view(rows, n), W, out, bias=bias)
+        plan.status()
+    return out.view(-1)[:z.numel()]
+
+
+@pytest.mark.parametrize("act", route.ACTIVATIONS)
+def test_activations_in_fp32(act):
+    """Within layer_ref's bound for the activations' own evaluation (z exact)."""
+    z = every_bf16(2.0 ** -20, 40.0)
+    got = activated(act, z)
+    want = ref.rounded(ref.act(act, ref.exact(z))[0], FP32)
+    assert ref.worst(got, want) <= 1
+
+
+def test_gelu_tail():
+    """gelu of negative z relative to itself.  The tail's exponent z^2 / 2 has
+    three roundings, each of which moves the tail by z^2 / 2 times U; the rest
+    (t: 3 U, the polynomial and its fit: 4 U, the exponential: 4 U, products: 3 U)
+    is within 16 U."""
+    z = every_bf16(2.0 ** -8, 8.0)
+    z = z[z < 0]
+    v = z.double()
+    want = v * torch.erfc(-v / 2 ** 0.5) / 2
+    e = (1.5 * v * v + 16) * U * want.abs()
+    assert ref.worst(activated("gelu", z), (want, e)) <= 1
