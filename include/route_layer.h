@@ -32,7 +32,8 @@
  *    that many rows.  With none, forward calls launch nothing and backward
  *    calls write zeros into the parameters' gradients.
  *  - A plan holds scratch memory and must not run on two streams at the same
- *    time.  Calls do not allocate.
+ *    time.  Calls of several host threads on one plan (and stream) are taken one
+ *    after another.  Calls do not allocate.
  *  - Results are reproducible bit for bit: no sum's order depends on timing.
  *  - `out` may be the residual itself (in place); no other output may
  *    overlap an input or another output.

@@ -8,6 +8,7 @@
 #include <cstddef>
 #include <cstring>
 #include <initializer_list>
+#include <mutex>
 #include <new>
 
 #include "api_util.h"
@@ -54,6 +55,9 @@ struct route_layer {
     size_t o_part;     // split partials (norm: column-sum partials)
     size_t o_sum;      // the bias gradient's partials
     size_t o_x, o_w[3], o_dout, o_h, o_dg, o_du;
+    // Held for the whole of a call: its kernels share the scratch, and follow one
+    // another in the stream without another call's between them.
+    mutable std::mutex calls;
     mutable ChoiceMemo memo[kSlots];
 };
 
@@ -610,9 +614,8 @@ route_status check_prepare(int rows, std::initializer_list<int> widths, int max_
 }
 
 route_layer *new_plan(LayerKind kind, int rows, int type, int act, int train) {
-    route_layer *p = new (std::nothrow) route_layer;
+    route_layer *p = new (std::nothrow) route_layer();  // all zero
     if (!p) return nullptr;
-    memset(static_cast<void *>(p), 0, sizeof *p);
     p->kind = kind;
     p->rows = rows;
     p->type = p->out_type = type;
@@ -708,6 +711,7 @@ route_status route_norm_forward(const route_layer *p, int rows, const void *x, i
                                 int64_t ld_y, float *stats, void *stream) {
     route_status st = check_plan(p, kNorm, rows);
     if (st != ROUTE_OK) return st;
+    std::lock_guard<std::mutex> lock(p->calls);
     if (!(eps >= 0.f) || std::isinf(eps))
         return api_fail(ROUTE_ERR_PLAN, "eps must be finite and not negative");
     if (rows == 0) return ROUTE_OK;
@@ -737,6 +741,7 @@ route_status route_norm_backward(const route_layer *p, int rows, const void *dy,
                                  void *dbeta, void *stream) {
     route_status st = check_plan(p, kNorm, rows);
     if (st != ROUTE_OK) return st;
+    std::lock_guard<std::mutex> lock(p->calls);
     const int es = layer_esize(p->type);
     if ((st = check_vec("gamma", gamma, es)) != ROUTE_OK ||
         (st = check_vec("dgamma", dgamma, es)) != ROUTE_OK ||
@@ -775,6 +780,7 @@ route_status route_linear_forward(const route_layer *p, int rows, const void *x,
                                   int64_t ld_out, void *saved, void *stream) {
     route_status st = check_plan(p, kLinear, rows);
     if (st != ROUTE_OK) return st;
+    std::lock_guard<std::mutex> lock(p->calls);
     if (saved && (!p->train || p->act == kActNone))
         return api_fail(ROUTE_ERR_PLAN, "the plan saves nothing (no training, or no activation)");
     if (rows == 0) return ROUTE_OK;
@@ -803,6 +809,7 @@ route_status route_linear_backward(const route_layer *p, int rows, const void *d
                                    void *dW, int64_t ld_dW, void *dbias, void *stream) {
     route_status st = check_plan(p, kLinear, rows);
     if (st != ROUTE_OK) return st;
+    std::lock_guard<std::mutex> lock(p->calls);
     if (!p->train) return api_fail(ROUTE_ERR_PLAN, "the plan was prepared without train");
     if (dW && (st = check_mat({"dW", dW, ld_dW, p->k, p->n, 2, false})) != ROUTE_OK) return st;
     if ((st = check_vec("dbias", dbias, 2)) != ROUTE_OK) return st;
@@ -865,6 +872,7 @@ route_status route_gated_forward(const route_layer *p, int rows, const void *x, 
                                  int64_t ld_out, void *saved, void *stream) {
     route_status st = check_plan(p, kGated, rows);
     if (st != ROUTE_OK) return st;
+    std::lock_guard<std::mutex> lock(p->calls);
     if (saved && !p->train) return api_fail(ROUTE_ERR_PLAN, "the plan was prepared without train");
     if (rows == 0) return ROUTE_OK;
     if ((st = check_mats({{"x", x, ld_x, rows, p->k, 2, true},
@@ -905,6 +913,7 @@ route_status route_gated_backward(const route_layer *p, int rows, const void *do
                                   int64_t ld_dup, void *dW_down, int64_t ld_ddown, void *stream) {
     route_status st = check_plan(p, kGated, rows);
     if (st != ROUTE_OK) return st;
+    std::lock_guard<std::mutex> lock(p->calls);
     if (!p->train) return api_fail(ROUTE_ERR_PLAN, "the plan was prepared without train");
     const Mat grads[3] = {{"dW_gate", dW_gate, ld_dgate, p->k, p->f, 2, false},
                           {"dW_up", dW_up, ld_dup, p->k, p->f, 2, false},

@@ -1,0 +1,71 @@
+"""Host threads that share a layer operator's plan and stream: each call's
+kernels stay together, and each is cut for its own number of rows."""
+
+import threading
+
+import pytest
+import torch
+
+import latent_projection_top_gb300 as route
+from gpu_util import DEV, require_gpu
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def normal(seed, *shape, scale=1.0):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return (torch.randn(shape, generator=g, device=DEV) * scale).to(BF16)
+
+
+@pytest.mark.parametrize("by_stream", [True, False])
+def test_threads_share_a_plan(by_stream):
+    """By ctypes (a stream is given) and by the compiled way."""
+    k, f, n, times = 264, 1000, 520, 200
+    w = normal(1, k, f, scale=k ** -0.5), normal(2, k, f, scale=k ** -0.5), normal(3, f, n, scale=f ** -0.5)
+    stream = torch.cuda.current_stream()
+    jobs = []
+    with route.GatedPlan(3000, k, f, n, BF16, train=True) as plan:
+        for rows in (1, 3000, 17, 700):
+            x, dout = normal(rows, rows, k), normal(rows + 1, rows, n)
+
+            def step(out, dx, dWd, saved, x=x, dout=dout):
+                s = stream if by_stream else None
+                route.gated_forward(plan, x, *w, out, saved=saved, stream=s)
+                route.gated_backward(plan, dout, x, *w, saved, dx=dx, dW_down=dWd, stream=s)
+
+            sets = [(torch.full((rows, n), float("nan"), dtype=BF16, device=DEV),
+                     torch.full((rows, k), float("nan"), dtype=BF16, device=DEV),
+                     torch.full((f, n), float("nan"), dtype=BF16, device=DEV)) for _ in range(2)]
+            saved = [plan.new_saved(rows) for _ in range(2)]
+            step(*sets[0], saved[0])
+            jobs.append((step, sets, saved))
+        plan.status()
+        torch.cuda.synchronize()
+        errors = []
+
+        def work(step, out, saved):
+            try:
+                with torch.cuda.stream(stream):
+                    for _ in range(times):
+                        step(*out, saved)
+            except Exception as e:  # shown by the assertion below
+                errors.append(e)
+
+        threads = [threading.Thread(target=work, args=(step, sets[1], saved[1]))
+                   for step, sets, saved in jobs]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        plan.status()
+    assert not errors
+    for _, (want, got), _ in jobs:
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
