@@ -69,3 +69,20 @@ def test_threads_share_a_plan(by_stream):
     assert not errors
     for _, (want, got), _ in jobs:
         assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("by_stream", [True, False])
+def test_first_cuda_call_of_a_thread(by_stream):
+    """A host thread needs no CUDA context of its own making before a call."""
+    rows, k, n = 40, 264, 520
+    x, W = normal(1, rows, k), normal(2, k, n, scale=k ** -0.5)
+    want, got = (torch.empty((rows, n), dtype=BF16, device=DEV) for _ in range(2))
+    stream = torch.cuda.current_stream() if by_stream else None
+    with route.LinearPlan(rows, k, n, BF16) as plan:
+        route.linear_forward(plan, x, W, want)
+        t = threading.Thread(target=lambda: route.linear_forward(plan, x, W, got, stream=stream))
+        torch.cuda.synchronize()
+        t.start()
+        t.join()
+        plan.status()
+    assert torch.equal(want, got)
