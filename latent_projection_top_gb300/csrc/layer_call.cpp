@@ -104,6 +104,17 @@ struct Args {
     }
 };
 
+// An entry point's status.  Other Python threads run meanwhile, as they do
+// during a call by ctypes: a launch may wait for room in its stream, and a
+// call for another thread's on the same plan.
+template <class F, class... A>
+int enter(F entry, A... args) {
+    PyThreadState *state = PyEval_SaveThread();
+    const int status = (int)entry(args...);
+    PyEval_RestoreThread(state);
+    return status;
+}
+
 // Runs `call(plan, args)` on a call's arguments; whatever goes wrong in
 // reading them is left to layer.py's checks.
 template <class F>
@@ -133,7 +144,7 @@ PyObject *norm_forward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const double eps = PyFloat_Check(v[5]) ? PyFloat_AS_DOUBLE(v[5]) : -1.0;
         void *s = g.stream(v[6]);
         if (!g.ok || !(eps >= 0)) return kOther;
-        return (int)p_norm_forward(p.handle, R, x, lx, gamma, beta, (float)eps, out, lo, stats, s);
+        return enter(p_norm_forward, p.handle, R, x, lx, gamma, beta, (float)eps, out, lo, stats, s);
     });
 }
 
@@ -148,7 +159,7 @@ PyObject *norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         void *dx = g.opt(v[4], R, p.k, p.type, ld), *dgamma = g.vec(v[5], p.k), *dbeta = g.vec(v[6], p.k);
         void *s = g.stream(v[7]);
         if (!g.ok) return kOther;
-        return (int)p_norm_backward(p.handle, R, dy, ly, x, lx, gamma, stats, dx, ld, dgamma, dbeta, s);
+        return enter(p_norm_backward, p.handle, R, dy, ly, x, lx, gamma, stats, dx, ld, dgamma, dbeta, s);
     });
 }
 
@@ -161,7 +172,7 @@ PyObject *linear_forward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         void *out = g.mat(v[2], R, p.n, p.out_type, lo), *bias = g.vec(v[3], p.n);
         void *res = g.opt(v[4], R, p.n, p.out_type, lr), *saved = g.saved(v[5], R), *s = g.stream(v[6]);
         if (!g.ok) return kOther;
-        return (int)p_linear_forward(p.handle, R, x, lx, W, lw, bias, res, lr, out, lo, saved, s);
+        return enter(p_linear_forward, p.handle, R, x, lx, W, lw, bias, res, lr, out, lo, saved, s);
     });
 }
 
@@ -175,7 +186,7 @@ PyObject *linear_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         void *dx = g.opt(v[4], R, p.k, p.type, ldx), *dW = g.opt(v[5], p.k, p.n, p.type, ldw);
         void *db = g.vec(v[6], p.n), *s = g.stream(v[7]);
         if (!g.ok) return kOther;
-        return (int)p_linear_backward(p.handle, R, dy, ly, x, lx, W, lw, saved, dx, ldx, dW, ldw, db, s);
+        return enter(p_linear_backward, p.handle, R, dy, ly, x, lx, W, lw, saved, dx, ldx, dW, ldw, db, s);
     });
 }
 
@@ -189,7 +200,7 @@ PyObject *gated_forward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         void *out = g.mat(v[4], R, p.n, p.type, lo), *res = g.opt(v[5], R, p.n, p.type, lr);
         void *saved = g.saved(v[6], R), *s = g.stream(v[7]);
         if (!g.ok) return kOther;
-        return (int)p_gated_forward(p.handle, R, x, lx, wg, lg, wu, lu, wd, ld, res, lr, out, lo, saved, s);
+        return enter(p_gated_forward, p.handle, R, x, lx, wg, lg, wu, lu, wd, ld, res, lr, out, lo, saved, s);
     });
 }
 
@@ -205,7 +216,7 @@ PyObject *gated_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         void *du = g.opt(v[8], p.k, p.f, p.type, ldu), *dd = g.opt(v[9], p.f, p.n, p.type, ldd);
         void *s = g.stream(v[10]);
         if (!g.ok) return kOther;
-        return (int)p_gated_backward(p.handle, R, dy, ly, x, lx, wg, lg, wu, lu, wd, ld, saved, dx, ldx, dg, ldg,
+        return enter(p_gated_backward, p.handle, R, dy, ly, x, lx, wg, lg, wu, lu, wd, ld, saved, dx, ldx, dg, ldg,
                                      du, ldu, dd, ldd, s);
     });
 }

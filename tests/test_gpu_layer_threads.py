@@ -86,3 +86,37 @@ def test_first_cuda_call_of_a_thread(by_stream):
         t.join()
         plan.status()
     assert torch.equal(want, got)
+
+
+def test_other_threads_run_during_a_call():
+    """While an entry point waits (here one that only sleeps takes its place),
+    other Python threads go on."""
+    import ctypes
+    import time
+
+    from latent_projection_top_gb300 import layer
+    short = layer._short_way()
+    x = normal(1, 4, 64)
+    names = ("norm_forward", "norm_backward", "linear_forward", "linear_backward", "gated_forward",
+             "gated_backward")
+    address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+    ticks, stop = [], threading.Event()
+
+    def tick():
+        while not stop.wait(0.005):
+            ticks.append(time.perf_counter())
+
+    t = threading.Thread(target=tick)
+    t.start()
+    try:
+        # usleep's only argument is the first one, a plan's handle
+        short.bind(*[address(ctypes.CDLL(None).usleep)] * 6)
+        start = time.perf_counter()
+        assert short.norm_forward((400000, 0, 0, 0, 64, 0, 0, 0), x, None, None, x, None, 1e-5, 0) == 0
+        end = time.perf_counter()
+    finally:
+        short.bind(*(address(getattr(route.lib(), f"route_{n}")) for n in names))
+        stop.set()
+        t.join()
+    assert end - start >= 0.4
+    assert sum(start + 0.1 < at < end - 0.1 for at in ticks) >= 5
