@@ -9,14 +9,17 @@ in the kernels, and a failed check is reported through the device status
 word (``route_device_status`` returns ROUTE_ERR_DEVICE_BOUNDS) instead of
 faulting.  The binding loads it when the environment sets ROUTE_DEBUG_LIB=1.
 
-With either goes ``_build/_layer_call.so``, the Python module of the layer
-operators' calls (``csrc/layer_call.cpp``, host code only).
+With either goes the Python module of the layer operators' calls
+(``csrc/layer_call.cpp``, host code only).  It reads tensors through torch's
+and Python's binary interfaces, so its file's name says which of each it was
+built for (``call_module()``).
 """
 
 from __future__ import annotations
 
 import importlib.util
 import os
+import re
 import subprocess
 import sys
 import sysconfig
@@ -30,7 +33,6 @@ LIB = os.path.join(BUILD, "libroute.so")
 DEBUG_BUILD = os.path.join(BUILD, "debug")
 DEBUG_LIB = os.path.join(DEBUG_BUILD, "libroute_debug.so")
 INCLUDE = os.path.join(ROOT, "include")
-CALL_MODULE = os.path.join(BUILD, "_layer_call.so")
 CALL_SOURCE = os.path.join(CSRC, "layer_call.cpp")
 
 SOURCES = ["decode_kernel.cu", "prefill_kernel.cu", "topk_kernel.cu", "stage_kernel.cu",
@@ -77,17 +79,31 @@ def _link(objs: list, lib: str) -> None:
     os.replace(tmp, lib)
 
 
+def _torch_dir() -> str:
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def call_module() -> str:
+    """The calls' module for this Python and the torch that it would import
+    (read from torch's version file: importing it takes seconds)."""
+    text = open(os.path.join(_torch_dir(), "version.py")).read()
+    version = re.search(r"""^__version__ = ['"]([^'"]+)""", text, re.M).group(1)
+    return os.path.join(BUILD, f"_layer_call.torch-{version}.{sysconfig.get_config_var('SOABI')}.so")
+
+
 def _compile_call_module() -> None:
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
-    tmp = CALL_MODULE + f".tmp{os.getpid()}"
+    import torch
+    abi, torch = int(torch._C._GLIBCXX_USE_CXX11_ABI), _torch_dir()
+    module = call_module()
+    tmp = module + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", CALL_SOURCE,
            "-o", tmp, "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
            "-I", os.path.join(torch, "include"), "-L", os.path.join(torch, "lib"),
-           "-ltorch_python", "-ltorch_cpu", "-lc10"]
+           f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed for layer_call.cpp:\n{res.stdout}\n{res.stderr}")
-    os.replace(tmp, CALL_MODULE)
+    os.replace(tmp, module)
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False,
@@ -101,7 +117,7 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False,
     todo = [(lib, d, x) for lib, d, x in targets if force or _stale(lib)]
     call_inputs = [CALL_SOURCE, os.path.join(INCLUDE, "route.h"),
                    os.path.join(INCLUDE, "route_layer.h"), os.path.abspath(__file__)]
-    call = force or _stale(CALL_MODULE, call_inputs)
+    call = force or _stale(call_module(), call_inputs)
     os.makedirs(BUILD, exist_ok=True)
     if not todo and call:
         _compile_call_module()

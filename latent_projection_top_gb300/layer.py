@@ -101,10 +101,11 @@ def _short_way():
 
         from . import builder
         L = _route.lib()
-        if not os.path.exists(builder.CALL_MODULE):
-            raise _route.RouteError(5, f"{builder.CALL_MODULE} is missing: it must be built "
+        path = builder.call_module()
+        if not os.path.exists(path):
+            raise _route.RouteError(5, f"{path} is missing: it must be built "
                                        "(latent_projection_top_gb300.build())")
-        loader = ExtensionFileLoader("_layer_call", builder.CALL_MODULE)
+        loader = ExtensionFileLoader("_layer_call", path)
         module = importlib.util.module_from_spec(
             importlib.util.spec_from_loader("_layer_call", loader))
         loader.exec_module(module)
