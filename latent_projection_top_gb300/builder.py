@@ -12,7 +12,9 @@ faulting.  The binding loads it when the environment sets ROUTE_DEBUG_LIB=1.
 With either goes the Python module of the layer operators' calls
 (``csrc/layer_call.cpp``, host code only).  It reads tensors through torch's
 and Python's binary interfaces, so its file's name says which of each it was
-built for (``call_module()``).
+built for (``call_module()``).  The library is complete without it: where it
+cannot be built (no torch, or no headers of torch's or Python's) ``build()``
+warns, and the calls go through ctypes.
 """
 
 from __future__ import annotations
@@ -23,6 +25,7 @@ import re
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -79,16 +82,33 @@ def _link(objs: list, lib: str) -> None:
     os.replace(tmp, lib)
 
 
-def _torch_dir() -> str:
-    return importlib.util.find_spec("torch").submodule_search_locations[0]
+def _torch_dir() -> str | None:
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec else None
 
 
-def call_module() -> str:
+def call_module() -> str | None:
     """The calls' module for this Python and the torch that it would import
-    (read from torch's version file: importing it takes seconds)."""
+    (read from torch's version file: importing it takes seconds); None where
+    there is no torch."""
+    if _torch_dir() is None:
+        return None
     text = open(os.path.join(_torch_dir(), "version.py")).read()
     version = re.search(r"""^__version__ = ['"]([^'"]+)""", text, re.M).group(1)
     return os.path.join(BUILD, f"_layer_call.torch-{version}.{sysconfig.get_config_var('SOABI')}.so")
+
+
+def _build_call_module(force: bool) -> None:
+    """Build the calls' module if it is stale; warn if that is not possible."""
+    try:
+        module = call_module()
+        if module is None:
+            raise RuntimeError("torch is not installed")
+        if force or _stale(module, [CALL_SOURCE, os.path.join(INCLUDE, "route.h"),
+                                    os.path.join(INCLUDE, "route_layer.h"), os.path.abspath(__file__)]):
+            _compile_call_module()
+    except Exception as e:  # the library and the binding work without it
+        warnings.warn(f"the layer operators' calls will go through ctypes (2 to 5 us more each): {e}")
 
 
 def _compile_call_module() -> None:
@@ -115,21 +135,17 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False,
     if debug or both:
         targets.append((DEBUG_LIB, DEBUG_BUILD, ["-DROUTE_DEBUG"]))
     todo = [(lib, d, x) for lib, d, x in targets if force or _stale(lib)]
-    call_inputs = [CALL_SOURCE, os.path.join(INCLUDE, "route.h"),
-                   os.path.join(INCLUDE, "route_layer.h"), os.path.abspath(__file__)]
-    call = force or _stale(call_module(), call_inputs)
     os.makedirs(BUILD, exist_ok=True)
-    if not todo and call:
-        _compile_call_module()
+    if not todo:
+        _build_call_module(force)
     if todo:
         for _, d, _ in todo:
             os.makedirs(d, exist_ok=True)
         jobs = [(src, d, x) for _, d, x in todo for src in SOURCES]
         with ThreadPoolExecutor(max_workers=len(jobs) + 1) as pool:
-            module = pool.submit(_compile_call_module) if call else None
+            module = pool.submit(_build_call_module, force)
             results = list(pool.map(lambda j: _compile(*j), jobs))
-            if module:
-                module.result()
+            module.result()
         for k, (lib, d, _) in enumerate(todo):
             part = results[k * len(SOURCES):(k + 1) * len(SOURCES)]
             with open(os.path.join(d, "ptxas.log"), "w") as f:

@@ -87,28 +87,32 @@ def _act_code(act: str) -> int:
 
 
 _short = None
+_without = False  # the compiled module could not be loaded
 
 
 def _short_way():
-    """The compiled module, bound to the loaded library."""
-    global _short
-    if _short is None:
+    """The compiled module, bound to the loaded library; None (and one warning)
+    where it is missing or does not load: the calls then go through ctypes."""
+    global _short, _without
+    if _short is None and not _without:
         import importlib.util
-        import os
         from importlib.machinery import ExtensionFileLoader
 
         import torch  # noqa: F401  (the module needs its libraries)
 
         from . import builder
         L = _route.lib()
-        path = builder.call_module()
-        if not os.path.exists(path):
-            raise _route.RouteError(5, f"{path} is missing: it must be built "
-                                       "(latent_projection_top_gb300.build())")
-        loader = ExtensionFileLoader("_layer_call", path)
-        module = importlib.util.module_from_spec(
-            importlib.util.spec_from_loader("_layer_call", loader))
-        loader.exec_module(module)
+        try:
+            loader = ExtensionFileLoader("_layer_call", builder.call_module())
+            module = importlib.util.module_from_spec(
+                importlib.util.spec_from_loader("_layer_call", loader))
+            loader.exec_module(module)
+        except (ImportError, OSError) as e:
+            import warnings
+            _without = True
+            warnings.warn(f"layer calls go through ctypes, 2 to 5 us more each: {e} "
+                          "(latent_projection_top_gb300.build() makes the module)")
+            return None
         module.bind(*(ctypes.cast(getattr(L, f"route_{name}"), _vp).value for name in (
             "norm_forward", "norm_backward", "linear_forward", "linear_backward",
             "gated_forward", "gated_backward")))
@@ -122,7 +126,6 @@ class _LayerPlan:
     def __init__(self, prepare: str, rows: int, dtype, device: int, *args, out_dtype=None,
                  widths: tuple):
         self._h = None
-        _short_way()
         h = ctypes.c_void_p()
         _route._check(getattr(_route.lib(), prepare)(int(rows), *args, int(device),
                                                      ctypes.byref(h)))
@@ -133,10 +136,10 @@ class _LayerPlan:
         self.device = int(device)
         # what a training forward call keeps of each row
         self.saved_row = _route._lib.route_layer_saved_bytes(h, 1)
-        # the plan as the short way takes it; None once closed
-        self._plain = (self._p, self.device, _type_code(dtype),
-                       _type_code(dtype if out_dtype is None else out_dtype), *widths,
-                       self.saved_row)
+        # the plan as the short way takes it; None once closed, or without the module
+        self._plain = None if _short_way() is None else (
+            self._p, self.device, _type_code(dtype),
+            _type_code(dtype if out_dtype is None else out_dtype), *widths, self.saved_row)
 
     @property
     def handle(self) -> ctypes.c_void_p:

@@ -1,5 +1,6 @@
-"""Host threads that share a layer operator's plan and stream: each call's
-kernels stay together, and each is cut for its own number of rows."""
+"""Host threads and the ways of a layer operator's call.  Threads that share a
+plan and stream: each call's kernels stay together, and each is cut for its own
+number of rows."""
 
 import threading
 
@@ -120,3 +121,18 @@ def test_other_threads_run_during_a_call():
         t.join()
     assert end - start >= 0.4
     assert sum(start + 0.1 < at < end - 0.1 for at in ticks) >= 5
+
+
+def test_calls_without_the_compiled_module(monkeypatch):
+    from latent_projection_top_gb300 import layer
+    rows, k, n = 40, 264, 520
+    x, W = normal(1, rows, k), normal(2, k, n, scale=k ** -0.5)
+    want, got = (torch.empty((rows, n), dtype=BF16, device=DEV) for _ in range(2))
+    with route.LinearPlan(rows, k, n, BF16) as plan:
+        route.linear_forward(plan, x, W, want)
+    monkeypatch.setattr(layer, "_short", None)
+    monkeypatch.setattr(layer, "_without", True)
+    with route.LinearPlan(rows, k, n, BF16) as plan:
+        route.linear_forward(plan, x, W, got)
+        plan.status()
+    assert torch.equal(want, got)

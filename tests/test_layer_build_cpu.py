@@ -32,3 +32,28 @@ def test_another_torch_is_another_module(tmp_path, monkeypatch):
     other = builder.call_module()
     assert other != here and "9.9.9+cu999" in other
     assert builder._stale(other, [builder.CALL_SOURCE])
+
+
+def test_build_without_torch_or_its_headers(tmp_path, monkeypatch):
+    """The library does not need the module: build() goes on, and says so."""
+    monkeypatch.setattr(builder, "_torch_dir", lambda: None)
+    with pytest.warns(UserWarning, match="torch is not installed"):
+        assert builder.build() == builder.LIB
+    (tmp_path / "version.py").write_text("__version__ = '9.9.9'\n")  # and no include/
+    monkeypatch.setattr(builder, "_torch_dir", lambda: str(tmp_path))
+    with pytest.warns(UserWarning, match="layer_call.cpp"):
+        assert builder.build() == builder.LIB
+    assert not os.path.exists(builder.call_module())
+
+
+def test_binding_without_the_module(tmp_path, monkeypatch):
+    monkeypatch.setattr(layer, "_short", None)
+    monkeypatch.setattr(layer, "_without", False)
+    for path in (tmp_path / "missing.so", tmp_path / "broken.so"):
+        if path.name == "broken.so":
+            path.write_bytes(b"not a library")
+        monkeypatch.setattr(layer, "_without", False)
+        monkeypatch.setattr(builder, "call_module", lambda p=path: str(p))
+        with pytest.warns(UserWarning, match="ctypes"):
+            assert layer._short_way() is None
+        assert layer._short_way() is None  # warned once
