@@ -79,6 +79,12 @@ def _type_code(dtype) -> int:
         raise TypeError(f"dtype {dtype} is not one of {tuple(_TYPES)}") from None
 
 
+def _c_int(v) -> int:
+    """An int as the C ABI takes it; one outside its range stays outside every
+    limit there (ctypes would cut it to 32 bits: 2**32 + 4 rows to 4)."""
+    return max(-2 ** 31, min(int(v), 2 ** 31 - 1))
+
+
 def _act_code(act: str) -> int:
     try:
         return ACTIVATIONS.index(act)
@@ -127,7 +133,7 @@ class _LayerPlan:
                  widths: tuple):
         self._h = None
         h = ctypes.c_void_p()
-        _route._check(getattr(_route.lib(), prepare)(int(rows), *args, int(device),
+        _route._check(getattr(_route.lib(), prepare)(_c_int(rows), *args, _c_int(device),
                                                      ctypes.byref(h)))
         self._h = h
         self._p = h.value  # what the calls pass; None once closed
@@ -149,8 +155,8 @@ class _LayerPlan:
 
     def saved_bytes(self, rows: int | None = None) -> int:
         """Bytes a training forward call of `rows` rows keeps for its backward call."""
-        return _route.lib().route_layer_saved_bytes(self.handle,
-                                                    self.rows if rows is None else int(rows))
+        self.handle  # raises: closed
+        return self.saved_row * max(0, self.rows if rows is None else int(rows))
 
     def new_saved(self, rows: int | None = None):
         """A buffer for what a training forward call keeps (None if nothing)."""
@@ -184,7 +190,7 @@ class NormPlan(_LayerPlan):
     """Layer norm of up to `rows` rows of `dim` values (BF16, FP16 or FP32)."""
 
     def __init__(self, rows: int, dim: int, dtype, device: int = 0):
-        super().__init__("route_norm_prepare", rows, dtype, device, int(dim), _type_code(dtype),
+        super().__init__("route_norm_prepare", rows, dtype, device, _c_int(dim), _type_code(dtype),
                          widths=(int(dim), 0, 0))
         self.dim = int(dim)
 
@@ -195,7 +201,7 @@ class LinearPlan(_LayerPlan):
     def __init__(self, rows: int, k: int, n: int, dtype, act: str = "none", train: bool = False,
                  out_dtype=None, device: int = 0):
         out_dtype = dtype if out_dtype is None else out_dtype
-        super().__init__("route_linear_prepare", rows, dtype, device, int(k), int(n),
+        super().__init__("route_linear_prepare", rows, dtype, device, _c_int(k), _c_int(n),
                          _type_code(dtype), _type_code(out_dtype), _act_code(act), int(train),
                          out_dtype=out_dtype, widths=(int(k), 0, int(n)))
         self.k, self.n, self.act, self.train = int(k), int(n), act, bool(train)
@@ -208,7 +214,7 @@ class GatedPlan(_LayerPlan):
 
     def __init__(self, rows: int, k: int, f: int, n: int, dtype, act: str = "silu",
                  train: bool = False, device: int = 0):
-        super().__init__("route_gated_prepare", rows, dtype, device, int(k), int(f), int(n),
+        super().__init__("route_gated_prepare", rows, dtype, device, _c_int(k), _c_int(f), _c_int(n),
                          _type_code(dtype), _act_code(act), int(train),
                          widths=(int(k), int(f), int(n)))
         self.k, self.f, self.n, self.act, self.train = int(k), int(f), int(n), act, bool(train)
@@ -316,12 +322,12 @@ def _taken(status) -> bool:
     return status == 0
 
 
-def _call(name, plan, *args):
+def _call(name, plan, rows, *args):
     """One C entry point; the message of a refusal is its exception's."""
     handle = plan._p
     if handle is None:
         plan.handle  # raises: closed
-    status = getattr(_route._lib, name)(handle, *args)
+    status = getattr(_route._lib, name)(handle, _c_int(rows), *args)
     if status:
         _route._check(status)
 
