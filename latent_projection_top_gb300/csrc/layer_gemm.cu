@@ -563,29 +563,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
                 }
                 continue;
             }
-            if (ACCESS == kColumns && whole) {  // rows of odd widths: a column a thread
-                constexpr int kRows = EPI == kEpiDGate ? 4 : 8;
+            if (ACCESS == kColumns && whole) {
+                if constexpr (ACCESS == kColumns) {
+                    constexpr int kRows = 8;
 #pragma unroll 1
-                for (int g = 0; g < kWarpCols / kG; ++g) {
-                    __syncwarp();  // the last group has been read
-                    put(acc + (uint32_t)(g * kG), 0u);
-                    if (EPI == kEpiGated) put(acc + (uint32_t)(g * kG) + kTileCols, kHalfTurn);
-                    __syncwarp();
-                    if (g + 1 == kWarpCols / kG) read_out();
-                    const int c = c0 + g * kG + lane;
+                    for (int g = 0; g < kWarpCols / kG; ++g) {
+                        __syncwarp();  // the last group has been read
+                        put(acc + (uint32_t)(g * kG), 0u);
+                        __syncwarp();
+                        if (g + 1 == kWarpCols / kG) read_out();
+                        const int c = c0 + g * kG + lane;
 #pragma unroll 1
-                    for (int r = 0; r < 32; r += kRows) {
-                        ColumnIn<EPI, kRows> in;
-                        column_load<EPI, kRows>(p, r0 + r, c, 1, in);
-                        float v[kRows], u[EPI == kEpiGated ? kRows : 1];
+                        for (int r = 0; r < 32; r += kRows) {
+                            uint32_t in[kRows];
+                            column_load<kRows>(p, r0 + r, c, 1, in);
+                            float v[kRows];
 #pragma unroll
-                        for (int j = 0; j < kRows; ++j) {
-                            const uint32_t at = unit(r + j, lane >> 2) + (lane & 3) * 4u;
-                            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[j]) : "r"(at) : "memory");
-                            if constexpr (EPI == kEpiGated)
-                                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(u[j]) : "r"(at + kHalfTurn) : "memory");
+                            for (int j = 0; j < kRows; ++j) {
+                                const uint32_t at = unit(r + j, lane >> 2) + (lane & 3) * 4u;
+                                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[j]) : "r"(at) : "memory");
+                            }
+                            column_epilogue<EPI, kRows>(p, r0 + r, c, 1, v, in);
                         }
-                        column_epilogue<EPI, kRows>(p, r0 + r, c, 1, v, u, in);
                     }
                 }
                 continue;
@@ -696,12 +695,13 @@ const void *kernel_of(int form, int epi, int bn, Access access) {
     ROUTE_GEMM(F, E, kColumns) ROUTE_GEMM(F, E, kFours) ROUTE_GEMM(F, E, kPacked) ROUTE_GEMM(F, E, kPackedAny)
     ROUTE_GEMM4(kFormNT, kEpiLinear)
     ROUTE_GEMM4(kFormNT, kEpiAct)
-    ROUTE_GEMM4(kFormNT, kEpiGated)
     ROUTE_GEMM(kFormNT, kEpiLinear, kPackedResidual)
     ROUTE_GEMM(kFormNT, kEpiAct, kPackedResidual)
-    ROUTE_GEMM(kFormNN, kEpiDGate, kColumns)
-    ROUTE_GEMM(kFormNN, kEpiDGate, kFours)
     ROUTE_GEMM4(kFormMixed, kEpiLinear)
+    // h, d gate and d up have padded rows: fours at least
+    ROUTE_GEMM(kFormNT, kEpiGated, kFours)
+    ROUTE_GEMM(kFormNT, kEpiGated, kPacked)
+    ROUTE_GEMM(kFormNN, kEpiDGate, kFours)
 #undef ROUTE_GEMM4
 #undef ROUTE_GEMM
     return nullptr;

@@ -551,31 +551,20 @@ __device__ __forceinline__ void pack_values(bool half, const float (&v)[W], uint
 // For rows that cannot be accessed four values at a time (odd widths):
 // neighbouring threads still take neighbouring columns, so that an
 // instruction's accesses are one stretch of a row (four scattered values a
-// thread write every 32-byte sector four times).
+// thread write every 32-byte sector four times).  Of linear results only: what
+// a gated block's products write (h, d gate, d up) has padded rows.
 
-template <int EPI, int R>
-struct ColumnIn {
-    uint32_t w[R][EPI == kEpiDGate ? 2 : 1];
-};
-
-// Column c of rows r, r + step, ..: R of them.
-template <int EPI, int R>
-__device__ __forceinline__ void column_load(const Epilogue &p, int r, int c, int step, ColumnIn<EPI, R> &in) {
-    if (c >= p.N) return;
+// Column c of rows r, r + step, .. of the residual: R of them.
+template <int R>
+__device__ __forceinline__ void column_load(const Epilogue &p, int r, int c, int step, uint32_t (&in)[R]) {
+    if (c >= p.N || p.residual == nullptr) return;
 #pragma unroll
     for (int j = 0; j < R; ++j) {
         const int row = r + j * step;
         if (row >= p.M) break;
-        if constexpr (epi_linear(EPI)) {
-            if (p.residual != nullptr) {
-                const long long i = (long long)row * p.ld_res + c;
-                in.w[j][0] = p.out_type == kFp32 ? static_cast<const uint32_t *>(p.residual)[i]
-                                                 : static_cast<const uint16_t *>(p.residual)[i];
-            }
-        } else if constexpr (EPI == kEpiDGate) {
-            const long long i = (long long)row * p.ld_saved + c;
-            in.w[j][0] = __float_as_uint(p.saved[i]), in.w[j][1] = __float_as_uint(p.saved2[i]);
-        }
+        const long long i = (long long)row * p.ld_res + c;
+        in[j] = p.out_type == kFp32 ? static_cast<const uint32_t *>(p.residual)[i]
+                                    : static_cast<const uint16_t *>(p.residual)[i];
     }
 }
 
@@ -589,47 +578,24 @@ __device__ __forceinline__ void column_store(void *out, int type, long long ld, 
 
 template <int EPI, int R>
 __device__ __forceinline__ void column_epilogue(const Epilogue &p, int r, int c, int step, float (&v)[R],
-                                                const float (&u)[EPI == kEpiGated ? R : 1],
-                                                const ColumnIn<EPI, R> &in) {
+                                                const uint32_t (&in)[R]) {
+    static_assert(epi_linear(EPI), "rows of a gated block's products are padded");
     if (c >= p.N) return;
-    if constexpr (epi_linear(EPI)) {
-        if (p.bias != nullptr) {
-            const float b = load_elem(p.bias, p.bias_type, c);
+    if (p.bias != nullptr) {
+        const float b = load_elem(p.bias, p.bias_type, c);
 #pragma unroll
-            for (int j = 0; j < R; ++j) v[j] += b;
-        }
-        if constexpr (EPI == kEpiAct) {
-            if (p.saved != nullptr) column_store<R>(p.saved, kFp32, p.ld_saved, r, p.M, c, step, v);
-            act_values<R>(p.act, v);
-        }
-        if (p.residual != nullptr) {
-#pragma unroll
-            for (int j = 0; j < R; ++j)
-                v[j] += p.out_type == kFp32 ? __uint_as_float(in.w[j][0]) : unpack16(in.w[j][0], p.out_type).x;
-        }
-        column_store<R>(p.out, p.out_type, p.ld_out, r, p.M, c, step, v);
-    } else if constexpr (EPI == kEpiGated) {
-        if (p.saved != nullptr) {
-            column_store<R>(p.saved, kFp32, p.ld_saved, r, p.M, c, step, v);
-            column_store<R>(p.saved2, kFp32, p.ld_saved, r, p.M, c, step, u);
-        }
-        act_values<R>(p.act, v);
-#pragma unroll
-        for (int j = 0; j < R; ++j) v[j] *= u[j];
-        column_store<R>(p.out, p.out_type, p.ld_out, r, p.M, c, step, v);
-    } else {
-        float a[R], d[R];
-#pragma unroll
-        for (int j = 0; j < R; ++j) a[j] = __uint_as_float(in.w[j][0]);
-        act_slopes<R>(p.act, a, a, d);
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            a[j] *= v[j];
-            d[j] *= v[j] * __uint_as_float(in.w[j][1]);
-        }
-        column_store<R>(p.out, p.out_type, p.ld_out, r, p.M, c, step, d);
-        column_store<R>(p.out2, p.out_type, p.ld_out, r, p.M, c, step, a);
+        for (int j = 0; j < R; ++j) v[j] += b;
     }
+    if constexpr (EPI == kEpiAct) {
+        if (p.saved != nullptr) column_store<R>(p.saved, kFp32, p.ld_saved, r, p.M, c, step, v);
+        act_values<R>(p.act, v);
+    }
+    if (p.residual != nullptr) {
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+            v[j] += p.out_type == kFp32 ? __uint_as_float(in[j]) : unpack16(in[j], p.out_type).x;
+    }
+    column_store<R>(p.out, p.out_type, p.ld_out, r, p.M, c, step, v);
 }
 
 }  // namespace route

@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // A thread's item is G columns of a row, neighbouring threads on
     // neighbouring columns: four, or one where rows cannot be accessed four
     // values at a time.  The cluster's CTAs share a tile's items.
-    const bool wide = (ep.vec & kVecOut) != 0;
+    const bool wide = !epi_linear(EPI) || (ep.vec & kVecOut) != 0;  // (a gated block's: padded rows)
     float *sums = reinterpret_cast<float *>(smem_raw + (sbase - raw));
     if (warp >= 2) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -358,14 +358,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             // a thread's rows of one column
 #pragma unroll 2
             for (int r = rows0 + e / kTileCols; r < rows1; r += kStep) {
-                float v = 0.f, u = 0.f;
-                for (int j = 0; j < C; ++j) {
-                    const uint32_t q = ptx::map_to_rank(value_at(r), (uint32_t)j);
-                    v += ld_cluster_f(q);
-                    if (EPI == kEpiGated) u += ld_cluster_f(q + kTileCols * 4u);
-                }
+                float v = 0.f;
+                for (int j = 0; j < C; ++j) v += ld_cluster_f(ptx::map_to_rank(value_at(r), (uint32_t)j));
                 st_shared_f(value_at(r), v);
-                if (EPI == kEpiGated) st_shared_f(value_at(r) + kTileCols * 4u, u);
             }
         }
         __syncwarp();
@@ -387,23 +382,22 @@ __global__ void __launch_bounds__(kThreads, 2)
             in = next;
         }
     } else if (warp >= 2 && ok) {
-        // a thread's rows of one column, kRows of them at a time
-        constexpr int kRows = EPI == kEpiGated || EPI == kEpiDGate ? 2 : 4;
-        const int c = e % kTileCols;
-        for (int r = rows0 + e / kTileCols; r < rows1; r += kStep * kRows) {
-            ColumnIn<EPI, kRows> in;
-            column_load<EPI, kRows>(ep, row0 + r, col0 + c, kStep, in);
-            float v[kRows] = {}, u[EPI == kEpiGated ? kRows : 1] = {};
+        if constexpr (epi_linear(EPI)) {
+            // a thread's rows of one column, kRows of them at a time
+            constexpr int kRows = 4;
+            const int c = e % kTileCols;
+            for (int r = rows0 + e / kTileCols; r < rows1; r += kStep * kRows) {
+                uint32_t res[kRows];
+                column_load<kRows>(ep, row0 + r, col0 + c, kStep, res);
+                float v[kRows] = {};
 #pragma unroll
-            for (int k = 0; k < kRows; ++k)
-                if (r + k * kStep < rows1) {
-                    v[k] += ld_shared_f(value_at(r + k * kStep));
-                    if constexpr (EPI == kEpiGated) u[k] += ld_shared_f(value_at(r + k * kStep) + kTileCols * 4u);
-                }
-            // rows of other CTAs' shares are not this one's to write
-            Epilogue own = ep;
-            own.M = row0 + rows1;
-            column_epilogue<EPI, kRows>(own, row0 + r, col0 + c, kStep, v, u, in);
+                for (int k = 0; k < kRows; ++k)
+                    if (r + k * kStep < rows1) v[k] += ld_shared_f(value_at(r + k * kStep));
+                // rows of other CTAs' shares are not this one's to write
+                Epilogue own = ep;
+                own.M = row0 + rows1;
+                column_epilogue<EPI, kRows>(own, row0 + r, col0 + c, kStep, v, res);
+            }
         }
     }
     if (warp == 1) {
