@@ -90,7 +90,8 @@ route_status route_gated_prepare(int rows, int k, int f, int n, int type, int ac
 route_status route_layer_destroy(route_layer *plan);
 
 /* route_layer_status: synchronise the plan's device, then report and clear
- * the device-side error word, as route_device_status does. */
+ * the device-side error word: ROUTE_OK, or ROUTE_ERR_DEVICE_TIMEOUT (a bounded
+ * wait expired; the outputs of that launch are invalid). */
 route_status route_layer_status(const route_layer *plan);
 
 /* Bytes of the `saved` buffer that a training forward call of `rows` rows

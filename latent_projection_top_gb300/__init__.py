@@ -59,8 +59,9 @@ STATUS_CODES = {name: code for code, name in STATUS_NAMES.items()}
 _HERE = os.path.dirname(os.path.abspath(__file__))
 RELEASE_LIB_PATH = os.path.join(_HERE, "_build", "libroute.so")
 DEBUG_LIB_PATH = os.path.join(_HERE, "_build", "debug", "libroute_debug.so")
-# ROUTE_DEBUG_LIB=1 selects the checked library (every computed global index
-# of the kernels bounds-checked; see builder.py), e.g. for a test process.
+# ROUTE_DEBUG_LIB=1 selects the checked library (every global index that the
+# route step's kernels compute is bounds-checked; see builder.py), e.g. for a
+# test process.
 LIB_PATH = DEBUG_LIB_PATH if os.environ.get("ROUTE_DEBUG_LIB") == "1" else RELEASE_LIB_PATH
 
 # Every symbol the header declares (checked by the CPU tests).

@@ -4,10 +4,10 @@ The translation units compile in parallel; ptxas resource usage (registers,
 spills, shared memory) is written to ``_build/ptxas.log``.
 
 ``build(debug=True)`` builds the same sources with ``-DROUTE_DEBUG`` into
-``_build/debug/libroute_debug.so``: every computed global index is checked
-in the kernels, and a failed check is reported through the device status
-word (``route_device_status`` returns ROUTE_ERR_DEVICE_BOUNDS) instead of
-faulting.  The binding loads it when the environment sets ROUTE_DEBUG_LIB=1.
+``_build/debug/libroute_debug.so``: every global index that the route step's
+kernels compute is checked, and a failed check is reported through the device
+status word (``route_device_status`` returns ROUTE_ERR_DEVICE_BOUNDS) instead
+of faulting.  The layer operators' kernels are the same in both.  The binding loads it when the environment sets ROUTE_DEBUG_LIB=1.
 
 With either goes the Python module of the layer operators' calls
 (``csrc/layer_call.cpp``, host code only).  It reads tensors through torch's

@@ -40,8 +40,8 @@ constexpr unsigned kStatusTimeout = 1u;
 constexpr unsigned kStatusBounds = 2u;  // debug library: an index out of range was skipped
 
 // ROUTE_IN_BOUNDS(ok, status): in the debug library (built with -DROUTE_DEBUG)
-// every computed global index is checked before its access; a failed check
-// sets kStatusBounds in the status word and the access is skipped, so the
+// every global index that the route step's kernels compute is checked before
+// its access (the layer operators' kernels check none); a failed check sets kStatusBounds in the status word and the access is skipped, so the
 // kernel neither faults nor traps.  In the release library it is `true`.
 #ifdef ROUTE_DEBUG
 __device__ __forceinline__ bool route_in_bounds(bool ok, unsigned *status) {

@@ -684,8 +684,6 @@ route_status route_layer_status(const route_layer *p) {
     if ((e = cudaMemcpy(&w, p->words, sizeof w, cudaMemcpyDeviceToHost)) != cudaSuccess ||
         (e = cudaMemset(p->words, 0, sizeof w)) != cudaSuccess)
         return cuda_fail(e, "status word");
-    if (w & kStatusBounds)
-        return api_fail(ROUTE_ERR_DEVICE_BOUNDS, "a kernel skipped an index out of range");
     if (w & kStatusTimeout)
         return api_fail(ROUTE_ERR_DEVICE_TIMEOUT, "a kernel gave up waiting; its outputs are invalid");
     return ROUTE_OK;
