@@ -41,8 +41,9 @@ constexpr unsigned kStatusBounds = 2u;  // debug library: an index out of range 
 
 // ROUTE_IN_BOUNDS(ok, status): in the debug library (built with -DROUTE_DEBUG)
 // every global index that the route step's kernels compute is checked before
-// its access (the layer operators' kernels check none); a failed check sets kStatusBounds in the status word and the access is skipped, so the
-// kernel neither faults nor traps.  In the release library it is `true`.
+// its access (the layer operators' kernels check none); a failed check sets
+// kStatusBounds in the status word and the access is skipped, so the kernel
+// neither faults nor traps.  In the release library it is `true`.
 #ifdef ROUTE_DEBUG
 __device__ __forceinline__ bool route_in_bounds(bool ok, unsigned *status) {
     if (!ok) atomicOr(status, kStatusBounds);
