@@ -116,6 +116,7 @@ def test_pair_tiles_with_calls_right_behind(rows, k, n, act):
     (16, 16384, 256),     # small tiles, more blocks than stages a CTA
     (4096, 512, 2048),    # pair tiles, one or two a pair
     (16384, 192, 2048),   # pair tiles, many a pair
+    (139, 3520, 4536),    # pair tiles, split
 ])
 @pytest.mark.parametrize("act", ["none", "silu"])
 def test_expired_waits_leave_the_next_call_right(rows, k, n, act):
