@@ -20,7 +20,9 @@
  *    statistics and kept pre-activations are FP32.  Between an operator's
  *    inputs and its results there is at most one rounding to 16 bits besides
  *    the result's own: h = act(gate) * up before W_down, and the gradients
- *    of pre-activations before the products that read them.
+ *    of pre-activations before the products that read them.  These have the
+ *    plan's type and so its range: an FP16 plan's become infinite past 65504,
+ *    and lose bits below 6.1e-5, though the result may be far from both.
  *  - Matrices that a product reads (x, dout, the weights) and whose width is
  *    a multiple of 8 start on 16 bytes and have row strides that are
  *    multiples of 8, otherwise ROUTE_ERR_ALIGN.  Where the width is not a

@@ -1,6 +1,7 @@
 // Launch arguments and internal launch entry points of the layer operators
 // (layer norm, linear, gated block): the kernels' side is in layer_gemm.cu,
-// layer_elem.cu and layer_norm.cu, the C ABI's in layer_api.cu.
+// layer_small.cu, layer_elem.cu and layer_norm.cu, the C ABI's in layer_api.cu
+// (layer_call.cpp, the Python module, sees the C ABI only).
 #pragma once
 
 #include <cstdint>

@@ -248,6 +248,8 @@ Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
             if (count == 1) {  // equal items
                 t += longest + (ceil_div(items, p->pairs) - 1) * (longest < drain_us ? drain_us : longest);
             } else {
+                // items do not end together (16x3584x7168's backward pass 27.6 us, 32.4
+                // without this; with 0.7 512x2048x512 7.6, so 6.7)
                 level += 0.35 * longest;
                 t += level > longest ? level : longest;
             }
@@ -279,7 +281,8 @@ Choice choose(const route_layer *p, int epi, const Prod *w, int count) {
                     const long long ctas = (long long)ceil_div(w[i].M, bn) * ceil_div(w[i].N, cols) * s;
                     level += (double)ctas * one / p->sms;
                 }
-                // one round of CTAs is as long as the longest of them
+                // one round of CTAs is as long as the longest of them; of several, not all
+                // end together (3000x256x2048's backward pass 16.1 us, 17.1 without)
                 if (tiles * s <= p->sms) level = 0;
                 double t = count > 1 && level > 0 ? level + 0.3 * longest : longest;
                 t = t < longest ? longest : t < level ? level : t;
@@ -307,7 +310,9 @@ void set_tiles(GemmProblem &q, int tile_rows, int tile_cols, int pairs) {
     // 4096x3584x7168: 129.0, 8 columns 131.9), else about a square of tiles at
     // work (8192x3584x7168: 8 columns 264.7, 28 270.8, 2 269.3).
     int band = q.tiles_n <= 16 ? q.tiles_n : q.tiles_m <= 16 ? 2 : 8;
-    const int least = ceil_div(pairs, q.tiles_m);  // as many tiles as pairs in a band
+    // With few rows, as many tiles as pairs in a band (512x3584x16384 42.4 us, by
+    // the line above 43.1; with 8 rows of tiles, 2048x7168x7168, 113.8 and 109.3).
+    const int least = ceil_div(pairs, q.tiles_m);
     band = q.tiles_m < 8 && band < least ? least : band;
     q.band = band < q.tiles_n ? band : q.tiles_n;
 }
@@ -500,7 +505,8 @@ route_status backward_products(const route_layer *p, int rows, Prod *all, int co
     const Choice &weights = choice_of(p, kSlotWeights, rows, kEpiLinear, all + 1, count - 1);
     Prod w[kGemmMaxProblems];
     int n = 0;
-    // (the second launch's start hides behind the first)
+    // (the second launch's start hides behind the first, but for 1.4 us: 16x3584x7168
+    // 27.6 us in two launches, 32.8 in one; 2050x896x3584 25.5 in one, 33.2 in two)
     if (input.us + weights.us + 1.4 < one.us) {
         Prod *dx = all[0].e.out ? all : nullptr;
         for (int i = 1; i < count; ++i)

@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(256, 4) dz_kernel(const __grid_constant__ DzAr
 constexpr int kBiasRows = 4;  // rows whose loads are on the way together
 constexpr int kBiasWarps = 4;
 constexpr int kBiasMaxBlocks = kDzMaxBlocks / kBiasWarps;
+// dbias alone, 3584 columns: 128 rows 4.2 us, in row blocks 5.4; 256 rows 4.4, in one 6.8.
 constexpr int kBiasOneBlock = 128;  // rows
 __global__ void __launch_bounds__(32 * kBiasWarps)
     bias_part_kernel(const __grid_constant__ DzArgs a, int rows_per_warp, int vec, int after) {

@@ -727,8 +727,10 @@ int gemm_smem_bytes() { return (int)(smem_of(256) > smem_of(128) ? smem_of(256) 
 cudaError_t gemm_launch(int form, int epi, int bn, const GemmMaps &maps, const GemmArgs &args,
                         cudaStream_t stream) {
     // A residual is read packed only where a tile's products take longer than
-    // that, since no buffer is left to read it a tile ahead (4096x3584x7168 132.7
-    // us, by fours 135.5; 4096x1024x3584 28.0, by fours 27.3).
+    // that, since no buffer is left to read it a tile ahead (residuals from memory:
+    // 4096x64x3584 25.5 us, by fours 21.1; 4096x1024x3584, 16 k-blocks, 28.5 and
+    // 27.5; 4096x1472x3584, 23 of them, 31.1 and 32.8; in L2 packed is as fast or
+    // faster at all of these, and with one tile a pair: 700x512x2048 6.5 and 7.6).
     constexpr int kResidualBlocks = 24;
     bool fours = true, any = epi != kEpiDGate, packed = any, residual = false;
     for (int i = 0; i < args.nprob; ++i) {

@@ -15,10 +15,10 @@
 // 896x896 the sums' last step took 25 of 31 us when one CTA did it for a
 // tile, from partials in L2.
 //
-// Bound by HBM where the weights are large (8x3584x7168 11.9 us, 51.7 MB: 4.3
+// Bound by HBM where the weights are large (8x3584x7168 12.0 us, 51.7 MB: 4.3
 // TB/s over the whole launch, which is the memory's rate plus 4 us of the
 // launch's start, the first copies' latency and the sums), else by those
-// latencies (16x64x128 3.3 us, 64x896x896 4.6).
+// latencies (16x64x128 3.2 us, 64x896x896 4.8).
 //
 // Two CTAs fit an SM, so that a call's second product fetches its first
 // weights under the first one's last sums.
