@@ -149,6 +149,18 @@ __device__ __forceinline__ void add_parts(uint32_t at, uint32_t next, int C) {
     }
 }
 
+// The same of one value.
+__device__ __forceinline__ void add_parts(uint32_t at, int C) {
+    float f[kSmallMaxSplits], v = 0.f;
+#pragma unroll
+    for (int j = 0; j < kSmallMaxSplits; ++j)
+        if (j < C) f[j] = ld_cluster_f(ptx::map_to_rank(at, (uint32_t)j));
+#pragma unroll
+    for (int j = 0; j < kSmallMaxSplits; ++j)
+        if (j < C) v += f[j];
+    st_shared_f(at, v);
+}
+
 template <int EPI, int BN>
 __global__ void __launch_bounds__(kThreads, 2)
     layer_small_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs args,
@@ -348,6 +360,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     auto col_of = [&](int x) { return col0 + x % kGroups * 4; };
     EpiIn<EPI> in, next;
     if (warp >= 2 && wide && i0 + e < i1) epi_load<EPI>(ep, row_of(i0 + e), col_of(i0 + e), in);
+    constexpr int kRows = 4;  // of a column that a thread takes together
+    const int own0 = rows0 + e / kTileCols;
+    uint32_t res[kRows];
+    if constexpr (epi_linear(EPI))
+        if (warp >= 2 && !wide && own0 < rows1) column_load<kRows>(ep, row0 + own0, col0 + e % kTileCols, kStep, res);
     if (C > 1) {
         if (warp >= 2 && ok && wide) {
             for (int x = i0 + e; x < i1; x += kEpiThreads) {
@@ -356,12 +373,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         } else if (warp >= 2 && ok && e % kTileCols < cols) {
             // a thread's rows of one column
-#pragma unroll 2
-            for (int r = rows0 + e / kTileCols; r < rows1; r += kStep) {
-                float v = 0.f;
-                for (int j = 0; j < C; ++j) v += ld_cluster_f(ptx::map_to_rank(value_at(r), (uint32_t)j));
-                st_shared_f(value_at(r), v);
-            }
+            for (int r = own0; r < rows1; r += kStep) add_parts(value_at(r), C);
         }
         __syncwarp();
         // After the last remote read (ordered: peers may leave; the order takes 0.17
@@ -383,12 +395,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     } else if (warp >= 2 && ok) {
         if constexpr (epi_linear(EPI)) {
-            // a thread's rows of one column, kRows of them at a time
-            constexpr int kRows = 4;
-            const int c = e % kTileCols;
-            for (int r = rows0 + e / kTileCols; r < rows1; r += kStep * kRows) {
-                uint32_t res[kRows];
-                column_load<kRows>(ep, row0 + r, col0 + c, kStep, res);
+            for (int r = own0; r < rows1; r += kStep * kRows) {
+                if (r != own0) column_load<kRows>(ep, row0 + r, col0 + e % kTileCols, kStep, res);
                 float v[kRows] = {};
 #pragma unroll
                 for (int k = 0; k < kRows; ++k)
@@ -396,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 // rows of other CTAs' shares are not this one's to write
                 Epilogue own = ep;
                 own.M = row0 + rows1;
-                column_epilogue<EPI, kRows>(own, row0 + r, col0 + c, kStep, v, res);
+                column_epilogue<EPI, kRows>(own, row0 + r, col0 + e % kTileCols, kStep, v, res);
             }
         }
     }
