@@ -3,9 +3,9 @@
 Argument marshalling only, like the route step's binding: tensors are checked
 for dtype, shape, stride and device, then their pointers, row strides and the
 CUDA stream go to the C entry points of the same names.  Calls whose arguments
-are plainly right take a short way, a compiled module that makes the same
-checks (``csrc/layer_call.cpp``: 2 to 5 us less a call); all others go through
-the checks here, which raise what is wrong.
+are plainly right take a short way where it is built, a compiled module that
+makes the same checks (``csrc/layer_call.cpp``: 2 to 5 us less a call); all
+others go through the checks here, which raise what is wrong.
 
 * ``norm_forward`` / ``norm_backward`` -- layer norm of token rows;
 * ``linear_forward`` / ``linear_backward`` -- ``act(x W + bias) + residual``;
