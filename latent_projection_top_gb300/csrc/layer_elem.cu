@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(256, 4) dz_kernel(const __grid_constant__ DzAr
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] = e < n ? v[e] * d[e] : 0.f;
                 }
+                // 16 bits: an operand of the products (the sums below take it unrounded)
                 if (dz != nullptr)  // ld_dz is a multiple of 8
                     *reinterpret_cast<uint4 *>(dz + (long long)row * a.ld_dz + c) =
                         make_uint4(pack16(v[0], v[1], a.type), pack16(v[2], v[3], a.type),

@@ -279,6 +279,12 @@ __device__ __forceinline__ void epi_load(const Epilogue &p, int r, int c, EpiIn<
 
 // The epilogue of four columns from column c (a multiple of 4) of row r: v
 // holds the FP32 sums (gated: u the up sums), `in` what epi_load read.
+//
+// A gated block's h, d gate and d up are rounded to the operands' 16 bits here,
+// as dz is in layer_elem.cu: the next product reads them as tensor-core
+// operands, which have no more (in FP32 they would take two or three products
+// of 16-bit parts each).  With the result's own rounding the error against 64
+// bits is 1.4 times that of one rounding; in FP16 they are infinite past 65504.
 template <int EPI>
 __device__ __forceinline__ void epilogue(const Epilogue &p, int r, int c, float (&v)[4],
                                          const float (&u)[4], const EpiIn<EPI> &in) {
