@@ -31,6 +31,12 @@ The route step of one MoE layer (see ``include/route.h``):
 What a layer runs next to the route step (``layer.py``, ``include/route_layer.h``):
 ``NormPlan``, ``LinearPlan``, ``GatedPlan`` and ``norm_``, ``linear_`` and
 ``gated_`` ``forward`` / ``backward``.
+
+The routed experts, from the step's ids and weights to the residual stream
+(``experts.py``, ``include/route_experts.h``): ``DispatchPlan`` with
+``dispatch_sort``, ``dispatch_gather`` and ``dispatch_combine``, ``ExpertsPlan``
+with ``experts_forward``, ``DropoutPlan`` with ``dropout_forward``, and their
+``_backward``.
 """
 
 from __future__ import annotations
@@ -150,6 +156,7 @@ def lib() -> ctypes.CDLL:
                   "route_step", "route_step_host", "route_step_sumsq", "route_device_status"):
             getattr(L, f).restype = i32
         _layer.declare(L)
+        _experts.declare(L)
         _lib = L
     return _lib
 
@@ -587,3 +594,11 @@ from . import layer as _layer  # noqa: E402  (it uses the names above)
 from .layer import (  # noqa: E402,F401
     ACTIVATIONS, LAYER_MAX_ROWS, LAYER_MAX_WIDTH, NORM_MAX_WIDTH, GatedPlan, LinearPlan, NormPlan,
     gated_backward, gated_forward, linear_backward, linear_forward, norm_backward, norm_forward)
+
+# ---- the routed experts' operators, and dropout (experts.py) ------------------
+
+from . import experts as _experts  # noqa: E402
+from .experts import (  # noqa: E402,F401
+    EXPERTS_MAX_ROWS, MAX_EXPERTS, MAX_TOPK, DispatchPlan, DropoutPlan, ExpertsPlan,
+    dispatch_combine, dispatch_combine_backward, dispatch_gather, dispatch_gather_backward,
+    dispatch_sort, dropout_backward, dropout_forward, experts_backward, experts_forward)

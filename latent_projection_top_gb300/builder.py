@@ -40,9 +40,10 @@ CALL_SOURCE = os.path.join(CSRC, "layer_call.cpp")
 
 SOURCES = ["decode_kernel.cu", "prefill_kernel.cu", "topk_kernel.cu", "stage_kernel.cu",
            "route_api.cu", "layer_gemm.cu", "layer_small.cu", "layer_elem.cu",
-           "layer_norm.cu", "layer_api.cu"]
+           "layer_norm.cu", "layer_api.cu", "dispatch_kernel.cu", "experts_kernel.cu",
+           "dropout_kernel.cu", "experts_api.cu"]
 HEADERS = ["common.cuh", "sm103_ptx.cuh", "topk16.cuh", "twofloat.cuh", "api_util.h", "layer.cuh",
-           "layer_math.cuh", "layer_ptx.cuh"]
+           "layer_math.cuh", "layer_ptx.cuh", "layer_plan.h", "experts.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -52,7 +53,7 @@ FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
 
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
-    files += [os.path.join(INCLUDE, h) for h in ("route.h", "route_layer.h")]
+    files += [os.path.join(INCLUDE, h) for h in ("route.h", "route_layer.h", "route_experts.h")]
     files.append(os.path.abspath(__file__))
     return files
 

@@ -19,4 +19,10 @@ route_status api_encode_operand(CUtensorMap *m, const void *ptr, bool fp16, uint
                                 uint64_t outer, uint64_t ld, uint32_t box_inner,
                                 uint32_t box_outer, const char *what);
 
+// The same of `count` such matrices, `step` values apart (a multiple of 8), in
+// boxes of one of them.
+route_status api_encode_operands(CUtensorMap *m, const void *ptr, bool fp16, uint64_t inner, uint64_t outer,
+                                 uint64_t count, uint64_t ld, uint64_t step, uint32_t box_inner,
+                                 uint32_t box_outer, const char *what);
+
 }  // namespace route

@@ -1,0 +1,380 @@
+// Tokens sorted by expert and back: the stable counting sort of the (row,
+// expert) pairs, the rows copied to their places, and the weighted sums that
+// bring the experts' results back, with their gradients.
+#include "experts.cuh"
+#include "layer_math.cuh"
+
+namespace route {
+namespace {
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortMaxCtas = 8;  // of the cluster
+
+// ---- sort -------------------------------------------------------------------------
+//
+// One cluster sorts all pairs.  Every warp takes a run of them, counts its
+// pairs of each expert in shared memory, and after the counts have been summed
+// over the warps before it, the CTAs before its own (distributed shared memory)
+// and the experts before each, it goes through its run once more and gives
+// each pair its place: the order within an expert is that of the pairs.
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ SortArgs a, int warps) {
+    extern __shared__ int smem[];
+    int *counts = smem;                          // [warps][experts]
+    int *total = smem + warps * a.experts;       // [experts], read by the cluster
+    int *base = total + a.experts;               // [experts]
+    __shared__ int s_scan[kSortWarps];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int ctas = gridDim.x, rank = blockIdx.x;
+    const int E = a.experts;
+    const int pairs = a.rows * a.topk;
+    // a warp's run: whole groups of 32
+    const int runs = ctas * warps;
+    const int run = ((pairs + runs - 1) / runs + 31) & ~31;
+    const long long from = (long long)(rank * warps + warp) * run;
+    const int p0 = warp < warps ? (int)(from < pairs ? from : pairs) : pairs;
+    const int p1 = (long long)p0 + run < pairs ? p0 + run : pairs;
+    for (int i = tid; i < warps * E; i += kSortThreads) counts[i] = 0;
+    __syncthreads();
+    auto key_of = [&](int p) {
+        if (p >= p1) return -1;
+        const int r = p / a.topk;
+        const int id = a.ids[(long long)r * a.ld_ids + (p - r * a.topk)];
+        const int k = (int)((unsigned)id - (unsigned)a.first);
+        return id >= a.first && k < E ? k : -1;
+    };
+    for (int p = p0; p < p1; p += 32) {
+        const int k = key_of(p + lane);
+        if (k >= 0) atomicAdd(&counts[warp * E + k], 1);
+    }
+    __syncthreads();
+    // counts become what the CTA's warps before hold; totals of the CTA
+    const int e = tid;
+    int mine = 0;
+    if (e < E) {
+        for (int w = 0; w < warps; ++w) {
+            const int c = counts[w * E + e];
+            counts[w * E + e] = mine;
+            mine += c;
+        }
+        total[e] = mine;
+    }
+    int before = 0, all = mine;
+    if (ctas > 1) {
+        ptx::cluster_sync();
+        if (e < E) {
+            all = 0;
+            for (int j = 0; j < ctas; ++j) {
+                int c;
+                asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                             : "=r"(c)
+                             : "r"(ptx::map_to_rank(ptx::smem_addr(total + e), (uint32_t)j))
+                             : "memory");
+                if (j < rank) before += c;
+                all += c;
+            }
+        }
+        ptx::cluster_arrive();  // after the last remote read
+    }
+    // exclusive sums over the experts
+    int scan = all;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int t = __shfl_up_sync(0xFFFFFFFFu, scan, d);
+        if (lane >= d) scan += t;
+    }
+    if (lane == 31) s_scan[warp] = scan;
+    __syncthreads();
+    if (warp == 0) {
+        int t = s_scan[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, t, d);
+            if (lane >= d) t += u;
+        }
+        s_scan[lane] = t;
+    }
+    __syncthreads();
+    scan += warp > 0 ? s_scan[warp - 1] : 0;
+    if (e < E) {
+        base[e] = scan - all + before;
+        if (rank == 0) {
+            a.offsets[e + 1] = scan;
+            if (e == 0) a.offsets[0] = 0;
+        }
+    }
+    __syncthreads();
+    for (int p = p0; p < p1; p += 32) {
+        const int k = key_of(p + lane);
+        const unsigned same = __match_any_sync(0xFFFFFFFFu, k);
+        const int at = k >= 0 ? base[k] + counts[warp * E + k] + __popc(same & ((1u << lane) - 1u)) : -1;
+        __syncwarp();
+        if (k >= 0 && (same >> lane) == 1u) counts[warp * E + k] += __popc(same);  // the last of them
+        __syncwarp();
+        if (p + lane < p1) {
+            a.place[p + lane] = at;
+            if (k >= 0 && a.source != nullptr) a.source[at] = p + lane;
+        }
+    }
+    if (ctas > 1) ptx::cluster_wait();  // nobody leaves while another may read its totals
+}
+
+// ---- moves ------------------------------------------------------------------------
+
+// The values of one 16-byte piece (W of a type), or of one element.
+template <int TY, bool VEC>
+struct Piece {
+    static constexpr int kN = VEC ? 16 / layer_esize(TY) : 1;
+    uint32_t w[VEC ? 4 : 1];
+    __device__ __forceinline__ void load(const void *p, long long i) {
+        if constexpr (VEC) {
+            const uint4 t = *reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + i * layer_esize(TY));
+            w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
+        } else if constexpr (TY == kFp32) {
+            w[0] = static_cast<const uint32_t *>(p)[i];
+        } else {
+            w[0] = static_cast<const uint16_t *>(p)[i];
+        }
+    }
+    __device__ __forceinline__ void store(void *p, long long i) const {
+        if constexpr (VEC) {
+            *reinterpret_cast<uint4 *>(static_cast<char *>(p) + i * layer_esize(TY)) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else if constexpr (TY == kFp32) {
+            static_cast<uint32_t *>(p)[i] = w[0];
+        } else {
+            static_cast<uint16_t *>(p)[i] = (uint16_t)w[0];
+        }
+    }
+    __device__ __forceinline__ void values(float (&v)[kN]) const {
+        if constexpr (TY == kFp32) {
+#pragma unroll
+            for (int e = 0; e < kN; ++e) v[e] = __uint_as_float(w[e]);
+        } else if constexpr (VEC) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = unpack16(w[e], TY);
+                v[2 * e] = f.x, v[2 * e + 1] = f.y;
+            }
+        } else {
+            v[0] = unpack16(w[0], TY).x;
+        }
+    }
+    __device__ __forceinline__ void set(const float (&v)[kN]) {
+        if constexpr (TY == kFp32) {
+#pragma unroll
+            for (int e = 0; e < kN; ++e) w[e] = __float_as_uint(v[e]);
+        } else if constexpr (VEC) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = pack16(v[2 * e], v[2 * e + 1], TY);
+        } else {
+            w[0] = pack16(v[0], 0.f, TY) & 0xFFFFu;
+        }
+    }
+};
+
+// A row's places that are there, in the row's order.
+struct Places {
+    int n;
+    int at[kMaxTopk];
+    float w[kMaxTopk];
+    int j[kMaxTopk];
+};
+__device__ __forceinline__ void find_places(const MoveArgs &a, int r, Places &s) {
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        const long long i = (long long)r * a.topk + lane;
+        const int p = lane < a.topk ? a.place[i] : -1;
+        const bool there = p >= 0 && p < a.pairs;
+        const unsigned all = __ballot_sync(0xFFFFFFFFu, there);
+        if (there) {
+            const int k = __popc(all & ((1u << lane) - 1u));
+            s.at[k] = p;
+            s.w[k] = a.weights != nullptr ? a.weights[i] : 1.f;
+            s.j[k] = lane;
+        }
+        if (lane == 0) s.n = __popc(all);
+        if (a.dweights != nullptr && lane < a.topk && !there) a.dweights[i] = 0.f;
+    }
+    __syncthreads();
+}
+
+// A block a row: out[place] = x[row].
+template <int ES, bool VEC>
+__global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ MoveArgs a) {
+    using P = Piece<ES == 4 ? kFp32 : kBf16, VEC>;
+    __shared__ Places s;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int r = blockIdx.x;
+    find_places(a, r, s);
+    const int n = s.n, pieces = a.dim / P::kN;
+    for (int i = threadIdx.x; i < pieces && n > 0; i += blockDim.x) {
+        P p;
+        p.load(a.a, r * a.ld_a + (long long)i * P::kN);
+        for (int k = 0; k < n; ++k) p.store(a.out, s.at[k] * a.ld_out + (long long)i * P::kN);
+    }
+}
+
+// A block a row: out[row] = residual[row] + sum_j w_j b[place_j], in the order
+// of j.
+constexpr int kAhead = 8;  // experts' rows on the way together
+template <int TY, bool VEC>
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ MoveArgs a) {
+    using P = Piece<TY, VEC>;
+    __shared__ Places s;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int r = blockIdx.x;
+    find_places(a, r, s);
+    const int n = s.n, pieces = a.dim / P::kN;
+    for (int i = threadIdx.x; i < pieces; i += blockDim.x) {
+        const long long c = (long long)i * P::kN;
+        float sum[P::kN] = {};
+        P res;
+        if (a.a != nullptr) res.load(a.a, r * a.ld_a + c);
+        for (int k0 = 0; k0 < n; k0 += kAhead) {
+            P p[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (k0 + k < n) p[k].load(a.b, s.at[k0 + k] * a.ld_b + c);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (k0 + k < n) {
+                    float v[P::kN];
+                    p[k].values(v);
+                    const float w = s.w[k0 + k];
+#pragma unroll
+                    for (int e = 0; e < P::kN; ++e) sum[e] = a.weights != nullptr ? fmaf(w, v[e], sum[e]) : sum[e] + v[e];
+                }
+        }
+        if (a.a != nullptr) {
+            float v[P::kN];
+            res.values(v);
+#pragma unroll
+            for (int e = 0; e < P::kN; ++e) sum[e] += v[e];
+        }
+        P o;
+        o.set(sum);
+        o.store(a.out, r * a.ld_out + c);
+    }
+}
+
+// A block a row, a warp an expert's row at a time: out[place_j] = w_j dout[row],
+// dweights_j = <dout[row], b[place_j]>.
+template <int TY, bool VEC>
+__global__ void __launch_bounds__(256) combine_backward_kernel(const __grid_constant__ MoveArgs a) {
+    using P = Piece<TY, VEC>;
+    __shared__ Places s;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int r = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    find_places(a, r, s);
+    const int n = s.n, pieces = a.dim / P::kN;
+    for (int k = warp; k < n; k += blockDim.x >> 5) {
+        const float w = s.w[k];
+        float dot[P::kN] = {};
+#pragma unroll 2
+        for (int i = lane; i < pieces; i += 32) {
+            const long long c = (long long)i * P::kN;
+            P g;
+            g.load(a.a, r * a.ld_a + c);
+            float gv[P::kN], v[P::kN];
+            g.values(gv);
+            if (a.dweights != nullptr) {
+                P y;
+                y.load(a.b, s.at[k] * a.ld_b + c);
+                y.values(v);
+#pragma unroll
+                for (int e = 0; e < P::kN; ++e) dot[e] = fmaf(gv[e], v[e], dot[e]);
+            }
+            if (a.out != nullptr) {
+#pragma unroll
+                for (int e = 0; e < P::kN; ++e) v[e] = w * gv[e];
+                P o;
+                o.set(v);
+                o.store(a.out, s.at[k] * a.ld_out + c);
+            }
+        }
+        float t = 0.f;
+#pragma unroll
+        for (int e = 0; e < P::kN; ++e) t += dot[e];
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
+        if (lane == 0 && a.dweights != nullptr) a.dweights[(long long)r * a.topk + s.j[k]] = t;
+    }
+}
+
+// Rows that may be accessed 16 bytes at a time.
+bool vectors(const MoveArgs &a) {
+    const int es = layer_esize(a.type);
+    auto rows_on = [&](const void *p, long long ld) {
+        return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0);
+    };
+    return a.dim * es % 16 == 0 && rows_on(a.a, a.ld_a) && rows_on(a.b, a.ld_b) && rows_on(a.out, a.ld_out);
+}
+
+cudaError_t launch(const void *k, unsigned grid, unsigned block, size_t smem, unsigned cluster, void **params,
+                   cudaStream_t stream) {
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute attr[2];
+    c.gridDim = dim3(grid);
+    c.blockDim = dim3(block);
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    c.attrs = attr;
+    c.numAttrs = 2;
+    return cudaLaunchKernelExC(&c, k, params);
+}
+
+size_t sort_smem(int warps, int experts) { return ((size_t)warps + 2) * experts * sizeof(int); }
+
+#define ROUTE_MOVE(K, A, V)                                                              \
+    ((A).type == kFp32   ? reinterpret_cast<const void *>(K<kFp32, V>)                   \
+     : (A).type == kFp16 ? reinterpret_cast<const void *>(K<kFp16, V>)                   \
+                         : reinterpret_cast<const void *>(K<kBf16, V>))
+
+}  // namespace
+
+cudaError_t sort_configure() {
+    return cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)sort_smem(kSortWarps, kMaxExperts));
+}
+
+cudaError_t sort_launch(const SortArgs &args, cudaStream_t stream) {
+    const long long pairs = (long long)args.rows * args.topk;
+    const long long groups = (pairs + 31) / 32;
+    int warps = groups < kSortWarps ? (int)(groups < 1 ? 1 : groups) : kSortWarps;
+    unsigned ctas = 1;
+    while (ctas < kSortMaxCtas && groups > 4ll * ctas * kSortWarps) ctas *= 2;
+    void *params[] = {const_cast<SortArgs *>(&args), &warps};
+    return launch(reinterpret_cast<const void *>(sort_kernel), ctas, kSortThreads, sort_smem(warps, args.experts),
+                  ctas, params, stream);
+}
+
+cudaError_t gather_launch(const MoveArgs &args, int, cudaStream_t stream) {
+    const bool vec = vectors(args);
+    const void *k = layer_esize(args.type) == 4 ? (vec ? reinterpret_cast<const void *>(gather_kernel<4, true>)
+                                                       : reinterpret_cast<const void *>(gather_kernel<4, false>))
+                                                : (vec ? reinterpret_cast<const void *>(gather_kernel<2, true>)
+                                                       : reinterpret_cast<const void *>(gather_kernel<2, false>));
+    void *params[] = {const_cast<MoveArgs *>(&args)};
+    return launch(k, (unsigned)args.rows, 256, 0, 1, params, stream);
+}
+
+cudaError_t combine_launch(const MoveArgs &args, cudaStream_t stream) {
+    const void *k = vectors(args) ? ROUTE_MOVE(combine_kernel, args, true) : ROUTE_MOVE(combine_kernel, args, false);
+    void *params[] = {const_cast<MoveArgs *>(&args)};
+    return launch(k, (unsigned)args.rows, 256, 0, 1, params, stream);
+}
+
+cudaError_t combine_backward_launch(const MoveArgs &args, cudaStream_t stream) {
+    const void *k = vectors(args) ? ROUTE_MOVE(combine_backward_kernel, args, true)
+                                  : ROUTE_MOVE(combine_backward_kernel, args, false);
+    void *params[] = {const_cast<MoveArgs *>(&args)};
+    return launch(k, (unsigned)args.rows, 256, 0, 1, params, stream);
+}
+
+}  // namespace route

@@ -1,0 +1,720 @@
+// The routed experts' matrix products on the sm_103a tensor cores, two SMs per
+// tile: every expert's weights meet the run of sorted rows that is its own.
+//
+//   D[r, c] = sum_k A[r, k] B_e[k, c]     offsets[e] <= r < offsets[e + 1]
+//   dW_e[m, n] = sum_r A[r, m] B[r, n]    over the same rows
+//
+// 16-bit operands, FP32 sums, and what the operator makes of them before they
+// are written (layer_math.cuh: epilogue).  How many rows an expert has is known
+// on the device only: a launch is as many CTA pairs as the GPU holds, and each
+// finds its tiles from the offsets.
+//
+// Rows kernel: columns of D (the weights') are the tensor cores' M side, 256 a
+// tile and 128 a CTA, rows their N side, as many as there are up to 256 in
+// steps of 32: an expert with two rows costs the reading of its weights, one
+// with a thousand runs at the tensor cores' rate, and no rule chooses between
+// them.  A run of more than 256 rows is cut into equal parts.
+//
+// Gradient kernel: rows of dW are the M side, its columns the N side, 256 x 256
+// a tile.  The last block of an expert's rows holds rows of the next one: they
+// are overwritten with zeros in shared memory, in both operands, before the
+// tensor cores read them (a product with zero would keep an infinity or a NaN).
+//
+// Warp roles, waits and their limits as in layer_gemm.cu.
+#include "experts.cuh"
+#include "layer_math.cuh"
+#include "layer_ptx.cuh"
+
+namespace route {
+namespace {
+
+constexpr uint32_t kSmemLimit = 227 * 1024;
+constexpr uint32_t kWaitHintNs = 20000;
+
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+    d |= 1ull << 46;  // descriptor version for tcgen05
+    d |= 2ull << 61;  // 128-byte swizzle
+    return d;
+}
+
+// 16 k of an operand tile, as in layer_gemm.cu.
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t base, int kk) {
+    return MN ? smem_desc(base + kk * 2048u, 8192u, 1024u) : smem_desc(base + kk * 32u, 16u, 1024u);
+}
+
+template <class Args>
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const Args &a, volatile int *abort_flag) {
+    if (ptx::mbar_try_wait_hint(bar, parity, kWaitHintNs)) return true;
+    const uint64_t t0 = ptx::global_timer_ns();
+    for (;;) {
+        if (ptx::mbar_try_wait_hint(bar, parity, kWaitHintNs)) return true;
+        if (*abort_flag) return false;
+        if (ptx::global_timer_ns() - t0 > a.timeout_ns) {
+            *abort_flag = 1;
+            atomicOr(a.status, kStatusTimeout);
+            return false;
+        }
+    }
+}
+
+// Bounded wait used only while tearing down.
+template <class Args>
+__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, const Args &a) {
+    const uint64_t t0 = ptx::global_timer_ns();
+    while (!ptx::mbar_try_wait_hint(bar, parity, kWaitHintNs)) {
+        if (ptx::global_timer_ns() - t0 > a.timeout_ns) {
+            atomicOr(a.status, kStatusTimeout);
+            return;
+        }
+    }
+}
+
+// The rows of expert e: within 0 .. rows whatever the offsets say.
+struct Run {
+    int lo, hi;
+};
+__device__ __forceinline__ Run run_of(const int *offsets, int e, int rows) {
+    Run r;
+    r.lo = min(max(offsets[e], 0), rows);
+    r.hi = max(min(offsets[e + 1], rows), r.lo);
+    return r;
+}
+
+// ---- rows -------------------------------------------------------------------------
+
+constexpr int kRowsThreads = 320;
+constexpr int kRowsStages = 5;
+constexpr uint32_t kWBytes = 128 * 64 * 2;                  // a CTA's weight columns of a k-block
+constexpr uint32_t kTBytes = kExpertRows / 2 * 64 * 2;      // its rows, at most
+constexpr uint32_t kRowsStage = kWBytes + kTBytes;
+constexpr int kTurnRows = 32;                               // rows an epilogue group turns around at once
+constexpr uint32_t kTurnBytes = kTurnRows * 128 * 4;
+constexpr uint32_t kRowsBars = 256;
+constexpr uint32_t kRowsTable = 2 * (kMaxExperts + 4) * 4;  // parts before each expert, and offsets
+constexpr uint32_t kRowsSmem = 1024 + kRowsStages * kRowsStage + 2 * kTurnBytes + kRowsBars + kRowsTable;
+static_assert(kRowsSmem <= kSmemLimit, "shared memory");
+
+// Equal parts of at most 256 rows, in steps of 32.
+__device__ __forceinline__ int part_rows(int rows) {
+    const int parts = (rows + kExpertRows - 1) / kExpertRows;
+    return parts > 0 ? ((rows + parts - 1) / parts + 31) & ~31 : 32;
+}
+
+// A tile: expert, rows row0 .. end, column tile, columns of the MMA (rows
+// rounded up to 32).
+struct Tile {
+    int e, row0, end, tn, n;
+};
+struct Table {
+    const int *first;    // parts of the experts before; [experts]: all parts
+    const int *offsets;  // in shared memory
+};
+__device__ __forceinline__ Tile tile_of(const ExpertsArgs &a, const Table &t, unsigned i) {
+    Tile x;
+    const int part = (int)(i / (unsigned)a.tiles_n);
+    x.tn = (int)(i - (unsigned)part * (unsigned)a.tiles_n);
+    int lo = 0, hi = a.experts;  // first[lo] <= part < first[hi]
+    while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (t.first[m] <= part)
+            lo = m;
+        else
+            hi = m;
+    }
+    x.e = lo;
+    const Run r = run_of(t.offsets, lo, a.rows);
+    const int step = part_rows(r.hi - r.lo);
+    x.row0 = r.lo + (part - t.first[lo]) * step;
+    x.end = min(r.hi, x.row0 + step);
+    x.n = (x.end - x.row0 + 31) & ~31;
+    return x;
+}
+
+// All threads: the table of parts.  Returns the number of them.
+__device__ __forceinline__ int make_table(const ExpertsArgs &a, int *first, int *offsets, int *scan) {
+    constexpr int kEach = 4;
+    static_assert(kEach * kRowsThreads >= kMaxExperts, "a thread's experts");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int e = tid; e <= a.experts; e += kRowsThreads) offsets[e] = a.offsets[e];
+    __syncthreads();
+    int parts[kEach], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        const int e = tid * kEach + j;
+        parts[j] = 0;
+        if (e < a.experts) {
+            const Run r = run_of(offsets, e, a.rows);
+            const int step = part_rows(r.hi - r.lo);
+            parts[j] = (r.hi - r.lo + step - 1) / step;
+        }
+        sum += parts[j];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += u;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int before = incl - sum;
+    for (int w = 0; w < warp; ++w) before += scan[w];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        const int e = tid * kEach + j;
+        if (e < a.experts) first[e] = before;
+        before += parts[j];
+        if (e == a.experts - 1) first[a.experts] = before;
+    }
+    __syncthreads();
+    return first[a.experts];
+}
+
+// EPI: what the epilogue makes of the sums; W_MN: the weights' columns are
+// contiguous in memory (forward), else the contraction is (gradients).
+template <int EPI, bool W_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
+    experts_rows_kernel(const __grid_constant__ ExpertsMaps maps, const __grid_constant__ ExpertsArgs args) {
+    constexpr int S = kRowsStages;
+    constexpr int kCtaCols = EPI == kEpiGated ? 64 : 128;  // columns of D a CTA
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t s_tmem_base;
+    __shared__ volatile int s_abort;
+    __shared__ int s_scan[kRowsThreads / 32];
+
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    const uint32_t turn = sbase + S * kRowsStage;
+    const uint32_t bars = turn + 2 * kTurnBytes;
+    int *const first = reinterpret_cast<int *>(smem_raw + (bars + kRowsBars - raw));
+    int *const offsets = first + kMaxExperts + 4;
+    auto full_bar = [&](int s) { return bars + 8u * s; };  // leader's are used
+    auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
+    auto tfull_bar = [&](int t) { return bars + 8u * (2 * S + t); };
+    auto tempty_bar = [&](int t) { return bars + 8u * (2 * S + 2 + t); };  // leader's
+    const uint32_t drain_bar = bars + 8u * (2 * S + 4);
+
+    const uint32_t rank = ptx::cluster_ctarank();
+    const bool leader = rank == 0u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned pair = blockIdx.x >> 1;
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(full_bar(s), 1);
+            ptx::mbar_init(empty_bar(s), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(tfull_bar(t), 1);
+            ptx::mbar_init(tempty_bar(t), 16);  // each epilogue warp of both CTAs
+        }
+        ptx::mbar_init(drain_bar, 1);
+        ptx::fence_barrier_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(ptx::smem_addr(&s_tmem_base), 512);
+        ptx::tmem_relinquish_pair();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Table table = {first, offsets};
+    const unsigned items = (unsigned)make_table(args, first, offsets, s_scan) * (unsigned)args.tiles_n;
+    ptx::tc_fence_before();
+    ptx::cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
+    ptx::tc_fence_after();
+    if (threadIdx.x == 0 && args.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint32_t tmem_base = s_tmem_base;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA producer (both CTAs) ----------------
+            const uint64_t pol = ptx::policy_evict_normal(), pol_t = ptx::policy_evict_last();
+            uint32_t armed = 0u, armed_par = 0u;
+            bool ok = true;
+            int it = 0;
+            for (unsigned i = pair; ok && i < items; i += (unsigned)args.pairs) {
+                const Tile x = tile_of(args, table, i);
+                const int half = x.n / 2, box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
+                const uint32_t tx = 2u * (args.w_bytes + (16u << box) * 128u);
+                const int c0 = (x.tn * 2 + (int)rank) * kCtaCols, r0 = x.row0 + (int)rank * half;
+                for (int kb = 0; kb < args.kblocks; ++kb, ++it) {
+                    const int s = it % S;
+                    const uint32_t ph = (uint32_t)(it / S) & 1u;
+                    if (!(ok = wait_phase(empty_bar(s), ph ^ 1u, args, &s_abort))) break;
+                    const uint32_t fb = ptx::map_to_rank(full_bar(s), 0u);
+                    if (leader) {
+                        ptx::mbar_arrive_expect_tx(full_bar(s), tx);
+                        armed |= 1u << s;
+                        armed_par = (armed_par & ~(1u << s)) | (ph << s);
+                    }
+                    // test hook: it never arrives
+                    if (args.test_stall && kb == args.kblocks - 1 && leader) continue;
+                    const int seg = kb >= args.kswitch, k0 = (seg ? kb - args.kswitch : kb) * 64;
+                    const uint32_t sw = sbase + s * kRowsStage, st = sw + kWBytes;
+                    if (EPI == kEpiGated) {
+                        ptx::tma_load_3d_pair(sw, &maps.w[0], fb, c0, k0, x.e, pol);
+                        ptx::tma_load_3d_pair(sw + 8192u, &maps.w[1], fb, c0, k0, x.e, pol);
+                    } else if (W_MN) {
+                        ptx::tma_load_3d_pair(sw, &maps.w[0], fb, c0, k0, x.e, pol);
+                        ptx::tma_load_3d_pair(sw + 8192u, &maps.w[0], fb, c0 + 64, k0, x.e, pol);
+                    } else {
+                        ptx::tma_load_3d_pair(sw, &maps.w[seg], fb, k0, c0, x.e, pol);
+                    }
+                    ptx::tma_load_2d_pair(st, &maps.t[seg][box], fb, k0, r0, pol_t);
+                }
+            }
+            // The leader's MMAs release the last stages in both CTAs.
+            for (int j = it > S ? it - S : 0; ok && j < it; ++j)
+                ok = wait_phase(empty_bar(j % S), (uint32_t)(j / S) & 1u, args, &s_abort);
+            // After an abort the leader lets every copy it armed land.
+            if (leader && !ok) {
+                for (int s = 0; s < S; ++s)
+                    if (armed & (1u << s)) wait_drain(full_bar(s), (armed_par >> s) & 1u, args);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            // ---------------- MMA issuer (leader CTA) ----------------
+            const uint32_t fmt = args.fp16 ? 0u : 1u;
+            const uint32_t idesc0 = (1u << 4) | (fmt << 7) | (fmt << 10) | ((W_MN ? 1u : 0u) << 15) | ((256u >> 4) << 24);
+            int it = 0, job = 0, done = 0;
+            bool ok = true;
+            for (unsigned i = pair; ok && i < items; i += (unsigned)args.pairs, ++job) {
+                const Tile x = tile_of(args, table, i);
+                const uint32_t idesc = idesc0 | ((uint32_t)(x.n >> 3) << 17);
+                const int t = job & 1;
+                if (!wait_phase(tempty_bar(t), (((uint32_t)job >> 1) & 1u) ^ 1u, args, &s_abort)) break;
+                ptx::tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (uint32_t)(t * 256);
+                for (int kb = 0; kb < args.kblocks; ++kb, ++it) {
+                    const int s = it % S;
+                    if (!(ok = wait_phase(full_bar(s), (uint32_t)(it / S) & 1u, args, &s_abort))) break;
+                    ptx::tc_fence_after();
+                    const uint32_t sw = sbase + s * kRowsStage, st = sw + kWBytes;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        ptx::mma_bf16_pair(d_tmem, operand_desc<W_MN>(sw, kk), operand_desc<false>(st, kk), idesc,
+                                           (kb > 0 || kk > 0) ? 1u : 0u);
+                    ptx::mma_commit_pair(empty_bar(s), 0x3);  // frees stage s in both CTAs
+                }
+                if (ok) ptx::mma_commit_pair(tfull_bar(t), 0x3), ++done;
+            }
+            ptx::mma_commit_pair(drain_bar, 0x3);  // every MMA retired before TMEM is freed
+            wait_drain(drain_bar, 0u, args);
+            // the peer's arrivals for the last tiles have landed
+            for (int t = 0; t < 2; ++t) {
+                const int tiles = (done + 1 - t) / 2;
+                if (tiles > 0) wait_drain(tempty_bar(t), (uint32_t)(tiles - 1) & 1u, args);
+            }
+        }
+    } else {
+        // ---------------- epilogue (both CTAs) ----------------
+        // Columns of D are the TMEM lanes.  Four warps, a group, hold the CTA's 128
+        // of them and turn 32 rows around in shared memory, so that neighbouring
+        // threads have neighbouring columns; the two groups take every other 32 rows.
+        const int lq = warp & 3, group = (warp - 2) >> 2;
+        const int tid = lq * 32 + lane;  // in the group
+        const uint32_t lanes = tmem_base + ((uint32_t)(32 * lq) << 16);
+        const uint32_t buf = turn + (uint32_t)group * kTurnBytes;
+        constexpr int kGroups = kCtaCols / 4, kStep = 128 / kGroups, kR = kTurnRows / kStep;
+        constexpr int kBatch = 4;
+        static_assert(kR % kBatch == 0, "whole batches");
+        const int tr = tid / kGroups, tc = tid % kGroups * 4;
+        int job = 0;
+        Epilogue p = args.e;
+        for (unsigned i = pair; i < items; i += (unsigned)args.pairs, ++job) {
+            const Tile x = tile_of(args, table, i);
+            const int t = job & 1;
+            p.M = x.end;
+            const int c = (x.tn * 2 + (int)rank) * kCtaCols + tc;
+            // one warp of a group polls, the others sleep at the barrier
+            const bool ok = lq != 2 || wait_phase(tfull_bar(t), ((uint32_t)job >> 1) & 1u, args, &s_abort);
+            if (!ptx::named_bar_and(1 + group, 128, ok)) break;
+            ptx::tc_fence_after();
+            const uint32_t acc = lanes + (uint32_t)(t * 256);
+            for (int b = group * kTurnRows; b < x.n; b += 2 * kTurnRows) {
+                uint32_t v[kTurnRows];
+                ptx::tmem_ld_x16(acc + (uint32_t)b, reinterpret_cast<uint32_t(&)[16]>(v[0]));
+                ptx::tmem_ld_x16(acc + (uint32_t)b + 16u, reinterpret_cast<uint32_t(&)[16]>(v[16]));
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < kTurnRows; ++j)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(buf + (uint32_t)(j * 128 + tid) * 4u), "r"(v[j])
+                                 : "memory");
+                ptx::named_bar_sync(1 + group, 128);
+#pragma unroll
+                for (int q = 0; q < kR; q += kBatch) {
+                    const int r = x.row0 + b + tr + q * kStep;
+                    if (r >= p.M) break;
+                    GroupIn<EPI, kBatch> in;
+                    group_load<EPI, kBatch>(p, r, c, kStep, in);
+                    float d[4 * kBatch], u[EPI == kEpiGated ? 4 * kBatch : 1];
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j) {
+                        const uint32_t at = buf + (uint32_t)((tr + (q + j) * kStep) * 128 + tc) * 4u;
+                        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                     : "=f"(d[4 * j]), "=f"(d[4 * j + 1]), "=f"(d[4 * j + 2]), "=f"(d[4 * j + 3])
+                                     : "r"(at)
+                                     : "memory");
+                        if constexpr (EPI == kEpiGated)
+                            asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                         : "=f"(u[4 * j]), "=f"(u[4 * j + 1]), "=f"(u[4 * j + 2]), "=f"(u[4 * j + 3])
+                                         : "r"(at + 256u)
+                                         : "memory");
+                    }
+                    group_epilogue<EPI, kBatch>(p, r, c, kStep, d, u, in);
+                }
+                ptx::named_bar_sync(1 + group, 128);  // the rows have left shared memory
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {  // everything has left TMEM
+                if (leader)
+                    ptx::mbar_arrive(tempty_bar(t));
+                else
+                    ptx::mbar_arrive_remote_relaxed(ptx::map_to_rank(tempty_bar(t), 0u));
+            }
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        // the leader's MMAs write this CTA's TMEM: the peer waits for them too
+        if (lane == 0 && !leader) wait_drain(drain_bar, 0u, args);
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem_base, 512);
+    }
+    ptx::cluster_sync_relaxed();  // neither CTA leaves while the other may reach its shared memory
+}
+
+// ---- weights' gradients -----------------------------------------------------------
+
+constexpr int kGradThreads = 96 + 512;  // producer, MMA issuer, zeros; 16 epilogue warps
+constexpr int kGradStages = 5;
+constexpr uint32_t kGradStage = 4 * 8192;  // a CTA's 128 rows of A and 128 columns of B of 64 rows of the batch
+constexpr uint32_t kGradTurn = 32 * 64 * 2;  // a warp's 32 rows of 64 columns, 16 bits each
+constexpr uint32_t kGradSmem = 1024 + kGradStages * kGradStage + 16 * kGradTurn + 256;
+static_assert(kGradSmem <= kSmemLimit, "shared memory");
+
+struct GradTile {
+    int e, p, tm, tn, lo, hi;
+};
+__device__ __forceinline__ GradTile grad_tile(const GradArgs &a, unsigned i) {
+    GradTile x;
+    x.e = (int)(i / (unsigned)a.per_expert);
+    int r = (int)(i - (unsigned)x.e * (unsigned)a.per_expert);
+    x.p = 0;
+    while (x.p + 1 < a.nprob && r >= a.p[x.p + 1].base) ++x.p;
+    r -= a.p[x.p].base;
+    x.tm = r / a.p[x.p].tiles_n;
+    x.tn = r - x.tm * a.p[x.p].tiles_n;
+    const Run run = run_of(a.offsets, x.e, a.rows);
+    x.lo = run.lo, x.hi = run.hi;
+    return x;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
+    experts_grad_kernel(const __grid_constant__ GradMaps maps, const __grid_constant__ GradArgs args) {
+    constexpr int S = kGradStages;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t s_tmem_base;
+    __shared__ volatile int s_abort;
+
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    const uint32_t turn = sbase + S * kGradStage;
+    const uint32_t bars = turn + 16 * kGradTurn;
+    auto full_bar = [&](int s) { return bars + 8u * s; };  // leader's are used
+    auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
+    auto tfull_bar = [&](int t) { return bars + 8u * (2 * S + t); };
+    auto tempty_bar = [&](int t) { return bars + 8u * (2 * S + 2 + t); };  // leader's
+    const uint32_t drain_bar = bars + 8u * (2 * S + 4);
+    // a run's last rows have landed in this CTA; one for each stage, since several
+    // short runs' are on their way at once
+    auto tail_bar = [&](int s) { return bars + 8u * (2 * S + 5 + s); };
+
+    const uint32_t rank = ptx::cluster_ctarank();
+    const bool leader = rank == 0u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned pair = blockIdx.x >> 1;
+    const unsigned items = (unsigned)args.experts * (unsigned)args.per_expert;
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(full_bar(s), 2);  // one arrival of each CTA
+            ptx::mbar_init(empty_bar(s), 1);
+            ptx::mbar_init(tail_bar(s), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(tfull_bar(t), 1);
+            ptx::mbar_init(tempty_bar(t), 32);  // each epilogue warp of both CTAs
+        }
+        ptx::mbar_init(drain_bar, 1);
+        ptx::fence_barrier_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(ptx::smem_addr(&s_tmem_base), 512);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = s_tmem_base;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA producer (both CTAs) ----------------
+            const uint64_t pol = ptx::policy_evict_last();
+            uint32_t armed = 0u, armed_par = 0u;  // copies counted on this CTA's full barriers
+            uint32_t tails = 0u, tail_par = 0u;   // and on its tail barriers: the next phase's parity
+            bool ok = true;
+            int it = 0;
+            for (unsigned i = pair; ok && i < items; i += (unsigned)args.pairs) {
+                const GradTile x = grad_tile(args, i);
+                const int m0 = x.tm * 256 + (int)rank * 128, n0 = x.tn * 256 + (int)rank * 128;
+                for (int r = x.lo; r < x.hi; r += 64, ++it) {
+                    const int s = it % S;
+                    const uint32_t ph = (uint32_t)(it / S) & 1u;
+                    if (!(ok = wait_phase(empty_bar(s), ph ^ 1u, args, &s_abort))) break;
+                    const bool tail = r + 64 > x.hi;
+                    const bool stall = args.test_stall && r + 64 >= x.hi && leader;  // test hook: it never arrives
+                    const uint32_t sa = sbase + s * kGradStage, sb = sa + 16384u;
+                    const CUtensorMap *ma = &maps.a[x.p], *mb = &maps.b[x.p];
+                    if (tail) {
+                        // counted here: the zeros' warp goes on from there
+                        const uint32_t tb = tail_bar(s);
+                        ptx::mbar_arrive_expect_tx(tb, kGradStage);
+                        tails |= 1u << s, armed &= ~(1u << s);
+                        tail_par ^= 1u << s;
+                        if (stall) continue;
+                        ptx::tma_load_2d(sa, ma, tb, m0, r, pol);
+                        ptx::tma_load_2d(sa + 8192u, ma, tb, m0 + 64, r, pol);
+                        ptx::tma_load_2d(sb, mb, tb, n0, r, pol);
+                        ptx::tma_load_2d(sb + 8192u, mb, tb, n0 + 64, r, pol);
+                        continue;
+                    }
+                    const uint32_t fb = ptx::map_to_rank(full_bar(s), 0u);
+                    tails &= ~(1u << s);
+                    if (leader) {
+                        ptx::mbar_arrive_expect_tx(full_bar(s), 2 * kGradStage);
+                        armed |= 1u << s;
+                        armed_par = (armed_par & ~(1u << s)) | (ph << s);
+                    } else {
+                        ptx::mbar_arrive_remote_relaxed(fb);
+                    }
+                    if (stall) continue;
+                    ptx::tma_load_2d_pair(sa, ma, fb, m0, r, pol);
+                    ptx::tma_load_2d_pair(sa + 8192u, ma, fb, m0 + 64, r, pol);
+                    ptx::tma_load_2d_pair(sb, mb, fb, n0, r, pol);
+                    ptx::tma_load_2d_pair(sb + 8192u, mb, fb, n0 + 64, r, pol);
+                }
+            }
+            for (int j = it > S ? it - S : 0; ok && j < it; ++j)
+                ok = wait_phase(empty_bar(j % S), (uint32_t)(j / S) & 1u, args, &s_abort);
+            // After an abort every copy that was issued lands first.
+            if (!ok) {
+                for (int s = 0; s < S; ++s) {
+                    if (armed & (1u << s)) wait_drain(full_bar(s), (armed_par >> s) & 1u, args);
+                    if (tails & (1u << s)) wait_drain(tail_bar(s), ((tail_par >> s) & 1u) ^ 1u, args);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            // ---------------- MMA issuer (leader CTA) ----------------
+            const uint32_t fmt = args.fp16 ? 0u : 1u;
+            const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 15) | (1u << 16) |
+                                   ((256u >> 3) << 17) | ((256u >> 4) << 24);
+            int it = 0, job = 0, done = 0;
+            bool ok = true;
+            for (unsigned i = pair; ok && i < items; i += (unsigned)args.pairs) {
+                const GradTile x = grad_tile(args, i);
+                if (x.lo >= x.hi) continue;  // zeros: the epilogue's alone
+                const int t = job & 1;
+                if (!wait_phase(tempty_bar(t), (((uint32_t)job >> 1) & 1u) ^ 1u, args, &s_abort)) break;
+                ptx::tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (uint32_t)(t * 256);
+                for (int r = x.lo; r < x.hi; r += 64, ++it) {
+                    const int s = it % S;
+                    if (!(ok = wait_phase(full_bar(s), (uint32_t)(it / S) & 1u, args, &s_abort))) break;
+                    ptx::tc_fence_after();
+                    const uint32_t sa = sbase + s * kGradStage, sb = sa + 16384u;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        ptx::mma_bf16_pair(d_tmem, operand_desc<true>(sa, kk), operand_desc<true>(sb, kk), idesc,
+                                           (r > x.lo || kk > 0) ? 1u : 0u);
+                    ptx::mma_commit_pair(empty_bar(s), 0x3);
+                }
+                if (ok) ptx::mma_commit_pair(tfull_bar(t), 0x3), ++done;
+                ++job;
+            }
+            ptx::mma_commit_pair(drain_bar, 0x3);
+            wait_drain(drain_bar, 0u, args);
+            for (int t = 0; t < 2; ++t) {
+                const int tiles = (done + 1 - t) / 2;
+                if (tiles > 0) wait_drain(tempty_bar(t), (uint32_t)(tiles - 1) & 1u, args);
+            }
+        }
+    } else if (warp == 2) {
+        // ---------------- zeros behind a run's last row (both CTAs) ----------------
+        int it = 0;
+        uint32_t tail_par = 0u;
+        bool ok = true;
+        for (unsigned i = pair; ok && i < items; i += (unsigned)args.pairs) {
+            const GradTile x = grad_tile(args, i);
+            const int blocks = (x.hi - x.lo + 63) / 64, left = (x.hi - x.lo) & 63;
+            it += blocks;
+            if (left == 0) continue;
+            const int s = (it - 1) % S;
+            ok = __all_sync(0xFFFFFFFFu, wait_phase(tail_bar(s), (tail_par >> s) & 1u, args, &s_abort));
+            tail_par ^= 1u << s;
+            if (!ok) break;
+            // row r of the batch is 128 bytes of each of the four boxes
+            const uint32_t at = sbase + s * kGradStage + (uint32_t)left * 128u;
+            const int pieces = (64 - left) * 8;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                for (int j = lane; j < pieces; j += 32)
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at + 8192u * b + 16u * j), "r"(0)
+                                 : "memory");
+            asm volatile("fence.proxy.async;" ::: "memory");  // before the tensor cores' reads
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_remote(ptx::map_to_rank(full_bar(s), 0u));
+        }
+    } else {
+        // ---------------- epilogue (both CTAs) ----------------
+        const int lq = warp & 3;              // TMEM lanes 32 lq .. + 31 = rows of D
+        const int cs = (warp - 3) >> 2;       // which 64 of the tile's columns
+        const uint32_t lanes = tmem_base + ((uint32_t)(32 * lq) << 16);
+        const uint32_t mine = turn + (uint32_t)(warp - 3) * kGradTurn;
+        // 16 bytes (unit x) of a row sit at unit x ^ (row & 7)
+        auto slot = [&](int row, int x) { return mine + (uint32_t)(row * 128 + ((x ^ (row & 7)) << 4)); };
+        const int px = lane & 7, pr = lane >> 3;
+        int job = 0;
+        for (unsigned i = pair; i < items; i += (unsigned)args.pairs) {
+            const GradTile x = grad_tile(args, i);
+            const auto &p = args.p[x.p];
+            const int r0 = x.tm * 256 + (int)rank * 128 + 32 * lq, c = x.tn * 256 + cs * 64 + 8 * px;
+            uint16_t *q = static_cast<uint16_t *>(p.out) + x.e * p.es + (long long)(r0 + pr) * p.ld + c;
+            const int M = p.M, N = p.N;
+            const long long ld = p.ld;
+            if (x.lo >= x.hi) {
+                for (int j = 0; j < 32; j += 4, q += 4 * ld)
+                    if (r0 + pr + j < M && c < N) *reinterpret_cast<uint4 *>(q) = make_uint4(0u, 0u, 0u, 0u);
+                continue;
+            }
+            const int t = job & 1;
+            // one warp polls, the others sleep at the barrier
+            const bool ok = warp != 3 || wait_phase(tfull_bar(t), ((uint32_t)job >> 1) & 1u, args, &s_abort);
+            if (!ptx::named_bar_and(1, 512, ok)) break;
+            ++job;
+            ptx::tc_fence_after();
+            const uint32_t acc = lanes + (uint32_t)(t * 256 + cs * 64);
+            __syncwarp();  // the last tile's rows have left shared memory
+#pragma unroll
+            for (int g = 0; g < 64; g += 32) {
+                uint32_t v[32];
+                ptx::tmem_ld_x16(acc + (uint32_t)g, reinterpret_cast<uint32_t(&)[16]>(v[0]));
+                ptx::tmem_ld_x16(acc + (uint32_t)g + 16u, reinterpret_cast<uint32_t(&)[16]>(v[16]));
+                ptx::tmem_ld_wait();
+                float f[32];
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]);
+                pack_values<32>(args.fp16 != 0, f, w);
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(slot(lane, g / 8 + h)), "r"(w[4 * h]),
+                                 "r"(w[4 * h + 1]), "r"(w[4 * h + 2]), "r"(w[4 * h + 3])
+                                 : "memory");
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader)
+                    ptx::mbar_arrive(tempty_bar(t));
+                else
+                    ptx::mbar_arrive_remote_relaxed(ptx::map_to_rank(tempty_bar(t), 0u));
+            }
+#pragma unroll
+            for (int j = 0; j < 32; j += 4, q += 4 * ld) {
+                uint4 w;
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                             : "r"(slot(pr + j, px))
+                             : "memory");
+                if (r0 + pr + j < M && c < N) *reinterpret_cast<uint4 *>(q) = w;
+            }
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        if (lane == 0 && !leader) wait_drain(drain_bar, 0u, args);
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem_base, 512);
+    }
+    ptx::cluster_sync_relaxed();
+}
+
+const void *kernel_of(int epi, bool n_contiguous) {
+    if (epi == kEpiGated && n_contiguous) return reinterpret_cast<const void *>(experts_rows_kernel<kEpiGated, true>);
+    if (epi == kEpiLinear && n_contiguous) return reinterpret_cast<const void *>(experts_rows_kernel<kEpiLinear, true>);
+    if (epi == kEpiLinear) return reinterpret_cast<const void *>(experts_rows_kernel<kEpiLinear, false>);
+    if (epi == kEpiDGate && !n_contiguous) return reinterpret_cast<const void *>(experts_rows_kernel<kEpiDGate, false>);
+    return nullptr;
+}
+
+cudaError_t launch(const void *k, unsigned grid, unsigned block, size_t smem, void **params, cudaStream_t stream) {
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute attr[1];
+    c.gridDim = dim3(grid);
+    c.blockDim = dim3(block);
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = attr;
+    c.numAttrs = 1;
+    return cudaLaunchKernelExC(&c, k, params);
+}
+
+}  // namespace
+
+cudaError_t experts_configure() {
+    for (int epi : {kEpiGated, kEpiLinear, kEpiDGate})
+        for (bool n : {true, false})
+            if (const void *k = kernel_of(epi, n)) {
+                const cudaError_t e =
+                    cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRowsSmem);
+                if (e != cudaSuccess) return e;
+            }
+    return cudaFuncSetAttribute(experts_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGradSmem);
+}
+
+int experts_smem_bytes() { return (int)(kRowsSmem > kGradSmem ? kRowsSmem : kGradSmem); }
+
+cudaError_t experts_launch(int epi, bool n_contiguous, const ExpertsMaps &maps, const ExpertsArgs &args,
+                           cudaStream_t stream) {
+    const void *k = kernel_of(epi, n_contiguous);
+    if (k == nullptr || args.pairs < 1) return cudaErrorInvalidConfiguration;
+    void *params[] = {const_cast<ExpertsMaps *>(&maps), const_cast<ExpertsArgs *>(&args)};
+    return launch(k, 2u * (unsigned)args.pairs, kRowsThreads, kRowsSmem, params, stream);
+}
+
+cudaError_t experts_grad_launch(const GradMaps &maps, const GradArgs &args, cudaStream_t stream) {
+    if (args.pairs < 1 || args.per_expert < 1) return cudaErrorInvalidConfiguration;
+    void *params[] = {const_cast<GradMaps *>(&maps), const_cast<GradArgs *>(&args)};
+    return launch(reinterpret_cast<const void *>(experts_grad_kernel), 2u * (unsigned)args.pairs, kGradThreads,
+                  kGradSmem, params, stream);
+}
+
+}  // namespace route

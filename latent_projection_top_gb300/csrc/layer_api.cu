@@ -5,136 +5,18 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <cstddef>
-#include <cstring>
-#include <initializer_list>
-#include <mutex>
-#include <new>
 
-#include "api_util.h"
-#include "layer.cuh"
+#include "experts.cuh"
 #include "layer_math.cuh"
-#include "route_layer.h"
+#include "layer_plan.h"
 
 using namespace route;
 
 namespace {
 
-enum LayerKind { kNorm, kLinear, kGated };
-
-// How a launch covers its products: CTA-pair tiles of 256 x bn
-// (layer_gemm.cu), or 128-column tiles of bn rows (layer_small.cu), and the
-// splits of the contraction.
-struct Choice {
-    bool small;
-    int bn;
-    int splits[kGemmMaxProblems];  // of each product (small tiles: the same for all)
-    double us;                     // the estimate that it was chosen by
-};
-
-// What the last call of a kind chose, for its number of rows.
-enum ChoiceSlot { kSlotForward, kSlotDown, kSlotDGate, kSlotBackward, kSlotInput, kSlotWeights, kSlots };
-struct ChoiceMemo {
-    int rows;
-    Choice c;
-};
-
-}  // namespace
-
-struct route_layer {
-    LayerKind kind;
-    int rows, k, f, n;
-    int type, out_type, act, train;
-    int device, sms, pairs;
-    int test_stall;
-    unsigned long long timeout_ns;
-    unsigned *words;   // device status word
-    uint8_t *scratch;
-    size_t scratch_bytes;
-    // offsets into scratch (0 size where the plan needs none)
-    size_t o_part;     // split partials (norm: column-sum partials)
-    size_t o_sum;      // the bias gradient's partials
-    size_t o_x, o_w[3], o_dout, o_h, o_dg, o_du;
-    // Held for the whole of a call: its kernels share the scratch, and follow one
-    // another in the stream without another call's between them.
-    mutable std::mutex calls;
-    mutable ChoiceMemo memo[kSlots];
-};
-
-namespace {
-
-constexpr unsigned long long kTimeoutNs = 2000000000ull;
 // A launch's split products have at most two items a CTA pair: FP32 partials
 // of a 256 x 256 tile each.
 constexpr size_t kTilePartBytes = 256 * 256 * 4;
-
-route_status cuda_fail(cudaError_t e, const char *what) {
-    return api_fail(ROUTE_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
-}
-
-struct DeviceGuard {
-    int prev = -1;
-    bool changed = false;
-    cudaError_t err;
-    explicit DeviceGuard(int dev) {
-        err = cudaGetDevice(&prev);
-        if (err == cudaSuccess && prev != dev) {
-            err = cudaSetDevice(dev);
-            changed = err == cudaSuccess;
-        }
-    }
-    ~DeviceGuard() {
-        if (changed) cudaSetDevice(prev);
-    }
-};
-
-long long up8(long long v) { return (v + 7) & ~7ll; }
-long long up16(long long v) { return (v + 15) & ~15ll; }
-bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// ---- argument checks ----------------------------------------------------------
-
-// A matrix argument: its name, width and whether a product reads it by TMA.
-struct Mat {
-    const char *name;
-    const void *p;
-    int64_t ld;
-    int rows, cols, esize;
-    bool operand;
-};
-
-route_status check_mat(const Mat &m) {
-    if (!m.p) return api_fail(ROUTE_ERR_NULL, "%s must be non-NULL", m.name);
-    if (!aligned(m.p, (unsigned)m.esize))
-        return api_fail(ROUTE_ERR_ALIGN, "%s is not aligned to its element", m.name);
-    if (m.rows > 1 && m.ld < m.cols)
-        return api_fail(ROUTE_ERR_PLAN, "%s: row stride %lld is less than its %d columns", m.name,
-                        (long long)m.ld, m.cols);
-    if (m.operand && m.cols % 8 == 0 && (!aligned(m.p, 16) || (m.rows > 1 && m.ld % 8 != 0)))
-        return api_fail(ROUTE_ERR_ALIGN,
-                        "%s must start on 16 bytes with a row stride that is a multiple of 8", m.name);
-    return ROUTE_OK;
-}
-
-route_status check_mats(std::initializer_list<Mat> ms) {
-    for (const Mat &m : ms)
-        if (const route_status st = check_mat(m)) return st;
-    return ROUTE_OK;
-}
-
-route_status check_vec(const char *name, const void *p, int esize) {
-    if (p && !aligned(p, (unsigned)esize))
-        return api_fail(ROUTE_ERR_ALIGN, "%s is not aligned to its element", name);
-    return ROUTE_OK;
-}
-
-route_status check_plan(const route_layer *p, LayerKind kind, int rows) {
-    if (!p) return api_fail(ROUTE_ERR_NULL, "plan is NULL");
-    if (p->kind != kind) return api_fail(ROUTE_ERR_PLAN, "the plan is another operator's");
-    if (rows < 0 || rows > p->rows)
-        return api_fail(ROUTE_ERR_ROWS, "rows %d outside the plan's 0-%d", rows, p->rows);
-    return ROUTE_OK;
-}
 
 int vec_bits(const void *out, long long ld_out, const void *out2, const void *res, long long ld_res,
              int out_type, const void *bias) {
@@ -527,9 +409,13 @@ route_status zero_matrix(void *p, int64_t ld, int rows, int cols, int esize, cud
     return e == cudaSuccess ? ROUTE_OK : cuda_fail(e, "cudaMemset2DAsync");
 }
 
+}  // namespace
+
+namespace route {
+
 // ---- plans ------------------------------------------------------------------------
 
-route_status finish_prepare(route_layer *p, int device, route_layer **out) {
+route_status layer_finish_prepare(route_layer *p, int device, route_layer **out) {
     DeviceGuard guard(device);
     if (guard.err != cudaSuccess) {
         delete p;
@@ -538,20 +424,26 @@ route_status finish_prepare(route_layer *p, int device, route_layer **out) {
     cudaDeviceProp prop;
     cudaError_t e = cudaGetDeviceProperties(&prop, device);
     route_status st = ROUTE_OK;
+    const bool products = p->kind == kLinear || p->kind == kGated;
     if (e != cudaSuccess) {
         st = cuda_fail(e, "cudaGetDeviceProperties");
     } else if (prop.major != 10 || prop.minor != 3) {
         st = api_fail(ROUTE_ERR_DEVICE, "device %d is sm_%d%d; this library is built for sm_103a only",
                       device, prop.major, prop.minor);
-    } else if (p->kind != kNorm && ((size_t)gemm_smem_bytes() > prop.sharedMemPerBlockOptin ||
-                                    (size_t)small_smem_bytes() > prop.sharedMemPerBlockOptin ||
-                                    prop.multiProcessorCount < 2)) {
+    } else if (products && ((size_t)gemm_smem_bytes() > prop.sharedMemPerBlockOptin ||
+                            (size_t)small_smem_bytes() > prop.sharedMemPerBlockOptin ||
+                            prop.multiProcessorCount < 2)) {
         st = api_fail(ROUTE_ERR_DEVICE, "the product kernels need %d B of shared memory per block",
                       gemm_smem_bytes());
-    } else if (p->kind == kNorm && (e = norm_configure()) != cudaSuccess) {
-        st = cuda_fail(e, "cudaFuncSetAttribute");
-    } else if (p->kind != kNorm && ((e = gemm_configure()) != cudaSuccess ||
-                                    (e = small_configure()) != cudaSuccess)) {
+    } else if (p->kind == kExpertBlocks && ((size_t)experts_smem_bytes() > prop.sharedMemPerBlockOptin ||
+                                            prop.multiProcessorCount < 2)) {
+        st = api_fail(ROUTE_ERR_DEVICE, "the experts' kernels need %d B of shared memory per block",
+                      experts_smem_bytes());
+    } else if ((e = p->kind == kNorm           ? norm_configure()
+                    : p->kind == kDispatch     ? sort_configure()
+                    : p->kind == kExpertBlocks ? experts_configure()
+                                               : cudaSuccess) != cudaSuccess ||
+               (products && ((e = gemm_configure()) != cudaSuccess || (e = small_configure()) != cudaSuccess))) {
         st = cuda_fail(e, "cudaFuncSetAttribute");
     }
     if (st != ROUTE_OK) {
@@ -573,7 +465,13 @@ route_status finish_prepare(route_layer *p, int device, route_layer **out) {
     auto copy = [&](size_t rows, int cols) { return area(cols % 8 ? rows * up8(cols) * 2 : 0); };
     if (p->kind == kNorm) {
         p->o_part = area(norm_part_floats(p->k, p->sms) * 4);
-    } else {
+    } else if (p->kind == kExpertBlocks) {
+        p->o_h = area(R * up16(p->f) * 2);
+        if (p->train) {
+            p->o_dg = area(R * up16(p->f) * 2);
+            p->o_du = area(R * up16(p->f) * 2);
+        }
+    } else if (products) {
         p->o_part = area(2 * (size_t)p->pairs * kTilePartBytes);
         p->o_x = copy(R, p->k);
         if (p->kind == kLinear) {
@@ -604,12 +502,12 @@ route_status finish_prepare(route_layer *p, int device, route_layer **out) {
     return ROUTE_OK;
 }
 
-route_status check_prepare(int rows, std::initializer_list<int> widths, int max_width, int type,
-                           bool fp32, int act, route_layer **out) {
+route_status layer_check_prepare(int rows, int max_rows, std::initializer_list<int> widths, int max_width,
+                                 int type, bool fp32, int act, route_layer **out) {
     if (!out) return api_fail(ROUTE_ERR_NULL, "out must be non-NULL");
     *out = nullptr;
-    if (rows < 1 || rows > ROUTE_LAYER_MAX_ROWS)
-        return api_fail(ROUTE_ERR_ROWS, "rows %d outside 1-%d", rows, ROUTE_LAYER_MAX_ROWS);
+    if (rows < 1 || rows > max_rows)
+        return api_fail(ROUTE_ERR_ROWS, "rows %d outside 1-%d", rows, max_rows);
     for (int w : widths)
         if (w < 1 || w > max_width)
             return api_fail(ROUTE_ERR_PLAN, "width %d outside 1-%d", w, max_width);
@@ -619,7 +517,7 @@ route_status check_prepare(int rows, std::initializer_list<int> widths, int max_
     return ROUTE_OK;
 }
 
-route_layer *new_plan(LayerKind kind, int rows, int type, int act, int train) {
+route_layer *layer_new_plan(LayerKind kind, int rows, int type, int act, int train) {
     route_layer *p = new (std::nothrow) route_layer();  // all zero
     if (!p) return nullptr;
     p->kind = kind;
@@ -630,45 +528,42 @@ route_layer *new_plan(LayerKind kind, int rows, int type, int act, int train) {
     return p;
 }
 
-// Offsets of the parts of `saved`.
-size_t saved_h(const route_layer *p, int rows) { return (size_t)rows * 2 * up16(p->f) * 4; }
-
-}  // namespace
+}  // namespace route
 
 extern "C" {
 
 route_status route_norm_prepare(int rows, int dim, int type, int device, route_layer **out) {
-    route_status st = check_prepare(rows, {dim}, ROUTE_NORM_MAX_WIDTH, type, true, 0, out);
+    route_status st = layer_check_prepare(rows, ROUTE_LAYER_MAX_ROWS, {dim}, ROUTE_NORM_MAX_WIDTH, type, true, 0, out);
     if (st != ROUTE_OK) return st;
-    route_layer *p = new_plan(kNorm, rows, type, 0, 0);
+    route_layer *p = layer_new_plan(kNorm, rows, type, 0, 0);
     if (!p) return api_fail(ROUTE_ERR_CUDA, "out of host memory");
     p->k = dim;
-    return finish_prepare(p, device, out);
+    return layer_finish_prepare(p, device, out);
 }
 
 route_status route_linear_prepare(int rows, int k, int n, int type, int out_type, int act,
                                   int train, int device, route_layer **out) {
-    route_status st = check_prepare(rows, {k, n}, ROUTE_LAYER_MAX_WIDTH, type, false, act, out);
+    route_status st = layer_check_prepare(rows, ROUTE_LAYER_MAX_ROWS, {k, n}, ROUTE_LAYER_MAX_WIDTH, type, false, act, out);
     if (st != ROUTE_OK) return st;
     if (out_type != type && out_type != kFp32)
         return api_fail(ROUTE_ERR_MODE, "out_type %d is neither the plan's type nor FP32", out_type);
     if (train && out_type != type)
         return api_fail(ROUTE_ERR_PLAN, "a training plan's results have the plan's type");
-    route_layer *p = new_plan(kLinear, rows, type, act, train);
+    route_layer *p = layer_new_plan(kLinear, rows, type, act, train);
     if (!p) return api_fail(ROUTE_ERR_CUDA, "out of host memory");
     p->k = k, p->n = n;
     p->out_type = out_type;
-    return finish_prepare(p, device, out);
+    return layer_finish_prepare(p, device, out);
 }
 
 route_status route_gated_prepare(int rows, int k, int f, int n, int type, int act, int train,
                                  int device, route_layer **out) {
-    route_status st = check_prepare(rows, {k, f, n}, ROUTE_LAYER_MAX_WIDTH, type, false, act, out);
+    route_status st = layer_check_prepare(rows, ROUTE_LAYER_MAX_ROWS, {k, f, n}, ROUTE_LAYER_MAX_WIDTH, type, false, act, out);
     if (st != ROUTE_OK) return st;
-    route_layer *p = new_plan(kGated, rows, type, act, train);
+    route_layer *p = layer_new_plan(kGated, rows, type, act, train);
     if (!p) return api_fail(ROUTE_ERR_CUDA, "out of host memory");
     p->k = k, p->f = f, p->n = n;
-    return finish_prepare(p, device, out);
+    return layer_finish_prepare(p, device, out);
 }
 
 route_status route_layer_destroy(route_layer *p) {
@@ -699,7 +594,8 @@ int64_t route_layer_saved_bytes(const route_layer *p, int rows) {
     if (!p) return -1;
     if (rows <= 0 || !p->train) return 0;
     if (p->kind == kLinear) return p->act == kActNone ? 0 : (int64_t)rows * up16(p->n) * 4;
-    if (p->kind == kGated) return (int64_t)saved_h(p, rows) + (int64_t)rows * up16(p->f) * 2;
+    if (p->kind == kGated || p->kind == kExpertBlocks)
+        return (int64_t)saved_h(p, rows) + (int64_t)rows * up16(p->f) * 2;
     return 0;
 }
 

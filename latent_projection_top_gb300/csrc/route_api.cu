@@ -1287,18 +1287,14 @@ route_status api_fail(route_status st, const char *fmt, ...) {
     return st;
 }
 
-route_status api_encode_operand(CUtensorMap *m, const void *ptr, bool fp16, uint64_t inner,
-                                uint64_t outer, uint64_t ld, uint32_t box_inner,
-                                uint32_t box_outer, const char *what) {
+static route_status encode_operand(CUtensorMap *m, const void *ptr, bool fp16, int rank, const cuuint64_t *dims,
+                                   const cuuint64_t *strides, const cuuint32_t *box, const char *what) {
     EncodeTiledFn enc = nullptr;
     route_status st = get_encode(&enc);
     if (st != ROUTE_OK) return st;
-    cuuint64_t dims[2] = {inner, outer};
-    cuuint64_t strides[1] = {ld * 2};
-    cuuint32_t box[2] = {box_inner, box_outer};
-    cuuint32_t estr[2] = {1, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
     auto encode = [&] {
-        return enc(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+        return enc(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
                    const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1312,6 +1308,24 @@ route_status api_encode_operand(CUtensorMap *m, const void *ptr, bool fp16, uint
     if (r != CUDA_SUCCESS)
         return api_fail(ROUTE_ERR_CUDA, "tensor map for %s rejected (CUresult %d)", what, (int)r);
     return ROUTE_OK;
+}
+
+route_status api_encode_operand(CUtensorMap *m, const void *ptr, bool fp16, uint64_t inner,
+                                uint64_t outer, uint64_t ld, uint32_t box_inner,
+                                uint32_t box_outer, const char *what) {
+    cuuint64_t dims[2] = {inner, outer};
+    cuuint64_t strides[1] = {ld * 2};
+    cuuint32_t box[2] = {box_inner, box_outer};
+    return encode_operand(m, ptr, fp16, 2, dims, strides, box, what);
+}
+
+route_status api_encode_operands(CUtensorMap *m, const void *ptr, bool fp16, uint64_t inner, uint64_t outer,
+                                 uint64_t count, uint64_t ld, uint64_t step, uint32_t box_inner,
+                                 uint32_t box_outer, const char *what) {
+    cuuint64_t dims[3] = {inner, outer, count};
+    cuuint64_t strides[2] = {ld * 2, step * 2};
+    cuuint32_t box[3] = {box_inner, box_outer, 1};
+    return encode_operand(m, ptr, fp16, 3, dims, strides, box, what);
 }
 
 }  // namespace route
