@@ -72,6 +72,7 @@ struct ExpertsArgs {
 constexpr int kMaxGrads = 3;
 struct GradMaps {
     CUtensorMap a[kMaxGrads], b[kMaxGrads];
+    CUtensorMap d[kMaxGrads];   // the results [experts][M][N], in boxes of 32 rows x 64 columns
 };
 struct GradArgs {
     const int *offsets;
@@ -85,8 +86,6 @@ struct GradArgs {
     unsigned *status;
     struct {
         int M, N, tiles_m, tiles_n, base;
-        void *out;              // [experts][M][N]
-        long long ld, es;       // strides of rows and of experts
     } p[kMaxGrads];
 };
 

@@ -395,8 +395,10 @@ route_status route_experts_backward(const route_layer *p, int rows, const void *
         q.tiles_m = ceil_div(q.M, 256), q.tiles_n = ceil_div(q.N, 256);
         q.base = a.per_expert;
         a.per_expert += q.tiles_m * q.tiles_n;
-        q.out = const_cast<void *>(g.p);
-        q.ld = stride_of(g.rows, g.ld, g.cols), q.es = p->experts > 1 ? g.es : 0;
+        const long long ld = stride_of(g.rows, g.ld, g.cols), es = p->experts > 1 ? g.es : g.rows * ld;
+        if (st == ROUTE_OK)
+            st = api_encode_operands(&maps.d[a.nprob], g.p, a.fp16, (uint64_t)g.cols, (uint64_t)g.rows,
+                                     (uint64_t)p->experts, (uint64_t)ld, (uint64_t)es, 64, 32, g.name);
         if (i < 2)
             map(&maps.a[a.nprob], x, stride_of(rows, ld_x, p->k), p->k, "x");
         else

@@ -593,65 +593,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         const int cs = (warp - 3) >> 2;       // which 64 of the tile's columns
         const uint32_t lanes = tmem_base + ((uint32_t)(32 * lq) << 16);
         const uint32_t mine = turn + (uint32_t)(warp - 3) * kGradTurn;
-        // 16 bytes (unit x) of a row sit at unit x ^ (row & 7)
-        auto slot = [&](int row, int x) { return mine + (uint32_t)(row * 128 + ((x ^ (row & 7)) << 4)); };
-        const int px = lane & 7, pr = lane >> 3;
+        // the 128-byte swizzle of the results' boxes: 16 bytes (unit x) of a row sit at unit x ^ (row & 7)
+        auto slot = [&](int x) { return mine + (uint32_t)(lane * 128 + ((x ^ (lane & 7)) << 4)); };
         int job = 0;
         for (unsigned i = pair; i < items; i += (unsigned)args.pairs) {
             const GradTile x = grad_tile(args, i);
-            const auto &p = args.p[x.p];
-            const int r0 = x.tm * 256 + (int)rank * 128 + 32 * lq, c = x.tn * 256 + cs * 64 + 8 * px;
-            uint16_t *q = static_cast<uint16_t *>(p.out) + x.e * p.es + (long long)(r0 + pr) * p.ld + c;
-            const int M = p.M, N = p.N;
-            const long long ld = p.ld;
-            if (x.lo >= x.hi) {
-                for (int j = 0; j < 32; j += 4, q += 4 * ld)
-                    if (r0 + pr + j < M && c < N) *reinterpret_cast<uint4 *>(q) = make_uint4(0u, 0u, 0u, 0u);
-                continue;
-            }
+            const int r0 = x.tm * 256 + (int)rank * 128 + 32 * lq, c0 = x.tn * 256 + cs * 64;
+            const bool some = x.lo < x.hi;
             const int t = job & 1;
-            // one warp polls, the others sleep at the barrier
-            const bool ok = warp != 3 || wait_phase(tfull_bar(t), ((uint32_t)job >> 1) & 1u, args, &s_abort);
-            if (!ptx::named_bar_and(1, 512, ok)) break;
-            ++job;
-            ptx::tc_fence_after();
+            if (some) {
+                if (!__all_sync(0xFFFFFFFFu, wait_phase(tfull_bar(t), ((uint32_t)job >> 1) & 1u, args, &s_abort))) break;
+                ++job;
+                ptx::tc_fence_after();
+            }
             const uint32_t acc = lanes + (uint32_t)(t * 256 + cs * 64);
-            __syncwarp();  // the last tile's rows have left shared memory
+            if (lane == 0) ptx::bulk_wait_group_read<0>();  // the last tile's rows have left shared memory
+            __syncwarp();
 #pragma unroll
             for (int g = 0; g < 64; g += 32) {
-                uint32_t v[32];
-                ptx::tmem_ld_x16(acc + (uint32_t)g, reinterpret_cast<uint32_t(&)[16]>(v[0]));
-                ptx::tmem_ld_x16(acc + (uint32_t)g + 16u, reinterpret_cast<uint32_t(&)[16]>(v[16]));
-                ptx::tmem_ld_wait();
-                float f[32];
-                uint32_t w[16];
+                uint32_t w[16] = {};
+                if (some) {
+                    uint32_t v[32];
+                    ptx::tmem_ld_x16(acc + (uint32_t)g, reinterpret_cast<uint32_t(&)[16]>(v[0]));
+                    ptx::tmem_ld_x16(acc + (uint32_t)g + 16u, reinterpret_cast<uint32_t(&)[16]>(v[16]));
+                    ptx::tmem_ld_wait();
+                    float f[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]);
-                pack_values<32>(args.fp16 != 0, f, w);
+                    for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]);
+                    pack_values<32>(args.fp16 != 0, f, w);
+                }
 #pragma unroll
                 for (int h = 0; h < 4; ++h)
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(slot(lane, g / 8 + h)), "r"(w[4 * h]),
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(slot(g / 8 + h)), "r"(w[4 * h]),
                                  "r"(w[4 * h + 1]), "r"(w[4 * h + 2]), "r"(w[4 * h + 3])
                                  : "memory");
             }
-            ptx::tc_fence_before();
+            if (some) ptx::tc_fence_before();
+            ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                if (leader)
-                    ptx::mbar_arrive(tempty_bar(t));
-                else
-                    ptx::mbar_arrive_remote_relaxed(ptx::map_to_rank(tempty_bar(t), 0u));
-            }
-#pragma unroll
-            for (int j = 0; j < 32; j += 4, q += 4 * ld) {
-                uint4 w;
-                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                             : "r"(slot(pr + j, px))
-                             : "memory");
-                if (r0 + pr + j < M && c < N) *reinterpret_cast<uint4 *>(q) = w;
+                if (some) {
+                    if (leader)
+                        ptx::mbar_arrive(tempty_bar(t));
+                    else
+                        ptx::mbar_arrive_remote_relaxed(ptx::map_to_rank(tempty_bar(t), 0u));
+                }
+                if (r0 < args.p[x.p].M && c0 < args.p[x.p].N) ptx::tma_store_3d(&maps.d[x.p], mine, c0, r0, x.e);
+                ptx::bulk_commit_group();
             }
         }
+        if (lane == 0) ptx::bulk_wait_group_all();
     }
 
     ptx::tc_fence_before();
