@@ -44,8 +44,8 @@ cudaError_t combine_backward_launch(const MoveArgs &args, cudaStream_t stream);
 
 // ---- the experts' products ----------------------------------------------------------
 
-// Rows of token maps: one for each height of a box, 16 << i rows.
-constexpr int kTokenBoxes = 4;
+// Maps of the rows, one for each height of a box: 16 (i + 1) rows.
+constexpr int kTokenBoxes = 8;
 struct ExpertsMaps {
     CUtensorMap w[2];                // the weights [experts][..][..] (gated: of gate and of up)
     CUtensorMap t[2][kTokenBoxes];   // the rows of each segment of the contraction
@@ -61,6 +61,10 @@ struct ExpertsArgs {
     unsigned w_bytes;           // bytes of a CTA's weight boxes of a k-block
     int fp16;
     int trigger;                // another kernel of the call follows
+    // The call's kernel before this one waited for its own predecessors before it
+    // let this one launch, and writes neither the offsets nor the weights: both
+    // are read at once.
+    int chained;
     int pairs;                  // CTA pairs launched
     int test_stall;
     unsigned long long timeout_ns;

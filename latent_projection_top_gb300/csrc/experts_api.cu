@@ -100,7 +100,7 @@ struct Rows {
     void tokens(int seg, const void *src, long long ld, int K) {
         for (int i = 0; i < kTokenBoxes && st == ROUTE_OK; ++i)
             st = api_encode_operand(&maps.t[seg][i], src, a.fp16, (uint64_t)K, (uint64_t)a.rows, (uint64_t)ld, 64,
-                                    16u << i, "the sorted rows");
+                                    16u * (i + 1), "the sorted rows");
     }
     // a segment's weights: box of 64 columns x 64 rows, or of 64 columns x a CTA's share of the rows
     void weights(int i, const Stack &w, bool n_contiguous) {
@@ -112,9 +112,9 @@ struct Rows {
             st = api_encode_operands(&maps.w[i], w.p, a.fp16, (uint64_t)w.cols, (uint64_t)w.rows,
                                      (uint64_t)p->experts, (uint64_t)ld, (uint64_t)es, 64, box, w.name);
     }
-    route_status launch(int epi, bool n_contiguous, bool more, cudaStream_t s) {
+    route_status launch(int epi, bool n_contiguous, bool chained, bool more, cudaStream_t s) {
         if (st != ROUTE_OK) return st;
-        a.trigger = more;
+        a.chained = chained, a.trigger = more;
         return launched(experts_launch(epi, n_contiguous, maps, a, s), "experts' product kernel launch");
     }
 };
@@ -307,12 +307,12 @@ route_status route_experts_forward(const route_layer *p, int rows, const void *x
     up.a.e.out = h, up.a.e.ld_out = ldf;
     up.a.e.saved = static_cast<float *>(saved), up.a.e.ld_saved = ldf;
     up.a.e.saved2 = saved ? up.a.e.saved + (size_t)rows * ldf : nullptr;
-    if ((st = up.launch(kEpiGated, true, true, s)) != ROUTE_OK) return st;
+    if ((st = up.launch(kEpiGated, true, false, true, s)) != ROUTE_OK) return st;
     Rows down(p, rows, offsets, p->n, kExpertCols, p->f, 1);
     down.tokens(0, h, ldf, p->f);
     down.weights(0, wd, true);
     down.a.e.out = out, down.a.e.ld_out = stride_of(rows, ld_out, p->n);
-    return down.launch(kEpiLinear, true, false, s);
+    return down.launch(kEpiLinear, true, true, false, s);
 }
 
 route_status route_experts_backward(const route_layer *p, int rows, const void *dout, int64_t ld_dout, const void *x,
@@ -361,7 +361,7 @@ route_status route_experts_backward(const route_layer *p, int rows, const void *
         g.a.e.out = dg, g.a.e.out2 = du, g.a.e.ld_out = ldf;
         g.a.e.saved = static_cast<float *>(const_cast<void *>(saved)), g.a.e.ld_saved = ldf;
         g.a.e.saved2 = g.a.e.saved + (size_t)rows * ldf;
-        if ((st = g.launch(kEpiDGate, false, dx || weights, s)) != ROUTE_OK) return st;
+        if ((st = g.launch(kEpiDGate, false, false, dx || weights, s)) != ROUTE_OK) return st;
     }
     if (dx) {
         Rows g(p, rows, offsets, p->k, kExpertCols, p->f, 2);
@@ -370,7 +370,7 @@ route_status route_experts_backward(const route_layer *p, int rows, const void *
         g.weights(0, wg, false);
         g.weights(1, wu, false);
         g.a.e.out = dx, g.a.e.ld_out = stride_of(rows, ld_dx, p->k);
-        if ((st = g.launch(kEpiLinear, false, weights, s)) != ROUTE_OK) return st;
+        if ((st = g.launch(kEpiLinear, false, true, weights, s)) != ROUTE_OK) return st;
     }
     if (!weights) return ROUTE_OK;
     GradMaps maps;

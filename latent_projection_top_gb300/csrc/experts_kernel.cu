@@ -87,16 +87,19 @@ __device__ __forceinline__ Run run_of(const int *offsets, int e, int rows) {
 // ---- rows -------------------------------------------------------------------------
 
 constexpr int kRowsThreads = 320;
-constexpr int kRowsStages = 5;
+constexpr int kRowsStages = 10;                             // at most
 constexpr uint32_t kWBytes = 128 * 64 * 2;                  // a CTA's weight columns of a k-block
-constexpr uint32_t kTBytes = kExpertRows / 2 * 64 * 2;      // its rows, at most
-constexpr uint32_t kRowsStage = kWBytes + kTBytes;
+constexpr uint32_t kRowBytes = 64 * 2;                      // one row of it
 constexpr int kTurnRows = 32;                               // rows an epilogue group turns around at once
 constexpr uint32_t kTurnBytes = kTurnRows * 128 * 4;
 constexpr uint32_t kRowsBars = 256;
 constexpr uint32_t kRowsTable = 2 * (kMaxExperts + 4) * 4;  // parts before each expert, and offsets
-constexpr uint32_t kRowsSmem = 1024 + kRowsStages * kRowsStage + 2 * kTurnBytes + kRowsBars + kRowsTable;
-static_assert(kRowsSmem <= kSmemLimit, "shared memory");
+// What is left is the stages': as many as fit of the size that the largest
+// part needs (five with 256 rows, ten with 32), so that short parts, which are
+// bound by memory, have more on the way.
+constexpr uint32_t kRowsRing = (kSmemLimit - 1024 - 2 * kTurnBytes - kRowsBars - kRowsTable) & ~1023u;
+constexpr uint32_t kRowsSmem = 1024 + kRowsRing + 2 * kTurnBytes + kRowsBars + kRowsTable;
+static_assert(kRowsSmem <= kSmemLimit && kRowsRing >= 5 * (kWBytes + kExpertRows / 2 * kRowBytes), "shared memory");
 
 // Equal parts of at most 256 rows, in steps of 32.
 __device__ __forceinline__ int part_rows(int rows) {
@@ -134,14 +137,15 @@ __device__ __forceinline__ Tile tile_of(const ExpertsArgs &a, const Table &t, un
     return x;
 }
 
-// All threads: the table of parts.  Returns the number of them.
-__device__ __forceinline__ int make_table(const ExpertsArgs &a, int *first, int *offsets, int *scan) {
+// All threads: the table of parts.  Returns the number of them; `most`: the
+// rows of the largest part, rounded up to 32.
+__device__ __forceinline__ int make_table(const ExpertsArgs &a, int *first, int *offsets, int *scan, int &most) {
     constexpr int kEach = 4;
     static_assert(kEach * kRowsThreads >= kMaxExperts, "a thread's experts");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int e = tid; e <= a.experts; e += kRowsThreads) offsets[e] = a.offsets[e];
     __syncthreads();
-    int parts[kEach], sum = 0;
+    int parts[kEach], sum = 0, rows = 32;
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
         const int e = tid * kEach + j;
@@ -150,19 +154,27 @@ __device__ __forceinline__ int make_table(const ExpertsArgs &a, int *first, int 
             const Run r = run_of(offsets, e, a.rows);
             const int step = part_rows(r.hi - r.lo);
             parts[j] = (r.hi - r.lo + step - 1) / step;
+            rows = max(rows, min(step, (r.hi - r.lo + 31) & ~31));
         }
         sum += parts[j];
     }
+    rows = __reduce_max_sync(0xFFFFFFFFu, rows);
     int incl = sum;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
         const int u = __shfl_up_sync(0xFFFFFFFFu, incl, d);
         if (lane >= d) incl += u;
     }
-    if (lane == 31) scan[warp] = incl;
+    constexpr int kWarps = kRowsThreads / 32;
+    if (lane == 31) scan[warp] = incl, scan[kWarps + warp] = rows;
     __syncthreads();
     int before = incl - sum;
-    for (int w = 0; w < warp; ++w) before += scan[w];
+    most = 32;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        before += w < warp ? scan[w] : 0;
+        most = max(most, scan[kWarps + w]);
+    }
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
         const int e = tid * kEach + j;
@@ -179,24 +191,23 @@ __device__ __forceinline__ int make_table(const ExpertsArgs &a, int *first, int 
 template <int EPI, bool W_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
     experts_rows_kernel(const __grid_constant__ ExpertsMaps maps, const __grid_constant__ ExpertsArgs args) {
-    constexpr int S = kRowsStages;
     constexpr int kCtaCols = EPI == kEpiGated ? 64 : 128;  // columns of D a CTA
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t s_tmem_base;
     __shared__ volatile int s_abort;
-    __shared__ int s_scan[kRowsThreads / 32];
+    __shared__ int s_scan[2 * kRowsThreads / 32];
 
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
-    const uint32_t turn = sbase + S * kRowsStage;
+    const uint32_t turn = sbase + kRowsRing;
     const uint32_t bars = turn + 2 * kTurnBytes;
     int *const first = reinterpret_cast<int *>(smem_raw + (bars + kRowsBars - raw));
     int *const offsets = first + kMaxExperts + 4;
     auto full_bar = [&](int s) { return bars + 8u * s; };  // leader's are used
-    auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
-    auto tfull_bar = [&](int t) { return bars + 8u * (2 * S + t); };
-    auto tempty_bar = [&](int t) { return bars + 8u * (2 * S + 2 + t); };  // leader's
-    const uint32_t drain_bar = bars + 8u * (2 * S + 4);
+    auto empty_bar = [&](int s) { return bars + 8u * (kRowsStages + s); };
+    auto tfull_bar = [&](int t) { return bars + 8u * (2 * kRowsStages + t); };
+    auto tempty_bar = [&](int t) { return bars + 8u * (2 * kRowsStages + 2 + t); };  // leader's
+    const uint32_t drain_bar = bars + 8u * (2 * kRowsStages + 4);
 
     const uint32_t rank = ptx::cluster_ctarank();
     const bool leader = rank == 0u;
@@ -204,7 +215,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
     const unsigned pair = blockIdx.x >> 1;
     if (threadIdx.x == 0) {
         s_abort = 0;
-        for (int s = 0; s < S; ++s) {
+        for (int s = 0; s < kRowsStages; ++s) {
             ptx::mbar_init(full_bar(s), 1);
             ptx::mbar_init(empty_bar(s), 1);
         }
@@ -219,13 +230,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
         ptx::tmem_alloc_pair(ptx::smem_addr(&s_tmem_base), 512);
         ptx::tmem_relinquish_pair();
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!args.chained) asm volatile("griddepcontrol.wait;" ::: "memory");
     const Table table = {first, offsets};
-    const unsigned items = (unsigned)make_table(args, first, offsets, s_scan) * (unsigned)args.tiles_n;
+    int most;
+    const unsigned items = (unsigned)make_table(args, first, offsets, s_scan, most) * (unsigned)args.tiles_n;
+    const uint32_t stage = kWBytes + (uint32_t)(most / 2) * kRowBytes;
+    const int S = min(kRowsStages, (int)(kRowsRing / stage));
     ptx::tc_fence_before();
     ptx::cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
     ptx::tc_fence_after();
-    if (threadIdx.x == 0 && args.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem_base = s_tmem_base;
 
     if (warp == 0) {
@@ -234,45 +247,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
             const uint64_t pol = ptx::policy_evict_normal(), pol_t = ptx::policy_evict_last();
             uint32_t armed = 0u, armed_par = 0u;
             bool ok = true;
-            int it = 0;
+            int it = 0, s = 0;  // k-blocks so far, and the stage and
+            uint32_t ph = 0u;   // parity of the next one
+            auto weights = [&](const Tile &x, int kb, int s, uint32_t ph) {
+                const int half = x.n / 2, c0 = (x.tn * 2 + (int)rank) * kCtaCols;
+                const uint32_t fb = ptx::map_to_rank(full_bar(s), 0u), sw = sbase + s * stage;
+                if (leader) {
+                    ptx::mbar_arrive_expect_tx(full_bar(s), 2u * (args.w_bytes + (uint32_t)half * kRowBytes));
+                    armed |= 1u << s;
+                    armed_par = (armed_par & ~(1u << s)) | (ph << s);
+                }
+                const int seg = kb >= args.kswitch, k0 = (seg ? kb - args.kswitch : kb) * 64;
+                if (EPI == kEpiGated) {
+                    ptx::tma_load_3d_pair(sw, &maps.w[0], fb, c0, k0, x.e, pol);
+                    ptx::tma_load_3d_pair(sw + 8192u, &maps.w[1], fb, c0, k0, x.e, pol);
+                } else if (W_MN) {
+                    ptx::tma_load_3d_pair(sw, &maps.w[0], fb, c0, k0, x.e, pol);
+                    ptx::tma_load_3d_pair(sw + 8192u, &maps.w[0], fb, c0 + 64, k0, x.e, pol);
+                } else {
+                    ptx::tma_load_3d_pair(sw, &maps.w[seg], fb, k0, c0, x.e, pol);
+                }
+            };
+            // of the first tile the weights of the first stages, ahead of the wait
+            const int ahead = args.chained && pair < items ? min(S, args.kblocks) : 0;
+            if (ahead > 0) {
+                const Tile x = tile_of(args, table, pair);
+                for (int kb = 0; kb < ahead; ++kb) weights(x, kb, kb, 0u);
+            }
+            if (args.chained) asm volatile("griddepcontrol.wait;" ::: "memory");
+            // after the wait: what follows may read this call's weights at once
+            if (args.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
             for (unsigned i = pair; ok && i < items; i += (unsigned)args.pairs) {
                 const Tile x = tile_of(args, table, i);
-                const int half = x.n / 2, box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
-                const uint32_t tx = 2u * (args.w_bytes + (16u << box) * 128u);
-                const int c0 = (x.tn * 2 + (int)rank) * kCtaCols, r0 = x.row0 + (int)rank * half;
+                const int half = x.n / 2, r0 = x.row0 + (int)rank * half;
+                const CUtensorMap *mt = &maps.t[0][half / 16 - 1];
                 for (int kb = 0; kb < args.kblocks; ++kb, ++it) {
-                    const int s = it % S;
-                    const uint32_t ph = (uint32_t)(it / S) & 1u;
-                    if (!(ok = wait_phase(empty_bar(s), ph ^ 1u, args, &s_abort))) break;
-                    const uint32_t fb = ptx::map_to_rank(full_bar(s), 0u);
-                    if (leader) {
-                        ptx::mbar_arrive_expect_tx(full_bar(s), tx);
-                        armed |= 1u << s;
-                        armed_par = (armed_par & ~(1u << s)) | (ph << s);
+                    if (it >= ahead) {
+                        if (!(ok = wait_phase(empty_bar(s), ph ^ 1u, args, &s_abort))) break;
+                        weights(x, kb, s, ph);
                     }
-                    // test hook: it never arrives
-                    if (args.test_stall && kb == args.kblocks - 1 && leader) continue;
                     const int seg = kb >= args.kswitch, k0 = (seg ? kb - args.kswitch : kb) * 64;
-                    const uint32_t sw = sbase + s * kRowsStage, st = sw + kWBytes;
-                    if (EPI == kEpiGated) {
-                        ptx::tma_load_3d_pair(sw, &maps.w[0], fb, c0, k0, x.e, pol);
-                        ptx::tma_load_3d_pair(sw + 8192u, &maps.w[1], fb, c0, k0, x.e, pol);
-                    } else if (W_MN) {
-                        ptx::tma_load_3d_pair(sw, &maps.w[0], fb, c0, k0, x.e, pol);
-                        ptx::tma_load_3d_pair(sw + 8192u, &maps.w[0], fb, c0 + 64, k0, x.e, pol);
-                    } else {
-                        ptx::tma_load_3d_pair(sw, &maps.w[seg], fb, k0, c0, x.e, pol);
-                    }
-                    ptx::tma_load_2d_pair(st, &maps.t[seg][box], fb, k0, r0, pol_t);
+                    // test hook: the last rows never arrive
+                    if (!(args.test_stall && kb == args.kblocks - 1 && leader))
+                        ptx::tma_load_2d_pair(sbase + s * stage + kWBytes, mt + seg * kTokenBoxes,
+                                              ptx::map_to_rank(full_bar(s), 0u), k0, r0, pol_t);
+                    if (++s == S) s = 0, ph ^= 1u;
                 }
             }
             // The leader's MMAs release the last stages in both CTAs.
-            for (int j = it > S ? it - S : 0; ok && j < it; ++j)
-                ok = wait_phase(empty_bar(j % S), (uint32_t)(j / S) & 1u, args, &s_abort);
+            for (int j = it < S ? it : S; ok && j > 0; --j) {
+                // j k-blocks before the next one
+                const int back = s - j, at = back < 0 ? back + S : back;
+                ok = wait_phase(empty_bar(at), back < 0 ? ph ^ 1u : ph, args, &s_abort);
+            }
             // After an abort the leader lets every copy it armed land.
             if (leader && !ok) {
-                for (int s = 0; s < S; ++s)
-                    if (armed & (1u << s)) wait_drain(full_bar(s), (armed_par >> s) & 1u, args);
+                for (int j = 0; j < S; ++j)
+                    if (armed & (1u << j)) wait_drain(full_bar(j), (armed_par >> j) & 1u, args);
             }
         }
     } else if (warp == 1) {
@@ -280,7 +311,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
             // ---------------- MMA issuer (leader CTA) ----------------
             const uint32_t fmt = args.fp16 ? 0u : 1u;
             const uint32_t idesc0 = (1u << 4) | (fmt << 7) | (fmt << 10) | ((W_MN ? 1u : 0u) << 15) | ((256u >> 4) << 24);
-            int it = 0, job = 0, done = 0;
+            int s = 0, job = 0, done = 0;
+            uint32_t ph = 0u;
             bool ok = true;
             for (unsigned i = pair; ok && i < items; i += (unsigned)args.pairs, ++job) {
                 const Tile x = tile_of(args, table, i);
@@ -289,16 +321,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
                 if (!wait_phase(tempty_bar(t), (((uint32_t)job >> 1) & 1u) ^ 1u, args, &s_abort)) break;
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(t * 256);
-                for (int kb = 0; kb < args.kblocks; ++kb, ++it) {
-                    const int s = it % S;
-                    if (!(ok = wait_phase(full_bar(s), (uint32_t)(it / S) & 1u, args, &s_abort))) break;
+                for (int kb = 0; kb < args.kblocks; ++kb) {
+                    if (!(ok = wait_phase(full_bar(s), ph, args, &s_abort))) break;
                     ptx::tc_fence_after();
-                    const uint32_t sw = sbase + s * kRowsStage, st = sw + kWBytes;
+                    const uint32_t sw = sbase + s * stage, st = sw + kWBytes;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         ptx::mma_bf16_pair(d_tmem, operand_desc<W_MN>(sw, kk), operand_desc<false>(st, kk), idesc,
                                            (kb > 0 || kk > 0) ? 1u : 0u);
                     ptx::mma_commit_pair(empty_bar(s), 0x3);  // frees stage s in both CTAs
+                    if (++s == S) s = 0, ph ^= 1u;
                 }
                 if (ok) ptx::mma_commit_pair(tfull_bar(t), 0x3), ++done;
             }
@@ -317,6 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
         // threads have neighbouring columns; the two groups take every other 32 rows.
         const int lq = warp & 3, group = (warp - 2) >> 2;
         const int tid = lq * 32 + lane;  // in the group
+        if (args.chained) asm volatile("griddepcontrol.wait;" ::: "memory");
         const uint32_t lanes = tmem_base + ((uint32_t)(32 * lq) << 16);
         const uint32_t buf = turn + (uint32_t)group * kTurnBytes;
         constexpr int kGroups = kCtaCols / 4, kStep = 128 / kGroups, kR = kTurnRows / kStep;
