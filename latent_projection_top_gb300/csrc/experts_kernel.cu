@@ -93,7 +93,8 @@ constexpr uint32_t kRowBytes = 64 * 2;                      // one row of it
 constexpr int kTurnRows = 32;                               // rows an epilogue group turns around at once
 constexpr uint32_t kTurnBytes = kTurnRows * 128 * 4;
 constexpr uint32_t kRowsBars = 256;
-constexpr uint32_t kRowsTable = 2 * (kMaxExperts + 4) * 4;  // parts before each expert, and offsets
+constexpr int kPartTable = 2048;                            // parts whose expert is looked up
+constexpr uint32_t kRowsTable = 2 * (kMaxExperts + 4) * 4 + kPartTable * 2;
 // What is left is the stages': as many as fit of the size that the largest
 // part needs (five with 256 rows, ten with 32), so that short parts, which are
 // bound by memory, have more on the way.
@@ -112,38 +113,58 @@ __device__ __forceinline__ int part_rows(int rows) {
 struct Tile {
     int e, row0, end, tn, n;
 };
+// In shared memory: parts of the experts before each ([experts]: all of them),
+// the offsets, and the expert of each of the first kPartTable parts.
 struct Table {
-    const int *first;    // parts of the experts before; [experts]: all parts
-    const int *offsets;  // in shared memory
+    int *first, *offsets;
+    uint16_t *expert;
 };
-__device__ __forceinline__ Tile tile_of(const ExpertsArgs &a, const Table &t, unsigned i) {
-    Tile x;
-    const int part = (int)(i / (unsigned)a.tiles_n);
-    x.tn = (int)(i - (unsigned)part * (unsigned)a.tiles_n);
-    int lo = 0, hi = a.experts;  // first[lo] <= part < first[hi]
-    while (hi - lo > 1) {
-        const int m = (lo + hi) >> 1;
-        if (t.first[m] <= part)
-            lo = m;
-        else
-            hi = m;
+
+// A pair's tiles, one after another: i = part * tiles_n + tn goes up by `pairs`
+// without a division (one and a binary search of the table a tile took the
+// roles of a single thread 0.4 us).
+struct RowsWalk {
+    int part, tn, dpart, dtn;
+    __device__ __forceinline__ RowsWalk(const ExpertsArgs &a, unsigned pair) {
+        dpart = a.pairs / a.tiles_n, dtn = a.pairs - dpart * a.tiles_n;
+        part = (int)pair / a.tiles_n, tn = (int)pair - part * a.tiles_n;
     }
-    x.e = lo;
-    const Run r = run_of(t.offsets, lo, a.rows);
-    const int step = part_rows(r.hi - r.lo);
-    x.row0 = r.lo + (part - t.first[lo]) * step;
-    x.end = min(r.hi, x.row0 + step);
-    x.n = (x.end - x.row0 + 31) & ~31;
-    return x;
-}
+    __device__ __forceinline__ void next(const ExpertsArgs &a) {
+        part += dpart, tn += dtn;
+        if (tn >= a.tiles_n) tn -= a.tiles_n, ++part;
+    }
+    __device__ __forceinline__ Tile tile(const ExpertsArgs &a, const Table &t) const {
+        Tile x;
+        x.tn = tn;
+        if (part < kPartTable) {
+            x.e = t.expert[part];
+        } else {
+            int lo = 0, hi = a.experts;  // first[lo] <= part < first[hi]
+            while (hi - lo > 1) {
+                const int m = (lo + hi) >> 1;
+                if (t.first[m] <= part)
+                    lo = m;
+                else
+                    hi = m;
+            }
+            x.e = lo;
+        }
+        const Run r = run_of(t.offsets, x.e, a.rows);
+        const int step = part_rows(r.hi - r.lo);
+        x.row0 = r.lo + (part - t.first[x.e]) * step;
+        x.end = min(r.hi, x.row0 + step);
+        x.n = (x.end - x.row0 + 31) & ~31;
+        return x;
+    }
+};
 
 // All threads: the table of parts.  Returns the number of them; `most`: the
 // rows of the largest part, rounded up to 32.
-__device__ __forceinline__ int make_table(const ExpertsArgs &a, int *first, int *offsets, int *scan, int &most) {
+__device__ __forceinline__ int make_table(const ExpertsArgs &a, const Table &t, int *scan, int &most) {
     constexpr int kEach = 4;
     static_assert(kEach * kRowsThreads >= kMaxExperts, "a thread's experts");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int e = tid; e <= a.experts; e += kRowsThreads) offsets[e] = a.offsets[e];
+    for (int e = tid; e <= a.experts; e += kRowsThreads) t.offsets[e] = a.offsets[e];
     __syncthreads();
     int parts[kEach], sum = 0, rows = 32;
 #pragma unroll
@@ -151,7 +172,7 @@ __device__ __forceinline__ int make_table(const ExpertsArgs &a, int *first, int 
         const int e = tid * kEach + j;
         parts[j] = 0;
         if (e < a.experts) {
-            const Run r = run_of(offsets, e, a.rows);
+            const Run r = run_of(t.offsets, e, a.rows);
             const int step = part_rows(r.hi - r.lo);
             parts[j] = (r.hi - r.lo + step - 1) / step;
             rows = max(rows, min(step, (r.hi - r.lo + 31) & ~31));
@@ -178,12 +199,13 @@ __device__ __forceinline__ int make_table(const ExpertsArgs &a, int *first, int 
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
         const int e = tid * kEach + j;
-        if (e < a.experts) first[e] = before;
+        if (e < a.experts) t.first[e] = before;
+        for (int k = before; k < min(before + parts[j], kPartTable); ++k) t.expert[k] = (uint16_t)e;
         before += parts[j];
-        if (e == a.experts - 1) first[a.experts] = before;
+        if (e == a.experts - 1) t.first[a.experts] = before;
     }
     __syncthreads();
-    return first[a.experts];
+    return t.first[a.experts];
 }
 
 // EPI: what the epilogue makes of the sums; W_MN: the weights' columns are
@@ -201,8 +223,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
     const uint32_t sbase = (raw + 1023u) & ~1023u;
     const uint32_t turn = sbase + kRowsRing;
     const uint32_t bars = turn + 2 * kTurnBytes;
-    int *const first = reinterpret_cast<int *>(smem_raw + (bars + kRowsBars - raw));
-    int *const offsets = first + kMaxExperts + 4;
+    int *const words = reinterpret_cast<int *>(smem_raw + (bars + kRowsBars - raw));
+    const Table table = {words, words + kMaxExperts + 4, reinterpret_cast<uint16_t *>(words + 2 * (kMaxExperts + 4))};
     auto full_bar = [&](int s) { return bars + 8u * s; };  // leader's are used
     auto empty_bar = [&](int s) { return bars + 8u * (kRowsStages + s); };
     auto tfull_bar = [&](int t) { return bars + 8u * (2 * kRowsStages + t); };
@@ -231,9 +253,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
         ptx::tmem_relinquish_pair();
     }
     if (!args.chained) asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Table table = {first, offsets};
     int most;
-    const unsigned items = (unsigned)make_table(args, first, offsets, s_scan, most) * (unsigned)args.tiles_n;
+    const int parts = make_table(args, table, s_scan, most);
     const uint32_t stage = kWBytes + (uint32_t)(most / 2) * kRowBytes;
     const int S = min(kRowsStages, (int)(kRowsRing / stage));
     ptx::tc_fence_before();
@@ -269,16 +290,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
                 }
             };
             // of the first tile the weights of the first stages, ahead of the wait
-            const int ahead = args.chained && pair < items ? min(S, args.kblocks) : 0;
+            RowsWalk walk(args, pair);
+            const int ahead = args.chained && walk.part < parts ? min(S, args.kblocks) : 0;
             if (ahead > 0) {
-                const Tile x = tile_of(args, table, pair);
+                const Tile x = walk.tile(args, table);
                 for (int kb = 0; kb < ahead; ++kb) weights(x, kb, kb, 0u);
             }
             if (args.chained) asm volatile("griddepcontrol.wait;" ::: "memory");
             // after the wait: what follows may read this call's weights at once
             if (args.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-            for (unsigned i = pair; ok && i < items; i += (unsigned)args.pairs) {
-                const Tile x = tile_of(args, table, i);
+            for (; ok && walk.part < parts; walk.next(args)) {
+                const Tile x = walk.tile(args, table);
                 const int half = x.n / 2, r0 = x.row0 + (int)rank * half;
                 const CUtensorMap *mt = &maps.t[0][half / 16 - 1];
                 for (int kb = 0; kb < args.kblocks; ++kb, ++it) {
@@ -314,8 +336,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
             int s = 0, job = 0, done = 0;
             uint32_t ph = 0u;
             bool ok = true;
-            for (unsigned i = pair; ok && i < items; i += (unsigned)args.pairs, ++job) {
-                const Tile x = tile_of(args, table, i);
+            for (RowsWalk walk(args, pair); ok && walk.part < parts; walk.next(args), ++job) {
+                const Tile x = walk.tile(args, table);
                 const uint32_t idesc = idesc0 | ((uint32_t)(x.n >> 3) << 17);
                 const int t = job & 1;
                 if (!wait_phase(tempty_bar(t), (((uint32_t)job >> 1) & 1u) ^ 1u, args, &s_abort)) break;
@@ -353,22 +375,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
         const uint32_t lanes = tmem_base + ((uint32_t)(32 * lq) << 16);
         const uint32_t buf = turn + (uint32_t)group * kTurnBytes;
         constexpr int kGroups = kCtaCols / 4, kStep = 128 / kGroups, kR = kTurnRows / kStep;
-        constexpr int kBatch = 4;
+        constexpr int kBatch = 4, kBatches = kR / kBatch;
         static_assert(kR % kBatch == 0, "whole batches");
         const int tr = tid / kGroups, tc = tid % kGroups * 4;
         int job = 0;
         Epilogue p = args.e;
-        for (unsigned i = pair; i < items; i += (unsigned)args.pairs, ++job) {
-            const Tile x = tile_of(args, table, i);
+        for (RowsWalk walk(args, pair); walk.part < parts; walk.next(args), ++job) {
+            const Tile x = walk.tile(args, table);
             const int t = job & 1;
             p.M = x.end;
             const int c = (x.tn * 2 + (int)rank) * kCtaCols + tc;
+            // what is read besides goes out before the tile's sums are complete (read
+            // after them, 256 experts of 1024x512 with 63 rows: d gate 86 us, so 55)
+            GroupIn<EPI, kBatch> in[kBatches];
+            auto inputs = [&](int b) {
+#pragma unroll
+                for (int q = 0; q < kBatches; ++q)
+                    group_load<EPI, kBatch>(p, x.row0 + b + tr + q * kBatch * kStep, c, kStep, in[q]);
+            };
+            inputs(group * kTurnRows);
             // one warp of a group polls, the others sleep at the barrier
             const bool ok = lq != 2 || wait_phase(tfull_bar(t), ((uint32_t)job >> 1) & 1u, args, &s_abort);
             if (!ptx::named_bar_and(1 + group, 128, ok)) break;
             ptx::tc_fence_after();
             const uint32_t acc = lanes + (uint32_t)(t * 256);
             for (int b = group * kTurnRows; b < x.n; b += 2 * kTurnRows) {
+                if (b >= 2 * kTurnRows) inputs(b);
                 uint32_t v[kTurnRows];
                 ptx::tmem_ld_x16(acc + (uint32_t)b, reinterpret_cast<uint32_t(&)[16]>(v[0]));
                 ptx::tmem_ld_x16(acc + (uint32_t)b + 16u, reinterpret_cast<uint32_t(&)[16]>(v[16]));
@@ -379,15 +411,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
                                  : "memory");
                 ptx::named_bar_sync(1 + group, 128);
 #pragma unroll
-                for (int q = 0; q < kR; q += kBatch) {
-                    const int r = x.row0 + b + tr + q * kStep;
+                for (int q = 0; q < kBatches; ++q) {
+                    const int r = x.row0 + b + tr + q * kBatch * kStep;
                     if (r >= p.M) break;
-                    GroupIn<EPI, kBatch> in;
-                    group_load<EPI, kBatch>(p, r, c, kStep, in);
                     float d[4 * kBatch], u[EPI == kEpiGated ? 4 * kBatch : 1];
 #pragma unroll
                     for (int j = 0; j < kBatch; ++j) {
-                        const uint32_t at = buf + (uint32_t)((tr + (q + j) * kStep) * 128 + tc) * 4u;
+                        const uint32_t at = buf + (uint32_t)((tr + (q * kBatch + j) * kStep) * 128 + tc) * 4u;
                         asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
                                      : "=f"(d[4 * j]), "=f"(d[4 * j + 1]), "=f"(d[4 * j + 2]), "=f"(d[4 * j + 3])
                                      : "r"(at)
@@ -398,7 +428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
                                          : "r"(at + 256u)
                                          : "memory");
                     }
-                    group_epilogue<EPI, kBatch>(p, r, c, kStep, d, u, in);
+                    group_epilogue<EPI, kBatch>(p, r, c, kStep, d, u, in[q]);
                 }
                 ptx::named_bar_sync(1 + group, 128);  // the rows have left shared memory
             }
@@ -435,21 +465,39 @@ constexpr uint32_t kGradSmem = 1024 + kGradStages * kGradStage + 16 * kGradTurn 
 static_assert(kGradSmem <= kSmemLimit, "shared memory");
 
 struct GradTile {
-    int e, p, tm, tn, lo, hi;
+    int e, p, m0, n0, lo, hi;
 };
-__device__ __forceinline__ GradTile grad_tile(const GradArgs &a, unsigned i) {
-    GradTile x;
-    x.e = (int)(i / (unsigned)a.per_expert);
-    int r = (int)(i - (unsigned)x.e * (unsigned)a.per_expert);
-    x.p = 0;
-    while (x.p + 1 < a.nprob && r >= a.p[x.p + 1].base) ++x.p;
-    r -= a.p[x.p].base;
-    x.tm = r / a.p[x.p].tiles_n;
-    x.tn = r - x.tm * a.p[x.p].tiles_n;
-    const Run run = run_of(a.offsets, x.e, a.rows);
-    x.lo = run.lo, x.hi = run.hi;
-    return x;
-}
+// A pair's tiles, one after another, an expert's together; the next one's
+// offsets are on their way while a tile is worked on.
+struct GradWalk {
+    int e, r, de, dr, o0, o1;
+    __device__ __forceinline__ GradWalk(const GradArgs &a, unsigned pair) {
+        de = a.pairs / a.per_expert, dr = a.pairs - de * a.per_expert;
+        e = (int)pair / a.per_expert, r = (int)pair - e * a.per_expert;
+        fetch(a);
+    }
+    __device__ __forceinline__ void fetch(const GradArgs &a) {
+        if (e < a.experts) o0 = a.offsets[e], o1 = a.offsets[e + 1];
+    }
+    __device__ __forceinline__ bool more(const GradArgs &a) const { return e < a.experts; }
+    __device__ __forceinline__ GradTile take(const GradArgs &a) {
+        GradTile x;
+        x.e = e;
+        x.lo = min(max(o0, 0), a.rows);
+        x.hi = max(min(o1, a.rows), x.lo);
+        int base = 0, tiles_n = a.p[0].tiles_n;
+        x.p = 0;
+#pragma unroll
+        for (int j = 1; j < kMaxGrads; ++j)
+            if (j < a.nprob && r >= a.p[j].base) x.p = j, base = a.p[j].base, tiles_n = a.p[j].tiles_n;
+        const unsigned q = (unsigned)(r - base), tm = q / (unsigned)tiles_n;
+        x.m0 = (int)tm * 256, x.n0 = (int)(q - tm * (unsigned)tiles_n) * 256;
+        e += de, r += dr;
+        if (r >= a.per_expert) r -= a.per_expert, ++e;
+        fetch(a);
+        return x;
+    }
+};
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     experts_grad_kernel(const __grid_constant__ GradMaps maps, const __grid_constant__ GradArgs args) {
@@ -475,7 +523,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     const bool leader = rank == 0u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned pair = blockIdx.x >> 1;
-    const unsigned items = (unsigned)args.experts * (unsigned)args.per_expert;
     if (threadIdx.x == 0) {
         s_abort = 0;
         for (int s = 0; s < S; ++s) {
@@ -508,14 +555,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
             uint32_t tails = 0u, tail_par = 0u;   // and on its tail barriers: the next phase's parity
             bool ok = true;
             int it = 0;
-            for (unsigned i = pair; ok && i < items; i += (unsigned)args.pairs) {
-                const GradTile x = grad_tile(args, i);
-                const int m0 = x.tm * 256 + (int)rank * 128, n0 = x.tn * 256 + (int)rank * 128;
+            for (GradWalk walk(args, pair); ok && walk.more(args);) {
+                const GradTile x = walk.take(args);
+                const int m0 = x.m0 + (int)rank * 128, n0 = x.n0 + (int)rank * 128;
                 for (int r = x.lo; r < x.hi; r += 64, ++it) {
                     const int s = it % S;
                     const uint32_t ph = (uint32_t)(it / S) & 1u;
                     if (!(ok = wait_phase(empty_bar(s), ph ^ 1u, args, &s_abort))) break;
-                    const bool tail = r + 64 > x.hi;
+                    // the tensor cores take 16 rows at a time: past those nothing is read
+                    const bool tail = r + 64 > x.hi && (x.hi - r) % 16 != 0;
                     const bool stall = args.test_stall && r + 64 >= x.hi && leader;  // test hook: it never arrives
                     const uint32_t sa = sbase + s * kGradStage, sb = sa + 16384u;
                     const CUtensorMap *ma = &maps.a[x.p], *mb = &maps.b[x.p];
@@ -566,8 +614,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
                                    ((256u >> 3) << 17) | ((256u >> 4) << 24);
             int it = 0, job = 0, done = 0;
             bool ok = true;
-            for (unsigned i = pair; ok && i < items; i += (unsigned)args.pairs) {
-                const GradTile x = grad_tile(args, i);
+            for (GradWalk walk(args, pair); ok && walk.more(args);) {
+                const GradTile x = walk.take(args);
                 if (x.lo >= x.hi) continue;  // zeros: the epilogue's alone
                 const int t = job & 1;
                 if (!wait_phase(tempty_bar(t), (((uint32_t)job >> 1) & 1u) ^ 1u, args, &s_abort)) break;
@@ -580,8 +628,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
                     const uint32_t sa = sbase + s * kGradStage, sb = sa + 16384u;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        ptx::mma_bf16_pair(d_tmem, operand_desc<true>(sa, kk), operand_desc<true>(sb, kk), idesc,
-                                           (r > x.lo || kk > 0) ? 1u : 0u);
+                        if (kk == 0 || r + 16 * kk < x.hi)
+                            ptx::mma_bf16_pair(d_tmem, operand_desc<true>(sa, kk), operand_desc<true>(sb, kk), idesc,
+                                               (r > x.lo || kk > 0) ? 1u : 0u);
                     ptx::mma_commit_pair(empty_bar(s), 0x3);
                 }
                 if (ok) ptx::mma_commit_pair(tfull_bar(t), 0x3), ++done;
@@ -599,18 +648,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         int it = 0;
         uint32_t tail_par = 0u;
         bool ok = true;
-        for (unsigned i = pair; ok && i < items; i += (unsigned)args.pairs) {
-            const GradTile x = grad_tile(args, i);
+        for (GradWalk walk(args, pair); ok && walk.more(args);) {
+            const GradTile x = walk.take(args);
             const int blocks = (x.hi - x.lo + 63) / 64, left = (x.hi - x.lo) & 63;
             it += blocks;
-            if (left == 0) continue;
+            if (left % 16 == 0) continue;
             const int s = (it - 1) % S;
             ok = __all_sync(0xFFFFFFFFu, wait_phase(tail_bar(s), (tail_par >> s) & 1u, args, &s_abort));
             tail_par ^= 1u << s;
             if (!ok) break;
             // row r of the batch is 128 bytes of each of the four boxes
             const uint32_t at = sbase + s * kGradStage + (uint32_t)left * 128u;
-            const int pieces = (64 - left) * 8;
+            const int pieces = (16 - left % 16) * 8;
 #pragma unroll
             for (int b = 0; b < 4; ++b)
                 for (int j = lane; j < pieces; j += 32)
@@ -629,9 +678,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         // the 128-byte swizzle of the results' boxes: 16 bytes (unit x) of a row sit at unit x ^ (row & 7)
         auto slot = [&](int x) { return mine + (uint32_t)(lane * 128 + ((x ^ (lane & 7)) << 4)); };
         int job = 0;
-        for (unsigned i = pair; i < items; i += (unsigned)args.pairs) {
-            const GradTile x = grad_tile(args, i);
-            const int r0 = x.tm * 256 + (int)rank * 128 + 32 * lq, c0 = x.tn * 256 + cs * 64;
+        for (GradWalk walk(args, pair); walk.more(args);) {
+            const GradTile x = walk.take(args);
+            const int r0 = x.m0 + (int)rank * 128 + 32 * lq, c0 = x.n0 + cs * 64;
             const bool some = x.lo < x.hi;
             const int t = job & 1;
             if (some) {
