@@ -86,11 +86,12 @@ __device__ __forceinline__ Run run_of(const int *offsets, int e, int rows) {
 
 // ---- rows -------------------------------------------------------------------------
 
-constexpr int kRowsThreads = 320;
+constexpr int kEpiGroups = 4;                               // of four epilogue warps
+constexpr int kRowsThreads = 64 + 128 * kEpiGroups;
 constexpr int kRowsStages = 10;                             // at most
 constexpr uint32_t kWBytes = 128 * 64 * 2;                  // a CTA's weight columns of a k-block
 constexpr uint32_t kRowBytes = 64 * 2;                      // one row of it
-constexpr int kTurnRows = 32;                               // rows an epilogue group turns around at once
+constexpr int kTurnRows = 16;                               // rows an epilogue group turns around at once
 constexpr uint32_t kTurnBytes = kTurnRows * 128 * 4;
 constexpr uint32_t kRowsBars = 256;
 constexpr int kPartTable = 2048;                            // parts whose expert is looked up
@@ -98,8 +99,8 @@ constexpr uint32_t kRowsTable = 2 * (kMaxExperts + 4) * 4 + kPartTable * 2;
 // What is left is the stages': as many as fit of the size that the largest
 // part needs (five with 256 rows, ten with 32), so that short parts, which are
 // bound by memory, have more on the way.
-constexpr uint32_t kRowsRing = (kSmemLimit - 1024 - 2 * kTurnBytes - kRowsBars - kRowsTable) & ~1023u;
-constexpr uint32_t kRowsSmem = 1024 + kRowsRing + 2 * kTurnBytes + kRowsBars + kRowsTable;
+constexpr uint32_t kRowsRing = (kSmemLimit - 1024 - kEpiGroups * kTurnBytes - kRowsBars - kRowsTable) & ~1023u;
+constexpr uint32_t kRowsSmem = 1024 + kRowsRing + kEpiGroups * kTurnBytes + kRowsBars + kRowsTable;
 static_assert(kRowsSmem <= kSmemLimit && kRowsRing >= 5 * (kWBytes + kExpertRows / 2 * kRowBytes), "shared memory");
 
 // Equal parts of at most 256 rows, in steps of 32.
@@ -161,7 +162,7 @@ struct RowsWalk {
 // All threads: the table of parts.  Returns the number of them; `most`: the
 // rows of the largest part, rounded up to 32.
 __device__ __forceinline__ int make_table(const ExpertsArgs &a, const Table &t, int *scan, int &most) {
-    constexpr int kEach = 4;
+    constexpr int kEach = 2;
     static_assert(kEach * kRowsThreads >= kMaxExperts, "a thread's experts");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int e = tid; e <= a.experts; e += kRowsThreads) t.offsets[e] = a.offsets[e];
@@ -222,7 +223,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
     const uint32_t turn = sbase + kRowsRing;
-    const uint32_t bars = turn + 2 * kTurnBytes;
+    const uint32_t bars = turn + kEpiGroups * kTurnBytes;
     int *const words = reinterpret_cast<int *>(smem_raw + (bars + kRowsBars - raw));
     const Table table = {words, words + kMaxExperts + 4, reinterpret_cast<uint16_t *>(words + 2 * (kMaxExperts + 4))};
     auto full_bar = [&](int s) { return bars + 8u * s; };  // leader's are used
@@ -243,7 +244,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
         }
         for (int t = 0; t < 2; ++t) {
             ptx::mbar_init(tfull_bar(t), 1);
-            ptx::mbar_init(tempty_bar(t), 16);  // each epilogue warp of both CTAs
+            ptx::mbar_init(tempty_bar(t), 8 * kEpiGroups);  // each epilogue warp of both CTAs
         }
         ptx::mbar_init(drain_bar, 1);
         ptx::fence_barrier_init();
@@ -367,16 +368,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
     } else {
         // ---------------- epilogue (both CTAs) ----------------
         // Columns of D are the TMEM lanes.  Four warps, a group, hold the CTA's 128
-        // of them and turn 32 rows around in shared memory, so that neighbouring
-        // threads have neighbouring columns; the two groups take every other 32 rows.
+        // of them and turn 16 rows around in shared memory, so that neighbouring
+        // threads have neighbouring columns; the groups take every fourth 16 rows.
         const int lq = warp & 3, group = (warp - 2) >> 2;
         const int tid = lq * 32 + lane;  // in the group
         if (args.chained) asm volatile("griddepcontrol.wait;" ::: "memory");
         const uint32_t lanes = tmem_base + ((uint32_t)(32 * lq) << 16);
         const uint32_t buf = turn + (uint32_t)group * kTurnBytes;
         constexpr int kGroups = kCtaCols / 4, kStep = 128 / kGroups, kR = kTurnRows / kStep;
-        constexpr int kBatch = 4, kBatches = kR / kBatch;
-        static_assert(kR % kBatch == 0, "whole batches");
         const int tr = tid / kGroups, tc = tid % kGroups * 4;
         int job = 0;
         Epilogue p = args.e;
@@ -387,50 +386,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
             const int c = (x.tn * 2 + (int)rank) * kCtaCols + tc;
             // what is read besides goes out before the tile's sums are complete (read
             // after them, 256 experts of 1024x512 with 63 rows: d gate 86 us, so 55)
-            GroupIn<EPI, kBatch> in[kBatches];
-            auto inputs = [&](int b) {
-#pragma unroll
-                for (int q = 0; q < kBatches; ++q)
-                    group_load<EPI, kBatch>(p, x.row0 + b + tr + q * kBatch * kStep, c, kStep, in[q]);
-            };
-            inputs(group * kTurnRows);
+            GroupIn<EPI, kR> in;
+            const int r0 = x.row0 + tr;
+            group_load<EPI, kR>(p, r0 + group * kTurnRows, c, kStep, in);
             // one warp of a group polls, the others sleep at the barrier
             const bool ok = lq != 2 || wait_phase(tfull_bar(t), ((uint32_t)job >> 1) & 1u, args, &s_abort);
             if (!ptx::named_bar_and(1 + group, 128, ok)) break;
             ptx::tc_fence_after();
             const uint32_t acc = lanes + (uint32_t)(t * 256);
-            for (int b = group * kTurnRows; b < x.n; b += 2 * kTurnRows) {
-                if (b >= 2 * kTurnRows) inputs(b);
+            for (int b = group * kTurnRows; b < x.n; b += kEpiGroups * kTurnRows) {
+                if (b >= kEpiGroups * kTurnRows) group_load<EPI, kR>(p, r0 + b, c, kStep, in);
                 uint32_t v[kTurnRows];
-                ptx::tmem_ld_x16(acc + (uint32_t)b, reinterpret_cast<uint32_t(&)[16]>(v[0]));
-                ptx::tmem_ld_x16(acc + (uint32_t)b + 16u, reinterpret_cast<uint32_t(&)[16]>(v[16]));
+                ptx::tmem_ld_x16(acc + (uint32_t)b, v);
                 ptx::tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < kTurnRows; ++j)
                     asm volatile("st.shared.b32 [%0], %1;" ::"r"(buf + (uint32_t)(j * 128 + tid) * 4u), "r"(v[j])
                                  : "memory");
                 ptx::named_bar_sync(1 + group, 128);
+                float d[4 * kR], u[EPI == kEpiGated ? 4 * kR : 1];
 #pragma unroll
-                for (int q = 0; q < kBatches; ++q) {
-                    const int r = x.row0 + b + tr + q * kBatch * kStep;
-                    if (r >= p.M) break;
-                    float d[4 * kBatch], u[EPI == kEpiGated ? 4 * kBatch : 1];
-#pragma unroll
-                    for (int j = 0; j < kBatch; ++j) {
-                        const uint32_t at = buf + (uint32_t)((tr + (q * kBatch + j) * kStep) * 128 + tc) * 4u;
+                for (int j = 0; j < kR; ++j) {
+                    const uint32_t at = buf + (uint32_t)((tr + j * kStep) * 128 + tc) * 4u;
+                    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                 : "=f"(d[4 * j]), "=f"(d[4 * j + 1]), "=f"(d[4 * j + 2]), "=f"(d[4 * j + 3])
+                                 : "r"(at)
+                                 : "memory");
+                    if constexpr (EPI == kEpiGated)
                         asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                                     : "=f"(d[4 * j]), "=f"(d[4 * j + 1]), "=f"(d[4 * j + 2]), "=f"(d[4 * j + 3])
-                                     : "r"(at)
+                                     : "=f"(u[4 * j]), "=f"(u[4 * j + 1]), "=f"(u[4 * j + 2]), "=f"(u[4 * j + 3])
+                                     : "r"(at + 256u)
                                      : "memory");
-                        if constexpr (EPI == kEpiGated)
-                            asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                                         : "=f"(u[4 * j]), "=f"(u[4 * j + 1]), "=f"(u[4 * j + 2]), "=f"(u[4 * j + 3])
-                                         : "r"(at + 256u)
-                                         : "memory");
-                    }
-                    group_epilogue<EPI, kBatch>(p, r, c, kStep, d, u, in[q]);
                 }
                 ptx::named_bar_sync(1 + group, 128);  // the rows have left shared memory
+                group_epilogue<EPI, kR>(p, r0 + b, c, kStep, d, u, in);
             }
             ptx::tc_fence_before();
             __syncwarp();
