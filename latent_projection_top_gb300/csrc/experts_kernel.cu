@@ -103,12 +103,6 @@ constexpr uint32_t kRowsRing = (kSmemLimit - 1024 - kEpiGroups * kTurnBytes - kR
 constexpr uint32_t kRowsSmem = 1024 + kRowsRing + kEpiGroups * kTurnBytes + kRowsBars + kRowsTable;
 static_assert(kRowsSmem <= kSmemLimit && kRowsRing >= 5 * (kWBytes + kExpertRows / 2 * kRowBytes), "shared memory");
 
-// Equal parts of at most 256 rows, in steps of 32.
-__device__ __forceinline__ int part_rows(int rows) {
-    const int parts = (rows + kExpertRows - 1) / kExpertRows;
-    return parts > 0 ? ((rows + parts - 1) / parts + 31) & ~31 : 32;
-}
-
 // A tile: expert, rows row0 .. end, column tile, columns of the MMA (rows
 // rounded up to 32).
 struct Tile {
@@ -119,6 +113,7 @@ struct Tile {
 struct Table {
     int *first, *offsets;
     uint16_t *expert;
+    int shift;  // parts have up to 1 << shift rows
 };
 
 // A pair's tiles, one after another: i = part * tiles_n + tn goes up by `pairs`
@@ -151,7 +146,10 @@ struct RowsWalk {
             x.e = lo;
         }
         const Run r = run_of(t.offsets, x.e, a.rows);
-        const int step = part_rows(r.hi - r.lo);
+        // an expert's parts are equal, in steps of 32 (8192 rows of 3584x2048: 444 us, the
+        // last one what is left: 452); none is empty, because a step is no more than the most
+        const int parts = (r.hi - r.lo + (1 << t.shift) - 1) >> t.shift;
+        const int step = parts > 1 ? ((r.hi - r.lo + parts - 1) / parts + 31) & ~31 : r.hi - r.lo;
         x.row0 = r.lo + (part - t.first[x.e]) * step;
         x.end = min(r.hi, x.row0 + step);
         x.n = (x.end - x.row0 + 31) & ~31;
@@ -159,44 +157,75 @@ struct RowsWalk {
     }
 };
 
+// The time of a launch whose parts have up to `n` rows, in ns: a k-block of a
+// tile takes as long as its copies to an SM, 95 bytes a nanosecond, or its MMAs
+// (the same at 256 rows), its epilogue `epi_ns` for 64 rows; the last one is in
+// nobody's shadow.
+__device__ __forceinline__ int launch_ns(const ExpertsArgs &a, int parts, int n, int epi_ns) {
+    const int rounds = (parts * a.tiles_n + a.pairs - 1) / a.pairs;
+    const int load = a.kblocks * (172 + 2 * n / 3), epi = (n + 63) / 64 * epi_ns;
+    return min(rounds, 4096) * min(max(load, epi), 1 << 17) + epi;
+}
+
 // All threads: the table of parts.  Returns the number of them; `most`: the
 // rows of the largest part, rounded up to 32.
-__device__ __forceinline__ int make_table(const ExpertsArgs &a, const Table &t, int *scan, int &most) {
-    constexpr int kEach = 2;
+//
+// Parts have up to 256 rows, or, where that leaves too few tiles for the pairs,
+// up to 128, 64 or 32: more tiles read the same weights, from L2, and each
+// pair's share and last epilogue are shorter.
+__device__ __forceinline__ int make_table(const ExpertsArgs &a, Table &t, int epi_ns, int *scan, int &most) {
+    constexpr int kEach = 2, kSizes = 4, kLargest = 8, kWarps = kRowsThreads / 32;
+    static_assert(1 << kLargest == kExpertRows, "parts");
     static_assert(kEach * kRowsThreads >= kMaxExperts, "a thread's experts");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int e = tid; e <= a.experts; e += kRowsThreads) t.offsets[e] = a.offsets[e];
     __syncthreads();
-    int parts[kEach], sum = 0, rows = 32;
+    int rows[kEach], most_rows = 0;
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
         const int e = tid * kEach + j;
-        parts[j] = 0;
+        rows[j] = 0;
         if (e < a.experts) {
             const Run r = run_of(t.offsets, e, a.rows);
-            const int step = part_rows(r.hi - r.lo);
-            parts[j] = (r.hi - r.lo + step - 1) / step;
-            rows = max(rows, min(step, (r.hi - r.lo + 31) & ~31));
+            rows[j] = r.hi - r.lo;
         }
-        sum += parts[j];
+        most_rows = max(most_rows, rows[j]);
     }
-    rows = __reduce_max_sync(0xFFFFFFFFu, rows);
+    auto parts_of = [&](int rows, int shift) { return (rows + (1 << shift) - 1) >> shift; };
+    // parts for each size of them, and the most rows of an expert
+#pragma unroll
+    for (int c = 0; c < kSizes; ++c) {
+        int sum = 0;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) sum += parts_of(rows[j], kLargest - c);
+        sum = __reduce_add_sync(0xFFFFFFFFu, sum);
+        if (lane == 0) scan[c * kWarps + warp] = sum;
+    }
+    most_rows = __reduce_max_sync(0xFFFFFFFFu, most_rows);
+    if (lane == 0) scan[kSizes * kWarps + warp] = most_rows;
+    __syncthreads();
+    static_assert(kWarps <= 32, "a lane a warp");
+    auto of_warp = [&](int i) { return lane < kWarps ? scan[i * kWarps + lane] : 0; };
+    most_rows = __reduce_max_sync(0xFFFFFFFFu, of_warp(kSizes));
+    int best = 0x7FFFFFFF;
+#pragma unroll
+    for (int c = 0; c < kSizes; ++c) {
+        const int parts = __reduce_add_sync(0xFFFFFFFFu, of_warp(c));
+        const int n = max(32, min(1 << (kLargest - c), (most_rows + 31) & ~31));
+        const int ns = launch_ns(a, parts, n, epi_ns);
+        if (ns < best) best = ns, t.shift = kLargest - c, most = n;
+    }
+    const int before_warp = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? of_warp(kLargest - t.shift) : 0);
+    int parts[kEach], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) parts[j] = parts_of(rows[j], t.shift), sum += parts[j];
     int incl = sum;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
         const int u = __shfl_up_sync(0xFFFFFFFFu, incl, d);
         if (lane >= d) incl += u;
     }
-    constexpr int kWarps = kRowsThreads / 32;
-    if (lane == 31) scan[warp] = incl, scan[kWarps + warp] = rows;
-    __syncthreads();
-    int before = incl - sum;
-    most = 32;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        before += w < warp ? scan[w] : 0;
-        most = max(most, scan[kWarps + w]);
-    }
+    int before = before_warp + incl - sum;
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
         const int e = tid * kEach + j;
@@ -218,14 +247,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t s_tmem_base;
     __shared__ volatile int s_abort;
-    __shared__ int s_scan[2 * kRowsThreads / 32];
+    __shared__ int s_scan[5 * kRowsThreads / 32];
 
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
     const uint32_t turn = sbase + kRowsRing;
     const uint32_t bars = turn + kEpiGroups * kTurnBytes;
     int *const words = reinterpret_cast<int *>(smem_raw + (bars + kRowsBars - raw));
-    const Table table = {words, words + kMaxExperts + 4, reinterpret_cast<uint16_t *>(words + 2 * (kMaxExperts + 4))};
+    Table table = {words, words + kMaxExperts + 4, reinterpret_cast<uint16_t *>(words + 2 * (kMaxExperts + 4)), 0};
     auto full_bar = [&](int s) { return bars + 8u * s; };  // leader's are used
     auto empty_bar = [&](int s) { return bars + 8u * (kRowsStages + s); };
     auto tfull_bar = [&](int t) { return bars + 8u * (2 * kRowsStages + t); };
@@ -255,7 +284,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
     }
     if (!args.chained) asm volatile("griddepcontrol.wait;" ::: "memory");
     int most;
-    const int parts = make_table(args, table, s_scan, most);
+    constexpr int kEpiNs = EPI == kEpiLinear ? 800 : EPI == kEpiGated ? 1200 : 2200;
+    const int parts = make_table(args, table, kEpiNs, s_scan, most);
     const uint32_t stage = kWBytes + (uint32_t)(most / 2) * kRowBytes;
     const int S = min(kRowsStages, (int)(kRowsRing / stage));
     ptx::tc_fence_before();
