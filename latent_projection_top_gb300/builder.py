@@ -106,7 +106,8 @@ def _build_call_module(force: bool) -> None:
         if module is None:
             raise RuntimeError("torch is not installed")
         if force or _stale(module, [CALL_SOURCE, os.path.join(INCLUDE, "route.h"),
-                                    os.path.join(INCLUDE, "route_layer.h"), os.path.abspath(__file__)]):
+                                    os.path.join(INCLUDE, "route_layer.h"),
+                                    os.path.join(INCLUDE, "route_experts.h"), os.path.abspath(__file__)]):
             _compile_call_module()
     except Exception as e:  # the library and the binding work without it
         warnings.warn(f"the layer operators' calls will go through ctypes (2 to 5 us more each): {e}")

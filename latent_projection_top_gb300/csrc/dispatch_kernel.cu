@@ -9,7 +9,8 @@ namespace {
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortMaxCtas = 8;  // of the cluster
+constexpr int kSortMaxCtas = 16;  // of the cluster
+constexpr int kSortAhead = 8;     // groups of 32 pairs whose ids are on the way together
 
 // ---- sort -------------------------------------------------------------------------
 //
@@ -18,7 +19,7 @@ constexpr int kSortMaxCtas = 8;  // of the cluster
 // over the warps before it, the CTAs before its own (distributed shared memory)
 // and the experts before each, it goes through its run once more and gives
 // each pair its place: the order within an expert is that of the pairs.
-__global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ SortArgs a, int warps) {
+__global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_constant__ SortArgs a, int warps) {
     extern __shared__ int smem[];
     int *counts = smem;                          // [warps][experts]
     int *total = smem + warps * a.experts;       // [experts], read by the cluster
@@ -35,18 +36,37 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
     const long long from = (long long)(rank * warps + warp) * run;
     const int p0 = warp < warps ? (int)(from < pairs ? from : pairs) : pairs;
     const int p1 = (long long)p0 + run < pairs ? p0 + run : pairs;
-    for (int i = tid; i < warps * E; i += kSortThreads) counts[i] = 0;
-    __syncthreads();
+    // the first ids are on their way while the counts are cleared
     auto key_of = [&](int p) {
         if (p >= p1) return -1;
-        const int r = p / a.topk;
-        const int id = a.ids[(long long)r * a.ld_ids + (p - r * a.topk)];
+        int id;
+        if (a.ld_ids == a.topk) {
+            id = a.ids[p];
+        } else {
+            const int r = p / a.topk;
+            id = a.ids[(long long)r * a.ld_ids + (p - r * a.topk)];
+        }
         const int k = (int)((unsigned)id - (unsigned)a.first);
         return id >= a.first && k < E ? k : -1;
     };
-    for (int p = p0; p < p1; p += 32) {
-        const int k = key_of(p + lane);
-        if (k >= 0) atomicAdd(&counts[warp * E + k], 1);
+    int keys[kSortAhead];
+    auto fetch = [&](int p) {
+#pragma unroll
+        for (int j = 0; j < kSortAhead; ++j) keys[j] = key_of(p + 32 * j + lane);
+    };
+    fetch(p0);
+    for (int i = 4 * tid; i < warps * E; i += 4 * kSortThreads) {
+        if (i + 4 <= warps * E)
+            *reinterpret_cast<int4 *>(counts + i) = make_int4(0, 0, 0, 0);
+        else
+            for (int j = i; j < warps * E; ++j) counts[j] = 0;
+    }
+    __syncthreads();
+    for (int p = p0; p < p1; p += 32 * kSortAhead) {
+        if (p > p0) fetch(p);
+#pragma unroll
+        for (int j = 0; j < kSortAhead; ++j)
+            if (keys[j] >= 0) atomicAdd(&counts[warp * E + keys[j]], 1);
     }
     __syncthreads();
     // counts become what the CTA's warps before hold; totals of the CTA
@@ -105,16 +125,22 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
         }
     }
     __syncthreads();
-    for (int p = p0; p < p1; p += 32) {
-        const int k = key_of(p + lane);
-        const unsigned same = __match_any_sync(0xFFFFFFFFu, k);
-        const int at = k >= 0 ? base[k] + counts[warp * E + k] + __popc(same & ((1u << lane) - 1u)) : -1;
-        __syncwarp();
-        if (k >= 0 && (same >> lane) == 1u) counts[warp * E + k] += __popc(same);  // the last of them
-        __syncwarp();
-        if (p + lane < p1) {
-            a.place[p + lane] = at;
-            if (k >= 0 && a.source != nullptr) a.source[at] = p + lane;
+    const bool once = p0 + 32 * kSortAhead >= p1;  // the run's keys are still at hand
+    for (int p = p0; p < p1; p += 32 * kSortAhead) {
+        if (!once) fetch(p);
+#pragma unroll
+        for (int j = 0; j < kSortAhead; ++j) {
+            const int at0 = p + 32 * j, k = keys[j];
+            if (at0 >= p1) break;
+            const unsigned same = __match_any_sync(0xFFFFFFFFu, k);
+            const int at = k >= 0 ? base[k] + counts[warp * E + k] + __popc(same & ((1u << lane) - 1u)) : -1;
+            __syncwarp();
+            if (k >= 0 && (same >> lane) == 1u) counts[warp * E + k] += __popc(same);  // the last of them
+            __syncwarp();
+            if (at0 + lane < p1) {
+                a.place[at0 + lane] = at;
+                if (k >= 0 && a.source != nullptr) a.source[at] = at0 + lane;
+            }
         }
     }
     if (ctas > 1) ptx::cluster_wait();  // nobody leaves while another may read its totals
@@ -339,8 +365,10 @@ size_t sort_smem(int warps, int experts) { return ((size_t)warps + 2) * experts 
 }  // namespace
 
 cudaError_t sort_configure() {
-    return cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)sort_smem(kSortWarps, kMaxExperts));
+    const cudaError_t e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)sort_smem(kSortWarps, kMaxExperts));
+    // sixteen CTAs a cluster
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
 cudaError_t sort_launch(const SortArgs &args, cudaStream_t stream) {
@@ -348,7 +376,7 @@ cudaError_t sort_launch(const SortArgs &args, cudaStream_t stream) {
     const long long groups = (pairs + 31) / 32;
     int warps = groups < kSortWarps ? (int)(groups < 1 ? 1 : groups) : kSortWarps;
     unsigned ctas = 1;
-    while (ctas < kSortMaxCtas && groups > 4ll * ctas * kSortWarps) ctas *= 2;
+    while (ctas < kSortMaxCtas && groups > 2ll * ctas * kSortWarps) ctas *= 2;
     void *params[] = {const_cast<SortArgs *>(&args), &warps};
     return launch(reinterpret_cast<const void *>(sort_kernel), ctas, kSortThreads, sort_smem(warps, args.experts),
                   ctas, params, stream);

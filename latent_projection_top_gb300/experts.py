@@ -23,9 +23,10 @@ import ctypes
 
 import latent_projection_top_gb300 as _route
 
+from . import layer as _layer
 from .layer import (
     _MAT, _act_code, _c_int, _call, _i32, _i64, _LayerPlan, _mat, _opt_mat, _refuse, _rows,
-    _saved, _stream, _type_code, _vp)
+    _saved, _stream, _taken, _type_code, _vp)
 
 MAX_EXPERTS = 1024
 MAX_TOPK = 32
@@ -73,7 +74,7 @@ class DispatchPlan(_LayerPlan):
                  topk: int = _route.TOPK, first: int = 0, device: int = 0):
         super().__init__("route_dispatch_prepare", rows, dtype, device, _c_int(dim),
                          _type_code(dtype), _c_int(experts), _c_int(first), _c_int(topk),
-                         widths=(int(dim), 0, 0))
+                         widths=(int(dim), 0, 0), routed=(int(experts), int(topk)))
         self.dim, self.experts, self.topk, self.first = int(dim), int(experts), int(topk), int(first)
 
 
@@ -86,7 +87,7 @@ class ExpertsPlan(_LayerPlan):
                  train: bool = False, device: int = 0):
         super().__init__("route_experts_prepare", rows, dtype, device, _c_int(k), _c_int(f), _c_int(n),
                          _c_int(experts), _type_code(dtype), _act_code(act), int(train),
-                         widths=(int(k), int(f), int(n)))
+                         widths=(int(k), int(f), int(n)), routed=(int(experts), 0))
         self.k, self.f, self.n, self.experts = int(k), int(f), int(n), int(experts)
         self.act, self.train = act, bool(train)
 
@@ -184,6 +185,9 @@ def dispatch_sort(plan: DispatchPlan, ids, offsets, place, source=None, stream=N
     """`ids` [rows, topk] int32: `offsets` [experts + 1] receives where each
     expert's run begins, `place` [rows, topk] each pair's place (-1: not here),
     `source` [rows * topk] the pair at each place."""
+    if stream is None and plan._plain is not None and _taken(_layer._short.dispatch_sort(
+            plan._plain, ids, offsets, place, source, _layer._current_stream(plan.device))):
+        return
     if _INT32 is None:
         _types()
     R, dev = _rows(ids, "ids"), plan.device
@@ -195,6 +199,9 @@ def dispatch_sort(plan: DispatchPlan, ids, offsets, place, source=None, stream=N
 
 def dispatch_gather(plan: DispatchPlan, x, place, out, stream=None) -> None:
     """``out[place[r, j]] = x[r]``."""
+    if stream is None and plan._plain is not None and _taken(_layer._short.dispatch_gather(
+            plan._plain, x, place, out, _layer._current_stream(plan.device))):
+        return
     R, P, d, dev, dt = _rows(x, "x"), _rows(out, "out"), plan.dim, plan.device, plan.dtype
     _call("route_dispatch_gather", plan, R, *_mat(x, "x", R, d, dt, dev),
           _ints(place, "place", (R, plan.topk), dev), _c_int(P), *_mat(out, "out", P, d, dt, dev),
@@ -203,6 +210,9 @@ def dispatch_gather(plan: DispatchPlan, x, place, out, stream=None) -> None:
 
 def dispatch_gather_backward(plan: DispatchPlan, dout, place, dx, stream=None) -> None:
     """``dx[r] = sum over j of dout[place[r, j]]``."""
+    if stream is None and plan._plain is not None and _taken(_layer._short.dispatch_gather_backward(
+            plan._plain, dout, place, dx, _layer._current_stream(plan.device))):
+        return
     R, P, d, dev, dt = _rows(dx, "dx"), _rows(dout, "dout"), plan.dim, plan.device, plan.dtype
     _call("route_dispatch_gather_backward", plan, R, *_mat(dout, "dout", P, d, dt, dev), _c_int(P),
           _ints(place, "place", (R, plan.topk), dev), *_mat(dx, "dx", R, d, dt, dev),
@@ -212,6 +222,9 @@ def dispatch_gather_backward(plan: DispatchPlan, dout, place, dx, stream=None) -
 def dispatch_combine(plan: DispatchPlan, y, place, weights, out, residual=None, stream=None) -> None:
     """``out[r] = sum over j of weights[r, j] y[place[r, j]] + residual[r]``;
     weights [rows, topk] FP32 may be None (1)."""
+    if stream is None and plan._plain is not None and _taken(_layer._short.dispatch_combine(
+            plan._plain, y, place, weights, out, residual, _layer._current_stream(plan.device))):
+        return
     R, P, d, dev, dt = _rows(out, "out"), _rows(y, "y"), plan.dim, plan.device, plan.dtype
     _call("route_dispatch_combine", plan, R, *_mat(y, "y", P, d, dt, dev), _c_int(P),
           _ints(place, "place", (R, plan.topk), dev),
@@ -224,6 +237,9 @@ def dispatch_combine_backward(plan: DispatchPlan, dout, y, place, weights, dy=No
                               stream=None) -> None:
     """``dy[place[r, j]] = weights[r, j] dout[r]``, ``dweights[r, j] =
     <dout[r], y[place[r, j]]>``.  y may be None without dweights."""
+    if stream is None and plan._plain is not None and _taken(_layer._short.dispatch_combine_backward(
+            plan._plain, dout, y, place, weights, dy, dweights, _layer._current_stream(plan.device))):
+        return
     R, d, dev, dt = _rows(dout, "dout"), plan.dim, plan.device, plan.dtype
     P = _rows(y, "y") if y is not None else _rows(dy, "dy") if dy is not None else 0
     if dweights is not None and y is None:
@@ -238,6 +254,9 @@ def experts_forward(plan: ExpertsPlan, x, offsets, W_gate, W_up, W_down, out, sa
                     stream=None) -> None:
     """`x` [rows, k] sorted by expert, `offsets` [experts + 1] int32: rows that
     are nobody's are not written in `out` [rows, n]."""
+    if stream is None and plan._plain is not None and _taken(_layer._short.experts_forward(
+            plan._plain, x, offsets, W_gate, W_up, W_down, out, saved, _layer._current_stream(plan.device))):
+        return
     R, k, f, n, dev, dt = _rows(x, "x"), plan.k, plan.f, plan.n, plan.device, plan.dtype
     E = plan.experts
     _call("route_experts_forward", plan, R, *_mat(x, "x", R, k, dt, dev),
@@ -249,6 +268,9 @@ def experts_forward(plan: ExpertsPlan, x, offsets, W_gate, W_up, W_down, out, sa
 def experts_backward(plan: ExpertsPlan, dout, x, offsets, W_gate, W_up, W_down, saved, dx=None,
                      dW_gate=None, dW_up=None, dW_down=None, stream=None) -> None:
     """Any of the gradients; those of an expert's weights without rows are 0."""
+    if stream is None and plan._plain is not None and _taken(_layer._short.experts_backward(
+            plan._plain, dout, x, offsets, W_gate, W_up, W_down, saved, dx, dW_gate, dW_up, dW_down, _layer._current_stream(plan.device))):
+        return
     R, k, f, n, dev, dt = _rows(dout, "dout"), plan.k, plan.f, plan.n, plan.device, plan.dtype
     E = plan.experts
     _call("route_experts_backward", plan, R, *_mat(dout, "dout", R, n, dt, dev),
@@ -267,6 +289,9 @@ def dropout_forward(plan: DropoutPlan, x, p: float, seed: int, out, offset: int 
     ``plan.draws(rows)`` apart have lots of their own.  `step`, an int64 tensor
     of one value on the device, is added to the offset when the kernel runs
     (for captured calls)."""
+    if stream is None and plan._plain is not None and _taken(_layer._short.dropout_forward(
+            plan._plain, x, p, seed, out, offset, residual, step, _layer._current_stream(plan.device))):
+        return
     R, d, dev, dt = _rows(x, "x"), plan.dim, plan.device, plan.dtype
     _call("route_dropout_forward", plan, R, *_mat(x, "x", R, d, dt, dev), p, _c_u64(seed, "seed"),
           _c_u64(offset, "offset"), _step(step, dev), *_opt_mat(residual, "residual", R, d, dt, dev),
@@ -277,6 +302,9 @@ def dropout_backward(plan: DropoutPlan, dout, p: float, seed: int, dx, offset: i
                      stream=None) -> None:
     """``dx = keep * dout / (1 - p)`` with the lots of the forward call of the
     same seed, offset and step."""
+    if stream is None and plan._plain is not None and _taken(_layer._short.dropout_backward(
+            plan._plain, dout, p, seed, dx, offset, step, _layer._current_stream(plan.device))):
+        return
     R, d, dev, dt = _rows(dout, "dout"), plan.dim, plan.device, plan.dtype
     _call("route_dropout_backward", plan, R, *_mat(dout, "dout", R, d, dt, dev), p,
           _c_u64(seed, "seed"), _c_u64(offset, "offset"), _step(step, dev),

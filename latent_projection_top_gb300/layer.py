@@ -121,7 +121,9 @@ def _short_way():
             return None
         module.bind(*(ctypes.cast(getattr(L, f"route_{name}"), _vp).value for name in (
             "norm_forward", "norm_backward", "linear_forward", "linear_backward",
-            "gated_forward", "gated_backward")))
+            "gated_forward", "gated_backward", "dispatch_sort", "dispatch_gather",
+            "dispatch_gather_backward", "dispatch_combine", "dispatch_combine_backward",
+            "experts_forward", "experts_backward", "dropout_forward", "dropout_backward")))
         _short = module
     return _short
 
@@ -130,7 +132,7 @@ class _LayerPlan:
     """A prepared layer operator; a context manager, or call ``close()``."""
 
     def __init__(self, prepare: str, rows: int, dtype, device: int, *args, out_dtype=None,
-                 widths: tuple):
+                 widths: tuple, routed: tuple = ()):
         self._h = None
         h = ctypes.c_void_p()
         _route._check(getattr(_route.lib(), prepare)(_c_int(rows), *args, _c_int(device),
@@ -145,7 +147,7 @@ class _LayerPlan:
         # the plan as the short way takes it; None once closed, or without the module
         self._plain = None if _short_way() is None else (
             self._p, self.device, _type_code(dtype),
-            _type_code(dtype if out_dtype is None else out_dtype), *widths, self.saved_row)
+            _type_code(dtype if out_dtype is None else out_dtype), *widths, self.saved_row, *routed)
 
     @property
     def handle(self) -> ctypes.c_void_p:
