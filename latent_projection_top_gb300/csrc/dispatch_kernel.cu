@@ -73,10 +73,15 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
     const int e = tid;
     int mine = 0;
     if (e < E) {
-        for (int w = 0; w < warps; ++w) {
-            const int c = counts[w * E + e];
-            counts[w * E + e] = mine;
-            mine += c;
+        for (int w0 = 0; w0 < warps; w0 += 8) {  // eight loads on the way together
+            int c[8];
+#pragma unroll
+            for (int w = 0; w < 8; ++w) c[w] = w0 + w < warps ? counts[(w0 + w) * E + e] : 0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                if (w0 + w < warps) counts[(w0 + w) * E + e] = mine;
+                mine += c[w];
+            }
         }
         total[e] = mine;
     }
@@ -84,16 +89,21 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
     if (ctas > 1) {
         ptx::cluster_sync();
         if (e < E) {
+            int c[kSortMaxCtas];
+#pragma unroll
+            for (int j = 0; j < kSortMaxCtas; ++j)
+                if (j < ctas)
+                    asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                                 : "=r"(c[j])
+                                 : "r"(ptx::map_to_rank(ptx::smem_addr(total + e), (uint32_t)j))
+                                 : "memory");
             all = 0;
-            for (int j = 0; j < ctas; ++j) {
-                int c;
-                asm volatile("ld.shared::cluster.s32 %0, [%1];"
-                             : "=r"(c)
-                             : "r"(ptx::map_to_rank(ptx::smem_addr(total + e), (uint32_t)j))
-                             : "memory");
-                if (j < rank) before += c;
-                all += c;
-            }
+#pragma unroll
+            for (int j = 0; j < kSortMaxCtas; ++j)
+                if (j < ctas) {
+                    if (j < rank) before += c[j];
+                    all += c[j];
+                }
         }
         ptx::cluster_arrive();  // after the last remote read
     }
@@ -252,71 +262,98 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Mo
     const int r = blockIdx.x;
     find_places(a, r, s);
     const int n = s.n, pieces = a.dim / P::kN;
-    for (int i = threadIdx.x; i < pieces; i += blockDim.x) {
-        const long long c = (long long)i * P::kN;
-        float sum[P::kN] = {};
-        P res;
-        if (a.a != nullptr) res.load(a.a, r * a.ld_a + c);
-        for (int k0 = 0; k0 < n; k0 += kAhead) {
-            P p[kAhead];
+    // single values: four a thread at a time, so that as much is on the way
+    constexpr int kPieces = VEC ? 1 : 4, kRows = VEC ? kAhead : 4;
+    for (int i0 = threadIdx.x; i0 < pieces; i0 += kPieces * blockDim.x) {
+        float sum[kPieces][P::kN] = {};
+        P res[kPieces];
+        auto each = [&](auto &&f) {
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (k0 + k < n) p[k].load(a.b, s.at[k0 + k] * a.ld_b + c);
+            for (int q = 0; q < kPieces; ++q) {
+                const int i = i0 + q * (int)blockDim.x;
+                if (kPieces == 1 || i < pieces) f(q, (long long)i * P::kN);
+            }
+        };
+        if (a.a != nullptr) each([&](int q, long long c) { res[q].load(a.a, r * a.ld_a + c); });
+        for (int k0 = 0; k0 < n; k0 += kRows) {
+            P p[kPieces][kRows];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k)
+            for (int k = 0; k < kRows; ++k)
+                if (k0 + k < n) each([&](int q, long long c) { p[q][k].load(a.b, s.at[k0 + k] * a.ld_b + c); });
+#pragma unroll
+            for (int k = 0; k < kRows; ++k)
                 if (k0 + k < n) {
-                    float v[P::kN];
-                    p[k].values(v);
                     const float w = s.w[k0 + k];
+                    each([&](int q, long long) {
+                        float v[P::kN];
+                        p[q][k].values(v);
 #pragma unroll
-                    for (int e = 0; e < P::kN; ++e) sum[e] = a.weights != nullptr ? fmaf(w, v[e], sum[e]) : sum[e] + v[e];
+                        for (int e = 0; e < P::kN; ++e)
+                            sum[q][e] = a.weights != nullptr ? fmaf(w, v[e], sum[q][e]) : sum[q][e] + v[e];
+                    });
                 }
         }
-        if (a.a != nullptr) {
-            float v[P::kN];
-            res.values(v);
+        each([&](int q, long long c) {
+            if (a.a != nullptr) {
+                float v[P::kN];
+                res[q].values(v);
 #pragma unroll
-            for (int e = 0; e < P::kN; ++e) sum[e] += v[e];
-        }
-        P o;
-        o.set(sum);
-        o.store(a.out, r * a.ld_out + c);
+                for (int e = 0; e < P::kN; ++e) sum[q][e] += v[e];
+            }
+            P o;
+            o.set(sum[q]);
+            o.store(a.out, r * a.ld_out + c);
+        });
     }
 }
 
-// A block a row, a warp an expert's row at a time: out[place_j] = w_j dout[row],
-// dweights_j = <dout[row], b[place_j]>.
+// A block a row, `share` warps an expert's row at a time (all of the block's
+// where there are few): out[place_j] = w_j dout[row], dweights_j = <dout[row],
+// b[place_j]>.
+constexpr int kBackWarps = 8;
 template <int TY, bool VEC>
-__global__ void __launch_bounds__(256) combine_backward_kernel(const __grid_constant__ MoveArgs a) {
+__global__ void __launch_bounds__(32 * kBackWarps) combine_backward_kernel(const __grid_constant__ MoveArgs a) {
     using P = Piece<TY, VEC>;
+    constexpr int kPieces = VEC ? 2 : 8;  // on the way together
     __shared__ Places s;
+    __shared__ float s_dot[kMaxTopk][kBackWarps];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int r = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     find_places(a, r, s);
     const int n = s.n, pieces = a.dim / P::kN;
-    for (int k = warp; k < n; k += blockDim.x >> 5) {
+    const int share = n <= 1 ? 8 : n <= 2 ? 4 : n <= 4 ? 2 : 1;
+    const int part = warp & (share - 1);
+    for (int k = warp / share; k < n; k += kBackWarps / share) {
         const float w = s.w[k];
+        const long long ia = r * a.ld_a, ib = s.at[k] * a.ld_b, io = s.at[k] * a.ld_out;
         float dot[P::kN] = {};
-#pragma unroll 2
-        for (int i = lane; i < pieces; i += 32) {
-            const long long c = (long long)i * P::kN;
-            P g;
-            g.load(a.a, r * a.ld_a + c);
-            float gv[P::kN], v[P::kN];
-            g.values(gv);
-            if (a.dweights != nullptr) {
-                P y;
-                y.load(a.b, s.at[k] * a.ld_b + c);
-                y.values(v);
+        for (int i = part * 32 + lane; i < pieces; i += share * 32 * kPieces) {
+            P g[kPieces], y[kPieces];
 #pragma unroll
-                for (int e = 0; e < P::kN; ++e) dot[e] = fmaf(gv[e], v[e], dot[e]);
+            for (int q = 0; q < kPieces; ++q) {
+                const int at = i + q * share * 32;
+                if (at >= pieces) break;
+                g[q].load(a.a, ia + (long long)at * P::kN);
+                if (a.dweights != nullptr) y[q].load(a.b, ib + (long long)at * P::kN);
             }
-            if (a.out != nullptr) {
 #pragma unroll
-                for (int e = 0; e < P::kN; ++e) v[e] = w * gv[e];
-                P o;
-                o.set(v);
-                o.store(a.out, s.at[k] * a.ld_out + c);
+            for (int q = 0; q < kPieces; ++q) {
+                const int at = i + q * share * 32;
+                if (at >= pieces) break;
+                float gv[P::kN], v[P::kN];
+                g[q].values(gv);
+                if (a.dweights != nullptr) {
+                    y[q].values(v);
+#pragma unroll
+                    for (int e = 0; e < P::kN; ++e) dot[e] = fmaf(gv[e], v[e], dot[e]);
+                }
+                if (a.out != nullptr) {
+#pragma unroll
+                    for (int e = 0; e < P::kN; ++e) v[e] = w * gv[e];
+                    P o;
+                    o.set(v);
+                    o.store(a.out, io + (long long)at * P::kN);
+                }
             }
         }
         float t = 0.f;
@@ -324,7 +361,14 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const __grid_cons
         for (int e = 0; e < P::kN; ++e) t += dot[e];
 #pragma unroll
         for (int d = 16; d > 0; d /= 2) t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
-        if (lane == 0 && a.dweights != nullptr) a.dweights[(long long)r * a.topk + s.j[k]] = t;
+        if (lane == 0) s_dot[k][part] = t;
+    }
+    if (a.dweights == nullptr) return;
+    __syncthreads();
+    if (threadIdx.x < n) {
+        float t = 0.f;
+        for (int j = 0; j < share; ++j) t += s_dot[threadIdx.x][j];
+        a.dweights[(long long)r * a.topk + s.j[threadIdx.x]] = t;
     }
 }
 
@@ -402,7 +446,7 @@ cudaError_t combine_backward_launch(const MoveArgs &args, cudaStream_t stream) {
     const void *k = vectors(args) ? ROUTE_MOVE(combine_backward_kernel, args, true)
                                   : ROUTE_MOVE(combine_backward_kernel, args, false);
     void *params[] = {const_cast<MoveArgs *>(&args)};
-    return launch(k, (unsigned)args.rows, 256, 0, 1, params, stream);
+    return launch(k, (unsigned)args.rows, 32 * kBackWarps, 0, 1, params, stream);
 }
 
 }  // namespace route

@@ -5,6 +5,8 @@
 // easy as 1, 2, 3", SC 2011) makes of it: 16 bits, a lot, for each.  A value
 // is dropped if its lot is below the threshold.  Nothing but the seed and the
 // offset is kept: the backward pass draws the same lots.
+#include <type_traits>
+
 #include "experts.cuh"
 #include "layer_math.cuh"
 
@@ -144,21 +146,28 @@ __global__ void __launch_bounds__(256) dropout_any_kernel(const __grid_constant_
         uint32_t keep = 0u;  // bit e: the lane's eight neighbours' e-th
 #pragma unroll
         for (int e = 0; e < 8; ++e) keep |= ((e % 2 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu) >= a.threshold ? 1u : 0u) << e;
-        float v[8], res[8];
+        const long long at = c + lane, ix = r * a.ld_x + at, ir = r * a.ld_res + at, io = r * a.ld_out + at;
+        auto take = [&](auto all_there) {
+            constexpr bool whole = decltype(all_there)::value;
+            float v[8], res[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int k = c + 32 * j + lane;
-            v[j] = k < a.dim ? load_elem(a.x, TY, r * a.ld_x + k) : 0.f;
-            res[j] = k < a.dim && a.residual != nullptr ? load_elem(a.residual, TY, r * a.ld_res + k) : 0.f;
-        }
+            for (int j = 0; j < 8; ++j) {
+                const bool there = whole || at + 32 * j < a.dim;
+                v[j] = there ? load_elem(a.x, TY, ix + 32 * j) : 0.f;
+                res[j] = there && a.residual != nullptr ? load_elem(a.residual, TY, ir + 32 * j) : 0.f;
+            }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int k = c + 32 * j + lane;
-            const bool on = (__shfl_sync(0xFFFFFFFFu, keep, 4 * j + (lane >> 3)) >> (lane & 7)) & 1u;
-            v[j] = on ? v[j] * a.scale : 0.f;
-            if (a.residual != nullptr) v[j] += res[j];
-            if (k < a.dim) store_elem(a.out, TY, r * a.ld_out + k, v[j]);
-        }
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t of = __shfl_sync(0xFFFFFFFFu, keep, 4 * j + (lane >> 3));
+                v[j] = (of >> (lane & 7)) & 1u ? v[j] * a.scale : 0.f;
+                if (a.residual != nullptr) v[j] += res[j];
+                if (whole || at + 32 * j < a.dim) store_elem(a.out, TY, io + 32 * j, v[j]);
+            }
+        };
+        if (c + 256 <= a.dim)
+            take(std::true_type{});
+        else
+            take(std::false_type{});
     }
 }
 
