@@ -8,7 +8,11 @@ namespace route {
 namespace {
 
 constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
+// Warps that go through the pairs: sixteen cost less to set up (8192 pairs 6.1
+// us, thirty-two 7.9; 65536 11.4 and 12.1), thirty-two go through many faster
+// (1048576 pairs 90 us, 97).
+constexpr int kSortWarps = 16, kSortMoreWarps = 32;
+constexpr int kSortMorePairs = 1 << 18;
 constexpr int kSortMaxCtas = 16;  // of the cluster
 constexpr int kSortAhead = 8;     // groups of 32 pairs whose ids are on the way together
 
@@ -24,8 +28,11 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
     int *counts = smem;                          // [warps][experts]
     int *total = smem + warps * a.experts;       // [experts], read by the cluster
     int *base = total + a.experts;               // [experts]
-    __shared__ int s_scan[kSortWarps];
+    __shared__ int s_scan[kSortThreads / 32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // after the wait: only the offsets and places are still to come, which no
+    // kernel reads ahead of its own
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ctas = gridDim.x, rank = blockIdx.x;
     const int E = a.experts;
@@ -410,17 +417,34 @@ size_t sort_smem(int warps, int experts) { return ((size_t)warps + 2) * experts 
 
 cudaError_t sort_configure() {
     const cudaError_t e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)sort_smem(kSortWarps, kMaxExperts));
+                                               (int)sort_smem(kSortMoreWarps, kMaxExperts));
     // sixteen CTAs a cluster
     return e != cudaSuccess ? e : cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
-cudaError_t sort_launch(const SortArgs &args, cudaStream_t stream) {
+int sort_max_ctas() {
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kSortMaxCtas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    c.gridDim = dim3(kSortMaxCtas);
+    c.blockDim = dim3(kSortThreads);
+    c.dynamicSmemBytes = sort_smem(kSortMoreWarps, kMaxExperts);
+    c.attrs = attr;
+    c.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, sort_kernel, &c) != cudaSuccess) cudaGetLastError(), clusters = 0;
+    return clusters > 0 ? kSortMaxCtas : 8;
+}
+
+cudaError_t sort_launch(const SortArgs &args, int max_ctas, cudaStream_t stream) {
     const long long pairs = (long long)args.rows * args.topk;
     const long long groups = (pairs + 31) / 32;
-    int warps = groups < kSortWarps ? (int)(groups < 1 ? 1 : groups) : kSortWarps;
+    const int most = pairs < kSortMorePairs ? kSortWarps : kSortMoreWarps;
+    int warps = groups < most ? (int)(groups < 1 ? 1 : groups) : most;
     unsigned ctas = 1;
-    while (ctas < kSortMaxCtas && groups > 2ll * ctas * kSortWarps) ctas *= 2;
+    while (ctas < (unsigned)max_ctas && groups > 2ll * ctas * most) ctas *= 2;
     void *params[] = {const_cast<SortArgs *>(&args), &warps};
     return launch(reinterpret_cast<const void *>(sort_kernel), ctas, kSortThreads, sort_smem(warps, args.experts),
                   ctas, params, stream);

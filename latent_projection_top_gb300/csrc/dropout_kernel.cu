@@ -14,17 +14,29 @@ namespace route {
 namespace {
 
 // The 128 bits of one counter: 64 bits of it are used, the others are 0.
-__device__ __forceinline__ uint4 philox(unsigned long long counter, unsigned long long key) {
+__device__ __forceinline__ uint4 philox(unsigned long long counter, const DropoutArgs &a) {
     uint4 c = make_uint4((uint32_t)counter, (uint32_t)(counter >> 32), 0u, 0u);
-    uint32_t k0 = (uint32_t)key, k1 = (uint32_t)(key >> 32);
 #pragma unroll
-    for (int r = 0; r < 10; ++r) {
+    for (int r = 0; r < kPhiloxRounds; ++r) {
         const unsigned long long p0 = 0xD2511F53ull * c.x, p1 = 0xCD9E8D57ull * c.z;
-        c = make_uint4((uint32_t)(p1 >> 32) ^ c.y ^ k0, (uint32_t)p1, (uint32_t)(p0 >> 32) ^ c.w ^ k1, (uint32_t)p0);
-        k0 += 0x9E3779B9u, k1 += 0xBB67AE85u;
+        c = make_uint4((uint32_t)(p1 >> 32) ^ c.y ^ a.keys[2 * r], (uint32_t)p1,
+                       (uint32_t)(p0 >> 32) ^ c.w ^ a.keys[2 * r + 1], (uint32_t)p0);
     }
     return c;
 }
+
+// The comparison of the e-th of a counter's lots with the threshold: both in
+// the upper half of a word, so that an odd one needs no shift.
+struct Lots {
+    uint32_t least;
+    bool none;  // a threshold that no lot reaches
+    __device__ __forceinline__ explicit Lots(const DropoutArgs &a)
+        : least(a.threshold << 16), none(a.threshold > 0xFFFFu) {}
+    __device__ __forceinline__ bool keep(const uint4 &bits, int e) const {
+        const uint32_t w = e < 2 ? bits.x : e < 4 ? bits.y : e < 6 ? bits.z : bits.w;
+        return (e % 2 ? w : w << 16) >= least && !none;
+    }
+};
 
 // Eight values from element i on, `n` of them there; `vec`: as vectors.
 template <int TY>
@@ -88,44 +100,43 @@ __device__ __forceinline__ void store8(void *p, long long i, int n, bool vec, co
     }
 }
 
-// One of a row's values, as it was dropped or kept.  A dropped value is not
-// multiplied: an infinity or a NaN there is gone.
-__device__ __forceinline__ float kept(float v, uint32_t lot, const DropoutArgs &a) {
-    return lot >= a.threshold ? v * a.scale : 0.f;
-}
-
 __device__ __forceinline__ unsigned long long first_counter(const DropoutArgs &a) {
     return a.offset + (a.step != nullptr ? (unsigned long long)*a.step : 0ull);
 }
 
-// Rows that take 16 bytes at a time: eight values, a counter's, a thread.
-template <int TY>
+// Rows that take 16 bytes at a time: eight values, a counter's, a thread.  FLAT:
+// the rows follow one another in every matrix.  A dropped value is not
+// multiplied: an infinity or a NaN there is gone.
+//
+// Bound by HBM where a residual is added, else by the instructions issued, of
+// which ten rounds are 40 for eight values and half of those at half the rate.
+template <int TY, bool FLAT>
 __global__ void __launch_bounds__(256) dropout_kernel(const __grid_constant__ DropoutArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int groups = (a.dim + 7) >> 3;
+    const unsigned groups = (unsigned)(a.dim + 7) >> 3, all = (unsigned)a.rows * groups;
+    const unsigned step = gridDim.x * blockDim.x;
     const unsigned long long offset = first_counter(a);
-    // a thread's groups are `step` apart: by row and column, without a division each
-    const unsigned step = gridDim.x * blockDim.x, at = blockIdx.x * blockDim.x + threadIdx.x;
-    const int dr = (int)(step / (unsigned)groups), dg = (int)(step - (unsigned)dr * groups);
-    int r = (int)(at / (unsigned)groups), g = (int)(at - (unsigned)r * groups);
-    for (; r < a.rows; r += dr, g += dg) {
-        if (g >= groups) {
-            g -= groups;
-            if (++r >= a.rows) break;
+    const Lots lots(a);
+    for (unsigned i = blockIdx.x * blockDim.x + threadIdx.x; i < all; i += step) {
+        long long x = 8ll * i, res = x, out = x;
+        int n = 8;
+        if (!FLAT) {
+            const unsigned r = i / groups;
+            const int c = (int)(i - r * groups) * 8;
+            n = a.dim - c;
+            x = r * a.ld_x + c, res = r * a.ld_res + c, out = r * a.ld_out + c;
         }
-        const int c = 8 * g, n = a.dim - c;
-        const bool whole = n >= 8;
-        float v[8], res[8];
-        load8<TY>(a.x, r * a.ld_x + c, n, whole, v);
-        if (a.residual != nullptr) load8<TY>(a.residual, r * a.ld_res + c, n, whole, res);
-        const uint4 bits = philox(offset + (unsigned long long)((long long)r * groups + g), a.seed);
-        const uint32_t w[4] = {bits.x, bits.y, bits.z, bits.w};
+        const bool whole = FLAT || n >= 8;
+        float v[8], add[8];
+        load8<TY>(a.x, x, n, whole, v);
+        if (a.residual != nullptr) load8<TY>(a.residual, res, n, whole, add);
+        const uint4 bits = philox(offset + i, a);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = kept(v[e], e % 2 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu, a);
+        for (int e = 0; e < 8; ++e) v[e] = lots.keep(bits, e) ? v[e] * a.scale : 0.f;
         if (a.residual != nullptr)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += res[e];
-        store8<TY>(a.out, r * a.ld_out + c, n, whole, v);
+            for (int e = 0; e < 8; ++e) v[e] += add[e];
+        store8<TY>(a.out, out, n, whole, v);
     }
 }
 
@@ -138,14 +149,14 @@ __global__ void __launch_bounds__(256) dropout_any_kernel(const __grid_constant_
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int groups = (a.dim + 7) >> 3, pieces = (a.dim + 255) >> 8, lane = threadIdx.x & 31;
     const unsigned long long offset = first_counter(a);
+    const Lots lots(a);
     const unsigned all = (unsigned)a.rows * (unsigned)pieces, step = gridDim.x * (blockDim.x >> 5);
     for (unsigned i = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i < all; i += step) {
         const int r = (int)(i / (unsigned)pieces), c = (int)(i - (unsigned)r * pieces) * 256;
-        const uint4 bits = philox(offset + (unsigned long long)((long long)r * groups + c / 8 + lane), a.seed);
-        const uint32_t w[4] = {bits.x, bits.y, bits.z, bits.w};
+        const uint4 bits = philox(offset + (unsigned long long)((long long)r * groups + c / 8 + lane), a);
         uint32_t keep = 0u;  // bit e: the lane's eight neighbours' e-th
 #pragma unroll
-        for (int e = 0; e < 8; ++e) keep |= ((e % 2 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu) >= a.threshold ? 1u : 0u) << e;
+        for (int e = 0; e < 8; ++e) keep |= (lots.keep(bits, e) ? 1u : 0u) << e;
         const long long at = c + lane, ix = r * a.ld_x + at, ir = r * a.ld_res + at, io = r * a.ld_out + at;
         auto take = [&](auto all_there) {
             constexpr bool whole = decltype(all_there)::value;
@@ -192,8 +203,12 @@ cudaError_t dropout_launch(const DropoutArgs &args, int sms, cudaStream_t stream
     c.attrs = attr;
     c.numAttrs = 1;
     void *params[] = {const_cast<DropoutArgs *>(&args)};
-#define ROUTE_DROPOUT(T) \
-    (vec ? reinterpret_cast<const void *>(dropout_kernel<T>) : reinterpret_cast<const void *>(dropout_any_kernel<T>))
+    const bool flat = args.dim % 8 == 0 && args.ld_x == args.dim && args.ld_out == args.dim &&
+                      (args.residual == nullptr || args.ld_res == args.dim);
+#define ROUTE_DROPOUT(T)                                                  \
+    (!vec   ? reinterpret_cast<const void *>(dropout_any_kernel<T>)       \
+     : flat ? reinterpret_cast<const void *>(dropout_kernel<T, true>)     \
+            : reinterpret_cast<const void *>(dropout_kernel<T, false>))
     const void *k = args.type == kBf16   ? ROUTE_DROPOUT(kBf16)
                     : args.type == kFp16 ? ROUTE_DROPOUT(kFp16)
                                          : ROUTE_DROPOUT(kFp32);

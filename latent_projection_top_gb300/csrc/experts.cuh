@@ -21,7 +21,8 @@ struct SortArgs {
     int *source;                // [rows * topk] or null
 };
 cudaError_t sort_configure();
-cudaError_t sort_launch(const SortArgs &args, cudaStream_t stream);
+int sort_max_ctas();  // that fit a cluster of the current device
+cudaError_t sort_launch(const SortArgs &args, int max_ctas, cudaStream_t stream);
 
 // What gather and combine, and their gradients, read and write: rows of `dim`
 // values in the tokens' order (a) and in the experts' order (b).
@@ -103,11 +104,13 @@ cudaError_t experts_grad_launch(const GradMaps &maps, const GradArgs &args, cuda
 
 // ---- dropout ----------------------------------------------------------------------------
 
+constexpr int kPhiloxRounds = 10;
 struct DropoutArgs {
     int rows, dim, type;
     unsigned threshold;         // of 65536: lots below it are dropped
     float scale;                // 65536 / (65536 - threshold)
-    unsigned long long seed, offset;
+    uint32_t keys[2 * kPhiloxRounds];  // each round's
+    unsigned long long offset;
     const long long *step;      // added to the offset; may be null
     const void *x;
     long long ld_x;

@@ -151,7 +151,11 @@ route_status dropout(const route_layer *p, int rows, const char *name, const voi
     a.rows = rows, a.dim = p->k, a.type = p->type;
     a.threshold = (unsigned)std::floor(prob * 65536.0 + 0.5);
     a.scale = a.threshold < 65536u ? (float)(65536.0 / (65536.0 - a.threshold)) : 0.f;
-    a.seed = seed, a.offset = offset;
+    a.offset = offset;
+    for (int r = 0; r < kPhiloxRounds; ++r) {
+        a.keys[2 * r] = (uint32_t)seed + 0x9E3779B9u * (uint32_t)r;
+        a.keys[2 * r + 1] = (uint32_t)(seed >> 32) + 0xBB67AE85u * (uint32_t)r;
+    }
     a.step = reinterpret_cast<const long long *>(step);
     a.x = x, a.ld_x = stride_of(rows, ld_x, p->k);
     a.residual = residual, a.ld_res = stride_of(rows, ld_residual, p->k);
@@ -193,7 +197,7 @@ route_status route_dispatch_sort(const route_layer *p, int rows, const int32_t *
     a.ids = ids, a.ld_ids = stride_of(rows, ld_ids, p->topk);
     a.offsets = offsets, a.place = place, a.source = source;
     DeviceGuard guard(p->device);
-    return launched(sort_launch(a, static_cast<cudaStream_t>(stream)), "sort kernel launch");
+    return launched(sort_launch(a, p->sort_ctas, static_cast<cudaStream_t>(stream)), "sort kernel launch");
 }
 
 route_status route_dispatch_gather(const route_layer *p, int rows, const void *x, int64_t ld_x,
