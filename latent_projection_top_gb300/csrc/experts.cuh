@@ -67,6 +67,7 @@ struct ExpertsArgs {
     // are read at once.
     int chained;
     int pairs;                  // CTA pairs launched
+    float tiles_a_pair;         // tiles_n / pairs
     int test_stall;
     unsigned long long timeout_ns;
     unsigned *status;

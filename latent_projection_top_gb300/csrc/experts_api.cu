@@ -88,6 +88,7 @@ struct Rows {
         a.kswitch = ceil_div(K, 64), a.kblocks = terms * a.kswitch;
         a.fp16 = p->type == kFp16;
         a.pairs = p->pairs;
+        a.tiles_a_pair = (float)a.tiles_n / (float)a.pairs;
         a.test_stall = p->test_stall;
         a.timeout_ns = p->timeout_ns;
         a.status = p->words;

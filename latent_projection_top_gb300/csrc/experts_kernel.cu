@@ -77,10 +77,10 @@ __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, const 
 struct Run {
     int lo, hi;
 };
-__device__ __forceinline__ Run run_of(const int *offsets, int e, int rows) {
+__device__ __forceinline__ Run run_of(int from, int to, int rows) {
     Run r;
-    r.lo = min(max(offsets[e], 0), rows);
-    r.hi = max(min(offsets[e + 1], rows), r.lo);
+    r.lo = min(max(from, 0), rows);
+    r.hi = max(min(to, rows), r.lo);
     return r;
 }
 
@@ -145,7 +145,7 @@ struct RowsWalk {
             }
             x.e = lo;
         }
-        const Run r = run_of(t.offsets, x.e, a.rows);
+        const Run r = run_of(t.offsets[x.e], t.offsets[x.e + 1], a.rows);
         // an expert's parts are equal, in steps of 32 (8192 rows of 3584x2048: 444 us, the
         // last one what is left: 452); none is empty, because a step is no more than the most
         const int parts = (r.hi - r.lo + (1 << t.shift) - 1) >> t.shift;
@@ -161,10 +161,10 @@ struct RowsWalk {
 // tile takes as long as its copies to an SM, 95 bytes a nanosecond, or its MMAs
 // (the same at 256 rows), its epilogue `epi_ns` for 64 rows; the last one is in
 // nobody's shadow.
-__device__ __forceinline__ int launch_ns(const ExpertsArgs &a, int parts, int n, int epi_ns) {
-    const int rounds = (parts * a.tiles_n + a.pairs - 1) / a.pairs;
-    const int load = a.kblocks * (172 + 2 * n / 3), epi = (n + 63) / 64 * epi_ns;
-    return min(rounds, 4096) * min(max(load, epi), 1 << 17) + epi;
+__device__ __forceinline__ float launch_ns(const ExpertsArgs &a, int parts, int n, float epi_ns) {
+    const float rounds = ceilf((float)parts * a.tiles_a_pair);
+    const float load = (float)a.kblocks * (172.f + 0.667f * n), epi = (float)((n + 63) >> 6) * epi_ns;
+    return rounds * fmaxf(load, epi) + epi;
 }
 
 // All threads: the table of parts.  Returns the number of them; `most`: the
@@ -173,22 +173,23 @@ __device__ __forceinline__ int launch_ns(const ExpertsArgs &a, int parts, int n,
 // Parts have up to 256 rows, or, where that leaves too few tiles for the pairs,
 // up to 128, 64 or 32: more tiles read the same weights, from L2, and each
 // pair's share and last epilogue are shorter.
-__device__ __forceinline__ int make_table(const ExpertsArgs &a, Table &t, int epi_ns, int *scan, int &most) {
+__device__ __forceinline__ int make_table(const ExpertsArgs &a, Table &t, float epi_ns, int *scan, int &most) {
     constexpr int kEach = 2, kSizes = 4, kLargest = 8, kWarps = kRowsThreads / 32;
     static_assert(1 << kLargest == kExpertRows, "parts");
-    static_assert(kEach * kRowsThreads >= kMaxExperts, "a thread's experts");
+    static_assert(kEach * kRowsThreads >= kMaxExperts && kWarps <= 32, "a thread's experts, a lane a warp");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int e = tid; e <= a.experts; e += kRowsThreads) t.offsets[e] = a.offsets[e];
-    __syncthreads();
-    int rows[kEach], most_rows = 0;
+    int o[kEach + 1], rows[kEach], most_rows = 0;
+#pragma unroll
+    for (int j = 0; j <= kEach; ++j) {
+        const int e = tid * kEach + j;
+        o[j] = e <= a.experts ? a.offsets[e] : 0;
+    }
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
         const int e = tid * kEach + j;
-        rows[j] = 0;
-        if (e < a.experts) {
-            const Run r = run_of(t.offsets, e, a.rows);
-            rows[j] = r.hi - r.lo;
-        }
+        if (e <= a.experts) t.offsets[e] = o[j];
+        const Run r = run_of(o[j], o[j + 1], a.rows);
+        rows[j] = e < a.experts ? r.hi - r.lo : 0;
         most_rows = max(most_rows, rows[j]);
     }
     auto parts_of = [&](int rows, int shift) { return (rows + (1 << shift) - 1) >> shift; };
@@ -204,18 +205,21 @@ __device__ __forceinline__ int make_table(const ExpertsArgs &a, Table &t, int ep
     most_rows = __reduce_max_sync(0xFFFFFFFFu, most_rows);
     if (lane == 0) scan[kSizes * kWarps + warp] = most_rows;
     __syncthreads();
-    static_assert(kWarps <= 32, "a lane a warp");
     auto of_warp = [&](int i) { return lane < kWarps ? scan[i * kWarps + lane] : 0; };
     most_rows = __reduce_max_sync(0xFFFFFFFFu, of_warp(kSizes));
-    int best = 0x7FFFFFFF;
+    float best = 0.f;
+    t.shift = kLargest;
+    most = max(32, min(kExpertRows, (most_rows + 31) & ~31));
+    if (most_rows > 32) {
 #pragma unroll
-    for (int c = 0; c < kSizes; ++c) {
-        const int parts = __reduce_add_sync(0xFFFFFFFFu, of_warp(c));
-        const int n = max(32, min(1 << (kLargest - c), (most_rows + 31) & ~31));
-        const int ns = launch_ns(a, parts, n, epi_ns);
-        if (ns < best) best = ns, t.shift = kLargest - c, most = n;
+        for (int c = 0; c < kSizes; ++c) {
+            const int parts = __reduce_add_sync(0xFFFFFFFFu, of_warp(c));
+            const int n = min(1 << (kLargest - c), (most_rows + 31) & ~31);
+            const float ns = launch_ns(a, parts, n, epi_ns);
+            if (c == 0 || ns < best) best = ns, t.shift = kLargest - c, most = n;
+        }
     }
-    const int before_warp = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? of_warp(kLargest - t.shift) : 0);
+    int before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? of_warp(kLargest - t.shift) : 0);
     int parts[kEach], sum = 0;
 #pragma unroll
     for (int j = 0; j < kEach; ++j) parts[j] = parts_of(rows[j], t.shift), sum += parts[j];
@@ -225,7 +229,7 @@ __device__ __forceinline__ int make_table(const ExpertsArgs &a, Table &t, int ep
         const int u = __shfl_up_sync(0xFFFFFFFFu, incl, d);
         if (lane >= d) incl += u;
     }
-    int before = before_warp + incl - sum;
+    before += incl - sum;
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
         const int e = tid * kEach + j;
@@ -282,14 +286,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
         ptx::tmem_alloc_pair(ptx::smem_addr(&s_tmem_base), 512);
         ptx::tmem_relinquish_pair();
     }
+    ptx::tc_fence_before();
+    ptx::cluster_arrive();  // this CTA's barriers initialised and TMEM allocated
+    const RowsWalk begin(args, pair);
     if (!args.chained) asm volatile("griddepcontrol.wait;" ::: "memory");
     int most;
-    constexpr int kEpiNs = EPI == kEpiLinear ? 800 : EPI == kEpiGated ? 1200 : 2200;
+    constexpr float kEpiNs = EPI == kEpiLinear ? 800.f : EPI == kEpiGated ? 1200.f : 2200.f;
     const int parts = make_table(args, table, kEpiNs, s_scan, most);
     const uint32_t stage = kWBytes + (uint32_t)(most / 2) * kRowBytes;
     const int S = min(kRowsStages, (int)(kRowsRing / stage));
-    ptx::tc_fence_before();
-    ptx::cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
+    ptx::cluster_wait();
     ptx::tc_fence_after();
     const uint32_t tmem_base = s_tmem_base;
 
@@ -321,7 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
                 }
             };
             // of the first tile the weights of the first stages, ahead of the wait
-            RowsWalk walk(args, pair);
+            RowsWalk walk = begin;
             const int ahead = args.chained && walk.part < parts ? min(S, args.kblocks) : 0;
             if (ahead > 0) {
                 const Tile x = walk.tile(args, table);
@@ -367,7 +373,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
             int s = 0, job = 0, done = 0;
             uint32_t ph = 0u;
             bool ok = true;
-            for (RowsWalk walk(args, pair); ok && walk.part < parts; walk.next(args), ++job) {
+            // descriptors of stage 0; the others' differ in the address, the low half's
+            const uint64_t a_desc = operand_desc<W_MN>(sbase, 0), b_desc = operand_desc<false>(sbase + kWBytes, 0);
+            const uint32_t a0 = (uint32_t)a_desc, a_hi = (uint32_t)(a_desc >> 32), b_hi = (uint32_t)(b_desc >> 32);
+            const uint32_t b_off = (uint32_t)b_desc - a0;
+            constexpr uint32_t kAStep = (W_MN ? 2048u : 32u) >> 4;
+            for (RowsWalk walk = begin; ok && walk.part < parts; walk.next(args), ++job) {
                 const Tile x = walk.tile(args, table);
                 const uint32_t idesc = idesc0 | ((uint32_t)(x.n >> 3) << 17);
                 const int t = job & 1;
@@ -377,11 +388,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
                 for (int kb = 0; kb < args.kblocks; ++kb) {
                     if (!(ok = wait_phase(full_bar(s), ph, args, &s_abort))) break;
                     ptx::tc_fence_after();
-                    const uint32_t sw = sbase + s * stage, st = sw + kWBytes;
+                    const uint32_t a_lo = a0 + (uint32_t)s * (stage >> 4), b_lo = a_lo + b_off;
+                    ptx::mma_bf16_pair(d_tmem, a_lo, a_hi, b_lo, b_hi, idesc, kb > 0 ? 1u : 0u);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        ptx::mma_bf16_pair(d_tmem, operand_desc<W_MN>(sw, kk), operand_desc<false>(st, kk), idesc,
-                                           (kb > 0 || kk > 0) ? 1u : 0u);
+                    for (int kk = 1; kk < 4; ++kk)
+                        ptx::mma_bf16_pair(d_tmem, a_lo + (uint32_t)kk * kAStep, a_hi, b_lo + (uint32_t)kk * 2u, b_hi,
+                                           idesc, 1u);
                     ptx::mma_commit_pair(empty_bar(s), 0x3);  // frees stage s in both CTAs
                     if (++s == S) s = 0, ph ^= 1u;
                 }
@@ -409,7 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
         const int tr = tid / kGroups, tc = tid % kGroups * 4;
         int job = 0;
         Epilogue p = args.e;
-        for (RowsWalk walk(args, pair); walk.part < parts; walk.next(args), ++job) {
+        for (RowsWalk walk = begin; walk.part < parts; walk.next(args), ++job) {
             const Tile x = walk.tile(args, table);
             const int t = job & 1;
             p.M = x.end;
@@ -502,8 +514,8 @@ struct GradWalk {
     __device__ __forceinline__ GradTile take(const GradArgs &a) {
         GradTile x;
         x.e = e;
-        x.lo = min(max(o0, 0), a.rows);
-        x.hi = max(min(o1, a.rows), x.lo);
+        const Run run = run_of(o0, o1, a.rows);
+        x.lo = run.lo, x.hi = run.hi;
         int base = 0, tiles_n = a.p[0].tiles_n;
         x.p = 0;
 #pragma unroll
