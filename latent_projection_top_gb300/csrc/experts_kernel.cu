@@ -61,6 +61,17 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const 
     }
 }
 
+// The same by all lanes of a warp, with one answer.  The MMA issuer's loop is the
+// whole warp's and one lane issues: what it works out is then the same in all
+// lanes, as the MMAs need their operands (a k-block's four MMAs took a thread
+// alone 250 cycles to issue, the warp 65; the producer's copies gain nothing).
+template <class Args>
+__device__ __forceinline__ bool wait_phase_warp(uint32_t bar, uint32_t parity, const Args &a, volatile int *abort_flag) {
+    if (__all_sync(0xFFFFFFFFu, ptx::mbar_try_wait_hint(bar, parity, kWaitHintNs))) return true;
+    return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, a, abort_flag));
+}
+__device__ __forceinline__ int same(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
 // Bounded wait used only while tearing down.
 template <class Args>
 __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, const Args &a) {
@@ -366,8 +377,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {
             // ---------------- MMA issuer (leader CTA) ----------------
+            const bool issue = ptx::elect_one();
+            const int stages = same(S), all = same(parts);
+            const uint32_t stage_step = (uint32_t)same((int)stage) >> 4, d_base = (uint32_t)same((int)tmem_base);
             const uint32_t fmt = args.fp16 ? 0u : 1u;
             const uint32_t idesc0 = (1u << 4) | (fmt << 7) | (fmt << 10) | ((W_MN ? 1u : 0u) << 15) | ((256u >> 4) << 24);
             int s = 0, job = 0, done = 0;
@@ -378,34 +392,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
             const uint32_t a0 = (uint32_t)a_desc, a_hi = (uint32_t)(a_desc >> 32), b_hi = (uint32_t)(b_desc >> 32);
             const uint32_t b_off = (uint32_t)b_desc - a0;
             constexpr uint32_t kAStep = (W_MN ? 2048u : 32u) >> 4;
-            for (RowsWalk walk = begin; ok && walk.part < parts; walk.next(args), ++job) {
-                const Tile x = walk.tile(args, table);
-                const uint32_t idesc = idesc0 | ((uint32_t)(x.n >> 3) << 17);
+            for (RowsWalk walk = begin; ok && walk.part < all; walk.next(args), ++job) {
+                const uint32_t idesc = idesc0 | ((uint32_t)(same(walk.tile(args, table).n) >> 3) << 17);
                 const int t = job & 1;
-                if (!wait_phase(tempty_bar(t), (((uint32_t)job >> 1) & 1u) ^ 1u, args, &s_abort)) break;
+                if (!wait_phase_warp(tempty_bar(t), (((uint32_t)job >> 1) & 1u) ^ 1u, args, &s_abort)) break;
                 ptx::tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(t * 256);
+                const uint32_t d_tmem = d_base + (uint32_t)(t * 256);
                 for (int kb = 0; kb < args.kblocks; ++kb) {
-                    if (!(ok = wait_phase(full_bar(s), ph, args, &s_abort))) break;
+                    if (!(ok = wait_phase_warp(full_bar(s), ph, args, &s_abort))) break;
                     ptx::tc_fence_after();
-                    const uint32_t a_lo = a0 + (uint32_t)s * (stage >> 4), b_lo = a_lo + b_off;
-                    ptx::mma_bf16_pair(d_tmem, a_lo, a_hi, b_lo, b_hi, idesc, kb > 0 ? 1u : 0u);
+                    const uint32_t a_lo = a0 + (uint32_t)s * stage_step, b_lo = a_lo + b_off;
+                    if (issue) {
+                        ptx::mma_bf16_pair(d_tmem, a_lo, a_hi, b_lo, b_hi, idesc, kb > 0 ? 1u : 0u);
 #pragma unroll
-                    for (int kk = 1; kk < 4; ++kk)
-                        ptx::mma_bf16_pair(d_tmem, a_lo + (uint32_t)kk * kAStep, a_hi, b_lo + (uint32_t)kk * 2u, b_hi,
-                                           idesc, 1u);
-                    ptx::mma_commit_pair(empty_bar(s), 0x3);  // frees stage s in both CTAs
-                    if (++s == S) s = 0, ph ^= 1u;
+                        for (int kk = 1; kk < 4; ++kk)
+                            ptx::mma_bf16_pair(d_tmem, a_lo + (uint32_t)kk * kAStep, a_hi, b_lo + (uint32_t)kk * 2u,
+                                               b_hi, idesc, 1u);
+                        ptx::mma_commit_pair(empty_bar(s), 0x3);  // frees stage s in both CTAs
+                    }
+                    __syncwarp();
+                    if (++s == stages) s = 0, ph ^= 1u;
                 }
-                if (ok) ptx::mma_commit_pair(tfull_bar(t), 0x3), ++done;
+                if (ok && issue) ptx::mma_commit_pair(tfull_bar(t), 0x3);
+                if (ok) ++done;
             }
-            ptx::mma_commit_pair(drain_bar, 0x3);  // every MMA retired before TMEM is freed
-            wait_drain(drain_bar, 0u, args);
-            // the peer's arrivals for the last tiles have landed
-            for (int t = 0; t < 2; ++t) {
-                const int tiles = (done + 1 - t) / 2;
-                if (tiles > 0) wait_drain(tempty_bar(t), (uint32_t)(tiles - 1) & 1u, args);
+            if (issue) {
+                ptx::mma_commit_pair(drain_bar, 0x3);  // every MMA retired before TMEM is freed
+                wait_drain(drain_bar, 0u, args);
+                // the peer's arrivals for the last tiles have landed
+                for (int t = 0; t < 2; ++t) {
+                    const int tiles = (done + 1 - t) / 2;
+                    if (tiles > 0) wait_drain(tempty_bar(t), (uint32_t)(tiles - 1) & 1u, args);
+                }
             }
+            __syncwarp();
         }
     } else {
         // ---------------- epilogue (both CTAs) ----------------
