@@ -508,8 +508,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
 
 // ---- weights' gradients -----------------------------------------------------------
 
-constexpr int kGradThreads = 96 + 512;  // producer, MMA issuer, zeros; 16 epilogue warps
 constexpr int kGradStages = 5;
+// Warps that write the zeros, one a stage (which so sees each phase of its tail
+// barrier): an arrival with its order at the pair's other CTA takes 2000 cycles
+// and more, which several tails then share (one warp: 256 experts of 1024x512 with
+// 63 rows 184 us).
+constexpr int kZeroWarps = kGradStages;
+constexpr int kGradEpi = 2 + kZeroWarps;               // the first epilogue warp, of 16
+constexpr int kGradThreads = 32 * kGradEpi + 512;
 constexpr uint32_t kGradStage = 4 * 8192;  // a CTA's 128 rows of A and 128 columns of B of 64 rows of the batch
 constexpr uint32_t kGradTurn = 32 * 64 * 2;  // a warp's 32 rows of 64 columns, 16 bits each
 constexpr uint32_t kGradSmem = 1024 + kGradStages * kGradStage + 16 * kGradTurn + 256;
@@ -658,43 +664,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {
             // ---------------- MMA issuer (leader CTA) ----------------
+            const bool issue = ptx::elect_one();
+            const uint32_t d_base = (uint32_t)same((int)tmem_base);
             const uint32_t fmt = args.fp16 ? 0u : 1u;
             const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 15) | (1u << 16) |
                                    ((256u >> 3) << 17) | ((256u >> 4) << 24);
-            int it = 0, job = 0, done = 0;
+            const uint64_t desc = operand_desc<true>(sbase, 0);  // of A in stage 0
+            const uint32_t a0 = (uint32_t)desc, hi = (uint32_t)(desc >> 32);
+            int s = 0, job = 0, done = 0;
+            uint32_t ph = 0u;
             bool ok = true;
             for (GradWalk walk(args, pair); ok && walk.more(args);) {
                 const GradTile x = walk.take(args);
-                if (x.lo >= x.hi) continue;  // zeros: the epilogue's alone
+                const int rows = same(x.hi - x.lo);
+                if (rows <= 0) continue;  // zeros: the epilogue's alone
                 const int t = job & 1;
-                if (!wait_phase(tempty_bar(t), (((uint32_t)job >> 1) & 1u) ^ 1u, args, &s_abort)) break;
+                if (!wait_phase_warp(tempty_bar(t), (((uint32_t)job >> 1) & 1u) ^ 1u, args, &s_abort)) break;
                 ptx::tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(t * 256);
-                for (int r = x.lo; r < x.hi; r += 64, ++it) {
-                    const int s = it % S;
-                    if (!(ok = wait_phase(full_bar(s), (uint32_t)(it / S) & 1u, args, &s_abort))) break;
+                const uint32_t d_tmem = d_base + (uint32_t)(t * 256);
+                for (int r = 0; r < rows; r += 64) {
+                    if (!(ok = wait_phase_warp(full_bar(s), ph, args, &s_abort))) break;
                     ptx::tc_fence_after();
-                    const uint32_t sa = sbase + s * kGradStage, sb = sa + 16384u;
+                    const uint32_t a_lo = a0 + (uint32_t)s * (kGradStage >> 4), b_lo = a_lo + (16384u >> 4);
+                    if (issue) {
+                        ptx::mma_bf16_pair(d_tmem, a_lo, hi, b_lo, hi, idesc, r > 0 ? 1u : 0u);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        if (kk == 0 || r + 16 * kk < x.hi)
-                            ptx::mma_bf16_pair(d_tmem, operand_desc<true>(sa, kk), operand_desc<true>(sb, kk), idesc,
-                                               (r > x.lo || kk > 0) ? 1u : 0u);
-                    ptx::mma_commit_pair(empty_bar(s), 0x3);
+                        for (uint32_t kk = 1; kk < 4; ++kk)
+                            if (r + 16 * (int)kk < rows)
+                                ptx::mma_bf16_pair(d_tmem, a_lo + kk * 128u, hi, b_lo + kk * 128u, hi, idesc, 1u);
+                        ptx::mma_commit_pair(empty_bar(s), 0x3);
+                    }
+                    __syncwarp();
+                    if (++s == S) s = 0, ph ^= 1u;
                 }
-                if (ok) ptx::mma_commit_pair(tfull_bar(t), 0x3), ++done;
+                if (ok && issue) ptx::mma_commit_pair(tfull_bar(t), 0x3);
+                if (ok) ++done;
                 ++job;
             }
-            ptx::mma_commit_pair(drain_bar, 0x3);
-            wait_drain(drain_bar, 0u, args);
-            for (int t = 0; t < 2; ++t) {
-                const int tiles = (done + 1 - t) / 2;
-                if (tiles > 0) wait_drain(tempty_bar(t), (uint32_t)(tiles - 1) & 1u, args);
+            if (issue) {
+                ptx::mma_commit_pair(drain_bar, 0x3);
+                wait_drain(drain_bar, 0u, args);
+                for (int t = 0; t < 2; ++t) {
+                    const int tiles = (done + 1 - t) / 2;
+                    if (tiles > 0) wait_drain(tempty_bar(t), (uint32_t)(tiles - 1) & 1u, args);
+                }
             }
+            __syncwarp();
         }
-    } else if (warp == 2) {
+    } else if (warp < kGradEpi) {
         // ---------------- zeros behind a run's last row (both CTAs) ----------------
         int it = 0;
         uint32_t tail_par = 0u;
@@ -705,9 +724,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
             it += blocks;
             if (left % 16 == 0) continue;
             const int s = (it - 1) % S;
-            ok = __all_sync(0xFFFFFFFFu, wait_phase(tail_bar(s), (tail_par >> s) & 1u, args, &s_abort));
-            tail_par ^= 1u << s;
-            if (!ok) break;
+            if (s != warp - 2) continue;
+            if (!(ok = wait_phase_warp(tail_bar(s), tail_par, args, &s_abort))) break;
+            tail_par ^= 1u;
             // row r of the batch is 128 bytes of each of the four boxes
             const uint32_t at = sbase + s * kGradStage + (uint32_t)left * 128u;
             const int pieces = (16 - left % 16) * 8;
@@ -716,16 +735,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
                 for (int j = lane; j < pieces; j += 32)
                     asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at + 8192u * b + 16u * j), "r"(0)
                                  : "memory");
-            asm volatile("fence.proxy.async;" ::: "memory");  // before the tensor cores' reads
+            ptx::fence_proxy_async_smem();  // before the tensor cores' reads
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_remote(ptx::map_to_rank(full_bar(s), 0u));
+            if (lane == 0) {
+                if (leader)
+                    ptx::mbar_arrive(full_bar(s));
+                else
+                    ptx::mbar_arrive_remote(ptx::map_to_rank(full_bar(s), 0u));
+            }
         }
     } else {
         // ---------------- epilogue (both CTAs) ----------------
         const int lq = warp & 3;              // TMEM lanes 32 lq .. + 31 = rows of D
-        const int cs = (warp - 3) >> 2;       // which 64 of the tile's columns
+        const int cs = (warp - kGradEpi) >> 2;  // which 64 of the tile's columns
         const uint32_t lanes = tmem_base + ((uint32_t)(32 * lq) << 16);
-        const uint32_t mine = turn + (uint32_t)(warp - 3) * kGradTurn;
+        const uint32_t mine = turn + (uint32_t)(warp - kGradEpi) * kGradTurn;
         // the 128-byte swizzle of the results' boxes: 16 bytes (unit x) of a row sit at unit x ^ (row & 7)
         auto slot = [&](int x) { return mine + (uint32_t)(lane * 128 + ((x ^ (lane & 7)) << 4)); };
         int job = 0;
