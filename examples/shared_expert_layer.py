@@ -7,8 +7,8 @@ Serving, for a batch of residual-stream rows x:
     x = x + latent W_out                         route.linear_forward (in place)
     x = x + shared expert(n)                     route.gated_forward  (in place)
 
-(the routed experts, which would turn `latent` into their weighted sum before
-its projection back to the hidden width, are the caller's).
+(the routed experts, which turn `latent` into their weighted sum before its
+projection back to the hidden width: routed_experts_layer.py).
 
 Training, for the norm and the shared expert of the same layer:
 
