@@ -41,7 +41,7 @@ CALL_SOURCE = os.path.join(CSRC, "layer_call.cpp")
 SOURCES = ["decode_kernel.cu", "prefill_kernel.cu", "topk_kernel.cu", "stage_kernel.cu",
            "route_api.cu", "layer_gemm.cu", "layer_small.cu", "layer_elem.cu",
            "layer_norm.cu", "layer_api.cu", "dispatch_kernel.cu", "experts_kernel.cu",
-           "dropout_kernel.cu", "experts_api.cu"]
+           "experts_small.cu", "dropout_kernel.cu", "experts_api.cu"]
 HEADERS = ["common.cuh", "sm103_ptx.cuh", "topk16.cuh", "twofloat.cuh", "api_util.h", "layer.cuh",
            "layer_math.cuh", "layer_ptx.cuh", "layer_plan.h", "experts.cuh"]
 

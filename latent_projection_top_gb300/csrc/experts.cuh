@@ -101,6 +101,17 @@ cudaError_t experts_configure();
 int experts_smem_bytes();
 cudaError_t experts_launch(int epi, bool n_contiguous, const ExpertsMaps &maps, const ExpertsArgs &args,
                            cudaStream_t stream);
+
+// Products of few rows (at most kFewRows) and few tiles, of weights whose columns
+// are contiguous: `tiles` tiles of 128 columns (gated: 64 hidden ones), one for
+// each column tile of every expert that could have rows, over `ctas` CTAs each.
+constexpr int kFewRows = 32;
+constexpr int kFewCols = 128;
+constexpr int kFewCtas = 8;
+cudaError_t experts_small_configure();
+cudaError_t experts_small_launch(int epi, int tiles, int ctas, const ExpertsMaps &maps, const ExpertsArgs &args,
+                                 cudaStream_t stream);
+
 cudaError_t experts_grad_launch(const GradMaps &maps, const GradArgs &args, cudaStream_t stream);
 
 // ---- dropout ----------------------------------------------------------------------------

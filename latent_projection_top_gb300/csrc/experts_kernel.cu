@@ -438,6 +438,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
         const uint32_t lanes = tmem_base + ((uint32_t)(32 * lq) << 16);
         const uint32_t buf = turn + (uint32_t)group * kTurnBytes;
         constexpr int kGroups = kCtaCols / 4, kStep = 128 / kGroups, kR = kTurnRows / kStep;
+        // rows worked on together: of d gate's, all four at a time did not fit the
+        // registers, and inputs that are spilled are waited for (192 rows of FP16 gelu:
+        // 5400 cycles a block)
+        constexpr int kBatch = EPI == kEpiDGate ? 2 : kR, kBatches = kR / kBatch;
         const int tr = tid / kGroups, tc = tid % kGroups * 4;
         int job = 0;
         Epilogue p = args.e;
@@ -448,16 +452,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
             const int c = (x.tn * 2 + (int)rank) * kCtaCols + tc;
             // what is read besides goes out before the tile's sums are complete (read
             // after them, 256 experts of 1024x512 with 63 rows: d gate 86 us, so 55)
-            GroupIn<EPI, kR> in;
+            GroupIn<EPI, kBatch> in[kBatches];
             const int r0 = x.row0 + tr;
-            group_load<EPI, kR>(p, r0 + group * kTurnRows, c, kStep, in);
+            auto inputs = [&](int b) {
+#pragma unroll
+                for (int q = 0; q < kBatches; ++q)
+                    group_load<EPI, kBatch>(p, r0 + b + q * kBatch * kStep, c, kStep, in[q]);
+            };
+            inputs(group * kTurnRows);
             // one warp of a group polls, the others sleep at the barrier
             const bool ok = lq != 2 || wait_phase(tfull_bar(t), ((uint32_t)job >> 1) & 1u, args, &s_abort);
             if (!ptx::named_bar_and(1 + group, 128, ok)) break;
             ptx::tc_fence_after();
             const uint32_t acc = lanes + (uint32_t)(t * 256);
             for (int b = group * kTurnRows; b < x.n; b += kEpiGroups * kTurnRows) {
-                if (b >= kEpiGroups * kTurnRows) group_load<EPI, kR>(p, r0 + b, c, kStep, in);
+                if (b >= kEpiGroups * kTurnRows) inputs(b);
                 uint32_t v[kTurnRows];
                 ptx::tmem_ld_x16(acc + (uint32_t)b, v);
                 ptx::tmem_ld_wait();
@@ -466,22 +475,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
                     asm volatile("st.shared.b32 [%0], %1;" ::"r"(buf + (uint32_t)(j * 128 + tid) * 4u), "r"(v[j])
                                  : "memory");
                 ptx::named_bar_sync(1 + group, 128);
-                float d[4 * kR], u[EPI == kEpiGated ? 4 * kR : 1];
+                float d[kBatches][4 * kBatch], u[kBatches][EPI == kEpiGated ? 4 * kBatch : 1];
 #pragma unroll
                 for (int j = 0; j < kR; ++j) {
+                    float *dj = d[j / kBatch] + 4 * (j % kBatch);
                     const uint32_t at = buf + (uint32_t)((tr + j * kStep) * 128 + tc) * 4u;
                     asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                                 : "=f"(d[4 * j]), "=f"(d[4 * j + 1]), "=f"(d[4 * j + 2]), "=f"(d[4 * j + 3])
+                                 : "=f"(dj[0]), "=f"(dj[1]), "=f"(dj[2]), "=f"(dj[3])
                                  : "r"(at)
                                  : "memory");
-                    if constexpr (EPI == kEpiGated)
+                    if constexpr (EPI == kEpiGated) {
+                        float *uj = u[j / kBatch] + 4 * (j % kBatch);
                         asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                                     : "=f"(u[4 * j]), "=f"(u[4 * j + 1]), "=f"(u[4 * j + 2]), "=f"(u[4 * j + 3])
+                                     : "=f"(uj[0]), "=f"(uj[1]), "=f"(uj[2]), "=f"(uj[3])
                                      : "r"(at + 256u)
                                      : "memory");
+                    }
                 }
                 ptx::named_bar_sync(1 + group, 128);  // the rows have left shared memory
-                group_epilogue<EPI, kR>(p, r0 + b, c, kStep, d, u, in);
+#pragma unroll
+                for (int q = 0; q < kBatches; ++q)
+                    group_epilogue<EPI, kBatch>(p, r0 + b + q * kBatch * kStep, c, kStep, d[q], u[q], in[q]);
             }
             ptx::tc_fence_before();
             __syncwarp();

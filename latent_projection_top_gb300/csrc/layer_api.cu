@@ -443,6 +443,7 @@ route_status layer_finish_prepare(route_layer *p, int device, route_layer **out)
                     : p->kind == kDispatch     ? sort_configure()
                     : p->kind == kExpertBlocks ? experts_configure()
                                                : cudaSuccess) != cudaSuccess ||
+               (p->kind == kExpertBlocks && (e = experts_small_configure()) != cudaSuccess) ||
                (products && ((e = gemm_configure()) != cudaSuccess || (e = small_configure()) != cudaSuccess))) {
         st = cuda_fail(e, "cudaFuncSetAttribute");
     }
