@@ -321,7 +321,8 @@ constexpr int kBackWarps = 8;
 template <int TY, bool VEC>
 __global__ void __launch_bounds__(32 * kBackWarps) combine_backward_kernel(const __grid_constant__ MoveArgs a) {
     using P = Piece<TY, VEC>;
-    constexpr int kPieces = VEC ? 2 : 8;  // on the way together
+    // on the way together (16 bytes, 4096x3584: one 178 us, two 169, four 153)
+    constexpr int kPieces = VEC ? 4 : 8;
     __shared__ Places s;
     __shared__ float s_dot[kMaxTopk][kBackWarps];
     asm volatile("griddepcontrol.wait;" ::: "memory");
