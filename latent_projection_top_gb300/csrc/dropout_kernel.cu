@@ -108,8 +108,9 @@ __device__ __forceinline__ unsigned long long first_counter(const DropoutArgs &a
 // the rows follow one another in every matrix.  A dropped value is not
 // multiplied: an infinity or a NaN there is gone.
 //
-// Bound by HBM where a residual is added, else by the instructions issued, of
-// which ten rounds are 40 for eight values and half of those at half the rate.
+// Bound by HBM where a residual is added (8192x7168 BF16 51 us, 352 MB, 6.9 TB/s),
+// else by the instructions issued, of which ten rounds are 40 for eight values and
+// half of those at half the rate (41 us, 235 MB, 5.7 TB/s).
 template <int TY, bool FLAT>
 __global__ void __launch_bounds__(256) dropout_kernel(const __grid_constant__ DropoutArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -142,8 +143,8 @@ __global__ void __launch_bounds__(256) dropout_kernel(const __grid_constant__ Dr
 
 // Rows at any alignment: a warp takes 256 values of a row, each lane draws the
 // lots of eight neighbours, and then has every 32nd value, so that its accesses
-// are whole stretches of the row (eight neighbours a lane, 8192x3583 BF16 with a
-// residual: 67.8 us).
+// are whole stretches of the row (8192x3583 BF16 with a residual 46 us; eight
+// neighbours a lane, 68).
 template <int TY>
 __global__ void __launch_bounds__(256) dropout_any_kernel(const __grid_constant__ DropoutArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");

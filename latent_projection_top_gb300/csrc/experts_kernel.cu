@@ -13,12 +13,19 @@
 // tile and 128 a CTA, rows their N side, as many as there are up to 256 in
 // steps of 32: an expert with two rows costs the reading of its weights, one
 // with a thousand runs at the tensor cores' rate, and no rule chooses between
-// them.  A run of more than 256 rows is cut into equal parts.
+// them.  Longer runs are cut into parts (make_table).  Bound by HBM where experts
+// have few rows (8 rows of 3584x2048 at 14 experts 89 us, 616 MB of weights: 6.9
+// TB/s), by the tensor cores where they have many (16890 rows at 16 experts of
+// 3584x2048 443-460 us, 1,615-1,680 TFLOP/s, the power limit's), in between by
+// whole rounds of tiles over the pairs, and by 3 us of a launch's start (0.7 of it
+// the table) and 3 of the last epilogue.
 //
 // Gradient kernel: rows of dW are the M side, its columns the N side, 256 x 256
-// a tile.  The last block of an expert's rows holds rows of the next one: they
-// are overwritten with zeros in shared memory, in both operands, before the
-// tensor cores read them (a product with zero would keep an infinity or a NaN).
+// a tile.  The last block of an expert's rows holds rows of the next one: what of
+// them the tensor cores would read, 16 rows at a time, is overwritten with zeros in
+// shared memory, in both operands (a product with zero would keep an infinity or
+// a NaN).  Bound by what it writes where experts have few rows (256 experts of
+// 1024x512 with 63 rows each, 805 MB: 158 us, 5.1 TB/s), by the tensor cores else.
 //
 // Warp roles, waits and their limits as in layer_gemm.cu.
 #include "experts.cuh"
@@ -190,10 +197,11 @@ __device__ __forceinline__ int make_table(const ExpertsArgs &a, Table &t, float 
     static_assert(kEach * kRowsThreads >= kMaxExperts && kWarps <= 32, "a thread's experts, a lane a warp");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int o[kEach + 1], rows[kEach], most_rows = 0;
+    // from L2: a chained kernel reads them ahead of its wait
 #pragma unroll
     for (int j = 0; j <= kEach; ++j) {
         const int e = tid * kEach + j;
-        o[j] = e <= a.experts ? a.offsets[e] : 0;
+        o[j] = e <= a.experts ? __ldcg(a.offsets + e) : 0;
     }
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
@@ -439,8 +447,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
         const uint32_t buf = turn + (uint32_t)group * kTurnBytes;
         constexpr int kGroups = kCtaCols / 4, kStep = 128 / kGroups, kR = kTurnRows / kStep;
         // rows worked on together: of d gate's, all four at a time did not fit the
-        // registers, and inputs that are spilled are waited for (192 rows of FP16 gelu:
-        // 5400 cycles a block)
+        // registers, and inputs that are spilled are waited for (256 experts of 1024x512
+        // with 63 rows: d gate 78 us, so 63)
         constexpr int kBatch = EPI == kEpiDGate ? 2 : kR, kBatches = kR / kBatch;
         const int tr = tid / kGroups, tc = tid % kGroups * 4;
         int job = 0;
@@ -450,8 +458,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
             const int t = job & 1;
             p.M = x.end;
             const int c = (x.tn * 2 + (int)rank) * kCtaCols + tc;
-            // what is read besides goes out before the tile's sums are complete (read
-            // after them, 256 experts of 1024x512 with 63 rows: d gate 86 us, so 55)
+            // what is read besides goes out before the tile's sums are complete
             GroupIn<EPI, kBatch> in[kBatches];
             const int r0 = x.row0 + tr;
             auto inputs = [&](int b) {

@@ -11,7 +11,7 @@
 // finds its expert from the offsets, and the call has no more tiles than clusters
 // (the host's rule, by the rows that there could be).
 //
-// Bound by latencies: 1 row at two of 64 experts, 896x448, 8.6 us for both
+// Bound by latencies: 1 row at two of 64 experts, 896x448, 10.0 us for both
 // products (12.3 by the pair kernel, whose 16 busy SMs take 500 cycles a k-block).
 //
 // Warp roles (320 threads): warp 0 TMA producer, warp 1 TMEM owner and MMA
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     constexpr int kEach = (kMaxExperts + kThreads - 1) / kThreads;
     int o[kEach + 1], mine = 0;
 #pragma unroll
-    for (int j = 0; j <= kEach; ++j) o[j] = tid * kEach + j <= args.experts ? args.offsets[tid * kEach + j] : 0;
+    for (int j = 0; j <= kEach; ++j) o[j] = tid * kEach + j <= args.experts ? __ldcg(args.offsets + tid * kEach + j) : 0;
     auto run = [&](int j, int &lo, int &hi) {
         lo = min(max(o[j], 0), args.rows);
         hi = tid * kEach + j < args.experts ? max(min(o[j + 1], args.rows), lo) : lo;

@@ -431,6 +431,53 @@ def test_experts_reports_a_wait_that_expired():
     assert torch.equal(out, want)
 
 
+FEW = [
+    # k, f, n, offsets, dtype, act: so few tiles that each is split over a cluster
+    (64, 64, 128, sizes(1), BF16, "silu"),
+    (8, 8, 8, sizes(0, 3, 0), FP16, "relu"),
+    (200, 72, 264, sizes(0, 5, 0, 0, 1), BF16, "gelu"),
+    (3584, 192, 520, sizes(0, 0, 17, 2), BF16, "silu"),
+    (896, 448, 896, sizes(1, 0, 0, 1), FP16, "gelu_tanh"),
+    (7168, 64, 128, sizes(32), BF16, "sigmoid"),
+    (512, 1024, 72, sizes(*[0] * 1023, 2), BF16, "silu"),
+]
+
+
+@pytest.mark.parametrize("k,f,n,offsets,dt,act", FEW)
+def test_experts_of_few_rows_and_tiles(k, f, n, offsets, dt, act):
+    E, T = len(offsets) - 1, int(offsets[-1])
+    x = normal(1, T + 1, k, dt=dt)
+    x[T:] = float("nan")
+    W = stack(3, E, k, f, dt, k ** -0.5) if E < 100 else normal(3, E, k, f, dt=dt, scale=k ** -0.5), \
+        normal(4, E, k, f, dt=dt, scale=k ** -0.5), normal(5, E, f, n, dt=dt, scale=f ** -0.5)
+    o = to_gpu(offsets).to(I32)
+    out, buf = sevens(T + 1, n, dt)
+    L = route.lib()
+    with route.ExpertsPlan(64, k, f, n, E, dt, act=act, train=True) as plan:
+        saved = plan.new_saved(T)
+        for _ in range(3):
+            route.experts_forward(plan, x[:T], o, *W, out[:T], saved=saved)
+        dx = torch.empty((T, k), dtype=dt, device=DEV)
+        route.experts_backward(plan, out[:T], None, o, *W, saved, dx=dx)  # what it saved
+        plan.status()
+        L.route_layer_test_stall(plan.handle, 1, 20_000_000)
+        again = torch.full_like(out, 7.0)
+        route.experts_forward(plan, x[:T], o, *W, again[:T])
+        with pytest.raises(route.RouteError, match="TIMEOUT"):
+            plan.status()
+        L.route_layer_test_stall(plan.handle, 0, 0)
+        route.experts_forward(plan, x[:T], o, *W, again[:T])
+        plan.status()
+    assert torch.equal(again, out)
+    written(out, buf, slice(int(offsets[0]), T))
+    for e, (lo, hi) in enumerate(experts_ref.runs_of(offsets, T)):
+        if lo < hi:
+            w = [t[e] for t in W]
+            want, kept = ref.gated(x[lo:hi], *w, None, act, dt)
+            check(f"out of {e}", out[lo:hi], want)
+            check(f"dx of {e}", dx[lo:hi], ref.gated_grads(x[lo:hi], *w, kept, out[lo:hi], act, dt)["dx"])
+
+
 # ---- dropout ------------------------------------------------------------------------
 
 DROPOUT = [
