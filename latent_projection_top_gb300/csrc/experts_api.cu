@@ -247,7 +247,7 @@ route_status route_dispatch_combine(const route_layer *p, int rows, const void *
     a.b = y, a.ld_b = stride_of(pairs, ld_y, p->k);
     a.out = out, a.ld_out = stride_of(rows, ld_out, p->k);
     DeviceGuard guard(p->device);
-    return launched(combine_launch(a, static_cast<cudaStream_t>(stream)), "combine kernel launch");
+    return launched(combine_launch(a, p->sms, static_cast<cudaStream_t>(stream)), "combine kernel launch");
 }
 
 route_status route_dispatch_gather_backward(const route_layer *p, int rows, const void *dout, int64_t ld_dout,
