@@ -85,6 +85,10 @@ struct GradArgs {
     int experts, rows;
     int nprob;
     int fp16;
+    // The call's kernel before this one waited for what made A and B before it let
+    // this one launch, and writes neither: the two run side by side, and this one
+    // waits for it before it ends.
+    int beside;
     int pairs;
     int per_expert;             // tiles of one expert, of all problems
     int test_stall;

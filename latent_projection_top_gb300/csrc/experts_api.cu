@@ -396,6 +396,8 @@ route_status route_experts_backward(const route_layer *p, int rows, const void *
     a.offsets = offsets;
     a.experts = p->experts, a.rows = rows;
     a.fp16 = p->type == kFp16;
+    // dx's product has waited for dgate and dup's (without it they are the ones before)
+    a.beside = dx != nullptr;
     a.pairs = p->pairs;
     a.test_stall = p->test_stall;
     a.timeout_ns = p->timeout_ns;

@@ -623,7 +623,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     ptx::cluster_sync();
     ptx::tc_fence_after();
     const uint32_t tmem_base = s_tmem_base;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!args.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp == 0) {
         if (lane == 0) {
@@ -823,6 +823,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         if (lane == 0) ptx::bulk_wait_group_all();
     }
 
+    // what follows this kernel follows the one before it too
+    if (args.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
     ptx::tc_fence_before();
     __syncthreads();
     if (warp == 1) {
