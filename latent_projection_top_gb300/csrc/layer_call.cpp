@@ -409,30 +409,49 @@ PyObject *dropout_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// bind(addresses of the entry points, in the order above)
-PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    constexpr int kEntries = 15;
-    if (n != kEntries) {
-        PyErr_SetString(PyExc_TypeError, "bind takes fifteen addresses");
-        return nullptr;
+// N addresses of entry points; false (and an exception) where there are others.
+template <int N>
+bool addresses(PyObject *const *a, Py_ssize_t n, void *(&p)[N]) {
+    if (n != N) {
+        PyErr_Format(PyExc_TypeError, "takes %d addresses", N);
+        return false;
     }
-    void *p[kEntries];
-    for (int i = 0; i < kEntries; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
-    if (PyErr_Occurred()) return nullptr;
-    int i = 0;
-    auto next = [&](auto &entry) { entry = reinterpret_cast<std::decay_t<decltype(entry)>>(p[i++]); };
-    next(p_norm_forward), next(p_norm_backward);
-    next(p_linear_forward), next(p_linear_backward);
-    next(p_gated_forward), next(p_gated_backward);
-    next(p_dispatch_sort), next(p_dispatch_gather), next(p_dispatch_gather_backward);
-    next(p_dispatch_combine), next(p_dispatch_combine_backward);
-    next(p_experts_forward), next(p_experts_backward);
-    next(p_dropout_forward), next(p_dropout_backward);
+    for (int i = 0; i < N; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
+    return !PyErr_Occurred();
+}
+
+// bind(addresses of the layer operators' six entry points, in the order above)
+PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    void *p[6];
+    if (!addresses(a, n, p)) return nullptr;
+    p_norm_forward = reinterpret_cast<decltype(p_norm_forward)>(p[0]);
+    p_norm_backward = reinterpret_cast<decltype(p_norm_backward)>(p[1]);
+    p_linear_forward = reinterpret_cast<decltype(p_linear_forward)>(p[2]);
+    p_linear_backward = reinterpret_cast<decltype(p_linear_backward)>(p[3]);
+    p_gated_forward = reinterpret_cast<decltype(p_gated_forward)>(p[4]);
+    p_gated_backward = reinterpret_cast<decltype(p_gated_backward)>(p[5]);
+    Py_RETURN_NONE;
+}
+
+// bind_routed(addresses of the routed experts' and dropout's nine, in the order above)
+PyObject *bind_routed(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    void *p[9];
+    if (!addresses(a, n, p)) return nullptr;
+    p_dispatch_sort = reinterpret_cast<decltype(p_dispatch_sort)>(p[0]);
+    p_dispatch_gather = reinterpret_cast<decltype(p_dispatch_gather)>(p[1]);
+    p_dispatch_gather_backward = reinterpret_cast<decltype(p_dispatch_gather_backward)>(p[2]);
+    p_dispatch_combine = reinterpret_cast<decltype(p_dispatch_combine)>(p[3]);
+    p_dispatch_combine_backward = reinterpret_cast<decltype(p_dispatch_combine_backward)>(p[4]);
+    p_experts_forward = reinterpret_cast<decltype(p_experts_forward)>(p[5]);
+    p_experts_backward = reinterpret_cast<decltype(p_experts_backward)>(p[6]);
+    p_dropout_forward = reinterpret_cast<decltype(p_dropout_forward)>(p[7]);
+    p_dropout_backward = reinterpret_cast<decltype(p_dropout_backward)>(p[8]);
     Py_RETURN_NONE;
 }
 
 #define ROUTE_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {ROUTE_METHOD(bind),           ROUTE_METHOD(norm_forward),    ROUTE_METHOD(norm_backward),
+PyMethodDef methods[] = {ROUTE_METHOD(bind),           ROUTE_METHOD(bind_routed),
+                         ROUTE_METHOD(norm_forward),    ROUTE_METHOD(norm_backward),
                          ROUTE_METHOD(linear_forward), ROUTE_METHOD(linear_backward), ROUTE_METHOD(gated_forward),
                          ROUTE_METHOD(gated_backward), ROUTE_METHOD(dispatch_sort),   ROUTE_METHOD(dispatch_gather),
                          ROUTE_METHOD(dispatch_gather_backward), ROUTE_METHOD(dispatch_combine),

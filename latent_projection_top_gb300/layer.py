@@ -119,11 +119,14 @@ def _short_way():
             warnings.warn(f"layer calls go through ctypes, 2 to 5 us more each: {e} "
                           "(latent_projection_top_gb300.build() makes the module)")
             return None
-        module.bind(*(ctypes.cast(getattr(L, f"route_{name}"), _vp).value for name in (
-            "norm_forward", "norm_backward", "linear_forward", "linear_backward",
-            "gated_forward", "gated_backward", "dispatch_sort", "dispatch_gather",
-            "dispatch_gather_backward", "dispatch_combine", "dispatch_combine_backward",
-            "experts_forward", "experts_backward", "dropout_forward", "dropout_backward")))
+        for bind, names in (
+                (module.bind, ("norm_forward", "norm_backward", "linear_forward", "linear_backward",
+                               "gated_forward", "gated_backward")),
+                (module.bind_routed, ("dispatch_sort", "dispatch_gather", "dispatch_gather_backward",
+                                      "dispatch_combine", "dispatch_combine_backward",
+                                      "experts_forward", "experts_backward", "dropout_forward",
+                                      "dropout_backward"))):
+            bind(*(ctypes.cast(getattr(L, f"route_{name}"), _vp).value for name in names))
         _short = module
     return _short
 
