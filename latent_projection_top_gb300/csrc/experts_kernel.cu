@@ -112,10 +112,10 @@ constexpr uint32_t kRowBytes = 64 * 2;                      // one row of it
 constexpr int kTurnRows = 16;                               // rows an epilogue group turns around at once
 constexpr uint32_t kTurnBytes = kTurnRows * 128 * 4;
 constexpr uint32_t kRowsBars = 256;
-constexpr int kPartTable = 2048;                            // parts whose expert is looked up
-constexpr uint32_t kRowsTable = 2 * (kMaxExperts + 4) * 4 + kPartTable * 2;
+constexpr int kPartTable = 2048;                            // parts that are looked up
+constexpr uint32_t kRowsTable = kPartTable * 8 + 2 * (kMaxExperts + 4) * 4;
 // What is left is the stages': as many as fit of the size that the largest
-// part needs (five with 256 rows, ten with 32), so that short parts, which are
+// part needs (five with 256 rows, nine with 32), so that short parts, which are
 // bound by memory, have more on the way.
 constexpr uint32_t kRowsRing = (kSmemLimit - 1024 - kEpiGroups * kTurnBytes - kRowsBars - kRowsTable) & ~1023u;
 constexpr uint32_t kRowsSmem = 1024 + kRowsRing + kEpiGroups * kTurnBytes + kRowsBars + kRowsTable;
@@ -126,17 +126,24 @@ static_assert(kRowsSmem <= kSmemLimit && kRowsRing >= 5 * (kWBytes + kExpertRows
 struct Tile {
     int e, row0, end, tn, n;
 };
-// In shared memory: parts of the experts before each ([experts]: all of them),
-// the offsets, and the expert of each of the first kPartTable parts.
+// In shared memory: the first kPartTable parts (their first row; expert and, from
+// bit 16 on, rows), parts of the experts before each ([experts]: all of them), and
+// the offsets.
 struct Table {
+    int2 *part;
     int *first, *offsets;
-    uint16_t *expert;
     int shift;  // parts have up to 1 << shift rows
 };
+// The rows of each of an expert's parts but the last: equal, in steps of 32 (8192
+// rows of 3584x2048: 444 us, the last one what is left: 452).  No part is empty,
+// because a step is no more than the most.
+__device__ __forceinline__ int part_step(int rows, int parts) {
+    return parts > 1 ? ((rows + parts - 1) / parts + 31) & ~31 : rows;
+}
 
 // A pair's tiles, one after another: i = part * tiles_n + tn goes up by `pairs`
-// without a division (one and a binary search of the table a tile took the
-// roles of a single thread 0.4 us).
+// without a division, and a part is one access (a division and a binary search a
+// tile took each role 0.4 us).
 struct RowsWalk {
     int part, tn, dpart, dtn;
     __device__ __forceinline__ RowsWalk(const ExpertsArgs &a, unsigned pair) {
@@ -151,7 +158,8 @@ struct RowsWalk {
         Tile x;
         x.tn = tn;
         if (part < kPartTable) {
-            x.e = t.expert[part];
+            const int2 p = t.part[part];
+            x.row0 = p.x, x.e = p.y & 0xFFFF, x.end = p.x + (p.y >> 16);
         } else {
             int lo = 0, hi = a.experts;  // first[lo] <= part < first[hi]
             while (hi - lo > 1) {
@@ -162,14 +170,11 @@ struct RowsWalk {
                     hi = m;
             }
             x.e = lo;
+            const Run r = run_of(t.offsets[lo], t.offsets[lo + 1], a.rows);
+            const int step = part_step(r.hi - r.lo, (r.hi - r.lo + (1 << t.shift) - 1) >> t.shift);
+            x.row0 = r.lo + (part - t.first[lo]) * step;
+            x.end = min(r.hi, x.row0 + step);
         }
-        const Run r = run_of(t.offsets[x.e], t.offsets[x.e + 1], a.rows);
-        // an expert's parts are equal, in steps of 32 (8192 rows of 3584x2048: 444 us, the
-        // last one what is left: 452); none is empty, because a step is no more than the most
-        const int parts = (r.hi - r.lo + (1 << t.shift) - 1) >> t.shift;
-        const int step = parts > 1 ? ((r.hi - r.lo + parts - 1) / parts + 31) & ~31 : r.hi - r.lo;
-        x.row0 = r.lo + (part - t.first[x.e]) * step;
-        x.end = min(r.hi, x.row0 + step);
         x.n = (x.end - x.row0 + 31) & ~31;
         return x;
     }
@@ -196,7 +201,7 @@ __device__ __forceinline__ int make_table(const ExpertsArgs &a, Table &t, float 
     static_assert(1 << kLargest == kExpertRows, "parts");
     static_assert(kEach * kRowsThreads >= kMaxExperts && kWarps <= 32, "a thread's experts, a lane a warp");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int o[kEach + 1], rows[kEach], most_rows = 0;
+    int o[kEach + 1], rows[kEach], lo[kEach], most_rows = 0;
     // from L2: a chained kernel reads them ahead of its wait
 #pragma unroll
     for (int j = 0; j <= kEach; ++j) {
@@ -208,6 +213,7 @@ __device__ __forceinline__ int make_table(const ExpertsArgs &a, Table &t, float 
         const int e = tid * kEach + j;
         if (e <= a.experts) t.offsets[e] = o[j];
         const Run r = run_of(o[j], o[j + 1], a.rows);
+        lo[j] = r.lo;
         rows[j] = e < a.experts ? r.hi - r.lo : 0;
         most_rows = max(most_rows, rows[j]);
     }
@@ -253,7 +259,21 @@ __device__ __forceinline__ int make_table(const ExpertsArgs &a, Table &t, float 
     for (int j = 0; j < kEach; ++j) {
         const int e = tid * kEach + j;
         if (e < a.experts) t.first[e] = before;
-        for (int k = before; k < min(before + parts[j], kPartTable); ++k) t.expert[k] = (uint16_t)e;
+        const int step = part_step(rows[j], parts[j]);
+        auto put = [&](int e, int lo, int rows, int step, int at, int k) {
+            if (at + k < kPartTable) t.part[at + k] = make_int2(lo + k * step, e | min(step, rows - k * step) << 16);
+        };
+        // few parts by the expert's thread, many by its warp
+        constexpr int kFew = 8;
+        if (parts[j] <= kFew)
+            for (int k = 0; k < parts[j]; ++k) put(e, lo[j], rows[j], step, before, k);
+        for (unsigned many = __ballot_sync(0xFFFFFFFFu, parts[j] > kFew); many != 0u; many &= many - 1u) {
+            const int from = __ffs(many) - 1;
+            const int e1 = __shfl_sync(0xFFFFFFFFu, e, from), lo1 = __shfl_sync(0xFFFFFFFFu, lo[j], from),
+                      rows1 = __shfl_sync(0xFFFFFFFFu, rows[j], from), step1 = __shfl_sync(0xFFFFFFFFu, step, from),
+                      at1 = __shfl_sync(0xFFFFFFFFu, before, from), parts1 = __shfl_sync(0xFFFFFFFFu, parts[j], from);
+            for (int k = lane; k < parts1 && at1 + k < kPartTable; k += 32) put(e1, lo1, rows1, step1, at1, k);
+        }
         before += parts[j];
         if (e == a.experts - 1) t.first[a.experts] = before;
     }
@@ -276,8 +296,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
     const uint32_t sbase = (raw + 1023u) & ~1023u;
     const uint32_t turn = sbase + kRowsRing;
     const uint32_t bars = turn + kEpiGroups * kTurnBytes;
-    int *const words = reinterpret_cast<int *>(smem_raw + (bars + kRowsBars - raw));
-    Table table = {words, words + kMaxExperts + 4, reinterpret_cast<uint16_t *>(words + 2 * (kMaxExperts + 4)), 0};
+    int2 *const part_table = reinterpret_cast<int2 *>(smem_raw + (bars + kRowsBars - raw));
+    int *const words = reinterpret_cast<int *>(part_table + kPartTable);
+    Table table = {part_table, words, words + kMaxExperts + 4, 0};
     auto full_bar = [&](int s) { return bars + 8u * s; };  // leader's are used
     auto empty_bar = [&](int s) { return bars + 8u * (kRowsStages + s); };
     auto tfull_bar = [&](int t) { return bars + 8u * (2 * kRowsStages + t); };
