@@ -8,44 +8,54 @@ namespace route {
 namespace {
 
 constexpr int kSortThreads = 1024;
-// Warps that go through the pairs: sixteen cost less to set up (8192 pairs 6.1
-// us, thirty-two 7.9; 65536 11.4 and 12.1), thirty-two go through many faster
-// (1048576 pairs 90 us, 97).
+// Warps that go through the pairs: sixteen cost less to set up (in one cluster 8192
+// pairs 6.1 us, thirty-two 7.9), thirty-two go through many faster (1048576 pairs
+// 90 us, 97).
 constexpr int kSortWarps = 16, kSortMoreWarps = 32;
 constexpr int kSortMorePairs = 1 << 18;
+// Slices of the experts, a cluster each, from so many pairs and experts on (65536
+// pairs of 896 experts: one 11.4 us, six 6.5; eight clusters of sixteen CTAs do not
+// run side by side and took twice four's time).
+constexpr int kSortSlices = 6, kSortSlicePairs = 1 << 10, kSortSliceExperts = 16;
 constexpr int kSortMaxCtas = 16;  // of the cluster
 constexpr int kSortAhead = 8;     // groups of 32 pairs whose ids are on the way together
 
 // ---- sort -------------------------------------------------------------------------
 //
-// One cluster sorts all pairs.  Every warp takes a run of them, counts its
-// pairs of each expert in shared memory, and after the counts have been summed
-// over the warps before it, the CTAs before its own (distributed shared memory)
-// and the experts before each, it goes through its run once more and gives
-// each pair its place: the order within an expert is that of the pairs.
-__global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_constant__ SortArgs a, int warps) {
+// A cluster sorts the pairs of its slice of the experts (one cluster all of
+// them, where the pairs are few).  Every warp takes a run of all pairs, counts its
+// pairs of each of the slice's experts in shared memory, and how many are at
+// experts below it; after the counts have been summed over the warps before it,
+// the CTAs before its own (distributed shared memory) and the experts before each,
+// it goes through its run once more and gives each pair its place: the order within
+// an expert is that of the pairs.
+//
+// Bound by latencies up to 30,000 pairs (128 pairs 3.1 us, 8192 4.4, 32768 5.3),
+// then by the votes for equal keys and the scattered stores (65536 pairs 6.5 us,
+// 1048576 40).
+__global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_constant__ SortArgs a, int warps, int run,
+                                                               int per_slice) {
     extern __shared__ int smem[];
-    int *counts = smem;                          // [warps][experts]
-    int *total = smem + warps * a.experts;       // [experts], read by the cluster
-    int *base = total + a.experts;               // [experts]
-    __shared__ int s_scan[kSortThreads / 32];
+    __shared__ int s_scan[kSortThreads / 32], s_lows[kSortThreads / 32], s_low;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // after the wait: only the offsets and places are still to come, which no
     // kernel reads ahead of its own
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int ctas = gridDim.x, rank = blockIdx.x;
-    const int E = a.experts;
+    const int ctas = gridDim.x, slices = gridDim.y, slice = blockIdx.y, rank = blockIdx.x;
+    const int e0 = slice * per_slice, E = min(per_slice, a.experts - e0);
+    int *counts = smem;                          // [warps][E]
+    int *total = smem + warps * E;               // [E] and the pairs below, read by the cluster
+    int *base = total + E + 1;                   // [E]
     const int pairs = a.rows * a.topk;
-    // a warp's run: whole groups of 32
-    const int runs = ctas * warps;
-    const int run = ((pairs + runs - 1) / runs + 31) & ~31;
+    // a warp's run of pairs: whole groups of 32
     const long long from = (long long)(rank * warps + warp) * run;
     const int p0 = warp < warps ? (int)(from < pairs ? from : pairs) : pairs;
     const int p1 = (long long)p0 + run < pairs ? p0 + run : pairs;
-    // the first ids are on their way while the counts are cleared
+    // an expert's number in the slice: negative below it and where the id is nobody's
+    constexpr int kNone = -0x7FFFFFFF - 1;
     auto key_of = [&](int p) {
-        if (p >= p1) return -1;
+        if (p >= p1) return kNone;
         int id;
         if (a.ld_ids == a.topk) {
             id = a.ids[p];
@@ -54,9 +64,10 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
             id = a.ids[(long long)r * a.ld_ids + (p - r * a.topk)];
         }
         const int k = (int)((unsigned)id - (unsigned)a.first);
-        return id >= a.first && k < E ? k : -1;
+        return id >= a.first && k < a.experts ? k - e0 : kNone;
     };
-    int keys[kSortAhead];
+    // the first ids are on their way while the counts are cleared
+    int keys[kSortAhead], low = 0;
     auto fetch = [&](int p) {
 #pragma unroll
         for (int j = 0; j < kSortAhead; ++j) keys[j] = key_of(p + 32 * j + lane);
@@ -72,8 +83,18 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
     for (int p = p0; p < p1; p += 32 * kSortAhead) {
         if (p > p0) fetch(p);
 #pragma unroll
-        for (int j = 0; j < kSortAhead; ++j)
-            if (keys[j] >= 0) atomicAdd(&counts[warp * E + keys[j]], 1);
+        for (int j = 0; j < kSortAhead; ++j) {
+            if ((unsigned)keys[j] < (unsigned)E)
+                atomicAdd(&counts[warp * E + keys[j]], 1);
+            else
+                low += keys[j] < 0 && keys[j] != kNone;
+        }
+    }
+    if (slices > 1) {
+        low = __reduce_add_sync(0xFFFFFFFFu, low);
+        if (lane == 0) s_lows[warp] = low;
+    } else if (tid == 0) {
+        s_low = 0;
     }
     __syncthreads();
     // counts become what the CTA's warps before hold; totals of the CTA
@@ -92,18 +113,26 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
         }
         total[e] = mine;
     }
+    if (slices > 1 && warp == kSortThreads / 32 - 1) {
+        low = __reduce_add_sync(0xFFFFFFFFu, s_lows[lane]);
+        if (lane == 0) total[E] = s_low = low;
+    }
     int before = 0, all = mine;
     if (ctas > 1) {
+        auto of_cta = [&](int i, int j) {
+            int c;
+            asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                         : "=r"(c)
+                         : "r"(ptx::map_to_rank(ptx::smem_addr(total + i), (uint32_t)j))
+                         : "memory");
+            return c;
+        };
         ptx::cluster_sync();
         if (e < E) {
             int c[kSortMaxCtas];
 #pragma unroll
             for (int j = 0; j < kSortMaxCtas; ++j)
-                if (j < ctas)
-                    asm volatile("ld.shared::cluster.s32 %0, [%1];"
-                                 : "=r"(c[j])
-                                 : "r"(ptx::map_to_rank(ptx::smem_addr(total + e), (uint32_t)j))
-                                 : "memory");
+                if (j < ctas) c[j] = of_cta(e, j);
             all = 0;
 #pragma unroll
             for (int j = 0; j < kSortMaxCtas; ++j)
@@ -112,6 +141,11 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
                     all += c[j];
                 }
         }
+        if (warp == kSortThreads / 32 - 1 && slices > 1) {  // the pairs below the slice, of all CTAs
+            const int t = __reduce_add_sync(0xFFFFFFFFu, lane < ctas ? of_cta(E, lane) : 0);
+            if (lane == 0) s_low = t;
+        }
+        __syncwarp();
         ptx::cluster_arrive();  // after the last remote read
     }
     // exclusive sums over the experts
@@ -133,12 +167,12 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
         s_scan[lane] = t;
     }
     __syncthreads();
-    scan += warp > 0 ? s_scan[warp - 1] : 0;
+    scan += s_low + (warp > 0 ? s_scan[warp - 1] : 0);
     if (e < E) {
         base[e] = scan - all + before;
         if (rank == 0) {
-            a.offsets[e + 1] = scan;
-            if (e == 0) a.offsets[0] = 0;
+            a.offsets[e0 + e + 1] = scan;
+            if (e0 + e == 0) a.offsets[0] = 0;
         }
     }
     __syncthreads();
@@ -147,16 +181,19 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
         if (!once) fetch(p);
 #pragma unroll
         for (int j = 0; j < kSortAhead; ++j) {
-            const int at0 = p + 32 * j, k = keys[j];
+            const int at0 = p + 32 * j;
             if (at0 >= p1) break;
+            const bool here = (unsigned)keys[j] < (unsigned)E;
+            const int k = here ? keys[j] : -1;
             const unsigned same = __match_any_sync(0xFFFFFFFFu, k);
-            const int at = k >= 0 ? base[k] + counts[warp * E + k] + __popc(same & ((1u << lane) - 1u)) : -1;
+            const int at = here ? base[k] + counts[warp * E + k] + __popc(same & ((1u << lane) - 1u)) : -1;
             __syncwarp();
-            if (k >= 0 && (same >> lane) == 1u) counts[warp * E + k] += __popc(same);  // the last of them
+            if (here && (same >> lane) == 1u) counts[warp * E + k] += __popc(same);  // the last of them
             __syncwarp();
-            if (at0 + lane < p1) {
+            // nobody's pairs are the first slice's to mark
+            if (at0 + lane < p1 && (here || (slice == 0 && keys[j] == kNone))) {
                 a.place[at0 + lane] = at;
-                if (k >= 0 && a.source != nullptr) a.source[at] = at0 + lane;
+                if (here && a.source != nullptr) a.source[at] = at0 + lane;
             }
         }
     }
@@ -417,7 +454,7 @@ cudaError_t launch(const void *k, dim3 grid, unsigned block, size_t smem, unsign
     return cudaLaunchKernelExC(&c, k, params);
 }
 
-size_t sort_smem(int warps, int experts) { return ((size_t)warps + 2) * experts * sizeof(int); }
+size_t sort_smem(int warps, int experts) { return (((size_t)warps + 2) * experts + 1) * sizeof(int); }
 
 #define ROUTE_MOVE(K, A, V)                                                              \
     ((A).type == kFp32   ? reinterpret_cast<const void *>(K<kFp32, V>)                   \
@@ -433,32 +470,41 @@ cudaError_t sort_configure() {
     return e != cudaSuccess ? e : cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
-int sort_max_ctas() {
-    cudaLaunchConfig_t c = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kSortMaxCtas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    c.gridDim = dim3(kSortMaxCtas);
-    c.blockDim = dim3(kSortThreads);
-    c.dynamicSmemBytes = sort_smem(kSortMoreWarps, kMaxExperts);
-    c.attrs = attr;
-    c.numAttrs = 1;
-    int clusters = 0;
-    if (cudaOccupancyMaxActiveClusters(&clusters, sort_kernel, &c) != cudaSuccess) cudaGetLastError(), clusters = 0;
-    return clusters > 0 ? kSortMaxCtas : 8;
+SortShape sort_shape() {
+    for (int ctas : {kSortMaxCtas, 8}) {
+        cudaLaunchConfig_t c = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)ctas;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        c.gridDim = dim3((unsigned)ctas);
+        c.blockDim = dim3(kSortThreads);
+        c.dynamicSmemBytes = sort_smem(kSortMoreWarps, kMaxExperts);
+        c.attrs = attr;
+        c.numAttrs = 1;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, sort_kernel, &c) != cudaSuccess) cudaGetLastError(), clusters = 0;
+        if (clusters > 0) return {ctas, clusters < kSortSlices ? clusters : kSortSlices};
+    }
+    return {8, 1};
 }
 
-cudaError_t sort_launch(const SortArgs &args, int max_ctas, cudaStream_t stream) {
+cudaError_t sort_launch(const SortArgs &args, SortShape most_of, cudaStream_t stream) {
     const long long pairs = (long long)args.rows * args.topk;
     const long long groups = (pairs + 31) / 32;
     const int most = pairs < kSortMorePairs ? kSortWarps : kSortMoreWarps;
     int warps = groups < most ? (int)(groups < 1 ? 1 : groups) : most;
     unsigned ctas = 1;
-    while (ctas < (unsigned)max_ctas && groups > 2ll * ctas * most) ctas *= 2;
-    void *params[] = {const_cast<SortArgs *>(&args), &warps};
-    return launch(reinterpret_cast<const void *>(sort_kernel), dim3(ctas), kSortThreads, sort_smem(warps, args.experts),
-                  ctas, params, stream);
+    while (ctas < (unsigned)most_of.ctas && groups > 2ll * ctas * most) ctas *= 2;
+    const int slices = pairs >= kSortSlicePairs && args.experts >= kSortSliceExperts ? most_of.slices : 1;
+    int per_slice = (args.experts + slices - 1) / slices;
+    const long long runs = (long long)ctas * warps;
+    int run = (int)(((pairs + runs - 1) / runs + 31) & ~31ll);
+    void *params[] = {const_cast<SortArgs *>(&args), &warps, &run, &per_slice};
+    // (slices that are rounded up may leave the last without experts)
+    return launch(reinterpret_cast<const void *>(sort_kernel),
+                  dim3(ctas, (unsigned)((args.experts + per_slice - 1) / per_slice)), kSortThreads,
+                  sort_smem(warps, per_slice), ctas, params, stream);
 }
 
 cudaError_t gather_launch(const MoveArgs &args, int sms, cudaStream_t stream) {

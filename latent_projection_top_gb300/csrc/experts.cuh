@@ -21,8 +21,10 @@ struct SortArgs {
     int *source;                // [rows * topk] or null
 };
 cudaError_t sort_configure();
-int sort_max_ctas();  // that fit a cluster of the current device
-cudaError_t sort_launch(const SortArgs &args, int max_ctas, cudaStream_t stream);
+// The CTAs that a cluster may have and the clusters that run side by side on the
+// current device.
+SortShape sort_shape();
+cudaError_t sort_launch(const SortArgs &args, SortShape most_of, cudaStream_t stream);
 
 // What gather and combine, and their gradients, read and write: rows of `dim`
 // values in the tokens' order (a) and in the experts' order (b).

@@ -210,7 +210,7 @@ route_status route_dispatch_sort(const route_layer *p, int rows, const int32_t *
     a.ids = ids, a.ld_ids = stride_of(rows, ld_ids, p->topk);
     a.offsets = offsets, a.place = place, a.source = source;
     DeviceGuard guard(p->device);
-    return launched(sort_launch(a, p->sort_ctas, static_cast<cudaStream_t>(stream)), "sort kernel launch");
+    return launched(sort_launch(a, p->sort, static_cast<cudaStream_t>(stream)), "sort kernel launch");
 }
 
 route_status route_dispatch_gather(const route_layer *p, int rows, const void *x, int64_t ld_x,

@@ -162,6 +162,11 @@ cudaError_t dz_launch(const DzArgs &args, cudaStream_t stream);
 // here: the sums then run beside it.
 cudaError_t bias_launch(const DzArgs &args, bool after, cudaStream_t stream);
 
+// What a sort may have of the device (experts.cuh).
+struct SortShape {
+    int ctas, slices;
+};
+
 struct NormArgs {
     int rows, dim, type;
     float eps;

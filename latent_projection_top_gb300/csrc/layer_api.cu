@@ -455,7 +455,7 @@ route_status layer_finish_prepare(route_layer *p, int device, route_layer **out)
     p->sms = prop.multiProcessorCount;
     p->pairs = p->sms / 2;
     p->timeout_ns = kTimeoutNs;
-    if (p->kind == kDispatch) p->sort_ctas = sort_max_ctas();
+    if (p->kind == kDispatch) p->sort = sort_shape();
 
     size_t at = 0;
     auto area = [&](size_t bytes) {

@@ -43,7 +43,7 @@ struct route_layer {
     int rows, k, f, n;
     int type, out_type, act, train;
     int experts, first, topk;  // routed experts' plans: experts here, the first one's id, ids a row
-    int sort_ctas;     // a dispatch plan's: CTAs that a sort may have
+    route::SortShape sort;  // a dispatch plan's: what a sort may have of the device
     int device, sms, pairs;
     int test_stall;
     unsigned long long timeout_ns;
