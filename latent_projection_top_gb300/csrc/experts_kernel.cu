@@ -182,12 +182,13 @@ struct RowsWalk {
 
 // The time of a launch whose parts have up to `n` rows, in ns: a k-block of a
 // tile takes as long as its copies to an SM, 95 bytes a nanosecond, or its MMAs
-// (the same at 256 rows), its epilogue `epi_ns` for 64 rows; the last one is in
-// nobody's shadow.
+// (the same at 256 rows), its epilogue `epi_ns` for 64 rows and 400 for itself; the
+// last one is in nobody's shadow.  (Without the 400 an epilogue-bound launch of
+// many rows was cut small: 19456 rows of 512x1024 104 us, 86 with it.)
 __device__ __forceinline__ float launch_ns(const ExpertsArgs &a, int parts, int n, float epi_ns) {
     const float rounds = ceilf((float)parts * a.tiles_a_pair);
     const float load = (float)a.kblocks * (172.f + 0.667f * n), epi = (float)((n + 63) >> 6) * epi_ns;
-    return rounds * fmaxf(load, epi) + epi;
+    return rounds * fmaxf(load, epi + 400.f) + epi;
 }
 
 // All threads: the table of parts.  Returns the number of them; `most`: the
@@ -331,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowsThreads, 1)
     const RowsWalk begin(args, pair);
     if (!args.chained) asm volatile("griddepcontrol.wait;" ::: "memory");
     int most;
-    constexpr float kEpiNs = EPI == kEpiLinear ? 800.f : EPI == kEpiGated ? 1200.f : 2200.f;
+    constexpr float kEpiNs = EPI == kEpiLinear ? 800.f : EPI == kEpiGated ? 1200.f : 1500.f;
     const int parts = make_table(args, table, kEpiNs, s_scan, most);
     const uint32_t stage = kWBytes + (uint32_t)(most / 2) * kRowBytes;
     const int S = min(kRowsStages, (int)(kRowsRing / stage));
