@@ -181,14 +181,15 @@ struct RowsWalk {
 };
 
 // The time of a launch whose parts have up to `n` rows, in ns: a k-block of a
-// tile takes as long as its copies to an SM, 95 bytes a nanosecond, or its MMAs
-// (the same at 256 rows), its epilogue `epi_ns` for 64 rows and 400 for itself; the
-// last one is in nobody's shadow.  (Without the 400 an epilogue-bound launch of
-// many rows was cut small: 19456 rows of 512x1024 104 us, 86 with it.)
+// tile takes 342 at 256 rows and 290 at 128 (a tile of half the rows is not half as
+// long), its epilogue `epi_ns` for 64 rows and 400 for itself; the last one is in
+// nobody's shadow.  Taking a k-block's time for that of its copies, and an epilogue's
+// without the 400, cut launches of many rows too small: 19456 rows of 512x1024 104
+// us, so 81; 11733 of 648x1528 at five experts 85 and 64.
 __device__ __forceinline__ float launch_ns(const ExpertsArgs &a, int parts, int n, float epi_ns) {
     const float rounds = ceilf((float)parts * a.tiles_a_pair);
-    const float load = (float)a.kblocks * (172.f + 0.667f * n), epi = (float)((n + 63) >> 6) * epi_ns;
-    return rounds * fmaxf(load, epi + 400.f) + epi;
+    const float blocks = (float)a.kblocks * (237.f + 0.41f * n), epi = (float)((n + 63) >> 6) * epi_ns;
+    return rounds * fmaxf(blocks, epi + 400.f) + epi;
 }
 
 // All threads: the table of parts.  Returns the number of them; `most`: the
