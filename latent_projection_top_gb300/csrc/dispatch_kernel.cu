@@ -202,222 +202,361 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
 
 // ---- moves ------------------------------------------------------------------------
 
-// The values of one 16-byte piece (W of a type), or of one element.
+// What lies between a matrix's first value and its last.
+struct Span {
+    const char *lo, *hi;
+    __device__ __forceinline__ Span(const void *p, long long rows, long long ld, int dim, int es)
+        : lo(static_cast<const char *>(p)), hi(lo + ((rows - 1) * ld + dim) * es) {}
+};
+
+// 16 bytes of a row.  VEC: every row of every matrix lies on 16 bytes.  Else they
+// are taken out of the two aligned 16 bytes that they lie in, of which what
+// belongs to others is not used, and the pieces of a row are those that lie
+// aligned where they are written (4096x1001 BF16, 4 places: combine with a residual
+// 16.3 us and its gradient 24, a value at a time 23.5 and 31; 4096x2047 from 16
+// places 74 and 102.  FP32 gains little, 2049x1001 from 4 places 9.7 and 10.1,
+// and loses in combine's gradient, 4096x1001 40 and 35).
 template <int TY, bool VEC>
 struct Piece {
-    static constexpr int kN = VEC ? 16 / layer_esize(TY) : 1;
-    uint32_t w[VEC ? 4 : 1];
-    __device__ __forceinline__ void load(const void *p, long long i) {
+    static constexpr int kSize = layer_esize(TY), kN = 16 / kSize;
+    uint32_t w[VEC ? 4 : 8];
+    unsigned off = 0;  // where in w they begin, bytes
+
+    // Pieces of a row that is written at p (or read, where it is not written), and
+    // how many values there would be before its first, in the first piece.
+    static __device__ __forceinline__ int before(const void *p) {
+        return VEC ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15u) / kSize;
+    }
+    static __device__ __forceinline__ int count(int dim, int skip) { return (dim + skip + kN - 1) / kN; }
+
+    __device__ __forceinline__ void load(const char *p, const Span &in) {
         if constexpr (VEC) {
-            const uint4 t = *reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + i * layer_esize(TY));
+            const uint4 t = *reinterpret_cast<const uint4 *>(p);
             w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
-        } else if constexpr (TY == kFp32) {
-            w[0] = static_cast<const uint32_t *>(p)[i];
         } else {
-            w[0] = static_cast<const uint16_t *>(p)[i];
+            off = (unsigned)(reinterpret_cast<uintptr_t>(p) & 15u);
+            const char *q = p - off, *q1 = off != 0u ? q + 16 : q;
+            if (q >= in.lo && q1 + 16 <= in.hi) {
+                const uint4 t = *reinterpret_cast<const uint4 *>(q), u = *reinterpret_cast<const uint4 *>(q1);
+                w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
+                w[4] = u.x, w[5] = u.y, w[6] = u.z, w[7] = u.w;
+            } else {  // the matrix's first and last
+                off = 0u;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = 0u;
+#pragma unroll
+                    for (int h = 0; h < 4 / kSize; ++h) {
+                        const char *at = p + 4 * e + kSize * h;
+                        if (at < in.lo || at >= in.hi) continue;
+                        if constexpr (kSize == 4)
+                            w[e] = *reinterpret_cast<const uint32_t *>(at);
+                        else
+                            w[e] |= (uint32_t)*reinterpret_cast<const uint16_t *>(at) << (16 * h);
+                    }
+                }
+            }
         }
     }
-    __device__ __forceinline__ void store(void *p, long long i) const {
+    __device__ __forceinline__ void words(uint32_t (&o)[4]) const {
         if constexpr (VEC) {
-            *reinterpret_cast<uint4 *>(static_cast<char *>(p) + i * layer_esize(TY)) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else if constexpr (TY == kFp32) {
-            static_cast<uint32_t *>(p)[i] = w[0];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = w[e];
         } else {
-            static_cast<uint16_t *>(p)[i] = (uint16_t)w[0];
+            uint32_t t[7], u[5];
+#pragma unroll
+            for (int e = 0; e < 7; ++e) t[e] = off & 4u ? w[e + 1] : w[e];
+#pragma unroll
+            for (int e = 0; e < 5; ++e) u[e] = off & 8u ? t[e + 2] : t[e];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = kSize == 4 ? u[e] : __funnelshift_r(u[e], u[e + 1], 8u * (off & 3u));
         }
     }
     __device__ __forceinline__ void values(float (&v)[kN]) const {
+        uint32_t o[4];
+        words(o);
         if constexpr (TY == kFp32) {
 #pragma unroll
-            for (int e = 0; e < kN; ++e) v[e] = __uint_as_float(w[e]);
-        } else if constexpr (VEC) {
+            for (int e = 0; e < kN; ++e) v[e] = __uint_as_float(o[e]);
+        } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float2 f = unpack16(w[e], TY);
+                const float2 f = unpack16(o[e], TY);
                 v[2 * e] = f.x, v[2 * e + 1] = f.y;
             }
-        } else {
-            v[0] = unpack16(w[0], TY).x;
         }
     }
-    __device__ __forceinline__ void set(const float (&v)[kN]) {
+    // The piece's values from the c-th of `row` on, those of them that the row has.
+    static __device__ __forceinline__ void store(char *row, int c, int dim, const uint32_t (&o)[4]) {
+        char *p = row + (long long)c * kSize;
+        if (VEC || (c >= 0 && c + kN <= dim)) {
+            *reinterpret_cast<uint4 *>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kN; ++e) {
+                if (c + e < 0 || c + e >= dim) continue;
+                if constexpr (kSize == 4)
+                    reinterpret_cast<uint32_t *>(p)[e] = o[e];
+                else
+                    reinterpret_cast<uint16_t *>(p)[e] = (uint16_t)(o[e / 2] >> (16 * (e % 2)));
+            }
+        }
+    }
+    static __device__ __forceinline__ void store(char *row, int c, int dim, const float (&v)[kN]) {
+        uint32_t o[4];
         if constexpr (TY == kFp32) {
 #pragma unroll
-            for (int e = 0; e < kN; ++e) w[e] = __float_as_uint(v[e]);
-        } else if constexpr (VEC) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = pack16(v[2 * e], v[2 * e + 1], TY);
+            for (int e = 0; e < kN; ++e) o[e] = __float_as_uint(v[e]);
         } else {
-            w[0] = pack16(v[0], 0.f, TY) & 0xFFFFu;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = pack16(v[2 * e], v[2 * e + 1], TY);
         }
+        store(row, c, dim, o);
     }
 };
+
+template <int TY>
+__device__ __forceinline__ const char *row_of(const void *p, long long ld, long long r) {
+    return static_cast<const char *>(p) + r * ld * layer_esize(TY);
+}
+template <int TY>
+__device__ __forceinline__ char *row_of(void *p, long long ld, long long r) {
+    return static_cast<char *>(p) + r * ld * layer_esize(TY);
+}
 
 // A row's places that are there, in the row's order.
 struct Places {
     int n;
     int at[kMaxTopk];
     float w[kMaxTopk];
-    int j[kMaxTopk];
 };
+
+// Row r's places, found by the row's first 32 threads (none of a row that is not
+// there); for all of the block.
 __device__ __forceinline__ void find_places(const MoveArgs &a, int r, Places &s) {
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
         const long long i = (long long)r * a.topk + lane;
-        const int p = lane < a.topk ? a.place[i] : -1;
+        const bool mine = lane < a.topk && r < a.rows;
+        const int p = mine ? a.place[i] : -1;
         const bool there = p >= 0 && p < a.pairs;
         const unsigned all = __ballot_sync(0xFFFFFFFFu, there);
         if (there) {
             const int k = __popc(all & ((1u << lane) - 1u));
             s.at[k] = p;
             s.w[k] = a.weights != nullptr ? a.weights[i] : 1.f;
-            s.j[k] = lane;
         }
         if (lane == 0) s.n = __popc(all);
-        if (a.dweights != nullptr && lane < a.topk && !there) a.dweights[i] = 0.f;
     }
     __syncthreads();
 }
 
-// A block a row: out[place] = x[row], each row read once.  Bound by HBM: 4096 rows
-// of 3584 BF16 to 16 places 74 us (499 MB, 6.7 TB/s).
-template <int ES, bool VEC>
+// Rows of gather and combine: a row's threads, a piece each, up to 256; rows of a
+// block of 128 threads (a block of one warp a row: half the warps that an SM
+// holds); and blocks of a row: one, or, where the rows are few, as many as its
+// pieces take (1 row of 3584 from 16 places 4.9 us with one).
+constexpr int kRowThreads = 256, kBlockThreads = 128, kMostRows = kBlockThreads / 32;
+struct RowShape {
+    dim3 grid, block;
+    RowShape(const MoveArgs &a, int sms) {
+        const int pieces = (a.dim * layer_esize(a.type) + 15) / 16;
+        const unsigned threads = pieces < kRowThreads ? (unsigned)(pieces + 31) / 32 * 32 : kRowThreads;
+        const unsigned rows = threads < kBlockThreads ? kBlockThreads / threads : 1u;
+        block = dim3(threads, rows);
+        const unsigned blocks = (unsigned)(pieces + kRowThreads - 1) / kRowThreads;
+        grid = dim3(((unsigned)a.rows + rows - 1) / rows, (long long)a.rows * blocks > 4ll * sms ? 1u : blocks);
+    }
+};
+
+// out[place] = x[row], each row read once.  Bound by HBM: 4096 rows of 3584 BF16 to
+// 16 places 74 us (499 MB, 6.7 TB/s).  Short rows are bound by how many are on
+// their way, so a row has no more threads than pieces (with the sort, 4096x128 to 16
+// places 10.4 us; a block of 256 threads a row 14.3).
+template <int ES>
 __global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ MoveArgs a) {
-    using P = Piece<ES == 4 ? kFp32 : kBf16, VEC>;
-    __shared__ Places s;
+    constexpr int TY = ES == 4 ? kFp32 : kBf16;
+    using P = Piece<TY, true>;
+    __shared__ Places places[kMostRows];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int r = blockIdx.x;
+    const int r = blockIdx.x * blockDim.y + threadIdx.y;
+    Places &s = places[threadIdx.y];
+    const int first = blockIdx.y * blockDim.x + threadIdx.x, step = gridDim.y * blockDim.x;
+    const Span in(a.a, a.rows, a.ld_a, a.dim, ES);
+    const char *x = row_of<TY>(a.a, a.ld_a, r);
+    const int pieces = P::count(a.dim, 0);
+    P p;
+    if (first < pieces && r < a.rows) p.load(x + 16ll * first, in);  // beside the places
     find_places(a, r, s);
-    const int n = s.n, pieces = a.dim / P::kN;
-    for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < pieces && n > 0; i += gridDim.y * blockDim.x) {
-        P p;
-        p.load(a.a, r * a.ld_a + (long long)i * P::kN);
-        for (int k = 0; k < n; ++k) p.store(a.out, s.at[k] * a.ld_out + (long long)i * P::kN);
+    const int n = s.n;
+    for (int i = first; i < pieces && n > 0; i += step) {
+        if (i != first) p.load(x + 16ll * i, in);
+        uint32_t o[4];
+        p.words(o);
+        for (int k = 0; k < n; ++k) P::store(row_of<TY>(a.out, a.ld_out, s.at[k]), i * P::kN, a.dim, o);
     }
 }
 
-// A block a row: out[row] = residual[row] + sum_j w_j b[place_j], in the order
-// of j.  Bound by HBM: 4096 rows of 3584 BF16 from 16 places, with a residual, 82
-// us (529 MB, 6.5 TB/s), as the gather's gradient 74 (6.7).
-constexpr int kAhead = 8;  // experts' rows on the way together
-template <int TY, bool VEC>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ MoveArgs a) {
-    using P = Piece<TY, VEC>;
-    __shared__ Places s;
+// The pair of (row, place) that `threads` threads (a power of two) of a block have.
+struct Pair {
+    int part;  // which of them this thread is
+    unsigned at, row;
+    int place;  // -1: there is none
+    bool mine;  // the pair is there, with or without a place
+    __device__ __forceinline__ Pair(const MoveArgs &a, int threads)
+        : part((int)threadIdx.x & (threads - 1)),
+          at(blockIdx.x * (blockDim.x / (unsigned)threads) + threadIdx.x / (unsigned)threads),
+          row(at / (unsigned)a.topk), place(-1), mine(row < (unsigned)a.rows) {
+        if (mine) place = a.place[at];
+        if (place >= a.pairs) place = -1;
+    }
+};
+
+// gather_kernel for rows off 16 bytes: each place has its own alignment, and so its
+// own pieces.
+template <int ES>
+__global__ void __launch_bounds__(256) gather_any_kernel(const __grid_constant__ MoveArgs a, int threads) {
+    constexpr int TY = ES == 4 ? kFp32 : kBf16;
+    using P = Piece<TY, false>;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int r = blockIdx.x;
+    const Pair pair(a, threads);
+    if (pair.place < 0) return;
+    const Span in(a.a, a.rows, a.ld_a, a.dim, ES);
+    const char *x = row_of<TY>(a.a, a.ld_a, pair.row);
+    char *out = row_of<TY>(a.out, a.ld_out, pair.place);
+    const int skip = P::before(out), pieces = P::count(a.dim, skip);
+    for (int i = pair.part; i < pieces; i += threads) {
+        const int c = i * P::kN - skip;
+        P p;
+        p.load(x + (long long)c * ES, in);
+        uint32_t o[4];
+        p.words(o);
+        P::store(out, c, a.dim, o);
+    }
+}
+
+// Blocks an SM of combine_kernel: as many rows on their way as the registers of
+// AHEAD places' pieces leave room for (4096x3584 from 16 places: 64 registers 82 us,
+// 69 87).
+constexpr int combine_blocks(bool vec, int ahead) {
+    return ahead <= 2 ? (vec ? 7 : 5) : ahead <= 4 && vec ? 5 : 4;
+}
+
+// out[row] = residual[row] + sum_j w_j b[place_j], in the order of j, AHEAD of the
+// experts' rows on the way together: fewer where a row has few places (4096x2048
+// from 2 places 11.9 us, with eight ahead 18.4).  Bound by HBM: 4096 rows of 3584 BF16
+// from 16 places, with a residual, 83 us (529 MB, 6.4 TB/s), as the gather's gradient
+// 74 (6.7); short rows as gather's (4096x512 from 8 places 6.4 us, a block of 256
+// threads a row 12.5).
+template <int TY, bool VEC, int AHEAD>
+__global__ void __launch_bounds__(256, combine_blocks(VEC, AHEAD))
+    combine_kernel(const __grid_constant__ MoveArgs a) {
+    using P = Piece<TY, VEC>;
+    __shared__ Places places[kMostRows];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int r = blockIdx.x * blockDim.y + threadIdx.y;
+    Places &s = places[threadIdx.y];
     find_places(a, r, s);
-    const int n = s.n, pieces = a.dim / P::kN;
-    // single values: four a thread at a time, so that as much is on the way
-    constexpr int kPieces = VEC ? 1 : 4, kRows = VEC ? kAhead : 4;
-    for (int i0 = blockIdx.y * kPieces * blockDim.x + threadIdx.x; i0 < pieces; i0 += gridDim.y * kPieces * blockDim.x) {
-        float sum[kPieces][P::kN] = {};
-        P res[kPieces];
-        auto each = [&](auto &&f) {
+    if (r >= a.rows) return;
+    char *out = row_of<TY>(a.out, a.ld_out, r);
+    const int n = s.n, skip = P::before(out), pieces = P::count(a.dim, skip);
+    const Span in(a.b, a.pairs, a.ld_b, a.dim, P::kSize), res_in(a.a, a.rows, a.ld_a, a.dim, P::kSize);
+    for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < pieces; i += gridDim.y * blockDim.x) {
+        const int c = i * P::kN - skip;
+        const long long at = (long long)c * P::kSize;
+        float sum[P::kN] = {};
+        P res;
+        if (a.a != nullptr) res.load(row_of<TY>(a.a, a.ld_a, r) + at, res_in);
+        for (int k0 = 0; k0 < n; k0 += AHEAD) {
+            P p[AHEAD];
 #pragma unroll
-            for (int q = 0; q < kPieces; ++q) {
-                const int i = i0 + q * (int)blockDim.x;
-                if (kPieces == 1 || i < pieces) f(q, (long long)i * P::kN);
-            }
-        };
-        if (a.a != nullptr) each([&](int q, long long c) { res[q].load(a.a, r * a.ld_a + c); });
-        for (int k0 = 0; k0 < n; k0 += kRows) {
-            P p[kPieces][kRows];
+            for (int k = 0; k < AHEAD; ++k)
+                if (k0 + k < n) p[k].load(row_of<TY>(a.b, a.ld_b, s.at[k0 + k]) + at, in);
 #pragma unroll
-            for (int k = 0; k < kRows; ++k)
-                if (k0 + k < n) each([&](int q, long long c) { p[q][k].load(a.b, s.at[k0 + k] * a.ld_b + c); });
-#pragma unroll
-            for (int k = 0; k < kRows; ++k)
+            for (int k = 0; k < AHEAD; ++k)
                 if (k0 + k < n) {
                     const float w = s.w[k0 + k];
-                    each([&](int q, long long) {
-                        float v[P::kN];
-                        p[q][k].values(v);
+                    float v[P::kN];
+                    p[k].values(v);
 #pragma unroll
-                        for (int e = 0; e < P::kN; ++e)
-                            sum[q][e] = a.weights != nullptr ? fmaf(w, v[e], sum[q][e]) : sum[q][e] + v[e];
-                    });
+                    for (int e = 0; e < P::kN; ++e)
+                        sum[e] = a.weights != nullptr ? fmaf(w, v[e], sum[e]) : sum[e] + v[e];
                 }
         }
-        each([&](int q, long long c) {
-            if (a.a != nullptr) {
-                float v[P::kN];
-                res[q].values(v);
+        if (a.a != nullptr) {
+            float v[P::kN];
+            res.values(v);
 #pragma unroll
-                for (int e = 0; e < P::kN; ++e) sum[q][e] += v[e];
-            }
-            P o;
-            o.set(sum[q]);
-            o.store(a.out, r * a.ld_out + c);
-        });
+            for (int e = 0; e < P::kN; ++e) sum[e] += v[e];
+        }
+        P::store(out, c, a.dim, sum);
     }
 }
 
-// A block a row, `share` warps an expert's row at a time (all of the block's
-// where there are few): out[place_j] = w_j dout[row], dweights_j = <dout[row],
-// b[place_j]>.  Bound by HBM: 4096 rows of 3584 BF16 at 16 places 153 us (970 MB,
-// 6.3 TB/s); rows off 16 bytes by accesses of one value (4096x1001 at 4 places 31).
-constexpr int kBackWarps = 8;
+// `threads` threads a pair, none of which waits for another pair's: out[place_j] =
+// w_j dout[row], dweights_j = <dout[row], b[place_j]>.  Bound by HBM: 4096 rows of
+// 3584 BF16 at 16 places 148 us (970 MB, 6.5 TB/s; a block a row 153).  Two pieces of
+// each matrix on the way and 48 registers (one piece 175, four and 72 registers
+// 159; 4096x1000 at 4 places 16.1 us, 20.0 and 18.4; a block a row 28.8).
 template <int TY, bool VEC>
-__global__ void __launch_bounds__(32 * kBackWarps) combine_backward_kernel(const __grid_constant__ MoveArgs a) {
+__global__ void __launch_bounds__(256, 5) combine_backward_kernel(const __grid_constant__ MoveArgs a, int threads) {
     using P = Piece<TY, VEC>;
-    // on the way together (16 bytes, 4096x3584: one 178 us, two 169, four 153)
-    constexpr int kPieces = VEC ? 4 : 8;
-    __shared__ Places s;
-    __shared__ float s_dot[kMaxTopk][kBackWarps];
+    constexpr int kPieces = VEC ? 2 : 1;  // on the way together (off 16 bytes a piece is two loads)
+    __shared__ float s_dot[8];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int r = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    find_places(a, r, s);
-    const int n = s.n, pieces = a.dim / P::kN;
-    const int share = n <= 1 ? 8 : n <= 2 ? 4 : n <= 4 ? 2 : 1;
-    const int part = warp & (share - 1);
-    for (int k = warp / share; k < n; k += kBackWarps / share) {
-        const float w = s.w[k];
-        const long long ia = r * a.ld_a, ib = s.at[k] * a.ld_b, io = s.at[k] * a.ld_out;
-        float dot[P::kN] = {};
-        for (int i = part * 32 + lane; i < pieces; i += share * 32 * kPieces) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Pair pair(a, threads);
+    float dot[P::kN] = {};
+    if (pair.place >= 0) {
+        const float w = a.weights != nullptr ? a.weights[pair.at] : 1.f;
+        const Span g_in(a.a, a.rows, a.ld_a, a.dim, P::kSize), y_in(a.b, a.pairs, a.ld_b, a.dim, P::kSize);
+        const char *g_row = row_of<TY>(a.a, a.ld_a, pair.row), *y_row = row_of<TY>(a.b, a.ld_b, pair.place);
+        char *out = row_of<TY>(a.out, a.ld_out, pair.place);
+        const int skip = P::before(a.out != nullptr ? out : y_row), pieces = P::count(a.dim, skip);
+        for (int i = pair.part; i < pieces; i += threads * kPieces) {
             P g[kPieces], y[kPieces];
 #pragma unroll
             for (int q = 0; q < kPieces; ++q) {
-                const int at = i + q * share * 32;
+                const int at = i + q * threads;
                 if (at >= pieces) break;
-                g[q].load(a.a, ia + (long long)at * P::kN);
-                if (a.dweights != nullptr) y[q].load(a.b, ib + (long long)at * P::kN);
+                const long long c = ((long long)at * P::kN - skip) * P::kSize;
+                g[q].load(g_row + c, g_in);
+                if (a.dweights != nullptr) y[q].load(y_row + c, y_in);
             }
 #pragma unroll
             for (int q = 0; q < kPieces; ++q) {
-                const int at = i + q * share * 32;
+                const int at = i + q * threads;
                 if (at >= pieces) break;
+                const int c = at * P::kN - skip;
                 float gv[P::kN], v[P::kN];
                 g[q].values(gv);
                 if (a.dweights != nullptr) {
                     y[q].values(v);
+                    const bool whole = VEC || (c >= 0 && c + P::kN <= a.dim);
 #pragma unroll
-                    for (int e = 0; e < P::kN; ++e) dot[e] = fmaf(gv[e], v[e], dot[e]);
+                    for (int e = 0; e < P::kN; ++e)
+                        if (whole || (c + e >= 0 && c + e < a.dim)) dot[e] = fmaf(gv[e], v[e], dot[e]);
                 }
                 if (a.out != nullptr) {
 #pragma unroll
                     for (int e = 0; e < P::kN; ++e) v[e] = w * gv[e];
-                    P o;
-                    o.set(v);
-                    o.store(a.out, io + (long long)at * P::kN);
+                    P::store(out, c, a.dim, v);
                 }
             }
         }
-        float t = 0.f;
-#pragma unroll
-        for (int e = 0; e < P::kN; ++e) t += dot[e];
-#pragma unroll
-        for (int d = 16; d > 0; d /= 2) t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
-        if (lane == 0) s_dot[k][part] = t;
     }
     if (a.dweights == nullptr) return;
-    __syncthreads();
-    if (threadIdx.x < n) {
-        float t = 0.f;
-        for (int j = 0; j < share; ++j) t += s_dot[threadIdx.x][j];
-        a.dweights[(long long)r * a.topk + s.j[threadIdx.x]] = t;
+    float t = 0.f;
+#pragma unroll
+    for (int e = 0; e < P::kN; ++e) t += dot[e];
+    for (int d = (threads < 32 ? threads : 32) / 2; d > 0; d /= 2) t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
+    if (threads > 32) {
+        if (lane == 0) s_dot[warp] = t;
+        __syncthreads();
+        if (pair.part != 0) return;
+        t = 0.f;
+        for (int j = 0; j < threads / 32; ++j) t += s_dot[warp + j];
     }
+    if (pair.part == 0 && pair.mine) a.dweights[pair.at] = pair.place >= 0 ? t : 0.f;
 }
 
 // Rows that may be accessed 16 bytes at a time.
@@ -429,19 +568,12 @@ bool vectors(const MoveArgs &a) {
     return a.dim * es % 16 == 0 && rows_on(a.a, a.ld_a) && rows_on(a.b, a.ld_b) && rows_on(a.out, a.ld_out);
 }
 
-// Blocks of a row: one, or, where the rows are few, one for every piece a thread
-// (1 row of 3584 from 16 places 4.9 us with one).
-unsigned blocks_of_row(const MoveArgs &a, bool vec, int sms) {
-    const int pieces = vec ? a.dim * layer_esize(a.type) / 16 : a.dim, blocks = (pieces + 255) / 256;
-    return (long long)a.rows * blocks <= 4ll * sms ? (unsigned)blocks : 1u;
-}
-
-cudaError_t launch(const void *k, dim3 grid, unsigned block, size_t smem, unsigned cluster, void **params,
+cudaError_t launch(const void *k, dim3 grid, dim3 block, size_t smem, unsigned cluster, void **params,
                    cudaStream_t stream) {
     cudaLaunchConfig_t c = {};
     cudaLaunchAttribute attr[2];
     c.gridDim = grid;
-    c.blockDim = dim3(block);
+    c.blockDim = block;
     c.dynamicSmemBytes = smem;
     c.stream = stream;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -507,28 +639,60 @@ cudaError_t sort_launch(const SortArgs &args, SortShape most_of, cudaStream_t st
                   sort_smem(warps, per_slice), ctas, params, stream);
 }
 
+// Threads of a pair (a power of two), and the grid for blocks of 256: up to a warp,
+// but four pieces each (4096x256 at 16 places 16.2 us, a piece each 30; 512 at 8
+// 16.0 and 19.1); more than a warp where the pairs are few.
+int pair_threads(const MoveArgs &a, int sms, dim3 &grid) {
+    const int pieces = (a.dim * layer_esize(a.type) + 15) / 16;
+    const long long pairs = (long long)a.rows * a.topk;
+    int threads = 8;
+    while (threads < 256 && threads < pieces &&
+           (pairs * threads < 1024ll * sms || (threads < 32 && 8 * threads <= pieces)))
+        threads *= 2;
+    const int per_block = 256 / threads;
+    grid = dim3((unsigned)((pairs + per_block - 1) / per_block));
+    return threads;
+}
+
 cudaError_t gather_launch(const MoveArgs &args, int sms, cudaStream_t stream) {
-    const bool vec = vectors(args);
-    const void *k = layer_esize(args.type) == 4 ? (vec ? reinterpret_cast<const void *>(gather_kernel<4, true>)
-                                                       : reinterpret_cast<const void *>(gather_kernel<4, false>))
-                                                : (vec ? reinterpret_cast<const void *>(gather_kernel<2, true>)
-                                                       : reinterpret_cast<const void *>(gather_kernel<2, false>));
-    void *params[] = {const_cast<MoveArgs *>(&args)};
-    return launch(k, dim3((unsigned)args.rows, blocks_of_row(args, vec, sms)), 256, 0, 1, params, stream);
+    const bool four = layer_esize(args.type) == 4;
+    dim3 grid;
+    int threads = pair_threads(args, sms, grid);
+    void *params[] = {const_cast<MoveArgs *>(&args), &threads};
+    if (!vectors(args))
+        return launch(four ? reinterpret_cast<const void *>(gather_any_kernel<4>)
+                           : reinterpret_cast<const void *>(gather_any_kernel<2>),
+                      grid, 256, 0, 1, params, stream);
+    const RowShape shape(args, sms);
+    return launch(four ? reinterpret_cast<const void *>(gather_kernel<4>)
+                       : reinterpret_cast<const void *>(gather_kernel<2>),
+                  shape.grid, shape.block, 0, 1, params, stream);
 }
 
 cudaError_t combine_launch(const MoveArgs &args, int sms, cudaStream_t stream) {
     const bool vec = vectors(args);
-    const void *k = vec ? ROUTE_MOVE(combine_kernel, args, true) : ROUTE_MOVE(combine_kernel, args, false);
+#define ROUTE_COMBINE(T)                                                                             \
+    (!vec             ? reinterpret_cast<const void *>(combine_kernel<T, false, T == kFp32 ? 2 : 4>) \
+     : args.topk <= 2 ? reinterpret_cast<const void *>(combine_kernel<T, true, 2>)                   \
+     : args.topk <= 4 ? reinterpret_cast<const void *>(combine_kernel<T, true, 4>)                   \
+                      : reinterpret_cast<const void *>(combine_kernel<T, true, 8>))
+    const void *k = args.type == kFp32   ? ROUTE_COMBINE(kFp32)
+                    : args.type == kFp16 ? ROUTE_COMBINE(kFp16)
+                                         : ROUTE_COMBINE(kBf16);
+#undef ROUTE_COMBINE
     void *params[] = {const_cast<MoveArgs *>(&args)};
-    return launch(k, dim3((unsigned)args.rows, blocks_of_row(args, vec, sms)), 256, 0, 1, params, stream);
+    const RowShape shape(args, sms);
+    return launch(k, shape.grid, shape.block, 0, 1, params, stream);
 }
 
-cudaError_t combine_backward_launch(const MoveArgs &args, cudaStream_t stream) {
-    const void *k = vectors(args) ? ROUTE_MOVE(combine_backward_kernel, args, true)
-                                  : ROUTE_MOVE(combine_backward_kernel, args, false);
-    void *params[] = {const_cast<MoveArgs *>(&args)};
-    return launch(k, dim3((unsigned)args.rows), 32 * kBackWarps, 0, 1, params, stream);
+cudaError_t combine_backward_launch(const MoveArgs &args, int sms, cudaStream_t stream) {
+    const bool vec = vectors(args);
+    const void *k = vec ? ROUTE_MOVE(combine_backward_kernel, args, true)
+                        : ROUTE_MOVE(combine_backward_kernel, args, false);
+    dim3 grid;
+    int threads = pair_threads(args, sms, grid);
+    void *params[] = {const_cast<MoveArgs *>(&args), &threads};
+    return launch(k, grid, 256, 0, 1, params, stream);
 }
 
 }  // namespace route

@@ -43,7 +43,7 @@ struct MoveArgs {
 };
 cudaError_t gather_launch(const MoveArgs &args, int sms, cudaStream_t stream);
 cudaError_t combine_launch(const MoveArgs &args, int sms, cudaStream_t stream);
-cudaError_t combine_backward_launch(const MoveArgs &args, cudaStream_t stream);
+cudaError_t combine_backward_launch(const MoveArgs &args, int sms, cudaStream_t stream);
 
 // ---- the experts' products ----------------------------------------------------------
 

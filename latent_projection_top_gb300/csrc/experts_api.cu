@@ -276,7 +276,7 @@ route_status route_dispatch_combine_backward(const route_layer *p, int rows, con
     a.out = dy, a.ld_out = stride_of(pairs, ld_dy, p->k);
     a.dweights = dweights;
     DeviceGuard guard(p->device);
-    return launched(combine_backward_launch(a, static_cast<cudaStream_t>(stream)), "combine gradient kernel launch");
+    return launched(combine_backward_launch(a, p->sms, static_cast<cudaStream_t>(stream)), "combine gradient kernel launch");
 }
 
 route_status route_experts_prepare(int rows, int k, int f, int n, int experts, int type, int act, int train,

@@ -214,6 +214,51 @@ def test_moves_of_strided_views(dim, dt):
         written(dy, b2, slice(None))
 
 
+@pytest.mark.parametrize("dim", [1, 2, 7, 8, 9, 15, 16, 23, 40, 259, 2051])
+@pytest.mark.parametrize("dt", [BF16, FP16, FP32])
+def test_moves_at_every_alignment(dim, dt):
+    """Rows that begin anywhere in 16 bytes, tight and apart, NaN around them: what
+    is read beside a row counts for nothing, and nothing is written there."""
+    rows, topk, P = 9, 2, 16
+    rng = np.random.default_rng(dim)
+    place = np.full(rows * topk, -1)
+    place[:P] = rng.permutation(P)
+    at = to_gpu(rng.permutation(place).reshape(rows, topk)).to(I32)
+    r, j = torch.nonzero(at >= 0, as_tuple=True)
+    w = torch.rand((rows, topk), device=DEV)
+    dw, dw_only = torch.empty((2, rows, topk), device=DEV)
+    with route.DispatchPlan(rows, dim, dt, experts=4, topk=topk) as plan:
+        for o in range(8):
+            x = normal(o, rows, dim, dt=dt, ld=dim + o, offset=o)
+            y = normal(o + 8, P, dim, dt=dt, ld=dim + (5 * o) % 8, offset=(3 * o + 1) % 8)
+            xs, b0 = sevens(P, dim, dt, ld=dim + (o + 4) % 8, offset=(5 * o + 2) % 8)
+            route.dispatch_gather(plan, x, at, xs)
+            assert torch.equal(xs[at[r, j].long()], x[r])
+            written(xs, b0, slice(None))
+            out, b1 = sevens(rows, dim, dt, ld=dim + (3 * o) % 8, offset=(7 * o) % 8)
+            route.dispatch_combine(plan, y, at, w, out, residual=x)
+            check("out", out, experts_ref.combine(y, at, w, x, dt))
+            written(out, b1, slice(None))
+            dx, b2 = sevens(rows, dim, dt, ld=dim + o // 2, offset=7 - o)
+            route.dispatch_gather_backward(plan, y, at, dx)
+            check("dx", dx, experts_ref.combine(y, at, None, None, dt))
+            written(dx, b2, slice(None))
+            dy, b3 = sevens(P, dim, dt, ld=dim + (7 * o + 3) % 8, offset=(o + 5) % 8)
+            route.dispatch_combine_backward(plan, x, y, at, w, dy=dy, dweights=dw)
+            i, want_dy, want_dw = experts_ref.combine_grads(x, y, at, w, dt, P)
+            check("dy", dy[i], want_dy)
+            check("dw", dw, want_dw)
+            written(dy, b3, slice(None))
+            route.dispatch_combine_backward(plan, x, y, at, w, dweights=dw_only)
+            check("dw alone", dw_only, want_dw)
+            # in place: the residual is the result
+            before = out.clone()
+            route.dispatch_combine(plan, y, at, w, out, residual=out)
+            check("in place", out, experts_ref.combine(y, at, w, before, dt))
+            written(out, b1, slice(None))
+        plan.status()
+
+
 def test_places_outside_the_rows_are_none():
     rows, topk, dim, P = 40, 4, 64, 30
     at = torch.randint(-5, 40, (rows, topk), device=DEV, dtype=I32)
