@@ -209,30 +209,44 @@ struct Span {
         : lo(static_cast<const char *>(p)), hi(lo + ((rows - 1) * ld + dim) * es) {}
 };
 
-// 16 bytes of a row.  VEC: every row of every matrix lies on 16 bytes.  Else they
-// are taken out of the two aligned 16 bytes that they lie in, of which what
-// belongs to others is not used, and the pieces of a row are those that lie
-// aligned where they are written (4096x1001 BF16, 4 places: combine with a residual
-// 16.3 us and its gradient 24, a value at a time 23.5 and 31; 4096x2047 from 16
-// places 74 and 102.  FP32 gains little, 2049x1001 from 4 places 9.7 and 10.1,
-// and loses in combine's gradient, 4096x1001 40 and 35).
+// 16 bytes' values of a row, for one of its `threads` threads.  VEC: every row of
+// every matrix lies on 16 bytes.  Else 16-bit values are taken out of the two
+// aligned 16 bytes that they lie in, of which what belongs to others is not used,
+// and the pieces of a row are those that lie aligned where they are written
+// (4096x1001 BF16, 4 places: combine with a residual 16.3 us and its gradient 24, a
+// value at a time 23.5 and 31; 4096x2047 from 16 places 74 and 102); and FP32 values
+// are a row's threads apart, so that a warp's accesses are whole stretches of it
+// (2049x1001 from 4 places 11.1 us, in shifted pieces 14.2; combine's gradient
+// 4096x1001 30 and 40).
 template <int TY, bool VEC>
 struct Piece {
     static constexpr int kSize = layer_esize(TY), kN = 16 / kSize;
-    uint32_t w[VEC ? 4 : 8];
+    static constexpr bool kApart = !VEC && TY == kFp32, kShifted = !VEC && TY != kFp32;
+    uint32_t w[kShifted ? 8 : 4];
     unsigned off = 0;  // where in w they begin, bytes
 
-    // Pieces of a row that is written at p (or read, where it is not written), and
-    // how many values there would be before its first, in the first piece.
-    static __device__ __forceinline__ int before(const void *p) {
-        return VEC ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15u) / kSize;
-    }
-    static __device__ __forceinline__ int count(int dim, int skip) { return (dim + skip + kN - 1) / kN; }
+    // Where a row's pieces are: the i-th is from value i kN - skip on, `apart` apart.
+    struct Way {
+        int skip, count, apart;
+        // a row that is written at p (or read, where it is not written); thread t of `threads`
+        __device__ __forceinline__ Way(const void *p, int dim, int t, int threads) {
+            skip = kApart ? (kN - 1) * t : kShifted ? (int)(reinterpret_cast<uintptr_t>(p) & 15u) / kSize : 0;
+            count = kApart ? (dim + kN * threads - 1) / (kN * threads) * threads : (dim + skip + kN - 1) / kN;
+            apart = kApart ? threads : 1;
+        }
+        __device__ __forceinline__ int at(int i) const { return i * kN - skip; }
+    };
 
-    __device__ __forceinline__ void load(const char *p, const Span &in) {
+    // The values of `row` from the c-th on.
+    __device__ __forceinline__ void load(const char *row, int c, int dim, const Way &way, const Span &in) {
+        const char *p = row + (long long)c * kSize;
         if constexpr (VEC) {
             const uint4 t = *reinterpret_cast<const uint4 *>(p);
             w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
+        } else if constexpr (kApart) {
+#pragma unroll
+            for (int e = 0; e < kN; ++e)
+                w[e] = c + e * way.apart < dim ? reinterpret_cast<const uint32_t *>(p)[e * way.apart] : 0u;
         } else {
             off = (unsigned)(reinterpret_cast<uintptr_t>(p) & 15u);
             const char *q = p - off, *q1 = off != 0u ? q + 16 : q;
@@ -246,12 +260,9 @@ struct Piece {
                 for (int e = 0; e < 4; ++e) {
                     w[e] = 0u;
 #pragma unroll
-                    for (int h = 0; h < 4 / kSize; ++h) {
-                        const char *at = p + 4 * e + kSize * h;
-                        if (at < in.lo || at >= in.hi) continue;
-                        if constexpr (kSize == 4)
-                            w[e] = *reinterpret_cast<const uint32_t *>(at);
-                        else
+                    for (int h = 0; h < 2; ++h) {
+                        const char *at = p + 4 * e + 2 * h;
+                        if (at >= in.lo && at < in.hi)
                             w[e] |= (uint32_t)*reinterpret_cast<const uint16_t *>(at) << (16 * h);
                     }
                 }
@@ -259,7 +270,7 @@ struct Piece {
         }
     }
     __device__ __forceinline__ void words(uint32_t (&o)[4]) const {
-        if constexpr (VEC) {
+        if constexpr (!kShifted) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[e] = w[e];
         } else {
@@ -269,7 +280,7 @@ struct Piece {
 #pragma unroll
             for (int e = 0; e < 5; ++e) u[e] = off & 8u ? t[e + 2] : t[e];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = kSize == 4 ? u[e] : __funnelshift_r(u[e], u[e + 1], 8u * (off & 3u));
+            for (int e = 0; e < 4; ++e) o[e] = __funnelshift_r(u[e], u[e + 1], 8u * (off & 3u));
         }
     }
     __device__ __forceinline__ void values(float (&v)[kN]) const {
@@ -286,23 +297,27 @@ struct Piece {
             }
         }
     }
-    // The piece's values from the c-th of `row` on, those of them that the row has.
-    static __device__ __forceinline__ void store(char *row, int c, int dim, const uint32_t (&o)[4]) {
+    // Whether the row has the e-th value of its piece from the c-th on.
+    static __device__ __forceinline__ bool has(int c, int e, int dim, const Way &way) {
+        return VEC || (c + e * way.apart >= 0 && c + e * way.apart < dim);
+    }
+    // The values of `row` from the c-th on, those of them that it has.
+    static __device__ __forceinline__ void store(char *row, int c, int dim, const Way &way, const uint32_t (&o)[4]) {
         char *p = row + (long long)c * kSize;
-        if (VEC || (c >= 0 && c + kN <= dim)) {
+        if (!kApart && (VEC || (c >= 0 && c + kN <= dim))) {
             *reinterpret_cast<uint4 *>(p) = make_uint4(o[0], o[1], o[2], o[3]);
         } else {
 #pragma unroll
             for (int e = 0; e < kN; ++e) {
-                if (c + e < 0 || c + e >= dim) continue;
+                if (!has(c, e, dim, way)) continue;
                 if constexpr (kSize == 4)
-                    reinterpret_cast<uint32_t *>(p)[e] = o[e];
+                    reinterpret_cast<uint32_t *>(p)[e * way.apart] = o[e];
                 else
                     reinterpret_cast<uint16_t *>(p)[e] = (uint16_t)(o[e / 2] >> (16 * (e % 2)));
             }
         }
     }
-    static __device__ __forceinline__ void store(char *row, int c, int dim, const float (&v)[kN]) {
+    static __device__ __forceinline__ void store(char *row, int c, int dim, const Way &way, const float (&v)[kN]) {
         uint32_t o[4];
         if constexpr (TY == kFp32) {
 #pragma unroll
@@ -311,7 +326,7 @@ struct Piece {
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[e] = pack16(v[2 * e], v[2 * e + 1], TY);
         }
-        store(row, c, dim, o);
+        store(row, c, dim, way, o);
     }
 };
 
@@ -383,16 +398,16 @@ __global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ Mov
     const int first = blockIdx.y * blockDim.x + threadIdx.x, step = gridDim.y * blockDim.x;
     const Span in(a.a, a.rows, a.ld_a, a.dim, ES);
     const char *x = row_of<TY>(a.a, a.ld_a, r);
-    const int pieces = P::count(a.dim, 0);
+    const typename P::Way way(a.out, a.dim, (int)threadIdx.x, (int)blockDim.x);
     P p;
-    if (first < pieces && r < a.rows) p.load(x + 16ll * first, in);  // beside the places
+    if (first < way.count && r < a.rows) p.load(x, way.at(first), a.dim, way, in);  // beside the places
     find_places(a, r, s);
     const int n = s.n;
-    for (int i = first; i < pieces && n > 0; i += step) {
-        if (i != first) p.load(x + 16ll * i, in);
+    for (int i = first; i < way.count && n > 0; i += step) {
+        if (i != first) p.load(x, way.at(i), a.dim, way, in);
         uint32_t o[4];
         p.words(o);
-        for (int k = 0; k < n; ++k) P::store(row_of<TY>(a.out, a.ld_out, s.at[k]), i * P::kN, a.dim, o);
+        for (int k = 0; k < n; ++k) P::store(row_of<TY>(a.out, a.ld_out, s.at[k]), way.at(i), a.dim, way, o);
     }
 }
 
@@ -423,14 +438,13 @@ __global__ void __launch_bounds__(256) gather_any_kernel(const __grid_constant__
     const Span in(a.a, a.rows, a.ld_a, a.dim, ES);
     const char *x = row_of<TY>(a.a, a.ld_a, pair.row);
     char *out = row_of<TY>(a.out, a.ld_out, pair.place);
-    const int skip = P::before(out), pieces = P::count(a.dim, skip);
-    for (int i = pair.part; i < pieces; i += threads) {
-        const int c = i * P::kN - skip;
+    const typename P::Way way(out, a.dim, pair.part, threads);
+    for (int i = pair.part; i < way.count; i += threads) {
         P p;
-        p.load(x + (long long)c * ES, in);
+        p.load(x, way.at(i), a.dim, way, in);
         uint32_t o[4];
         p.words(o);
-        P::store(out, c, a.dim, o);
+        P::store(out, way.at(i), a.dim, way, o);
     }
 }
 
@@ -438,7 +452,7 @@ __global__ void __launch_bounds__(256) gather_any_kernel(const __grid_constant__
 // AHEAD places' pieces leave room for (4096x3584 from 16 places: 64 registers 82 us,
 // 69 87).
 constexpr int combine_blocks(bool vec, int ahead) {
-    return ahead <= 2 ? (vec ? 7 : 5) : ahead <= 4 && vec ? 5 : 4;
+    return ahead <= 2 ? 7 : ahead <= 4 && vec ? 5 : 4;
 }
 
 // out[row] = residual[row] + sum_j w_j b[place_j], in the order of j, AHEAD of the
@@ -458,19 +472,19 @@ __global__ void __launch_bounds__(256, combine_blocks(VEC, AHEAD))
     find_places(a, r, s);
     if (r >= a.rows) return;
     char *out = row_of<TY>(a.out, a.ld_out, r);
-    const int n = s.n, skip = P::before(out), pieces = P::count(a.dim, skip);
+    const int n = s.n;
+    const typename P::Way way(out, a.dim, (int)threadIdx.x, (int)blockDim.x);
     const Span in(a.b, a.pairs, a.ld_b, a.dim, P::kSize), res_in(a.a, a.rows, a.ld_a, a.dim, P::kSize);
-    for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < pieces; i += gridDim.y * blockDim.x) {
-        const int c = i * P::kN - skip;
-        const long long at = (long long)c * P::kSize;
+    for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < way.count; i += gridDim.y * blockDim.x) {
+        const int c = way.at(i);
         float sum[P::kN] = {};
         P res;
-        if (a.a != nullptr) res.load(row_of<TY>(a.a, a.ld_a, r) + at, res_in);
+        if (a.a != nullptr) res.load(row_of<TY>(a.a, a.ld_a, r), c, a.dim, way, res_in);
         for (int k0 = 0; k0 < n; k0 += AHEAD) {
             P p[AHEAD];
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k)
-                if (k0 + k < n) p[k].load(row_of<TY>(a.b, a.ld_b, s.at[k0 + k]) + at, in);
+                if (k0 + k < n) p[k].load(row_of<TY>(a.b, a.ld_b, s.at[k0 + k]), c, a.dim, way, in);
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k)
                 if (k0 + k < n) {
@@ -488,7 +502,7 @@ __global__ void __launch_bounds__(256, combine_blocks(VEC, AHEAD))
 #pragma unroll
             for (int e = 0; e < P::kN; ++e) sum[e] += v[e];
         }
-        P::store(out, c, a.dim, sum);
+        P::store(out, c, a.dim, way, sum);
     }
 }
 
@@ -500,7 +514,7 @@ __global__ void __launch_bounds__(256, combine_blocks(VEC, AHEAD))
 template <int TY, bool VEC>
 __global__ void __launch_bounds__(256, 5) combine_backward_kernel(const __grid_constant__ MoveArgs a, int threads) {
     using P = Piece<TY, VEC>;
-    constexpr int kPieces = VEC ? 2 : 1;  // on the way together (off 16 bytes a piece is two loads)
+    constexpr int kPieces = P::kShifted ? 1 : 2;  // on the way together (a shifted piece is two loads)
     __shared__ float s_dot[8];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -511,35 +525,35 @@ __global__ void __launch_bounds__(256, 5) combine_backward_kernel(const __grid_c
         const Span g_in(a.a, a.rows, a.ld_a, a.dim, P::kSize), y_in(a.b, a.pairs, a.ld_b, a.dim, P::kSize);
         const char *g_row = row_of<TY>(a.a, a.ld_a, pair.row), *y_row = row_of<TY>(a.b, a.ld_b, pair.place);
         char *out = row_of<TY>(a.out, a.ld_out, pair.place);
-        const int skip = P::before(a.out != nullptr ? out : y_row), pieces = P::count(a.dim, skip);
-        for (int i = pair.part; i < pieces; i += threads * kPieces) {
+        const typename P::Way way(a.out != nullptr ? out : y_row, a.dim, pair.part, threads);
+        for (int i = pair.part; i < way.count; i += threads * kPieces) {
             P g[kPieces], y[kPieces];
 #pragma unroll
             for (int q = 0; q < kPieces; ++q) {
                 const int at = i + q * threads;
-                if (at >= pieces) break;
-                const long long c = ((long long)at * P::kN - skip) * P::kSize;
-                g[q].load(g_row + c, g_in);
-                if (a.dweights != nullptr) y[q].load(y_row + c, y_in);
+                if (at >= way.count) break;
+                g[q].load(g_row, way.at(at), a.dim, way, g_in);
+                if (a.dweights != nullptr) y[q].load(y_row, way.at(at), a.dim, way, y_in);
             }
 #pragma unroll
             for (int q = 0; q < kPieces; ++q) {
                 const int at = i + q * threads;
-                if (at >= pieces) break;
-                const int c = at * P::kN - skip;
+                if (at >= way.count) break;
+                const int c = way.at(at);
                 float gv[P::kN], v[P::kN];
                 g[q].values(gv);
                 if (a.dweights != nullptr) {
                     y[q].values(v);
-                    const bool whole = VEC || (c >= 0 && c + P::kN <= a.dim);
+                    // (values apart that the row does not have are zeros)
+                    const bool whole = !P::kShifted || (c >= 0 && c + P::kN <= a.dim);
 #pragma unroll
                     for (int e = 0; e < P::kN; ++e)
-                        if (whole || (c + e >= 0 && c + e < a.dim)) dot[e] = fmaf(gv[e], v[e], dot[e]);
+                        if (whole || P::has(c, e, a.dim, way)) dot[e] = fmaf(gv[e], v[e], dot[e]);
                 }
                 if (a.out != nullptr) {
 #pragma unroll
                     for (int e = 0; e < P::kN; ++e) v[e] = w * gv[e];
-                    P::store(out, c, a.dim, v);
+                    P::store(out, c, a.dim, way, v);
                 }
             }
         }
@@ -672,7 +686,7 @@ cudaError_t gather_launch(const MoveArgs &args, int sms, cudaStream_t stream) {
 cudaError_t combine_launch(const MoveArgs &args, int sms, cudaStream_t stream) {
     const bool vec = vectors(args);
 #define ROUTE_COMBINE(T)                                                                             \
-    (!vec             ? reinterpret_cast<const void *>(combine_kernel<T, false, T == kFp32 ? 2 : 4>) \
+    (!vec             ? reinterpret_cast<const void *>(combine_kernel<T, false, 4>) \
      : args.topk <= 2 ? reinterpret_cast<const void *>(combine_kernel<T, true, 2>)                   \
      : args.topk <= 4 ? reinterpret_cast<const void *>(combine_kernel<T, true, 4>)                   \
                       : reinterpret_cast<const void *>(combine_kernel<T, true, 8>))

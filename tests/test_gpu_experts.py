@@ -568,6 +568,30 @@ def test_dropout(rows, dim, dt, p, residual):
         plan.status()
 
 
+@pytest.mark.parametrize("dim", [1, 7, 8, 9, 63, 247, 248, 249, 256, 500])
+@pytest.mark.parametrize("dt", [BF16, FP16, FP32])
+def test_dropout_at_every_alignment(dim, dt):
+    """The lots are the places', wherever rows begin; NaN around them, and nothing
+    written there."""
+    rows, p, seed = 9, 0.3, 77
+    with route.DropoutPlan(rows, dim, dt) as plan:
+        for o in range(8):
+            x = normal(o, rows, dim, dt=dt, ld=dim + o, offset=o)
+            res = normal(o + 8, rows, dim, dt=dt, ld=dim + (5 * o) % 8, offset=(3 * o + 1) % 8)
+            out, buf = sevens(rows, dim, dt, ld=dim + (3 * o) % 8, offset=(7 * o) % 8)
+            route.dropout_forward(plan, x, p, seed, out, offset=o, residual=res)
+            want, keep = experts_ref.dropout(x, p, seed, o, res, dt)
+            check("out", out, want)
+            written(out, buf, slice(None))
+            route.dropout_backward(plan, x, p, seed, out, offset=o)
+            check("dx", out, experts_ref.dropout(x, p, seed, o, None, dt)[0])
+            written(out, buf, slice(None))
+            # in place
+            route.dropout_forward(plan, x, p, seed, res, offset=o, residual=res)
+            check("in place", res, want)
+        plan.status()
+
+
 def test_dropout_views_rows_and_offsets():
     """Lots go by the place in the matrix, not by strides or the number of rows."""
     rows, dim, dt = 29, 75, BF16
