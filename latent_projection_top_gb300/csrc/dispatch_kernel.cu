@@ -35,7 +35,7 @@ constexpr int kSortAhead = 8;     // groups of 32 pairs whose ids are on the way
 // 1048576 40).
 __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_constant__ SortArgs a, int warps, int run,
                                                                int per_slice) {
-    extern __shared__ int smem[];
+    extern __shared__ __align__(16) int smem[];  // the counts are cleared 16 bytes at a time
     __shared__ int s_scan[kSortThreads / 32], s_lows[kSortThreads / 32], s_low;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // after the wait: only the offsets and places are still to come, which no
