@@ -98,7 +98,8 @@ _without = False  # the compiled module could not be loaded
 
 def _short_way():
     """The compiled module, bound to the loaded library; None (and one warning)
-    where it is missing or does not load: the calls then go through ctypes."""
+    where it is missing, does not load or is another version's: the calls then
+    go through ctypes."""
     global _short, _without
     if _short is None and not _without:
         import importlib.util
@@ -113,20 +114,21 @@ def _short_way():
             module = importlib.util.module_from_spec(
                 importlib.util.spec_from_loader("_layer_call", loader))
             loader.exec_module(module)
-        except (ImportError, OSError) as e:
+            for bind, names in (
+                    (module.bind, ("norm_forward", "norm_backward", "linear_forward",
+                                   "linear_backward", "gated_forward", "gated_backward")),
+                    (module.bind_routed, ("dispatch_sort", "dispatch_gather", "dispatch_gather_backward",
+                                          "dispatch_combine", "dispatch_combine_backward",
+                                          "experts_forward", "experts_backward", "dropout_forward",
+                                          "dropout_backward"))):
+                bind(*(ctypes.cast(getattr(L, f"route_{name}"), _vp).value for name in names))
+        except (ImportError, OSError, AttributeError, TypeError) as e:
+            # (the last two: a module of another version of this binding)
             import warnings
             _without = True
             warnings.warn(f"layer calls go through ctypes, 2 to 5 us more each: {e} "
                           "(latent_projection_top_gb300.build() makes the module)")
             return None
-        for bind, names in (
-                (module.bind, ("norm_forward", "norm_backward", "linear_forward", "linear_backward",
-                               "gated_forward", "gated_backward")),
-                (module.bind_routed, ("dispatch_sort", "dispatch_gather", "dispatch_gather_backward",
-                                      "dispatch_combine", "dispatch_combine_backward",
-                                      "experts_forward", "experts_backward", "dropout_forward",
-                                      "dropout_backward"))):
-            bind(*(ctypes.cast(getattr(L, f"route_{name}"), _vp).value for name in names))
         _short = module
     return _short
 
