@@ -101,15 +101,19 @@ def call_module() -> str | None:
 
 def _build_call_module(force: bool) -> None:
     """Build the calls' module if it is stale; warn if that is not possible."""
+    inputs = [CALL_SOURCE, *(os.path.join(INCLUDE, h) for h in ("route.h", "route_layer.h", "route_experts.h")),
+              os.path.abspath(__file__)]
+    module = None
     try:
         module = call_module()
         if module is None:
             raise RuntimeError("torch is not installed")
-        if force or _stale(module, [CALL_SOURCE, os.path.join(INCLUDE, "route.h"),
-                                    os.path.join(INCLUDE, "route_layer.h"),
-                                    os.path.join(INCLUDE, "route_experts.h"), os.path.abspath(__file__)]):
+        if force or _stale(module, inputs):
             _compile_call_module()
     except Exception as e:  # the library and the binding work without it
+        # one older than the entry points would call them by their old arguments
+        if module is not None and os.path.exists(module) and _stale(module, inputs):
+            os.remove(module)
         warnings.warn(f"the layer operators' calls will go through ctypes (2 to 5 us more each): {e}")
 
 

@@ -1,5 +1,6 @@
 """A compiled calls' module that is not this binding's: the calls go through ctypes."""
 
+import os
 import subprocess
 import sysconfig
 
@@ -35,3 +36,31 @@ def test_a_module_of_another_version_is_not_used(tmp_path, monkeypatch, takes):
         assert layer._short_way() is None
     assert layer._short is None
     assert layer._short_way() is None  # warned once
+
+
+def failing(*_):
+    raise RuntimeError("no compiler")
+
+
+def test_a_module_that_could_not_be_rebuilt_is_not_left(tmp_path, monkeypatch):
+    """What build() warns of holds: a module older than its source is not loaded."""
+    so = tmp_path / "_layer_call.so"
+    so.write_bytes(b"")
+    os.utime(so, (0, 0))
+    monkeypatch.setattr(builder, "call_module", lambda: str(so))
+    monkeypatch.setattr(builder, "_compile_call_module", failing)
+    with pytest.warns(UserWarning, match="ctypes.*no compiler"):
+        builder._build_call_module(False)
+    assert not so.exists()
+
+
+def test_a_module_that_is_up_to_date_stays(tmp_path, monkeypatch):
+    so = tmp_path / "_layer_call.so"
+    so.write_bytes(b"")
+    monkeypatch.setattr(builder, "call_module", lambda: str(so))
+    monkeypatch.setattr(builder, "_compile_call_module", failing)
+    builder._build_call_module(False)
+    assert so.exists()
+    with pytest.warns(UserWarning, match="no compiler"):
+        builder._build_call_module(True)
+    assert so.exists()
