@@ -98,7 +98,9 @@ route_status route_dispatch_combine_backward(const route_layer *plan, int rows, 
  *
  * Expert e's rows are offsets[e] .. offsets[e + 1] - 1 (route_dispatch_sort's);
  * offsets outside 0 .. rows are cut to it.  Rows that are nobody's are not
- * written, and what they hold changes no result.
+ * written, and what they hold changes no result.  Offsets must not descend:
+ * where they do, so that runs overlap, what the call's results hold is
+ * unspecified (a row may be any of its experts' or be left as it was).
  *
  * All matrices start on 16 bytes with row strides that are multiples of 8
  * (ROUTE_ERR_ALIGN); es_* are the distances between experts' matrices in
