@@ -141,7 +141,9 @@ route_status route_experts_backward(const route_layer *plan, int rows, const voi
 route_status route_dropout_prepare(int rows, int dim, int type, int device, route_layer **out);
 
 /*
- * route_dropout_forward: out = keep * x / (1 - q) + residual, one rounding.
+ * route_dropout_forward: out = keep * x / (1 - q) + residual, in FP32: 1 / (1 - q),
+ * its product with x and the sum are each rounded to it, and a 16-bit result
+ * once more.
  *
  * Each value has a lot of 16 bits, and is kept if its lot is at least t =
  * p 65536 rounded to the nearest whole number (0 <= p <= 1): q = t / 65536 is
@@ -165,8 +167,8 @@ route_status route_dropout_forward(const route_layer *plan, int rows, const void
                                    const void *residual, int64_t ld_residual, void *out,
                                    int64_t ld_out, void *stream);
 
-/* route_dropout_backward: dx = keep * dout / (1 - q) with the same lots.  The
- * residual's gradient is dout itself.  dx may be dout. */
+/* route_dropout_backward: dx = keep * dout / (1 - q) with the same lots and the
+ * same roundings.  The residual's gradient is dout itself.  dx may be dout. */
 route_status route_dropout_backward(const route_layer *plan, int rows, const void *dout,
                                     int64_t ld_dout, double p, uint64_t seed, uint64_t offset,
                                     const int64_t *step, void *dx, int64_t ld_dx, void *stream);
