@@ -47,6 +47,27 @@ MoveArgs move_args(const route_layer *p, int rows, int pairs, const int32_t *pla
     return a;
 }
 
+// Weighted sums over places: combine, and (without weights and residual) gather's gradient.
+route_status combine(const route_layer *p, int rows, const char *y_name, const void *y, int64_t ld_y, int pairs,
+                     const int32_t *place, const float *weights, const void *residual, int64_t ld_residual,
+                     const char *out_name, void *out, int64_t ld_out, void *stream) {
+    route_status st = check_plan(p, kDispatch, rows);
+    if (st != ROUTE_OK || (st = check_pairs(p, pairs)) != ROUTE_OK) return st;
+    if (rows == 0) return ROUTE_OK;
+    const int es = layer_esize(p->type);
+    if ((pairs > 0 && (st = check_mat({y_name, y, ld_y, pairs, p->k, es, false})) != ROUTE_OK) ||
+        (st = check_mat({out_name, out, ld_out, rows, p->k, es, false})) != ROUTE_OK ||
+        (residual && (st = check_mat({"residual", residual, ld_residual, rows, p->k, es, false})) != ROUTE_OK) ||
+        (st = need(place, "place", 4)) != ROUTE_OK || (st = check_vec("weights", weights, 4)) != ROUTE_OK)
+        return st;
+    MoveArgs a = move_args(p, rows, pairs, place, weights);
+    a.a = residual, a.ld_a = stride_of(rows, ld_residual, p->k);
+    a.b = y, a.ld_b = stride_of(pairs, ld_y, p->k);
+    a.out = out, a.ld_out = stride_of(rows, ld_out, p->k);
+    DeviceGuard guard(p->device);
+    return launched(combine_launch(a, p->sms, static_cast<cudaStream_t>(stream)), "combine kernel launch");
+}
+
 // ---- the experts' products --------------------------------------------------------
 
 // The experts' matrices [experts][rows, cols].
@@ -233,27 +254,13 @@ route_status route_dispatch_gather(const route_layer *p, int rows, const void *x
 route_status route_dispatch_combine(const route_layer *p, int rows, const void *y, int64_t ld_y, int pairs,
                                     const int32_t *place, const float *weights, const void *residual,
                                     int64_t ld_residual, void *out, int64_t ld_out, void *stream) {
-    route_status st = check_plan(p, kDispatch, rows);
-    if (st != ROUTE_OK || (st = check_pairs(p, pairs)) != ROUTE_OK) return st;
-    if (rows == 0) return ROUTE_OK;
-    const int es = layer_esize(p->type);
-    if ((pairs > 0 && (st = check_mat({"y", y, ld_y, pairs, p->k, es, false})) != ROUTE_OK) ||
-        (st = check_mat({"out", out, ld_out, rows, p->k, es, false})) != ROUTE_OK ||
-        (residual && (st = check_mat({"residual", residual, ld_residual, rows, p->k, es, false})) != ROUTE_OK) ||
-        (st = need(place, "place", 4)) != ROUTE_OK || (st = check_vec("weights", weights, 4)) != ROUTE_OK)
-        return st;
-    MoveArgs a = move_args(p, rows, pairs, place, weights);
-    a.a = residual, a.ld_a = stride_of(rows, ld_residual, p->k);
-    a.b = y, a.ld_b = stride_of(pairs, ld_y, p->k);
-    a.out = out, a.ld_out = stride_of(rows, ld_out, p->k);
-    DeviceGuard guard(p->device);
-    return launched(combine_launch(a, p->sms, static_cast<cudaStream_t>(stream)), "combine kernel launch");
+    return combine(p, rows, "y", y, ld_y, pairs, place, weights, residual, ld_residual, "out", out, ld_out, stream);
 }
 
 route_status route_dispatch_gather_backward(const route_layer *p, int rows, const void *dout, int64_t ld_dout,
                                             int pairs, const int32_t *place, void *dx, int64_t ld_dx,
                                             void *stream) {
-    return route_dispatch_combine(p, rows, dout, ld_dout, pairs, place, nullptr, nullptr, 0, dx, ld_dx, stream);
+    return combine(p, rows, "dout", dout, ld_dout, pairs, place, nullptr, nullptr, 0, "dx", dx, ld_dx, stream);
 }
 
 route_status route_dispatch_combine_backward(const route_layer *p, int rows, const void *dout, int64_t ld_dout,
