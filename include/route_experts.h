@@ -55,9 +55,10 @@ route_status route_dispatch_sort(const route_layer *plan, int rows, const int32_
                                  int64_t ld_ids, int32_t *offsets, int32_t *place, int32_t *source,
                                  void *stream);
 
-/* route_dispatch_gather: out[place[r, j]] = x[r].  out has `pairs` rows; a
- * place outside 0 .. pairs - 1 is none, and rows that no place names are left
- * as they were.  Of two pairs with the same place either may win. */
+/* route_dispatch_gather: out[place[r, j]] = x[r].  out has `pairs` rows (0 ..
+ * the plan's rows * topk, else ROUTE_ERR_ROWS; so in the calls below); a place
+ * outside 0 .. pairs - 1 is none, and rows that no place names are left as they
+ * were.  Of two pairs with the same place either may win, value by value. */
 route_status route_dispatch_gather(const route_layer *plan, int rows, const void *x, int64_t ld_x,
                                    const int32_t *place, int pairs, void *out, int64_t ld_out,
                                    void *stream);
@@ -81,8 +82,10 @@ route_status route_dispatch_combine(const route_layer *plan, int rows, const voi
  * route_dispatch_combine_backward:
  *   dy[place[r, j]] = weights[r, j] dout[r],  dweights[r, j] = <dout[r], y[place[r, j]]>
  * dweights [rows][topk] FP32 is 0 where a pair has no place; rows of dy that no
- * place names are left as they were.  Either of dy and dweights may be NULL;
- * y may be NULL without dweights, weights are 1 where NULL.
+ * place names are left as they were, and of two pairs with the same place either
+ * may win, value by value (combine's gradient would be their sum).  Either of dy
+ * and dweights may be NULL; y may be NULL without dweights, weights are 1 where
+ * NULL.
  */
 route_status route_dispatch_combine_backward(const route_layer *plan, int rows, const void *dout,
                                              int64_t ld_dout, const void *y, int64_t ld_y, int pairs,
@@ -123,8 +126,10 @@ route_status route_experts_forward(const route_layer *plan, int rows, const void
  * dgate = dh * up * act'(gate), dup = dh * act(gate):
  *   dx = dgate W_gate^T + dup W_up^T,  dW_gate = x^T dgate,  dW_up = x^T dup,
  *   dW_down = h^T dout
- * Any of dx, dW_gate, dW_up and dW_down may be NULL.  The weights' gradients of
- * an expert without rows are 0.  x may be NULL without dW_gate and dW_up.
+ * rows, offsets and x are those of the forward call that filled `saved` (whose
+ * layout goes by rows).  Any of dx, dW_gate, dW_up and dW_down may be NULL.  The
+ * weights' gradients of an expert without rows are 0.  x may be NULL without
+ * dW_gate and dW_up.
  */
 route_status route_experts_backward(const route_layer *plan, int rows, const void *dout,
                                     int64_t ld_dout, const void *x, int64_t ld_x,
