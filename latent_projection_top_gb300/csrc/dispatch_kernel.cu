@@ -450,7 +450,9 @@ __global__ void __launch_bounds__(256) gather_any_kernel(const __grid_constant__
 
 // Blocks an SM of combine_kernel: as many rows on their way as the registers of
 // AHEAD places' pieces leave room for (4096x3584 from 16 places: 64 registers 82 us,
-// 69 87).
+// 69 87).  Those of two places, of eight, and of rows off 16 bytes spill 12 to 68
+// bytes for it; a block less spills nothing and is slower (BF16, 4096 rows: 2048 from
+// 2 places 13.4 us, 14.1; 3584 from 16 83.6, 88.3; 2047 from 16 77, 89).
 constexpr int combine_blocks(bool vec, int ahead) {
     return ahead <= 2 ? 7 : ahead <= 4 && vec ? 5 : 4;
 }
@@ -458,8 +460,8 @@ constexpr int combine_blocks(bool vec, int ahead) {
 // out[row] = residual[row] + sum_j w_j b[place_j], in the order of j, AHEAD of the
 // experts' rows on the way together: fewer where a row has few places (4096x2048
 // from 2 places 11.9 us, with eight ahead 18.4).  Bound by HBM: 4096 rows of 3584 BF16
-// from 16 places, with a residual, 83 us (529 MB, 6.4 TB/s), as the gather's gradient
-// 74 (6.7); short rows as gather's (4096x512 from 8 places 6.4 us, a block of 256
+// from 16 places, with a residual, 84 us (529 MB, 6.3 TB/s), as the gather's gradient
+// 75 (6.6); short rows as gather's (4096x512 from 8 places 6.4 us, a block of 256
 // threads a row 12.5).
 template <int TY, bool VEC, int AHEAD>
 __global__ void __launch_bounds__(256, combine_blocks(VEC, AHEAD))
@@ -510,7 +512,9 @@ __global__ void __launch_bounds__(256, combine_blocks(VEC, AHEAD))
 // w_j dout[row], dweights_j = <dout[row], b[place_j]>.  Bound by HBM: 4096 rows of
 // 3584 BF16 at 16 places 148 us (970 MB, 6.5 TB/s; a block a row 153).  Two pieces of
 // each matrix on the way and 48 registers (one piece 175, four and 72 registers
-// 159; 4096x1000 at 4 places 16.1 us, 20.0 and 18.4; a block a row 28.8).
+// 159; 4096x1000 at 4 places 16.1 us, 20.0 and 18.4; a block a row 28.8).  Of 16-bit
+// rows off 16 bytes 40 bytes are spilled (four blocks an SM, no spills: 4096x2047 at 16
+// places 160 us, so 158; 4096x1001 at 4 23.7 and 25.4).
 template <int TY, bool VEC>
 __global__ void __launch_bounds__(256, 5) combine_backward_kernel(const __grid_constant__ MoveArgs a, int threads) {
     using P = Piece<TY, VEC>;

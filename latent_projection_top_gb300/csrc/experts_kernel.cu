@@ -14,11 +14,12 @@
 // steps of 32: an expert with two rows costs the reading of its weights, one
 // with a thousand runs at the tensor cores' rate, and no rule chooses between
 // them.  Longer runs are cut into parts (make_table).  Bound by HBM where experts
-// have few rows (8 rows of 3584x2048 at 14 experts 89 us, 616 MB of weights: 6.9
-// TB/s), by the tensor cores where they have many (16890 rows at 16 experts of
-// 3584x2048 443-460 us, 1,615-1,680 TFLOP/s, the power limit's), in between by
-// whole rounds of tiles over the pairs, and by 3 us of a launch's start (0.7 of it
-// the table) and 3 of the last epilogue.
+// have few rows (8 to 22 rows of 3584x2048 at 8 to 16 experts 62-112 us, 352-705 MB
+// of weights, 5.4-6.5 TB/s by how the tiles divide over the pairs), by the tensor
+// cores where they have many (12600 to 22900 rows at 16 experts of 3584x2048 398-603
+// us, 1,370-1,690 TFLOP/s, by the power limit and how the parts divide), in between by
+// whole rounds of tiles over the pairs, and by 3 us of a launch's start (0.7 of it the
+// table) and 3 of the last epilogue.
 //
 // Gradient kernel: rows of dW are the M side, its columns the N side, 256 x 256
 // a tile.  The last block of an expert's rows holds rows of the next one: what of
