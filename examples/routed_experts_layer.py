@@ -14,9 +14,11 @@ A rank that holds a shard of the experts (first .. first + experts) runs the sam
 calls: pairs of other ranks' experts have no place, and the ranks' `mixed` add
 up to the layer's.
 
-Training, for the routed experts of the same layer (what the route step made is
-given): y = residual + dropout(mixed), then the gradients of the latent rows, of
-the routing weights and of every expert's weights.
+Training, for the routed experts alone, in the latent width (what the route step
+made is given, and it has no gradient): y = residual + dropout(mixed), then the
+gradients of the latent rows, of the routing weights and of every expert's weights.
+A layer that is trained whole has its dropout behind W_out, in the hidden width, with
+route.linear_forward and linear_backward between it and `mixed`.
 
     python examples/routed_experts_layer.py [rows]
 """
