@@ -451,8 +451,9 @@ __global__ void __launch_bounds__(256) gather_any_kernel(const __grid_constant__
 // Blocks an SM of combine_kernel: as many rows on their way as the registers of
 // AHEAD places' pieces leave room for (4096x3584 from 16 places: 64 registers 82 us,
 // 69 87).  Those of two places, of eight, and of rows off 16 bytes spill 12 to 68
-// bytes for it; a block less spills nothing and is slower (BF16, 4096 rows: 2048 from
-// 2 places 13.4 us, 14.1; 3584 from 16 83.6, 88.3; 2047 from 16 77, 89).
+// bytes for it; a block less spills nothing and is mostly slower (4096 rows, BF16: 2048
+// from 2 places 13.4 us, 14.1; 3584 from 16 83.6, 88.3; 2047 from 16 77, 89; but FP32,
+// 512 from 2, 7.8 and 7.5).
 constexpr int combine_blocks(bool vec, int ahead) {
     return ahead <= 2 ? 7 : ahead <= 4 && vec ? 5 : 4;
 }
